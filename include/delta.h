@@ -57,6 +57,8 @@
 #ifndef DELTA_H_
 #define DELTA_H_
 
+#include <stdint.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -433,6 +435,123 @@ int delta_inject_failure(int count);
  * if the launch fails.
  */
 int delta_selftest_wait(int polls, struct CUstream_st *stream);
+
+/*
+ * ---- Operators around the token mixers in a block ------------------------
+ *
+ * The calls below follow the conventions above (asynchronous, checked before
+ * anything is enqueued, thread-safe) with these differences: inputs that are
+ * slices of a wider tensor are given with strides and need only be aligned to
+ * their elements; outputs are contiguous and 16-byte aligned; gradients take
+ * the type of what they are the gradient of, except those of the small
+ * parameters (weights of the norm, bias) and of the states, which are
+ * float32.  All sums, statistics and states are float32.  Sizes may be 0.
+ */
+
+typedef enum {
+    DELTA_SCAN_LINEAR = 0, /* h = a h + x, gate = a, float32, any value; 0 resets */
+    DELTA_SCAN_SIGMOID = 1 /* h = s(f) h + (1 - s(f)) x, gate = f in x's type, s the logistic function */
+} delta_scan_form;
+
+/*
+ * delta_scan_fwd -- the gated linear recurrence with one state per channel,
+ *
+ *   h_t = a_t h_{t-1} + u_t x_t,   out_t = h_t,
+ *
+ * over B rows of T steps and D channels, a_t and u_t from the form above.  A
+ * step with a_t = 0 drops the state whatever it holds (Inf and NaN included).
+ *
+ *   x       [B, T, D]  dtype    element strides x_sb, x_st, 1
+ *   gate    [B, T, D]  float32 (linear) or dtype (sigmoid), strides g_sb, g_st, 1
+ *   h0      [B, D]     float32 or NULL (=> 0)
+ *   lengths [B]        int32 steps of each row, taken into [0, T], or NULL (=> T);
+ *                      later steps are not read, leave the state alone and
+ *                      have out = 0
+ *   out     [B, T, D]  dtype
+ *   hT      [B, D]     float32 state after the last step, or NULL; hT == h0 allowed
+ *   states  [B, ceil(T/64), D] float32 state before every 64th step, which
+ *                      delta_scan_bwd takes, or NULL
+ *
+ * A stride of an axis with one entry is not used.  One kernel, no scratch; the
+ * result does not depend on scheduling.
+ */
+int delta_scan_fwd(const void *x, const void *gate, const float *h0, const int *lengths, void *out,
+                   float *hT, float *states, int B, int T, int D, int64_t x_sb, int64_t x_st,
+                   int64_t g_sb, int64_t g_st, delta_dtype dtype, delta_scan_form form,
+                   struct CUstream_st *stream);
+
+/*
+ * delta_scan_step -- one step of the same recurrence: state [B, D] float32 is
+ * updated in place, out [B, D] dtype; x and gate [B, D] with row strides.
+ */
+int delta_scan_step(const void *x, const void *gate, float *state, void *out, int B, int D, int64_t x_sb,
+                    int64_t g_sb, delta_dtype dtype, delta_scan_form form, struct CUstream_st *stream);
+
+/*
+ * delta_scan_bwd -- gradients of delta_scan_fwd's out and hT.
+ *
+ *   x, gate, lengths   as in the forward
+ *   states  [B, ceil(T/64), D] what the forward wrote
+ *   dout    [B, T, D]  dtype, contiguous
+ *   dhT     [B, D]     float32 or NULL (=> 0)
+ *   dx      [B, T, D]  dtype
+ *   dgate   [B, T, D]  gate's type; at a reset of the linear form (a = 0) the
+ *                      derivative with respect to a, dh_t h_{t-1}
+ *   dh0     [B, D]     float32 or NULL; dh0 == dhT allowed
+ *
+ * Steps past a row's length have zero gradients.  One kernel, no scratch.
+ */
+int delta_scan_bwd(const void *x, const void *gate, const float *states, const int *lengths,
+                   const void *dout, const float *dhT, void *dx, void *dgate, float *dh0, int B, int T,
+                   int D, int64_t x_sb, int64_t x_st, int64_t g_sb, int64_t g_st, delta_dtype dtype,
+                   delta_scan_form form, struct CUstream_st *stream);
+
+/*
+ * delta_add_rmsnorm_fwd -- the residual addition and the root-mean-square norm,
+ *
+ *   t = x + residual,  rstd = (mean_d t_d^2 + eps)^(-1/2),  y = t * rstd * weight.
+ *
+ *   x, residual [rows, D] dtype, row strides ldx, ldr; residual NULL: t = x
+ *   weight      [D]       wdtype
+ *   y           [rows, D] dtype
+ *   sum_out     [rows, D] dtype, t rounded for the residual stream, or NULL;
+ *                         may be x or residual itself (then contiguous)
+ *   rstd        [rows]    float32 or NULL
+ *
+ * The norm is of the unrounded t.  D <= 8192, eps > 0.
+ */
+int delta_add_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *y, void *sum_out,
+                          float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
+                          delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream);
+
+/*
+ * delta_add_rmsnorm_quant -- the same with y in 8 bits: y_scale[row] = max |y|
+ * / 448 (1 for a row of zeros, or whose quotient is below float32's normal
+ * range), y [rows, D] = e4m3(y / y_scale), to nearest even.  y * y_scale
+ * stands for the row.
+ */
+int delta_add_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *y, float *y_scale,
+                            void *sum_out, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
+                            delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream);
+
+/*
+ * delta_add_rmsnorm_bwd -- its gradients: with t^ = sum * rstd,
+ *
+ *   dx = rstd (w dy - t^ mean_d(w dy t^)) + dsum,   dweight = sum over rows of dy t^.
+ *
+ *   dy, sum [rows, D] dtype, contiguous; sum is the forward's sum_out (or x)
+ *   dsum    [rows, D] dtype gradient that arrives at sum_out, or NULL
+ *   rstd    [rows]    float32, from the forward
+ *   dx      [rows, D] dtype, the gradient of x and of residual alike; may be
+ *                     dy or dsum itself
+ *   dweight [D]       float32
+ *
+ * Takes one float32 row of D per resident CTA from the library's pool,
+ * stream-ordered, as delta_fwd does; the result does not depend on scheduling.
+ */
+int delta_add_rmsnorm_bwd(const void *dy, const void *sum, const void *weight, const float *rstd,
+                          const void *dsum, void *dx, float *dweight, int64_t rows, int D,
+                          delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream);
 
 #ifdef __cplusplus
 }

@@ -5,7 +5,8 @@ A thin Python binding over the C ABI of ``libdelta.so`` (declared in
 arguments: shape/dtype checks, output allocation through PyTorch, the
 current CUDA stream, and status-to-exception mapping.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback, and a
-missing library raises immediately.
+missing library raises immediately.  The operators around the mixers in a
+block (scan, norm) are in ``block.py`` and exported here.
 """
 from __future__ import annotations
 
@@ -14,6 +15,10 @@ import os
 import threading
 
 import torch
+
+from . import block
+from .block import (delta_add_rmsnorm_bwd, delta_add_rmsnorm_fwd, delta_add_rmsnorm_quant,
+                    delta_scan_bwd, delta_scan_fwd, delta_scan_step)
 
 __all__ = ["delta_fwd", "delta_bwd", "delta_fwd_kda", "delta_step_kda", "delta_prologue",
            "delta_fwd_prologue", "delta_step_prologue",
@@ -24,7 +29,7 @@ __all__ = ["delta_fwd", "delta_bwd", "delta_fwd_kda", "delta_step_kda", "delta_p
            "delta_version", "DeltaError", "library_path", "load_library",
            "DELTA_OK", "DELTA_ERR_INVALID", "DELTA_ERR_UNSUPPORTED",
            "DELTA_ERR_ALIGN", "DELTA_ERR_CUDA", "DELTA_F32", "DELTA_BF16",
-           "DELTA_BETA_SIGMOID", "DELTA_BETA_2SIGMOID", "EXPORTED_SYMBOLS"]
+           "DELTA_BETA_SIGMOID", "DELTA_BETA_2SIGMOID", "EXPORTED_SYMBOLS", *block.SYMBOLS]
 
 DELTA_OK = 0
 DELTA_ERR_INVALID = -1
@@ -45,7 +50,7 @@ EXPORTED_SYMBOLS = ("delta_fwd", "delta_bwd", "delta_fwd_kda", "delta_step_kda",
                     "delta_status_string",
                     "delta_last_error", "delta_check_device", "delta_version",
                     "delta_inject_failure", "delta_selftest_wait", "delta_state_erank",
-                    "delta_attention_map")
+                    "delta_attention_map") + block.SYMBOLS
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -117,6 +122,7 @@ def load_library():
         lib.delta_inject_failure.argtypes = [i]
         lib.delta_selftest_wait.restype = i
         lib.delta_selftest_wait.argtypes = [i, ctypes.c_void_p]
+        block.declare(lib)
         _lib = lib
         return lib
 

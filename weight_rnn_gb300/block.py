@@ -1,0 +1,300 @@
+"""Operators around the token mixers in a block: the gated linear recurrence
+(``delta_scan_*``) and the residual addition with RMS norm
+(``delta_add_rmsnorm_*``).
+
+Bindings over the C ABI of ``libdelta.so`` with the ABI's names: argument
+checks, output allocation, the current CUDA stream, statuses as exceptions.
+With ``stream=`` the outputs are allocated for that stream; inputs made on
+another stream are the caller's to order and to keep, as with any kernel.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+DELTA_SCAN_LINEAR = 0
+DELTA_SCAN_SIGMOID = 1
+_SCAN_FORMS = {"linear": DELTA_SCAN_LINEAR, "sigmoid": DELTA_SCAN_SIGMOID}
+SCAN_BLOCK = 64  # steps between two saved states
+_CODES = {torch.float32: 0, torch.bfloat16: 1}
+E4M3 = torch.float8_e4m3fn
+
+SYMBOLS = ("delta_scan_fwd", "delta_scan_step", "delta_scan_bwd", "delta_add_rmsnorm_fwd",
+           "delta_add_rmsnorm_quant", "delta_add_rmsnorm_bwd")
+
+
+def declare(lib) -> None:
+    """Argument types of this module's entry points."""
+    p, i, n, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+    for name, args in (
+            ("delta_scan_fwd", [p] * 7 + [i] * 3 + [n] * 4 + [i] * 2 + [p]),
+            ("delta_scan_step", [p] * 4 + [i] * 2 + [n] * 2 + [i] * 2 + [p]),
+            ("delta_scan_bwd", [p] * 9 + [i] * 3 + [n] * 4 + [i] * 2 + [p]),
+            ("delta_add_rmsnorm_fwd", [p] * 6 + [n, i, n, n, f, i, i, p]),
+            ("delta_add_rmsnorm_quant", [p] * 6 + [n, i, n, n, f, i, i, p]),
+            ("delta_add_rmsnorm_bwd", [p] * 7 + [n, i, i, i, p])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = i, args
+
+
+def _lib():
+    from . import load_library
+    global _lib
+    lib = load_library()
+    _lib = lambda: lib  # noqa: E731  (the library stays open for the process)
+    return lib
+
+
+def _raise(st):
+    from . import DeltaError, delta_last_error
+    raise DeltaError(st, delta_last_error())
+
+
+def _tensor(t, name, shape, dtype, device, strided=False):
+    """Check one tensor; with ``strided`` any non-negative strides with
+    contiguous rows are taken, else it has to be contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if strided:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _optional(t, name, shape, dtype, device):
+    return None if t is None else _tensor(t, name, shape, dtype, device)
+
+
+def _begin(x, name, dims, what="x"):
+    """dtype code and device of the operator's leading tensor"""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} needs CUDA tensors")
+    if dims and x.dim() != dims:
+        raise ValueError(f"{what} must have {dims} axes, got shape {tuple(x.shape)}")
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be bfloat16 or float32, got {x.dtype}")
+    return code, dev
+
+
+class _On:
+    """The stream of a call, and allocation for it."""
+
+    __slots__ = ("raw", "side", "dev")
+
+    def __init__(self, dev, stream):
+        self.dev, self.side = dev, stream
+        self.raw = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+    def empty(self, shape, dtype):
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.side):
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def out(self, t, name, shape, dtype):
+        if t is None:
+            return self.empty(shape, dtype)
+        _tensor(t, name, shape, dtype, self.dev)
+        return t
+
+
+def _scan_form(form, dt):
+    code = _SCAN_FORMS.get(form)
+    if code is None:
+        raise ValueError(f"form must be one of {sorted(_SCAN_FORMS)}, got {form!r}")
+    return code, (torch.float32 if code == DELTA_SCAN_LINEAR else dt)
+
+
+def delta_scan_fwd(x, gate, h0=None, *, form="sigmoid", lengths=None, save_states=False,
+                   out=None, hT=None, stream=None):
+    """Gated linear recurrence ``h_t = a_t h_{t-1} + u_t x_t`` per channel.
+
+    x [B,T,D] bfloat16 or float32.  ``form="sigmoid"``: gate [B,T,D] in x's
+    type holds logits, a = sigmoid(gate), u = 1 - a.  ``form="linear"``: gate
+    [B,T,D] float32 is a itself, u = 1, and a = 0 drops the state whatever it
+    holds.  x and gate may be slices (contiguous last axis).  h0 [B,D] float32
+    or None; lengths [B] int32: later steps are not read, leave the state
+    alone and have out = 0.  Returns ``(out [B,T,D], hT [B,D] float32)``, and
+    with ``save_states`` the states [B, ceil(T/64), D] that ``delta_scan_bwd``
+    takes.  ``hT`` may be ``h0`` to update the state in place.
+    """
+    code, dev = _begin(x, "delta_scan_fwd", 3)
+    B, T, D = x.shape
+    fcode, gdt = _scan_form(form, x.dtype)
+    px = _tensor(x, "x", x.shape, x.dtype, dev, True)
+    pg = _tensor(gate, "gate", x.shape, gdt, dev, True)
+    ph = _optional(h0, "h0", (B, D), torch.float32, dev)
+    pl = _optional(lengths, "lengths", (B,), torch.int32, dev)
+    on = _On(dev, stream)
+    out = on.out(out, "out", (B, T, D), x.dtype)
+    hT = on.out(hT, "hT", (B, D), torch.float32)
+    states = on.empty((B, -(-T // SCAN_BLOCK), D), torch.float32) if save_states else None
+    st = _lib().delta_scan_fwd(px, pg, ph, pl, out.data_ptr(), hT.data_ptr(),
+                               None if states is None else states.data_ptr(), B, T, D,
+                               x.stride(0), x.stride(1), gate.stride(0), gate.stride(1), code,
+                               fcode, on.raw)
+    if st:
+        _raise(st)
+    return (out, hT, states) if save_states else (out, hT)
+
+
+def delta_scan_step(x, gate, state, *, form="sigmoid", out=None, stream=None):
+    """One step of the recurrence: x, gate [B,D] (rows may be strided), state
+    [B,D] float32 updated in place.  Returns out [B,D] in x's type."""
+    code, dev = _begin(x, "delta_scan_step", 2)
+    B, D = x.shape
+    fcode, gdt = _scan_form(form, x.dtype)
+    px = _tensor(x, "x", x.shape, x.dtype, dev, True)
+    pg = _tensor(gate, "gate", x.shape, gdt, dev, True)
+    ps = _tensor(state, "state", x.shape, torch.float32, dev)
+    on = _On(dev, stream)
+    out = on.out(out, "out", x.shape, x.dtype)
+    st = _lib().delta_scan_step(px, pg, ps, out.data_ptr(), B, D, x.stride(0), gate.stride(0),
+                                code, fcode, on.raw)
+    if st:
+        _raise(st)
+    return out
+
+
+def delta_scan_bwd(x, gate, states, dout, dhT=None, *, form="sigmoid", lengths=None, stream=None):
+    """Gradients of ``delta_scan_fwd``: x, gate, lengths as there, the states
+    it saved, dout [B,T,D] contiguous in x's type, dhT [B,D] float32 or None.
+    Returns ``(dx, dgate, dh0)``: dx in x's type, dgate in gate's, dh0 float32.
+    """
+    code, dev = _begin(x, "delta_scan_bwd", 3)
+    B, T, D = x.shape
+    fcode, gdt = _scan_form(form, x.dtype)
+    px = _tensor(x, "x", x.shape, x.dtype, dev, True)
+    pg = _tensor(gate, "gate", x.shape, gdt, dev, True)
+    ps = _tensor(states, "states", (B, -(-T // SCAN_BLOCK), D), torch.float32, dev)
+    po = _tensor(dout, "dout", x.shape, x.dtype, dev)
+    pt = _optional(dhT, "dhT", (B, D), torch.float32, dev)
+    pl = _optional(lengths, "lengths", (B,), torch.int32, dev)
+    on = _On(dev, stream)
+    dx, dgate = on.empty(x.shape, x.dtype), on.empty(x.shape, gdt)
+    dh0 = on.empty((B, D), torch.float32)
+    st = _lib().delta_scan_bwd(px, pg, ps, pl, po, pt, dx.data_ptr(), dgate.data_ptr(),
+                               dh0.data_ptr(), B, T, D, x.stride(0), x.stride(1),
+                               gate.stride(0), gate.stride(1), code, fcode, on.raw)
+    if st:
+        _raise(st)
+    return dx, dgate, dh0
+
+
+def _rows(t, name, shape, dtype, dev):
+    """A tensor [..., D] as rows: pointer and row stride.  Leading axes must
+    fold into one."""
+    p = _tensor(t, name, shape, dtype, dev, True)
+    if t.dim() <= 2:
+        return p, t.stride(0) if t.dim() == 2 else t.shape[-1]
+    if not t.is_contiguous():
+        t = t.flatten(0, -2) if _folds(t) else None
+        if t is None:
+            raise ValueError(f"the leading axes of {name} must fold into one row axis")
+        return p, t.stride(0)
+    return p, t.shape[-1]
+
+
+def _folds(t):
+    axes = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    return all(s == n2 * s2 for (_, s), (n2, s2) in zip(axes, axes[1:]))
+
+
+def _weight(weight, D, dt, dev, name="weight"):
+    wdt = weight.dtype if isinstance(weight, torch.Tensor) else None
+    if wdt not in _CODES:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+    return _tensor(weight, name, (D,), wdt, dev), _CODES[wdt]
+
+
+def _norm_begin(x, weight, residual, name):
+    code, dev = _begin(x, name, 0)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    D = x.shape[-1]
+    px, ldx = _rows(x, "x", x.shape, x.dtype, dev)
+    pr, ldr = (None, D) if residual is None else _rows(residual, "residual", x.shape, x.dtype, dev)
+    pw, wcode = _weight(weight, D, x.dtype, dev)
+    rows = x.numel() // D if D else 0
+    return code, dev, D, rows, px, ldx, pr, ldr, pw, wcode
+
+
+def delta_add_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, sum_out=None, stream=None):
+    """``t = x + residual``, ``y = t * rsqrt(mean t^2 + eps) * weight`` over the
+    last axis (at most 8192 wide).
+
+    x, residual [..., D] bfloat16 or float32 (rows may be strided), weight [D]
+    float32 or bfloat16.  Returns ``(y, sum, rstd)``: y in x's type, sum = t
+    rounded to it (x itself without a residual), rstd [...] float32.
+    ``sum_out`` may be ``x`` or ``residual`` to update the stream in place.
+    """
+    code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
+                                                                 "delta_add_rmsnorm_fwd")
+    on = _On(dev, stream)
+    y, rstd = on.empty(x.shape, x.dtype), on.empty(x.shape[:-1], torch.float32)
+    if residual is not None:
+        sum_out = on.out(sum_out, "sum_out", x.shape, x.dtype)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual: without one the sum is x")
+    st = _lib().delta_add_rmsnorm_fwd(px, pr, pw, y.data_ptr(),
+                                      None if sum_out is None else sum_out.data_ptr(),
+                                      rstd.data_ptr(), rows, D, ldx, ldr, eps, code, wcode, on.raw)
+    if st:
+        _raise(st)
+    return y, (x if sum_out is None else sum_out), rstd
+
+
+def delta_add_rmsnorm_quant(x, weight, residual=None, *, eps=1e-6, sum_out=None, stream=None):
+    """The same with y in e4m3 and one float32 scale a row (max |y| / 448; 1
+    for a row of zeros).  Returns ``(y float8_e4m3fn, scale [...], sum)``."""
+    code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
+                                                                 "delta_add_rmsnorm_quant")
+    on = _On(dev, stream)
+    y, scale = on.empty(x.shape, E4M3), on.empty(x.shape[:-1], torch.float32)
+    if residual is not None:
+        sum_out = on.out(sum_out, "sum_out", x.shape, x.dtype)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual: without one the sum is x")
+    st = _lib().delta_add_rmsnorm_quant(px, pr, pw, y.data_ptr(), scale.data_ptr(),
+                                        None if sum_out is None else sum_out.data_ptr(), rows, D,
+                                        ldx, ldr, eps, code, wcode, on.raw)
+    if st:
+        _raise(st)
+    return y, scale, (x if sum_out is None else sum_out)
+
+
+def delta_add_rmsnorm_bwd(dy, sum, weight, rstd, dsum=None, *, dx=None, stream=None):
+    """Gradients of ``delta_add_rmsnorm_fwd``: dy and the forward's sum [..., D]
+    (contiguous, one type), rstd, and dsum, the gradient that arrives at sum,
+    or None.  Returns ``(dx, dweight)``: dx (of x and of residual alike) in
+    dy's type, dweight [D] float32.  ``dx`` may be ``dy`` or ``dsum``."""
+    code, dev = _begin(dy, "delta_add_rmsnorm_bwd", 0, "dy")
+    if dy.dim() < 1:
+        raise ValueError("dy must have at least one axis")
+    D = dy.shape[-1]
+    py = _tensor(dy, "dy", dy.shape, dy.dtype, dev)
+    ps = _tensor(sum, "sum", dy.shape, dy.dtype, dev)
+    pd = _optional(dsum, "dsum", dy.shape, dy.dtype, dev)
+    pr = _tensor(rstd, "rstd", dy.shape[:-1], torch.float32, dev)
+    pw, wcode = _weight(weight, D, dy.dtype, dev)
+    on = _On(dev, stream)
+    dx = on.out(dx, "dx", dy.shape, dy.dtype)
+    dweight = on.empty((D,), torch.float32)
+    st = _lib().delta_add_rmsnorm_bwd(py, ps, pw, pr, pd, dx.data_ptr(), dweight.data_ptr(),
+                                      dy.numel() // D if D else 0, D, code, wcode, on.raw)
+    if st:
+        _raise(st)
+    return dx, dweight

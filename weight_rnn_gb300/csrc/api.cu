@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "../../include/delta.h"
+#include "api_common.h"
 #include "kernels.h"
 
 // Scratch of delta_fwd_static_scratch: the T tiles of at most 4096 chunks
@@ -21,7 +22,8 @@
 constexpr int64_t kStaticScratchBytes = int64_t(32) << 20;
 static __device__ __align__(256) unsigned char g_static_scratch[kStaticScratchBytes];
 
-namespace {
+namespace delta {
+namespace api {
 
 thread_local char g_last_error[256] = "no error";
 // calls still to fail on purpose (delta_inject_failure)
@@ -35,7 +37,6 @@ bool take_injection() {
   return false;
 }
 
-int fail(int status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int status, const char *fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -49,28 +50,15 @@ int cuda_fail(cudaError_t err, const char *what) {
               cudaGetErrorString(err));
 }
 
-bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool supported_chunk(int c) { return c == 16 || c == 32 || c == 64; }
-bool aligned16(const void *p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Range range(const void *p, int64_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{lo, lo + (uintptr_t)bytes};
-}
-bool overlap(Range a, Range b) {
-  return a.lo != 0 && b.lo != 0 && a.hi > a.lo && b.hi > b.lo && a.lo < b.hi && b.lo < a.hi;
-}
-
-// Scratch for the T tiles handed from the UT pass to the state pass: stream-
-// ordered allocations from one memory pool per device, owned by the library,
-// that keeps freed memory for reuse (release threshold: unlimited), so calls
-// after the first reuse it without reaching the driver.
-constexpr int kMaxDevices = 64;
+// Scratch (the T tiles handed from the UT pass to the state pass, and the other
+// calls' workspaces): stream-ordered allocations from one memory pool per
+// device, owned by the library, that keeps freed memory for reuse (release
+// threshold: unlimited), so calls after the first reuse it without reaching
+// the driver.
+namespace {
 std::mutex g_pool_mu;
 cudaMemPool_t g_pool[kMaxDevices] = {};
+}  // namespace
 
 cudaError_t scratch_pool(cudaMemPool_t *out) {
   int dev = 0;
@@ -97,6 +85,16 @@ cudaError_t scratch_pool(cudaMemPool_t *out) {
   *out = g_pool[dev];
   return cudaSuccess;
 }
+
+}  // namespace api
+}  // namespace delta
+
+namespace {
+
+using namespace delta::api;
+
+bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool supported_chunk(int c) { return c == 16 || c == 32 || c == 64; }
 
 // Device address of g_static_scratch on the current device, looked up (with
 // that device current) the first time each device asks.

@@ -1,0 +1,293 @@
+// block_api.cu -- the C ABI of the operators that stand around the token
+// mixers in a block (scan, norm): argument checks, scratch and launches, with
+// the conventions of api.cu: nothing is synchronised, errors are returned
+// before anything is enqueued.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/delta.h"
+#include "api_common.h"
+#include "kernels.h"
+
+namespace {
+
+using namespace delta::api;
+
+constexpr int64_t kMaxElems = int64_t(1) << 40;  // products of sizes stay far inside 64 bits
+
+int64_t esize(delta_dtype dt) { return dt == DELTA_BF16 ? 2 : 4; }
+
+int check_dtype(delta_dtype dt) {
+  return dt == DELTA_F32 || dt == DELTA_BF16 ? DELTA_OK : fail(DELTA_ERR_INVALID, "unknown dtype %d", (int)dt);
+}
+
+bool aligned_to(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)n == 0; }
+
+// no output may overlap an input or another output; where one may be updated
+// in place the caller leaves that pair out
+struct Span {
+  const char *name;
+  Range r;
+};
+template <int NO, int NI>
+int check_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < NI; ++j)
+      if (overlap(outs[i].r, ins[j].r))
+        return fail(DELTA_ERR_INVALID, "%s overlaps %s", outs[i].name, ins[j].name);
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(outs[i].r, outs[j].r))
+        return fail(DELTA_ERR_INVALID, "%s overlaps %s", outs[i].name, outs[j].name);
+  }
+  return DELTA_OK;
+}
+
+// bytes from the first to the last element of a [B][T][D] view
+int64_t view_bytes(int64_t B, int64_t T, int64_t D, int64_t sb, int64_t st, int64_t e) {
+  return ((B - 1) * sb + (T - 1) * st + D) * e;
+}
+
+int scan_sizes(int B, int T, int D, int64_t x_sb, int64_t x_st, int64_t g_sb, int64_t g_st,
+               delta_dtype dtype, delta_scan_form form, delta::ScanArgs &a) {
+  if (B < 0 || T < 0 || D < 0) return fail(DELTA_ERR_INVALID, "negative size B=%d T=%d D=%d", B, T, D);
+  int st;
+  if ((st = check_dtype(dtype)) != DELTA_OK) return st;
+  if (form != DELTA_SCAN_LINEAR && form != DELTA_SCAN_SIGMOID)
+    return fail(DELTA_ERR_INVALID, "unknown scan form %d", (int)form);
+  a.B = B; a.T = T; a.D = D;
+  // the stride of an axis with one entry is never used
+  a.x_sb = B > 1 ? x_sb : 0; a.x_st = T > 1 ? x_st : 0;
+  a.g_sb = B > 1 ? g_sb : 0; a.g_st = T > 1 ? g_st : 0;
+  a.bf16 = dtype == DELTA_BF16;
+  a.sigmoid = form == DELTA_SCAN_SIGMOID;
+  if ((int64_t)B * T >= kMaxElems / (D > 0 ? D : 1))
+    return fail(DELTA_ERR_UNSUPPORTED, "B*T*D too large");
+  for (const int64_t s : {a.x_sb, a.x_st, a.g_sb, a.g_st})
+    if (s < 0 || s >= kMaxElems) return fail(DELTA_ERR_INVALID, "stride %lld out of range", (long long)s);
+  if ((B > 1 && a.x_sb >= kMaxElems / B) || (T > 1 && a.x_st >= kMaxElems / T) ||
+      (B > 1 && a.g_sb >= kMaxElems / B) || (T > 1 && a.g_st >= kMaxElems / T))
+    return fail(DELTA_ERR_UNSUPPORTED, "strides too large");
+  // one CTA (of a cluster of at most 8) per row and 32 channels
+  if ((int64_t)B * ((D + 31) / 32) >= (int64_t(1) << 31) / 8)
+    return fail(DELTA_ERR_UNSUPPORTED, "B*D=%lld too large", (long long)B * D);
+  return DELTA_OK;
+}
+
+int scan_pointers(const delta::ScanArgs &a, delta_dtype dtype) {
+  if (!a.x || !a.gate) return fail(DELTA_ERR_INVALID, "x and gate must be non-NULL");
+  const int64_t e = esize(dtype), ge = a.sigmoid ? e : 4;
+  if (!aligned_to(a.x, e) || !aligned_to(a.gate, ge) || !aligned_to(a.lengths, 4))
+    return fail(DELTA_ERR_ALIGN, "x, gate and lengths must be aligned to their elements");
+  return DELTA_OK;
+}
+
+Span span_x(const delta::ScanArgs &a, delta_dtype dt) {
+  return {"x", range(a.x, view_bytes(a.B, a.T, a.D, a.x_sb, a.x_st, esize(dt)))};
+}
+Span span_gate(const delta::ScanArgs &a, delta_dtype dt) {
+  return {"gate", range(a.gate, view_bytes(a.B, a.T, a.D, a.g_sb, a.g_st, a.sigmoid ? esize(dt) : 4))};
+}
+
+int norm_sizes(int64_t rows, int D, int64_t ldx, int64_t ldr, float eps, delta_dtype dtype,
+               delta_dtype wdtype) {
+  if (rows < 0 || D < 0) return fail(DELTA_ERR_INVALID, "negative size rows=%lld D=%d", (long long)rows, D);
+  int st;
+  if ((st = check_dtype(dtype)) != DELTA_OK || (st = check_dtype(wdtype)) != DELTA_OK) return st;
+  if (!(eps > 0.f)) return fail(DELTA_ERR_INVALID, "eps=%g must be positive", (double)eps);
+  if (D > delta::kNormMaxD)
+    return fail(DELTA_ERR_UNSUPPORTED, "D=%d: the norm is built for D <= %d", D, delta::kNormMaxD);
+  if (rows >= kMaxElems / (D > 0 ? D : 1)) return fail(DELTA_ERR_UNSUPPORTED, "rows*D too large");
+  if (rows > 1 && (ldx < D || ldr < D || ldx >= kMaxElems / rows || ldr >= kMaxElems / rows))
+    return fail(DELTA_ERR_INVALID, "row strides %lld, %lld must be at least D=%d", (long long)ldx,
+                (long long)ldr, D);
+  return DELTA_OK;
+}
+
+int run_norm_fwd(const void *x, const void *residual, const void *weight, void *y, float *scale,
+                 void *sum_out, float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
+                 delta_dtype dtype, delta_dtype wdtype, bool quant, struct CUstream_st *stream) {
+  int st;
+  if ((st = norm_sizes(rows, D, ldx, residual ? ldr : D, eps, dtype, wdtype)) != DELTA_OK) return st;
+  if (rows == 0 || D == 0) return DELTA_OK;
+  if (!x || !weight || !y || (quant && !scale))
+    return fail(DELTA_ERR_INVALID, "x, weight, the output and its scales must be non-NULL");
+  if (sum_out && !residual) return fail(DELTA_ERR_INVALID, "sum_out without a residual: the sum is x");
+  const int64_t e = esize(dtype), we = esize(wdtype);
+  if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned_to(weight, we))
+    return fail(DELTA_ERR_ALIGN, "x, residual and weight must be aligned to their elements");
+  if (!aligned16(y) || !aligned16(sum_out) || !aligned16(rstd) || !aligned16(scale))
+    return fail(DELTA_ERR_ALIGN, "every output must be 16-byte aligned");
+  const Span xs = {"x", range(x, ((rows - 1) * ldx + D) * e)};
+  const Span rs = {"residual", range(residual, ((rows - 1) * ldr + D) * e)};
+  const Span ws = {"weight", range(weight, D * we)};
+  const Span ys = {"y", range(y, rows * D * (quant ? 1 : e))};
+  const Span ss = {"sum_out", range(sum_out, rows * D * e)};
+  const Span ds = {"rstd", range(rstd, rows * 4)}, cs = {"y_scale", range(scale, rows * 4)};
+  if ((st = check_overlap({ys, ds, cs}, {xs, rs, ws})) != DELTA_OK) return st;
+  if ((st = check_overlap({ss}, {ws, ys, ds, cs})) != DELTA_OK) return st;
+  // the residual stream may be updated in place: the same rows, or none
+  for (const Span &in : {xs, rs}) {
+    const bool same = in.r.lo == ss.r.lo && (rows == 1 || (in.r.lo == rs.r.lo ? ldr : ldx) == D);
+    if (overlap(ss.r, in.r) && !same) return fail(DELTA_ERR_INVALID, "sum_out partly overlaps %s", in.name);
+  }
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  delta::NormArgs a{};
+  a.x = x; a.residual = residual; a.weight = weight; a.y = y; a.sum = sum_out; a.rstd = rstd;
+  a.scale = quant ? scale : nullptr;
+  a.rows = rows; a.D = D; a.ldx = rows > 1 ? ldx : 0; a.ldr = rows > 1 ? ldr : 0;
+  a.eps = eps; a.bf16 = dtype == DELTA_BF16; a.w_bf16 = wdtype == DELTA_BF16;
+  const cudaError_t err = delta::launch_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "norm kernel launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+int delta_scan_fwd(const void *x, const void *gate, const float *h0, const int *lengths, void *out,
+                   float *hT, float *states, int B, int T, int D, int64_t x_sb, int64_t x_st,
+                   int64_t g_sb, int64_t g_st, delta_dtype dtype, delta_scan_form form,
+                   struct CUstream_st *stream) {
+  delta::ScanArgs a{};
+  int st;
+  if ((st = scan_sizes(B, T, D, x_sb, x_st, g_sb, g_st, dtype, form, a)) != DELTA_OK) return st;
+  if (a.B * a.D == 0) return DELTA_OK;
+  a.x = x; a.gate = gate; a.h0 = h0; a.lengths = lengths; a.out = out; a.hT = hT; a.states = states;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!aligned16(h0) || !aligned16(out) || !aligned16(hT) || !aligned16(states))
+    return fail(DELTA_ERR_ALIGN, "h0, out, hT and states must be 16-byte aligned");
+  const int64_t n = a.B * a.D;
+  const Span hs = {"h0", range(h0, n * 4)}, ts = {"hT", range(hT, n * 4)};
+  if (hT != h0 && overlap(ts.r, hs.r)) return fail(DELTA_ERR_INVALID, "hT partly overlaps h0");
+  if (T == 0) {
+    if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+    const cudaError_t err = delta::launch_scan_passthrough(h0, hT, n, s);
+    return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "state passthrough");
+  }
+  if ((st = scan_pointers(a, dtype)) != DELTA_OK) return st;
+  if (!out) return fail(DELTA_ERR_INVALID, "out must be non-NULL");
+  const Span xs = span_x(a, dtype), gs = span_gate(a, dtype), ls = {"lengths", range(lengths, B * 4)};
+  const Span os = {"out", range(out, n * T * esize(dtype))};
+  const Span ss = {"states", range(states, n * ((T + delta::kScanBlock - 1) / delta::kScanBlock) * 4)};
+  if ((st = check_overlap({os, ss}, {xs, gs, ls, hs})) != DELTA_OK) return st;
+  if ((st = check_overlap({ts}, {xs, gs, ls, os, ss})) != DELTA_OK) return st;
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  const cudaError_t err = delta::launch_scan_fwd(a, s);
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "scan kernel launch");
+}
+
+int delta_scan_step(const void *x, const void *gate, float *state, void *out, int B, int D, int64_t x_sb,
+                    int64_t g_sb, delta_dtype dtype, delta_scan_form form, struct CUstream_st *stream) {
+  delta::ScanArgs a{};
+  int st;
+  if ((st = scan_sizes(B, 1, D, x_sb, 0, g_sb, 0, dtype, form, a)) != DELTA_OK) return st;
+  if (a.B * a.D == 0) return DELTA_OK;
+  a.x = x; a.gate = gate; a.h0 = state; a.hT = state; a.out = out;
+  if ((st = scan_pointers(a, dtype)) != DELTA_OK) return st;
+  if (!state || !out) return fail(DELTA_ERR_INVALID, "state and out must be non-NULL");
+  if (!aligned16(state) || !aligned16(out)) return fail(DELTA_ERR_ALIGN, "state and out must be 16-byte aligned");
+  const int64_t n = a.B * a.D;
+  if ((st = check_overlap({Span{"out", range(out, n * esize(dtype))}, Span{"state", range(state, n * 4)}},
+                          {span_x(a, dtype), span_gate(a, dtype)})) != DELTA_OK)
+    return st;
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  const cudaError_t err = delta::launch_scan_step(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "scan step launch");
+}
+
+int delta_scan_bwd(const void *x, const void *gate, const float *states, const int *lengths,
+                   const void *dout, const float *dhT, void *dx, void *dgate, float *dh0, int B, int T,
+                   int D, int64_t x_sb, int64_t x_st, int64_t g_sb, int64_t g_st, delta_dtype dtype,
+                   delta_scan_form form, struct CUstream_st *stream) {
+  delta::ScanBwdArgs a{};
+  int st;
+  if ((st = scan_sizes(B, T, D, x_sb, x_st, g_sb, g_st, dtype, form, a)) != DELTA_OK) return st;
+  if (a.B * a.D == 0) return DELTA_OK;
+  a.x = x; a.gate = gate; a.states = const_cast<float *>(states); a.lengths = lengths;
+  a.dout = dout; a.dhT = dhT; a.dx = dx; a.dgate = dgate; a.dh0 = dh0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!aligned16(states) || !aligned16(dout) || !aligned16(dhT) || !aligned16(dx) || !aligned16(dgate) ||
+      !aligned16(dh0))
+    return fail(DELTA_ERR_ALIGN, "states, dout, dhT and the gradients must be 16-byte aligned");
+  const int64_t n = a.B * a.D;
+  const Span hs = {"dhT", range(dhT, n * 4)}, zs = {"dh0", range(dh0, n * 4)};
+  if (dh0 != dhT && overlap(zs.r, hs.r)) return fail(DELTA_ERR_INVALID, "dh0 partly overlaps dhT");
+  if (T == 0) {
+    if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+    const cudaError_t err = delta::launch_scan_passthrough(dhT, dh0, n, s);
+    return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "state passthrough");
+  }
+  if ((st = scan_pointers(a, dtype)) != DELTA_OK) return st;
+  if (!states || !dout || !dx || !dgate)
+    return fail(DELTA_ERR_INVALID, "states, dout, dx and dgate must be non-NULL");
+  const int64_t e = esize(dtype);
+  const Span xs = span_x(a, dtype), gs = span_gate(a, dtype), ls = {"lengths", range(lengths, B * 4)};
+  const Span ss = {"states", range(states, n * ((T + delta::kScanBlock - 1) / delta::kScanBlock) * 4)};
+  const Span os = {"dout", range(dout, n * T * e)};
+  const Span dxs = {"dx", range(dx, n * T * e)}, dgs = {"dgate", range(dgate, n * T * (a.sigmoid ? e : 4))};
+  if ((st = check_overlap({dxs, dgs}, {xs, gs, ls, ss, os, hs})) != DELTA_OK) return st;
+  if ((st = check_overlap({zs}, {xs, gs, ls, ss, os, dxs, dgs})) != DELTA_OK) return st;
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  const cudaError_t err = delta::launch_scan_bwd(a, s);
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "scan backward launch");
+}
+
+int delta_add_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *y, void *sum_out,
+                          float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
+                          delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream) {
+  return run_norm_fwd(x, residual, weight, y, nullptr, sum_out, rstd, rows, D, ldx, ldr, eps, dtype,
+                      wdtype, false, stream);
+}
+
+int delta_add_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *y, float *y_scale,
+                            void *sum_out, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
+                            delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream) {
+  return run_norm_fwd(x, residual, weight, y, y_scale, sum_out, nullptr, rows, D, ldx, ldr, eps, dtype,
+                      wdtype, true, stream);
+}
+
+int delta_add_rmsnorm_bwd(const void *dy, const void *sum, const void *weight, const float *rstd,
+                          const void *dsum, void *dx, float *dweight, int64_t rows, int D,
+                          delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream) {
+  int st;
+  if ((st = norm_sizes(rows, D, D, D, 1.f, dtype, wdtype)) != DELTA_OK) return st;
+  if (D == 0) return DELTA_OK;
+  if (!dweight || !weight) return fail(DELTA_ERR_INVALID, "weight and dweight must be non-NULL");
+  if (rows > 0 && (!dy || !sum || !rstd || !dx))
+    return fail(DELTA_ERR_INVALID, "dy, sum, rstd and dx must be non-NULL");
+  const int64_t e = esize(dtype), we = esize(wdtype);
+  if (!aligned16(dy) || !aligned16(sum) || !aligned16(dsum) || !aligned16(dx) || !aligned16(rstd) ||
+      !aligned16(dweight) || !aligned_to(weight, we))
+    return fail(DELTA_ERR_ALIGN, "every pointer must be 16-byte aligned (weight: to its elements)");
+  const Span ys = {"dy", range(dy, rows * D * e)}, ss = {"sum", range(sum, rows * D * e)};
+  const Span gs = {"dsum", range(dsum, rows * D * e)}, ws = {"weight", range(weight, D * we)};
+  const Span rs = {"rstd", range(rstd, rows * 4)};
+  const Span xs = {"dx", range(dx, rows * D * e)}, dws = {"dweight", range(dweight, (int64_t)D * 4)};
+  if ((st = check_overlap({xs, dws}, {ss, ws, rs})) != DELTA_OK) return st;
+  if ((st = check_overlap({dws}, {ys, gs})) != DELTA_OK) return st;
+  for (const Span &in : {ys, gs})  // dx may take dy's or dsum's place
+    if (overlap(xs.r, in.r) && xs.r.lo != in.r.lo)
+      return fail(DELTA_ERR_INVALID, "dx partly overlaps %s", in.name);
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  delta::NormBwdArgs a{};
+  a.dy = dy; a.sum = sum; a.weight = weight; a.rstd = rstd; a.dsum = dsum; a.dx = dx; a.dweight = dweight;
+  a.rows = rows; a.D = D; a.bf16 = dtype == DELTA_BF16; a.w_bf16 = wdtype == DELTA_BF16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  const int64_t n = delta::norm_bwd_ctas(a) * D;
+  void *scr = nullptr;
+  if (n > 0) {
+    cudaMemPool_t pool;
+    if ((err = scratch_pool(&pool)) != cudaSuccess) return cuda_fail(err, "scratch pool");
+    if ((err = cudaMallocFromPoolAsync(&scr, (size_t)n * 4, pool, s)) != cudaSuccess)
+      return cuda_fail(err, "scratch allocation");
+  }
+  a.partial = static_cast<float *>(scr);
+  err = delta::launch_norm_bwd(a, s);
+  const cudaError_t ef = scr ? cudaFreeAsync(scr, s) : cudaSuccess;
+  if (err != cudaSuccess) return cuda_fail(err, "norm backward launch");
+  return ef == cudaSuccess ? DELTA_OK : cuda_fail(ef, "scratch release");
+}
+
+}  // extern "C"

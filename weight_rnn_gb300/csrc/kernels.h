@@ -118,4 +118,55 @@ cudaError_t launch_attention_map(const void *q, const void *k, const float *beta
                                  float *attn, int64_t B, int64_t H, int N, int dk, bool bf16,
                                  cudaStream_t s);
 
+// The gated linear recurrence (scan.cu).  x, gate: element strides of the batch
+// row (sb) and the step (st), channels contiguous; everything else contiguous.
+// gate is float32 in the linear form, in x's type in the sigmoid form.
+constexpr int kScanBlock = 64;  // steps between two saved states
+struct ScanArgs {
+  const void *x, *gate;
+  const float *h0;       // nullptr: 0
+  const int *lengths;    // [B], clamped to [0, T]; nullptr: T
+  void *out;
+  float *hT, *states;    // states [B][ceil(T / kScanBlock)][D] or nullptr
+  int64_t B, T, D, x_sb, x_st, g_sb, g_st;
+  bool bf16, sigmoid;
+};
+struct ScanBwdArgs : ScanArgs {  // states is read; out, hT and h0 are unused
+  const void *dout;
+  const float *dhT;      // nullptr: 0
+  void *dx, *dgate;
+  float *dh0;            // or nullptr
+};
+cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanBwdArgs &a, cudaStream_t s);
+// one token: h0 is the state before and hT the state after (the same memory)
+cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s);
+// hT <- h0 (or 0): a sequence without steps
+cudaError_t launch_scan_passthrough(const float *h0, float *hT, int64_t n, cudaStream_t s);
+
+// Residual addition and RMS norm (norm.cu), rows of D elements.  Row strides
+// ld* in elements; weight is float32 or, with w_bf16, bfloat16.
+struct NormArgs {
+  const void *x, *residual;  // residual nullptr: the sum is x and is not written
+  const void *weight;
+  void *y;                   // input type, or e4m3 with scale set
+  void *sum;                 // [rows][D] contiguous
+  float *rstd, *scale;       // [rows]; nullptr: not written
+  int64_t rows, D, ldx, ldr;
+  float eps;
+  bool bf16, w_bf16;
+};
+struct NormBwdArgs {
+  const void *dy, *sum, *weight, *dsum;  // dsum nullptr: 0
+  const float *rstd;
+  void *dx;
+  float *dweight, *partial;  // partial [norm_bwd_ctas()][D]
+  int64_t rows, D;
+  bool bf16, w_bf16;
+};
+constexpr int kNormMaxD = 8192;
+cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s);
+int64_t norm_bwd_ctas(const NormBwdArgs &a);
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t s);
+
 }  // namespace delta

@@ -1,0 +1,368 @@
+// norm.cu -- the residual addition with the root-mean-square norm:
+//
+//   t = x + r,   rstd = (mean_d t_d^2 + eps)^{-1/2},   y = t rstd w
+//
+// t goes out in the input type (the residual stream), y in the input type or
+// in e4m3 with one float32 scale a row (scale = max |y| / 448, q = y / scale).
+// The norm is taken of the float32 sum, before that is rounded for the stream.
+// Gradient, with t^ = t rstd:
+//
+//   dx = rstd (w dy - t^ mean_d(w dy t^)) + dsum,   dw = sum over rows of dy t^
+//
+// HBM-bound: two tensors in and two out (8 bytes an element in bfloat16, 7
+// with an 8-bit y; backward three in, one out).  A row stays in registers
+// between its reductions: a row has `nt` threads of kPer 16-byte vectors, and
+// the CTAs walk the rows with the next row's loads in flight, so that the
+// weight is read once a CTA and the backward keeps its column sums in
+// registers.  Those sums meet in a second kernel in CTA order, so the result
+// does not depend on scheduling.  Rows whose width, strides or addresses are
+// not multiples of 16 bytes take one element per load instead.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+
+namespace delta {
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr int kMostThreads = 512;  // of a CTA: 128 registers a thread
+
+// V elements: one 16-byte vector, or a single element
+template <typename T, int V>
+struct Pack {
+  T v[V];
+};
+template <typename T, int V>
+struct __align__(sizeof(T) * V) APack : Pack<T, V> {};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float x, float &r) { r = x; }
+__device__ __forceinline__ void from_f(float x, __nv_bfloat16 &r) { r = __float2bfloat16_rn(x); }
+
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T *p, const float (&v)[V]) {
+  APack<T, V> o;
+#pragma unroll
+  for (int i = 0; i < V; ++i) from_f(v[i], o.v[i]);
+  *reinterpret_cast<APack<T, V> *>(p) = o;
+}
+
+// V values to e4m3, saturating, round to nearest even
+template <int V>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    struct __align__(V) { __nv_fp8x2_storage_t h[V / 2]; } o;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      o.h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<decltype(o) *>(p) = o;
+  }
+}
+
+// One row's reduction over its nt threads (a multiple of 32): warp shuffles,
+// then the row's warps meet in `part`.  Every thread gets the same sum, taken
+// in the same order.  `part` alternates between calls, so one barrier a call
+// is enough.
+template <bool kMax>
+__device__ __forceinline__ float join(float a, float b) { return kMax ? fmaxf(a, b) : a + b; }
+template <bool kMax>
+__device__ __forceinline__ float row_reduce(float v, float *part, int nwarp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (nwarp == 1) return v;  // the same for every row of the CTA
+  const int w = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.y * 32 + w] = v;
+  __syncthreads();
+  v = part[threadIdx.y * 32];
+  for (int i = 1; i < nwarp; ++i) v = join<kMax>(v, part[threadIdx.y * 32 + i]);
+  return v;
+}
+
+// weights of this thread's elements, float32 in registers
+template <int V, int kPer>
+__device__ __forceinline__ void load_weight(const void *weight, bool w_bf16, int64_t D, float (&w)[kPer][V]) {
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V + i;
+      w[j][i] = d >= D ? 0.f
+                : w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(weight)[d])
+                         : static_cast<const float *>(weight)[d];
+    }
+}
+
+// ------------------------------------------------------------------ forward
+// blockDim (nt, rows a CTA); a thread's vectors are nt apart
+template <typename In, int V, int kPer, bool kQuant>
+__global__ void __launch_bounds__(kMostThreads) norm_fwd_kernel(NormArgs p) {
+  __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
+  using Vec = APack<In, V>;
+  const int nwarp = blockDim.x >> 5;
+  const In *x = static_cast<const In *>(p.x), *r = static_cast<const In *>(p.residual);
+  float w[kPer][V];
+  load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  Vec xv[kPer], rv[kPer];
+  auto fetch = [&](int64_t row) {
+    if (row >= p.rows) return;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+      if (d < p.D) {
+        xv[j] = *reinterpret_cast<const Vec *>(x + row * p.ldx + d);
+        if (r) rv[j] = *reinterpret_cast<const Vec *>(r + row * p.ldr + d);
+      }
+    }
+  };
+  fetch(first);
+  int buf = 0;
+  // every row of the CTA takes part in the barriers until the last is done
+  for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
+    float t[kPer][V], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool in = row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        t[j][i] = in ? to_f(xv[j].v[i]) + (r ? to_f(rv[j].v[i]) : 0.f) : 0.f;
+        ss = fmaf(t[j][i], t[j][i], ss);
+      }
+    }
+    fetch(row + step);
+    ss = row_reduce<false>(ss, part[kQuant ? 0 : buf], nwarp);
+    const float rstd = rsqrtf(ss / (float)p.D + p.eps);
+    float inv = 1.f;
+    if constexpr (kQuant) {
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(t[j][i] * rstd * w[j][i]));
+      top = row_reduce<true>(top, part[1], nwarp);
+      // a row of zeros, or of values too small for a float32 scale: scale 1
+      float scale = top / kE4m3Max;
+      if (scale < 1.1754944e-38f) scale = 1.f;
+      inv = 1.f / scale;
+      if (row < p.rows && threadIdx.x == 0) p.scale[row] = scale;
+    }
+    if (row < p.rows) {
+      if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+        if (d >= p.D) continue;
+        if (p.sum) store_v<In, V>(static_cast<In *>(p.sum) + row * p.D + d, t[j]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[j][i] = t[j][i] * rstd * w[j][i] * inv;
+        if constexpr (kQuant)
+          store_e4m3<V>(static_cast<uint8_t *>(p.y) + row * p.D + d, t[j]);
+        else
+          store_v<In, V>(static_cast<In *>(p.y) + row * p.D + d, t[j]);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- backward
+template <typename In, int V, int kPer>
+__global__ void __launch_bounds__(kMostThreads) norm_bwd_kernel(NormBwdArgs p) {
+  __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
+  using Vec = APack<In, V>;
+  const int nwarp = blockDim.x >> 5;
+  const In *dy = static_cast<const In *>(p.dy), *sum = static_cast<const In *>(p.sum),
+           *ds = static_cast<const In *>(p.dsum);
+  float w[kPer][V], dw[kPer][V];
+  load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  Vec gv[kPer], tv[kPer], sv[kPer];
+  float rs = 0.f;
+  auto fetch = [&](int64_t row) {
+    if (row >= p.rows) return;
+    rs = p.rstd[row];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+      if (d < p.D) {
+        gv[j] = *reinterpret_cast<const Vec *>(dy + row * p.D + d);
+        tv[j] = *reinterpret_cast<const Vec *>(sum + row * p.D + d);
+        if (ds) sv[j] = *reinterpret_cast<const Vec *>(ds + row * p.D + d);
+      }
+    }
+  };
+  fetch(first);
+  int buf = 0;
+  for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
+    float g[kPer][V], t[kPer][V], s[kPer][V], dot = 0.f;
+    const float rstd = rs;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool in = row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        t[j][i] = in ? to_f(tv[j].v[i]) * rstd : 0.f;
+        const float y = in ? to_f(gv[j].v[i]) : 0.f;
+        s[j][i] = in && ds ? to_f(sv[j].v[i]) : 0.f;
+        dw[j][i] = fmaf(y, t[j][i], dw[j][i]);
+        g[j][i] = y * w[j][i];
+        dot = fmaf(g[j][i], t[j][i], dot);
+      }
+    }
+    fetch(row + step);
+    dot = row_reduce<false>(dot, part[buf], nwarp) / (float)p.D;
+    if (row < p.rows) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+        if (d >= p.D) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[j][i] = fmaf(rstd, g[j][i] - t[j][i] * dot, s[j][i]);
+        store_v<In, V>(static_cast<In *>(p.dx) + row * p.D + d, g[j]);
+      }
+    }
+  }
+  const int64_t at = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.D;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V + i;
+      if (d < p.D) p.partial[at + d] = dw[j][i];
+    }
+}
+
+// dweight[d] = sum of n partial rows, 32 columns a CTA, in row order per
+// thread row and then over the 32 thread rows
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, float *dw, int64_t n, int64_t D) {
+  __shared__ float s[32][33];
+  const int64_t d = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  float v = 0.f;
+  if (d < D)
+    for (int64_t i = threadIdx.y; i < n; i += 32) v += partial[i * D + d];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  v = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && c < D) dw[c] = v;
+}
+
+// ------------------------------------------------------------------ launches
+struct Plan {
+  int V, per, nt, rpc;  // elements a vector, vectors a thread, threads a row, rows a CTA
+  int64_t grid;
+};
+
+bool vec_ok(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
+
+// One vector a thread while rows are few (latency), two where a row has more
+// than a warp's worth and there are rows for every SM (fewer, longer-lived
+// CTAs); more only where a row would not fit kMostThreads threads.
+Plan plan(int64_t rows, int64_t D, int vec, bool aligned) {
+  Plan q;
+  q.V = aligned ? vec : 1;
+  const int64_t n = (D + q.V - 1) / q.V;  // vectors a row
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (aligned)
+    q.per = rows >= 2 * sms && n > 32 ? 2 : 1;
+  else
+    q.per = n <= 256 ? 1 : 4;
+  while (n > (int64_t)q.per * kMostThreads) q.per *= 2;
+  q.nt = (int)((n + q.per - 1) / q.per + 31) / 32 * 32;
+  q.rpc = q.nt >= 256 ? 1 : 256 / q.nt;
+  const int64_t ctas = (rows + q.rpc - 1) / q.rpc;
+  const int64_t cap = (int64_t)sms * 4;
+  q.grid = ctas < cap ? ctas : cap;
+  return q;
+}
+
+// the instance for a plan: up to 4 (float32) or 2 (bfloat16) vectors of 16
+// bytes a thread, or up to 16 single elements, which covers kNormMaxD
+template <typename In, template <typename, int, int> class F, typename... X>
+cudaError_t dispatch(const Plan &q, X &&...x) {
+  constexpr int V = 16 / sizeof(In);
+  if (q.V == 1) switch (q.per) {
+      case 1: return F<In, 1, 1>::run(x...);
+      case 4: return F<In, 1, 4>::run(x...);
+      case 8: return F<In, 1, 8>::run(x...);
+      case 16: return F<In, 1, 16>::run(x...);
+    }
+  else switch (q.per) {
+      case 1: return F<In, V, 1>::run(x...);
+      case 2: return F<In, V, 2>::run(x...);
+      case 4:
+        if constexpr (V == 4) return F<In, V, 4>::run(x...);
+    }
+  return cudaErrorInvalidConfiguration;
+}
+
+template <typename In, int V, int kPer>
+struct FwdOne {
+  static cudaError_t run(const NormArgs &a, const Plan &q, cudaStream_t s) {
+    const dim3 block(q.nt, q.rpc);
+    if (a.scale)
+      norm_fwd_kernel<In, V, kPer, true><<<(unsigned)q.grid, block, 0, s>>>(a);
+    else
+      norm_fwd_kernel<In, V, kPer, false><<<(unsigned)q.grid, block, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
+template <typename In, int V, int kPer>
+struct BwdOne {
+  static cudaError_t run(const NormBwdArgs &a, const Plan &q, cudaStream_t s) {
+    norm_bwd_kernel<In, V, kPer><<<(unsigned)q.grid, dim3(q.nt, q.rpc), 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+template <typename In>
+cudaError_t fwd_all(const NormArgs &a, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(In);
+  const bool ok = a.D % V == 0 && a.ldx % V == 0 && (!a.residual || a.ldr % V == 0) && vec_ok(a.x) &&
+                  vec_ok(a.residual);
+  const Plan q = plan(a.rows, a.D, V, ok);
+  return dispatch<In, FwdOne>(q, a, q, s);
+}
+
+template <typename In>
+Plan bwd_plan(const NormBwdArgs &a) {
+  constexpr int V = 16 / sizeof(In);
+  return plan(a.rows, a.D, V, a.D % V == 0);
+}
+template <typename In>
+cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
+  const Plan q = bwd_plan<In>(a);
+  cudaError_t e = q.grid > 0 ? dispatch<In, BwdOne>(q, a, q, s) : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  norm_dw_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 32), 0, s>>>(a.partial, a.dweight, q.grid * q.rpc, a.D);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
+  return a.bf16 ? fwd_all<__nv_bfloat16>(a, s) : fwd_all<float>(a, s);
+}
+
+int64_t norm_bwd_ctas(const NormBwdArgs &a) {
+  const Plan q = a.bf16 ? bwd_plan<__nv_bfloat16>(a) : bwd_plan<float>(a);
+  return q.grid * q.rpc;
+}
+
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t s) {
+  return a.bf16 ? bwd_all<__nv_bfloat16>(a, s) : bwd_all<float>(a, s);
+}
+
+}  // namespace delta
