@@ -458,8 +458,9 @@ typedef enum {
  *
  *   h_t = a_t h_{t-1} + u_t x_t,   out_t = h_t,
  *
- * over B rows of T steps and D channels, a_t and u_t from the form above.  A
- * step with a_t = 0 drops the state whatever it holds (Inf and NaN included).
+ * over B rows of T steps and D channels, a_t and u_t from the form above.  In
+ * the linear form a step with a_t = 0 drops the state whatever it holds (Inf
+ * and NaN included); in the sigmoid form a logit of -Inf gives a_t = 0.
  *
  *   x       [B, T, D]  dtype    element strides x_sb, x_st, 1
  *   gate    [B, T, D]  float32 (linear) or dtype (sigmoid), strides g_sb, g_st, 1

@@ -2,31 +2,31 @@
 //
 //   h_t = a_t h_{t-1} + u_t x_t,   out_t = h_t
 //
-// linear form: a_t = gate_t (float32), u_t = 1; sigmoid form: a_t = sigma(f_t)
-// and u_t = 1 - a_t = sigma(-f_t), taken from the same exponential so that
-// neither loses digits when the other is close to 1.  a_t = 0 drops the past
+// linear form: a_t = gate_t (float32), u_t = 1, and a_t = 0 drops the past
 // whatever it holds (an infinite or NaN state does not cross a reset).
+// Sigmoid form: a_t = 1 / (1 + e), u_t = e / (1 + e) with e = exp(-f_t), so
+// that neither loses digits when the other is close to 1.
 //
 // Reverse: with c_T = dhT,  dh_t = dout_t + c_t  and  c_{t-1} = a_t dh_t;
 // dx_t = u_t dh_t, dgate_t = dh_t h_{t-1} (linear) or
 // dh_t a_t (u_t h_{t-1} - u_t x_t) (sigmoid), dh0 = c_0.
 //
 // Both directions are bound by HBM: every element is read once and written
-// once, about 20 operations each.  A recurrence step is the affine map
-// h -> a h + b, and maps compose: (A, B) after (A', B') is (A A', A B' + B).
-// So a tile of kTile = 64 steps of 32 VEC channels is cut into kWarps
-// sub-chunks of kSteps steps, one per warp, lane = VEC channels:
-//   1. each warp loads its steps into registers and composes its own map;
+// once.  A recurrence step is the affine map h -> a h + b, and maps compose:
+// (A, B) after (A', B') is (A A', A B' + B).  So a tile of 32 VEC channels is
+// cut into sub-chunks of consecutive steps, one per warp, lane = VEC channels:
+//   1. each warp takes its steps from its own ring in shared memory, filled
+//      kStages - 1 tiles ahead by asynchronous copies, and composes its map;
 //   2. the maps meet in shared memory (one barrier), and every warp folds
 //      them in time order onto the state carried from the last tile, which
 //      gives the state at its own start and, redundantly in every warp, the
 //      state carried to the next tile;
 //   3. each warp runs the recurrence again from its start and writes out.
-// The next tile's loads are issued before step 1's arithmetic.  Where the
-// (batch row, channel strip) pairs alone do not fill the GPU, a cluster of
-// `cs` CTAs takes cs neighbouring tiles at a time and exchanges one map per
-// CTA through distributed shared memory; the fold order is the time order, so
-// results do not depend on scheduling.  All maps and states are float32.
+// Where the (batch row, channel strip) pairs alone do not fill the GPU, a
+// cluster of `cs` CTAs takes cs neighbouring tiles at a time and exchanges one
+// map per CTA through distributed shared memory; the fold order is the time
+// order, so results do not depend on scheduling.  All maps and states are
+// float32; two channels of a lane go through packed float32 pairs.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -40,9 +40,11 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;
-constexpr int kSteps = 8;                // steps per warp and tile
-constexpr int kTile = kWarps * kSteps;   // steps between two saved states
-static_assert(kTile == kScanBlock, "a saved state per tile");
+constexpr int kStages = 3;               // tiles in a warp's ring
+constexpr int kFwdSteps = 16;            // steps per warp and tile
+constexpr int kBwdSteps = 8;             // (the reverse holds twice the values per step)
+static_assert(kScanBlock % kFwdSteps == 0 && kScanBlock == kWarps * kBwdSteps,
+              "states are saved at a warp's start, and taken at a reverse tile's");
 constexpr int kMaxCluster = 8;           // the portable cluster size
 
 // VEC neighbouring elements as they lie in memory
@@ -84,25 +86,98 @@ __device__ __forceinline__ void store(T *p, const float (&v)[VEC]) {
   __stcs(reinterpret_cast<typename Raw<T, VEC>::type *>(p), r);
 }
 
-// a and u of one element.  Sigmoid: with t = e^-|f| and r = 1 / (1 + t), the
-// larger of the pair is r and the smaller t r.
-template <bool kSig>
-__device__ __forceinline__ void gates(float g, float &a, float &u) {
-  if (kSig) {
-    const float t = __expf(-fabsf(g));
-    const float r = __fdividef(1.f, 1.f + t);
-    const float q = t * r;
-    a = g < 0.f ? q : r;  // NaN: both are NaN
-    u = g < 0.f ? r : q;
+// float32 pairs: one instruction for both channels
+__device__ __forceinline__ uint64_t pk(const float (&v)[2]) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v[0]), "f"(v[1]));
+  return r;
+}
+__device__ __forceinline__ void unpk(uint64_t r, float (&v)[2]) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(r));
+}
+template <int VEC>
+__device__ __forceinline__ void vfma(const float (&a)[VEC], const float (&b)[VEC], const float (&c)[VEC],
+                                     float (&d)[VEC]) {
+  if constexpr (VEC == 2) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)), "l"(pk(c)));
+    unpk(r, d);
   } else {
-    a = g;
-    u = 1.f;
+    d[0] = fmaf(a[0], b[0], c[0]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void vmul(const float (&a)[VEC], const float (&b)[VEC], float (&d)[VEC]) {
+  if constexpr (VEC == 2) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    unpk(r, d);
+  } else {
+    d[0] = a[0] * b[0];
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void vadd(const float (&a)[VEC], const float (&b)[VEC], float (&d)[VEC]) {
+  if constexpr (VEC == 2) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    unpk(r, d);
+  } else {
+    d[0] = a[0] + b[0];
   }
 }
 
-// a h + b; a = 0 drops h
-__device__ __forceinline__ float affine(float a, float h, float b) {
-  return a == 0.f ? b : fmaf(a, h, b);
+// d = a h + b, the step map; in the linear form a = 0 drops h
+template <bool kSig, int VEC>
+__device__ __forceinline__ void affine(const float (&a)[VEC], const float (&h)[VEC], const float (&b)[VEC],
+                                       float (&d)[VEC]) {
+  if constexpr (kSig) {
+    vfma(a, h, b, d);
+  } else {
+    float r[VEC];
+    vfma(a, h, b, r);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) d[i] = a[i] == 0.f ? b[i] : r[i];
+  }
+}
+// d = a h, likewise
+template <bool kSig, int VEC>
+__device__ __forceinline__ void decay(const float (&a)[VEC], const float (&h)[VEC], float (&d)[VEC]) {
+  float r[VEC];
+  vmul(a, h, r);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) d[i] = !kSig && a[i] == 0.f ? 0.f : r[i];
+}
+
+// a and u from the gate.  Sigmoid: e = 2^min(-f log2 e, 126) stays finite, so
+// that u = e / (1 + e) is 1 at f = -inf; taking 2^-126 off a then makes it
+// exactly 0 there, and changes no a above 2^-102.  The MUFU operations are
+// good to about 2^-22 and 2^-23.
+template <bool kSig, int VEC>
+__device__ __forceinline__ void gates(const float (&g)[VEC], float (&a)[VEC], float (&u)[VEC]) {
+  if constexpr (kSig) {
+    float e[VEC], l[VEC], one[VEC], low[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      l[i] = -1.4426950408889634f;
+      one[i] = 1.f;
+      low[i] = -1.1754943508222875e-38f;
+    }
+    vmul(g, l, e);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      asm("min.NaN.f32 %0, %1, %2;" : "=f"(e[i]) : "f"(e[i]), "f"(126.f));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(e[i]));
+    }
+    vadd(e, one, a);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a[i]) : "f"(a[i]));
+    vmul(e, a, u);
+    vadd(a, low, a);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) a[i] = g[i], u[i] = 1.f;
+  }
 }
 
 __device__ __forceinline__ int64_t row_length(const int *lengths, int64_t b, int64_t T) {
@@ -111,33 +186,79 @@ __device__ __forceinline__ int64_t row_length(const int *lengths, int64_t b, int
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
+// ---------------------------------------------------------- the warps' rings
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// S rows of a strip (32 VEC channels) into `to`, by one warp.  kWide: 16-byte
+// pieces, else a lane's own VEC elements.  Rows from n on and channels past D
+// are not read; their place is filled with zeros.
+template <typename T, int VEC, int S, bool kWide>
+__device__ __forceinline__ void ring_rows(T *to, const T *row, int64_t stride, int64_t n, int64_t left, int lane) {
+  constexpr int kPiece = kWide ? 16 / (int)sizeof(T) : VEC;  // elements
+  constexpr int kAcross = 32 * VEC / kPiece;                  // pieces a row
+  constexpr int kBytes = kPiece * (int)sizeof(T);
+#pragma unroll
+  for (int k = 0; k < S * kAcross / 32; ++k) {
+    const int i = k * 32 + lane, s = i / kAcross, c = (i % kAcross) * kPiece;
+    const bool in = s < n && c < left;
+    T *dst = to + s * 32 * VEC + c;
+    const T *src = row + (in ? s * stride + c : 0);
+    if constexpr (kBytes < 4) {  // a single 16-bit element: no asynchronous copy is that small
+      *dst = in ? *src : T(0.f);
+    } else {
+      const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+      const int bytes = in ? kBytes : 0;
+      if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(kBytes), "r"(bytes)
+                     : "memory");
+    }
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void ring_read(const T *at, float (&v)[VEC]) {
+  widen(*reinterpret_cast<const typename Raw<T, VEC>::type *>(at), v);
+}
+
+// one warp's map (or a CTA's): decays and offsets of a lane's channels
+template <int VEC, int kOffsets>
+struct Map {
+  float a[VEC], b[kOffsets][VEC];
+};
+
 // ------------------------------------------------------------------ forward
-template <typename In, bool kSig, int VEC, bool kCluster>
+template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
-  __shared__ float s_map[2][kWarps][2][VEC][32];
-  __shared__ float s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][2][VEC][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int S = kFwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ __align__(16) Map<VEC, 1> s_map[2][kWarps][32];
+  __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // the same for all lanes, also to the compiler
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
   const int64_t id = kCluster ? blockIdx.x / cs : blockIdx.x;
-  const int64_t b = id / strips, c0 = (id % strips) * (32 * VEC) + lane * VEC;
+  const int64_t b = id / strips, first = (id % strips) * kRow, c0 = first + lane * VEC;
   const bool live = c0 < p.D;
-  const int64_t len = row_length(p.lengths, b, p.T);
-  const int64_t tiles = (p.T + kTile - 1) / kTile;
-  const In *x = static_cast<const In *>(p.x) + b * p.x_sb + c0;
-  const Gate *g = static_cast<const Gate *>(p.gate) + b * p.g_sb + c0;
+  const int64_t len = row_length(p.lengths, b, p.T), left = p.D - first;
+  const int64_t tiles = (p.T + kTile - 1) / kTile, saved = (p.T + kScanBlock - 1) / kScanBlock;
+  const In *x = static_cast<const In *>(p.x) + b * p.x_sb + first;
+  const Gate *g = static_cast<const Gate *>(p.gate) + b * p.g_sb + first;
   In *out = static_cast<In *>(p.out) + b * p.T * p.D + c0;
+  In *rx = reinterpret_cast<In *>(ring) + warp * kStages * S * kRow;
+  Gate *rg = reinterpret_cast<Gate *>(ring + kWarps * kStages * S * kRow * sizeof(In)) + warp * kStages * S * kRow;
 
-  typename Raw<In, VEC>::type xr[kSteps];
-  typename Raw<Gate, VEC>::type gr[kSteps];
-  auto fetch = [&](int64_t tile) {
-    const int64_t t0 = tile * kTile + warp * kSteps;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      if (live && t0 + s < len) {
-        xr[s] = load<In, VEC>(x + (t0 + s) * p.x_st);
-        gr[s] = load<Gate, VEC>(g + (t0 + s) * p.g_st);
-      }
+  auto fetch = [&](int64_t tile, int slot) {
+    const int64_t t0 = tile * kTile + warp * S, n = len - t0;
+    if (n > 0) {
+      ring_rows<In, VEC, S, kWide>(rx + slot * S * kRow, x + t0 * p.x_st, p.x_st, n, left, lane);
+      ring_rows<Gate, VEC, S, kWide>(rg + slot * S * kRow, g + t0 * p.g_st, p.g_st, n, left, lane);
+    }
+    ring_commit();
   };
 
   float carry[VEC];
@@ -147,100 +268,119 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
   const int64_t rounds = (tiles + cs - 1) / cs;
   // every CTA of the cluster runs before any writes into its shared memory
   if (kCluster) cg::this_cluster().barrier_arrive();
-  fetch(rank);
-  if (kCluster) cg::this_cluster().barrier_wait();
-  for (int64_t it = 0; it < rounds; ++it) {
-    const int64_t tile = it * cs + rank, t0 = tile * kTile + warp * kSteps;
-    const int buf = (int)(it & 1);
-    float a[kSteps][VEC], u[kSteps][VEC];  // u: the whole input term
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (live && t0 + s < len) {
-        float xv[VEC], gv[VEC];
-        widen(xr[s], xv);
-        widen(gr[s], gv);
+  for (int i = 0; i < kStages - 1; ++i) fetch(rank + (int64_t)i * cs, i);
+  if (kCluster) cg::this_cluster().barrier_wait();
+  int slot = 0;
+  for (int64_t it = 0; it < rounds; ++it) {
+    const int64_t tile = it * cs + rank, t0 = tile * kTile + warp * S;
+    const int64_t n = len - t0;  // steps that count, if below S
+    const int buf = (int)(it & 1);
+    ring_wait<kStages - 2>();
+    __syncwarp();
+    fetch(tile + (int64_t)(kStages - 1) * cs, slot == 0 ? kStages - 1 : slot - 1);
+    float a[S][VEC], u[S][VEC];  // u: the whole input term
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      float xv[VEC], gv[VEC];
+      ring_read<In, VEC>(rx + (slot * S + s) * kRow + lane * VEC, xv);
+      ring_read<Gate, VEC>(rg + (slot * S + s) * kRow + lane * VEC, gv);
+      gates<kSig>(gv, a[s], u[s]);
+      vmul(u[s], xv, u[s]);
+    }
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    if (n < S) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          gates<kSig>(gv[i], a[s][i], u[s][i]);
-          u[s][i] *= xv[i];
+          a[s][i] = s < n ? a[s][i] : 1.f;
+          u[s][i] = s < n ? u[s][i] : 0.f;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) a[s][i] = 1.f, u[s][i] = 0.f;
-      }
     }
-    if (it + 1 < rounds) fetch(tile + cs);
+    {
+      Map<VEC, 1> m;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float A = 1.f, B = 0.f;
+      for (int i = 0; i < VEC; ++i) m.a[i] = a[0][i], m.b[0][i] = u[0][i];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        B = affine(a[s][i], B, u[s][i]);
-        A *= a[s][i];
+      for (int s = 1; s < S; ++s) {
+        affine<kSig>(a[s], m.b[0], u[s], m.b[0]);
+        vmul(m.a, a[s], m.a);
       }
-      s_map[buf][warp][0][i][lane] = A;
-      s_map[buf][warp][1][i][lane] = B;
+      s_map[buf][warp][lane] = m;
     }
     __syncthreads();
+    float h[VEC], start[VEC];
     if (kCluster) {
       // one map per CTA to every CTA of the cluster: warp w serves CTA w.  The
       // buffer written now was last read before the previous round's barrier.
       cg::cluster_group cluster = cg::this_cluster();
       if (warp < cs) {
-        float *to = cluster.map_shared_rank(&s_cta[buf][rank][0][0][0], warp);
+        Map<VEC, 1> m = s_map[buf][0][lane];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          float A = 1.f, B = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float aw = s_map[buf][w][0][i][lane];
-            B = affine(aw, B, s_map[buf][w][1][i][lane]);
-            A *= aw;
-          }
-          to[i * 32 + lane] = A;
-          to[(VEC + i) * 32 + lane] = B;
+        for (int w = 1; w < kWarps; ++w) {
+          const Map<VEC, 1> k = s_map[buf][w][lane];
+          affine<kSig>(k.a, m.b[0], k.b[0], m.b[0]);
+          vmul(m.a, k.a, m.a);
         }
+        cluster.map_shared_rank(&s_cta[buf][rank][0], warp)[lane] = m;
       }
       cluster.sync();
-    }
-    float start[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float h = carry[i];
-      if (kCluster) {
-        float mine = h;
-        for (int r = 0; r < cs; ++r) {
-          if (r == rank) mine = h;
-          h = affine(s_cta[buf][r][0][i][lane], h, s_cta[buf][r][1][i][lane]);
+      for (int i = 0; i < VEC; ++i) h[i] = carry[i];
+      for (int r = 0; r < cs; ++r) {
+        const Map<VEC, 1> k = s_cta[buf][r][lane];
+        if (r == rank) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) h[i] = carry[i];
         }
-        carry[i] = h;
-        h = mine;
+        affine<kSig>(k.a, carry, k.b[0], carry);
       }
-      if (p.states && warp == 0 && live && tile < tiles)
-        p.states[(b * tiles + tile) * p.D + c0 + i] = h;
-      start[i] = h;
-#pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) start[i] = h;
-        h = affine(s_map[buf][w][0][i][lane], h, s_map[buf][w][1][i][lane]);
-      }
-      if (!kCluster) carry[i] = h;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) h[i] = carry[i];
     }
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      float o[VEC];
+    for (int i = 0; i < VEC; ++i) start[i] = h[i];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        start[i] = affine(a[s][i], start[i], u[s][i]);
-        o[i] = t0 + s < len ? start[i] : 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+      const Map<VEC, 1> k = s_map[buf][w][lane];
+      affine<kSig>(k.a, h, k.b[0], h);
+      if (w + 1 == warp) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) start[i] = h[i];
       }
-      if (live && t0 + s < p.T) store<In, VEC>(out + (t0 + s) * p.D, o);
+    }
+    if (!kCluster) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) carry[i] = h[i];
+    }
+    if (p.states && t0 % kScanBlock == 0 && t0 < p.T && live)
+      store<float, VEC>(p.states + (b * saved + t0 / kScanBlock) * p.D + c0, start);
+    if (live) {
+      In *o = out + t0 * p.D;
+      if (n >= S) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          affine<kSig>(a[s], start, u[s], start);
+          store<In, VEC>(o, start);
+          o += p.D;
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          float v[VEC];
+          affine<kSig>(a[s], start, u[s], start);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[i] = s < n ? start[i] : 0.f;
+          if (t0 + s < p.T) store<In, VEC>(o, v);
+          o += p.D;
+        }
+      }
     }
   }
-  if (p.hT && rank == 0 && warp == 0 && live) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p.hT[b * p.D + c0 + i] = carry[i];
-  }
+  ring_wait<0>();
+  if (p.hT && rank == 0 && warp == 0 && live) store<float, VEC>(p.hT + b * p.D + c0, carry);
 }
 
 // ----------------------------------------------------------------- backward
@@ -248,42 +388,43 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 // again from the state saved at the tile's start (the forward's states, kept
 // in float32, so no rounded output enters the gradients); the gradients are
 // the reversed recurrence, whose maps compose from the last step to the first.
-template <typename In, bool kSig, int VEC, bool kCluster>
+template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
-  __shared__ float s_map[2][kWarps][3][VEC][32];  // decay, forward and reverse offsets
-  __shared__ float s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][2][VEC][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int S = kBwdSteps, kTile = kWarps * S, kRow = 32 * VEC, kSlot = S * kRow;
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ __align__(16) Map<VEC, 2> s_map[2][kWarps][32];  // offsets: forward, reverse
+  __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
   const int64_t id = kCluster ? blockIdx.x / cs : blockIdx.x;
-  const int64_t b = id / strips, c0 = (id % strips) * (32 * VEC) + lane * VEC;
+  const int64_t b = id / strips, first = (id % strips) * kRow, c0 = first + lane * VEC;
   const bool live = c0 < p.D;
-  const int64_t len = row_length(p.lengths, b, p.T);
+  const int64_t len = row_length(p.lengths, b, p.T), left = p.D - first;
   const int64_t tiles = (p.T + kTile - 1) / kTile;
-  const In *x = static_cast<const In *>(p.x) + b * p.x_sb + c0;
-  const Gate *g = static_cast<const Gate *>(p.gate) + b * p.g_sb + c0;
-  const In *dout = static_cast<const In *>(p.dout) + b * p.T * p.D + c0;
+  const In *x = static_cast<const In *>(p.x) + b * p.x_sb + first;
+  const Gate *g = static_cast<const Gate *>(p.gate) + b * p.g_sb + first;
+  const In *dout = static_cast<const In *>(p.dout) + b * p.T * p.D + first;
   In *dx = static_cast<In *>(p.dx) + b * p.T * p.D + c0;
   Gate *dg = static_cast<Gate *>(p.dgate) + b * p.T * p.D + c0;
+  In *rx = reinterpret_cast<In *>(ring) + warp * 2 * kStages * kSlot, *rd = rx + kStages * kSlot;
+  Gate *rg = reinterpret_cast<Gate *>(ring + 2 * kWarps * kStages * kSlot * sizeof(In)) + warp * kStages * kSlot;
 
-  typename Raw<In, VEC>::type xr[kSteps], dr[kSteps];
-  typename Raw<Gate, VEC>::type gr[kSteps];
-  float hs[VEC];
+  float ahead[VEC];  // the saved state of the next tile
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) hs[i] = 0.f;
-  auto fetch = [&](int64_t tile) {  // tile may be below 0: nothing is read
-    const int64_t t0 = tile * kTile + warp * kSteps;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      if (live && tile >= 0 && t0 + s < len) {
-        xr[s] = load<In, VEC>(x + (t0 + s) * p.x_st);
-        gr[s] = load<Gate, VEC>(g + (t0 + s) * p.g_st);
-        dr[s] = load<In, VEC>(dout + (t0 + s) * p.D);
-      }
-    if (live && tile >= 0) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) hs[i] = p.states[(b * tiles + tile) * p.D + c0 + i];
+  for (int i = 0; i < VEC; ++i) ahead[i] = 0.f;
+  auto fetch = [&](int64_t tile, int slot) {  // a tile below 0 is not there
+    const int64_t t0 = tile * kTile + warp * S, n = tile < 0 ? 0 : len - t0;
+    if (n > 0) {
+      ring_rows<In, VEC, S, kWide>(rx + slot * kSlot, x + t0 * p.x_st, p.x_st, n, left, lane);
+      ring_rows<In, VEC, S, kWide>(rd + slot * kSlot, dout + t0 * p.D, p.D, n, left, lane);
+      ring_rows<Gate, VEC, S, kWide>(rg + slot * kSlot, g + t0 * p.g_st, p.g_st, n, left, lane);
     }
+    ring_commit();
+  };
+  auto fetch_state = [&](int64_t tile) {
+    if (tile >= 0 && live) widen(load<float, VEC>(p.states + (b * tiles + tile) * p.D + c0), ahead);
   };
 
   float carry[VEC];
@@ -291,127 +432,160 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   for (int i = 0; i < VEC; ++i) carry[i] = live && p.dhT ? p.dhT[b * p.D + c0 + i] : 0.f;
 
   const int64_t rounds = (tiles + cs - 1) / cs;
-  // every CTA of the cluster runs before any writes into its shared memory
   if (kCluster) cg::this_cluster().barrier_arrive();
-  fetch(tiles - 1 - rank);
-  if (kCluster) cg::this_cluster().barrier_wait();
-  for (int64_t it = 0; it < rounds; ++it) {
-    const int64_t tile = tiles - 1 - (it * cs + rank), t0 = tile * kTile + warp * kSteps;
-    const int buf = (int)(it & 1);
-    float a[kSteps][VEC], u[kSteps][VEC], ux[kSteps][VEC], d[kSteps][VEC], h[VEC];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (live && tile >= 0 && t0 + s < len) {
-        float xv[VEC], gv[VEC];
-        widen(xr[s], xv);
-        widen(gr[s], gv);
-        widen(dr[s], d[s]);
+  for (int i = 0; i < kStages - 1; ++i) fetch(tiles - 1 - rank - (int64_t)i * cs, i);
+  fetch_state(tiles - 1 - rank);
+  if (kCluster) cg::this_cluster().barrier_wait();
+  int slot = 0;
+  for (int64_t it = 0; it < rounds; ++it) {
+    const int64_t tile = tiles - 1 - (it * cs + rank), t0 = tile * kTile + warp * S;
+    const int64_t n = tile < 0 ? 0 : len - t0;
+    const int buf = (int)(it & 1);
+    ring_wait<kStages - 2>();
+    __syncwarp();
+    fetch(tile - (int64_t)(kStages - 1) * cs, slot == 0 ? kStages - 1 : slot - 1);
+    float a[S][VEC], u[S][VEC], ux[S][VEC], d[S][VEC], h[VEC];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      float xv[VEC], gv[VEC];
+      ring_read<In, VEC>(rx + slot * kSlot + s * kRow + lane * VEC, xv);
+      ring_read<Gate, VEC>(rg + slot * kSlot + s * kRow + lane * VEC, gv);
+      ring_read<In, VEC>(rd + slot * kSlot + s * kRow + lane * VEC, d[s]);
+      gates<kSig>(gv, a[s], u[s]);
+      vmul(u[s], xv, ux[s]);
+    }
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    if (n < S) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          gates<kSig>(gv[i], a[s][i], u[s][i]);
-          ux[s][i] = u[s][i] * xv[i];
+          a[s][i] = s < n ? a[s][i] : 1.f;
+          u[s][i] = s < n ? u[s][i] : 0.f;
+          ux[s][i] = s < n ? ux[s][i] : 0.f;
+          d[s][i] = s < n ? d[s][i] : 0.f;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) a[s][i] = 1.f, u[s][i] = 0.f, ux[s][i] = 0.f, d[s][i] = 0.f;
-      }
     }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) h[i] = hs[i];
-    if (it + 1 < rounds) fetch(tile - cs);
+    for (int i = 0; i < VEC; ++i) h[i] = ahead[i];
+    if (it + 1 < rounds) fetch_state(tile - cs);
+    {
+      Map<VEC, 2> m;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float A = 1.f, F = 0.f, R = 0.f;
+      for (int i = 0; i < VEC; ++i) m.a[i] = a[0][i], m.b[0][i] = ux[0][i];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        F = affine(a[s][i], F, ux[s][i]);
-        A *= a[s][i];
-        const int q = kSteps - 1 - s;
-        R = a[q][i] == 0.f ? 0.f : a[q][i] * (d[q][i] + R);
+      for (int s = 1; s < S; ++s) {
+        affine<kSig>(a[s], m.b[0], ux[s], m.b[0]);
+        vmul(m.a, a[s], m.a);
       }
-      s_map[buf][warp][0][i][lane] = A;
-      s_map[buf][warp][1][i][lane] = F;
-      s_map[buf][warp][2][i][lane] = R;
+      decay<kSig>(a[S - 1], d[S - 1], m.b[1]);
+#pragma unroll
+      for (int s = S - 2; s >= 0; --s) {
+        vadd(d[s], m.b[1], m.b[1]);
+        decay<kSig>(a[s], m.b[1], m.b[1]);
+      }
+      s_map[buf][warp][lane] = m;
     }
     __syncthreads();
+    float r[VEC], c[VEC];
     if (kCluster) {
       cg::cluster_group cluster = cg::this_cluster();
       if (warp < cs) {
-        float *to = cluster.map_shared_rank(&s_cta[buf][rank][0][0][0], warp);
+        const Map<VEC, 2> last = s_map[buf][kWarps - 1][lane];
+        Map<VEC, 1> m;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          float A = 1.f, R = 0.f;
+        for (int i = 0; i < VEC; ++i) m.a[i] = last.a[i], m.b[0][i] = last.b[1][i];
 #pragma unroll
-          for (int w = kWarps - 1; w >= 0; --w) {
-            const float aw = s_map[buf][w][0][i][lane];
-            R = affine(aw, R, s_map[buf][w][2][i][lane]);
-            A *= aw;
-          }
-          to[i * 32 + lane] = A;
-          to[(VEC + i) * 32 + lane] = R;
+        for (int w = kWarps - 2; w >= 0; --w) {
+          const Map<VEC, 2> k = s_map[buf][w][lane];
+          affine<kSig>(k.a, m.b[0], k.b[1], m.b[0]);
+          vmul(m.a, k.a, m.a);
         }
+        cluster.map_shared_rank(&s_cta[buf][rank][0], warp)[lane] = m;
       }
       cluster.sync();
-    }
-    float c[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float r = carry[i];
-      if (kCluster) {
-        float mine = r;
-        for (int k = 0; k < cs; ++k) {
-          if (k == rank) mine = r;
-          r = affine(s_cta[buf][k][0][i][lane], r, s_cta[buf][k][1][i][lane]);
+      for (int i = 0; i < VEC; ++i) r[i] = carry[i];
+      for (int k = 0; k < cs; ++k) {
+        const Map<VEC, 1> q = s_cta[buf][k][lane];
+        if (k == rank) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) r[i] = carry[i];
         }
-        carry[i] = r;
-        r = mine;
+        affine<kSig>(q.a, carry, q.b[0], carry);
       }
-      c[i] = r;
-      float f = h[i];
-#pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) h[i] = f;
-        f = affine(s_map[buf][w][0][i][lane], f, s_map[buf][w][1][i][lane]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) r[i] = carry[i];
+    }
+    // the state at this warp's start, over the warps before it
+    for (int w = 0; w < warp; ++w) {
+      const Map<VEC, 2> k = s_map[buf][w][lane];
+      affine<kSig>(k.a, h, k.b[0], h);
+    }
+    // the gradient that arrives at its end, over the warps after it
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) c[i] = r[i];
+#pragma unroll
+    for (int w = kWarps - 1; w >= 0; --w) {
+      const Map<VEC, 2> k = s_map[buf][w][lane];
+      affine<kSig>(k.a, r, k.b[1], r);
+      if (w - 1 == warp) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) c[i] = r[i];
       }
-#pragma unroll 4
-      for (int w = kWarps - 1; w >= 0; --w) {
-        if (w == warp) c[i] = r;
-        r = affine(s_map[buf][w][0][i][lane], r, s_map[buf][w][2][i][lane]);
-      }
-      if (!kCluster) carry[i] = r;
+    }
+    if (!kCluster) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) carry[i] = r[i];
     }
     // the state before each step takes the place of its input term: sigmoid
-    // keeps u h_{t-1} - u x, linear keeps h_{t-1}
+    // keeps a (u h_{t-1} - u x), linear keeps h_{t-1}
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
+    for (int s = 0; s < S; ++s) {
+      float before[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float before = h[i];
-        h[i] = affine(a[s][i], before, ux[s][i]);
-        ux[s][i] = kSig ? u[s][i] * before - ux[s][i] : before;
+      for (int i = 0; i < VEC; ++i) before[i] = h[i];
+      affine<kSig>(a[s], before, ux[s], h);
+      if constexpr (kSig) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ux[s][i] = -ux[s][i];
+        vfma(u[s], before, ux[s], ux[s]);
+        vmul(a[s], ux[s], ux[s]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ux[s][i] = before[i];
       }
     }
+    if (live && tile >= 0) {
+      In *ox = dx + (t0 + S - 1) * p.D;
+      Gate *og = dg + (t0 + S - 1) * p.D;
 #pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s) {
-      float vx[VEC], vg[VEC];
-      const bool in = t0 + s < len;
+      for (int s = S - 1; s >= 0; --s) {
+        float dh[VEC], vx[VEC], vg[VEC];
+        vadd(d[s], c, dh);
+        decay<kSig>(a[s], dh, c);
+        vmul(u[s], dh, vx);
+        vmul(ux[s], dh, vg);
+        if (n < S) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float dh = d[s][i] + c[i];
-        c[i] = a[s][i] == 0.f ? 0.f : a[s][i] * dh;
-        vx[i] = in ? u[s][i] * dh : 0.f;
-        vg[i] = in ? (kSig ? dh * a[s][i] : dh) * ux[s][i] : 0.f;
-      }
-      if (live && tile >= 0 && t0 + s < p.T) {
-        store<In, VEC>(dx + (t0 + s) * p.D, vx);
-        store<Gate, VEC>(dg + (t0 + s) * p.D, vg);
+          for (int i = 0; i < VEC; ++i) {
+            vx[i] = s < n ? vx[i] : 0.f;
+            vg[i] = s < n ? vg[i] : 0.f;
+          }
+        }
+        if (n >= S || t0 + s < p.T) {
+          store<In, VEC>(ox, vx);
+          store<Gate, VEC>(og, vg);
+        }
+        ox -= p.D;
+        og -= p.D;
       }
     }
   }
-  if (p.dh0 && rank == 0 && warp == 0 && live) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p.dh0[b * p.D + c0 + i] = carry[i];
-  }
+  ring_wait<0>();
+  if (p.dh0 && rank == 0 && warp == 0 && live) store<float, VEC>(p.dh0 + b * p.D + c0, carry);
 }
 
 // --------------------------------------------------------------------- step
@@ -422,16 +596,13 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs p, int64_t n) {
   const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
   if (i0 >= n) return;
   const int64_t b = i0 / p.D, c = i0 - b * p.D;
-  float xv[VEC], gv[VEC], hv[VEC];
+  float xv[VEC], gv[VEC], hv[VEC], a[VEC], u[VEC];
   widen(load<In, VEC>(static_cast<const In *>(p.x) + b * p.x_sb + c), xv);
   widen(load<Gate, VEC>(static_cast<const Gate *>(p.gate) + b * p.g_sb + c), gv);
   widen(load<float, VEC>(p.h0 + i0), hv);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    float a, u;
-    gates<kSig>(gv[i], a, u);
-    hv[i] = affine(a, hv[i], u * xv[i]);
-  }
+  gates<kSig>(gv, a, u);
+  vmul(u, xv, u);
+  affine<kSig>(a, hv, u, hv);
   store<float, VEC>(p.hT + i0, hv);
   store<In, VEC>(static_cast<In *>(p.out) + i0, hv);
 }
@@ -445,13 +616,16 @@ int sm_count() {
   return n;
 }
 
-// two channels per lane need even offsets everywhere
-bool pairs(const ScanArgs &a) {
-  const int gsz = a.sigmoid && a.bf16 ? 2 : 4, esz = a.bf16 ? 2 : 4;
-  const auto ok = [](const void *q, int sz) { return (reinterpret_cast<uintptr_t>(q) % (2 * sz)) == 0; };
-  return a.D % 2 == 0 && a.x_sb % 2 == 0 && a.x_st % 2 == 0 && a.g_sb % 2 == 0 && a.g_st % 2 == 0 &&
-         ok(a.x, esz) && ok(a.gate, gsz);
+// the strides and addresses of x and gate allow pieces of nx and ng elements
+bool pieces(const ScanArgs &a, int nx, int ng) {
+  const int64_t ex = a.bf16 ? 2 : 4, eg = a.sigmoid ? ex : 4;
+  const auto ok = [](const void *q, int64_t n) { return reinterpret_cast<uintptr_t>(q) % (uintptr_t)n == 0; };
+  return a.D % nx == 0 && a.D % ng == 0 && a.x_sb % nx == 0 && a.x_st % nx == 0 && a.g_sb % ng == 0 &&
+         a.g_st % ng == 0 && ok(a.x, nx * ex) && ok(a.gate, ng * eg);
 }
+// two channels a lane need even offsets everywhere; 16-byte pieces are wide
+bool pairs(const ScanArgs &a) { return pieces(a, 2, 2); }
+bool wide(const ScanArgs &a) { return pieces(a, a.bf16 ? 8 : 4, a.bf16 && a.sigmoid ? 8 : 4); }
 
 // CTAs of a cluster along the time axis: enough to give every SM two CTAs,
 // as far as there are tiles
@@ -463,10 +637,14 @@ int cluster_size(int64_t rows, int64_t tiles) {
 }
 
 template <typename K, typename A>
-cudaError_t launch(K kern, const A &p, int64_t rows, int64_t strips, int cs, cudaStream_t s) {
+cudaError_t launch(K kern, const A &p, int64_t rows, int64_t strips, int cs, int smem, cudaStream_t s) {
+  // above 48 KB only after asking; asking again changes nothing
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * cs));
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -477,19 +655,21 @@ cudaError_t launch(K kern, const A &p, int64_t rows, int64_t strips, int cs, cud
   return cudaLaunchKernelEx(&cfg, kern, p, cs, strips);
 }
 
-template <typename In, bool kSig, int VEC>
+template <typename In, bool kSig, int VEC, bool kWide>
 cudaError_t launch_fwd(const ScanArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
-  const int cs = cluster_size(rows, (a.T + kTile - 1) / kTile);
-  return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, true>, a, rows, strips, cs, s)
-                : launch(scan_fwd_kernel<In, kSig, VEC, false>, a, rows, strips, cs, s);
+  const int cs = cluster_size(rows, (a.T + kWarps * kFwdSteps - 1) / (kWarps * kFwdSteps));
+  const int smem = kWarps * kStages * kFwdSteps * 32 * VEC * (int)(sizeof(In) + (kSig ? sizeof(In) : 4));
+  return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
+                : launch(scan_fwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
-template <typename In, bool kSig, int VEC>
+template <typename In, bool kSig, int VEC, bool kWide>
 cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
-  const int cs = cluster_size(rows, (a.T + kTile - 1) / kTile);
-  return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, true>, a, rows, strips, cs, s)
-                : launch(scan_bwd_kernel<In, kSig, VEC, false>, a, rows, strips, cs, s);
+  const int cs = cluster_size(rows, (a.T + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps));
+  const int smem = kWarps * kStages * kBwdSteps * 32 * VEC * (int)(2 * sizeof(In) + (kSig ? sizeof(In) : 4));
+  return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
+                : launch(scan_bwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
 template <typename In, bool kSig, int VEC>
 cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
@@ -501,23 +681,43 @@ cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s) {
-  const bool v2 = pairs(a);
+  const bool v2 = pairs(a), w = wide(a);
   if (a.bf16) {
-    if (a.sigmoid) return v2 ? launch_fwd<__nv_bfloat16, true, 2>(a, s) : launch_fwd<__nv_bfloat16, true, 1>(a, s);
-    return v2 ? launch_fwd<__nv_bfloat16, false, 2>(a, s) : launch_fwd<__nv_bfloat16, false, 1>(a, s);
+    if (a.sigmoid)
+      return w ? launch_fwd<__nv_bfloat16, true, 2, true>(a, s)
+           : v2 ? launch_fwd<__nv_bfloat16, true, 2, false>(a, s)
+                : launch_fwd<__nv_bfloat16, true, 1, false>(a, s);
+    return w ? launch_fwd<__nv_bfloat16, false, 2, true>(a, s)
+         : v2 ? launch_fwd<__nv_bfloat16, false, 2, false>(a, s)
+              : launch_fwd<__nv_bfloat16, false, 1, false>(a, s);
   }
-  if (a.sigmoid) return v2 ? launch_fwd<float, true, 2>(a, s) : launch_fwd<float, true, 1>(a, s);
-  return v2 ? launch_fwd<float, false, 2>(a, s) : launch_fwd<float, false, 1>(a, s);
+  if (a.sigmoid)
+    return w ? launch_fwd<float, true, 2, true>(a, s)
+         : v2 ? launch_fwd<float, true, 2, false>(a, s)
+              : launch_fwd<float, true, 1, false>(a, s);
+  return w ? launch_fwd<float, false, 2, true>(a, s)
+       : v2 ? launch_fwd<float, false, 2, false>(a, s)
+            : launch_fwd<float, false, 1, false>(a, s);
 }
 
 cudaError_t launch_scan_bwd(const ScanBwdArgs &a, cudaStream_t s) {
-  const bool v2 = pairs(a);
+  const bool v2 = pairs(a), w = wide(a);
   if (a.bf16) {
-    if (a.sigmoid) return v2 ? launch_bwd<__nv_bfloat16, true, 2>(a, s) : launch_bwd<__nv_bfloat16, true, 1>(a, s);
-    return v2 ? launch_bwd<__nv_bfloat16, false, 2>(a, s) : launch_bwd<__nv_bfloat16, false, 1>(a, s);
+    if (a.sigmoid)
+      return w ? launch_bwd<__nv_bfloat16, true, 2, true>(a, s)
+           : v2 ? launch_bwd<__nv_bfloat16, true, 2, false>(a, s)
+                : launch_bwd<__nv_bfloat16, true, 1, false>(a, s);
+    return w ? launch_bwd<__nv_bfloat16, false, 2, true>(a, s)
+         : v2 ? launch_bwd<__nv_bfloat16, false, 2, false>(a, s)
+              : launch_bwd<__nv_bfloat16, false, 1, false>(a, s);
   }
-  if (a.sigmoid) return v2 ? launch_bwd<float, true, 2>(a, s) : launch_bwd<float, true, 1>(a, s);
-  return v2 ? launch_bwd<float, false, 2>(a, s) : launch_bwd<float, false, 1>(a, s);
+  if (a.sigmoid)
+    return w ? launch_bwd<float, true, 2, true>(a, s)
+         : v2 ? launch_bwd<float, true, 2, false>(a, s)
+              : launch_bwd<float, true, 1, false>(a, s);
+  return w ? launch_bwd<float, false, 2, true>(a, s)
+       : v2 ? launch_bwd<float, false, 2, false>(a, s)
+            : launch_bwd<float, false, 1, false>(a, s);
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s) {
