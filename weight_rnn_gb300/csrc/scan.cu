@@ -16,7 +16,7 @@
 // (A, B) after (A', B') is (A A', A B' + B).  So a tile of 32 VEC channels is
 // cut into sub-chunks of consecutive steps, one per warp, lane = VEC channels:
 //   1. each warp takes its steps from its own ring in shared memory, filled
-//      kStages - 1 tiles ahead by asynchronous copies, and composes its map;
+//      a tile or two ahead by asynchronous copies, and composes its map;
 //   2. the maps meet in shared memory (one barrier), and every warp folds
 //      them in time order onto the state carried from the last tile, which
 //      gives the state at its own start and, redundantly in every warp, the
@@ -40,12 +40,13 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;
-constexpr int kStages = 3;               // tiles in a warp's ring
 constexpr int kFwdSteps = 16;            // steps per warp and tile
 constexpr int kBwdSteps = 8;             // (the reverse holds twice the values per step)
 static_assert(kScanBlock % kFwdSteps == 0 && kScanBlock == kWarps * kBwdSteps,
               "states are saved at a warp's start, and taken at a reverse tile's");
 constexpr int kMaxCluster = 8;           // the portable cluster size
+// tiles in a warp's ring: three where two CTAs' rings then fit an SM, else two
+__host__ __device__ constexpr int ring_stages(int tile_bytes) { return tile_bytes <= 32768 ? 3 : 2; }
 
 // VEC neighbouring elements as they lie in memory
 template <typename T, int VEC>
@@ -235,6 +236,7 @@ template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
   constexpr int S = kFwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
+  constexpr int kStages = ring_stages(kTile * kRow * (int)(sizeof(In) + sizeof(Gate)));
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 1> s_map[2][kWarps][32];
   __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
@@ -392,6 +394,7 @@ template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
   constexpr int S = kBwdSteps, kTile = kWarps * S, kRow = 32 * VEC, kSlot = S * kRow;
+  constexpr int kStages = ring_stages(kTile * kRow * (int)(2 * sizeof(In) + sizeof(Gate)));
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 2> s_map[2][kWarps][32];  // offsets: forward, reverse
   __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
@@ -623,7 +626,8 @@ bool pieces(const ScanArgs &a, int nx, int ng) {
   return a.D % nx == 0 && a.D % ng == 0 && a.x_sb % nx == 0 && a.x_st % nx == 0 && a.g_sb % ng == 0 &&
          a.g_st % ng == 0 && ok(a.x, nx * ex) && ok(a.gate, ng * eg);
 }
-// two channels a lane need even offsets everywhere; 16-byte pieces are wide
+// Two channels a lane (bfloat16; a row of a strip is 128 bytes either way) need
+// even offsets everywhere; 16-byte pieces are wide.
 bool pairs(const ScanArgs &a) { return pieces(a, 2, 2); }
 bool wide(const ScanArgs &a) { return pieces(a, a.bf16 ? 8 : 4, a.bf16 && a.sigmoid ? 8 : 4); }
 
@@ -659,7 +663,8 @@ template <typename In, bool kSig, int VEC, bool kWide>
 cudaError_t launch_fwd(const ScanArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kFwdSteps - 1) / (kWarps * kFwdSteps));
-  const int smem = kWarps * kStages * kFwdSteps * 32 * VEC * (int)(sizeof(In) + (kSig ? sizeof(In) : 4));
+  constexpr int tile = kWarps * kFwdSteps * 32 * VEC * (int)(sizeof(In) + (kSig ? sizeof(In) : 4));
+  const int smem = ring_stages(tile) * tile;
   return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_fwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
@@ -667,7 +672,8 @@ template <typename In, bool kSig, int VEC, bool kWide>
 cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps));
-  const int smem = kWarps * kStages * kBwdSteps * 32 * VEC * (int)(2 * sizeof(In) + (kSig ? sizeof(In) : 4));
+  constexpr int tile = kWarps * kBwdSteps * 32 * VEC * (int)(2 * sizeof(In) + (kSig ? sizeof(In) : 4));
+  const int smem = ring_stages(tile) * tile;
   return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_bwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
@@ -692,12 +698,8 @@ cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s) {
               : launch_fwd<__nv_bfloat16, false, 1, false>(a, s);
   }
   if (a.sigmoid)
-    return w ? launch_fwd<float, true, 2, true>(a, s)
-         : v2 ? launch_fwd<float, true, 2, false>(a, s)
-              : launch_fwd<float, true, 1, false>(a, s);
-  return w ? launch_fwd<float, false, 2, true>(a, s)
-       : v2 ? launch_fwd<float, false, 2, false>(a, s)
-            : launch_fwd<float, false, 1, false>(a, s);
+    return w ? launch_fwd<float, true, 1, true>(a, s) : launch_fwd<float, true, 1, false>(a, s);
+  return w ? launch_fwd<float, false, 1, true>(a, s) : launch_fwd<float, false, 1, false>(a, s);
 }
 
 cudaError_t launch_scan_bwd(const ScanBwdArgs &a, cudaStream_t s) {
@@ -712,12 +714,8 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs &a, cudaStream_t s) {
               : launch_bwd<__nv_bfloat16, false, 1, false>(a, s);
   }
   if (a.sigmoid)
-    return w ? launch_bwd<float, true, 2, true>(a, s)
-         : v2 ? launch_bwd<float, true, 2, false>(a, s)
-              : launch_bwd<float, true, 1, false>(a, s);
-  return w ? launch_bwd<float, false, 2, true>(a, s)
-       : v2 ? launch_bwd<float, false, 2, false>(a, s)
-            : launch_bwd<float, false, 1, false>(a, s);
+    return w ? launch_bwd<float, true, 1, true>(a, s) : launch_bwd<float, true, 1, false>(a, s);
+  return w ? launch_bwd<float, false, 1, true>(a, s) : launch_bwd<float, false, 1, false>(a, s);
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s) {
