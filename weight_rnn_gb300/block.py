@@ -51,9 +51,8 @@ def _raise(st):
     raise DeltaError(st, delta_last_error())
 
 
-def _tensor(t, name, shape, dtype, device, strided=False):
-    """Check one tensor; with ``strided`` any non-negative strides with
-    contiguous rows are taken, else it has to be contiguous."""
+def _refuse(t, name, shape, dtype, device, strided):
+    """Say what is wrong with a tensor that did not pass."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -62,12 +61,20 @@ def _tensor(t, name, shape, dtype, device, strided=False):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if strided:
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the last axis of {name} must be contiguous")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"the last axis of {name} must be contiguous" if strided
+                     else f"{name} must be contiguous")
+
+
+def _tensor(t, name, shape, dtype, device, strided=False):
+    """Check one tensor and give its address; with ``strided`` any non-negative
+    strides with contiguous rows are taken, else it has to be contiguous."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.device == device and (
+                t.is_contiguous() or strided and (t.shape[-1] <= 1 or t.stride(-1) == 1)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, device, strided)
 
 
 def _optional(t, name, shape, dtype, device):
@@ -76,39 +83,47 @@ def _optional(t, name, shape, dtype, device):
 
 def _begin(x, name, dims, what="x"):
     """dtype code and device of the operator's leading tensor"""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{what} must be a torch.Tensor")
-    dev = x.device
+    try:
+        dev, dt = x.device, x.dtype
+    except AttributeError:
+        raise TypeError(f"{what} must be a torch.Tensor") from None
     if dev.type != "cuda":
         raise ValueError(f"{name} needs CUDA tensors")
     if dims and x.dim() != dims:
         raise ValueError(f"{what} must have {dims} axes, got shape {tuple(x.shape)}")
-    code = _CODES.get(x.dtype)
+    code = _CODES.get(dt)
     if code is None:
-        raise TypeError(f"{what} must be bfloat16 or float32, got {x.dtype}")
+        raise TypeError(f"{what} must be bfloat16 or float32, got {dt}")
     return code, dev
 
 
-class _On:
-    """The stream of a call, and allocation for it."""
+def _raw_stream(dev, stream):
+    """The stream's handle.  The current one is asked for by device index,
+    which takes a twentieth of what making a Stream object does (2 us, as much
+    as the launch)."""
+    return _current(dev.index) if stream is None else stream.cuda_stream
 
-    __slots__ = ("raw", "side", "dev")
 
-    def __init__(self, dev, stream):
-        self.dev, self.side = dev, stream
-        self.raw = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
 
-    def empty(self, shape, dtype):
-        if self.side is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.side):
-            return torch.empty(shape, dtype=dtype, device=self.dev)
 
-    def out(self, t, name, shape, dtype):
-        if t is None:
-            return self.empty(shape, dtype)
-        _tensor(t, name, shape, dtype, self.dev)
-        return t
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _empty(shape, dtype, dev, stream):
+    """An output, allocated for the stream of the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _output(t, name, shape, dtype, dev, stream):
+    if t is None:
+        return _empty(shape, dtype, dev, stream)
+    _tensor(t, name, shape, dtype, dev)
+    return t
 
 
 def _scan_form(form, dt):
@@ -138,14 +153,13 @@ def delta_scan_fwd(x, gate, h0=None, *, form="sigmoid", lengths=None, save_state
     pg = _tensor(gate, "gate", x.shape, gdt, dev, True)
     ph = _optional(h0, "h0", (B, D), torch.float32, dev)
     pl = _optional(lengths, "lengths", (B,), torch.int32, dev)
-    on = _On(dev, stream)
-    out = on.out(out, "out", (B, T, D), x.dtype)
-    hT = on.out(hT, "hT", (B, D), torch.float32)
-    states = on.empty((B, -(-T // SCAN_BLOCK), D), torch.float32) if save_states else None
+    out = _output(out, "out", (B, T, D), x.dtype, dev, stream)
+    hT = _output(hT, "hT", (B, D), torch.float32, dev, stream)
+    states = _empty((B, -(-T // SCAN_BLOCK), D), torch.float32, dev, stream) if save_states else None
     st = _lib().delta_scan_fwd(px, pg, ph, pl, out.data_ptr(), hT.data_ptr(),
                                None if states is None else states.data_ptr(), B, T, D,
                                x.stride(0), x.stride(1), gate.stride(0), gate.stride(1), code,
-                               fcode, on.raw)
+                               fcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return (out, hT, states) if save_states else (out, hT)
@@ -160,10 +174,9 @@ def delta_scan_step(x, gate, state, *, form="sigmoid", out=None, stream=None):
     px = _tensor(x, "x", x.shape, x.dtype, dev, True)
     pg = _tensor(gate, "gate", x.shape, gdt, dev, True)
     ps = _tensor(state, "state", x.shape, torch.float32, dev)
-    on = _On(dev, stream)
-    out = on.out(out, "out", x.shape, x.dtype)
+    out = _output(out, "out", x.shape, x.dtype, dev, stream)
     st = _lib().delta_scan_step(px, pg, ps, out.data_ptr(), B, D, x.stride(0), gate.stride(0),
-                                code, fcode, on.raw)
+                                code, fcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return out
@@ -183,12 +196,11 @@ def delta_scan_bwd(x, gate, states, dout, dhT=None, *, form="sigmoid", lengths=N
     po = _tensor(dout, "dout", x.shape, x.dtype, dev)
     pt = _optional(dhT, "dhT", (B, D), torch.float32, dev)
     pl = _optional(lengths, "lengths", (B,), torch.int32, dev)
-    on = _On(dev, stream)
-    dx, dgate = on.empty(x.shape, x.dtype), on.empty(x.shape, gdt)
-    dh0 = on.empty((B, D), torch.float32)
+    dx, dgate = _empty(x.shape, x.dtype, dev, stream), _empty(x.shape, gdt, dev, stream)
+    dh0 = _empty((B, D), torch.float32, dev, stream)
     st = _lib().delta_scan_bwd(px, pg, ps, pl, po, pt, dx.data_ptr(), dgate.data_ptr(),
                                dh0.data_ptr(), B, T, D, x.stride(0), x.stride(1),
-                               gate.stride(0), gate.stride(1), code, fcode, on.raw)
+                               gate.stride(0), gate.stride(1), code, fcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return dx, dgate, dh0
@@ -243,15 +255,15 @@ def delta_add_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, sum_out=None, s
     """
     code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
                                                                  "delta_add_rmsnorm_fwd")
-    on = _On(dev, stream)
-    y, rstd = on.empty(x.shape, x.dtype), on.empty(x.shape[:-1], torch.float32)
+    y = _empty(x.shape, x.dtype, dev, stream)
+    rstd = _empty(x.shape[:-1], torch.float32, dev, stream)
     if residual is not None:
-        sum_out = on.out(sum_out, "sum_out", x.shape, x.dtype)
+        sum_out = _output(sum_out, "sum_out", x.shape, x.dtype, dev, stream)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual: without one the sum is x")
     st = _lib().delta_add_rmsnorm_fwd(px, pr, pw, y.data_ptr(),
                                       None if sum_out is None else sum_out.data_ptr(),
-                                      rstd.data_ptr(), rows, D, ldx, ldr, eps, code, wcode, on.raw)
+                                      rstd.data_ptr(), rows, D, ldx, ldr, eps, code, wcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return y, (x if sum_out is None else sum_out), rstd
@@ -262,15 +274,15 @@ def delta_add_rmsnorm_quant(x, weight, residual=None, *, eps=1e-6, sum_out=None,
     for a row of zeros).  Returns ``(y float8_e4m3fn, scale [...], sum)``."""
     code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
                                                                  "delta_add_rmsnorm_quant")
-    on = _On(dev, stream)
-    y, scale = on.empty(x.shape, E4M3), on.empty(x.shape[:-1], torch.float32)
+    y = _empty(x.shape, E4M3, dev, stream)
+    scale = _empty(x.shape[:-1], torch.float32, dev, stream)
     if residual is not None:
-        sum_out = on.out(sum_out, "sum_out", x.shape, x.dtype)
+        sum_out = _output(sum_out, "sum_out", x.shape, x.dtype, dev, stream)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual: without one the sum is x")
     st = _lib().delta_add_rmsnorm_quant(px, pr, pw, y.data_ptr(), scale.data_ptr(),
                                         None if sum_out is None else sum_out.data_ptr(), rows, D,
-                                        ldx, ldr, eps, code, wcode, on.raw)
+                                        ldx, ldr, eps, code, wcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return y, scale, (x if sum_out is None else sum_out)
@@ -290,11 +302,10 @@ def delta_add_rmsnorm_bwd(dy, sum, weight, rstd, dsum=None, *, dx=None, stream=N
     pd = _optional(dsum, "dsum", dy.shape, dy.dtype, dev)
     pr = _tensor(rstd, "rstd", dy.shape[:-1], torch.float32, dev)
     pw, wcode = _weight(weight, D, dy.dtype, dev)
-    on = _On(dev, stream)
-    dx = on.out(dx, "dx", dy.shape, dy.dtype)
-    dweight = on.empty((D,), torch.float32)
+    dx = _output(dx, "dx", dy.shape, dy.dtype, dev, stream)
+    dweight = _empty((D,), torch.float32, dev, stream)
     st = _lib().delta_add_rmsnorm_bwd(py, ps, pw, pr, pd, dx.data_ptr(), dweight.data_ptr(),
-                                      dy.numel() // D if D else 0, D, code, wcode, on.raw)
+                                      dy.numel() // D if D else 0, D, code, wcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return dx, dweight

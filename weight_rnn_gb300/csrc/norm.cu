@@ -10,13 +10,15 @@
 //   dx = rstd (w dy - t^ mean_d(w dy t^)) + dsum,   dw = sum over rows of dy t^
 //
 // HBM-bound: two tensors in and two out (8 bytes an element in bfloat16, 7
-// with an 8-bit y; backward three in, one out).  A row stays in registers
-// between its reductions: a row has `nt` threads of kPer 16-byte vectors, and
-// the CTAs walk the rows with the next row's loads in flight, so that the
-// weight is read once a CTA and the backward keeps its column sums in
-// registers.  Those sums meet in a second kernel in CTA order, so the result
-// does not depend on scheduling.  Rows whose width, strides or addresses are
-// not multiples of 16 bytes take one element per load instead.
+// with an 8-bit y; backward three in, one out).  A row has `nt` threads of
+// kPer 16-byte vectors.  The CTAs walk the rows, so that the weight is read
+// once a CTA and the backward keeps its column sums in registers; each thread
+// copies its own vectors of the next row or two into its own places of a
+// ring in shared memory, asynchronously, which keeps the memory busy during
+// the reductions without a barrier or a register.  The column sums meet in a
+// second kernel in CTA order, so the result does not depend on scheduling.
+// Rows whose width, strides or addresses are not multiples of 16 bytes take
+// one element per load, straight into registers.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -96,45 +98,120 @@ __device__ __forceinline__ void load_weight(const void *weight, bool w_bf16, int
     }
 }
 
+// rows in a thread's ring: three, or two where a row of N tensors of `per`
+// vectors and kMostThreads threads would pass a CTA's shared memory
+__host__ __device__ constexpr int ring_rows(int N, int per) { return N * per >= 12 ? 2 : 3; }
+
+// This thread's vectors of one row: N tensors of kPer vectors.  Whole vectors
+// (V > 1) pass through the thread's ring, single elements through registers,
+// one row ahead.
+template <typename In, int V, int kPer, int N>
+struct Rows {
+  using Vec = APack<In, V>;
+  static constexpr bool kRing = V > 1;
+  static constexpr int kStages = ring_rows(N, kPer);
+  const In *base[N];
+  int64_t ld[N], rows, D;
+  Vec *ring;  // [kStages][N][kPer][threads of the CTA]
+  Vec held[kRing ? 1 : N][kRing ? 1 : kPer], next[kRing ? 1 : N][kRing ? 1 : kPer];
+  int slot = 0;
+
+  __device__ __forceinline__ int threads() const { return blockDim.x * blockDim.y; }
+  __device__ __forceinline__ int self() const { return threadIdx.y * blockDim.x + threadIdx.x; }
+  __device__ __forceinline__ void fetch(int64_t row, int to) {
+    if constexpr (kRing) {
+      if (row < rows) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+            if (d < D && base[n]) {
+              const uint32_t at =
+                  (uint32_t)__cvta_generic_to_shared(ring + ((to * N + n) * kPer + j) * threads() + self());
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(base[n] + row * ld[n] + d)
+                           : "memory");
+            }
+          }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else if (row < rows) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int64_t d = (int64_t)j * blockDim.x + threadIdx.x;
+          if (d < D && base[n]) next[n][j].v[0] = base[n][row * ld[n] + d];
+        }
+    }
+  }
+  __device__ __forceinline__ void start(int64_t first, int64_t step) {
+    if constexpr (kRing) {
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) fetch(first + i * step, i);
+    } else {
+      fetch(first, 0);
+    }
+  }
+  // the row becomes readable, and a later one is asked for
+  __device__ __forceinline__ void turn(int64_t row, int64_t step) {
+    if constexpr (kRing) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      fetch(row + (kStages - 1) * step, slot == 0 ? kStages - 1 : slot - 1);
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) held[n][j] = next[n][j];
+      fetch(row + step, 0);
+    }
+  }
+  __device__ __forceinline__ void done() {
+    if constexpr (kRing) slot = slot == kStages - 1 ? 0 : slot + 1;
+  }
+  __device__ __forceinline__ void finish() {
+    if constexpr (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __device__ __forceinline__ Vec get(int n, int j) const {
+    if constexpr (kRing)
+      return ring[((slot * N + n) * kPer + j) * threads() + self()];
+    else
+      return held[n][j];
+  }
+};
+
 // ------------------------------------------------------------------ forward
 // blockDim (nt, rows a CTA); a thread's vectors are nt apart
 template <typename In, int V, int kPer, bool kQuant>
-__global__ void __launch_bounds__(kMostThreads) norm_fwd_kernel(NormArgs p) {
+__global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) norm_fwd_kernel(NormArgs p) {
   __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
-  using Vec = APack<In, V>;
+  extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
-  const In *x = static_cast<const In *>(p.x), *r = static_cast<const In *>(p.residual);
   float w[kPer][V];
   load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Vec xv[kPer], rv[kPer];
-  auto fetch = [&](int64_t row) {
-    if (row >= p.rows) return;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
-      if (d < p.D) {
-        xv[j] = *reinterpret_cast<const Vec *>(x + row * p.ldx + d);
-        if (r) rv[j] = *reinterpret_cast<const Vec *>(r + row * p.ldr + d);
-      }
-    }
-  };
-  fetch(first);
+  Rows<In, V, kPer, 2> in;
+  in.base[0] = static_cast<const In *>(p.x); in.base[1] = static_cast<const In *>(p.residual);
+  in.ld[0] = p.ldx; in.ld[1] = p.ldr; in.rows = p.rows; in.D = p.D;
+  in.ring = reinterpret_cast<APack<In, V> *>(ring);
+  in.start(first, step);
   int buf = 0;
   // every row of the CTA takes part in the barriers until the last is done
   for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
+    in.turn(row, step);
     float t[kPer][V], ss = 0.f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const bool in = row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
+      const bool on = row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
+      const APack<In, V> xv = in.get(0, j), rv = in.get(1, j);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        t[j][i] = in ? to_f(xv[j].v[i]) + (r ? to_f(rv[j].v[i]) : 0.f) : 0.f;
+        t[j][i] = on ? to_f(xv.v[i]) + (p.residual ? to_f(rv.v[i]) : 0.f) : 0.f;
         ss = fmaf(t[j][i], t[j][i], ss);
       }
     }
-    fetch(row + step);
+    in.done();
     ss = row_reduce<false>(ss, part[kQuant ? 0 : buf], nwarp);
     const float rstd = rsqrtf(ss / (float)p.D + p.eps);
     float inv = 1.f;
@@ -167,16 +244,17 @@ __global__ void __launch_bounds__(kMostThreads) norm_fwd_kernel(NormArgs p) {
       }
     }
   }
+  in.finish();
 }
 
 // ----------------------------------------------------------------- backward
+// The row is read from its ring twice, before and after the reduction, rather
+// than held: that is what lets two CTAs of 512 threads share an SM.
 template <typename In, int V, int kPer>
-__global__ void __launch_bounds__(kMostThreads) norm_bwd_kernel(NormBwdArgs p) {
-  __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
-  using Vec = APack<In, V>;
+__global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) norm_bwd_kernel(NormBwdArgs p) {
+  __shared__ float part[2][8 * 32];
+  extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
-  const In *dy = static_cast<const In *>(p.dy), *sum = static_cast<const In *>(p.sum),
-           *ds = static_cast<const In *>(p.dsum);
   float w[kPer][V], dw[kPer][V];
   load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
 #pragma unroll
@@ -185,52 +263,49 @@ __global__ void __launch_bounds__(kMostThreads) norm_bwd_kernel(NormBwdArgs p) {
     for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Vec gv[kPer], tv[kPer], sv[kPer];
-  float rs = 0.f;
-  auto fetch = [&](int64_t row) {
-    if (row >= p.rows) return;
-    rs = p.rstd[row];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
-      if (d < p.D) {
-        gv[j] = *reinterpret_cast<const Vec *>(dy + row * p.D + d);
-        tv[j] = *reinterpret_cast<const Vec *>(sum + row * p.D + d);
-        if (ds) sv[j] = *reinterpret_cast<const Vec *>(ds + row * p.D + d);
-      }
-    }
-  };
-  fetch(first);
+  Rows<In, V, kPer, 3> in;
+  in.base[0] = static_cast<const In *>(p.dy); in.base[1] = static_cast<const In *>(p.sum);
+  in.base[2] = static_cast<const In *>(p.dsum);
+  in.ld[0] = in.ld[1] = in.ld[2] = in.D = p.D; in.rows = p.rows;
+  in.ring = reinterpret_cast<APack<In, V> *>(ring);
+  in.start(first, step);
+  float ahead = first < p.rows ? p.rstd[first] : 0.f;
   int buf = 0;
   for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
-    float g[kPer][V], t[kPer][V], s[kPer][V], dot = 0.f;
-    const float rstd = rs;
+    in.turn(row, step);
+    const float rstd = ahead;
+    if (row + step < p.rows) ahead = p.rstd[row + step];
+    float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const bool in = row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
+      const APack<In, V> gv = in.get(0, j), tv = in.get(1, j);
+      if (row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        t[j][i] = in ? to_f(tv[j].v[i]) * rstd : 0.f;
-        const float y = in ? to_f(gv[j].v[i]) : 0.f;
-        s[j][i] = in && ds ? to_f(sv[j].v[i]) : 0.f;
-        dw[j][i] = fmaf(y, t[j][i], dw[j][i]);
-        g[j][i] = y * w[j][i];
-        dot = fmaf(g[j][i], t[j][i], dot);
+        for (int i = 0; i < V; ++i) {
+          const float t = to_f(tv.v[i]) * rstd, y = to_f(gv.v[i]);
+          dw[j][i] = fmaf(y, t, dw[j][i]);
+          dot = fmaf(y * w[j][i], t, dot);
+        }
       }
     }
-    fetch(row + step);
     dot = row_reduce<false>(dot, part[buf], nwarp) / (float)p.D;
     if (row < p.rows) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
         if (d >= p.D) continue;
+        const APack<In, V> gv = in.get(0, j), tv = in.get(1, j), sv = in.get(2, j);
+        float g[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[j][i] = fmaf(rstd, g[j][i] - t[j][i] * dot, s[j][i]);
-        store_v<In, V>(static_cast<In *>(p.dx) + row * p.D + d, g[j]);
+        for (int i = 0; i < V; ++i)
+          g[i] = fmaf(rstd, to_f(gv.v[i]) * w[j][i] - to_f(tv.v[i]) * rstd * dot,
+                      p.dsum ? to_f(sv.v[i]) : 0.f);
+        store_v<In, V>(static_cast<In *>(p.dx) + row * p.D + d, g);
       }
     }
+    in.done();
   }
+  in.finish();
   const int64_t at = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.D;
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
@@ -262,6 +337,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, flo
 struct Plan {
   int V, per, nt, rpc;  // elements a vector, vectors a thread, threads a row, rows a CTA
   int64_t grid;
+  int smem;             // the ring
 };
 
 bool vec_ok(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
@@ -269,7 +345,7 @@ bool vec_ok(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0;
 // One vector a thread while rows are few (latency), two where a row has more
 // than a warp's worth and there are rows for every SM (fewer, longer-lived
 // CTAs); more only where a row would not fit kMostThreads threads.
-Plan plan(int64_t rows, int64_t D, int vec, bool aligned) {
+Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors) {
   Plan q;
   q.V = aligned ? vec : 1;
   const int64_t n = (D + q.V - 1) / q.V;  // vectors a row
@@ -283,7 +359,11 @@ Plan plan(int64_t rows, int64_t D, int vec, bool aligned) {
   q.nt = (int)((n + q.per - 1) / q.per + 31) / 32 * 32;
   q.rpc = q.nt >= 256 ? 1 : 256 / q.nt;
   const int64_t ctas = (rows + q.rpc - 1) / q.rpc;
-  const int64_t cap = (int64_t)sms * 4;
+  q.smem = aligned ? ring_rows(tensors, q.per) * tensors * q.per * q.nt * q.rpc * 16 : 0;
+  // as many CTAs as an SM holds: by threads at 64 registers, and by rings
+  int fit = 1024 / (q.nt * q.rpc);
+  if (q.smem && fit > 200 * 1024 / q.smem) fit = 200 * 1024 / q.smem;
+  const int64_t cap = (int64_t)sms * (fit > 1 ? fit : 1);
   q.grid = ctas < cap ? ctas : cap;
   return q;
 }
@@ -308,22 +388,27 @@ cudaError_t dispatch(const Plan &q, X &&...x) {
   return cudaErrorInvalidConfiguration;
 }
 
+template <typename K, typename A>
+cudaError_t go(K kern, const A &a, const Plan &q, cudaStream_t s) {
+  if (q.smem > 48 * 1024 - 4096) {  // more than the default only after asking
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, q.smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(unsigned)q.grid, dim3(q.nt, q.rpc), q.smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename In, int V, int kPer>
 struct FwdOne {
   static cudaError_t run(const NormArgs &a, const Plan &q, cudaStream_t s) {
-    const dim3 block(q.nt, q.rpc);
-    if (a.scale)
-      norm_fwd_kernel<In, V, kPer, true><<<(unsigned)q.grid, block, 0, s>>>(a);
-    else
-      norm_fwd_kernel<In, V, kPer, false><<<(unsigned)q.grid, block, 0, s>>>(a);
-    return cudaGetLastError();
+    return a.scale ? go(norm_fwd_kernel<In, V, kPer, true>, a, q, s)
+                   : go(norm_fwd_kernel<In, V, kPer, false>, a, q, s);
   }
 };
 template <typename In, int V, int kPer>
 struct BwdOne {
   static cudaError_t run(const NormBwdArgs &a, const Plan &q, cudaStream_t s) {
-    norm_bwd_kernel<In, V, kPer><<<(unsigned)q.grid, dim3(q.nt, q.rpc), 0, s>>>(a);
-    return cudaGetLastError();
+    return go(norm_bwd_kernel<In, V, kPer>, a, q, s);
   }
 };
 
@@ -332,14 +417,14 @@ cudaError_t fwd_all(const NormArgs &a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(In);
   const bool ok = a.D % V == 0 && a.ldx % V == 0 && (!a.residual || a.ldr % V == 0) && vec_ok(a.x) &&
                   vec_ok(a.residual);
-  const Plan q = plan(a.rows, a.D, V, ok);
+  const Plan q = plan(a.rows, a.D, V, ok, 2);
   return dispatch<In, FwdOne>(q, a, q, s);
 }
 
 template <typename In>
 Plan bwd_plan(const NormBwdArgs &a) {
   constexpr int V = 16 / sizeof(In);
-  return plan(a.rows, a.D, V, a.D % V == 0);
+  return plan(a.rows, a.D, V, a.D % V == 0, 3);
 }
 template <typename In>
 cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
