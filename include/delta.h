@@ -554,6 +554,65 @@ int delta_add_rmsnorm_bwd(const void *dy, const void *sum, const void *weight, c
                           const void *dsum, void *dx, float *dweight, int64_t rows, int D,
                           delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream);
 
+typedef enum {
+    DELTA_ACT_NONE = 0,
+    DELTA_ACT_SILU = 1, /* p s(p), s the logistic function */
+    DELTA_ACT_GELU = 2  /* the tanh form, p s(2 sqrt(2/pi) (p + 0.044715 p^3)) */
+} delta_act;
+
+/*
+ * delta_linear_fwd -- a linear layer with its epilogue,
+ *
+ *   pre = x w^T + bias,   out = act(pre) + residual,
+ *
+ * summed and finished in float32 and rounded once.
+ *
+ *   x        [M, K]  dtype, row stride ldx
+ *   w        [N, K]  dtype, row stride ldw
+ *   bias     [N]     bdtype, or NULL
+ *   residual [M, N]  dtype, row stride ldr, or NULL
+ *   out      [M, N]  dtype; may be residual itself (then contiguous)
+ *   pre      [M, N]  dtype, for delta_linear_bwd, or NULL
+ *
+ * K > 0.  bfloat16 runs on the tensor cores: tcgen05 for M > 32, and for
+ * fewer rows a kernel that streams w once.  x or w whose address or row stride
+ * is not a multiple of 16 bytes is first copied to scratch (M > 32), taken
+ * stream-ordered from the library's pool as delta_fwd does.  float32 runs on
+ * the CUDA cores, a correctness path.
+ */
+int delta_linear_fwd(const void *x, const void *w, const void *bias, const void *residual, void *out, void *pre,
+                     int M, int N, int K, int64_t ldx, int64_t ldw, int64_t ldr, delta_act act,
+                     delta_dtype dtype, delta_dtype bdtype, struct CUstream_st *stream);
+
+/*
+ * delta_linear_quant -- the same with x and w in e4m3, x_scale [M] and w_scale
+ * [N] float32 (a scale a row, as delta_add_rmsnorm_quant writes them):
+ *
+ *   pre = (x w^T) x_scale[m] w_scale[n] + bias.   out and residual are bfloat16.
+ */
+int delta_linear_quant(const void *x, const float *x_scale, const void *w, const float *w_scale,
+                       const void *bias, const void *residual, void *out, int M, int N, int K, int64_t ldx,
+                       int64_t ldw, int64_t ldr, delta_act act, delta_dtype bdtype, struct CUstream_st *stream);
+
+/*
+ * delta_linear_bwd -- gradients of delta_linear_fwd: with dpre = dout act'(pre),
+ *
+ *   dx = dpre w,   dw = dpre^T x,   dbias = sum over rows of dpre
+ *
+ * (the residual's gradient is dout itself).
+ *
+ *   x, w   as in the forward;  dout, pre [M, N] dtype, contiguous (pre may be
+ *          NULL without an activation)
+ *   dx     [M, K] dtype,  dw [N, K] dtype,  dbias [N] float32; NULL: not wanted
+ *
+ * In bfloat16, dpre is rounded to bfloat16 as an operand of the two products
+ * (dbias sums it unrounded).  It and packed operands go to scratch from the
+ * library's pool, stream-ordered.
+ */
+int delta_linear_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
+                     float *dbias, int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act,
+                     delta_dtype dtype, struct CUstream_st *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -118,8 +118,55 @@ def test_norm_quant_refuses(lib, kw, status):
 def test_norm_bwd_refuses(lib, kw, status):
     assert call(lib.delta_add_rmsnorm_bwd, NBWD, NBWD, kw) == status
 
+LIN = dict(x=P(1), w=P(2), bias=P(3), residual=P(4), out=P(5), pre=P(6), M=40, N=64, K=32, ldx=32, ldw=32,
+           ldr=64, act=1, dtype=1, bdtype=0, stream=None)
+LQ = dict(x=P(1), x_scale=P(2), w=P(3), w_scale=P(4), bias=P(5), residual=P(6), out=P(7), M=40, N=64, K=32,
+          ldx=32, ldw=32, ldr=64, act=1, bdtype=0, stream=None)
+LB = dict(x=P(1), w=P(2), dout=P(3), pre=P(4), dx=P(5), dw=P(6), dbias=P(7), M=40, N=64, K=32, ldx=32,
+          ldw=32, act=1, dtype=1, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(K=-1), INVALID), (dict(K=0), INVALID),
+    (dict(act=3), INVALID), (dict(dtype=2), INVALID), (dict(bdtype=5), INVALID),
+    (dict(ldx=31), INVALID), (dict(ldw=31), INVALID), (dict(ldr=63), INVALID), (dict(ldx=1 << 31), UNSUP),
+    (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(out=None), INVALID),
+    (dict(x=P(1, 1)), ALIGN), (dict(w=P(2, 1)), ALIGN), (dict(bias=P(3, 2)), ALIGN),
+    (dict(residual=P(4, 1)), ALIGN), (dict(out=P(5, 8)), ALIGN), (dict(pre=P(6, 2)), ALIGN),
+    (dict(out=P(1)), INVALID), (dict(out=P(2, 32)), INVALID), (dict(out=P(3)), INVALID),
+    (dict(out=P(4, 128)), INVALID), (dict(out=P(4), ldr=72), INVALID), (dict(pre=P(4)), INVALID),
+    (dict(pre=P(5)), INVALID),
+])
+def test_linear_fwd_refuses(lib, kw, status):
+    assert call(lib.delta_linear_fwd, LIN, LIN, kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(K=0), INVALID), (dict(act=-1), INVALID), (dict(x_scale=None), INVALID), (dict(w_scale=None), INVALID),
+    (dict(x_scale=P(2, 2)), ALIGN), (dict(w_scale=P(4, 1)), ALIGN), (dict(out=P(7, 4)), ALIGN),
+    (dict(out=P(2)), INVALID), (dict(out=P(4)), INVALID), (dict(residual=P(6, 1)), ALIGN),
+])
+def test_linear_quant_refuses(lib, kw, status):
+    assert call(lib.delta_linear_quant, LQ, LQ, kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), INVALID), (dict(K=0), INVALID), (dict(act=9), INVALID), (dict(dtype=2), INVALID),
+    (dict(dout=None), INVALID), (dict(pre=None), INVALID), (dict(x=None), INVALID), (dict(w=None), INVALID),
+    (dict(ldx=8), INVALID), (dict(ldw=8), INVALID),
+    (dict(dout=P(3, 2)), ALIGN), (dict(pre=P(4, 8)), ALIGN), (dict(dx=P(5, 2)), ALIGN),
+    (dict(dbias=P(7, 4)), ALIGN), (dict(x=P(1, 1)), ALIGN),
+    (dict(dx=P(1)), INVALID), (dict(dw=P(2)), INVALID), (dict(dw=P(3)), INVALID), (dict(dbias=P(4)), INVALID),
+    (dict(dw=P(5)), INVALID),
+])
+def test_linear_bwd_refuses(lib, kw, status):
+    assert call(lib.delta_linear_bwd, LB, LB, kw) == status
+
 
 def test_empty_problems_are_fine(lib):
+    assert call(lib.delta_linear_fwd, LIN, LIN, dict(M=0)) == 0
+    assert call(lib.delta_linear_quant, LQ, LQ, dict(N=0)) == 0
+    assert call(lib.delta_linear_bwd, LB, LB, dict(dx=None, dw=None, dbias=None)) == 0
     assert call(lib.delta_scan_fwd, SCAN, SCAN, dict(B=0)) == 0
     assert call(lib.delta_scan_fwd, SCAN, SCAN, dict(D=0)) == 0
     assert call(lib.delta_scan_step, STEP, STEP, dict(B=0)) == 0
@@ -130,7 +177,8 @@ def test_empty_problems_are_fine(lib):
 
 @pytest.mark.parametrize("name,order", [
     ("delta_scan_fwd", SCAN), ("delta_scan_step", STEP), ("delta_scan_bwd", SBWD),
-    ("delta_add_rmsnorm_fwd", NORM), ("delta_add_rmsnorm_quant", QUANT), ("delta_add_rmsnorm_bwd", NBWD)])
+    ("delta_add_rmsnorm_fwd", NORM), ("delta_add_rmsnorm_quant", QUANT), ("delta_add_rmsnorm_bwd", NBWD),
+    ("delta_linear_fwd", LIN), ("delta_linear_quant", LQ), ("delta_linear_bwd", LB)])
 def test_injected_failure(lib, name, order):
     wr.delta_inject_failure(1)
     try:
@@ -144,7 +192,8 @@ def test_binding_refuses_host_tensors():
     x, w = torch.zeros(1, 4, 8), torch.ones(8)
     for f in (lambda: wr.delta_scan_fwd(x, x), lambda: wr.delta_scan_step(x[0], x[0], x[0]),
               lambda: wr.delta_scan_bwd(x, x, x, x), lambda: wr.delta_add_rmsnorm_fwd(x, w),
-              lambda: wr.delta_add_rmsnorm_quant(x, w), lambda: wr.delta_add_rmsnorm_bwd(x, x, w, x[..., 0])):
+              lambda: wr.delta_linear_fwd(x, x[0]), lambda: wr.delta_linear_bwd(x, x[0], x),
+              lambda: wr.delta_linear_quant(x, w, x[0], w), lambda: wr.delta_add_rmsnorm_quant(x, w), lambda: wr.delta_add_rmsnorm_bwd(x, x, w, x[..., 0])):
         with pytest.raises(ValueError, match="needs CUDA tensors"):
             f()
 

@@ -6,7 +6,7 @@ arguments: shape/dtype checks, output allocation through PyTorch, the
 current CUDA stream, and status-to-exception mapping.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback, and a
 missing library raises immediately.  The operators around the mixers in a
-block (scan, norm) are in ``block.py`` and exported here.
+block (scan, norm, linear) are in ``block.py`` and exported here.
 """
 from __future__ import annotations
 
@@ -18,7 +18,8 @@ import torch
 
 from . import block
 from .block import (delta_add_rmsnorm_bwd, delta_add_rmsnorm_fwd, delta_add_rmsnorm_quant,
-                    delta_scan_bwd, delta_scan_fwd, delta_scan_step)
+                    delta_linear_bwd, delta_linear_fwd, delta_linear_quant, delta_scan_bwd,
+                    delta_scan_fwd, delta_scan_step)
 
 __all__ = ["delta_fwd", "delta_bwd", "delta_fwd_kda", "delta_step_kda", "delta_prologue",
            "delta_fwd_prologue", "delta_step_prologue",

@@ -1,6 +1,7 @@
 """Operators around the token mixers in a block: the gated linear recurrence
-(``delta_scan_*``) and the residual addition with RMS norm
-(``delta_add_rmsnorm_*``).
+(``delta_scan_*``), the residual addition with RMS norm
+(``delta_add_rmsnorm_*``) and the linear layer with its epilogue
+(``delta_linear_*``).
 
 Bindings over the C ABI of ``libdelta.so`` with the ABI's names: argument
 checks, output allocation, the current CUDA stream, statuses as exceptions.
@@ -17,11 +18,16 @@ DELTA_SCAN_LINEAR = 0
 DELTA_SCAN_SIGMOID = 1
 _SCAN_FORMS = {"linear": DELTA_SCAN_LINEAR, "sigmoid": DELTA_SCAN_SIGMOID}
 SCAN_BLOCK = 64  # steps between two saved states
+DELTA_ACT_NONE = 0
+DELTA_ACT_SILU = 1
+DELTA_ACT_GELU = 2
+_ACTS = {"none": DELTA_ACT_NONE, "silu": DELTA_ACT_SILU, "gelu": DELTA_ACT_GELU}
 _CODES = {torch.float32: 0, torch.bfloat16: 1}
 E4M3 = torch.float8_e4m3fn
 
 SYMBOLS = ("delta_scan_fwd", "delta_scan_step", "delta_scan_bwd", "delta_add_rmsnorm_fwd",
-           "delta_add_rmsnorm_quant", "delta_add_rmsnorm_bwd")
+           "delta_add_rmsnorm_quant", "delta_add_rmsnorm_bwd", "delta_linear_fwd",
+           "delta_linear_quant", "delta_linear_bwd")
 
 
 def declare(lib) -> None:
@@ -33,7 +39,10 @@ def declare(lib) -> None:
             ("delta_scan_bwd", [p] * 9 + [i] * 3 + [n] * 4 + [i] * 2 + [p]),
             ("delta_add_rmsnorm_fwd", [p] * 6 + [n, i, n, n, f, i, i, p]),
             ("delta_add_rmsnorm_quant", [p] * 6 + [n, i, n, n, f, i, i, p]),
-            ("delta_add_rmsnorm_bwd", [p] * 7 + [n, i, i, i, p])):
+            ("delta_add_rmsnorm_bwd", [p] * 7 + [n, i, i, i, p]),
+            ("delta_linear_fwd", [p] * 6 + [i] * 3 + [n] * 3 + [i] * 3 + [p]),
+            ("delta_linear_quant", [p] * 7 + [i] * 3 + [n] * 3 + [i] * 2 + [p]),
+            ("delta_linear_bwd", [p] * 7 + [i] * 3 + [n] * 2 + [i] * 2 + [p])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = i, args
 
@@ -309,3 +318,88 @@ def delta_add_rmsnorm_bwd(dy, sum, weight, rstd, dsum=None, *, dx=None, stream=N
     if st:
         _raise(st)
     return dx, dweight
+
+
+def _linear_begin(x, w, bias, residual, act, dtype, odt, dev):
+    """shared checks: sizes, pointers and row strides of a linear layer"""
+    acode = _ACTS.get(act)
+    if acode is None:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or x.dim() < 1:
+        raise ValueError("x must be [..., K] and w [N, K]")
+    N, K = w.shape
+    px, ldx = _rows(x, "x", x.shape[:-1] + (K,), dtype, dev)
+    pw = _tensor(w, "w", w.shape, dtype, dev, True)
+    pb, bcode = (None, 0) if bias is None else _weight(bias, N, odt, dev, "bias")
+    shape = x.shape[:-1] + (N,)
+    pr, ldr = (None, N) if residual is None else _rows(residual, "residual", shape, odt, dev)
+    M = 1
+    for n in x.shape[:-1]:
+        M *= n
+    return acode, M, N, K, px, ldx, pw, w.stride(0), pb, bcode, pr, ldr, shape
+
+
+def delta_linear_fwd(x, w, bias=None, residual=None, *, act="none", save_pre=False, out=None,
+                     stream=None):
+    """``out = act(x w^T + bias) + residual``, finished in float32.
+
+    x [..., K] and w [N, K] bfloat16 or float32 (rows may be strided), bias [N]
+    float32 or bfloat16, residual [..., N] in x's type; ``act`` is "none",
+    "silu" or "gelu" (tanh form).  Returns out [..., N], with ``save_pre``
+    ``(out, pre)`` for ``delta_linear_bwd``.  ``out`` may be ``residual``.
+    """
+    code, dev = _begin(x, "delta_linear_fwd", 0)
+    dt = x.dtype
+    acode, M, N, K, px, ldx, pw, ldw, pb, bcode, pr, ldr, shape = _linear_begin(
+        x, w, bias, residual, act, dt, dt, dev)
+    out = _output(out, "out", shape, dt, dev, stream)
+    pre = _empty(shape, dt, dev, stream) if save_pre else None
+    st = _lib().delta_linear_fwd(px, pw, pb, pr, out.data_ptr(),
+                                 None if pre is None else pre.data_ptr(), M, N, K, ldx, ldw, ldr,
+                                 acode, code, bcode, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return (out, pre) if save_pre else out
+
+
+def delta_linear_quant(x, x_scale, w, w_scale, bias=None, residual=None, *, act="none", out=None,
+                       stream=None):
+    """The same with x [..., K] and w [N, K] in float8_e4m3fn and a float32 scale
+    for each of their rows, x_scale [...] and w_scale [N]; residual and out are
+    bfloat16."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("delta_linear_quant needs CUDA tensors")
+    acode, M, N, K, px, ldx, pw, ldw, pb, bcode, pr, ldr, shape = _linear_begin(
+        x, w, bias, residual, act, E4M3, torch.bfloat16, dev)
+    psx = _tensor(x_scale, "x_scale", x.shape[:-1], torch.float32, dev)
+    psw = _tensor(w_scale, "w_scale", (N,), torch.float32, dev)
+    out = _output(out, "out", shape, torch.bfloat16, dev, stream)
+    st = _lib().delta_linear_quant(px, psx, pw, psw, pb, pr, out.data_ptr(), M, N, K, ldx, ldw,
+                                   ldr, acode, bcode, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return out
+
+
+def delta_linear_bwd(x, w, dout, pre=None, *, act="none", want=(True, True, True), stream=None):
+    """Gradients of ``delta_linear_fwd``: x and w as there, dout and pre [..., N]
+    contiguous (pre only with an activation).  Returns ``(dx, dw, dbias)``, dx
+    and dw in x's type, dbias float32; those not wanted are None."""
+    code, dev = _begin(x, "delta_linear_bwd", 0)
+    dt = x.dtype
+    acode, M, N, K, px, ldx, pw, ldw, _, _, _, _, shape = _linear_begin(
+        x, w, None, None, act, dt, dt, dev)
+    po = _tensor(dout, "dout", shape, dt, dev)
+    pp = _tensor(pre, "pre", shape, dt, dev) if acode or pre is not None else None
+    dx = _empty(x.shape, dt, dev, stream) if want[0] else None
+    dw = _empty((N, K), dt, dev, stream) if want[1] else None
+    db = _empty((N,), torch.float32, dev, stream) if want[2] else None
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = _lib().delta_linear_bwd(px, pw, po, pp, ptr(dx), ptr(dw), ptr(db), M, N, K, ldx, ldw,
+                                 acode, code, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return dx, dw, db

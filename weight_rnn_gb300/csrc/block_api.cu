@@ -1,5 +1,5 @@
 // block_api.cu -- the C ABI of the operators that stand around the token
-// mixers in a block (scan, norm): argument checks, scratch and launches, with
+// mixers in a block (scan, norm, linear): argument checks, scratch and launches, with
 // the conventions of api.cu: nothing is synchronised, errors are returned
 // before anything is enqueued.
 #include <cuda_runtime.h>
@@ -139,6 +139,174 @@ int run_norm_fwd(const void *x, const void *residual, const void *weight, void *
   a.eps = eps; a.bf16 = dtype == DELTA_BF16; a.w_bf16 = wdtype == DELTA_BF16;
   const cudaError_t err = delta::launch_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "norm kernel launch");
+}
+
+int linear_sizes(int M, int N, int K, int64_t ldx, int64_t ldw, int64_t ldr, delta_act act) {
+  if (M < 0 || N < 0 || K < 0) return fail(DELTA_ERR_INVALID, "negative size M=%d N=%d K=%d", M, N, K);
+  if (act != DELTA_ACT_NONE && act != DELTA_ACT_SILU && act != DELTA_ACT_GELU)
+    return fail(DELTA_ERR_INVALID, "unknown activation %d", (int)act);
+  if (K == 0) return fail(DELTA_ERR_INVALID, "K must be positive");
+  if ((M > 1 && (ldx < K || ldr < N)) || (N > 1 && ldw < K))
+    return fail(DELTA_ERR_INVALID, "row strides ldx=%lld ldw=%lld ldr=%lld must cover a row", (long long)ldx,
+                (long long)ldw, (long long)ldr);
+  const int64_t most = int64_t(1) << 31;
+  if (ldx >= most || ldw >= most || ldr >= most) return fail(DELTA_ERR_UNSUPPORTED, "row stride too large");
+  return DELTA_OK;
+}
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// Stream-ordered scratch of one call, cut into 256-byte pieces.
+struct Scratch {
+  void *base = nullptr;
+  int64_t used = 0, size = 0;
+  cudaStream_t s;
+  explicit Scratch(cudaStream_t st) : s(st) {}
+  void want(int64_t bytes) { size += up(bytes, 256); }
+  cudaError_t take() {
+    if (size == 0) return cudaSuccess;
+    cudaMemPool_t pool;
+    const cudaError_t e = scratch_pool(&pool);
+    return e != cudaSuccess ? e : cudaMallocFromPoolAsync(&base, (size_t)size, pool, s);
+  }
+  void *cut(int64_t bytes) {
+    void *p = static_cast<unsigned char *>(base) + used;
+    used += up(bytes, 256);
+    return p;
+  }
+  cudaError_t release() { return base ? cudaFreeAsync(base, s) : cudaSuccess; }
+};
+
+// an operand of the tensor-core product: usable as it lies, or to be packed
+// into rows that are multiples of 16 bytes
+struct Operand {
+  const void *p;
+  int64_t rows, cols, ld;
+  int size;
+  bool whole() const { return aligned16(p) && ld * size % 16 == 0; }
+  int64_t ldp() const { return up(cols, 16 / size); }
+  int64_t bytes() const { return rows * ldp() * size; }
+  cudaError_t pack(Scratch &scr, cudaStream_t s) {
+    if (whole()) return cudaSuccess;
+    void *to = scr.cut(bytes());
+    const cudaError_t e = delta::launch_pack(p, to, rows, cols, ld, ldp(), size, s);
+    p = to;
+    ld = ldp();
+    return e;
+  }
+};
+Operand operand(const void *p, int64_t rows, int64_t cols, int64_t ld, int size) {
+  return Operand{p, rows, cols, rows > 1 ? ld : up(cols, 16 / size), size};
+}
+
+cudaError_t linear_forward(const delta::LinearArgs &a, cudaStream_t s) {
+  if (a.kind == delta::kLinF32)
+    return delta::launch_gemm_f32(a, static_cast<const float *>(a.x), a.ldx, 1, static_cast<const float *>(a.w),
+                                  a.ldw, 1, a.K, s);
+  if (a.M <= delta::kLinSmallM) return delta::launch_linear_small(a, s);
+  const int size = a.kind == delta::kLinE4m3 ? 1 : 2;
+  Operand x = operand(a.x, a.M, a.K, a.ldx, size), w = operand(a.w, a.N, a.K, a.ldw, size);
+  Scratch scr(s);
+  if (!x.whole()) scr.want(x.bytes());
+  if (!w.whole()) scr.want(w.bytes());
+  cudaError_t err = scr.take();
+  if (err != cudaSuccess) return err;
+  err = x.pack(scr, s);
+  if (err == cudaSuccess) err = w.pack(scr, s);
+  if (err == cudaSuccess) err = delta::launch_gemm_tc({x.p, w.p, x.ld, w.ld, a.K, false, false, a}, s);
+  const cudaError_t ef = scr.release();
+  return err != cudaSuccess ? err : ef;
+}
+
+int run_linear(const void *x, const void *w, const float *x_scale, const float *w_scale, const void *bias,
+               const void *residual, void *out, void *pre, int M, int N, int K, int64_t ldx, int64_t ldw,
+               int64_t ldr, delta_act act, delta::LinearKind kind, delta_dtype bdtype,
+               struct CUstream_st *stream) {
+  int st;
+  if ((st = linear_sizes(M, N, K, ldx, ldw, residual ? ldr : N, act)) != DELTA_OK) return st;
+  if ((st = check_dtype(bdtype)) != DELTA_OK) return st;
+  if (M == 0 || N == 0) return DELTA_OK;
+  if (!x || !w || !out) return fail(DELTA_ERR_INVALID, "x, w and out must be non-NULL");
+  const bool quant = kind == delta::kLinE4m3;
+  if (quant && (!x_scale || !w_scale)) return fail(DELTA_ERR_INVALID, "the scales must be non-NULL");
+  const int64_t e = kind == delta::kLinF32 ? 4 : quant ? 1 : 2, oe = kind == delta::kLinF32 ? 4 : 2;
+  if (!aligned_to(x, e) || !aligned_to(w, e) || !aligned_to(residual, oe) || !aligned_to(bias, esize(bdtype)) ||
+      !aligned_to(x_scale, 4) || !aligned_to(w_scale, 4))
+    return fail(DELTA_ERR_ALIGN, "every input must be aligned to its elements");
+  if (!aligned16(out) || !aligned16(pre)) return fail(DELTA_ERR_ALIGN, "out and pre must be 16-byte aligned");
+  if (M <= 1) ldx = K, ldr = N;
+  if (N <= 1) ldw = K;
+  const int64_t m = M, n = N, k = K;
+  const Span rs = {"residual", range(residual, ((m - 1) * ldr + n) * oe)};
+  const Span os = {"out", range(out, m * n * oe)}, ps = {"pre", range(pre, m * n * oe)};
+  if ((st = check_overlap({os, ps}, {Span{"x", range(x, ((m - 1) * ldx + k) * e)},
+                                     Span{"w", range(w, ((n - 1) * ldw + k) * e)},
+                                     Span{"bias", range(bias, n * esize(bdtype))},
+                                     Span{"x_scale", range(x_scale, m * 4)},
+                                     Span{"w_scale", range(w_scale, n * 4)}})) != DELTA_OK)
+    return st;
+  if ((st = check_overlap({ps}, {rs})) != DELTA_OK) return st;
+  if (overlap(os.r, rs.r) && !(os.r.lo == rs.r.lo && ldr == n))
+    return fail(DELTA_ERR_INVALID, "out partly overlaps residual");
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  delta::LinearArgs a{};
+  a.x = x; a.w = w; a.bias = bias; a.residual = residual; a.x_scale = x_scale; a.w_scale = w_scale;
+  a.out = out; a.pre = pre; a.M = m; a.N = n; a.K = k; a.ldx = ldx; a.ldw = ldw; a.ldr = ldr;
+  a.act = (int)act; a.kind = kind; a.bias_bf16 = bdtype == DELTA_BF16;
+  const cudaError_t err = linear_forward(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "linear layer");
+}
+
+// Gradients of a float32 or bfloat16 layer.  dpre = dout act'(pre) is formed
+// once, in the operands' type: for bfloat16 that is a rounding of 2^-9 of each
+// term of dx and dw, the price of a tensor-core operand; dbias sums the
+// unrounded terms.
+cudaError_t linear_backward(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
+                            float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
+                            bool bf16, cudaStream_t s) {
+  const int64_t e = bf16 ? 2 : 4;
+  cudaError_t err = cudaSuccess;
+  if (M == 0 || N == 0) {  // empty sums
+    if (dw && N > 0) err = cudaMemsetAsync(dw, 0, (size_t)(N * K * e), s);
+    if (err == cudaSuccess && dbias && N > 0) err = cudaMemsetAsync(dbias, 0, (size_t)N * 4, s);
+    if (err == cudaSuccess && dx && M > 0) err = cudaMemsetAsync(dx, 0, (size_t)(M * K * e), s);
+    return err;
+  }
+  const bool form = (dx || dw) && (act != delta::kActNone || (bf16 && N % 8 != 0));
+  delta::DpreArgs d{};
+  d.dout = dout; d.pre = pre; d.dbias = dbias; d.M = M; d.N = N; d.act = act; d.bf16 = bf16;
+  d.ldp = form && bf16 ? up(N, 8) : N;
+  Operand ox = operand(x, M, K, ldx, (int)e), ow = operand(w, N, K, ldw, (int)e);
+  const bool packx = bf16 && dw && !ox.whole(), packw = bf16 && dx && !ow.whole();
+  Scratch scr(s);
+  if (form) scr.want(M * d.ldp * e), d.dpre = const_cast<void *>(dout);  // (a stand-in: aligned, set below)
+  const int64_t parts = dbias ? delta::dpre_parts(d) : 0;
+  if (dbias) scr.want(parts * N * 4);
+  if (packx) scr.want(ox.bytes());
+  if (packw) scr.want(ow.bytes());
+  if ((err = scr.take()) != cudaSuccess) return err;
+  d.dpre = form ? scr.cut(M * d.ldp * e) : nullptr;
+  if (dbias) d.partial = static_cast<float *>(scr.cut(parts * N * 4));
+  if (form || dbias) err = delta::launch_dpre(d, s);
+  if (err == cudaSuccess && packx) err = ox.pack(scr, s);
+  if (err == cudaSuccess && packw) err = ow.pack(scr, s);
+  const void *g = form ? d.dpre : dout;
+  delta::LinearArgs p{};
+  p.kind = bf16 ? delta::kLinBf16 : delta::kLinF32;
+  if (err == cudaSuccess && dx) {
+    p.out = dx; p.M = M; p.N = K;
+    err = bf16 ? delta::launch_gemm_tc({g, ow.p, d.ldp, ow.ld, N, false, true, p}, s)
+               : delta::launch_gemm_f32(p, static_cast<const float *>(g), d.ldp, 1, static_cast<const float *>(w), 1,
+                                        ldw, N, s);
+  }
+  if (err == cudaSuccess && dw) {
+    p.out = dw; p.M = N; p.N = K;
+    err = bf16 ? delta::launch_gemm_tc({g, ox.p, d.ldp, ox.ld, M, true, true, p}, s)
+               : delta::launch_gemm_f32(p, static_cast<const float *>(g), 1, d.ldp, static_cast<const float *>(x), 1,
+                                        ldx, M, s);
+  }
+  const cudaError_t ef = scr.release();
+  return err != cudaSuccess ? err : ef;
 }
 
 }  // namespace
@@ -288,6 +456,52 @@ int delta_add_rmsnorm_bwd(const void *dy, const void *sum, const void *weight, c
   const cudaError_t ef = scr ? cudaFreeAsync(scr, s) : cudaSuccess;
   if (err != cudaSuccess) return cuda_fail(err, "norm backward launch");
   return ef == cudaSuccess ? DELTA_OK : cuda_fail(ef, "scratch release");
+}
+
+int delta_linear_fwd(const void *x, const void *w, const void *bias, const void *residual, void *out, void *pre,
+                     int M, int N, int K, int64_t ldx, int64_t ldw, int64_t ldr, delta_act act,
+                     delta_dtype dtype, delta_dtype bdtype, struct CUstream_st *stream) {
+  const int st = check_dtype(dtype);
+  if (st != DELTA_OK) return st;
+  return run_linear(x, w, nullptr, nullptr, bias, residual, out, pre, M, N, K, ldx, ldw, ldr, act,
+                    dtype == DELTA_BF16 ? delta::kLinBf16 : delta::kLinF32, bdtype, stream);
+}
+
+int delta_linear_quant(const void *x, const float *x_scale, const void *w, const float *w_scale,
+                       const void *bias, const void *residual, void *out, int M, int N, int K, int64_t ldx,
+                       int64_t ldw, int64_t ldr, delta_act act, delta_dtype bdtype, struct CUstream_st *stream) {
+  return run_linear(x, w, x_scale, w_scale, bias, residual, out, nullptr, M, N, K, ldx, ldw, ldr, act,
+                    delta::kLinE4m3, bdtype, stream);
+}
+
+int delta_linear_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
+                     float *dbias, int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act,
+                     delta_dtype dtype, struct CUstream_st *stream) {
+  int st;
+  if ((st = check_dtype(dtype)) != DELTA_OK) return st;
+  if ((st = linear_sizes(M, N, K, ldx, ldw, N, act)) != DELTA_OK) return st;
+  if (!dx && !dw && !dbias) return DELTA_OK;
+  const int64_t e = esize(dtype), m = M, n = N, k = K;
+  if (M <= 1) ldx = K;
+  if (N <= 1) ldw = K;
+  if (!aligned16(dout) || !aligned16(pre) || !aligned16(dx) || !aligned16(dw) || !aligned16(dbias))
+    return fail(DELTA_ERR_ALIGN, "dout, pre and the gradients must be 16-byte aligned");
+  if (!aligned_to(x, e) || !aligned_to(w, e)) return fail(DELTA_ERR_ALIGN, "x and w must be aligned to their elements");
+  if (M > 0 && N > 0) {
+    if (!dout || (dw && !x) || (dx && !w)) return fail(DELTA_ERR_INVALID, "x, w and dout must be non-NULL");
+    if (act != DELTA_ACT_NONE && !pre) return fail(DELTA_ERR_INVALID, "an activation's gradient needs pre");
+  }
+  if ((st = check_overlap({Span{"dx", range(dx, m * k * e)}, Span{"dw", range(dw, n * k * e)},
+                           Span{"dbias", range(dbias, n * 4)}},
+                          {Span{"x", range(x, m > 0 ? ((m - 1) * ldx + k) * e : 0)},
+                           Span{"w", range(w, n > 0 ? ((n - 1) * ldw + k) * e : 0)},
+                           Span{"dout", range(dout, m * n * e)}, Span{"pre", range(pre, m * n * e)}})) != DELTA_OK)
+    return st;
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  const cudaError_t err = linear_backward(x, w, dout, act == DELTA_ACT_NONE ? nullptr : pre, dx, dw, dbias, m, n, k,
+                                          ldx, ldw, (int)act, dtype == DELTA_BF16,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "linear layer's gradients");
 }
 
 }  // extern "C"

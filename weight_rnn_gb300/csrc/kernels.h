@@ -169,4 +169,54 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s);
 int64_t norm_bwd_ctas(const NormBwdArgs &a);
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t s);
 
+// The linear layer (linear.cu, linear_tc.cu): out = act(x w^T + bias) +
+// residual, x [M][K], w [N][K], out and pre [M][N] contiguous.  kind: the type
+// of x and w; out, pre and residual are float32 for float32 operands, else
+// bfloat16.  e4m3 operands come with a scale per row of x and of w.
+enum LinearKind { kLinF32, kLinBf16, kLinE4m3 };
+constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
+struct LinearArgs {
+  const void *x, *w, *bias, *residual;  // bias, residual: nullptr for none
+  const float *x_scale, *w_scale;
+  void *out, *pre;                      // pre: nullptr if not wanted
+  int64_t M, N, K, ldx, ldw, ldr;
+  int act;
+  LinearKind kind;
+  bool bias_bf16;
+};
+// A matrix product of two operands for the tensor-core kernel, D[M][N] = sum_k
+// A(m, k) B(n, k).  *_mn: the operand lies with m (or n) contiguous and k as
+// the row (ld apart), else with k contiguous.  Base addresses and ld in bytes
+// are multiples of 16.
+struct GemmArgs {
+  const void *a, *b;
+  int64_t lda, ldb, K;
+  bool a_mn, b_mn;
+  LinearArgs epi;  // M, N, out and the epilogue
+};
+cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s);
+cudaError_t read_and_clear_linear_error(unsigned int *word);
+// few rows of x: the weight is streamed once (M <= kLinSmallM)
+constexpr int kLinSmallM = 32;
+cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s);
+// float32 on the CUDA cores, operands with any strides (elements)
+cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, int64_t ak, const float *b,
+                            int64_t bn, int64_t bk, int64_t K, cudaStream_t s);
+// rows x cols elements of `size` bytes into rows of ldp elements
+cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, int64_t ldp,
+                        int size, cudaStream_t s);
+// dpre = dout * act'(pre) in rows of ldp elements where dpre is set, and dbias = its column sums in float32 where dbias is set
+struct DpreArgs {
+  const void *dout, *pre;
+  void *dpre;
+  float *dbias, *partial;  // partial [dpre_parts()][N]
+  int64_t M, N, ldp;
+  int act;
+  bool bf16;
+};
+int64_t dpre_parts(const DpreArgs &a);
+cudaError_t launch_dpre(const DpreArgs &a, cudaStream_t s);
+// out[c] = sum over n partial rows (norm.cu)
+cudaError_t launch_column_sum(const float *partial, float *out, int64_t n, int64_t D, cudaStream_t s);
+
 }  // namespace delta

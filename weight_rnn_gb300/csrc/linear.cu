@@ -1,0 +1,313 @@
+// linear.cu -- the linear layer outside the large tensor-core products: the
+// form for few rows of x (decoding), float32 on the CUDA cores, and the
+// elementwise part of the gradients.
+#include <cooperative_groups.h>
+
+#include "linear.cuh"
+
+namespace delta {
+namespace {
+
+namespace cg = cooperative_groups;
+using namespace linear;
+
+int sm_count() {
+  int dev = 0, n = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+bool aligned_to(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)n == 0; }
+
+// ------------------------------------------------------------ few rows of x
+// Bound by reading w once.  A CTA has 16 rows of w, its warps (and the CTAs of
+// a cluster, where N alone does not fill the GPU) deal out k in blocks of
+// kBlocks 64-byte pieces per row.  The products run on warp-level matrix
+// instructions with w as the 16-row operand and up to 8 NT rows of x as the
+// other: at M <= 32 the 5th-generation units would wait for the same bytes,
+// and here a piece goes from memory to the operand's registers with nothing
+// between.  The instruction's order of k within a block is free as long as
+// both operands share it, so a lane takes 16 neighbouring bytes of its rows.
+// Partial sums meet in shared memory and in rank 0 in a fixed order.
+constexpr int kSmallWarps = 8;
+constexpr int kBlocks = 4;
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes of a row from byte k on; zeros past the row's `bytes`.  kVec: rows
+// are whole 16-byte pieces, else single elements of `size` bytes.
+template <bool kVec, int kSize, bool kStream>
+__device__ __forceinline__ uint4 piece(const uint8_t *row, int64_t k, int64_t bytes) {
+  if constexpr (kVec) {
+    if (k >= bytes) return make_uint4(0, 0, 0, 0);
+    const uint4 *p = reinterpret_cast<const uint4 *>(row + k);
+    return kStream ? __ldcs(p) : *p;
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16 / kSize; ++i)
+      if (k + i * kSize < bytes) {
+        const uint32_t v = kSize == 2 ? *reinterpret_cast<const uint16_t *>(row + k + 2 * i) : row[k + i];
+        w[i * kSize / 4] |= v << (8 * (i * kSize % 4));
+      }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <bool kF8, int NT, bool kVec>
+__global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, int cs) {
+  constexpr int kSize = kF8 ? 1 : 2, kTok = 8 * NT;
+  __shared__ float part[kSmallWarps][16][kTok + 1];
+  __shared__ float ranks[kMaxCluster][16 * kTok];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
+  const int64_t n0 = (int64_t)(blockIdx.x / cs) * 16;
+  if (cs > 1) cg::this_cluster().barrier_arrive();
+  const int64_t bytes = a.K * kSize;
+  // rows past the end repeat the last one; their results are not stored
+  const uint8_t *w0 = static_cast<const uint8_t *>(a.w) + (n0 + g < a.N ? n0 + g : a.N - 1) * a.ldw * kSize;
+  const uint8_t *w1 = static_cast<const uint8_t *>(a.w) + (n0 + g + 8 < a.N ? n0 + g + 8 : a.N - 1) * a.ldw * kSize;
+  const uint8_t *x[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    x[i] = static_cast<const uint8_t *>(a.x) + (8 * i + g < a.M ? 8 * i + g : a.M - 1) * a.ldx * kSize;
+  float c[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+
+  constexpr int64_t kSpan = kBlocks * 64;  // bytes of a row per turn
+  for (int64_t k0 = (rank * kSmallWarps + warp) * kSpan; k0 < bytes; k0 += kSpan * kSmallWarps * cs) {
+    uint4 u0[kBlocks], u1[kBlocks];
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) {
+      u0[j] = piece<kVec, kSize, true>(w0, k0 + j * 64 + t * 16, bytes);
+      u1[j] = piece<kVec, kSize, true>(w1, k0 + j * 64 + t * 16, bytes);
+    }
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint4 v = piece<kVec, kSize, false>(x[i], k0 + j * 64 + t * 16, bytes);
+        if constexpr (kF8) {
+          mma_e4m3(c[i], u0[j].x, u1[j].x, u0[j].y, u1[j].y, v.x, v.y);
+          mma_e4m3(c[i], u0[j].z, u1[j].z, u0[j].w, u1[j].w, v.z, v.w);
+        } else {
+          mma_bf16(c[i], u0[j].x, u1[j].x, u0[j].y, u1[j].y, v.x, v.y);
+          mma_bf16(c[i], u0[j].z, u1[j].z, u0[j].w, u1[j].w, v.z, v.w);
+        }
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    part[warp][g][8 * i + 2 * t] = c[i][0];
+    part[warp][g][8 * i + 2 * t + 1] = c[i][1];
+    part[warp][g + 8][8 * i + 2 * t] = c[i][2];
+    part[warp][g + 8][8 * i + 2 * t + 1] = c[i][3];
+  }
+  __syncthreads();
+  if (cs > 1) cg::this_cluster().barrier_wait();  // every CTA of the cluster has begun
+  for (int i = threadIdx.x; i < 16 * kTok; i += kSmallWarps * 32) {
+    const int r = i & 15, tok = i >> 4;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSmallWarps; ++w) s += part[w][r][tok];
+    if (cs > 1)
+      cg::this_cluster().map_shared_rank(&ranks[rank][0], 0)[i] = s;
+    else if (tok < a.M && n0 + r < a.N)
+      finish<__nv_bfloat16>(a, tok, n0 + r, s);
+  }
+  if (cs > 1) {
+    cg::this_cluster().sync();
+    if (rank == 0)
+      for (int i = threadIdx.x; i < 16 * kTok; i += kSmallWarps * 32) {
+        const int r = i & 15, tok = i >> 4;
+        float s = 0.f;
+        for (int q = 0; q < cs; ++q) s += ranks[q][i];
+        if (tok < a.M && n0 + r < a.N) finish<__nv_bfloat16>(a, tok, n0 + r, s);
+      }
+  }
+}
+
+template <bool kF8, int NT>
+cudaError_t run_small(const LinearArgs &a, cudaStream_t s) {
+  const int64_t size = kF8 ? 1 : 2, e = 16 / size;
+  const bool vec = a.K % e == 0 && a.ldx % e == 0 && a.ldw % e == 0 && aligned_to(a.x, 16) && aligned_to(a.w, 16);
+  // CTAs along k until every SM has two, as far as k has a turn for each warp
+  const int64_t groups = (a.N + 15) / 16, turns = (a.K * size + kBlocks * 64 - 1) / (kBlocks * 64);
+  int cs = 1;
+  while (cs < kMaxCluster && groups * cs < 2 * sm_count() && turns > (int64_t)kSmallWarps * cs) cs *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * cs));
+  cfg.blockDim = dim3(kSmallWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
+  return vec ? cudaLaunchKernelEx(&cfg, small_kernel<kF8, NT, true>, a, cs)
+             : cudaLaunchKernelEx(&cfg, small_kernel<kF8, NT, false>, a, cs);
+}
+
+// ------------------------------------------------------ float32, CUDA cores
+// A correctness path: 64 x 64 tiles, 4 x 4 elements a thread, operands with
+// any strides.
+__global__ void __launch_bounds__(256) gemm_f32_kernel(LinearArgs e, const float *a, int64_t am, int64_t ak,
+                                                       const float *b, int64_t bn, int64_t bk, int64_t K) {
+  __shared__ float sa[16][65], sb[16][65];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t nt = (e.N + 63) / 64, m0 = (int64_t)blockIdx.x / nt * 64, n0 = (int64_t)blockIdx.x % nt * 64;
+  float c[4][4] = {};
+  for (int64_t k0 = 0; k0 < K; k0 += 16) {
+    for (int i = threadIdx.x; i < 1024; i += 256) {
+      // neighbouring threads along the contiguous axis of each operand
+      const int ka = ak == 1 ? i & 15 : i >> 6, ma = ak == 1 ? i >> 4 : i & 63;
+      const int kb = bk == 1 ? i & 15 : i >> 6, nb = bk == 1 ? i >> 4 : i & 63;
+      sa[ka][ma] = m0 + ma < e.M && k0 + ka < K ? a[(m0 + ma) * am + (k0 + ka) * ak] : 0.f;
+      sb[kb][nb] = n0 + nb < e.N && k0 + kb < K ? b[(n0 + nb) * bn + (k0 + kb) * bk] : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], c[i][j]);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
+      if (m < e.M && n < e.N) finish<float>(e, m, n, c[i][j]);
+    }
+}
+
+// ----------------------------------------------------------------- gradients
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(const T *src, T *dst, int64_t rows, int64_t cols, int64_t ld,
+                                                   int64_t ldp) {
+  const int64_t n = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cols, c = i - r * cols;
+    dst[r * ldp + c] = src[r * ld + c];
+  }
+}
+
+// dpre = dout act'(pre) and its column sums: a CTA has 32 V columns and every
+// parts-th group of 8 rows; one element (V = 1) or 16 bytes a lane.  The sums
+// take the unrounded products; part sums meet in launch_column_sum.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
+  struct __align__(sizeof(T) * V) Vec { T v[V]; };
+  __shared__ float sum[8][32 * V];
+  const int64_t c = ((int64_t)blockIdx.x * 32 + threadIdx.x) * V;
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = 0.f;
+  if (c < p.N)
+    for (int64_t m = (int64_t)blockIdx.y * 8 + threadIdx.y; m < p.M; m += (int64_t)gridDim.y * 8) {
+      const Vec d = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.dout) + m * p.N + c);
+      Vec q = d, o;
+      if (p.act != kActNone) q = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.pre) + m * p.N + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float v = to_f(d.v[i]);
+        if (p.act != kActNone) v *= slope(p.act, to_f(q.v[i]));
+        s[i] += v;
+        from_f(v, o.v[i]);
+      }
+      if (p.dpre) *reinterpret_cast<Vec *>(static_cast<T *>(p.dpre) + m * p.ldp + c) = o;
+    }
+  if (!p.dbias) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum[threadIdx.y][threadIdx.x * V + i] = s[i];
+  __syncthreads();
+  for (int i = threadIdx.y * 32 + threadIdx.x; i < 32 * V; i += 256) {
+    const int64_t n = (int64_t)blockIdx.x * 32 * V + i;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += sum[w][i];
+    if (n < p.N) p.partial[(int64_t)blockIdx.y * p.N + n] = v;
+  }
+}
+
+int dpre_vec(const DpreArgs &p) {
+  const int v = p.bf16 ? 8 : 4;
+  return p.N % v == 0 && (!p.dpre || p.ldp % v == 0) && aligned_to(p.dout, 16) && aligned_to(p.pre, 16) &&
+                 aligned_to(p.dpre, 16)
+             ? v
+             : 1;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s) {
+  if (a.kind == kLinE4m3)
+    return a.M <= 8 ? run_small<true, 1>(a, s) : a.M <= 16 ? run_small<true, 2>(a, s) : run_small<true, 4>(a, s);
+  return a.M <= 8 ? run_small<false, 1>(a, s) : a.M <= 16 ? run_small<false, 2>(a, s) : run_small<false, 4>(a, s);
+}
+
+cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, int64_t ak, const float *b,
+                            int64_t bn, int64_t bk, int64_t K, cudaStream_t s) {
+  const int64_t grid = ((epi.M + 63) / 64) * ((epi.N + 63) / 64);
+  if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  gemm_f32_kernel<<<(unsigned)grid, 256, 0, s>>>(epi, a, am, ak, b, bn, bk, K);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, int64_t ldp, int size,
+                        cudaStream_t s) {
+  const int64_t want = (rows * cols + 255) / 256, cap = (int64_t)sm_count() * 16;
+  const unsigned grid = (unsigned)(want < cap ? want : cap);
+  if (size == 2)
+    pack_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), rows, cols, ld, ldp);
+  else
+    pack_kernel<<<grid, 256, 0, s>>>(static_cast<const uint8_t *>(src), static_cast<uint8_t *>(dst), rows, cols, ld, ldp);
+  return cudaGetLastError();
+}
+
+int64_t dpre_parts(const DpreArgs &p) {
+  // CTAs for every SM several times over, but no fewer than 8 rows a thread
+  const int64_t across = (p.N + 32 * dpre_vec(p) - 1) / (32 * dpre_vec(p));
+  int64_t parts = (8 * (int64_t)sm_count() + across - 1) / across;
+  const int64_t most = (p.M + 63) / 64;
+  if (parts > most) parts = most;
+  return parts < 1 ? 1 : parts > 65535 ? 65535 : parts;
+}
+
+cudaError_t launch_dpre(const DpreArgs &p, cudaStream_t s) {
+  const int v = dpre_vec(p);
+  const int64_t parts = dpre_parts(p);
+  const dim3 grid((unsigned)((p.N + 32 * v - 1) / (32 * v)), (unsigned)parts), block(32, 8);
+  if (p.bf16) {
+    if (v == 1)
+      dpre_kernel<__nv_bfloat16, 1><<<grid, block, 0, s>>>(p);
+    else
+      dpre_kernel<__nv_bfloat16, 8><<<grid, block, 0, s>>>(p);
+  } else {
+    if (v == 1)
+      dpre_kernel<float, 1><<<grid, block, 0, s>>>(p);
+    else
+      dpre_kernel<float, 4><<<grid, block, 0, s>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.dbias) return e;
+  return launch_column_sum(p.partial, p.dbias, parts, p.N, s);
+}
+
+}  // namespace delta

@@ -1,0 +1,315 @@
+// linear_tc.cu -- the linear layer's matrix products on the 5th-generation
+// tensor cores, D[M][N] = sum_k A(m, k) B(n, k), with the epilogue of
+// linear.cuh.  The forward takes x and w with k contiguous; the gradients take
+// them as they lie, with k as the row (w for dx, both operands for dw), which
+// the shared-memory descriptors express as MN-major operands, so nothing is
+// transposed in memory.
+//
+// One persistent CTA per SM, six warps:
+//   warp 0: TMA producer, a ring of kStages stages of 128 bytes of k;
+//   warp 1: allocates TMEM and issues the products (one thread), 128 x BN per
+//           tile into one of two TMEM accumulators;
+//   warps 2-5: epilogue, one TMEM lane quarter (32 rows) each, while the next
+//           tile's products run into the other accumulator.
+// Tiles are dealt out in bands of kBand tile rows, so that the CTAs at work at
+// a time share operand rows in L2.  Every mbarrier wait is bounded: a timeout
+// sets a device error word and the kernel winds down.
+#include "linear.cuh"
+#include "sm100.cuh"
+#include "tma_host.h"
+
+namespace delta {
+namespace {
+
+using namespace sm100;
+
+__device__ unsigned int g_linear_error = 0;
+
+constexpr int kBM = 128;
+constexpr int kThreads = 192;
+constexpr int kBand = 16;
+constexpr int kRowBytes = 128;  // of k in a stage: 64 bfloat16 or 128 e4m3
+
+__host__ __device__ constexpr int stage_bytes(int BN) { return (kBM + BN) * kRowBytes; }
+__host__ __device__ constexpr int stages(int BN) { return BN == 256 ? 4 : BN == 128 ? 6 : 8; }
+__host__ __device__ constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN); }
+
+struct Shared {
+  uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+  volatile int dead;
+};
+
+__device__ __noinline__ bool wait_slow(Shared *sh, uint64_t *bar, uint32_t parity, int role) {
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 63 && sh->dead) return false;
+  }
+  sh->dead = 1;
+  atomicCAS(&g_linear_error, 0u, (unsigned)(1 + role));
+  return false;
+}
+__device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity, int role) {
+  return mbar_try_wait(bar, parity) || wait_slow(sh, bar, parity, role);
+}
+
+struct Tiles {
+  int64_t m_tiles, n_tiles, total;
+  int kblocks;
+};
+__device__ __forceinline__ void tile_at(const Tiles &t, int64_t i, int64_t &m, int64_t &n) {
+  const int64_t band = i / (kBand * t.n_tiles), first = band * kBand;
+  const int64_t high = t.m_tiles - first < kBand ? t.m_tiles - first : kBand;
+  const int64_t r = i - band * kBand * t.n_tiles;
+  m = first + r % high;
+  n = r / high;
+}
+
+// 32 columns of one row: scales, bias, activation, residual, stores.  `fast`:
+// all 32 columns are there and every row is 16-byte aligned.
+__device__ __forceinline__ void store_row(const LinearArgs &e, int64_t m, int64_t n0, uint32_t (&r)[32], bool fast) {
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + m * e.N + n0;
+  if (!fast) {
+    // (unrolled, so that r stays in registers)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n0 + i < e.N) linear::finish<__nv_bfloat16>(e, m, n0 + i, __uint_as_float(r[i]));
+    return;
+  }
+  const float sx = e.x_scale ? e.x_scale[m] : 1.f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * g + i]);
+    if (e.x_scale) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= sx * e.w_scale[n0 + 8 * g + i];
+    }
+    if (e.bias) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += linear::bias_at(e, n0 + 8 * g + i);
+    }
+    if (e.pre) {
+      uint4 p = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.pre) + m * e.N + n0 + 8 * g) = p;
+    }
+    if (e.act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = linear::activate(e.act, v[i]);
+    }
+    if (e.residual) {
+      const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.residual) + m * e.ldr + n0 + 8 * g);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += __uint_as_float(w[i] << 16);
+        v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+    *reinterpret_cast<uint4 *>(out + 8 * g) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+}
+
+template <int BN, bool kAMn, bool kBMn, bool kF8>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, Tiles tiles,
+                LinearArgs epi, bool aligned) {
+  constexpr int kStages = stages(BN), kStage = stage_bytes(BN);
+  constexpr int kElems = kF8 ? 128 : 64;                 // of k in a stage
+  constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;  // TMEM columns: two accumulators
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
+  // swizzle atoms are 1024-byte aligned
+  unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], 4);
+    mbar_init(&sh.drain, 1);
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&ma);
+      tma_prefetch_desc(&mb);
+      int slot = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+        int64_t tm, tn;
+        tile_at(tiles, i, tm, tn);
+        const int m0 = (int)(tm * kBM), n0 = (int)(tn * BN);
+        for (int kb = 0; kb < tiles.kblocks; ++kb) {
+          if (!(ok = wait(&sh, &sh.empty[slot], phase ^ 1, 0))) break;
+          unsigned char *st = base + slot * kStage;
+          mbar_arrive_expect_tx(&sh.full[slot], kStage);
+          if constexpr (kAMn) {
+            for (int j = 0; j < kBM / 64; ++j) tma_load_2d(st + j * 8192, &ma, &sh.full[slot], m0 + 64 * j, kb * 64);
+          } else {
+            tma_load_2d(st, &ma, &sh.full[slot], kb * kElems, m0);
+          }
+          if constexpr (kBMn) {
+            for (int j = 0; j < BN / 64; ++j)
+              tma_load_2d(st + kBM * kRowBytes + j * 8192, &mb, &sh.full[slot], n0 + 64 * j, kb * 64);
+          } else {
+            tma_load_2d(st + kBM * kRowBytes, &mb, &sh.full[slot], kb * kElems, n0);
+          }
+          ++issued;
+          if (++slot == kStages) slot = 0, phase ^= 1;
+        }
+      }
+      if (!ok) {  // winding down: this warp's own copies land first
+        for (int64_t i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
+          for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.full[i % kStages], (i / kStages) & 1); ++j) {
+          }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t id = kF8 ? idesc_e4m3(kBM, BN) : idesc_bf16(kBM, BN, kAMn, kBMn);
+      int slot = 0, acc = 0;
+      uint32_t phase = 0, accphase = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+        if (!(ok = wait(&sh, &sh.tempty[acc], accphase ^ 1, 1))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (int kb = 0; kb < tiles.kblocks; ++kb) {
+          if (!(ok = wait(&sh, &sh.full[slot], phase, 1))) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(base + slot * kStage);
+          // k-contiguous operands: a step of 16 (32) elements is 32 bytes of
+          // the 128-byte row; MN-major ones: 16 rows of 128 bytes
+          const uint64_t da = kAMn ? sdesc_sw128(st, 8192, 1024) : sdesc_sw128(st, 0, 1024);
+          const uint64_t db = kBMn ? sdesc_sw128(st + kBM * kRowBytes, 8192, 1024)
+                                   : sdesc_sw128(st + kBM * kRowBytes, 0, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t xa = da + (uint64_t)(k * (kAMn ? 2048 : 32) >> 4);
+            const uint64_t xb = db + (uint64_t)(k * (kBMn ? 2048 : 32) >> 4);
+            if constexpr (kF8)
+              mma_ss_f8(d, xa, xb, id, kb > 0 || k > 0);
+            else
+              mma_ss(d, xa, xb, id, kb > 0 || k > 0);
+          }
+          mma_commit(&sh.empty[slot]);
+          if (++slot == kStages) slot = 0, phase ^= 1;
+        }
+        if (!ok) break;
+        mma_commit(&sh.tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) accphase ^= 1;
+      }
+      if (!ok) {  // products in flight end before TMEM is given back
+        mma_commit(&sh.drain);
+        for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.drain, 0); ++j) {
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    int acc = 0;
+    uint32_t accphase = 0;
+    for (int64_t i = blockIdx.x; i < tiles.total; i += gridDim.x) {
+      if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
+      tc_fence_after();
+      int64_t tm, tn;
+      tile_at(tiles, i, tm, tn);
+      const int64_t m = tm * kBM + quarter * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        const int64_t n0 = tn * BN + c;
+        if (n0 >= epi.N) break;
+        uint32_t r[32];
+        tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + c), r);
+        tmem_wait_ld_regs(r);
+        if (m < epi.M) store_row(epi, m, n0, r, aligned && n0 + 32 <= epi.N);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.tempty[acc]);
+      acc ^= 1;
+      if (acc == 0) accphase ^= 1;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kCols);
+}
+
+int sm_count() {
+  int dev = 0, n = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+template <int BN, bool kAMn, bool kBMn, bool kF8>
+cudaError_t run(const GemmArgs &g, cudaStream_t s) {
+  const int size = kF8 ? 1 : 2;
+  const LinearArgs &e = g.epi;
+  CUtensorMap ma, mb;
+  cudaError_t err;
+  err = kAMn ? make_map_2d_sw128(&ma, g.a, (uint64_t)e.M, (uint64_t)g.K, (uint64_t)g.lda, size, 64)
+             : make_map_2d_sw128(&ma, g.a, (uint64_t)g.K, (uint64_t)e.M, (uint64_t)g.lda, size, kBM);
+  if (err != cudaSuccess) return err;
+  err = kBMn ? make_map_2d_sw128(&mb, g.b, (uint64_t)e.N, (uint64_t)g.K, (uint64_t)g.ldb, size, 64)
+             : make_map_2d_sw128(&mb, g.b, (uint64_t)g.K, (uint64_t)e.N, (uint64_t)g.ldb, size, BN);
+  if (err != cudaSuccess) return err;
+  Tiles t;
+  t.m_tiles = (e.M + kBM - 1) / kBM;
+  t.n_tiles = (e.N + BN - 1) / BN;
+  t.total = t.m_tiles * t.n_tiles;
+  const int elems = kF8 ? 128 : 64;
+  t.kblocks = (int)((g.K + elems - 1) / elems);
+  const auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const bool aligned = e.N % 8 == 0 && ok(e.out) && ok(e.pre) && ok(e.residual) && (!e.residual || e.ldr % 8 == 0);
+  auto kern = gemm_kernel<BN, kAMn, kBMn, kF8>;
+  if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN))) != cudaSuccess)
+    return err;
+  const int64_t sms = sm_count(), grid = t.total < sms ? t.total : sms;
+  kern<<<(unsigned)grid, kThreads, smem_bytes(BN), s>>>(ma, mb, t, e, aligned);
+  return cudaGetLastError();
+}
+
+template <bool kAMn, bool kBMn, bool kF8>
+cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
+  // the widest tile that still gives every SM one; below that, narrower tiles
+  // spread the work over more SMs
+  const int64_t m = (g.epi.M + kBM - 1) / kBM, sms = sm_count();
+  const auto tiles = [&](int bn) { return m * ((g.epi.N + bn - 1) / bn); };
+  if (tiles(256) >= sms) return run<256, kAMn, kBMn, kF8>(g, s);
+  if (tiles(128) >= sms) return run<128, kAMn, kBMn, kF8>(g, s);
+  return run<64, kAMn, kBMn, kF8>(g, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s) {
+  if (g.epi.kind == kLinE4m3) return g.a_mn || g.b_mn ? cudaErrorNotSupported : pick<false, false, true>(g, s);
+  if (!g.a_mn) return g.b_mn ? pick<false, true, false>(g, s) : pick<false, false, false>(g, s);
+  return g.b_mn ? pick<true, true, false>(g, s) : cudaErrorNotSupported;
+}
+
+cudaError_t read_and_clear_linear_error(unsigned int *word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_linear_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_linear_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace delta

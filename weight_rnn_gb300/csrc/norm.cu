@@ -316,9 +316,9 @@ __global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) 
     }
 }
 
-// dweight[d] = sum of n partial rows, 32 columns a CTA, in row order per
-// thread row and then over the 32 thread rows
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, float *dw, int64_t n, int64_t D) {
+// dw[d] = sum of n partial rows, 32 columns a CTA, in row order per thread row
+// and then over the 32 thread rows
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, float *dw, int64_t n, int64_t D) {
   __shared__ float s[32][33];
   const int64_t d = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
@@ -431,11 +431,15 @@ cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
   const Plan q = bwd_plan<In>(a);
   cudaError_t e = q.grid > 0 ? dispatch<In, BwdOne>(q, a, q, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  norm_dw_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 32), 0, s>>>(a.partial, a.dweight, q.grid * q.rpc, a.D);
-  return cudaGetLastError();
+  return launch_column_sum(a.partial, a.dweight, q.grid * q.rpc, a.D, s);
 }
 
 }  // namespace
+
+cudaError_t launch_column_sum(const float *partial, float *out, int64_t n, int64_t D, cudaStream_t s) {
+  column_sum_kernel<<<(unsigned)((D + 31) / 32), dim3(32, 32), 0, s>>>(partial, out, n, D);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
   return a.bf16 ? fwd_all<__nv_bfloat16>(a, s) : fwd_all<float>(a, s);

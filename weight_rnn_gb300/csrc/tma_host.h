@@ -61,4 +61,22 @@ inline cudaError_t make_map_3d_bf16_sw128(CUtensorMap *map, const void *base, ui
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A matrix of `rows` rows of `inner` elements (1 or 2 bytes each), `ld` elements
+// apart, tiled with a box of 128 bytes x box_rows and the 128-byte swizzle.
+// base and ld * size must be multiples of 16 bytes; outside reads as zero.
+inline cudaError_t make_map_2d_sw128(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
+                                     uint64_t ld, int size, uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {inner, rows};
+  const cuuint64_t strides[1] = {ld * (uint64_t)size};
+  const cuuint32_t box[2] = {128u / (uint32_t)size, box_rows};
+  const cuuint32_t estride[2] = {1, 1};
+  CUresult r = enc(map, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                   const_cast<void *>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace delta
