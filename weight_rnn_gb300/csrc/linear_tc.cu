@@ -28,11 +28,14 @@ __device__ unsigned int g_linear_error = 0;
 constexpr int kBM = 128;
 constexpr int kThreads = 192;
 constexpr int kBand = 16;
+constexpr int kPitch = 36;      // floats a row of an epilogue warp's stage
 constexpr int kRowBytes = 128;  // of k in a stage: 64 bfloat16 or 128 e4m3
 
 __host__ __device__ constexpr int stage_bytes(int BN) { return (kBM + BN) * kRowBytes; }
 __host__ __device__ constexpr int stages(int BN) { return BN == 256 ? 4 : BN == 128 ? 6 : 8; }
-__host__ __device__ constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN); }
+__host__ __device__ constexpr int smem_bytes(int BN) {
+  return 1024 + stages(BN) * stage_bytes(BN) + 4 * 32 * kPitch * 4;  // ring, and the epilogue warps' stages
+}
 
 struct Shared {
   uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
@@ -65,50 +68,81 @@ __device__ __forceinline__ void tile_at(const Tiles &t, int64_t i, int64_t &m, i
   n = r / high;
 }
 
-// 32 columns of one row: scales, bias, activation, residual, stores.  `fast`:
-// all 32 columns are there and every row is 16-byte aligned.
-__device__ __forceinline__ void store_row(const LinearArgs &e, int64_t m, int64_t n0, uint32_t (&r)[32], bool fast) {
-  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + m * e.N + n0;
-  if (!fast) {
-    // (unrolled, so that r stays in registers)
+// The epilogue of a warp's 32 rows, 32 columns at a time.  TMEM gives a lane
+// one row; a turn through shared memory gives it 8 neighbouring columns of
+// every eighth row instead, so that every global access is a whole 64-byte
+// piece of a row, the bias and the column scales stay in registers over the
+// rows, and the residual can be asked for a chunk ahead.  The pitch of 36
+// floats keeps both sides free of bank conflicts.
+
+struct Ahead {  // what a chunk needs from global memory
+  uint4 res[4];
+  float bias[8], scale[8];
+};
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void widen8(const uint4 &q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (n0 + i < e.N) linear::finish<__nv_bfloat16>(e, m, n0 + i, __uint_as_float(r[i]));
-    return;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  const float sx = e.x_scale ? e.x_scale[m] : 1.f;
+}
+__device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+// lane's columns start at n, its rows at m, 8 apart
+__device__ __forceinline__ void fetch_ahead(const LinearArgs &e, int64_t m, int64_t n, Ahead &h) {
+  if (n >= e.N) return;
+  if (e.residual) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
+    for (int i = 0; i < 4; ++i)
+      if (m + 8 * i < e.M)
+        h.res[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.residual) + (m + 8 * i) * e.ldr + n);
+  }
+  if (e.bias) {
+    if (e.bias_bf16)
+      widen8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.bias) + n), h.bias);
+    else
+      load8(static_cast<const float *>(e.bias) + n, h.bias);
+  }
+  if (e.x_scale) load8(e.w_scale + n, h.scale);
+}
+
+__device__ __forceinline__ void finish_chunk(const LinearArgs &e, const float *stage, int lane, int64_t m, int64_t n,
+                                             const float (&sx)[4], const Ahead &h) {
+  if (n >= e.N) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = m + 8 * i;
+    if (row >= e.M) break;
     float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * g + i]);
+    load8(stage + (lane / 4 + 8 * i) * kPitch + (lane % 4) * 8, v);
     if (e.x_scale) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= sx * e.w_scale[n0 + 8 * g + i];
+      for (int j = 0; j < 8; ++j) v[j] *= sx[i] * h.scale[j];
     }
     if (e.bias) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += linear::bias_at(e, n0 + 8 * g + i);
+      for (int j = 0; j < 8; ++j) v[j] += h.bias[j];
     }
-    if (e.pre) {
-      uint4 p = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.pre) + m * e.N + n0 + 8 * g) = p;
-    }
+    if (e.pre) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.pre) + row * e.N + n) = narrow8(v);
     if (e.act != kActNone) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = linear::activate(e.act, v[i]);
+      for (int j = 0; j < 8; ++j) v[j] = linear::activate(e.act, v[j]);
     }
     if (e.residual) {
-      const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.residual) + m * e.ldr + n0 + 8 * g);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      float q[8];
+      widen8(h.res[i], q);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] += __uint_as_float(w[i] << 16);
-        v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
-      }
+      for (int j = 0; j < 8; ++j) v[j] += q[j];
     }
-    *reinterpret_cast<uint4 *>(out + 8 * g) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.out) + row * e.N + n) = narrow8(v);
   }
 }
 
@@ -221,22 +255,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    float *stage = reinterpret_cast<float *>(base + kStages * kStage) + quarter * 32 * kPitch;
     int acc = 0;
     uint32_t accphase = 0;
     for (int64_t i = blockIdx.x; i < tiles.total; i += gridDim.x) {
-      if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
-      tc_fence_after();
       int64_t tm, tn;
       tile_at(tiles, i, tm, tn);
-      const int64_t m = tm * kBM + quarter * 32 + lane;
+      const int64_t m0 = tm * kBM + quarter * 32, m = m0 + lane / 4, n0 = tn * BN;
+      float sx[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sx[k] = epi.x_scale && m + 8 * k < epi.M ? epi.x_scale[m + 8 * k] : 1.f;
+      Ahead next, now;
+      if (aligned) fetch_ahead(epi, m, n0 + (lane % 4) * 8, next);
+      uint32_t r[32];
+      if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
+      tc_fence_after();
+      const int chunks = (int)(epi.N - n0 < BN ? (epi.N - n0 + 31) / 32 : BN / 32);
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        const int64_t n0 = tn * BN + c;
-        if (n0 >= epi.N) break;
-        uint32_t r[32];
-        tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + c), r);
+      for (int c = 0; c < chunks; ++c) {
+        tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + c * 32), r);
+        now = next;
+        if (aligned && c + 1 < chunks) fetch_ahead(epi, m, n0 + (c + 1) * 32 + (lane % 4) * 8, next);
         tmem_wait_ld_regs(r);
-        if (m < epi.M) store_row(epi, m, n0, r, aligned && n0 + 32 <= epi.N);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4 *>(stage + lane * kPitch + 4 * k) =
+              make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        __syncwarp();
+        if (aligned) {
+          finish_chunk(epi, stage, lane, m, n0 + c * 32 + (lane % 4) * 8, sx, now);
+        } else if (n0 + c * 32 + lane < epi.N) {
+          for (int k = 0; k < 32 && m0 + k < epi.M; ++k)
+            linear::finish<__nv_bfloat16>(epi, m0 + k, n0 + c * 32 + lane, stage[k * kPitch + lane]);
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -277,7 +329,8 @@ cudaError_t run(const GemmArgs &g, cudaStream_t s) {
   const int elems = kF8 ? 128 : 64;
   t.kblocks = (int)((g.K + elems - 1) / elems);
   const auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  const bool aligned = e.N % 8 == 0 && ok(e.out) && ok(e.pre) && ok(e.residual) && (!e.residual || e.ldr % 8 == 0);
+  const bool aligned = e.N % 8 == 0 && ok(e.out) && ok(e.pre) && ok(e.residual) && (!e.residual || e.ldr % 8 == 0) &&
+                       ok(e.bias) && ok(e.w_scale);
   auto kern = gemm_kernel<BN, kAMn, kBMn, kF8>;
   if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN))) != cudaSuccess)
     return err;
