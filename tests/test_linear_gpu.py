@@ -90,7 +90,7 @@ def test_many_tiles_a_cta(shape):
     assert torch.equal(out, again)
 
 
-@pytest.mark.parametrize("shape", SHAPES + [(2500, 1300, 136)], ids=str)
+@pytest.mark.parametrize("shape", SHAPES + [(2500, 1300, 136), (2100, 2600, 264)], ids=str)
 def test_eight_bits(shape):
     M, N, K = shape
     x, w, b, res, _ = inputs(*shape, F32, sum(shape) + 7)

@@ -7,13 +7,18 @@
 //
 // One persistent CTA per SM, six warps:
 //   warp 0: TMA producer, a ring of kStages stages of 128 bytes of k;
-//   warp 1: allocates TMEM and issues the products (one thread), 128 x BN per
-//           tile into one of two TMEM accumulators;
+//   warp 1: allocates TMEM and issues the products (one thread) into one of
+//           two TMEM accumulators of 128 x BN;
 //   warps 2-5: epilogue, one TMEM lane quarter (32 rows) each, while the next
 //           tile's products run into the other accumulator.
-// Tiles are dealt out in bands of kBand tile rows, so that the CTAs at work at
-// a time share operand rows in L2.  Every mbarrier wait is bounded: a timeout
-// sets a device error word and the kernel winds down.
+// A large product takes CTAs in pairs (cta_group::2): a tile of 256 x 256 of
+// which each CTA loads 128 rows of either operand, 32 KB a stage.  One CTA
+// alone on 128 x 256 needs 48 KB for the same work, which at full rate is more
+// than L2 gives 152 SMs (1.32 PFLOP/s).  Smaller ones take 128 x 128 or
+// 128 x 64 tiles of one CTA.  Tiles are dealt out in bands of kBand tile rows,
+// so that the CTAs at work at a time share operand rows in L2.  Every mbarrier
+// wait is bounded: a timeout sets a device error word and the kernel winds
+// down.
 #include "linear.cuh"
 #include "sm100.cuh"
 #include "tma_host.h"
@@ -27,14 +32,17 @@ __device__ unsigned int g_linear_error = 0;
 
 constexpr int kBM = 128;
 constexpr int kThreads = 192;
-constexpr int kBand = 16;
+constexpr int kBand = 8;
 constexpr int kPitch = 36;      // floats a row of an epilogue warp's stage
 constexpr int kRowBytes = 128;  // of k in a stage: 64 bfloat16 or 128 e4m3
 
-__host__ __device__ constexpr int stage_bytes(int BN) { return (kBM + BN) * kRowBytes; }
-__host__ __device__ constexpr int stages(int BN) { return BN == 256 ? 4 : BN == 128 ? 6 : 8; }
-__host__ __device__ constexpr int smem_bytes(int BN) {
-  return 1024 + stages(BN) * stage_bytes(BN) + 4 * 32 * kPitch * 4;  // ring, and the epilogue warps' stages
+// BN: columns of a tile; a pair's CTA loads half of B's rows
+__host__ __device__ constexpr int b_rows(int BN, bool pair) { return pair ? BN / 2 : BN; }
+__host__ __device__ constexpr int stage_bytes(int BN, bool pair) { return (kBM + b_rows(BN, pair)) * kRowBytes; }
+__host__ __device__ constexpr int stages(int BN, bool pair) { return pair || BN == 128 ? 6 : 8; }
+__host__ __device__ constexpr int smem_bytes(int BN, bool pair) {
+  // ring, and the epilogue warps' stages
+  return 1024 + stages(BN, pair) * stage_bytes(BN, pair) + 4 * 32 * kPitch * 4;
 }
 
 struct Shared {
@@ -146,11 +154,12 @@ __device__ __forceinline__ void finish_chunk(const LinearArgs &e, const float *s
   }
 }
 
-template <int BN, bool kAMn, bool kBMn, bool kF8>
+template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, Tiles tiles,
                 LinearArgs epi, bool aligned) {
-  constexpr int kStages = stages(BN), kStage = stage_bytes(BN);
+  constexpr int kStages = stages(BN, kPair), kStage = stage_bytes(BN, kPair), kBRows = b_rows(BN, kPair);
+  constexpr int kTM = kPair ? 2 * kBM : kBM;             // rows of a tile
   constexpr int kElems = kF8 ? 128 : 64;                 // of k in a stage
   constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;  // TMEM columns: two accumulators
   extern __shared__ unsigned char raw[];
@@ -158,19 +167,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   // swizzle atoms are 1024-byte aligned
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = kPair ? (int)cluster_rank() : 0;      // 0 issues the products
+  const int64_t worker = kPair ? blockIdx.x / 2 : blockIdx.x, workers = kPair ? gridDim.x / 2 : gridDim.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], kPair ? 8 : 4);
     mbar_init(&sh.drain, 1);
     sh.dead = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&sh.tmem, kCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(&sh.tmem, kCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&sh.tmem, kCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // barriers and TMEM of both CTAs are ready
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
@@ -182,42 +199,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int64_t issued = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+      for (int64_t i = worker; ok && i < tiles.total; i += workers) {
         int64_t tm, tn;
         tile_at(tiles, i, tm, tn);
-        const int m0 = (int)(tm * kBM), n0 = (int)(tn * BN);
+        const int m0 = (int)(tm * kTM) + rank * kBM, n0 = (int)(tn * BN) + rank * kBRows;
         for (int kb = 0; kb < tiles.kblocks; ++kb) {
           if (!(ok = wait(&sh, &sh.empty[slot], phase ^ 1, 0))) break;
-          unsigned char *st = base + slot * kStage;
-          mbar_arrive_expect_tx(&sh.full[slot], kStage);
+          unsigned char *st = base + slot * kStage, *stb = st + kBM * kRowBytes;
+          // a pair's copies all count on the leader's barrier
+          const uint32_t bar = kPair ? map_cluster(&sh.full[slot], 0) : 0;
+          const auto copy = [&](unsigned char *to, const CUtensorMap *map, int c0, int c1) {
+            if constexpr (kPair)
+              tma_load_2d_pair(to, map, bar, c0, c1);
+            else
+              tma_load_2d(to, map, &sh.full[slot], c0, c1);
+          };
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], kPair ? 2 * kStage : kStage);
           if constexpr (kAMn) {
-            for (int j = 0; j < kBM / 64; ++j) tma_load_2d(st + j * 8192, &ma, &sh.full[slot], m0 + 64 * j, kb * 64);
+            for (int j = 0; j < kBM / 64; ++j) copy(st + j * 8192, &ma, m0 + 64 * j, kb * 64);
           } else {
-            tma_load_2d(st, &ma, &sh.full[slot], kb * kElems, m0);
+            copy(st, &ma, kb * kElems, m0);
           }
           if constexpr (kBMn) {
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(st + kBM * kRowBytes + j * 8192, &mb, &sh.full[slot], n0 + 64 * j, kb * 64);
+            for (int j = 0; j < kBRows / 64; ++j) copy(stb + j * 8192, &mb, n0 + 64 * j, kb * 64);
           } else {
-            tma_load_2d(st + kBM * kRowBytes, &mb, &sh.full[slot], kb * kElems, n0);
+            copy(stb, &mb, kb * kElems, n0);
           }
           ++issued;
           if (++slot == kStages) slot = 0, phase ^= 1;
         }
       }
-      if (!ok) {  // winding down: this warp's own copies land first
+      if (!ok && rank != 0) {  // winding down: this warp's own copies land first
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // (the leader's barrier counts them)
+      } else if (!ok) {
         for (int64_t i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
           for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.full[i % kStages], (i / kStages) & 1); ++j) {
           }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t id = kF8 ? idesc_e4m3(kBM, BN) : idesc_bf16(kBM, BN, kAMn, kBMn);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id = kF8 ? idesc_e4m3(kTM, BN) : idesc_bf16(kTM, BN, kAMn, kBMn);
+      const auto commit = [](uint64_t *bar) {
+        if constexpr (kPair)
+          mma_commit_pair(bar);
+        else
+          mma_commit(bar);
+      };
       int slot = 0, acc = 0;
       uint32_t phase = 0, accphase = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+      for (int64_t i = worker; ok && i < tiles.total; i += workers) {
         if (!(ok = wait(&sh, &sh.tempty[acc], accphase ^ 1, 1))) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
@@ -234,21 +266,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k) {
             const uint64_t xa = da + (uint64_t)(k * (kAMn ? 2048 : 32) >> 4);
             const uint64_t xb = db + (uint64_t)(k * (kBMn ? 2048 : 32) >> 4);
-            if constexpr (kF8)
+            if constexpr (kPair)
+              mma_ss_pair<kF8>(d, xa, xb, id, kb > 0 || k > 0);
+            else if constexpr (kF8)
               mma_ss_f8(d, xa, xb, id, kb > 0 || k > 0);
             else
               mma_ss(d, xa, xb, id, kb > 0 || k > 0);
           }
-          mma_commit(&sh.empty[slot]);
+          commit(&sh.empty[slot]);
           if (++slot == kStages) slot = 0, phase ^= 1;
         }
         if (!ok) break;
-        mma_commit(&sh.tfull[acc]);
+        commit(&sh.tfull[acc]);
         acc ^= 1;
         if (acc == 0) accphase ^= 1;
       }
       if (!ok) {  // products in flight end before TMEM is given back
-        mma_commit(&sh.drain);
+        commit(&sh.drain);
         for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.drain, 0); ++j) {
         }
       }
@@ -258,10 +292,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *stage = reinterpret_cast<float *>(base + kStages * kStage) + quarter * 32 * kPitch;
     int acc = 0;
     uint32_t accphase = 0;
-    for (int64_t i = blockIdx.x; i < tiles.total; i += gridDim.x) {
+    for (int64_t i = worker; i < tiles.total; i += workers) {
       int64_t tm, tn;
       tile_at(tiles, i, tm, tn);
-      const int64_t m0 = tm * kBM + quarter * 32, m = m0 + lane / 4, n0 = tn * BN;
+      const int64_t m0 = tm * kTM + rank * kBM + quarter * 32, m = m0 + lane / 4, n0 = tn * BN;
       float sx[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) sx[k] = epi.x_scale && m + 8 * k < epi.M ? epi.x_scale[m + 8 * k] : 1.f;
@@ -292,7 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.tempty[acc]);
+      if (lane == 0) {
+        if constexpr (kPair)
+          mbar_arrive_cluster(map_cluster(&sh.tempty[acc], 0));
+        else
+          mbar_arrive(&sh.tempty[acc]);
+      }
       acc ^= 1;
       if (acc == 0) accphase ^= 1;
     }
@@ -300,8 +339,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // neither CTA leaves while the other may reach into it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kCols);
+  if (warp == 1) {
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, kCols);
+    else
+      tmem_dealloc(tmem, kCols);
+  }
 }
 
 int sm_count() {
@@ -310,7 +355,7 @@ int sm_count() {
   return n;
 }
 
-template <int BN, bool kAMn, bool kBMn, bool kF8>
+template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>
 cudaError_t run(const GemmArgs &g, cudaStream_t s) {
   const int size = kF8 ? 1 : 2;
   const LinearArgs &e = g.epi;
@@ -320,10 +365,11 @@ cudaError_t run(const GemmArgs &g, cudaStream_t s) {
              : make_map_2d_sw128(&ma, g.a, (uint64_t)g.K, (uint64_t)e.M, (uint64_t)g.lda, size, kBM);
   if (err != cudaSuccess) return err;
   err = kBMn ? make_map_2d_sw128(&mb, g.b, (uint64_t)e.N, (uint64_t)g.K, (uint64_t)g.ldb, size, 64)
-             : make_map_2d_sw128(&mb, g.b, (uint64_t)g.K, (uint64_t)e.N, (uint64_t)g.ldb, size, BN);
+             : make_map_2d_sw128(&mb, g.b, (uint64_t)g.K, (uint64_t)e.N, (uint64_t)g.ldb, size, b_rows(BN, kPair));
   if (err != cudaSuccess) return err;
   Tiles t;
-  t.m_tiles = (e.M + kBM - 1) / kBM;
+  constexpr int kTM = kPair ? 2 * kBM : kBM;
+  t.m_tiles = (e.M + kTM - 1) / kTM;
   t.n_tiles = (e.N + BN - 1) / BN;
   t.total = t.m_tiles * t.n_tiles;
   const int elems = kF8 ? 128 : 64;
@@ -331,23 +377,33 @@ cudaError_t run(const GemmArgs &g, cudaStream_t s) {
   const auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   const bool aligned = e.N % 8 == 0 && ok(e.out) && ok(e.pre) && ok(e.residual) && (!e.residual || e.ldr % 8 == 0) &&
                        ok(e.bias) && ok(e.w_scale);
-  auto kern = gemm_kernel<BN, kAMn, kBMn, kF8>;
-  if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN))) != cudaSuccess)
-    return err;
-  const int64_t sms = sm_count(), grid = t.total < sms ? t.total : sms;
-  kern<<<(unsigned)grid, kThreads, smem_bytes(BN), s>>>(ma, mb, t, e, aligned);
-  return cudaGetLastError();
+  auto kern = gemm_kernel<BN, kPair, kAMn, kBMn, kF8>;
+  constexpr int smem = smem_bytes(BN, kPair);
+  if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
+  const int64_t ctas = kPair ? 2 : 1, fit = sm_count() / ctas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((t.total < fit ? t.total : fit) * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = kPair ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, t, e, aligned);
 }
 
 template <bool kAMn, bool kBMn, bool kF8>
 cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
-  // the widest tile that still gives every SM one; below that, narrower tiles
-  // spread the work over more SMs
-  const int64_t m = (g.epi.M + kBM - 1) / kBM, sms = sm_count();
-  const auto tiles = [&](int bn) { return m * ((g.epi.N + bn - 1) / bn); };
-  if (tiles(256) >= sms) return run<256, kAMn, kBMn, kF8>(g, s);
-  if (tiles(128) >= sms) return run<128, kAMn, kBMn, kF8>(g, s);
-  return run<64, kAMn, kBMn, kF8>(g, s);
+  // the widest tile that still gives every SM one (a pair's tile counts for
+  // two); below that, narrower tiles spread the work over more SMs
+  const int64_t sms = sm_count();
+  const auto tiles = [&](int bm, int bn) { return ((g.epi.M + bm - 1) / bm) * ((g.epi.N + bn - 1) / bn); };
+  if (2 * tiles(256, 256) >= sms) return run<256, true, kAMn, kBMn, kF8>(g, s);
+  if (tiles(128, 128) >= sms) return run<128, false, kAMn, kBMn, kF8>(g, s);
+  return run<64, false, kAMn, kBMn, kF8>(g, s);
 }
 
 }  // namespace
