@@ -5,12 +5,13 @@
 // the shared-memory descriptors express as MN-major operands, so nothing is
 // transposed in memory.
 //
-// One persistent CTA per SM, six warps:
+// One persistent CTA per SM, ten warps:
 //   warp 0: TMA producer, a ring of kStages stages of 128 bytes of k;
 //   warp 1: allocates TMEM and issues the products (one thread) into one of
 //           two TMEM accumulators of 128 x BN;
-//   warps 2-5: epilogue, one TMEM lane quarter (32 rows) each, while the next
-//           tile's products run into the other accumulator.
+//   warps 2-9: epilogue, two to a TMEM lane quarter (32 rows) that take turns
+//           at its columns, while the next tile's products run into the other
+//           accumulator.
 // A large product takes CTAs in pairs (cta_group::2): a tile of 256 x 256 of
 // which each CTA loads 128 rows of either operand, 32 KB a stage.  One CTA
 // alone on 128 x 256 needs 48 KB for the same work, which at full rate is more
@@ -31,7 +32,8 @@ using namespace sm100;
 __device__ unsigned int g_linear_error = 0;
 
 constexpr int kBM = 128;
-constexpr int kThreads = 192;
+constexpr int kEpi = 8;          // epilogue warps
+constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kBand = 8;
 constexpr int kPitch = 36;      // floats a row of an epilogue warp's stage
 constexpr int kRowBytes = 128;  // of k in a stage: 64 bfloat16 or 128 e4m3
@@ -39,10 +41,10 @@ constexpr int kRowBytes = 128;  // of k in a stage: 64 bfloat16 or 128 e4m3
 // BN: columns of a tile; a pair's CTA loads half of B's rows
 __host__ __device__ constexpr int b_rows(int BN, bool pair) { return pair ? BN / 2 : BN; }
 __host__ __device__ constexpr int stage_bytes(int BN, bool pair) { return (kBM + b_rows(BN, pair)) * kRowBytes; }
-__host__ __device__ constexpr int stages(int BN, bool pair) { return pair || BN == 128 ? 6 : 8; }
+__host__ __device__ constexpr int stages(int BN, bool pair) { return pair || BN == 128 ? 5 : 7; }
 __host__ __device__ constexpr int smem_bytes(int BN, bool pair) {
   // ring, and the epilogue warps' stages
-  return 1024 + stages(BN, pair) * stage_bytes(BN, pair) + 4 * 32 * kPitch * 4;
+  return 1024 + stages(BN, pair) * stage_bytes(BN, pair) + kEpi * 32 * kPitch * 4;
 }
 
 struct Shared {
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t worker = kPair ? blockIdx.x / 2 : blockIdx.x, workers = kPair ? gridDim.x / 2 : gridDim.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], kPair ? 8 : 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], kPair ? 2 * kEpi : kEpi);
     mbar_init(&sh.drain, 1);
     sh.dead = 0;
     fence_mbar_init();
@@ -289,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
-    float *stage = reinterpret_cast<float *>(base + kStages * kStage) + quarter * 32 * kPitch;
+    const int half = (warp - 2) / 4;  // of the columns: every second chunk of 32
+    float *stage = reinterpret_cast<float *>(base + kStages * kStage) + (warp - 2) * 32 * kPitch;
     int acc = 0;
     uint32_t accphase = 0;
     for (int64_t i = worker; i < tiles.total; i += workers) {
@@ -299,22 +302,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sx[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) sx[k] = epi.x_scale && m + 8 * k < epi.M ? epi.x_scale[m + 8 * k] : 1.f;
+      const int chunks = (int)(epi.N - n0 < BN ? (epi.N - n0 + 31) / 32 : BN / 32);
       Ahead next, now;
-      if (aligned) fetch_ahead(epi, m, n0 + (lane % 4) * 8, next);
+      if (aligned && half < chunks) fetch_ahead(epi, m, n0 + half * 32 + (lane % 4) * 8, next);
       uint32_t r[32];
       if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
       tc_fence_after();
-      const int chunks = (int)(epi.N - n0 < BN ? (epi.N - n0 + 31) / 32 : BN / 32);
+      if (half < chunks) tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + half * 32), r);
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + c * 32), r);
+      for (int c = half; c < chunks; c += 2) {
         now = next;
-        if (aligned && c + 1 < chunks) fetch_ahead(epi, m, n0 + (c + 1) * 32 + (lane % 4) * 8, next);
+        if (aligned && c + 2 < chunks) fetch_ahead(epi, m, n0 + (c + 2) * 32 + (lane % 4) * 8, next);
         tmem_wait_ld_regs(r);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<uint4 *>(stage + lane * kPitch + 4 * k) =
               make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        // the next chunk comes out of TMEM while this one is finished
+        if (c + 2 < chunks) tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + (c + 2) * 32), r);
         __syncwarp();
         if (aligned) {
           finish_chunk(epi, stage, lane, m, n0 + c * 32 + (lane % 4) * 8, sx, now);
