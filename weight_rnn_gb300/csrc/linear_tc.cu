@@ -308,12 +308,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t r[32];
       if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
       tc_fence_after();
+      // this warp's part of the accumulator has been read: the products may
+      // overwrite it.  Nothing but TMEM is handed over, and the fence orders that.
+      const auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_cluster_relaxed(map_cluster(&sh.tempty[acc], 0));
+          else
+            mbar_arrive(&sh.tempty[acc]);
+        }
+      };
       if (half < chunks) tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + half * 32), r);
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         now = next;
         if (aligned && c + 2 < chunks) fetch_ahead(epi, m, n0 + (c + 2) * 32 + (lane % 4) * 8, next);
         tmem_wait_ld_regs(r);
+        if (c + 2 >= chunks) release();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<uint4 *>(stage + lane * kPitch + 4 * k) =
@@ -329,14 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair)
-          mbar_arrive_cluster(map_cluster(&sh.tempty[acc], 0));
-        else
-          mbar_arrive(&sh.tempty[acc]);
-      }
+      if (half >= chunks) release();
       acc ^= 1;
       if (acc == 0) accphase ^= 1;
     }

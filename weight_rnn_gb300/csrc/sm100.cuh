@@ -360,9 +360,11 @@ __device__ __forceinline__ uint32_t map_cluster(const void *p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-// One arrival on a barrier of another CTA, by its cluster address.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// One arrival on a barrier of another CTA, by its cluster address.  Relaxed:
+// it orders no memory accesses (a release at cluster scope would wait for this
+// thread's global stores to land, about a microsecond).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
