@@ -353,10 +353,11 @@ int delta_selftest_wait(int polls, struct CUstream_st *stream) {
 }
 
 int delta_check_device(void) {
-  unsigned int word = 0, ut_word = 0, linear_word = 0;
+  unsigned int word = 0, ut_word = 0, linear_word = 0, scan_word = 0;
   cudaError_t err = delta::read_and_clear_tc_error(&word);
   if (err == cudaSuccess) err = delta::read_and_clear_ut_error(&ut_word);
   if (err == cudaSuccess) err = delta::read_and_clear_linear_error(&linear_word);
+  if (err == cudaSuccess) err = delta::read_and_clear_scan_error(&scan_word);
   if (err != cudaSuccess) return cuda_fail(err, "device check");
   if (word != 0)
     return fail(DELTA_ERR_CUDA,
@@ -369,6 +370,8 @@ int delta_check_device(void) {
   if (linear_word != 0)
     return fail(DELTA_ERR_CUDA, "a wait of a linear layer gave up (role %u): results of that call are invalid",
                 linear_word - 1);
+  if (scan_word != 0)
+    return fail(DELTA_ERR_CUDA, "a wait of a scan's cluster gave up: results of that call are invalid");
   return DELTA_OK;
 }
 

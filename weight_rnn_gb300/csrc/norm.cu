@@ -65,6 +65,37 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[V]) {
   }
 }
 
+// float32 pairs: one instruction for two elements.  The single-element path
+// (V = 1) uses the plain forms.
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpk(uint64_t r, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// a vector as pairs
+template <typename T, int V>
+__device__ __forceinline__ uint64_t pair_of(const Pack<T, V> &p, int i) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w = reinterpret_cast<const uint32_t *>(p.v)[i];
+    return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  } else {
+    return pk(p.v[2 * i], p.v[2 * i + 1]);
+  }
+}
+
 // One row's reduction over its nt threads (a multiple of 32): warp shuffles,
 // then the row's warps meet in `part`.  Every thread gets the same sum, taken
 // in the same order.  `part` alternates between calls, so one barrier a call
@@ -105,19 +136,17 @@ __host__ __device__ constexpr int ring_rows(int N, int per) { return N * per >= 
 // This thread's vectors of one row: N tensors of kPer vectors.  Whole vectors
 // (V > 1) pass through the thread's ring, single elements through registers,
 // one row ahead.
-template <typename In, int V, int kPer, int N>
+template <typename In, int V, int kPer, int N, int kT>
 struct Rows {
   using Vec = APack<In, V>;
   static constexpr bool kRing = V > 1;
-  static constexpr int kStages = ring_rows(N, kPer);
+  static constexpr int kStages = kRing ? ring_rows(N, kPer) : 1;
   const In *base[N];
   int64_t ld[N], rows, D;
-  Vec *ring;  // [kStages][N][kPer][threads of the CTA]
+  Vec *ring;  // [kStages][N][kPer][kT], from this thread's place on
   Vec held[kRing ? 1 : N][kRing ? 1 : kPer], next[kRing ? 1 : N][kRing ? 1 : kPer];
   int slot = 0;
 
-  __device__ __forceinline__ int threads() const { return blockDim.x * blockDim.y; }
-  __device__ __forceinline__ int self() const { return threadIdx.y * blockDim.x + threadIdx.x; }
   __device__ __forceinline__ void fetch(int64_t row, int to) {
     if constexpr (kRing) {
       if (row < rows) {
@@ -128,7 +157,7 @@ struct Rows {
             const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
             if (d < D && base[n]) {
               const uint32_t at =
-                  (uint32_t)__cvta_generic_to_shared(ring + ((to * N + n) * kPer + j) * threads() + self());
+                  (uint32_t)__cvta_generic_to_shared(ring + ((to * N + n) * kPer + j) * kT);
               asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(base[n] + row * ld[n] + d)
                            : "memory");
             }
@@ -174,7 +203,7 @@ struct Rows {
   }
   __device__ __forceinline__ Vec get(int n, int j) const {
     if constexpr (kRing)
-      return ring[((slot * N + n) * kPer + j) * threads() + self()];
+      return ring[((slot * N + n) * kPer + j) * kT];
     else
       return held[n][j];
   }
@@ -182,8 +211,8 @@ struct Rows {
 
 // ------------------------------------------------------------------ forward
 // blockDim (nt, rows a CTA); a thread's vectors are nt apart
-template <typename In, int V, int kPer, bool kQuant>
-__global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) norm_fwd_kernel(NormArgs p) {
+template <typename In, int V, int kPer, int kT, bool kQuant>
+__global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? (kQuant ? 1024 : 768) / kT : 1) norm_fwd_kernel(NormArgs p) {
   __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
@@ -191,10 +220,10 @@ __global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) 
   load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Rows<In, V, kPer, 2> in;
+  Rows<In, V, kPer, 2, kT> in;
   in.base[0] = static_cast<const In *>(p.x); in.base[1] = static_cast<const In *>(p.residual);
   in.ld[0] = p.ldx; in.ld[1] = p.ldr; in.rows = p.rows; in.D = p.D;
-  in.ring = reinterpret_cast<APack<In, V> *>(ring);
+  in.ring = reinterpret_cast<APack<In, V> *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
   in.start(first, step);
   int buf = 0;
   // every row of the CTA takes part in the barriers until the last is done
@@ -250,8 +279,8 @@ __global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) 
 // ----------------------------------------------------------------- backward
 // The row is read from its ring twice, before and after the reduction, rather
 // than held: that is what lets two CTAs of 512 threads share an SM.
-template <typename In, int V, int kPer>
-__global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) norm_bwd_kernel(NormBwdArgs p) {
+template <typename In, int V, int kPer, int kT>
+__global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? 768 / kT : 1) norm_bwd_kernel(NormBwdArgs p) {
   __shared__ float part[2][8 * 32];
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
@@ -263,11 +292,11 @@ __global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) 
     for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Rows<In, V, kPer, 3> in;
+  Rows<In, V, kPer, 3, kT> in;
   in.base[0] = static_cast<const In *>(p.dy); in.base[1] = static_cast<const In *>(p.sum);
   in.base[2] = static_cast<const In *>(p.dsum);
   in.ld[0] = in.ld[1] = in.ld[2] = in.D = p.D; in.rows = p.rows;
-  in.ring = reinterpret_cast<APack<In, V> *>(ring);
+  in.ring = reinterpret_cast<APack<In, V> *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
   in.start(first, step);
   float ahead = first < p.rows ? p.rstd[first] : 0.f;
   int buf = 0;
@@ -280,11 +309,22 @@ __global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) 
     for (int j = 0; j < kPer; ++j) {
       const APack<In, V> gv = in.get(0, j), tv = in.get(1, j);
       if (row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D) {
+        if constexpr (V > 1) {
+          uint64_t sum = pk(0.f, 0.f);
+          const uint64_t rr = pk(rstd, rstd);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float t = to_f(tv.v[i]) * rstd, y = to_f(gv.v[i]);
-          dw[j][i] = fmaf(y, t, dw[j][i]);
-          dot = fmaf(y * w[j][i], t, dot);
+          for (int i = 0; i < V / 2; ++i) {
+            const uint64_t t = mul2(pair_of(tv, i), rr), y = pair_of(gv, i);
+            unpk(fma2(y, t, pk(dw[j][2 * i], dw[j][2 * i + 1])), dw[j][2 * i], dw[j][2 * i + 1]);
+            sum = fma2(mul2(y, pk(w[j][2 * i], w[j][2 * i + 1])), t, sum);
+          }
+          float a, b;
+          unpk(sum, a, b);
+          dot += a + b;
+        } else {
+          const float t = to_f(tv.v[0]) * rstd, y = to_f(gv.v[0]);
+          dw[j][0] = fmaf(y, t, dw[j][0]);
+          dot = fmaf(y * w[j][0], t, dot);
         }
       }
     }
@@ -296,10 +336,18 @@ __global__ void __launch_bounds__(kMostThreads, V *kPer <= 16 && V > 1 ? 2 : 1) 
         if (d >= p.D) continue;
         const APack<In, V> gv = in.get(0, j), tv = in.get(1, j), sv = in.get(2, j);
         float g[V];
+        // rstd (w dy - t^ dot) + dsum, with t^ = sum * rstd
+        const float c = -rstd * rstd * dot;
+        if constexpr (V > 1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          g[i] = fmaf(rstd, to_f(gv.v[i]) * w[j][i] - to_f(tv.v[i]) * rstd * dot,
-                      p.dsum ? to_f(sv.v[i]) : 0.f);
+          for (int i = 0; i < V / 2; ++i) {
+            const uint64_t wy = mul2(pair_of(gv, i), pk(w[j][2 * i], w[j][2 * i + 1]));
+            const uint64_t low = p.dsum ? pair_of(sv, i) : pk(0.f, 0.f);
+            unpk(fma2(wy, pk(rstd, rstd), fma2(pair_of(tv, i), pk(c, c), low)), g[2 * i], g[2 * i + 1]);
+          }
+        } else {
+          g[0] = fmaf(rstd, to_f(gv.v[0]) * w[j][0], fmaf(to_f(tv.v[0]), c, p.dsum ? to_f(sv.v[0]) : 0.f));
+        }
         store_v<In, V>(static_cast<In *>(p.dx) + row * p.D + d, g);
       }
     }
@@ -337,6 +385,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
 struct Plan {
   int V, per, nt, rpc;  // elements a vector, vectors a thread, threads a row, rows a CTA
   int64_t grid;
+  int threads;          // of a CTA at most, which its ring is laid out for
   int smem;             // the ring
 };
 
@@ -359,9 +408,10 @@ Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors) {
   q.nt = (int)((n + q.per - 1) / q.per + 31) / 32 * 32;
   q.rpc = q.nt >= 256 ? 1 : 256 / q.nt;
   const int64_t ctas = (rows + q.rpc - 1) / q.rpc;
-  q.smem = aligned ? ring_rows(tensors, q.per) * tensors * q.per * q.nt * q.rpc * 16 : 0;
+  q.threads = q.nt * q.rpc <= 256 ? 256 : kMostThreads;
+  q.smem = aligned ? ring_rows(tensors, q.per) * tensors * q.per * q.threads * 16 : 0;
   // as many CTAs as an SM holds: by threads at 64 registers, and by rings
-  int fit = 1024 / (q.nt * q.rpc);
+  int fit = 1024 / q.threads;
   if (q.smem && fit > 200 * 1024 / q.smem) fit = 200 * 1024 / q.smem;
   const int64_t cap = (int64_t)sms * (fit > 1 ? fit : 1);
   q.grid = ctas < cap ? ctas : cap;
@@ -401,14 +451,18 @@ cudaError_t go(K kern, const A &a, const Plan &q, cudaStream_t s) {
 template <typename In, int V, int kPer>
 struct FwdOne {
   static cudaError_t run(const NormArgs &a, const Plan &q, cudaStream_t s) {
-    return a.scale ? go(norm_fwd_kernel<In, V, kPer, true>, a, q, s)
-                   : go(norm_fwd_kernel<In, V, kPer, false>, a, q, s);
+    if (q.threads == 256)
+      return a.scale ? go(norm_fwd_kernel<In, V, kPer, 256, true>, a, q, s)
+                     : go(norm_fwd_kernel<In, V, kPer, 256, false>, a, q, s);
+    return a.scale ? go(norm_fwd_kernel<In, V, kPer, kMostThreads, true>, a, q, s)
+                   : go(norm_fwd_kernel<In, V, kPer, kMostThreads, false>, a, q, s);
   }
 };
 template <typename In, int V, int kPer>
 struct BwdOne {
   static cudaError_t run(const NormBwdArgs &a, const Plan &q, cudaStream_t s) {
-    return go(norm_bwd_kernel<In, V, kPer>, a, q, s);
+    return q.threads == 256 ? go(norm_bwd_kernel<In, V, kPer, 256>, a, q, s)
+                            : go(norm_bwd_kernel<In, V, kPer, kMostThreads>, a, q, s);
   }
 };
 

@@ -16,7 +16,7 @@
 // (A, B) after (A', B') is (A A', A B' + B).  So a tile of 32 VEC channels is
 // cut into sub-chunks of consecutive steps, one per warp, lane = VEC channels:
 //   1. each warp takes its steps from its own ring in shared memory, filled
-//      a tile or two ahead by asynchronous copies, and composes its map;
+//      a tile ahead by asynchronous copies, and composes its map;
 //   2. the maps meet in shared memory (one barrier), and every warp folds
 //      them in time order onto the state carried from the last tile, which
 //      gives the state at its own start and, redundantly in every warp, the
@@ -24,8 +24,10 @@
 //   3. each warp runs the recurrence again from its start and writes out.
 // Where the (batch row, channel strip) pairs alone do not fill the GPU, a
 // cluster of `cs` CTAs takes cs neighbouring tiles at a time and exchanges one
-// map per CTA through distributed shared memory; the fold order is the time
-// order, so results do not depend on scheduling.  All maps and states are
+// map per CTA through distributed shared memory, by asynchronous stores that
+// count on the receiver's mbarrier (a cluster-wide barrier would release, that
+// is wait for, every output store: it took a third of the cycles).  The fold
+// order is the time order, so results do not depend on scheduling.  All maps and states are
 // float32; two channels of a lane go through packed float32 pairs.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -33,9 +35,12 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace delta {
 namespace {
+
+__device__ unsigned int g_scan_error = 0;
 
 namespace cg = cooperative_groups;
 
@@ -45,8 +50,10 @@ constexpr int kBwdSteps = 8;             // (the reverse holds twice the values 
 static_assert(kScanBlock % kFwdSteps == 0 && kScanBlock == kWarps * kBwdSteps,
               "states are saved at a warp's start, and taken at a reverse tile's");
 constexpr int kMaxCluster = 8;           // the portable cluster size
-// tiles in a warp's ring: three where two CTAs' rings then fit an SM, else two
-__host__ __device__ constexpr int ring_stages(int tile_bytes) { return tile_bytes <= 32768 ? 3 : 2; }
+// Tiles in a warp's ring.  With three (where they fit) B4 T8192 D4096 took
+// 137 us instead of 127, and a reverse ring of the linear form kept a second
+// CTA off the SM (732 us instead of 423 at B1 T65536 D2048).
+constexpr int kStages = 2;
 
 // VEC neighbouring elements as they lie in memory
 template <typename T, int VEC>
@@ -231,15 +238,53 @@ struct Map {
   float a[VEC], b[kOffsets][VEC];
 };
 
+// The exchange of one map per CTA in a cluster.  Two buffers: a CTA sends
+// round r + 2 only after it has every map of round r + 1, which its peers send
+// after they have read round r.  Waits are bounded; one that runs out sets the
+// error word and lets the kernel end.
+struct Exchange {
+  uint64_t bar[2];
+  volatile int dead;
+
+  __device__ __forceinline__ void init() {
+    sm100::mbar_init(&bar[0], 1);
+    sm100::mbar_init(&bar[1], 1);
+    dead = 0;
+    sm100::fence_mbar_init();
+  }
+  template <int VEC>
+  __device__ __forceinline__ void send(int buf, const Map<VEC, 1> *slot, uint32_t to, const Map<VEC, 1> &m) {
+    const uint32_t at = sm100::map_cluster(slot, to), b = sm100::map_cluster(&bar[buf], to);
+    if constexpr (VEC == 2)
+      asm volatile(
+          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+          "f"(m.a[0]), "f"(m.a[1]), "f"(m.b[0][0]), "f"(m.b[0][1]), "r"(b)
+          : "memory");
+    else
+      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+                   "f"(m.a[0]), "f"(m.b[0][0]), "r"(b)
+                   : "memory");
+  }
+  __device__ __forceinline__ void expect(int buf, uint32_t bytes) { sm100::mbar_arrive_expect_tx(&bar[buf], bytes); }
+  __device__ __forceinline__ void wait(int buf, uint32_t parity) {
+    for (uint32_t i = 0; i < (1u << 22); ++i) {
+      if (sm100::mbar_try_wait(&bar[buf], parity)) return;
+      if (dead) return;
+    }
+    dead = 1;
+    atomicExch(&g_scan_error, 1u);
+  }
+};
+
 // ------------------------------------------------------------------ forward
 template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
   constexpr int S = kFwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
-  constexpr int kStages = ring_stages(kTile * kRow * (int)(sizeof(In) + sizeof(Gate)));
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 1> s_map[2][kWarps][32];
   __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
+  __shared__ Exchange ex;
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // the same for all lanes, also to the compiler
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
@@ -269,7 +314,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 
   const int64_t rounds = (tiles + cs - 1) / cs;
   // every CTA of the cluster runs before any writes into its shared memory
-  if (kCluster) cg::this_cluster().barrier_arrive();
+  if (kCluster) {
+    if (threadIdx.x == 0) ex.init();
+    cg::this_cluster().barrier_arrive();
+  }
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(rank + (int64_t)i * cs, i);
   if (kCluster) cg::this_cluster().barrier_wait();
@@ -314,9 +362,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
     __syncthreads();
     float h[VEC], start[VEC];
     if (kCluster) {
-      // one map per CTA to every CTA of the cluster: warp w serves CTA w.  The
-      // buffer written now was last read before the previous round's barrier.
-      cg::cluster_group cluster = cg::this_cluster();
+      // one map per CTA to every CTA of the cluster: warp w serves CTA w
+      if (threadIdx.x == 0) ex.expect(buf, cs * 32 * sizeof(Map<VEC, 1>));
       if (warp < cs) {
         Map<VEC, 1> m = s_map[buf][0][lane];
 #pragma unroll
@@ -325,9 +372,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
           affine<kSig>(k.a, m.b[0], k.b[0], m.b[0]);
           vmul(m.a, k.a, m.a);
         }
-        cluster.map_shared_rank(&s_cta[buf][rank][0], warp)[lane] = m;
+        ex.send(buf, &s_cta[buf][rank][lane], warp, m);
       }
-      cluster.sync();
+      ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) h[i] = carry[i];
       for (int r = 0; r < cs; ++r) {
@@ -394,10 +441,10 @@ template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
   constexpr int S = kBwdSteps, kTile = kWarps * S, kRow = 32 * VEC, kSlot = S * kRow;
-  constexpr int kStages = ring_stages(kTile * kRow * (int)(2 * sizeof(In) + sizeof(Gate)));
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 2> s_map[2][kWarps][32];  // offsets: forward, reverse
   __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
+  __shared__ Exchange ex;
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
@@ -435,7 +482,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   for (int i = 0; i < VEC; ++i) carry[i] = live && p.dhT ? p.dhT[b * p.D + c0 + i] : 0.f;
 
   const int64_t rounds = (tiles + cs - 1) / cs;
-  if (kCluster) cg::this_cluster().barrier_arrive();
+  if (kCluster) {
+    if (threadIdx.x == 0) ex.init();
+    cg::this_cluster().barrier_arrive();
+  }
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(tiles - 1 - rank - (int64_t)i * cs, i);
   fetch_state(tiles - 1 - rank);
@@ -493,7 +543,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
     __syncthreads();
     float r[VEC], c[VEC];
     if (kCluster) {
-      cg::cluster_group cluster = cg::this_cluster();
+      if (threadIdx.x == 0) ex.expect(buf, cs * 32 * sizeof(Map<VEC, 1>));
       if (warp < cs) {
         const Map<VEC, 2> last = s_map[buf][kWarps - 1][lane];
         Map<VEC, 1> m;
@@ -505,9 +555,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
           affine<kSig>(k.a, m.b[0], k.b[1], m.b[0]);
           vmul(m.a, k.a, m.a);
         }
-        cluster.map_shared_rank(&s_cta[buf][rank][0], warp)[lane] = m;
+        ex.send(buf, &s_cta[buf][rank][lane], warp, m);
       }
-      cluster.sync();
+      ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) r[i] = carry[i];
       for (int k = 0; k < cs; ++k) {
@@ -631,12 +681,14 @@ bool pieces(const ScanArgs &a, int nx, int ng) {
 bool pairs(const ScanArgs &a) { return pieces(a, 2, 2); }
 bool wide(const ScanArgs &a) { return pieces(a, a.bf16 ? 8 : 4, a.bf16 && a.sigmoid ? 8 : 4); }
 
-// CTAs of a cluster along the time axis: enough to give every SM two CTAs,
-// as far as there are tiles
+// CTAs of a cluster along the time axis: as many as keep all CTAs resident at
+// once (two an SM), and as there are tiles.  Past that a second wave costs more
+// than the shorter CTAs give: 256 rows of 8192 steps take 137 us alone and 155
+// to 205 in clusters of 2 to 8.
 int cluster_size(int64_t rows, int64_t tiles) {
-  const int64_t want = 2 * (int64_t)sm_count();
+  const int64_t fit = 2 * (int64_t)sm_count();
   int cs = 1;
-  while (cs < kMaxCluster && rows * cs < want && cs < tiles) cs *= 2;
+  while (cs < kMaxCluster && rows * cs * 2 <= fit && cs < tiles) cs *= 2;
   return cs;
 }
 
@@ -664,7 +716,7 @@ cudaError_t launch_fwd(const ScanArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kFwdSteps - 1) / (kWarps * kFwdSteps));
   constexpr int tile = kWarps * kFwdSteps * 32 * VEC * (int)(sizeof(In) + (kSig ? sizeof(In) : 4));
-  const int smem = ring_stages(tile) * tile;
+  const int smem = kStages * tile;
   return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_fwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
@@ -673,7 +725,7 @@ cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps));
   constexpr int tile = kWarps * kBwdSteps * 32 * VEC * (int)(2 * sizeof(In) + (kSig ? sizeof(In) : 4));
-  const int smem = ring_stages(tile) * tile;
+  const int smem = kStages * tile;
   return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_bwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
@@ -726,6 +778,13 @@ cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s) {
   }
   if (a.sigmoid) return v2 ? launch_one<float, true, 2>(a, s) : launch_one<float, true, 1>(a, s);
   return v2 ? launch_one<float, false, 2>(a, s) : launch_one<float, false, 1>(a, s);
+}
+
+cudaError_t read_and_clear_scan_error(unsigned int *word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_scan_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_scan_error, &zero, sizeof(unsigned int));
 }
 
 cudaError_t launch_scan_passthrough(const float *h0, float *hT, int64_t n, cudaStream_t s) {
