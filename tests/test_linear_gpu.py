@@ -63,7 +63,8 @@ def check(out, pre, x, w, b, res, act, scales=None):
 
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1000, 4096), (3, 17, 7), (8, 128, 200), (9, 100, 1024), (16, 257, 72),
           (17, 513, 130), (31, 40, 513), (32, 2048, 512), (33, 64, 64), (64, 65, 8), (100, 257, 63),
-          (127, 8, 1000), (129, 300, 65), (300, 520, 1000), (257, 1024, 2048)]
+          (127, 8, 1000), (129, 300, 65), (300, 520, 1000), (257, 1024, 2048),
+          (40, 131, 700), (520, 72, 1500), (200, 900, 4096), (90, 2000, 530)]
 
 
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])

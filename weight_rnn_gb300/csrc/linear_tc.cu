@@ -35,6 +35,7 @@ constexpr int kBM = 128;
 constexpr int kEpi = 8;          // epilogue warps
 constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kBand = 8;
+constexpr int kMaxSplit = 8;    // CTAs that share a tile's k: the portable cluster
 constexpr int kPitch = 36;      // floats a row of an epilogue warp's stage
 constexpr int kRowBytes = 128;  // of k in a stage: 64 bfloat16 or 128 e4m3
 
@@ -69,13 +70,15 @@ __device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity,
 struct Tiles {
   int64_t m_tiles, n_tiles, total;
   int kblocks;
+  int split, per;  // CTAs (or pairs) that share a tile's k, and blocks of k for each
 };
 __device__ __forceinline__ void tile_at(const Tiles &t, int64_t i, int64_t &m, int64_t &n) {
-  const int64_t band = i / (kBand * t.n_tiles), first = band * kBand;
-  const int64_t high = t.m_tiles - first < kBand ? t.m_tiles - first : kBand;
-  const int64_t r = i - band * kBand * t.n_tiles;
-  m = first + r % high;
-  n = r / high;
+  // (fewer than 2^32 tiles: 32-bit divisions, an order of magnitude shorter)
+  const uint32_t across = kBand * (uint32_t)t.n_tiles, band = (uint32_t)i / across, first = band * kBand;
+  const uint32_t left = (uint32_t)t.m_tiles - first, high = left < kBand ? left : kBand;
+  const uint32_t r = (uint32_t)i - band * across, down = r / high;
+  m = first + (r - down * high);
+  n = down;
 }
 
 // The epilogue of a warp's 32 rows, 32 columns at a time.  TMEM gives a lane
@@ -124,6 +127,31 @@ __device__ __forceinline__ void fetch_ahead(const LinearArgs &e, int64_t m, int6
   if (e.x_scale) load8(e.w_scale + n, h.scale);
 }
 
+// 8 columns of one row, start to end
+__device__ __forceinline__ void finish8(const LinearArgs &e, int64_t row, int64_t n, float (&v)[8], float sx,
+                                        const Ahead &h, const uint4 &res) {
+  if (e.x_scale) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= sx * h.scale[j];
+  }
+  if (e.bias) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += h.bias[j];
+  }
+  if (e.pre) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.pre) + row * e.N + n) = narrow8(v);
+  if (e.act != kActNone) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = linear::activate(e.act, v[j]);
+  }
+  if (e.residual) {
+    float q[8];
+    widen8(res, q);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += q[j];
+  }
+  *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.out) + row * e.N + n) = narrow8(v);
+}
+
 __device__ __forceinline__ void finish_chunk(const LinearArgs &e, const float *stage, int lane, int64_t m, int64_t n,
                                              const float (&sx)[4], const Ahead &h) {
   if (n >= e.N) return;
@@ -133,30 +161,56 @@ __device__ __forceinline__ void finish_chunk(const LinearArgs &e, const float *s
     if (row >= e.M) break;
     float v[8];
     load8(stage + (lane / 4 + 8 * i) * kPitch + (lane % 4) * 8, v);
-    if (e.x_scale) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= sx[i] * h.scale[j];
-    }
-    if (e.bias) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += h.bias[j];
-    }
-    if (e.pre) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.pre) + row * e.N + n) = narrow8(v);
-    if (e.act != kActNone) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = linear::activate(e.act, v[j]);
-    }
-    if (e.residual) {
-      float q[8];
-      widen8(h.res[i], q);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += q[j];
-    }
-    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.out) + row * e.N + n) = narrow8(v);
+    finish8(e, row, n, v, sx[i], h, h.res[i]);
   }
 }
 
-template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>
+// A tile whose k was shared by `split` CTAs of the cluster, `apart` ranks from
+// one another: each has its float32 sums in its own shared memory ([kBM] rows
+// of BN + 4), and finishes 1 / split of the rows, adding in rank order.
+template <int BN>
+__device__ __forceinline__ void finish_split(const LinearArgs &e, const float *sums, int split, int apart, int rank,
+                                             int64_t m0, int64_t n0, bool aligned) {
+  const int rows = kBM / split, mine = rank / apart, first = rank % apart;
+  for (int i = threadIdx.x; i < rows * (BN / 8); i += kThreads) {
+    const int r = mine * rows + i / (BN / 8), c = i % (BN / 8) * 8;
+    const int64_t row = m0 + r, n = n0 + c;
+    if (row >= e.M || n >= e.N) continue;
+    Ahead h;
+    float sx = 1.f;
+    if (aligned) {
+      LinearArgs one = e;  // the residual of this row alone
+      one.M = row + 1;
+      fetch_ahead(one, row, n, h);
+      if (e.x_scale) sx = e.x_scale[row];
+    }
+    // all parts are asked for before any is added: a read takes about a microsecond
+    float4 a[kMaxSplit], b[kMaxSplit];
+#pragma unroll
+    for (int q = 0; q < kMaxSplit; ++q)
+      if (q < split) {
+        const uint32_t at = map_cluster(sums + r * (BN + 4) + c, first + q * apart);
+        a[q] = ld_cluster_f4(at);
+        b[q] = ld_cluster_f4(at + 16);
+      }
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < kMaxSplit; ++q)
+      if (q < split) {
+        v[0] += a[q].x, v[1] += a[q].y, v[2] += a[q].z, v[3] += a[q].w;
+        v[4] += b[q].x, v[5] += b[q].y, v[6] += b[q].z, v[7] += b[q].w;
+      }
+    if (aligned) {
+      finish8(e, row, n, v, sx, h, h.res[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j < e.N) linear::finish<__nv_bfloat16>(e, row, n + j, v[j]);
+    }
+  }
+}
+
+template <int BN, bool kPair, bool kSplit, bool kAMn, bool kBMn, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, Tiles tiles,
                 LinearArgs epi, bool aligned) {
@@ -169,8 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // swizzle atoms are 1024-byte aligned
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = kPair ? (int)cluster_rank() : 0;      // 0 issues the products
-  const int64_t worker = kPair ? blockIdx.x / 2 : blockIdx.x, workers = kPair ? gridDim.x / 2 : gridDim.x;
+  constexpr int kWide = kPair ? 2 : 1;                   // CTAs of a tile, for one part of k
+  const int crank = kPair || kSplit ? (int)cluster_rank() : 0;
+  const int rank = crank % kWide, lead = crank - rank;   // rank 0 issues the products
+  const int ctas = kSplit ? kWide * tiles.split : kWide;
+  const int64_t worker = blockIdx.x / ctas, workers = gridDim.x / ctas;
+  const int kb0 = kSplit ? crank / kWide * tiles.per : 0;
+  const int kb1 = kSplit && kb0 + tiles.per < tiles.kblocks ? kb0 + tiles.per : tiles.kblocks;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], kPair ? 2 * kEpi : kEpi);
@@ -189,27 +248,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // barriers and TMEM of both CTAs are ready
+  if constexpr (kPair || kSplit) cluster_sync();  // barriers and TMEM of all its CTAs are ready
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
+  // The producer's and the issuer's loops run warp-wide, with one elected lane
+  // issuing: in code that only one lane reaches, the compiler cannot keep
+  // descriptors and addresses in uniform registers.
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&ma);
       tma_prefetch_desc(&mb);
-      int slot = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int64_t i = worker; ok && i < tiles.total; i += workers) {
-        int64_t tm, tn;
-        tile_at(tiles, i, tm, tn);
-        const int m0 = (int)(tm * kTM) + rank * kBM, n0 = (int)(tn * BN) + rank * kBRows;
-        for (int kb = 0; kb < tiles.kblocks; ++kb) {
-          if (!(ok = wait(&sh, &sh.empty[slot], phase ^ 1, 0))) break;
+    }
+    int slot = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t i = worker; ok && i < tiles.total; i += workers) {
+      int64_t tm, tn;
+      tile_at(tiles, i, tm, tn);
+      const int m0 = (int)(tm * kTM) + rank * kBM, n0 = (int)(tn * BN) + rank * kBRows;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = __all_sync(0xffffffffu, wait(&sh, &sh.empty[slot], phase ^ 1, 0)))) break;
+        if (elect_one()) {
           unsigned char *st = base + slot * kStage, *stb = st + kBM * kRowBytes;
           // a pair's copies all count on the leader's barrier
-          const uint32_t bar = kPair ? map_cluster(&sh.full[slot], 0) : 0;
+          const uint32_t bar = kPair ? map_cluster(&sh.full[slot], lead) : 0;
           const auto copy = [&](unsigned char *to, const CUtensorMap *map, int c0, int c1) {
             if constexpr (kPair)
               tma_load_2d_pair(to, map, bar, c0, c1);
@@ -218,33 +282,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], kPair ? 2 * kStage : kStage);
           if constexpr (kAMn) {
+#pragma unroll
             for (int j = 0; j < kBM / 64; ++j) copy(st + j * 8192, &ma, m0 + 64 * j, kb * 64);
           } else {
             copy(st, &ma, kb * kElems, m0);
           }
           if constexpr (kBMn) {
+#pragma unroll
             for (int j = 0; j < kBRows / 64; ++j) copy(stb + j * 8192, &mb, n0 + 64 * j, kb * 64);
           } else {
             copy(stb, &mb, kb * kElems, n0);
           }
-          ++issued;
-          if (++slot == kStages) slot = 0, phase ^= 1;
         }
-      }
-      if (!ok && rank != 0) {  // winding down: this warp's own copies land first
-        for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // (the leader's barrier counts them)
-      } else if (!ok) {
-        for (int64_t i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
-          for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.full[i % kStages], (i / kStages) & 1); ++j) {
-          }
+        __syncwarp();
+        ++issued;
+        if (++slot == kStages) slot = 0, phase ^= 1;
       }
     }
+    if (!ok && rank != 0) {  // winding down: this warp's own copies land first
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // (the leader's barrier counts them)
+    } else if (!ok) {
+      for (int64_t i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
+        for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.full[i % kStages], (i / kStages) & 1); ++j) {
+        }
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t id = kF8 ? idesc_e4m3(kTM, BN) : idesc_bf16(kTM, BN, kAMn, kBMn);
-      const auto commit = [](uint64_t *bar) {
+      const auto commit = [&](uint64_t *bar) {
         if constexpr (kPair)
-          mma_commit_pair(bar);
+          mma_commit_pair(bar, (uint16_t)(3 << lead));
         else
           mma_commit(bar);
       };
@@ -252,39 +319,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, accphase = 0;
       bool ok = true;
       for (int64_t i = worker; ok && i < tiles.total; i += workers) {
-        if (!(ok = wait(&sh, &sh.tempty[acc], accphase ^ 1, 1))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait(&sh, &sh.tempty[acc], accphase ^ 1, 1)))) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
-        for (int kb = 0; kb < tiles.kblocks; ++kb) {
-          if (!(ok = wait(&sh, &sh.full[slot], phase, 1))) break;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = __all_sync(0xffffffffu, wait(&sh, &sh.full[slot], phase, 1)))) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(base + slot * kStage);
-          // k-contiguous operands: a step of 16 (32) elements is 32 bytes of
-          // the 128-byte row; MN-major ones: 16 rows of 128 bytes
-          const uint64_t da = kAMn ? sdesc_sw128(st, 8192, 1024) : sdesc_sw128(st, 0, 1024);
-          const uint64_t db = kBMn ? sdesc_sw128(st + kBM * kRowBytes, 8192, 1024)
-                                   : sdesc_sw128(st + kBM * kRowBytes, 0, 1024);
+          if (elect_one()) {
+            const uint32_t st = smem_u32(base + slot * kStage);
+            // k-contiguous operands: a step of 16 (32) elements is 32 bytes of
+            // the 128-byte row; MN-major ones: 16 rows of 128 bytes
+            const uint64_t da = kAMn ? sdesc_sw128(st, 8192, 1024) : sdesc_sw128(st, 0, 1024);
+            const uint64_t db = kBMn ? sdesc_sw128(st + kBM * kRowBytes, 8192, 1024)
+                                     : sdesc_sw128(st + kBM * kRowBytes, 0, 1024);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t xa = da + (uint64_t)(k * (kAMn ? 2048 : 32) >> 4);
-            const uint64_t xb = db + (uint64_t)(k * (kBMn ? 2048 : 32) >> 4);
-            if constexpr (kPair)
-              mma_ss_pair<kF8>(d, xa, xb, id, kb > 0 || k > 0);
-            else if constexpr (kF8)
-              mma_ss_f8(d, xa, xb, id, kb > 0 || k > 0);
-            else
-              mma_ss(d, xa, xb, id, kb > 0 || k > 0);
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t xa = da + (uint64_t)(k * (kAMn ? 2048 : 32) >> 4);
+              const uint64_t xb = db + (uint64_t)(k * (kBMn ? 2048 : 32) >> 4);
+              if constexpr (kPair)
+                mma_ss_pair<kF8>(d, xa, xb, id, kb > kb0 || k > 0);
+              else if constexpr (kF8)
+                mma_ss_f8(d, xa, xb, id, kb > kb0 || k > 0);
+              else
+                mma_ss(d, xa, xb, id, kb > kb0 || k > 0);
+            }
+            commit(&sh.empty[slot]);
+            if (kb + 1 == kb1) commit(&sh.tfull[acc]);
           }
-          commit(&sh.empty[slot]);
+          __syncwarp();
           if (++slot == kStages) slot = 0, phase ^= 1;
         }
-        if (!ok) break;
-        commit(&sh.tfull[acc]);
         acc ^= 1;
         if (acc == 0) accphase ^= 1;
       }
       if (!ok) {  // products in flight end before TMEM is given back
-        commit(&sh.drain);
+        if (elect_one()) commit(&sh.drain);
         for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.drain, 0); ++j) {
         }
       }
@@ -303,6 +372,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) sx[k] = epi.x_scale && m + 8 * k < epi.M ? epi.x_scale[m + 8 * k] : 1.f;
       const int chunks = (int)(epi.N - n0 < BN ? (epi.N - n0 + 31) / 32 : BN / 32);
+      if constexpr (kSplit) {  // the one tile: its sums to shared memory, where the ring was
+        if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
+        tc_fence_after();
+        float *row = reinterpret_cast<float *>(base) + (quarter * 32 + lane) * (BN + 4);
+        for (int c = half; c < chunks; c += 2) {
+          uint32_t r[32];
+          tmem_ld32(tmem_addr(tmem, quarter * 32, c * 32), r);
+          tmem_wait_ld_regs(r);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(row + c * 32 + 4 * k) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        }
+        break;
+      }
       Ahead next, now;
       if (aligned && half < chunks) fetch_ahead(epi, m, n0 + half * 32 + (lane % 4) * 8, next);
       uint32_t r[32];
@@ -315,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if constexpr (kPair)
-            mbar_arrive_cluster_relaxed(map_cluster(&sh.tempty[acc], 0));
+            mbar_arrive_cluster_relaxed(map_cluster(&sh.tempty[acc], lead));
           else
             mbar_arrive(&sh.tempty[acc]);
         }
@@ -350,7 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // neither CTA leaves while the other may reach into it
+  if constexpr (kSplit) {
+    cluster_sync();
+    int64_t tm, tn;
+    tile_at(tiles, worker, tm, tn);
+    finish_split<BN>(epi, reinterpret_cast<const float *>(base), tiles.split, kWide, crank, tm * kTM + rank * kBM,
+                     tn * BN, aligned);
+  }
+  if constexpr (kPair || kSplit) cluster_sync_relaxed();  // no CTA leaves while another may reach into it
   tc_fence_after();
   if (warp == 1) {
     if constexpr (kPair)
@@ -366,8 +456,8 @@ int sm_count() {
   return n;
 }
 
-template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>
-cudaError_t run(const GemmArgs &g, cudaStream_t s) {
+template <int BN, bool kPair, bool kSplit, bool kAMn, bool kBMn, bool kF8>
+cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
   const int size = kF8 ? 1 : 2;
   const LinearArgs &e = g.epi;
   CUtensorMap ma, mb;
@@ -383,38 +473,69 @@ cudaError_t run(const GemmArgs &g, cudaStream_t s) {
   t.m_tiles = (e.M + kTM - 1) / kTM;
   t.n_tiles = (e.N + BN - 1) / BN;
   t.total = t.m_tiles * t.n_tiles;
+  if (t.total >= (int64_t(1) << 31) / kMaxSplit) return cudaErrorInvalidConfiguration;
   const int elems = kF8 ? 128 : 64;
   t.kblocks = (int)((g.K + elems - 1) / elems);
+  t.per = (t.kblocks + split - 1) / split;
+  t.split = split;
   const auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   const bool aligned = e.N % 8 == 0 && ok(e.out) && ok(e.pre) && ok(e.residual) && (!e.residual || e.ldr % 8 == 0) &&
                        ok(e.bias) && ok(e.w_scale);
-  auto kern = gemm_kernel<BN, kPair, kAMn, kBMn, kF8>;
+  auto kern = gemm_kernel<BN, kPair, kSplit, kAMn, kBMn, kF8>;
   constexpr int smem = smem_bytes(BN, kPair);
   if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
-  const int64_t ctas = kPair ? 2 : 1, fit = sm_count() / ctas;
+  const int64_t ctas = (kPair ? 2 : 1) * split, fit = sm_count() / ctas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((t.total < fit ? t.total : fit) * ctas));
+  // persistent, but for a split product: one cluster a tile
+  cfg.gridDim = dim3((unsigned)((kSplit || t.total < fit ? t.total : fit) * ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.x = (unsigned)ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = kPair ? 1 : 0;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, t, e, aligned);
 }
 
+template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>
+cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
+  return split > 1 ? run<BN, kPair, true, kAMn, kBMn, kF8>(g, split, s)
+                   : run<BN, kPair, false, kAMn, kBMn, kF8>(g, 1, s);
+}
+
+// The tile and the split of k, by an estimate of the time: rounds of tiles over
+// the SMs, blocks of k at the pace at which an SM is fed (about 95 GB/s from
+// L2, whatever the tile), and what a tile and an exchange of sums cost besides.
+// Rows of A past M cost no reads.
 template <bool kAMn, bool kBMn, bool kF8>
 cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
-  // the widest tile that still gives every SM one (a pair's tile counts for
-  // two); below that, narrower tiles spread the work over more SMs
-  const int64_t sms = sm_count();
-  const auto tiles = [&](int bm, int bn) { return ((g.epi.M + bm - 1) / bm) * ((g.epi.N + bn - 1) / bn); };
-  if (2 * tiles(256, 256) >= sms) return run<256, true, kAMn, kBMn, kF8>(g, s);
-  if (tiles(128, 128) >= sms) return run<128, false, kAMn, kBMn, kF8>(g, s);
-  return run<64, false, kAMn, kBMn, kF8>(g, s);
+  const int64_t M = g.epi.M, N = g.epi.N, sms = sm_count();
+  const int kblocks = (int)((g.K + (kF8 ? 127 : 63)) / (kF8 ? 128 : 64));
+  struct Shape { int bn, pair; };
+  constexpr Shape shapes[4] = {{256, 1}, {128, 1}, {128, 0}, {64, 0}};
+  int best = 0, split = 1;
+  double least = 1e30;
+  for (int i = 0; i < 4; ++i) {
+    const int bn = shapes[i].bn, wide = shapes[i].pair ? 2 : 1, bm = kBM * wide;
+    const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+    const double bytes = ((M < kBM ? (double)M : kBM) + b_rows(bn, wide == 2)) * kRowBytes;
+    for (int q = 1; q * wide <= kMaxSplit; q *= 2) {
+      if (q > 1 && (tiles * q * wide > sms || kblocks < 4 * q)) break;
+      if ((q - 1) * ((kblocks + q - 1) / q) >= kblocks) continue;  // every part has blocks
+      const int64_t rounds = (tiles * q * wide + sms - 1) / sms;
+      const double us = (double)rounds * ((kblocks + q - 1) / q * bytes / 95e3 + 1.5) + (q > 1 ? 1.5 : 0.0) + 2.0;
+      if (us < 0.98 * least) least = us, best = i, split = q;
+    }
+  }
+  switch (best) {
+    case 0: return run<256, true, kAMn, kBMn, kF8>(g, split, s);
+    case 1: return run<128, true, kAMn, kBMn, kF8>(g, split, s);
+    case 2: return run<128, false, kAMn, kBMn, kF8>(g, split, s);
+    default: return run<64, false, kAMn, kBMn, kF8>(g, split, s);
+  }
 }
 
 }  // namespace
