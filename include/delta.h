@@ -574,9 +574,9 @@ typedef enum {
  *   out      [M, N]  dtype; may be residual itself (then contiguous)
  *   pre      [M, N]  dtype, for delta_linear_bwd, or NULL
  *
- * K > 0.  bfloat16 runs on the tensor cores: tcgen05 for M > 32, and for
+ * K > 0.  bfloat16 runs on the tensor cores: tcgen05 for M > 16, and for
  * fewer rows a kernel that streams w once.  x or w whose address or row stride
- * is not a multiple of 16 bytes is first copied to scratch (M > 32), taken
+ * is not a multiple of 16 bytes is first copied to scratch (M > 16), taken
  * stream-ordered from the library's pool as delta_fwd does.  float32 runs on
  * the CUDA cores, a correctness path.
  */

@@ -198,7 +198,7 @@ struct GemmArgs {
 cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s);
 cudaError_t read_and_clear_linear_error(unsigned int *word);
 // few rows of x: the weight is streamed once (M <= kLinSmallM)
-constexpr int kLinSmallM = 32;
+constexpr int kLinSmallM = 16;
 cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s);
 // float32 on the CUDA cores, operands with any strides (elements)
 cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, int64_t ak, const float *b,

@@ -23,7 +23,7 @@ bool aligned_to(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p
 // a cluster, where N alone does not fill the GPU) deal out k in blocks of
 // kBlocks 64-byte pieces per row.  The products run on warp-level matrix
 // instructions with w as the 16-row operand and up to 8 NT rows of x as the
-// other: at M <= 32 the 5th-generation units would wait for the same bytes,
+// other: at M <= 16 the 5th-generation units would wait for the same bytes,
 // and here a piece goes from memory to the operand's registers with nothing
 // between.  The instruction's order of k within a block is free as long as
 // both operands share it, so a lane takes 16 neighbouring bytes of its rows.
@@ -258,8 +258,8 @@ int dpre_vec(const DpreArgs &p) {
 
 cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s) {
   if (a.kind == kLinE4m3)
-    return a.M <= 8 ? run_small<true, 1>(a, s) : a.M <= 16 ? run_small<true, 2>(a, s) : run_small<true, 4>(a, s);
-  return a.M <= 8 ? run_small<false, 1>(a, s) : a.M <= 16 ? run_small<false, 2>(a, s) : run_small<false, 4>(a, s);
+    return a.M <= 8 ? run_small<true, 1>(a, s) : run_small<true, 2>(a, s);
+  return a.M <= 8 ? run_small<false, 1>(a, s) : run_small<false, 2>(a, s);
 }
 
 cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, int64_t ak, const float *b,

@@ -165,6 +165,34 @@ __device__ __forceinline__ void finish_chunk(const LinearArgs &e, const float *s
   }
 }
 
+// The same chunk where rows are not whole 16-byte pieces: a lane has one column
+// of all 32 rows, single elements, four rows asked for at a time.
+__device__ __forceinline__ void finish_column(const LinearArgs &e, const float *stage, int lane, int64_t m0, int64_t n) {
+  if (n >= e.N) return;
+  const float bias = linear::bias_at(e, n), sw = e.x_scale ? e.w_scale[n] : 1.f;
+  const int rows = e.M - m0 < 32 ? (int)(e.M - m0) : 32;
+  const __nv_bfloat16 *res = e.residual ? static_cast<const __nv_bfloat16 *>(e.residual) + m0 * e.ldr + n : nullptr;
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + m0 * e.N + n;
+  __nv_bfloat16 *pre = e.pre ? static_cast<__nv_bfloat16 *>(e.pre) + m0 * e.N + n : nullptr;
+#pragma unroll 1
+  for (int k = 0; k < rows; k += 4) {
+    float r[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = k + i < rows;
+      r[i] = in && res ? __bfloat162float(res[(k + i) * e.ldr]) : 0.f;
+      s[i] = in && e.x_scale ? e.x_scale[m0 + k + i] * sw : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k + i < rows) {
+        const float p = stage[(k + i) * kPitch + lane] * s[i] + bias;
+        if (pre) pre[(k + i) * e.N] = __float2bfloat16_rn(p);
+        out[(k + i) * e.N] = __float2bfloat16_rn(linear::activate(e.act, p) + r[i]);
+      }
+  }
+}
+
 // A tile whose k was shared by `split` CTAs of the cluster, `apart` ranks from
 // one another: each has its float32 sums in its own shared memory ([kBM] rows
 // of BN + 4), and finishes 1 / split of the rows, adding in rank order.
@@ -419,9 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (aligned) {
           finish_chunk(epi, stage, lane, m, n0 + c * 32 + (lane % 4) * 8, sx, now);
-        } else if (n0 + c * 32 + lane < epi.N) {
-          for (int k = 0; k < 32 && m0 + k < epi.M; ++k)
-            linear::finish<__nv_bfloat16>(epi, m0 + k, n0 + c * 32 + lane, stage[k * kPitch + lane]);
+        } else {
+          finish_column(epi, stage, lane, m0, n0 + c * 32 + lane);
         }
         __syncwarp();
       }
@@ -506,27 +533,31 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
                    : run<BN, kPair, false, kAMn, kBMn, kF8>(g, 1, s);
 }
 
-// The tile and the split of k, by an estimate of the time: rounds of tiles over
-// the SMs, blocks of k at the pace at which an SM is fed (about 95 GB/s from
-// L2, whatever the tile), and what a tile and an exchange of sums cost besides.
-// Rows of A past M cost no reads.
+// The tile and the split of k, by an estimate of the time.  A block of k takes
+// 512 cycles for a pair's 256 x 256 (the tensor cores' own rate), and for the
+// smaller tiles 300 to 375, what the copies take to issue and land; starting,
+// filling the pipeline and writing out a tile cost about 4 us.  A split adds a
+// turn through shared memory and (q - 1) / q of the tile's sums over the
+// cluster's network, which carries about 20 GB/s a CTA.
 template <bool kAMn, bool kBMn, bool kF8>
 cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
   const int64_t M = g.epi.M, N = g.epi.N, sms = sm_count();
   const int kblocks = (int)((g.K + (kF8 ? 127 : 63)) / (kF8 ? 128 : 64));
-  struct Shape { int bn, pair; };
-  constexpr Shape shapes[4] = {{256, 1}, {128, 1}, {128, 0}, {64, 0}};
+  struct Shape { int bn, pair; double us; };
+  constexpr Shape shapes[4] = {{256, 1, 0.26}, {128, 1, 0.15}, {128, 0, 0.19}, {64, 0, 0.16}};
   int best = 0, split = 1;
   double least = 1e30;
   for (int i = 0; i < 4; ++i) {
     const int bn = shapes[i].bn, wide = shapes[i].pair ? 2 : 1, bm = kBM * wide;
     const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
-    const double bytes = ((M < kBM ? (double)M : kBM) + b_rows(bn, wide == 2)) * kRowBytes;
     for (int q = 1; q * wide <= kMaxSplit; q *= 2) {
-      if (q > 1 && (tiles * q * wide > sms || kblocks < 4 * q)) break;
+      // (of clusters of 8 such CTAs only 15 are resident, of 4 only 36)
+      const int64_t fit = q * wide == 8 ? 15 * 8 : q * wide == 4 ? 36 * 4 : sms;
+      if (q > 1 && (tiles * q * wide > fit || kblocks < 4 * q)) break;
       if ((q - 1) * ((kblocks + q - 1) / q) >= kblocks) continue;  // every part has blocks
       const int64_t rounds = (tiles * q * wide + sms - 1) / sms;
-      const double us = (double)rounds * ((kblocks + q - 1) / q * bytes / 95e3 + 1.5) + (q > 1 ? 1.5 : 0.0) + 2.0;
+      double us = (double)rounds * ((kblocks + q - 1) / q * shapes[i].us + bn * 0.005) + 3.0;
+      if (q > 1) us += 1.3 + kBM * bn * 4 * (q - 1) / q / 20e3;
       if (us < 0.98 * least) least = us, best = i, split = q;
     }
   }
