@@ -198,13 +198,15 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(LinearArgs e, const float
 }
 
 // ----------------------------------------------------------------- gradients
+// a CTA row of 32 threads per matrix row, the widest unit that all rows allow
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(const T *src, T *dst, int64_t rows, int64_t cols, int64_t ld,
                                                    int64_t ldp) {
-  const int64_t n = rows * cols;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cols, c = i - r * cols;
-    dst[r * ldp + c] = src[r * ld + c];
+  for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.y; r < rows; r += (int64_t)gridDim.x * 8) {
+    const T *from = src + r * ld;
+    T *to = dst + r * ldp;
+#pragma unroll 4
+    for (int64_t c = threadIdx.x; c < cols; c += 32) to[c] = from[c];
   }
 }
 
@@ -272,12 +274,23 @@ cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, i
 
 cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, int64_t ldp, int size,
                         cudaStream_t s) {
-  const int64_t want = (rows * cols + 255) / 256, cap = (int64_t)sm_count() * 16;
+  int64_t unit = 8;  // bytes; ldp and dst are whole 16-byte pieces
+  while (unit > size && ((cols * size) % unit || (ld * size) % unit || !aligned_to(src, unit))) unit /= 2;
+  const int64_t want = (rows + 7) / 8, cap = (int64_t)sm_count() * 8;
   const unsigned grid = (unsigned)(want < cap ? want : cap);
-  if (size == 2)
-    pack_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), rows, cols, ld, ldp);
+  const auto go = [&](auto t) {
+    using T = decltype(t);
+    pack_kernel<T><<<grid, dim3(32, 8), 0, s>>>(static_cast<const T *>(src), static_cast<T *>(dst), rows,
+                                                cols * size / unit, ld * size / unit, ldp * size / unit);
+  };
+  if (unit == 8)
+    go(uint64_t{});
+  else if (unit == 4)
+    go(uint32_t{});
+  else if (unit == 2)
+    go(uint16_t{});
   else
-    pack_kernel<<<grid, 256, 0, s>>>(static_cast<const uint8_t *>(src), static_cast<uint8_t *>(dst), rows, cols, ld, ldp);
+    go(uint8_t{});
   return cudaGetLastError();
 }
 

@@ -11,7 +11,11 @@
 //           two TMEM accumulators of 128 x BN;
 //   warps 2-9: epilogue, two to a TMEM lane quarter (32 rows) that take turns
 //           at its columns, while the next tile's products run into the other
-//           accumulator.
+//           accumulator.  A chunk of 32 x 32 is finished as TMEM gives it, a
+//           row a lane, and goes out in 32-byte pieces: whole sectors, though a
+//           lane's rows are apart.  (A turn through shared memory for coalesced
+//           pieces, or for TMA, took its bandwidth from the operands and was
+//           the slower way: 8192 x 4096 outputs at K = 512 in 31 and 34 us.)
 // A large product takes CTAs in pairs (cta_group::2): a tile of 256 x 256 of
 // which each CTA loads 128 rows of either operand, 32 KB a stage.  One CTA
 // alone on 128 x 256 needs 48 KB for the same work, which at full rate is more
@@ -36,7 +40,8 @@ constexpr int kEpi = 8;          // epilogue warps
 constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kBand = 8;
 constexpr int kMaxSplit = 8;    // CTAs that share a tile's k: the portable cluster
-constexpr int kPitch = 36;      // floats a row of an epilogue warp's stage
+constexpr int kPitch = 36;      // floats a row of an epilogue warp's stage (odd row widths)
+constexpr int kEpiBytes = 32 * kPitch * 4;
 constexpr int kRowBytes = 128;  // of k in a stage: 64 bfloat16 or 128 e4m3
 
 // BN: columns of a tile; a pair's CTA loads half of B's rows
@@ -44,8 +49,7 @@ __host__ __device__ constexpr int b_rows(int BN, bool pair) { return pair ? BN /
 __host__ __device__ constexpr int stage_bytes(int BN, bool pair) { return (kBM + b_rows(BN, pair)) * kRowBytes; }
 __host__ __device__ constexpr int stages(int BN, bool pair) { return pair || BN == 128 ? 5 : 7; }
 __host__ __device__ constexpr int smem_bytes(int BN, bool pair) {
-  // ring, and the epilogue warps' stages
-  return 1024 + stages(BN, pair) * stage_bytes(BN, pair) + kEpi * 32 * kPitch * 4;
+  return 1024 + stages(BN, pair) * stage_bytes(BN, pair) + kEpi * kEpiBytes;
 }
 
 struct Shared {
@@ -81,18 +85,6 @@ __device__ __forceinline__ void tile_at(const Tiles &t, int64_t i, int64_t &m, i
   n = down;
 }
 
-// The epilogue of a warp's 32 rows, 32 columns at a time.  TMEM gives a lane
-// one row; a turn through shared memory gives it 8 neighbouring columns of
-// every eighth row instead, so that every global access is a whole 64-byte
-// piece of a row, the bias and the column scales stay in registers over the
-// rows, and the residual can be asked for a chunk ahead.  The pitch of 36
-// floats keeps both sides free of bank conflicts.
-
-struct Ahead {  // what a chunk needs from global memory
-  uint4 res[4];
-  float bias[8], scale[8];
-};
-
 __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
   const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -109,59 +101,113 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
-// lane's columns start at n, its rows at m, 8 apart
-__device__ __forceinline__ void fetch_ahead(const LinearArgs &e, int64_t m, int64_t n, Ahead &h) {
-  if (n >= e.N) return;
-  if (e.residual) {
+// 8 columns of a row before the activation: scales and bias
+__device__ __forceinline__ void raise8(const LinearArgs &e, int64_t n, float (&v)[8], float sx) {
+  float q[8];
+  if (e.x_scale) {
+    load8(e.w_scale + n, q);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (m + 8 * i < e.M)
-        h.res[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.residual) + (m + 8 * i) * e.ldr + n);
+    for (int j = 0; j < 8; ++j) v[j] *= sx * q[j];
   }
   if (e.bias) {
     if (e.bias_bf16)
-      widen8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.bias) + n), h.bias);
+      widen8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.bias) + n), q);
     else
-      load8(static_cast<const float *>(e.bias) + n, h.bias);
+      load8(static_cast<const float *>(e.bias) + n, q);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += q[j];
   }
-  if (e.x_scale) load8(e.w_scale + n, h.scale);
 }
-
-// 8 columns of one row, start to end
-__device__ __forceinline__ void finish8(const LinearArgs &e, int64_t row, int64_t n, float (&v)[8], float sx,
-                                        const Ahead &h, const uint4 &res) {
-  if (e.x_scale) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= sx * h.scale[j];
-  }
-  if (e.bias) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += h.bias[j];
-  }
-  if (e.pre) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.pre) + row * e.N + n) = narrow8(v);
+__device__ __forceinline__ void activate8(const LinearArgs &e, float (&v)[8]) {
   if (e.act != kActNone) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = linear::activate(e.act, v[j]);
   }
-  if (e.residual) {
-    float q[8];
-    widen8(res, q);
+}
+__device__ __forceinline__ void add8(float (&v)[8], const uint4 &res) {
+  float q[8];
+  widen8(res, q);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += q[j];
-  }
-  *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.out) + row * e.N + n) = narrow8(v);
+  for (int j = 0; j < 8; ++j) v[j] += q[j];
 }
 
-__device__ __forceinline__ void finish_chunk(const LinearArgs &e, const float *stage, int lane, int64_t m, int64_t n,
-                                             const float (&sx)[4], const Ahead &h) {
-  if (n >= e.N) return;
+// 16 neighbouring elements of a row: one 32-byte access, or two of 16 bytes
+struct Half {
+  uint4 a, b;
+};
+__device__ __forceinline__ Half load16(const __nv_bfloat16 *p, bool wide) {
+  Half h;
+  if (wide)
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(h.a.x), "=r"(h.a.y), "=r"(h.a.z), "=r"(h.a.w), "=r"(h.b.x), "=r"(h.b.y), "=r"(h.b.z), "=r"(h.b.w)
+                 : "l"(p)
+                 : "memory");
+  else
+    h.a = *reinterpret_cast<const uint4 *>(p), h.b = *reinterpret_cast<const uint4 *>(p + 8);
+  return h;
+}
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const uint4 &a, const uint4 &b, bool wide) {
+  if (wide)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  else
+    *reinterpret_cast<uint4 *>(p) = a, *reinterpret_cast<uint4 *>(p + 8) = b;
+}
+
+// A row's 32 residuals of a chunk; the columns past N (a multiple of 8) are not
+// read.
+struct Residual {
+  Half h[2];
+};
+__device__ __forceinline__ void ask_residual(const LinearArgs &e, int64_t m, int64_t n0, bool wide, Residual &r) {
+  if (!e.residual || m >= e.M) return;
+  const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(e.residual) + m * e.ldr + n0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = m + 8 * i;
-    if (row >= e.M) break;
-    float v[8];
-    load8(stage + (lane / 4 + 8 * i) * kPitch + (lane % 4) * 8, v);
-    finish8(e, row, n, v, sx[i], h, h.res[i]);
+  for (int k = 0; k < 2; ++k) {
+    if (n0 + 16 * k + 16 <= e.N)
+      r.h[k] = load16(p + 16 * k, wide);
+    else if (n0 + 16 * k + 8 <= e.N)
+      r.h[k].a = *reinterpret_cast<const uint4 *>(p + 16 * k);
+  }
+}
+
+// One chunk of one row, start to end.  cols: the chunk's biases and column
+// scales in shared memory, [2][32].
+__device__ __forceinline__ void finish_row(const LinearArgs &e, int64_t m, int64_t n0, uint32_t (&r)[32], float sx,
+                                           const float *cols, const Residual &res, bool wide) {
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + m * e.N + n0;
+  __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(e.pre) + m * e.N + n0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint4 po[2], pp[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float v[8], q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[16 * k + 8 * g + i]);
+      if (e.x_scale) {
+        load8(cols + 32 + 16 * k + 8 * g, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= sx * q[i];
+      }
+      if (e.bias) {
+        load8(cols + 16 * k + 8 * g, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += q[i];
+      }
+      pp[g] = narrow8(v);
+      activate8(e, v);
+      if (e.residual) add8(v, g ? res.h[k].b : res.h[k].a);
+      po[g] = narrow8(v);
+    }
+    if (n0 + 16 * k + 16 <= e.N) {
+      if (e.pre) store16(pre + 16 * k, pp[0], pp[1], wide);
+      store16(out + 16 * k, po[0], po[1], wide);
+    } else if (n0 + 16 * k + 8 <= e.N) {
+      if (e.pre) *reinterpret_cast<uint4 *>(pre + 16 * k) = pp[0];
+      *reinterpret_cast<uint4 *>(out + 16 * k) = po[0];
+    }
   }
 }
 
@@ -204,14 +250,9 @@ __device__ __forceinline__ void finish_split(const LinearArgs &e, const float *s
     const int r = mine * rows + i / (BN / 8), c = i % (BN / 8) * 8;
     const int64_t row = m0 + r, n = n0 + c;
     if (row >= e.M || n >= e.N) continue;
-    Ahead h;
-    float sx = 1.f;
-    if (aligned) {
-      LinearArgs one = e;  // the residual of this row alone
-      one.M = row + 1;
-      fetch_ahead(one, row, n, h);
-      if (e.x_scale) sx = e.x_scale[row];
-    }
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (aligned && e.residual)
+      res = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.residual) + row * e.ldr + n);
     // all parts are asked for before any is added: a read takes about a microsecond
     float4 a[kMaxSplit], b[kMaxSplit];
 #pragma unroll
@@ -229,7 +270,11 @@ __device__ __forceinline__ void finish_split(const LinearArgs &e, const float *s
         v[4] += b[q].x, v[5] += b[q].y, v[6] += b[q].z, v[7] += b[q].w;
       }
     if (aligned) {
-      finish8(e, row, n, v, sx, h, h.res[0]);
+      raise8(e, n, v, e.x_scale ? e.x_scale[row] : 1.f);
+      if (e.pre) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.pre) + row * e.N + n) = narrow8(v);
+      activate8(e, v);
+      if (e.residual) add8(v, res);
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(e.out) + row * e.N + n) = narrow8(v);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -240,8 +285,8 @@ __device__ __forceinline__ void finish_split(const LinearArgs &e, const float *s
 
 template <int BN, bool kPair, bool kSplit, bool kAMn, bool kBMn, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, Tiles tiles,
-                LinearArgs epi, bool aligned) {
+    gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                Tiles tiles, LinearArgs epi, bool aligned, bool wide) {
   constexpr int kStages = stages(BN, kPair), kStage = stage_bytes(BN, kPair), kBRows = b_rows(BN, kPair);
   constexpr int kTM = kPair ? 2 * kBM : kBM;             // rows of a tile
   constexpr int kElems = kF8 ? 128 : 64;                 // of k in a stage
@@ -389,34 +434,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
     const int half = (warp - 2) / 4;  // of the columns: every second chunk of 32
-    float *stage = reinterpret_cast<float *>(base + kStages * kStage) + (warp - 2) * 32 * kPitch;
+    float *stage = reinterpret_cast<float *>(base + kStages * kStage + (warp - 2) * kEpiBytes);
     int acc = 0;
     uint32_t accphase = 0;
     for (int64_t i = worker; i < tiles.total; i += workers) {
       int64_t tm, tn;
       tile_at(tiles, i, tm, tn);
-      const int64_t m0 = tm * kTM + rank * kBM + quarter * 32, m = m0 + lane / 4, n0 = tn * BN;
-      float sx[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sx[k] = epi.x_scale && m + 8 * k < epi.M ? epi.x_scale[m + 8 * k] : 1.f;
+      const int64_t m0 = tm * kTM + rank * kBM + quarter * 32, m = m0 + lane, n0 = tn * BN;
       const int chunks = (int)(epi.N - n0 < BN ? (epi.N - n0 + 31) / 32 : BN / 32);
-      if constexpr (kSplit) {  // the one tile: its sums to shared memory, where the ring was
-        if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
-        tc_fence_after();
-        float *row = reinterpret_cast<float *>(base) + (quarter * 32 + lane) * (BN + 4);
-        for (int c = half; c < chunks; c += 2) {
-          uint32_t r[32];
-          tmem_ld32(tmem_addr(tmem, quarter * 32, c * 32), r);
-          tmem_wait_ld_regs(r);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4 *>(row + c * 32 + 4 * k) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+      // what a chunk needs from memory is asked for a chunk ahead; a lane has
+      // the bias and scale of one column, which shared memory hands to all
+      const bool rows = aligned && !kSplit;
+      float sx = 1.f, bias = 0.f, sw = 0.f;
+      Residual now, next;
+      const auto ask = [&](int c) {
+        if (!rows || c >= chunks) return;
+        ask_residual(epi, m, n0 + c * 32, wide, next);
+        const int64_t n = n0 + c * 32 + lane;
+        if (n < epi.N) {
+          bias = linear::bias_at(epi, n);
+          if (epi.x_scale) sw = epi.w_scale[n];
         }
-        break;
-      }
-      Ahead next, now;
-      if (aligned && half < chunks) fetch_ahead(epi, m, n0 + half * 32 + (lane % 4) * 8, next);
-      uint32_t r[32];
+      };
+      if (rows && epi.x_scale && m < epi.M) sx = epi.x_scale[m];
+      ask(half);
       if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
       tc_fence_after();
       // this warp's part of the accumulator has been read: the products may
@@ -431,23 +472,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sh.tempty[acc]);
         }
       };
-      if (half < chunks) tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + half * 32), r);
+      uint32_t r[32];
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
-        now = next;
-        if (aligned && c + 2 < chunks) fetch_ahead(epi, m, n0 + (c + 2) * 32 + (lane % 4) * 8, next);
+        tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + c * 32), r);
+        if (rows) {
+          if (epi.bias) stage[lane] = bias;
+          if (epi.x_scale) stage[32 + lane] = sw;
+          __syncwarp();
+          now = next;
+          ask(c + 2);
+        }
         tmem_wait_ld_regs(r);
         if (c + 2 >= chunks) release();
+        if constexpr (kSplit) {  // the one tile: its sums to shared memory, where the ring was
+          float *row = reinterpret_cast<float *>(base) + (quarter * 32 + lane) * (BN + 4) + c * 32;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4 *>(stage + lane * kPitch + 4 * k) =
-              make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-        // the next chunk comes out of TMEM while this one is finished
-        if (c + 2 < chunks) tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + (c + 2) * 32), r);
-        __syncwarp();
-        if (aligned) {
-          finish_chunk(epi, stage, lane, m, n0 + c * 32 + (lane % 4) * 8, sx, now);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(row + 4 * k) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        } else if (aligned) {
+          if (m < epi.M) finish_row(epi, m, n0 + c * 32, r, sx, stage, now, wide);
         } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(stage + lane * kPitch + 4 * k) =
+                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          __syncwarp();
           finish_column(epi, stage, lane, m0, n0 + c * 32 + lane);
         }
         __syncwarp();
@@ -508,6 +558,9 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
   const auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   const bool aligned = e.N % 8 == 0 && ok(e.out) && ok(e.pre) && ok(e.residual) && (!e.residual || e.ldr % 8 == 0) &&
                        ok(e.bias) && ok(e.w_scale);
+  const auto ok32 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };
+  const bool wide = aligned && e.N % 16 == 0 && ok32(e.out) && ok32(e.pre) && ok32(e.residual) &&
+                    (!e.residual || e.ldr % 16 == 0);
   auto kern = gemm_kernel<BN, kPair, kSplit, kAMn, kBMn, kF8>;
   constexpr int smem = smem_bytes(BN, kPair);
   if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
@@ -524,7 +577,7 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, t, e, aligned);
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, t, e, aligned, wide);
 }
 
 template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>
