@@ -5,6 +5,9 @@
 
 Bindings over the C ABI of ``libdelta.so`` with the ABI's names: argument
 checks, output allocation, the current CUDA stream, statuses as exceptions.
+The common case (plain CUDA tensors that fit, outputs to be allocated, the
+current stream) is taken by the compiled module ``_fast``; what that does not
+take is checked and called here, with the same results.
 With ``stream=`` the outputs are allocated for that stream; inputs made on
 another stream are the caller's to order and to keep, as with any kernel.
 """
@@ -53,6 +56,34 @@ def _lib():
     lib = load_library()
     _lib = lambda: lib  # noqa: E731  (the library stays open for the process)
     return lib
+
+
+class _Nothing:
+    """Stands for ``_fast`` where it was not built."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
+
+_fast = None
+
+
+def _open_fast():
+    global _fast
+    _lib()
+    try:
+        from . import _fast as module
+    except ImportError:
+        module = _Nothing()
+    _fast = module
+    return module
+
+
+def _checked(r):
+    """The compiled module's answer: outputs, or a status to raise."""
+    if type(r) is int:
+        _raise(r)
+    return r
 
 
 def _raise(st):
@@ -155,6 +186,11 @@ def delta_scan_fwd(x, gate, h0=None, *, form="sigmoid", lengths=None, save_state
     with ``save_states`` the states [B, ceil(T/64), D] that ``delta_scan_bwd``
     takes.  ``hT`` may be ``h0`` to update the state in place.
     """
+    if stream is None and out is None and hT is None:
+        r = (_fast or _open_fast()).scan_fwd(x, gate, h0, lengths, save_states,
+                                             _SCAN_FORMS.get(form, -1))
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev = _begin(x, "delta_scan_fwd", 3)
     B, T, D = x.shape
     fcode, gdt = _scan_form(form, x.dtype)
@@ -177,6 +213,10 @@ def delta_scan_fwd(x, gate, h0=None, *, form="sigmoid", lengths=None, save_state
 def delta_scan_step(x, gate, state, *, form="sigmoid", out=None, stream=None):
     """One step of the recurrence: x, gate [B,D] (rows may be strided), state
     [B,D] float32 updated in place.  Returns out [B,D] in x's type."""
+    if stream is None and out is None:
+        r = (_fast or _open_fast()).scan_step(x, gate, state, _SCAN_FORMS.get(form, -1))
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev = _begin(x, "delta_scan_step", 2)
     B, D = x.shape
     fcode, gdt = _scan_form(form, x.dtype)
@@ -196,6 +236,11 @@ def delta_scan_bwd(x, gate, states, dout, dhT=None, *, form="sigmoid", lengths=N
     it saved, dout [B,T,D] contiguous in x's type, dhT [B,D] float32 or None.
     Returns ``(dx, dgate, dh0)``: dx in x's type, dgate in gate's, dh0 float32.
     """
+    if stream is None:
+        r = (_fast or _open_fast()).scan_bwd(x, gate, states, dout, dhT, lengths,
+                                             _SCAN_FORMS.get(form, -1))
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev = _begin(x, "delta_scan_bwd", 3)
     B, T, D = x.shape
     fcode, gdt = _scan_form(form, x.dtype)
@@ -262,6 +307,10 @@ def delta_add_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, sum_out=None, s
     rounded to it (x itself without a residual), rstd [...] float32.
     ``sum_out`` may be ``x`` or ``residual`` to update the stream in place.
     """
+    if stream is None and sum_out is None:
+        r = (_fast or _open_fast()).norm_fwd(x, weight, residual, eps, False)
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
                                                                  "delta_add_rmsnorm_fwd")
     y = _empty(x.shape, x.dtype, dev, stream)
@@ -281,6 +330,10 @@ def delta_add_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, sum_out=None, s
 def delta_add_rmsnorm_quant(x, weight, residual=None, *, eps=1e-6, sum_out=None, stream=None):
     """The same with y in e4m3 and one float32 scale a row (max |y| / 448; 1
     for a row of zeros).  Returns ``(y float8_e4m3fn, scale [...], sum)``."""
+    if stream is None and sum_out is None:
+        r = (_fast or _open_fast()).norm_fwd(x, weight, residual, eps, True)
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
                                                                  "delta_add_rmsnorm_quant")
     y = _empty(x.shape, E4M3, dev, stream)
@@ -302,6 +355,10 @@ def delta_add_rmsnorm_bwd(dy, sum, weight, rstd, dsum=None, *, dx=None, stream=N
     (contiguous, one type), rstd, and dsum, the gradient that arrives at sum,
     or None.  Returns ``(dx, dweight)``: dx (of x and of residual alike) in
     dy's type, dweight [D] float32.  ``dx`` may be ``dy`` or ``dsum``."""
+    if stream is None and dx is None:
+        r = (_fast or _open_fast()).norm_bwd(dy, sum, weight, rstd, dsum)
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev = _begin(dy, "delta_add_rmsnorm_bwd", 0, "dy")
     if dy.dim() < 1:
         raise ValueError("dy must have at least one axis")
@@ -348,6 +405,10 @@ def delta_linear_fwd(x, w, bias=None, residual=None, *, act="none", save_pre=Fal
     "silu" or "gelu" (tanh form).  Returns out [..., N], with ``save_pre``
     ``(out, pre)`` for ``delta_linear_bwd``.  ``out`` may be ``residual``.
     """
+    if stream is None and out is None:
+        r = (_fast or _open_fast()).linear_fwd(x, w, bias, residual, _ACTS.get(act, -1), save_pre)
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev = _begin(x, "delta_linear_fwd", 0)
     dt = x.dtype
     acode, M, N, K, px, ldx, pw, ldw, pb, bcode, pr, ldr, shape = _linear_begin(
@@ -367,6 +428,11 @@ def delta_linear_quant(x, x_scale, w, w_scale, bias=None, residual=None, *, act=
     """The same with x [..., K] and w [N, K] in float8_e4m3fn and a float32 scale
     for each of their rows, x_scale [...] and w_scale [N]; residual and out are
     bfloat16."""
+    if stream is None and out is None:
+        r = (_fast or _open_fast()).linear_quant(x, x_scale, w, w_scale, bias, residual,
+                                                 _ACTS.get(act, -1))
+        if r is not NotImplemented:
+            return _checked(r)
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     dev = x.device
@@ -388,6 +454,10 @@ def delta_linear_bwd(x, w, dout, pre=None, *, act="none", want=(True, True, True
     """Gradients of ``delta_linear_fwd``: x and w as there, dout and pre [..., N]
     contiguous (pre only with an activation).  Returns ``(dx, dw, dbias)``, dx
     and dw in x's type, dbias float32; those not wanted are None."""
+    if stream is None:
+        r = (_fast or _open_fast()).linear_bwd(x, w, dout, pre, _ACTS.get(act, -1), *want)
+        if r is not NotImplemented:
+            return _checked(r)
     code, dev = _begin(x, "delta_linear_bwd", 0)
     dt = x.dtype
     acode, M, N, K, px, ldx, pw, ldw, _, _, _, _, shape = _linear_begin(

@@ -6,6 +6,12 @@ statically and the driver API is reached at run time through
 ``cudaGetDriverEntryPoint``, so the library loads on a machine without a GPU
 (it only fails when asked to compute).
 
+``csrc/binding.cpp``, the Python calls of the block operators' common case, is
+compiled by the host compiler against PyTorch's headers and linked to the
+library.  Where that fails the package works without it (its calls then go
+through ctypes alone, which costs a small call about 10 us more), so a failure
+is reported and not raised.
+
     python -m weight_rnn_gb300.build [--force] [-v]
 """
 from __future__ import annotations
@@ -23,6 +29,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdelta.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", "-I", os.path.join(ROOT, "include")]
@@ -53,6 +61,39 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_command(obj):
+    """How to compile binding.cpp, or None where there is nothing to do it with."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return None
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if not cxx:
+        return None
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    where = os.path.join(os.path.dirname(torch.__file__), "include")
+    return [cxx, "-O2", "-std=c++17", "-fPIC",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", where, "-I", os.path.join(where, "torch", "csrc", "api", "include"),
+            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+            "-c", BINDING_SRC, "-o", obj]
+
+
+def link_binding(obj):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    # torch's libraries are in the process before this one is loaded
+    cmd = [os.environ.get("CXX") or shutil.which("g++"), "-shared", "-o", tmp, obj,
+           "-L", PKG, "-l:libdelta.so", "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python",
+           "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(r.stdout + r.stderr)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile and link; returns the path of libdelta.so."""
     os.makedirs(BUILD, exist_ok=True)
@@ -69,12 +110,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
+    bobj = os.path.join(BUILD, "binding.o")
+    bcmd = None
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "delta.h")]):
+        bcmd = binding_command(bobj)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
     failed = []
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        bjob = ex.submit(run, bcmd) if bcmd else None
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
@@ -89,6 +136,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB)
+    if bjob is not None:
+        r = bjob.result()[1]
+        try:
+            if r.returncode != 0:
+                raise RuntimeError(r.stdout + r.stderr)
+            link_binding(bobj)
+        except RuntimeError as e:
+            sys.stderr.write(f"binding.cpp was not built; calls go through ctypes alone:\n{e}\n")
     return LIB
 
 
