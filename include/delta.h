@@ -574,11 +574,11 @@ typedef enum {
  *   out      [M, N]  dtype; may be residual itself (then contiguous)
  *   pre      [M, N]  dtype, for delta_linear_bwd, or NULL
  *
- * K > 0.  bfloat16 runs on the tensor cores: tcgen05 for M > 16, and for
- * fewer rows a kernel that streams w once.  x or w whose address or row stride
- * is not a multiple of 16 bytes is first copied to scratch (M > 16), taken
- * stream-ordered from the library's pool as delta_fwd does.  float32 runs on
- * the CUDA cores, a correctness path.
+ * K > 0.  bfloat16 runs on the tensor cores: on tcgen05, or, for up to 16 rows
+ * and for small products, in a kernel that streams w.  For tcgen05, x or w
+ * whose address or row stride is not a multiple of 16 bytes is first copied to
+ * scratch, taken stream-ordered from the library's pool as delta_fwd does.
+ * float32 runs on the CUDA cores, a correctness path.
  */
 int delta_linear_fwd(const void *x, const void *w, const void *bias, const void *residual, void *out, void *pre,
                      int M, int N, int K, int64_t ldx, int64_t ldw, int64_t ldr, delta_act act,

@@ -64,7 +64,9 @@ def check(out, pre, x, w, b, res, act, scales=None):
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1000, 4096), (3, 17, 7), (8, 128, 200), (9, 100, 1024), (16, 257, 72),
           (17, 513, 130), (31, 40, 513), (32, 2048, 512), (33, 64, 64), (64, 65, 8), (100, 257, 63),
           (127, 8, 1000), (129, 300, 65), (300, 520, 1000), (257, 1024, 2048),
-          (40, 131, 700), (520, 72, 1500), (200, 900, 4096), (90, 2000, 530)]
+          (40, 131, 700), (520, 72, 1500), (200, 900, 4096), (90, 2000, 530),
+          # past the small products: odd rows to pack, odd widths to store, k split with both
+          (700, 333, 401), (260, 1003, 300), (3000, 257, 129), (128, 4096, 257), (40, 1999, 1001)]
 
 
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
@@ -164,10 +166,10 @@ def test_gradients_bf16(shape, act):
     assert part[0] is None and part[2] is None and torch.equal(part[1], got[1])
 
 
-@pytest.mark.parametrize("M", [5, 150])
+@pytest.mark.parametrize("M,N", [(5, 72), (150, 72), (1500, 520)])
 @pytest.mark.parametrize("extra", [1, 8, 24])
-def test_strided_rows_read_nothing_beside_them(M, extra):
-    N, K = 72, 136
+def test_strided_rows_read_nothing_beside_them(M, N, extra):
+    K = 136
     x, w, b, res, do = inputs(M, N, K, BF, 21)
     xp, wp, rp = pad(x, extra), pad(w, extra), pad(res, extra)
     out, pre = wr.delta_linear_fwd(xp, wp, b.cuda(), rp, act="silu", save_pre=True)
@@ -182,7 +184,7 @@ def test_strided_rows_read_nothing_beside_them(M, extra):
     check(out, None, q.float(), k.float(), None, None, "silu", (sx, sw))
 
 
-@pytest.mark.parametrize("M", [4, 200])
+@pytest.mark.parametrize("M", [4, 200, 6000])
 def test_in_place_residual_and_leading_axes(M):
     x, w, b, res, _ = inputs(2 * M, 64, 128, BF, 5)
     stream = res.cuda().view(2, M, 64)
@@ -193,7 +195,7 @@ def test_in_place_residual_and_leading_axes(M):
 
 
 def test_nan_and_infinity_stay_in_their_rows():
-    for M in (8, 160):
+    for M in (8, 160, 6000):
         x, w, b, res, _ = inputs(M, 96, 160, BF, 6)
         x[2, 3], x[5, 100] = float("nan"), float("inf")
         out = wr.delta_linear_fwd(x.cuda(), w.cuda(), b.cuda(), res.cuda(), act="silu")
@@ -225,8 +227,9 @@ def test_gradient_against_differences_of_the_kernel():
         assert abs(num - ana) <= 35.0
 
 
-def test_graph_and_side_stream():
-    x, w, b, res, do = (t.cuda() for t in inputs(300, 200, 72, BF, 10))
+@pytest.mark.parametrize("M,N", [(300, 200), (3000, 400)])
+def test_graph_and_side_stream(M, N):
+    x, w, b, res, do = (t.cuda() for t in inputs(M, N, 72, BF, 10))
     want = wr.delta_linear_fwd(x, w, b, res, act="silu", save_pre=True)
     wgrad = wr.delta_linear_bwd(x, w, do, want[1], act="silu")
     small = wr.delta_linear_fwd(x[:2], w, b, res[:2], act="silu")

@@ -206,6 +206,13 @@ cudaError_t linear_forward(const delta::LinearArgs &a, cudaStream_t s) {
   if (a.M <= delta::kLinSmallM) return delta::launch_linear_small(a, s);
   const int size = a.kind == delta::kLinE4m3 ? 1 : 2;
   Operand x = operand(a.x, a.M, a.K, a.ldx, size), w = operand(a.w, a.N, a.K, a.ldw, size);
+  // Small products take the streaming kernel too, with a pass over w for every
+  // 16 rows: up to about 70 M multiplications that is shorter than filling the
+  // tensor cores' pipeline (M64 N2048 K512 in 4.2 us for 5.2, M128 N2048 K512 in
+  // 6.7 for 5.3) and than packing operands first (M93 N133 K473 in 4.0 for 17).
+  // Rows of 8-bit elements at odd addresses come a byte at a time: 12 M.
+  const int64_t few = int64_t(size == 1 && !(x.whole() && w.whole()) ? 12 : 70) * 1000000;
+  if (a.M * a.N <= few / a.K) return delta::launch_linear_small(a, s);
   Scratch scr(s);
   if (!x.whole()) scr.want(x.bytes());
   if (!w.whole()) scr.want(w.bytes());

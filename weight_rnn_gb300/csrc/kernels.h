@@ -197,7 +197,7 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s);
 cudaError_t read_and_clear_linear_error(unsigned int *word);
-// few rows of x: the weight is streamed once (M <= kLinSmallM)
+// streams the weight once for every 16 rows of x: for M <= kLinSmallM once
 constexpr int kLinSmallM = 16;
 cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s);
 // float32 on the CUDA cores, operands with any strides (elements)

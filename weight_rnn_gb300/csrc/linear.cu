@@ -27,9 +27,12 @@ bool aligned_to(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p
 // and here a piece goes from memory to the operand's registers with nothing
 // between.  The instruction's order of k within a block is free as long as
 // both operands share it, so a lane takes 16 neighbouring bytes of its rows.
-// Partial sums meet in shared memory and in rank 0 in a fixed order.
+// The next turn's pieces are asked for before this one's products (M1 N8192
+// K4096 bfloat16: 12.2 us, 5.5 TB/s; without, at four pieces a turn, 13.3).
+// Partial sums meet in shared memory and in rank 0 in a fixed order.  More
+// rows of x than 8 NT take the grid's second axis, each its own pass over w.
 constexpr int kSmallWarps = 8;
-constexpr int kBlocks = 4;
+constexpr int kBlocks = 2;
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
-  const int64_t n0 = (int64_t)(blockIdx.x / cs) * 16;
+  const int64_t n0 = (int64_t)(blockIdx.x / cs) * 16, m0 = (int64_t)blockIdx.y * kTok;
   if (cs > 1) cg::this_cluster().barrier_arrive();
   const int64_t bytes = a.K * kSize;
   // rows past the end repeat the last one; their results are not stored
@@ -82,19 +85,28 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
   const uint8_t *x[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
-    x[i] = static_cast<const uint8_t *>(a.x) + (8 * i + g < a.M ? 8 * i + g : a.M - 1) * a.ldx * kSize;
+    x[i] = static_cast<const uint8_t *>(a.x) + (m0 + 8 * i + g < a.M ? m0 + 8 * i + g : a.M - 1) * a.ldx * kSize;
   float c[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
 
   constexpr int64_t kSpan = kBlocks * 64;  // bytes of a row per turn
-  for (int64_t k0 = (rank * kSmallWarps + warp) * kSpan; k0 < bytes; k0 += kSpan * kSmallWarps * cs) {
-    uint4 u0[kBlocks], u1[kBlocks];
+  const int64_t step = kSpan * kSmallWarps * cs;
+  int64_t k0 = (rank * kSmallWarps + warp) * kSpan;
+  uint4 next0[kBlocks], next1[kBlocks];
+  const auto ask = [&](int64_t k) {
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j) {
-      u0[j] = piece<kVec, kSize, true>(w0, k0 + j * 64 + t * 16, bytes);
-      u1[j] = piece<kVec, kSize, true>(w1, k0 + j * 64 + t * 16, bytes);
+      next0[j] = piece<kVec, kSize, true>(w0, k + j * 64 + t * 16, bytes);
+      next1[j] = piece<kVec, kSize, true>(w1, k + j * 64 + t * 16, bytes);
     }
+  };
+  ask(k0);
+  for (; k0 < bytes; k0 += step) {
+    uint4 u0[kBlocks], u1[kBlocks];
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) u0[j] = next0[j], u1[j] = next1[j];
+    ask(k0 + step);
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
@@ -125,8 +137,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
     for (int w = 0; w < kSmallWarps; ++w) s += part[w][r][tok];
     if (cs > 1)
       cg::this_cluster().map_shared_rank(&ranks[rank][0], 0)[i] = s;
-    else if (tok < a.M && n0 + r < a.N)
-      finish<__nv_bfloat16>(a, tok, n0 + r, s);
+    else if (m0 + tok < a.M && n0 + r < a.N)
+      finish<__nv_bfloat16>(a, m0 + tok, n0 + r, s);
   }
   if (cs > 1) {
     cg::this_cluster().sync();
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
         const int r = i & 15, tok = i >> 4;
         float s = 0.f;
         for (int q = 0; q < cs; ++q) s += ranks[q][i];
-        if (tok < a.M && n0 + r < a.N) finish<__nv_bfloat16>(a, tok, n0 + r, s);
+        if (m0 + tok < a.M && n0 + r < a.N) finish<__nv_bfloat16>(a, m0 + tok, n0 + r, s);
       }
   }
 }
@@ -145,11 +157,11 @@ cudaError_t run_small(const LinearArgs &a, cudaStream_t s) {
   const int64_t size = kF8 ? 1 : 2, e = 16 / size;
   const bool vec = a.K % e == 0 && a.ldx % e == 0 && a.ldw % e == 0 && aligned_to(a.x, 16) && aligned_to(a.w, 16);
   // CTAs along k until every SM has two, as far as k has a turn for each warp
-  const int64_t groups = (a.N + 15) / 16, turns = (a.K * size + kBlocks * 64 - 1) / (kBlocks * 64);
+  const int64_t groups = (a.N + 15) / 16, passes = (a.M + 8 * NT - 1) / (8 * NT), turns = (a.K * size + kBlocks * 64 - 1) / (kBlocks * 64);
   int cs = 1;
-  while (cs < kMaxCluster && groups * cs < 2 * sm_count() && turns > (int64_t)kSmallWarps * cs) cs *= 2;
+  while (cs < kMaxCluster && groups * passes * cs < 2 * sm_count() && turns > (int64_t)kSmallWarps * cs) cs *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * cs));
+  cfg.gridDim = dim3((unsigned)(groups * cs), (unsigned)passes);
   cfg.blockDim = dim3(kSmallWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
