@@ -68,7 +68,7 @@ def test_forward_and_gradients(shape, dtype, form):
 
 # enough rows and strips that one CTA walks each alone, and few enough that
 # clusters of every size split the time axis
-@pytest.mark.parametrize("B,T,D", [(40, 200, 520), (12, 300, 512), (5, 300, 512), (3, 600, 510), (1, 700, 70)])
+@pytest.mark.parametrize("B,T,D", [(40, 200, 520), (12, 300, 512), (5, 300, 512), (3, 600, 510), (1, 700, 70), (1, 4500, 70)])
 @pytest.mark.parametrize("dtype,form", [(BF, "sigmoid"), (F32, "linear")])
 def test_every_split_of_time_agrees(B, T, D, dtype, form):
     x, gate, h0, dout, dhT = inputs(B, T, D, dtype, form, seed=T)

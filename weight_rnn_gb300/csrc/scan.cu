@@ -49,7 +49,7 @@ constexpr int kFwdSteps = 16;            // steps per warp and tile
 constexpr int kBwdSteps = 8;             // (the reverse holds twice the values per step)
 static_assert(kScanBlock % kFwdSteps == 0 && kScanBlock == kWarps * kBwdSteps,
               "states are saved at a warp's start, and taken at a reverse tile's");
-constexpr int kMaxCluster = 8;           // the portable cluster size
+constexpr int kMaxCluster = 16;          // (8 is the portable size, 16 the opt-in)
 // Tiles in a warp's ring.  With three (where they fit) B4 T8192 D4096 took
 // 137 us instead of 127, and a reverse ring of the linear form kept a second
 // CTA off the SM (732 us instead of 423 at B1 T65536 D2048).
@@ -135,11 +135,13 @@ __device__ __forceinline__ void vadd(const float (&a)[VEC], const float (&b)[VEC
   }
 }
 
-// d = a h + b, the step map; in the linear form a = 0 drops h
-template <bool kSig, int VEC>
+// d = a h + b, the step map; with kDrop a = 0 drops h whatever it holds.  The
+// selects that this takes are half of the linear form's instructions, so a warp
+// uses them only where a map has a decay that is 0 (or not a number) in it.
+template <bool kDrop, int VEC>
 __device__ __forceinline__ void affine(const float (&a)[VEC], const float (&h)[VEC], const float (&b)[VEC],
                                        float (&d)[VEC]) {
-  if constexpr (kSig) {
+  if constexpr (!kDrop) {
     vfma(a, h, b, d);
   } else {
     float r[VEC];
@@ -149,12 +151,21 @@ __device__ __forceinline__ void affine(const float (&a)[VEC], const float (&h)[V
   }
 }
 // d = a h, likewise
-template <bool kSig, int VEC>
+template <bool kDrop, int VEC>
 __device__ __forceinline__ void decay(const float (&a)[VEC], const float (&h)[VEC], float (&d)[VEC]) {
   float r[VEC];
   vmul(a, h, r);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) d[i] = !kSig && a[i] == 0.f ? 0.f : r[i];
+  for (int i = 0; i < VEC; ++i) d[i] = kDrop && a[i] == 0.f ? 0.f : r[i];
+}
+
+// whether any lane's map drops a state
+template <int VEC>
+__device__ __forceinline__ bool drops(const float (&a)[VEC]) {
+  bool z = false;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) z |= !(fabsf(a[i]) > 0.f);
+  return __any_sync(0xffffffffu, z);
 }
 
 // a and u from the gate.  Sigmoid: e = 2^min(-f log2 e, 126) stays finite, so
@@ -283,8 +294,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
   constexpr int S = kFwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 1> s_map[2][kWarps][32];
-  __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
   __shared__ Exchange ex;
+  // behind the ring: the maps of the cluster's CTAs, [2][cs][32]
+  auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * kRow * (sizeof(In) + sizeof(Gate)));
+  const auto cta = [&](int buf, int r) { return s_cta + (buf * cs + r) * 32; };
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // the same for all lanes, also to the compiler
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
@@ -348,42 +361,49 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
           u[s][i] = s < n ? u[s][i] : 0.f;
         }
     }
+    bool drop = false;
     {
       Map<VEC, 1> m;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) m.a[i] = a[0][i], m.b[0][i] = u[0][i];
 #pragma unroll
       for (int s = 1; s < S; ++s) {
-        affine<kSig>(a[s], m.b[0], u[s], m.b[0]);
+        affine<false>(a[s], m.b[0], u[s], m.b[0]);
         vmul(m.a, a[s], m.a);
+      }
+      if (!kSig && (drop = drops(m.a))) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) m.b[0][i] = u[0][i];
+#pragma unroll
+        for (int s = 1; s < S; ++s) affine<true>(a[s], m.b[0], u[s], m.b[0]);
       }
       s_map[buf][warp][lane] = m;
     }
     __syncthreads();
     float h[VEC], start[VEC];
     if (kCluster) {
-      // one map per CTA to every CTA of the cluster: warp w serves CTA w
+      // one map per CTA to every CTA of the cluster: warp w serves CTAs w and w + 8
       if (threadIdx.x == 0) ex.expect(buf, cs * 32 * sizeof(Map<VEC, 1>));
       if (warp < cs) {
         Map<VEC, 1> m = s_map[buf][0][lane];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
           const Map<VEC, 1> k = s_map[buf][w][lane];
-          affine<kSig>(k.a, m.b[0], k.b[0], m.b[0]);
+          affine<!kSig>(k.a, m.b[0], k.b[0], m.b[0]);
           vmul(m.a, k.a, m.a);
         }
-        ex.send(buf, &s_cta[buf][rank][lane], warp, m);
+        for (int to = warp; to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
       }
       ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) h[i] = carry[i];
       for (int r = 0; r < cs; ++r) {
-        const Map<VEC, 1> k = s_cta[buf][r][lane];
+        const Map<VEC, 1> k = cta(buf, r)[lane];
         if (r == rank) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) h[i] = carry[i];
         }
-        affine<kSig>(k.a, carry, k.b[0], carry);
+        affine<!kSig>(k.a, carry, k.b[0], carry);
       }
     } else {
 #pragma unroll
@@ -394,7 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const Map<VEC, 1> k = s_map[buf][w][lane];
-      affine<kSig>(k.a, h, k.b[0], h);
+      affine<!kSig>(k.a, h, k.b[0], h);
       if (w + 1 == warp) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) start[i] = h[i];
@@ -408,10 +428,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
       store<float, VEC>(p.states + (b * saved + t0 / kScanBlock) * p.D + c0, start);
     if (live) {
       In *o = out + t0 * p.D;
-      if (n >= S) {
+      if (n >= S && !drop) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          affine<kSig>(a[s], start, u[s], start);
+          affine<false>(a[s], start, u[s], start);
           store<In, VEC>(o, start);
           o += p.D;
         }
@@ -419,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           float v[VEC];
-          affine<kSig>(a[s], start, u[s], start);
+          affine<!kSig>(a[s], start, u[s], start);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) v[i] = s < n ? start[i] : 0.f;
           if (t0 + s < p.T) store<In, VEC>(o, v);
@@ -443,8 +463,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   constexpr int S = kBwdSteps, kTile = kWarps * S, kRow = 32 * VEC, kSlot = S * kRow;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 2> s_map[2][kWarps][32];  // offsets: forward, reverse
-  __shared__ __align__(16) Map<VEC, 1> s_cta[kCluster ? 2 : 1][kCluster ? kMaxCluster : 1][32];
   __shared__ Exchange ex;
+  // behind the ring: the maps of the cluster's CTAs, [2][cs][32]
+  auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * kRow * (2 * sizeof(In) + sizeof(Gate)));
+  const auto cta = [&](int buf, int r) { return s_cta + (buf * cs + r) * 32; };
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
@@ -523,21 +545,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
 #pragma unroll
     for (int i = 0; i < VEC; ++i) h[i] = ahead[i];
     if (it + 1 < rounds) fetch_state(tile - cs);
+    bool drop = false;
     {
       Map<VEC, 2> m;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) m.a[i] = a[0][i], m.b[0][i] = ux[0][i];
+      for (int i = 0; i < VEC; ++i) m.a[i] = a[0][i];
 #pragma unroll
-      for (int s = 1; s < S; ++s) {
-        affine<kSig>(a[s], m.b[0], ux[s], m.b[0]);
-        vmul(m.a, a[s], m.a);
-      }
-      decay<kSig>(a[S - 1], d[S - 1], m.b[1]);
+      for (int s = 1; s < S; ++s) vmul(m.a, a[s], m.a);
+      const auto offsets = [&](auto with) {
+        constexpr bool kDrop = decltype(with)::value;
 #pragma unroll
-      for (int s = S - 2; s >= 0; --s) {
-        vadd(d[s], m.b[1], m.b[1]);
-        decay<kSig>(a[s], m.b[1], m.b[1]);
-      }
+        for (int i = 0; i < VEC; ++i) m.b[0][i] = ux[0][i];
+#pragma unroll
+        for (int s = 1; s < S; ++s) affine<kDrop>(a[s], m.b[0], ux[s], m.b[0]);
+        decay<kDrop>(a[S - 1], d[S - 1], m.b[1]);
+#pragma unroll
+        for (int s = S - 2; s >= 0; --s) {
+          vadd(d[s], m.b[1], m.b[1]);
+          decay<kDrop>(a[s], m.b[1], m.b[1]);
+        }
+      };
+      if (!kSig && (drop = drops(m.a)))
+        offsets(std::true_type{});
+      else
+        offsets(std::false_type{});
       s_map[buf][warp][lane] = m;
     }
     __syncthreads();
@@ -552,21 +583,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
 #pragma unroll
         for (int w = kWarps - 2; w >= 0; --w) {
           const Map<VEC, 2> k = s_map[buf][w][lane];
-          affine<kSig>(k.a, m.b[0], k.b[1], m.b[0]);
+          affine<!kSig>(k.a, m.b[0], k.b[1], m.b[0]);
           vmul(m.a, k.a, m.a);
         }
-        ex.send(buf, &s_cta[buf][rank][lane], warp, m);
+        for (int to = warp; to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
       }
       ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) r[i] = carry[i];
       for (int k = 0; k < cs; ++k) {
-        const Map<VEC, 1> q = s_cta[buf][k][lane];
+        const Map<VEC, 1> q = cta(buf, k)[lane];
         if (k == rank) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) r[i] = carry[i];
         }
-        affine<kSig>(q.a, carry, q.b[0], carry);
+        affine<!kSig>(q.a, carry, q.b[0], carry);
       }
     } else {
 #pragma unroll
@@ -575,7 +606,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
     // the state at this warp's start, over the warps before it
     for (int w = 0; w < warp; ++w) {
       const Map<VEC, 2> k = s_map[buf][w][lane];
-      affine<kSig>(k.a, h, k.b[0], h);
+      affine<!kSig>(k.a, h, k.b[0], h);
     }
     // the gradient that arrives at its end, over the warps after it
 #pragma unroll
@@ -583,7 +614,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w) {
       const Map<VEC, 2> k = s_map[buf][w][lane];
-      affine<kSig>(k.a, r, k.b[1], r);
+      affine<!kSig>(k.a, r, k.b[1], r);
       if (w - 1 == warp) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) c[i] = r[i];
@@ -593,49 +624,56 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
 #pragma unroll
       for (int i = 0; i < VEC; ++i) carry[i] = r[i];
     }
-    // the state before each step takes the place of its input term: sigmoid
-    // keeps a (u h_{t-1} - u x), linear keeps h_{t-1}
+    const auto finish = [&](auto with) {
+      constexpr bool kDrop = decltype(with)::value;
+      // the state before each step takes the place of its input term: sigmoid
+      // keeps a (u h_{t-1} - u x), linear keeps h_{t-1}
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      float before[VEC];
+      for (int s = 0; s < S; ++s) {
+        float before[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) before[i] = h[i];
-      affine<kSig>(a[s], before, ux[s], h);
-      if constexpr (kSig) {
+        for (int i = 0; i < VEC; ++i) before[i] = h[i];
+        affine<kDrop>(a[s], before, ux[s], h);
+        if constexpr (kSig) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) ux[s][i] = -ux[s][i];
-        vfma(u[s], before, ux[s], ux[s]);
-        vmul(a[s], ux[s], ux[s]);
-      } else {
+          for (int i = 0; i < VEC; ++i) ux[s][i] = -ux[s][i];
+          vfma(u[s], before, ux[s], ux[s]);
+          vmul(a[s], ux[s], ux[s]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) ux[s][i] = before[i];
+          for (int i = 0; i < VEC; ++i) ux[s][i] = before[i];
+        }
       }
-    }
-    if (live && tile >= 0) {
-      In *ox = dx + (t0 + S - 1) * p.D;
-      Gate *og = dg + (t0 + S - 1) * p.D;
+      if (live && tile >= 0) {
+        In *ox = dx + (t0 + S - 1) * p.D;
+        Gate *og = dg + (t0 + S - 1) * p.D;
 #pragma unroll
-      for (int s = S - 1; s >= 0; --s) {
-        float dh[VEC], vx[VEC], vg[VEC];
-        vadd(d[s], c, dh);
-        decay<kSig>(a[s], dh, c);
-        vmul(u[s], dh, vx);
-        vmul(ux[s], dh, vg);
-        if (n < S) {
+        for (int s = S - 1; s >= 0; --s) {
+          float dh[VEC], vx[VEC], vg[VEC];
+          vadd(d[s], c, dh);
+          decay<kDrop>(a[s], dh, c);
+          vmul(u[s], dh, vx);
+          vmul(ux[s], dh, vg);
+          if (n < S) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            vx[i] = s < n ? vx[i] : 0.f;
-            vg[i] = s < n ? vg[i] : 0.f;
+            for (int i = 0; i < VEC; ++i) {
+              vx[i] = s < n ? vx[i] : 0.f;
+              vg[i] = s < n ? vg[i] : 0.f;
+            }
           }
+          if (n >= S || t0 + s < p.T) {
+            store<In, VEC>(ox, vx);
+            store<Gate, VEC>(og, vg);
+          }
+          ox -= p.D;
+          og -= p.D;
         }
-        if (n >= S || t0 + s < p.T) {
-          store<In, VEC>(ox, vx);
-          store<Gate, VEC>(og, vg);
-        }
-        ox -= p.D;
-        og -= p.D;
       }
-    }
+    };
+    if (!kSig && drop)
+      finish(std::true_type{});
+    else
+      finish(std::false_type{});
   }
   ring_wait<0>();
   if (p.dh0 && rank == 0 && warp == 0 && live) store<float, VEC>(p.dh0 + b * p.D + c0, carry);
@@ -655,7 +693,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs p, int64_t n) {
   widen(load<float, VEC>(p.h0 + i0), hv);
   gates<kSig>(gv, a, u);
   vmul(u, xv, u);
-  affine<kSig>(a, hv, u, hv);
+  affine<!kSig>(a, hv, u, hv);
   store<float, VEC>(p.hT + i0, hv);
   store<In, VEC>(static_cast<In *>(p.out) + i0, hv);
 }
@@ -688,7 +726,10 @@ bool wide(const ScanArgs &a) { return pieces(a, a.bf16 ? 8 : 4, a.bf16 && a.sigm
 int cluster_size(int64_t rows, int64_t tiles) {
   const int64_t fit = 2 * (int64_t)sm_count();
   int cs = 1;
-  while (cs < kMaxCluster && rows * cs * 2 <= fit && cs < tiles) cs *= 2;
+  while (cs < 8 && rows * cs * 2 <= fit && cs < tiles) cs *= 2;
+  // 16 only for so few rows that its CTAs have SMs of their own: 1 x 30000 x 64
+  // takes 34 us for 60, but 1 x 65536 x 512 (8 rows) 131 for 122
+  if (cs == 8 && rows <= 7 && tiles > 8) cs = kMaxCluster;
   return cs;
 }
 
@@ -697,6 +738,8 @@ cudaError_t launch(K kern, const A &p, int64_t rows, int64_t strips, int cs, int
   // above 48 KB only after asking; asking again changes nothing
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  if (cs > 8 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * cs));
   cfg.blockDim = dim3(kWarps * 32);
@@ -716,7 +759,7 @@ cudaError_t launch_fwd(const ScanArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kFwdSteps - 1) / (kWarps * kFwdSteps));
   constexpr int tile = kWarps * kFwdSteps * 32 * VEC * (int)(sizeof(In) + (kSig ? sizeof(In) : 4));
-  const int smem = kStages * tile;
+  const int smem = kStages * tile + (cs > 1 ? 2 * cs * 32 * (int)sizeof(Map<VEC, 1>) : 0);
   return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_fwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
@@ -725,7 +768,7 @@ cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps));
   constexpr int tile = kWarps * kBwdSteps * 32 * VEC * (int)(2 * sizeof(In) + (kSig ? sizeof(In) : 4));
-  const int smem = kStages * tile;
+  const int smem = kStages * tile + (cs > 1 ? 2 * cs * 32 * (int)sizeof(Map<VEC, 1>) : 0);
   return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_bwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
 }
