@@ -184,7 +184,7 @@ struct Operand {
   int64_t rows, cols, ld;
   int size;
   bool whole() const { return aligned16(p) && ld * size % 16 == 0; }
-  int64_t ldp() const { return up(cols, 16 / size); }
+  int64_t ldp() const { return up(cols, 128 / size); }  // whole lines: a copied box row touches one
   int64_t bytes() const { return rows * ldp() * size; }
   cudaError_t pack(Scratch &scr, cudaStream_t s) {
     if (whole()) return cudaSuccess;
@@ -282,7 +282,7 @@ cudaError_t linear_backward(const void *x, const void *w, const void *dout, cons
   const bool form = (dx || dw) && (act != delta::kActNone || (bf16 && N % 8 != 0));
   delta::DpreArgs d{};
   d.dout = dout; d.pre = pre; d.dbias = dbias; d.M = M; d.N = N; d.act = act; d.bf16 = bf16;
-  d.ldp = form && bf16 ? up(N, 8) : N;
+  d.ldp = form && bf16 ? up(N, 64) : N;
   Operand ox = operand(x, M, K, ldx, (int)e), ow = operand(w, N, K, ldw, (int)e);
   const bool packx = bf16 && dw && !ox.whole(), packw = bf16 && dx && !ow.whole();
   Scratch scr(s);

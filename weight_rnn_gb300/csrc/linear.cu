@@ -210,15 +210,46 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(LinearArgs e, const float
 }
 
 // ----------------------------------------------------------------- gradients
-// a CTA row of 32 threads per matrix row, the widest unit that all rows allow
-template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(const T *src, T *dst, int64_t rows, int64_t cols, int64_t ld,
-                                                   int64_t ldp) {
+// Rows of `bytes` bytes, ld bytes apart, into rows of ldp bytes (a multiple of
+// 16), whole 16-byte pieces; what lies past a row's end is not used.  A piece
+// is put together from five aligned words; in the rows where one could lie
+// outside the matrix, from the bytes that are in it.  A warp a row, four
+// pieces a lane in flight.
+__global__ void __launch_bounds__(256) pack_kernel(const unsigned char *src, unsigned char *dst, int64_t rows,
+                                                   int64_t bytes, int64_t ld, int64_t ldp) {
+  constexpr int kAhead = 4;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(src), hi = lo + (rows - 1) * ld + bytes;
   for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.y; r < rows; r += (int64_t)gridDim.x * 8) {
-    const T *from = src + r * ld;
-    T *to = dst + r * ldp;
-#pragma unroll 4
-    for (int64_t c = threadIdx.x; c < cols; c += 32) to[c] = from[c];
+    const uintptr_t row = lo + r * ld;
+    const uint32_t shift = 8 * (uint32_t)(row & 3);
+    const uintptr_t words = row & ~(uintptr_t)3;
+    const bool inside = words >= lo && row + bytes + 20 <= hi;
+    for (int64_t c0 = threadIdx.x * 16; c0 < bytes; c0 += 512 * kAhead) {
+      uint32_t w[kAhead][5];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t c = c0 + 512 * k;
+        if (c >= bytes) continue;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          const uintptr_t at = words + c + 4 * i;
+          if (inside || (at >= lo && at + 4 <= hi)) {
+            w[k][i] = *reinterpret_cast<const uint32_t *>(at);
+          } else {
+            w[k][i] = 0;
+            for (int b = 0; b < 4; ++b)
+              if (at + b >= lo && at + b < hi)
+                w[k][i] |= (uint32_t)*reinterpret_cast<const unsigned char *>(at + b) << (8 * b);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (c0 + 512 * k < bytes)
+          *reinterpret_cast<uint4 *>(dst + r * ldp + c0 + 512 * k) =
+              make_uint4(__funnelshift_r(w[k][0], w[k][1], shift), __funnelshift_r(w[k][1], w[k][2], shift),
+                         __funnelshift_r(w[k][2], w[k][3], shift), __funnelshift_r(w[k][3], w[k][4], shift));
+    }
   }
 }
 
@@ -233,19 +264,32 @@ __global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
   float s[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = 0.f;
+  constexpr int kAhead = V == 1 ? 4 : 2;  // rows a thread asks for at a time
+  const int64_t step = (int64_t)gridDim.y * 8;
   if (c < p.N)
-    for (int64_t m = (int64_t)blockIdx.y * 8 + threadIdx.y; m < p.M; m += (int64_t)gridDim.y * 8) {
-      const Vec d = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.dout) + m * p.N + c);
-      Vec q = d, o;
-      if (p.act != kActNone) q = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.pre) + m * p.N + c);
+    for (int64_t m0 = (int64_t)blockIdx.y * 8 + threadIdx.y; m0 < p.M; m0 += step * kAhead) {
+      Vec d[kAhead], q[kAhead];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float v = to_f(d.v[i]);
-        if (p.act != kActNone) v *= slope(p.act, to_f(q.v[i]));
-        s[i] += v;
-        from_f(v, o.v[i]);
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t m = m0 + k * step;
+        if (m >= p.M) continue;
+        d[k] = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.dout) + m * p.N + c);
+        if (p.act != kActNone) q[k] = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.pre) + m * p.N + c);
       }
-      if (p.dpre) *reinterpret_cast<Vec *>(static_cast<T *>(p.dpre) + m * p.ldp + c) = o;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t m = m0 + k * step;
+        if (m >= p.M) continue;
+        Vec o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float v = to_f(d[k].v[i]);
+          if (p.act != kActNone) v *= slope(p.act, to_f(q[k].v[i]));
+          s[i] += v;
+          from_f(v, o.v[i]);
+        }
+        if (p.dpre) *reinterpret_cast<Vec *>(static_cast<T *>(p.dpre) + m * p.ldp + c) = o;
+      }
     }
   if (!p.dbias) return;
 #pragma unroll
@@ -286,23 +330,9 @@ cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, i
 
 cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, int64_t ldp, int size,
                         cudaStream_t s) {
-  int64_t unit = 8;  // bytes; ldp and dst are whole 16-byte pieces
-  while (unit > size && ((cols * size) % unit || (ld * size) % unit || !aligned_to(src, unit))) unit /= 2;
   const int64_t want = (rows + 7) / 8, cap = (int64_t)sm_count() * 8;
-  const unsigned grid = (unsigned)(want < cap ? want : cap);
-  const auto go = [&](auto t) {
-    using T = decltype(t);
-    pack_kernel<T><<<grid, dim3(32, 8), 0, s>>>(static_cast<const T *>(src), static_cast<T *>(dst), rows,
-                                                cols * size / unit, ld * size / unit, ldp * size / unit);
-  };
-  if (unit == 8)
-    go(uint64_t{});
-  else if (unit == 4)
-    go(uint32_t{});
-  else if (unit == 2)
-    go(uint16_t{});
-  else
-    go(uint8_t{});
+  pack_kernel<<<(unsigned)(want < cap ? want : cap), dim3(32, 8), 0, s>>>(
+      static_cast<const unsigned char *>(src), static_cast<unsigned char *>(dst), rows, cols * size, ld * size, ldp * size);
   return cudaGetLastError();
 }
 

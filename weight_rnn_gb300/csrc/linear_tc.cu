@@ -212,30 +212,45 @@ __device__ __forceinline__ void finish_row(const LinearArgs &e, int64_t m, int64
 }
 
 // The same chunk where rows are not whole 16-byte pieces: a lane has one column
-// of all 32 rows, single elements, four rows asked for at a time.
+// of all 32 rows, single elements, eight rows asked for at a time.
 __device__ __forceinline__ void finish_column(const LinearArgs &e, const float *stage, int lane, int64_t m0, int64_t n) {
   if (n >= e.N) return;
+  constexpr int kRows = 8;
   const float bias = linear::bias_at(e, n), sw = e.x_scale ? e.w_scale[n] : 1.f;
   const int rows = e.M - m0 < 32 ? (int)(e.M - m0) : 32;
-  const __nv_bfloat16 *res = e.residual ? static_cast<const __nv_bfloat16 *>(e.residual) + m0 * e.ldr + n : nullptr;
+  const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(e.residual) + m0 * e.ldr + n;
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + m0 * e.N + n;
-  __nv_bfloat16 *pre = e.pre ? static_cast<__nv_bfloat16 *>(e.pre) + m0 * e.N + n : nullptr;
+  __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(e.pre) + m0 * e.N + n;
 #pragma unroll 1
-  for (int k = 0; k < rows; k += 4) {
-    float r[4], s[4];
+  for (int k = 0; k < rows; k += kRows) {
+    float v[kRows];
+    __nv_bfloat16 r[kRows];
+    if (e.residual) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = k + i < rows;
-      r[i] = in && res ? __bfloat162float(res[(k + i) * e.ldr]) : 0.f;
-      s[i] = in && e.x_scale ? e.x_scale[m0 + k + i] * sw : 1.f;
+      for (int i = 0; i < kRows; ++i, res += e.ldr)
+        if (k + i < rows) r[i] = *res;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (k + i < rows) {
-        const float p = stage[(k + i) * kPitch + lane] * s[i] + bias;
-        if (pre) pre[(k + i) * e.N] = __float2bfloat16_rn(p);
-        out[(k + i) * e.N] = __float2bfloat16_rn(linear::activate(e.act, p) + r[i]);
-      }
+    for (int i = 0; i < kRows; ++i) v[i] = stage[(k + i) * kPitch + lane];
+    if (e.x_scale) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (k + i < rows) v[i] *= e.x_scale[m0 + k + i] * sw;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) v[i] += bias;
+    if (e.pre) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i, pre += e.N)
+        if (k + i < rows) *pre = __float2bfloat16_rn(v[i]);
+    }
+    if (e.act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) v[i] = linear::activate(e.act, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i, out += e.N)
+      if (k + i < rows) *out = __float2bfloat16_rn(v[i] + (e.residual ? __bfloat162float(r[i]) : 0.f));
   }
 }
 

@@ -17,8 +17,10 @@
 // ring in shared memory, asynchronously, which keeps the memory busy during
 // the reductions without a barrier or a register.  The column sums meet in a
 // second kernel in CTA order, so the result does not depend on scheduling.
-// Rows whose width, strides or addresses are not multiples of 16 bytes take
-// one element per load, straight into registers.
+// Rows whose width, strides or addresses are not multiples of 16 bytes are
+// copied as the 16-byte pieces that cover them, by all threads of the row, and
+// read from there one element at a time (4096 x 4097 bfloat16: element loads
+// into registers took 124 us forward and 520 backward).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -129,90 +131,98 @@ __device__ __forceinline__ void load_weight(const void *weight, bool w_bf16, int
     }
 }
 
-// rows in a thread's ring: three, or two where a row of N tensors of `per`
-// vectors and kMostThreads threads would pass a CTA's shared memory
-__host__ __device__ constexpr int ring_rows(int N, int per) { return N * per >= 12 ? 2 : 3; }
+// rows in a ring: three, or two where N tensors of the widest rows would pass a
+// CTA's shared memory
+__host__ __device__ constexpr int ring_rows(int N, int per, int V, int size) {
+  return V > 1 ? (N * per >= 12 ? 2 : 3) : N == 3 && per == 16 && size == 4 ? 2 : 3;
+}
+// bytes that the pieces covering a row take, wherever it starts
+__host__ __device__ constexpr int64_t cover(int64_t bytes) { return (bytes + 31) / 16 * 16; }
 
-// This thread's vectors of one row: N tensors of kPer vectors.  Whole vectors
-// (V > 1) pass through the thread's ring, single elements through registers,
-// one row ahead.
+// One row of N tensors, kPer vectors a thread.  Whole vectors (V > 1) are
+// copied and read by the thread that uses them; single elements lie in a
+// buffer that the row's threads share.
 template <typename In, int V, int kPer, int N, int kT>
 struct Rows {
   using Vec = APack<In, V>;
-  static constexpr bool kRing = V > 1;
-  static constexpr int kStages = kRing ? ring_rows(N, kPer) : 1;
+  static constexpr int kStages = ring_rows(N, kPer, V, sizeof(In));
   const In *base[N];
   int64_t ld[N], rows, D;
-  Vec *ring;  // [kStages][N][kPer][kT], from this thread's place on
-  Vec held[kRing ? 1 : N][kRing ? 1 : kPer], next[kRing ? 1 : N][kRing ? 1 : kPer];
+  unsigned char *ring;  // V > 1: [kStages][N][kPer][kT] vectors; else [kStages][N][rows a CTA][cover()] bytes
+  const In *now[V > 1 ? 1 : N];
   int slot = 0;
 
+  // a shared buffer of tensor n, and where its row begins in it
+  __device__ __forceinline__ unsigned char *buffer(int s, int n) const {
+    return ring + ((s * N + n) * blockDim.y + threadIdx.y) * cover(D * sizeof(In));
+  }
+  __device__ __forceinline__ static void copy(void *to, const void *from, int bytes) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+  }
   __device__ __forceinline__ void fetch(int64_t row, int to) {
-    if constexpr (kRing) {
-      if (row < rows) {
+    if (row < rows) {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+      for (int n = 0; n < N; ++n) {
+        if (!base[n]) continue;
+        const In *from = base[n] + row * ld[n];
+        if constexpr (V > 1) {
+          Vec *mine = reinterpret_cast<Vec *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
             const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
-            if (d < D && base[n]) {
-              const uint32_t at =
-                  (uint32_t)__cvta_generic_to_shared(ring + ((to * N + n) * kPer + j) * kT);
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(base[n] + row * ld[n] + d)
-                           : "memory");
-            }
+            if (d < D) copy(mine + ((to * N + n) * kPer + j) * kT, from + d, 16);
           }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    } else if (row < rows) {
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int64_t d = (int64_t)j * blockDim.x + threadIdx.x;
-          if (d < D && base[n]) next[n][j].v[0] = base[n][row * ld[n] + d];
+        } else {
+          const int head = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+          const int bytes = head + (int)(D * sizeof(In));
+          const unsigned char *first = reinterpret_cast<const unsigned char *>(from) - head;
+          unsigned char *buf = buffer(to, n);
+          for (int c = threadIdx.x * 16; c < bytes; c += blockDim.x * 16)
+            copy(buf + c, first + c, bytes - c < 16 ? bytes - c : 16);
         }
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
   __device__ __forceinline__ void start(int64_t first, int64_t step) {
-    if constexpr (kRing) {
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) fetch(first + i * step, i);
-    } else {
-      fetch(first, 0);
-    }
+    for (int i = 0; i < kStages - 1; ++i) fetch(first + i * step, i);
   }
   // the row becomes readable, and a later one is asked for
   __device__ __forceinline__ void turn(int64_t row, int64_t step) {
-    if constexpr (kRing) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      fetch(row + (kStages - 1) * step, slot == 0 ? kStages - 1 : slot - 1);
-    } else {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    if constexpr (V == 1) {
+      // of all the row's threads; and the last row's reads are over
+      if (blockDim.x == 32)
+        __syncwarp();
+      else
+        __syncthreads();
 #pragma unroll
       for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) held[n][j] = next[n][j];
-      fetch(row + step, 0);
+        now[n] = reinterpret_cast<const In *>(buffer(slot, n) + (reinterpret_cast<uintptr_t>(base[n] + row * ld[n]) & 15));
     }
+    fetch(row + (kStages - 1) * step, slot == 0 ? kStages - 1 : slot - 1);
   }
-  __device__ __forceinline__ void done() {
-    if constexpr (kRing) slot = slot == kStages - 1 ? 0 : slot + 1;
-  }
-  __device__ __forceinline__ void finish() {
-    if constexpr (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  }
+  __device__ __forceinline__ void done() { slot = slot == kStages - 1 ? 0 : slot + 1; }
+  __device__ __forceinline__ void finish() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
   __device__ __forceinline__ Vec get(int n, int j) const {
-    if constexpr (kRing)
-      return ring[((slot * N + n) * kPer + j) * kT];
-    else
-      return held[n][j];
+    if constexpr (V > 1) {
+      const Vec *mine = reinterpret_cast<const Vec *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
+      return mine[((slot * N + n) * kPer + j) * kT];
+    } else {
+      const int64_t d = (int64_t)j * blockDim.x + threadIdx.x;
+      Vec v;
+      v.v[0] = now[n][d < D ? d : 0];
+      return v;
+    }
   }
 };
 
 // ------------------------------------------------------------------ forward
 // blockDim (nt, rows a CTA); a thread's vectors are nt apart
 template <typename In, int V, int kPer, int kT, bool kQuant>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? (kQuant ? 1024 : 768) / kT : 1) norm_fwd_kernel(NormArgs p) {
+__global__ void __launch_bounds__(kT, V *kPer <= 16 ? (kQuant ? 1024 : 768) / kT : 1) norm_fwd_kernel(NormArgs p) {
   __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? (kQuant ? 1024 : 
   Rows<In, V, kPer, 2, kT> in;
   in.base[0] = static_cast<const In *>(p.x); in.base[1] = static_cast<const In *>(p.residual);
   in.ld[0] = p.ldx; in.ld[1] = p.ldr; in.rows = p.rows; in.D = p.D;
-  in.ring = reinterpret_cast<APack<In, V> *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
+  in.ring = ring;
   in.start(first, step);
   int buf = 0;
   // every row of the CTA takes part in the barriers until the last is done
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? (kQuant ? 1024 : 
 // The row is read from its ring twice, before and after the reduction, rather
 // than held: that is what lets two CTAs of 512 threads share an SM.
 template <typename In, int V, int kPer, int kT>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? 768 / kT : 1) norm_bwd_kernel(NormBwdArgs p) {
+__global__ void __launch_bounds__(kT, V *kPer <= 16 ? 768 / kT : 1) norm_bwd_kernel(NormBwdArgs p) {
   __shared__ float part[2][8 * 32];
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? 768 / kT : 1) nor
   in.base[0] = static_cast<const In *>(p.dy); in.base[1] = static_cast<const In *>(p.sum);
   in.base[2] = static_cast<const In *>(p.dsum);
   in.ld[0] = in.ld[1] = in.ld[2] = in.D = p.D; in.rows = p.rows;
-  in.ring = reinterpret_cast<APack<In, V> *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
+  in.ring = ring;
   in.start(first, step);
   float ahead = first < p.rows ? p.rstd[first] : 0.f;
   int buf = 0;
@@ -354,13 +364,26 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 && V > 1 ? 768 / kT : 1) nor
     in.done();
   }
   in.finish();
-  const int64_t at = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.D;
+  // the CTA's rows of threads meet in order, where the ring was
+  float *sums = reinterpret_cast<float *>(ring);
+  const int width = blockDim.x * kPer * V;
+  if (blockDim.y > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sums[threadIdx.y * width + (j * blockDim.x + threadIdx.x) * V + i] = dw[j][i];
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+  }
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V + i;
-      if (d < p.D) p.partial[at + d] = dw[j][i];
+      const int d = (j * blockDim.x + threadIdx.x) * V + i;
+      float s = dw[j][i];
+      for (int y = 1; y < blockDim.y; ++y) s += sums[y * width + d];
+      if (d < p.D) p.partial[(int64_t)blockIdx.x * p.D + d] = s;
     }
 }
 
@@ -371,7 +394,13 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
   const int64_t d = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (d < D)
-    for (int64_t i = threadIdx.y; i < n; i += 32) v += partial[i * D + d];
+    for (int64_t i = threadIdx.y; i < n; i += 32 * 8) {
+      float p[8];  // asked for together, added in order
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] = i + 32 * k < n ? partial[(i + 32 * k) * D + d] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += p[k];
+    }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = s[threadIdx.x][threadIdx.y];
@@ -393,9 +422,12 @@ bool vec_ok(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0;
 
 // One vector a thread while rows are few (latency), two where a row has more
 // than a warp's worth and there are rows for every SM (fewer, longer-lived
-// CTAs); more only where a row would not fit kMostThreads threads.
+// CTAs); more only where a row would not fit kMostThreads threads.  Of single
+// elements as many as keep a row to few warps, one if it can be: then rows need
+// no barrier.
 Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors) {
   Plan q;
+  const int size = 16 / vec;
   q.V = aligned ? vec : 1;
   const int64_t n = (D + q.V - 1) / q.V;  // vectors a row
   int dev = 0, sms = 152;
@@ -403,16 +435,19 @@ Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors) {
   if (aligned)
     q.per = rows >= 2 * sms && n > 32 ? 2 : 1;
   else
-    q.per = n <= 256 ? 1 : 4;
+    q.per = rows < 2 * sms ? (n <= 256 ? 1 : 4) : n <= 32 ? 1 : n <= 128 ? 4 : n <= 256 ? 8 : 16;
   while (n > (int64_t)q.per * kMostThreads) q.per *= 2;
   q.nt = (int)((n + q.per - 1) / q.per + 31) / 32 * 32;
   q.rpc = q.nt >= 256 ? 1 : 256 / q.nt;
   const int64_t ctas = (rows + q.rpc - 1) / q.rpc;
   q.threads = q.nt * q.rpc <= 256 ? 256 : kMostThreads;
-  q.smem = aligned ? ring_rows(tensors, q.per) * tensors * q.per * q.threads * 16 : 0;
+  q.smem = ring_rows(tensors, q.per, q.V, size) * tensors *
+           (aligned ? q.per * q.threads * 16 : q.rpc * (int)cover(D * size));
+  // (the backward's column sums take the ring's place: 4 bytes an element)
+  if (q.smem < q.rpc * q.nt * q.per * q.V * 4) q.smem = q.rpc * q.nt * q.per * q.V * 4;
   // as many CTAs as an SM holds: by threads at 64 registers, and by rings
   int fit = 1024 / q.threads;
-  if (q.smem && fit > 200 * 1024 / q.smem) fit = 200 * 1024 / q.smem;
+  if (fit > 200 * 1024 / q.smem) fit = 200 * 1024 / q.smem;
   const int64_t cap = (int64_t)sms * (fit > 1 ? fit : 1);
   q.grid = ctas < cap ? ctas : cap;
   return q;
@@ -485,7 +520,7 @@ cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
   const Plan q = bwd_plan<In>(a);
   cudaError_t e = q.grid > 0 ? dispatch<In, BwdOne>(q, a, q, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  return launch_column_sum(a.partial, a.dweight, q.grid * q.rpc, a.D, s);
+  return launch_column_sum(a.partial, a.dweight, q.grid, a.D, s);
 }
 
 }  // namespace
@@ -501,7 +536,7 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
 
 int64_t norm_bwd_ctas(const NormBwdArgs &a) {
   const Plan q = a.bf16 ? bwd_plan<__nv_bfloat16>(a) : bwd_plan<float>(a);
-  return q.grid * q.rpc;
+  return q.grid;
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t s) {
