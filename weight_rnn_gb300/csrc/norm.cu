@@ -387,27 +387,29 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? 768 / kT : 1) norm_bwd_ker
     }
 }
 
-// dw[d] = sum of n partial rows, 32 columns a CTA, in row order per thread row
-// and then over the 32 thread rows
+// dw[d] = sum of n partial rows: C columns a CTA, every R-th row to a thread,
+// then a warp a column over the R sums.  Few columns take 8 at a time (a sector
+// of each row), so that there are CTAs; many take 32 (4096 x 8192: 53 us with
+// the gradients before it, 57 with 8).
+template <int C>
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, float *dw, int64_t n, int64_t D) {
-  __shared__ float s[32][33];
-  const int64_t d = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  constexpr int R = 1024 / C;
+  __shared__ float s[R][C + 1];
+  const int64_t d = (int64_t)blockIdx.x * C + threadIdx.x;
   float v = 0.f;
   if (d < D)
-    for (int64_t i = threadIdx.y; i < n; i += 32 * 8) {
-      float p[8];  // asked for together, added in order
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] = i + 32 * k < n ? partial[(i + 32 * k) * D + d] : 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v += p[k];
-    }
+    for (int64_t i = threadIdx.y; i < n; i += R) v += partial[i * D + d];
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  v = s[threadIdx.x][threadIdx.y];
+  const int warp = (threadIdx.y * C + threadIdx.x) / 32, lane = (threadIdx.y * C + threadIdx.x) % 32;
+  if (warp >= C) return;
+  v = 0.f;
+#pragma unroll
+  for (int k = 0; k < R; k += 32) v += s[lane + k][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && c < D) dw[c] = v;
+  const int64_t c = (int64_t)blockIdx.x * C + warp;
+  if (lane == 0 && c < D) dw[c] = v;
 }
 
 // ------------------------------------------------------------------ launches
@@ -526,7 +528,10 @@ cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_column_sum(const float *partial, float *out, int64_t n, int64_t D, cudaStream_t s) {
-  column_sum_kernel<<<(unsigned)((D + 31) / 32), dim3(32, 32), 0, s>>>(partial, out, n, D);
+  if (D < 1024)
+    column_sum_kernel<8><<<(unsigned)((D + 7) / 8), dim3(8, 128), 0, s>>>(partial, out, n, D);
+  else
+    column_sum_kernel<32><<<(unsigned)((D + 31) / 32), dim3(32, 32), 0, s>>>(partial, out, n, D);
   return cudaGetLastError();
 }
 
