@@ -121,7 +121,7 @@ __device__ __forceinline__ void vmul(const float (&a)[VEC], const float (&b)[VEC
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
     unpk(r, d);
   } else {
-    d[0] = a[0] * b[0];
+    d[0] = __fmul_rn(a[0], b[0]);  // (not to be fused: the same bits on every path, as for pairs)
   }
 }
 template <int VEC>
@@ -131,7 +131,7 @@ __device__ __forceinline__ void vadd(const float (&a)[VEC], const float (&b)[VEC
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
     unpk(r, d);
   } else {
-    d[0] = a[0] + b[0];
+    d[0] = __fadd_rn(a[0], b[0]);
   }
 }
 
@@ -159,13 +159,13 @@ __device__ __forceinline__ void decay(const float (&a)[VEC], const float (&h)[VE
   for (int i = 0; i < VEC; ++i) d[i] = kDrop && a[i] == 0.f ? 0.f : r[i];
 }
 
-// whether any lane's map drops a state
+// whether the map of any lane that has channels drops a state
 template <int VEC>
-__device__ __forceinline__ bool drops(const float (&a)[VEC]) {
+__device__ __forceinline__ bool drops(const float (&a)[VEC], bool live) {
   bool z = false;
 #pragma unroll
   for (int i = 0; i < VEC; ++i) z |= !(fabsf(a[i]) > 0.f);
-  return __any_sync(0xffffffffu, z);
+  return __any_sync(0xffffffffu, z && live);
 }
 
 // a and u from the gate.  Sigmoid: e = 2^min(-f log2 e, 126) stays finite, so
@@ -210,38 +210,49 @@ __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void ring_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// S rows of a strip (32 VEC channels) into `to`, by one warp.  kWide: 16-byte
-// pieces, else a lane's own VEC elements.  Rows from n on and channels past D
-// are not read; their place is filled with zeros.
-template <typename T, int VEC, int S, bool kWide>
-__device__ __forceinline__ void ring_rows(T *to, const T *row, int64_t stride, int64_t n, int64_t left, int lane) {
-  constexpr int kPiece = kWide ? 16 / (int)sizeof(T) : VEC;  // elements
-  constexpr int kAcross = 32 * VEC / kPiece;                  // pieces a row
-  constexpr int kBytes = kPiece * (int)sizeof(T);
+// A strip's row (32 VEC channels) in a ring.  kWide: rows are whole 16-byte
+// pieces.  Else the pieces that cover a row are copied, wherever it starts (in
+// memory before a tensor's first element lies the rest of its 16 bytes), and
+// its elements begin `head` bytes in.
+template <typename T, int VEC, bool kWide>
+struct Strip {
+  static constexpr int kBytes = 32 * VEC * (int)sizeof(T);
+  static constexpr int kPieces = kBytes / 16 + (kWide ? 0 : 1);
+  static constexpr int kPitch = kPieces * 16;
+
+  // S rows into `to`, by one warp.  Rows from n on and channels past `left`
+  // are not read.
+  template <int S>
+  __device__ __forceinline__ static void fetch(unsigned char *to, const T *row, int64_t stride, int64_t n,
+                                               int64_t left, int lane) {
+    const int have = left < 32 * VEC ? (int)left * (int)sizeof(T) : kBytes;
 #pragma unroll
-  for (int k = 0; k < S * kAcross / 32; ++k) {
-    const int i = k * 32 + lane, s = i / kAcross, c = (i % kAcross) * kPiece;
-    const bool in = s < n && c < left;
-    T *dst = to + s * 32 * VEC + c;
-    const T *src = row + (in ? s * stride + c : 0);
-    if constexpr (kBytes < 4) {  // a single 16-bit element: no asynchronous copy is that small
-      *dst = in ? *src : T(0.f);
-    } else {
-      const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-      const int bytes = in ? kBytes : 0;
-      if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
-      else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(kBytes), "r"(bytes)
-                     : "memory");
+    for (int k = 0; k < (S * kPieces + 31) / 32; ++k) {
+      const int i = k * 32 + lane, s = i / kPieces, c = i % kPieces * 16;
+      const uint32_t d = (uint32_t)__cvta_generic_to_shared(to + s * kPitch + c);
+      if constexpr (kWide) {
+        const bool in = s < n && c < have;  // what is not there becomes zeros
+        const T *from = row + (in ? s * stride + c / (int)sizeof(T) : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(from), "r"(in ? 16 : 0) : "memory");
+      } else {
+        const unsigned char *from = reinterpret_cast<const unsigned char *>(row + s * stride);
+        const int head = (int)(reinterpret_cast<uintptr_t>(from) & 15), bytes = have + head - c;
+        if (s < n && s < S && bytes > 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(from + c - head),
+                       "r"(bytes < 16 ? bytes : 16)
+                       : "memory");
+      }
     }
   }
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void ring_read(const T *at, float (&v)[VEC]) {
-  widen(*reinterpret_cast<const typename Raw<T, VEC>::type *>(at), v);
-}
+  // a lane's channels of row s, of a group whose row 0 is at `row`
+  __device__ __forceinline__ static void read(const unsigned char *at, const T *row, int64_t stride, int s, int lane,
+                                              float (&v)[VEC]) {
+    int off = s * kPitch + lane * VEC * (int)sizeof(T);
+    if constexpr (!kWide)
+      off += ((uint32_t)reinterpret_cast<uintptr_t>(row) + (uint32_t)s * (uint32_t)stride * (uint32_t)sizeof(T)) & 15;
+    widen(*reinterpret_cast<const typename Raw<T, VEC>::type *>(at + off), v);
+  }
+};
 
 // one warp's map (or a CTA's): decays and offsets of a lane's channels
 template <int VEC, int kOffsets>
@@ -291,12 +302,14 @@ struct Exchange {
 template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
+  using X = Strip<In, VEC, kWide>;
+  using G = Strip<Gate, VEC, kWide>;
   constexpr int S = kFwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 1> s_map[2][kWarps][32];
   __shared__ Exchange ex;
   // behind the ring: the maps of the cluster's CTAs, [2][cs][32]
-  auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * kRow * (sizeof(In) + sizeof(Gate)));
+  auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * (X::kPitch + G::kPitch));
   const auto cta = [&](int buf, int r) { return s_cta + (buf * cs + r) * 32; };
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // the same for all lanes, also to the compiler
@@ -309,14 +322,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
   const In *x = static_cast<const In *>(p.x) + b * p.x_sb + first;
   const Gate *g = static_cast<const Gate *>(p.gate) + b * p.g_sb + first;
   In *out = static_cast<In *>(p.out) + b * p.T * p.D + c0;
-  In *rx = reinterpret_cast<In *>(ring) + warp * kStages * S * kRow;
-  Gate *rg = reinterpret_cast<Gate *>(ring + kWarps * kStages * S * kRow * sizeof(In)) + warp * kStages * S * kRow;
+  unsigned char *rx = ring + warp * kStages * S * X::kPitch;
+  unsigned char *rg = ring + kWarps * kStages * S * X::kPitch + warp * kStages * S * G::kPitch;
 
   auto fetch = [&](int64_t tile, int slot) {
     const int64_t t0 = tile * kTile + warp * S, n = len - t0;
     if (n > 0) {
-      ring_rows<In, VEC, S, kWide>(rx + slot * S * kRow, x + t0 * p.x_st, p.x_st, n, left, lane);
-      ring_rows<Gate, VEC, S, kWide>(rg + slot * S * kRow, g + t0 * p.g_st, p.g_st, n, left, lane);
+      X::template fetch<S>(rx + slot * S * X::kPitch, x + t0 * p.x_st, p.x_st, n, left, lane);
+      G::template fetch<S>(rg + slot * S * G::kPitch, g + t0 * p.g_st, p.g_st, n, left, lane);
     }
     ring_commit();
   };
@@ -346,8 +359,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       float xv[VEC], gv[VEC];
-      ring_read<In, VEC>(rx + (slot * S + s) * kRow + lane * VEC, xv);
-      ring_read<Gate, VEC>(rg + (slot * S + s) * kRow + lane * VEC, gv);
+      X::read(rx + slot * S * X::kPitch, x + t0 * p.x_st, p.x_st, s, lane, xv);
+      G::read(rg + slot * S * G::kPitch, g + t0 * p.g_st, p.g_st, s, lane, gv);
       gates<kSig>(gv, a[s], u[s]);
       vmul(u[s], xv, u[s]);
     }
@@ -371,7 +384,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
         affine<false>(a[s], m.b[0], u[s], m.b[0]);
         vmul(m.a, a[s], m.a);
       }
-      if (!kSig && (drop = drops(m.a))) {
+      if (!kSig && (drop = drops(m.a, live))) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) m.b[0][i] = u[0][i];
 #pragma unroll
@@ -460,12 +473,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
-  constexpr int S = kBwdSteps, kTile = kWarps * S, kRow = 32 * VEC, kSlot = S * kRow;
+  using X = Strip<In, VEC, kWide>;
+  using G = Strip<Gate, VEC, kWide>;
+  constexpr int S = kBwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 2> s_map[2][kWarps][32];  // offsets: forward, reverse
   __shared__ Exchange ex;
   // behind the ring: the maps of the cluster's CTAs, [2][cs][32]
-  auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * kRow * (2 * sizeof(In) + sizeof(Gate)));
+  auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * (2 * X::kPitch + G::kPitch));
   const auto cta = [&](int buf, int r) { return s_cta + (buf * cs + r) * 32; };
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
@@ -480,8 +495,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   const In *dout = static_cast<const In *>(p.dout) + b * p.T * p.D + first;
   In *dx = static_cast<In *>(p.dx) + b * p.T * p.D + c0;
   Gate *dg = static_cast<Gate *>(p.dgate) + b * p.T * p.D + c0;
-  In *rx = reinterpret_cast<In *>(ring) + warp * 2 * kStages * kSlot, *rd = rx + kStages * kSlot;
-  Gate *rg = reinterpret_cast<Gate *>(ring + 2 * kWarps * kStages * kSlot * sizeof(In)) + warp * kStages * kSlot;
+  unsigned char *rx = ring + warp * 2 * kStages * S * X::kPitch, *rd = rx + kStages * S * X::kPitch;
+  unsigned char *rg = ring + 2 * kWarps * kStages * S * X::kPitch + warp * kStages * S * G::kPitch;
 
   float ahead[VEC];  // the saved state of the next tile
 #pragma unroll
@@ -489,9 +504,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   auto fetch = [&](int64_t tile, int slot) {  // a tile below 0 is not there
     const int64_t t0 = tile * kTile + warp * S, n = tile < 0 ? 0 : len - t0;
     if (n > 0) {
-      ring_rows<In, VEC, S, kWide>(rx + slot * kSlot, x + t0 * p.x_st, p.x_st, n, left, lane);
-      ring_rows<In, VEC, S, kWide>(rd + slot * kSlot, dout + t0 * p.D, p.D, n, left, lane);
-      ring_rows<Gate, VEC, S, kWide>(rg + slot * kSlot, g + t0 * p.g_st, p.g_st, n, left, lane);
+      X::template fetch<S>(rx + slot * S * X::kPitch, x + t0 * p.x_st, p.x_st, n, left, lane);
+      X::template fetch<S>(rd + slot * S * X::kPitch, dout + t0 * p.D, p.D, n, left, lane);
+      G::template fetch<S>(rg + slot * S * G::kPitch, g + t0 * p.g_st, p.g_st, n, left, lane);
     }
     ring_commit();
   };
@@ -524,9 +539,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       float xv[VEC], gv[VEC];
-      ring_read<In, VEC>(rx + slot * kSlot + s * kRow + lane * VEC, xv);
-      ring_read<Gate, VEC>(rg + slot * kSlot + s * kRow + lane * VEC, gv);
-      ring_read<In, VEC>(rd + slot * kSlot + s * kRow + lane * VEC, d[s]);
+      X::read(rx + slot * S * X::kPitch, x + t0 * p.x_st, p.x_st, s, lane, xv);
+      G::read(rg + slot * S * G::kPitch, g + t0 * p.g_st, p.g_st, s, lane, gv);
+      X::read(rd + slot * S * X::kPitch, dout + t0 * p.D, p.D, s, lane, d[s]);
       gates<kSig>(gv, a[s], u[s]);
       vmul(u[s], xv, ux[s]);
     }
@@ -565,7 +580,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
           decay<kDrop>(a[s], m.b[1], m.b[1]);
         }
       };
-      if (!kSig && (drop = drops(m.a)))
+      if (!kSig && (drop = drops(m.a, live)))
         offsets(std::true_type{});
       else
         offsets(std::false_type{});
@@ -715,7 +730,7 @@ bool pieces(const ScanArgs &a, int nx, int ng) {
          a.g_st % ng == 0 && ok(a.x, nx * ex) && ok(a.gate, ng * eg);
 }
 // Two channels a lane (bfloat16; a row of a strip is 128 bytes either way) need
-// even offsets everywhere; 16-byte pieces are wide.
+// even offsets everywhere; rows of whole 16-byte pieces are wide.
 bool pairs(const ScanArgs &a) { return pieces(a, 2, 2); }
 bool wide(const ScanArgs &a) { return pieces(a, a.bf16 ? 8 : 4, a.bf16 && a.sigmoid ? 8 : 4); }
 
@@ -758,7 +773,8 @@ template <typename In, bool kSig, int VEC, bool kWide>
 cudaError_t launch_fwd(const ScanArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kFwdSteps - 1) / (kWarps * kFwdSteps));
-  constexpr int tile = kWarps * kFwdSteps * 32 * VEC * (int)(sizeof(In) + (kSig ? sizeof(In) : 4));
+  using Gate = typename std::conditional<kSig, In, float>::type;
+  constexpr int tile = kWarps * kFwdSteps * (Strip<In, VEC, kWide>::kPitch + Strip<Gate, VEC, kWide>::kPitch);
   const int smem = kStages * tile + (cs > 1 ? 2 * cs * 32 * (int)sizeof(Map<VEC, 1>) : 0);
   return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_fwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
@@ -767,7 +783,8 @@ template <typename In, bool kSig, int VEC, bool kWide>
 cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
   const int64_t strips = (a.D + 32 * VEC - 1) / (32 * VEC), rows = a.B * strips;
   const int cs = cluster_size(rows, (a.T + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps));
-  constexpr int tile = kWarps * kBwdSteps * 32 * VEC * (int)(2 * sizeof(In) + (kSig ? sizeof(In) : 4));
+  using Gate = typename std::conditional<kSig, In, float>::type;
+  constexpr int tile = kWarps * kBwdSteps * (2 * Strip<In, VEC, kWide>::kPitch + Strip<Gate, VEC, kWide>::kPitch);
   const int smem = kStages * tile + (cs > 1 ? 2 * cs * 32 * (int)sizeof(Map<VEC, 1>) : 0);
   return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
                 : launch(scan_bwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
