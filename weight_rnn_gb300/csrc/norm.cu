@@ -30,7 +30,10 @@ namespace delta {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
-constexpr int kMostThreads = 512;  // of a CTA: 128 registers a thread
+constexpr int kMostThreads = 512;  // of a CTA
+// Threads an SM is compiled to hold.  More of them and fewer registers were
+// slower but for the 8-bit output (32768 x 4096: 182 us for 192; 162 for 173).
+constexpr int kSmThreads = 768, kQuantThreads = 1024;
 
 // V elements: one 16-byte vector, or a single element
 template <typename T, int V>
@@ -222,7 +225,7 @@ struct Rows {
 // ------------------------------------------------------------------ forward
 // blockDim (nt, rows a CTA); a thread's vectors are nt apart
 template <typename In, int V, int kPer, int kT, bool kQuant>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 ? (kQuant ? 1024 : 768) / kT : 1) norm_fwd_kernel(NormArgs p) {
+__global__ void __launch_bounds__(kT, V *kPer <= 16 ? (kQuant ? kQuantThreads : kSmThreads) / kT : 1) norm_fwd_kernel(NormArgs p) {
   __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? (kQuant ? 1024 : 768) / kT
 // The row is read from its ring twice, before and after the reduction, rather
 // than held: that is what lets two CTAs of 512 threads share an SM.
 template <typename In, int V, int kPer, int kT>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 ? 768 / kT : 1) norm_bwd_kernel(NormBwdArgs p) {
+__global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) norm_bwd_kernel(NormBwdArgs p) {
   __shared__ float part[2][8 * 32];
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
@@ -427,7 +430,7 @@ bool vec_ok(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0;
 // CTAs); more only where a row would not fit kMostThreads threads.  Of single
 // elements as many as keep a row to few warps, one if it can be: then rows need
 // no barrier.
-Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors) {
+Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors, int resident, bool many) {
   Plan q;
   const int size = 16 / vec;
   q.V = aligned ? vec : 1;
@@ -447,10 +450,15 @@ Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors) {
            (aligned ? q.per * q.threads * 16 : q.rpc * (int)cover(D * size));
   // (the backward's column sums take the ring's place: 4 bytes an element)
   if (q.smem < q.rpc * q.nt * q.per * q.V * 4) q.smem = q.rpc * q.nt * q.per * q.V * 4;
-  // as many CTAs as an SM holds: by threads at 64 registers, and by rings
-  int fit = 1024 / q.threads;
+  // as many CTAs as an SM holds, by its resident threads and by rings; with
+  // `many`, 8 to 16 an SM where each still has a dozen rows: CTAs that come
+  // later even out what the memory gives each (32768 x 4096 bfloat16 forward
+  // 161 us, 6.7 TB/s, for 182 with the resident ones alone; the backward, which
+  // ends in a row of sums per CTA, 195 for 173)
+  int fit = resident / q.threads;
   if (fit > 200 * 1024 / q.smem) fit = 200 * 1024 / q.smem;
-  const int64_t cap = (int64_t)sms * (fit > 1 ? fit : 1);
+  int64_t cap = (int64_t)sms * (fit > 1 ? fit : 1);
+  if (many && ctas / 12 >= 8 * sms) cap = ctas / 12 < 16 * sms ? ctas / 12 : 16 * sms;
   q.grid = ctas < cap ? ctas : cap;
   return q;
 }
@@ -508,14 +516,14 @@ cudaError_t fwd_all(const NormArgs &a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(In);
   const bool ok = a.D % V == 0 && a.ldx % V == 0 && (!a.residual || a.ldr % V == 0) && vec_ok(a.x) &&
                   vec_ok(a.residual);
-  const Plan q = plan(a.rows, a.D, V, ok, 2);
+  const Plan q = plan(a.rows, a.D, V, ok, 2, a.scale ? kQuantThreads : kSmThreads, true);
   return dispatch<In, FwdOne>(q, a, q, s);
 }
 
 template <typename In>
 Plan bwd_plan(const NormBwdArgs &a) {
   constexpr int V = 16 / sizeof(In);
-  return plan(a.rows, a.D, V, a.D % V == 0, 3);
+  return plan(a.rows, a.D, V, a.D % V == 0, 3, kSmThreads, false);
 }
 template <typename In>
 cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
