@@ -265,8 +265,8 @@ int run_linear(const void *x, const void *w, const float *x_scale, const float *
 }
 
 // Gradients of a float32 or bfloat16 layer.  dpre = dout act'(pre) is formed
-// once, in the operands' type: for bfloat16 that is a rounding of 2^-9 of each
-// term of dx and dw, the price of a tensor-core operand; dbias sums the
+// once, in the operands' type: for bfloat16 that is a rounding of at most 2^-8 of
+// each term of dx and dw, the price of a tensor-core operand; dbias sums the
 // unrounded terms.
 cudaError_t linear_backward(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                             float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,

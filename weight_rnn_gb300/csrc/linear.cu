@@ -337,10 +337,11 @@ cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, 
 }
 
 int64_t dpre_parts(const DpreArgs &p) {
-  // CTAs for every SM several times over, but no fewer than 8 rows a thread
+  // CTAs for every SM many times over, but no fewer than 4 rows a thread (M512
+  // N2048: 24 us of gradients in all, for 28 with a quarter of the CTAs)
   const int64_t across = (p.N + 32 * dpre_vec(p) - 1) / (32 * dpre_vec(p));
-  int64_t parts = (8 * (int64_t)sm_count() + across - 1) / across;
-  const int64_t most = (p.M + 63) / 64;
+  int64_t parts = (32 * (int64_t)sm_count() + across - 1) / across;
+  const int64_t most = (p.M + 31) / 32;
   if (parts > most) parts = most;
   return parts < 1 ? 1 : parts > 65535 ? 65535 : parts;
 }
