@@ -606,8 +606,9 @@ int delta_linear_quant(const void *x, const float *x_scale, const void *w, const
  *   dx     [M, K] dtype,  dw [N, K] dtype,  dbias [N] float32; NULL: not wanted
  *
  * In bfloat16, dpre is rounded to bfloat16 as an operand of the two products
- * (dbias sums it unrounded).  It and packed operands go to scratch from the
- * library's pool, stream-ordered.
+ * (dbias sums it unrounded); layers small enough for one launch keep it in
+ * float32.  It and packed operands go to scratch from the library's pool,
+ * stream-ordered.
  */
 int delta_linear_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                      float *dbias, int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act,

@@ -199,6 +199,8 @@ Operand operand(const void *p, int64_t rows, int64_t cols, int64_t ld, int size)
   return Operand{p, rows, cols, rows > 1 ? ld : up(cols, 16 / size), size};
 }
 
+constexpr double kPackUs = 10.0;  // scratch and two more kernels
+
 cudaError_t linear_forward(const delta::LinearArgs &a, cudaStream_t s) {
   if (a.kind == delta::kLinF32)
     return delta::launch_gemm_f32(a, static_cast<const float *>(a.x), a.ldx, 1, static_cast<const float *>(a.w),
@@ -207,12 +209,13 @@ cudaError_t linear_forward(const delta::LinearArgs &a, cudaStream_t s) {
   const int size = a.kind == delta::kLinE4m3 ? 1 : 2;
   Operand x = operand(a.x, a.M, a.K, a.ldx, size), w = operand(a.w, a.N, a.K, a.ldw, size);
   // Small products take the streaming kernel too, with a pass over w for every
-  // 16 rows: up to about 70 M multiplications that is shorter than filling the
-  // tensor cores' pipeline (M64 N2048 K512 in 4.2 us for 5.2, M128 N2048 K512 in
-  // 6.7 for 5.3) and than packing operands first (M93 N133 K473 in 4.0 for 17).
-  // Rows of 8-bit elements at odd addresses come a byte at a time: 12 M.
-  const int64_t few = int64_t(size == 1 && !(x.whole() && w.whole()) ? 12 : 70) * 1000000;
-  if (a.M * a.N <= few / a.K) return delta::launch_linear_small(a, s);
+  // 16 rows, where that is shorter than filling the tensor cores' pipeline (M64
+  // N2048 K512 in 4.2 us for 5.2, M128 N2048 K512 in 6.7 for 5.3), or than
+  // packing operands first, two launches and scratch more (M93 N133 K473 in 4.0
+  // for 17).
+  const bool f8 = size == 1, pack = !x.whole() || !w.whole();
+  if (delta::linear_small_us(a.M, a.N, a.K, f8, !pack) < delta::gemm_tc_us(a.M, a.N, a.K, f8) + (pack ? kPackUs : 0.0))
+    return delta::launch_linear_small(a, s);
   Scratch scr(s);
   if (!x.whole()) scr.want(x.bytes());
   if (!w.whole()) scr.want(w.bytes());
@@ -279,6 +282,8 @@ cudaError_t linear_backward(const void *x, const void *w, const void *dout, cons
     if (err == cudaSuccess && dx && M > 0) err = cudaMemsetAsync(dx, 0, (size_t)(M * K * e), s);
     return err;
   }
+  if (bf16 && delta::small_bwd_fits(M, N, K))
+    return delta::launch_small_bwd(x, w, dout, pre, dx, dw, dbias, M, N, K, ldx, ldw, act, s);
   const bool form = (dx || dw) && (act != delta::kActNone || (bf16 && N % 8 != 0));
   delta::DpreArgs d{};
   d.dout = dout; d.pre = pre; d.dbias = dbias; d.M = M; d.N = N; d.act = act; d.bf16 = bf16;

@@ -196,10 +196,21 @@ struct GemmArgs {
   LinearArgs epi;  // M, N, out and the epilogue
 };
 cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s);
+// about how long it takes
+double gemm_tc_us(int64_t M, int64_t N, int64_t K, bool f8);
 cudaError_t read_and_clear_linear_error(unsigned int *word);
 // streams the weight once for every 16 rows of x: for M <= kLinSmallM once
 constexpr int kLinSmallM = 16;
 cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s);
+// about how long it takes
+double linear_small_us(int64_t M, int64_t N, int64_t K, bool f8, bool whole);
+// all gradients of a small bfloat16 layer (those whose pointers are set), in one
+// launch without scratch
+constexpr double kSmallBwdUs = 15;
+bool small_bwd_fits(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
+                             float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
+                             cudaStream_t s);
 // float32 on the CUDA cores, operands with any strides (elements)
 cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, int64_t ak, const float *b,
                             int64_t bn, int64_t bk, int64_t K, cudaStream_t s);

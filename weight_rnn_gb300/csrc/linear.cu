@@ -49,22 +49,42 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // 16 bytes of a row from byte k on; zeros past the row's `bytes`.  kVec: rows
-// are whole 16-byte pieces, else single elements of `size` bytes.
-template <bool kVec, int kSize, bool kStream>
+// are whole 16-byte pieces.  Else they are put together from the two aligned
+// pieces that hold them (each read only if it holds a byte of the row), by
+// words and then by bytes.
+template <bool kVec, bool kStream>
 __device__ __forceinline__ uint4 piece(const uint8_t *row, int64_t k, int64_t bytes) {
+  if (k >= bytes) return make_uint4(0, 0, 0, 0);
   if constexpr (kVec) {
-    if (k >= bytes) return make_uint4(0, 0, 0, 0);
     const uint4 *p = reinterpret_cast<const uint4 *>(row + k);
     return kStream ? __ldcs(p) : *p;
   } else {
-    uint32_t w[4] = {0, 0, 0, 0};
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + k);
+    const uint32_t sh = (uint32_t)(at & 15);
+    const uint4 *p = reinterpret_cast<const uint4 *>(at - sh);
+    const uint4 lo = *p;
+    uint4 hi = make_uint4(0, 0, 0, 0);
+    if (sh && bytes - k > 16 - (int)sh) hi = p[1];
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (sh & 8) {
 #pragma unroll
-    for (int i = 0; i < 16 / kSize; ++i)
-      if (k + i * kSize < bytes) {
-        const uint32_t v = kSize == 2 ? *reinterpret_cast<const uint16_t *>(row + k + 2 * i) : row[k + i];
-        w[i * kSize / 4] |= v << (8 * (i * kSize % 4));
-      }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (sh & 4) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = 8 * (sh & 3);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    if (bytes - k < 16) {
+      const int have = (int)(bytes - k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = have >= 4 * i + 4 ? v[i] : have <= 4 * i ? 0u : v[i] & (0xFFFFFFFFu >> (8 * (4 * i + 4 - have)));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -97,8 +117,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
   const auto ask = [&](int64_t k) {
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j) {
-      next0[j] = piece<kVec, kSize, true>(w0, k + j * 64 + t * 16, bytes);
-      next1[j] = piece<kVec, kSize, true>(w1, k + j * 64 + t * 16, bytes);
+      next0[j] = piece<kVec, true>(w0, k + j * 64 + t * 16, bytes);
+      next1[j] = piece<kVec, true>(w1, k + j * 64 + t * 16, bytes);
     }
   };
   ask(k0);
@@ -111,7 +131,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
     for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const uint4 v = piece<kVec, kSize, false>(x[i], k0 + j * 64 + t * 16, bytes);
+        const uint4 v = piece<kVec, false>(x[i], k0 + j * 64 + t * 16, bytes);
         if constexpr (kF8) {
           mma_e4m3(c[i], u0[j].x, u1[j].x, u0[j].y, u1[j].y, v.x, v.y);
           mma_e4m3(c[i], u0[j].z, u1[j].z, u0[j].w, u1[j].w, v.z, v.w);
@@ -304,6 +324,138 @@ __global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
   }
 }
 
+// Small gradients, all in one kernel: C[m][n] = sum_r A(r, m) B(r, n) with A
+// formed on the way in as dpre = dout act'(pre), so that nothing is packed and
+// dpre is not rounded.  For dx, m is the row and r the output channel, B is w;
+// for dw, m is the output channel and r the row, B is x, and the column sums of
+// dpre come out beside it.  The first CTAs have dx's tiles, the others dw's.  A
+// CTA has 32 x 64 elements and every cs-th block of 32 r, 2 x 4 elements a thread
+// on the CUDA cores in float32, the next block's elements on their way meanwhile;
+// a cluster's sums meet through distributed shared memory in rank order.
+constexpr int kBm = 32, kBn = 64, kBr = 32, kBwdCluster = 8;
+
+struct SmallBwd {
+  const __nv_bfloat16 *dout, *pre;  // [M][N]
+  const __nv_bfloat16 *x, *w;       // [M][K], [N][K]
+  __nv_bfloat16 *dx, *dw;           // nullptr: not wanted
+  float *dbias;
+  int64_t M, N, K, ldx, ldw;
+  int64_t dx_tiles, dw_tiles;
+  int act, cs;
+};
+
+__global__ void __launch_bounds__(256) small_bwd_kernel(SmallBwd p) {
+  __shared__ float sa[kBr][kBm + 1];
+  __shared__ __align__(16) float sb[kBr][kBn + 4];
+  __shared__ __align__(16) float part[kBm][kBn + 4], bias[kBm];
+  const int tid = threadIdx.x, cs = p.cs;
+  const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
+  if (cs > 1) cg::this_cluster().barrier_arrive();
+  int64_t tile = blockIdx.x / cs;
+  const bool of_w = tile >= p.dx_tiles;  // same for a cluster
+  if (of_w) tile -= p.dx_tiles;
+  const __nv_bfloat16 *const other = of_w ? p.x : p.w;
+  __nv_bfloat16 *const out = of_w ? p.dw : p.dx;
+  const int64_t ldo = of_w ? p.ldx : p.ldw;
+  const int64_t rows = of_w ? p.N : p.M, red = of_w ? p.M : p.N;  // of C, and terms of its sums
+  const int64_t across = out ? (p.K + kBn - 1) / kBn : 1;
+  const int64_t m0 = tile / across * kBm, n0 = tile % across * kBn;
+  const bool sums = of_w && p.dbias && n0 == 0;
+  const int tm = tid / 16 * 2, tn = tid % 16 * 4;
+  float c[2][4] = {}, s = 0.f;
+  __nv_bfloat16 ra[kBr * kBm / 256], rp[kBr * kBm / 256], rb[kBr * kBn / 256];
+  const __nv_bfloat16 zero = __float2bfloat16_rn(0.f);
+  const auto fetch = [&](int64_t r0) {
+#pragma unroll
+    for (int k = 0; k < kBr * kBm / 256; ++k) {
+      // neighbouring threads along a row of dout: its columns are r for dx, m for dw
+      const int a = tid % 32, b = tid / 32 + 8 * k;
+      const int64_t row = of_w ? r0 + b : m0 + b, col = of_w ? m0 + a : r0 + a;
+      const bool in = row < p.M && col < p.N;
+      ra[k] = in ? p.dout[row * p.N + col] : zero;
+      rp[k] = in && p.act != kActNone ? p.pre[row * p.N + col] : zero;
+    }
+    if (out) {
+#pragma unroll
+      for (int k = 0; k < kBr * kBn / 256; ++k) {
+        const int a = tid % kBn, b = tid / kBn + 4 * k;
+        rb[k] = r0 + b < red && n0 + a < p.K ? other[(r0 + b) * ldo + n0 + a] : zero;
+      }
+    }
+  };
+  int64_t r0 = (int64_t)rank * kBr;
+  if (r0 < red) fetch(r0);
+  for (; r0 < red; r0 += (int64_t)kBr * cs) {
+#pragma unroll
+    for (int k = 0; k < kBr * kBm / 256; ++k) {
+      const int a = tid % 32, b = tid / 32 + 8 * k;
+      const float g = __bfloat162float(ra[k]);
+      // outside, dout stands as 0 and takes no factor
+      const float v = p.act == kActNone ? g : g * slope(p.act, __bfloat162float(rp[k]));
+      if (of_w)
+        sa[b][a] = v;
+      else
+        sa[a][b] = v;
+    }
+    if (out) {
+#pragma unroll
+      for (int k = 0; k < kBr * kBn / 256; ++k) sb[tid / kBn + 4 * k][tid % kBn] = __bfloat162float(rb[k]);
+    }
+    __syncthreads();
+    if (r0 + (int64_t)kBr * cs < red) fetch(r0 + (int64_t)kBr * cs);
+    if (out) {
+#pragma unroll 8
+      for (int r = 0; r < kBr; ++r) {
+        const float a0 = sa[r][tm], a1 = sa[r][tm + 1];
+        const float4 b = *reinterpret_cast<const float4 *>(&sb[r][tn]);
+        c[0][0] = fmaf(a0, b.x, c[0][0]), c[0][1] = fmaf(a0, b.y, c[0][1]);
+        c[0][2] = fmaf(a0, b.z, c[0][2]), c[0][3] = fmaf(a0, b.w, c[0][3]);
+        c[1][0] = fmaf(a1, b.x, c[1][0]), c[1][1] = fmaf(a1, b.y, c[1][1]);
+        c[1][2] = fmaf(a1, b.z, c[1][2]), c[1][3] = fmaf(a1, b.w, c[1][3]);
+      }
+    }
+    if (sums && tid < kBm) {
+#pragma unroll 8
+      for (int r = 0; r < kBr; ++r) s += sa[r][tid];
+    }
+    __syncthreads();
+  }
+  if (cs == 1) {
+    if (sums && tid < kBm && m0 + tid < p.N) p.dbias[m0 + tid] = s;
+    if (!out) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (m0 + tm + i < rows && n0 + tn + j < p.K)
+          out[(m0 + tm + i) * p.K + n0 + tn + j] = __float2bfloat16_rn(c[i][j]);
+    return;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.barrier_wait();  // every CTA of the cluster has begun
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<float4 *>(&part[tm + i][tn]) = make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
+  if (tid < kBm) bias[tid] = s;
+  cluster.sync();
+  // each CTA adds up and stores its share of the rows
+  const int share = kBm / cs;
+  for (int i = tid; i < share * kBn; i += 256) {
+    const int m = rank * share + i / kBn, n = i % kBn;
+    float v = 0.f;
+    for (int q = 0; q < cs; ++q) v += *cluster.map_shared_rank(&part[m][n], q);
+    if (out && m0 + m < rows && n0 + n < p.K) out[(m0 + m) * p.K + n0 + n] = __float2bfloat16_rn(v);
+  }
+  if (sums && tid < share && m0 + rank * share + tid < p.N) {
+    float v = 0.f;
+    for (int q = 0; q < cs; ++q) v += *cluster.map_shared_rank(&bias[rank * share + tid], q);
+    p.dbias[m0 + rank * share + tid] = v;
+  }
+  cluster.sync();  // no CTA leaves while another may read from it
+}
+
+int64_t tiles_of(int64_t rows, int64_t cols) { return (rows + kBm - 1) / kBm * ((cols + kBn - 1) / kBn); }
+
 int dpre_vec(const DpreArgs &p) {
   const int v = p.bf16 ? 8 : 4;
   return p.N % v == 0 && (!p.dpre || p.ldp % v == 0) && aligned_to(p.dout, 16) && aligned_to(p.pre, 16) &&
@@ -313,6 +465,14 @@ int dpre_vec(const DpreArgs &p) {
 }
 
 }  // namespace
+
+// From 30 measured sizes (M24..4000, N64..2048, K64..4096): 512 CTAs of 16 x 16
+// outputs take a round, of 1.15 us and 1.06 us per KB of a row of w; twice as
+// long where pieces are put together, three times of 8-bit elements.
+double linear_small_us(int64_t M, int64_t N, int64_t K, bool f8, bool whole) {
+  const double ctas = (double)((M + 15) / 16) * (double)((N + 15) / 16);
+  return (2.0 + ctas / 512.0 * (1.15 + 1.06 * (double)K * (f8 ? 1 : 2) / 1024.0)) * (whole ? 1.0 : f8 ? 3.0 : 2.0);
+}
 
 cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s) {
   if (a.kind == kLinE4m3)
@@ -364,6 +524,56 @@ cudaError_t launch_dpre(const DpreArgs &p, cudaStream_t s) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.dbias) return e;
   return launch_column_sum(p.partial, p.dbias, parts, p.N, s);
+}
+
+namespace {
+
+// CTAs along the sums while they do not fill the GPU and have blocks to share
+int small_bwd_cluster(int64_t tiles, int64_t red) {
+  int cs = 1;
+  while (cs < kBwdCluster && tiles * cs < 3 * sm_count() && red > (int64_t)kBr * cs) cs *= 2;
+  return cs;
+}
+
+}  // namespace
+
+// The launch's time is 3.2 us, 1.85 us a block of 32 terms that follow one
+// another in a CTA and 4 ns a block in all (14 measured sizes, M1..4096, N19..2048,
+// K27..3712).  The tensor cores' way takes 10..16 us on the device for small
+// products, but four to six launches, 21..29 us of a caller's time.
+bool small_bwd_fits(int64_t M, int64_t N, int64_t K) {
+  const int64_t m = (M + kBm - 1) / kBm, n = (N + kBm - 1) / kBm, k = (K + kBn - 1) / kBn;
+  if (m > 4096 || n > 4096 || k > 4096) return false;
+  const int64_t cs = small_bwd_cluster((m + n) * k, max(M, N)), chain = (max(m, n) + cs - 1) / cs;
+  return 3.2 + 1.85 * (double)chain + 0.004 * (double)(2 * m * n * k) < kSmallBwdUs;
+}
+
+cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
+                             float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
+                             cudaStream_t s) {
+  using T = __nv_bfloat16;
+  if (K == 0) dx = dw = nullptr;
+  SmallBwd p{};
+  p.dout = static_cast<const T *>(dout), p.pre = static_cast<const T *>(pre);
+  p.x = static_cast<const T *>(x), p.w = static_cast<const T *>(w);
+  p.dx = static_cast<T *>(dx), p.dw = static_cast<T *>(dw), p.dbias = dbias;
+  p.M = M, p.N = N, p.K = K, p.ldx = ldx, p.ldw = ldw, p.act = act;
+  p.dx_tiles = dx ? tiles_of(M, K) : 0;
+  p.dw_tiles = dw ? tiles_of(N, K) : dbias ? tiles_of(N, 1) : 0;
+  const int64_t tiles = p.dx_tiles + p.dw_tiles;
+  if (tiles == 0) return cudaSuccess;
+  p.cs = small_bwd_cluster(tiles, max(dx ? N : 0, p.dw_tiles ? M : 0));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.cs));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.cs > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, small_bwd_kernel, p);
 }
 
 }  // namespace delta

@@ -607,14 +607,16 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
 // filling the pipeline and writing out a tile cost about 4 us.  A split adds a
 // turn through shared memory and (q - 1) / q of the tile's sums over the
 // cluster's network, which carries about 20 GB/s a CTA.
-template <bool kAMn, bool kBMn, bool kF8>
-cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
-  const int64_t M = g.epi.M, N = g.epi.N, sms = sm_count();
-  const int kblocks = (int)((g.K + (kF8 ? 127 : 63)) / (kF8 ? 128 : 64));
+struct Choice {
+  int shape, split;  // shape: pair of 256, pair of 128, one CTA of 128, of 64 columns
+  double us;
+};
+Choice choose(int64_t M, int64_t N, int64_t K, bool f8) {
+  const int64_t sms = sm_count();
+  const int64_t kblocks = (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
   struct Shape { int bn, pair; double us; };
   constexpr Shape shapes[4] = {{256, 1, 0.26}, {128, 1, 0.15}, {128, 0, 0.19}, {64, 0, 0.16}};
-  int best = 0, split = 1;
-  double least = 1e30;
+  Choice c{0, 1, 1e30};
   for (int i = 0; i < 4; ++i) {
     const int bn = shapes[i].bn, wide = shapes[i].pair ? 2 : 1, bm = kBM * wide;
     const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
@@ -626,9 +628,16 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
       const int64_t rounds = (tiles * q * wide + sms - 1) / sms;
       double us = (double)rounds * ((kblocks + q - 1) / q * shapes[i].us + bn * 0.005) + 3.0;
       if (q > 1) us += 1.3 + kBM * bn * 4 * (q - 1) / q / 20e3;
-      if (us < 0.98 * least) least = us, best = i, split = q;
+      if (us < 0.98 * c.us) c = Choice{i, q, us};
     }
   }
+  return c;
+}
+
+template <bool kAMn, bool kBMn, bool kF8>
+cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
+  const Choice c = choose(g.epi.M, g.epi.N, g.K, kF8);
+  const int best = c.shape, split = c.split;
   switch (best) {
     case 0: return run<256, true, kAMn, kBMn, kF8>(g, split, s);
     case 1: return run<128, true, kAMn, kBMn, kF8>(g, split, s);
@@ -638,6 +647,8 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
 }
 
 }  // namespace
+
+double gemm_tc_us(int64_t M, int64_t N, int64_t K, bool f8) { return choose(M, N, K, f8).us + 0.7; }
 
 cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s) {
   if (g.epi.kind == kLinE4m3) return g.a_mn || g.b_mn ? cudaErrorNotSupported : pick<false, false, true>(g, s);

@@ -137,22 +137,23 @@ __device__ __forceinline__ void load_weight(const void *weight, bool w_bf16, int
 // rows in a ring: three, or two where N tensors of the widest rows would pass a
 // CTA's shared memory
 __host__ __device__ constexpr int ring_rows(int N, int per, int V, int size) {
-  return V > 1 ? (N * per >= 12 ? 2 : 3) : N == 3 && per == 16 && size == 4 ? 2 : 3;
+  return V * size == 16 ? (N * per >= 12 ? 2 : 3) : N == 3 && per == 16 && size == 4 ? 2 : 3;
 }
 // bytes that the pieces covering a row take, wherever it starts
 __host__ __device__ constexpr int64_t cover(int64_t bytes) { return (bytes + 31) / 16 * 16; }
 
-// One row of N tensors, kPer vectors a thread.  Whole vectors (V > 1) are
-// copied and read by the thread that uses them; single elements lie in a
-// buffer that the row's threads share.
+// One row of N tensors, kPer vectors a thread.  Whole vectors (16 bytes) are
+// copied and read by the thread that uses them; single elements and pairs lie
+// in a buffer that the row's threads share.
 template <typename In, int V, int kPer, int N, int kT>
 struct Rows {
   using Vec = APack<In, V>;
+  static constexpr bool kOwn = V * sizeof(In) == 16;
   static constexpr int kStages = ring_rows(N, kPer, V, sizeof(In));
   const In *base[N];
   int64_t ld[N], rows, D;
-  unsigned char *ring;  // V > 1: [kStages][N][kPer][kT] vectors; else [kStages][N][rows a CTA][cover()] bytes
-  const In *now[V > 1 ? 1 : N];
+  unsigned char *ring;  // own: [kStages][N][kPer][kT] vectors; else [kStages][N][rows a CTA][cover()] bytes
+  const In *now[kOwn ? 1 : N];
   int slot = 0;
 
   // a shared buffer of tensor n, and where its row begins in it
@@ -169,7 +170,7 @@ struct Rows {
       for (int n = 0; n < N; ++n) {
         if (!base[n]) continue;
         const In *from = base[n] + row * ld[n];
-        if constexpr (V > 1) {
+        if constexpr (kOwn) {
           Vec *mine = reinterpret_cast<Vec *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
@@ -195,7 +196,7 @@ struct Rows {
   // the row becomes readable, and a later one is asked for
   __device__ __forceinline__ void turn(int64_t row, int64_t step) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    if constexpr (V == 1) {
+    if constexpr (!kOwn) {
       // of all the row's threads; and the last row's reads are over
       if (blockDim.x == 32)
         __syncwarp();
@@ -210,14 +211,12 @@ struct Rows {
   __device__ __forceinline__ void done() { slot = slot == kStages - 1 ? 0 : slot + 1; }
   __device__ __forceinline__ void finish() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
   __device__ __forceinline__ Vec get(int n, int j) const {
-    if constexpr (V > 1) {
+    if constexpr (kOwn) {
       const Vec *mine = reinterpret_cast<const Vec *>(ring) + threadIdx.y * blockDim.x + threadIdx.x;
       return mine[((slot * N + n) * kPer + j) * kT];
     } else {
-      const int64_t d = (int64_t)j * blockDim.x + threadIdx.x;
-      Vec v;
-      v.v[0] = now[n][d < D ? d : 0];
-      return v;
+      const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+      return *reinterpret_cast<const Vec *>(now[n] + (d < D ? d : 0));
     }
   }
 };
@@ -423,17 +422,16 @@ struct Plan {
   int smem;             // the ring
 };
 
-bool vec_ok(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
-
 // One vector a thread while rows are few (latency), two where a row has more
 // than a warp's worth and there are rows for every SM (fewer, longer-lived
 // CTAs); more only where a row would not fit kMostThreads threads.  Of single
 // elements as many as keep a row to few warps, one if it can be: then rows need
 // no barrier.
-Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors, int resident, bool many) {
+Plan plan(int64_t rows, int64_t D, int vec, int wide, int tensors, int resident, bool many) {
   Plan q;
   const int size = 16 / vec;
-  q.V = aligned ? vec : 1;
+  const bool aligned = wide == vec;
+  q.V = wide;
   const int64_t n = (D + q.V - 1) / q.V;  // vectors a row
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -441,6 +439,7 @@ Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors, int resid
     q.per = rows >= 2 * sms && n > 32 ? 2 : 1;
   else
     q.per = rows < 2 * sms ? (n <= 256 ? 1 : 4) : n <= 32 ? 1 : n <= 128 ? 4 : n <= 256 ? 8 : 16;
+  if (q.V == 2 && q.per > 8) q.per = 8;
   while (n > (int64_t)q.per * kMostThreads) q.per *= 2;
   q.nt = (int)((n + q.per - 1) / q.per + 31) / 32 * 32;
   q.rpc = q.nt >= 256 ? 1 : 256 / q.nt;
@@ -464,10 +463,17 @@ Plan plan(int64_t rows, int64_t D, int vec, bool aligned, int tensors, int resid
 }
 
 // the instance for a plan: up to 4 (float32) or 2 (bfloat16) vectors of 16
-// bytes a thread, or up to 16 single elements, which covers kNormMaxD
+// bytes a thread, up to 8 pairs, or up to 16 single elements, which covers kNormMaxD
 template <typename In, template <typename, int, int> class F, typename... X>
 cudaError_t dispatch(const Plan &q, X &&...x) {
   constexpr int V = 16 / sizeof(In);
+  if constexpr (sizeof(In) == 2)
+    if (q.V == 2) switch (q.per) {
+        case 1: return F<In, 2, 1>::run(x...);
+        case 4: return F<In, 2, 4>::run(x...);
+        case 8: return F<In, 2, 8>::run(x...);
+        default: return cudaErrorInvalidConfiguration;
+      }
   if (q.V == 1) switch (q.per) {
       case 1: return F<In, 1, 1>::run(x...);
       case 4: return F<In, 1, 4>::run(x...);
@@ -514,16 +520,19 @@ struct BwdOne {
 template <typename In>
 cudaError_t fwd_all(const NormArgs &a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(In);
-  const bool ok = a.D % V == 0 && a.ldx % V == 0 && (!a.residual || a.ldr % V == 0) && vec_ok(a.x) &&
-                  vec_ok(a.residual);
-  const Plan q = plan(a.rows, a.D, V, ok, 2, a.scale ? kQuantThreads : kSmThreads, true);
+  // whole vectors, pairs, or single elements, by what every row's start allows
+  const auto ok = [&](int n) {
+    const auto at = [&](const void *p) { return reinterpret_cast<uintptr_t>(p) % (n * sizeof(In)) == 0; };
+    return a.D % n == 0 && a.ldx % n == 0 && (!a.residual || a.ldr % n == 0) && at(a.x) && at(a.residual);
+  };
+  const Plan q = plan(a.rows, a.D, V, ok(V) ? V : V == 8 && ok(2) ? 2 : 1, 2, a.scale ? kQuantThreads : kSmThreads, true);
   return dispatch<In, FwdOne>(q, a, q, s);
 }
 
 template <typename In>
 Plan bwd_plan(const NormBwdArgs &a) {
   constexpr int V = 16 / sizeof(In);
-  return plan(a.rows, a.D, V, a.D % V == 0, 3, kSmThreads, false);
+  return plan(a.rows, a.D, V, a.D % V == 0 ? V : V == 8 && a.D % 2 == 0 ? 2 : 1, 3, kSmThreads, false);
 }
 template <typename In>
 cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
