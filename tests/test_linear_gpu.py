@@ -61,6 +61,8 @@ def check(out, pre, x, w, b, res, act, scales=None):
     within(out, o, eo + half * (o.abs() + eo), "out")
 
 
+# gradients on both sides of the bound of the one-launch form, sums over 1..8 CTAs
+MIDDLE = [(1, 512, 512), (64, 512, 512), (100, 101, 102), (513, 40, 64), (260, 515, 333), (2816, 19, 257), (40, 1100, 330)]
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1000, 4096), (3, 17, 7), (8, 128, 200), (9, 100, 1024), (16, 257, 72),
           (17, 513, 130), (31, 40, 513), (32, 2048, 512), (33, 64, 64), (64, 65, 8), (100, 257, 63),
           (127, 8, 1000), (129, 300, 65), (300, 520, 1000), (257, 1024, 2048),
@@ -150,7 +152,7 @@ def gradients(got, x, w, do, pre, act):
 
 
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
-@pytest.mark.parametrize("shape", [s for s in SHAPES if s[1] < 1000] + [(300, 2600, 2100), (2100, 300, 2600)], ids=str)
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[1] < 1000] + [(300, 2600, 2100), (2100, 300, 2600)] + MIDDLE, ids=str)
 def test_gradients_bf16(shape, act):
     x, w, b, _, do = inputs(*shape, BF, sum(shape) + 1)
     pre = None if act == "none" else (x.float() @ w.float().T + b).to(BF)
@@ -158,12 +160,15 @@ def test_gradients_bf16(shape, act):
     got = wr.delta_linear_bwd(*args, act=act)
     again = wr.delta_linear_bwd(*args, act=act)
     part = wr.delta_linear_bwd(*args, act=act, want=(False, True, False))
+    rest = wr.delta_linear_bwd(*args, act=act, want=(True, False, False))
+    sums = wr.delta_linear_bwd(*args, act=act, want=(False, False, True))
     torch.cuda.synchronize()
     wr.delta_check_device()
     gradients(got, x, w, do, pre, act)
     for a, c in zip(got, again):
         assert torch.equal(a, c)
     assert part[0] is None and part[2] is None and torch.equal(part[1], got[1])
+    assert torch.equal(rest[0], got[0]) and torch.equal(sums[2], got[2])
 
 
 @pytest.mark.parametrize("M,N", [(5, 72), (150, 72), (1500, 520)])

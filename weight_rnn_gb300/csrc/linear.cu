@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
         for (int i = 0; i < V; ++i) {
           float v = to_f(d[k].v[i]);
           if (p.act != kActNone) v *= slope(p.act, to_f(q[k].v[i]));
-          s[i] += v;
+          s[i] = __fadd_rn(s[i], v);  // not contracted: the same with dpre wanted and without
           from_f(v, o.v[i]);
         }
         if (p.dpre) *reinterpret_cast<Vec *>(static_cast<T *>(p.dpre) + m * p.ldp + c) = o;
@@ -562,7 +562,8 @@ cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, con
   p.dw_tiles = dw ? tiles_of(N, K) : dbias ? tiles_of(N, 1) : 0;
   const int64_t tiles = p.dx_tiles + p.dw_tiles;
   if (tiles == 0) return cudaSuccess;
-  p.cs = small_bwd_cluster(tiles, max(dx ? N : 0, p.dw_tiles ? M : 0));
+  // of all gradients' tiles, whichever are wanted, so that each has the same value
+  p.cs = small_bwd_cluster(tiles_of(M, K) + tiles_of(N, K), max(M, N));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * p.cs));
   cfg.blockDim = dim3(256);
