@@ -470,6 +470,7 @@ int dpre_vec(const DpreArgs &p) {
 // outputs take a round, of 1.15 us and 1.06 us per KB of a row of w; twice as
 // long where pieces are put together, three times of 8-bit elements.
 double linear_small_us(int64_t M, int64_t N, int64_t K, bool f8, bool whole) {
+  if (M > 65535 * 16) return 1e30;  // (a grid's height)
   const double ctas = (double)((M + 15) / 16) * (double)((N + 15) / 16);
   return (2.0 + ctas / 512.0 * (1.15 + 1.06 * (double)K * (f8 ? 1 : 2) / 1024.0)) * (whole ? 1.0 : f8 ? 3.0 : 2.0);
 }
