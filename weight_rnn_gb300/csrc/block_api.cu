@@ -186,10 +186,12 @@ struct Operand {
   bool whole() const { return aligned16(p) && ld * size % 16 == 0; }
   int64_t ldp() const { return up(cols, 128 / size); }  // whole lines: a copied box row touches one
   int64_t bytes() const { return rows * ldp() * size; }
-  cudaError_t pack(Scratch &scr, cudaStream_t s) {
+  // after: a kernel of this call has been launched
+  cudaError_t pack(Scratch &scr, bool &after, cudaStream_t s) {
     if (whole()) return cudaSuccess;
     void *to = scr.cut(bytes());
-    const cudaError_t e = delta::launch_pack(p, to, rows, cols, ld, ldp(), size, s);
+    const cudaError_t e = delta::launch_pack(p, to, rows, cols, ld, ldp(), size, after, s);
+    after = true;
     p = to;
     ld = ldp();
     return e;
@@ -199,7 +201,7 @@ Operand operand(const void *p, int64_t rows, int64_t cols, int64_t ld, int size)
   return Operand{p, rows, cols, rows > 1 ? ld : up(cols, 16 / size), size};
 }
 
-constexpr double kPackUs = 10.0;  // scratch and two more kernels
+constexpr double kPackUs = 6.0;  // scratch and two more kernels
 
 cudaError_t linear_forward(const delta::LinearArgs &a, cudaStream_t s) {
   if (a.kind == delta::kLinF32)
@@ -221,9 +223,10 @@ cudaError_t linear_forward(const delta::LinearArgs &a, cudaStream_t s) {
   if (!w.whole()) scr.want(w.bytes());
   cudaError_t err = scr.take();
   if (err != cudaSuccess) return err;
-  err = x.pack(scr, s);
-  if (err == cudaSuccess) err = w.pack(scr, s);
-  if (err == cudaSuccess) err = delta::launch_gemm_tc({x.p, w.p, x.ld, w.ld, a.K, false, false, a}, s);
+  bool after = false;
+  err = x.pack(scr, after, s);
+  if (err == cudaSuccess) err = w.pack(scr, after, s);
+  if (err == cudaSuccess) err = delta::launch_gemm_tc({x.p, w.p, x.ld, w.ld, a.K, false, false, a, after}, s);
   const cudaError_t ef = scr.release();
   return err != cudaSuccess ? err : ef;
 }
@@ -299,21 +302,23 @@ cudaError_t linear_backward(const void *x, const void *w, const void *dout, cons
   if ((err = scr.take()) != cudaSuccess) return err;
   d.dpre = form ? scr.cut(M * d.ldp * e) : nullptr;
   if (dbias) d.partial = static_cast<float *>(scr.cut(parts * N * 4));
-  if (form || dbias) err = delta::launch_dpre(d, s);
-  if (err == cudaSuccess && packx) err = ox.pack(scr, s);
-  if (err == cudaSuccess && packw) err = ow.pack(scr, s);
+  bool after = form || dbias;
+  if (after) err = delta::launch_dpre(d, s);
+  if (err == cudaSuccess && packx) err = ox.pack(scr, after, s);
+  if (err == cudaSuccess && packw) err = ow.pack(scr, after, s);
   const void *g = form ? d.dpre : dout;
   delta::LinearArgs p{};
   p.kind = bf16 ? delta::kLinBf16 : delta::kLinF32;
   if (err == cudaSuccess && dx) {
     p.out = dx; p.M = M; p.N = K;
-    err = bf16 ? delta::launch_gemm_tc({g, ow.p, d.ldp, ow.ld, N, false, true, p}, s)
+    err = bf16 ? delta::launch_gemm_tc({g, ow.p, d.ldp, ow.ld, N, false, true, p, after}, s)
                : delta::launch_gemm_f32(p, static_cast<const float *>(g), d.ldp, 1, static_cast<const float *>(w), 1,
                                         ldw, N, s);
+    after = true;
   }
   if (err == cudaSuccess && dw) {
     p.out = dw; p.M = N; p.N = K;
-    err = bf16 ? delta::launch_gemm_tc({g, ox.p, d.ldp, ox.ld, M, true, true, p}, s)
+    err = bf16 ? delta::launch_gemm_tc({g, ox.p, d.ldp, ox.ld, M, true, true, p, after}, s)
                : delta::launch_gemm_f32(p, static_cast<const float *>(g), 1, d.ldp, static_cast<const float *>(x), 1,
                                         ldx, M, s);
   }

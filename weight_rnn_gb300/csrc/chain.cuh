@@ -1,0 +1,44 @@
+// chain.cuh -- kernels of one call that follow one another: a kernel launched
+// as a dependent starts while the one before it still runs, sets itself up,
+// and waits with chain_wait() for that kernel's end and memory before it reads
+// or writes any.  Every thread of it waits, so that its own end implies the end
+// of all before it.  The first kernel of a call is launched in the ordinary
+// way: what a caller's kernel holds (tensor memory, for one) is not known.
+// A gap between two kernels of a call shrinks from about 2.5 us to 1.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace delta {
+
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// the next kernel's CTAs may take the places that this one leaves free
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t chain_launch(void (*kern)(P...), dim3 grid, dim3 block, int smem, int cluster, bool dependent,
+                         cudaStream_t s, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = (unsigned)n;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+}  // namespace delta

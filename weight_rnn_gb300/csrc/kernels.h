@@ -194,6 +194,7 @@ struct GemmArgs {
   int64_t lda, ldb, K;
   bool a_mn, b_mn;
   LinearArgs epi;  // M, N, out and the epilogue
+  bool dependent;  // follows a kernel of the same call
 };
 cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s);
 // about how long it takes
@@ -206,7 +207,7 @@ cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s);
 double linear_small_us(int64_t M, int64_t N, int64_t K, bool f8, bool whole);
 // all gradients of a small bfloat16 layer (those whose pointers are set), in one
 // launch without scratch
-constexpr double kSmallBwdUs = 15;
+constexpr double kSmallBwdUs = 12;
 bool small_bwd_fits(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                              float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
@@ -216,7 +217,7 @@ cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, i
                             int64_t bn, int64_t bk, int64_t K, cudaStream_t s);
 // rows x cols elements of `size` bytes into rows of ldp elements
 cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, int64_t ldp,
-                        int size, cudaStream_t s);
+                        int size, bool dependent, cudaStream_t s);
 // dpre = dout * act'(pre) in rows of ldp elements where dpre is set, and dbias = its column sums in float32 where dbias is set
 struct DpreArgs {
   const void *dout, *pre;

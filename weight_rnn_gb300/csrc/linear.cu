@@ -3,6 +3,7 @@
 // elementwise part of the gradients.
 #include <cooperative_groups.h>
 
+#include "chain.cuh"
 #include "linear.cuh"
 
 namespace delta {
@@ -238,6 +239,8 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(LinearArgs e, const float
 __global__ void __launch_bounds__(256) pack_kernel(const unsigned char *src, unsigned char *dst, int64_t rows,
                                                    int64_t bytes, int64_t ld, int64_t ldp) {
   constexpr int kAhead = 4;
+  chain_next();
+  chain_wait();
   const uintptr_t lo = reinterpret_cast<uintptr_t>(src), hi = lo + (rows - 1) * ld + bytes;
   for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.y; r < rows; r += (int64_t)gridDim.x * 8) {
     const uintptr_t row = lo + r * ld;
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
   struct __align__(sizeof(T) * V) Vec { T v[V]; };
   __shared__ float sum[8][32 * V];
   const int64_t c = ((int64_t)blockIdx.x * 32 + threadIdx.x) * V;
+  chain_next();
   float s[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = 0.f;
@@ -490,11 +494,11 @@ cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, i
 }
 
 cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, int64_t ldp, int size,
-                        cudaStream_t s) {
+                        bool dependent, cudaStream_t s) {
   const int64_t want = (rows + 7) / 8, cap = (int64_t)sm_count() * 8;
-  pack_kernel<<<(unsigned)(want < cap ? want : cap), dim3(32, 8), 0, s>>>(
-      static_cast<const unsigned char *>(src), static_cast<unsigned char *>(dst), rows, cols * size, ld * size, ldp * size);
-  return cudaGetLastError();
+  return chain_launch(pack_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(32, 8), 0, 1, dependent, s,
+                      static_cast<const unsigned char *>(src), static_cast<unsigned char *>(dst), rows, cols * size,
+                      ld * size, ldp * size);
 }
 
 int64_t dpre_parts(const DpreArgs &p) {

@@ -24,6 +24,7 @@
 // so that the CTAs at work at a time share operand rows in L2.  Every mbarrier
 // wait is bounded: a timeout sets a device error word and the kernel winds
 // down.
+#include "chain.cuh"
 #include "linear.cuh"
 #include "sm100.cuh"
 #include "tma_host.h"
@@ -339,6 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair || kSplit) cluster_sync();  // barriers and TMEM of all its CTAs are ready
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // (and no chain_next(): a next product's CTA could take tensor memory that a
+  // CTA of this one has yet to ask for)
+  chain_wait();
 
   // The producer's and the issuer's loops run warp-wide, with one elected lane
   // issuing: in code that only one lane reaches, the compiler cannot keep
@@ -580,19 +584,9 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
   constexpr int smem = smem_bytes(BN, kPair);
   if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
   const int64_t ctas = (kPair ? 2 : 1) * split, fit = sm_count() / ctas;
-  cudaLaunchConfig_t cfg = {};
   // persistent, but for a split product: one cluster a tile
-  cfg.gridDim = dim3((unsigned)((kSplit || t.total < fit ? t.total : fit) * ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, t, e, aligned, wide);
+  return chain_launch(kern, dim3((unsigned)((kSplit || t.total < fit ? t.total : fit) * ctas)), dim3(kThreads), smem,
+                      (int)ctas, g.dependent, s, ma, mb, t, e, aligned, wide);
 }
 
 template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>

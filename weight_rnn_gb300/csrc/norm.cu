@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "chain.cuh"
 #include "kernels.h"
 
 namespace delta {
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) norm_
   __shared__ float part[2][8 * 32];
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
+  chain_next();
   float w[kPer][V], dw[kPer][V];
   load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
 #pragma unroll
@@ -400,6 +402,8 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
   __shared__ float s[R][C + 1];
   const int64_t d = (int64_t)blockIdx.x * C + threadIdx.x;
   float v = 0.f;
+  chain_next();
+  chain_wait();
   if (d < D)
     for (int64_t i = threadIdx.y; i < n; i += R) v += partial[i * D + d];
   s[threadIdx.y][threadIdx.x] = v;
@@ -546,11 +550,10 @@ cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_column_sum(const float *partial, float *out, int64_t n, int64_t D, cudaStream_t s) {
-  if (D < 1024)
-    column_sum_kernel<8><<<(unsigned)((D + 7) / 8), dim3(8, 128), 0, s>>>(partial, out, n, D);
-  else
-    column_sum_kernel<32><<<(unsigned)((D + 31) / 32), dim3(32, 32), 0, s>>>(partial, out, n, D);
-  return cudaGetLastError();
+  return D < 1024 ? chain_launch(column_sum_kernel<8>, dim3((unsigned)((D + 7) / 8)), dim3(8, 128), 0, 1, true, s,
+                                 partial, out, n, D)
+                  : chain_launch(column_sum_kernel<32>, dim3((unsigned)((D + 31) / 32)), dim3(32, 32), 0, 1, true, s,
+                                 partial, out, n, D);
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
