@@ -1,10 +1,11 @@
-// chain.cuh -- kernels of one call that follow one another: a kernel launched
-// as a dependent starts while the one before it still runs, sets itself up,
-// and waits with chain_wait() for that kernel's end and memory before it reads
-// or writes any.  Every thread of it waits, so that its own end implies the end
-// of all before it.  The first kernel of a call is launched in the ordinary
-// way: what a caller's kernel holds (tensor memory, for one) is not known.
-// A gap between two kernels of a call shrinks from about 2.5 us to 1.
+// chain.cuh -- kernels that follow one another on a stream: a kernel launched as
+// a dependent may start while the one before it ends, sets itself up, and waits
+// with chain_wait() for that kernel's end and memory before it reads or writes
+// any.  Every thread of it waits, so that its own end implies the end of all
+// before it.  A call's first kernel is a dependent too, but where the call goes
+// on to the tensor-core product: that takes tensor memory while it waits, and a
+// caller's kernel before it may have yet to take some.
+// A gap between two kernels shrinks from about 2.5 us to 1.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
+  chain_next();
+  chain_wait();
   const int64_t n0 = (int64_t)(blockIdx.x / cs) * 16, m0 = (int64_t)blockIdx.y * kTok;
   if (cs > 1) cg::this_cluster().barrier_arrive();
   const int64_t bytes = a.K * kSize;
@@ -181,18 +183,8 @@ cudaError_t run_small(const LinearArgs &a, cudaStream_t s) {
   const int64_t groups = (a.N + 15) / 16, passes = (a.M + 8 * NT - 1) / (8 * NT), turns = (a.K * size + kBlocks * 64 - 1) / (kBlocks * 64);
   int cs = 1;
   while (cs < kMaxCluster && groups * passes * cs < 2 * sm_count() && turns > (int64_t)kSmallWarps * cs) cs *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * cs), (unsigned)passes);
-  cfg.blockDim = dim3(kSmallWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
-  return vec ? cudaLaunchKernelEx(&cfg, small_kernel<kF8, NT, true>, a, cs)
-             : cudaLaunchKernelEx(&cfg, small_kernel<kF8, NT, false>, a, cs);
+  return chain_launch(vec ? small_kernel<kF8, NT, true> : small_kernel<kF8, NT, false>,
+                      dim3((unsigned)(groups * cs), (unsigned)passes), dim3(kSmallWarps * 32), 0, cs, true, s, a, cs);
 }
 
 // ------------------------------------------------------ float32, CUDA cores
@@ -355,6 +347,8 @@ __global__ void __launch_bounds__(256) small_bwd_kernel(SmallBwd p) {
   const int tid = threadIdx.x, cs = p.cs;
   const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
   if (cs > 1) cg::this_cluster().barrier_arrive();
+  chain_next();
+  chain_wait();
   int64_t tile = blockIdx.x / cs;
   const bool of_w = tile >= p.dx_tiles;  // same for a cluster
   if (of_w) tile -= p.dx_tiles;
@@ -569,17 +563,7 @@ cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, con
   if (tiles == 0) return cudaSuccess;
   // of all gradients' tiles, whichever are wanted, so that each has the same value
   p.cs = small_bwd_cluster(tiles_of(M, K) + tiles_of(N, K), max(M, N));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.cs));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = p.cs > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, small_bwd_kernel, p);
+  return chain_launch(small_bwd_kernel, dim3((unsigned)(tiles * p.cs)), dim3(256), 0, p.cs, true, s, p);
 }
 
 }  // namespace delta

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? (kQuant ? kQuantThreads : 
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
   float w[kPer][V];
+  chain_wait();
   load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) norm_
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5;
   chain_next();
+  chain_wait();
   float w[kPer][V], dw[kPer][V];
   load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
 #pragma unroll
@@ -402,8 +404,9 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
   __shared__ float s[R][C + 1];
   const int64_t d = (int64_t)blockIdx.x * C + threadIdx.x;
   float v = 0.f;
-  chain_next();
   chain_wait();
+  // (no chain_next(): the next gradient's CTAs, whose rows are dealt out evenly,
+  // would crowd on the SMs that are free early; 94 -> 108 us)
   if (d < D)
     for (int64_t i = threadIdx.y; i < n; i += R) v += partial[i * D + d];
   s[threadIdx.y][threadIdx.x] = v;
@@ -500,8 +503,7 @@ cudaError_t go(K kern, const A &a, const Plan &q, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, q.smem);
     if (e != cudaSuccess) return e;
   }
-  kern<<<(unsigned)q.grid, dim3(q.nt, q.rpc), q.smem, s>>>(a);
-  return cudaGetLastError();
+  return chain_launch(kern, dim3((unsigned)q.grid), dim3(q.nt, q.rpc), q.smem, 1, true, s, a);
 }
 
 template <typename In, int V, int kPer>

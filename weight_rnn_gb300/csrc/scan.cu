@@ -34,6 +34,7 @@
 
 #include <type_traits>
 
+#include "chain.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 
@@ -314,6 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // the same for all lanes, also to the compiler
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
+  chain_wait();
   const int64_t id = kCluster ? blockIdx.x / cs : blockIdx.x;
   const int64_t b = id / strips, first = (id % strips) * kRow, c0 = first + lane * VEC;
   const bool live = c0 < p.D;
@@ -485,6 +487,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int rank = kCluster ? (int)(blockIdx.x % cs) : 0;
+  chain_wait();
   const int64_t id = kCluster ? blockIdx.x / cs : blockIdx.x;
   const int64_t b = id / strips, first = (id % strips) * kRow, c0 = first + lane * VEC;
   const bool live = c0 < p.D;
@@ -700,6 +703,8 @@ template <typename In, bool kSig, int VEC>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs p, int64_t n) {
   using Gate = typename std::conditional<kSig, In, float>::type;
   const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
+  chain_next();
+  chain_wait();
   if (i0 >= n) return;
   const int64_t b = i0 / p.D, c = i0 - b * p.D;
   float xv[VEC], gv[VEC], hv[VEC], a[VEC], u[VEC];
@@ -755,18 +760,7 @@ cudaError_t launch(K kern, const A &p, int64_t rows, int64_t strips, int cs, int
   if (e != cudaSuccess) return e;
   if (cs > 8 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
     return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * cs));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p, cs, strips);
+  return chain_launch(kern, dim3((unsigned)(rows * cs)), dim3(kWarps * 32), smem, cs, true, s, p, cs, strips);
 }
 
 template <typename In, bool kSig, int VEC, bool kWide>
@@ -792,8 +786,7 @@ cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
 template <typename In, bool kSig, int VEC>
 cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
   const int64_t n = a.B * a.D, blocks = (n / VEC + 255) / 256;
-  scan_step_kernel<In, kSig, VEC><<<(unsigned)blocks, 256, 0, s>>>(a, n);
-  return cudaGetLastError();
+  return chain_launch(scan_step_kernel<In, kSig, VEC>, dim3((unsigned)blocks), dim3(256), 0, 1, true, s, a, n);
 }
 
 }  // namespace
