@@ -13,7 +13,9 @@
 namespace delta {
 
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// the next kernel's CTAs may take the places that this one leaves free
+// The next kernel's CTAs may take the places that this one leaves free: for a
+// next kernel of the same call.  A call's last kernel leaves it out, since CTAs
+// that come one by one crowd on the SMs that are free first.
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>

@@ -207,7 +207,7 @@ cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s);
 double linear_small_us(int64_t M, int64_t N, int64_t K, bool f8, bool whole);
 // all gradients of a small bfloat16 layer (those whose pointers are set), in one
 // launch without scratch
-constexpr double kSmallBwdUs = 12;
+constexpr double kSmallBwdUs = 14;
 bool small_bwd_fits(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                              float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,

@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
-  chain_next();
   chain_wait();
   const int64_t n0 = (int64_t)(blockIdx.x / cs) * 16, m0 = (int64_t)blockIdx.y * kTok;
   if (cs > 1) cg::this_cluster().barrier_arrive();
@@ -347,8 +346,7 @@ __global__ void __launch_bounds__(256) small_bwd_kernel(SmallBwd p) {
   const int tid = threadIdx.x, cs = p.cs;
   const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
   if (cs > 1) cg::this_cluster().barrier_arrive();
-  chain_next();
-  chain_wait();
+  chain_wait();  // (chain_next(): 512 x 512 x 128 13 -> 17 us, the next CTAs crowd on free SMs)
   int64_t tile = blockIdx.x / cs;
   const bool of_w = tile >= p.dx_tiles;  // same for a cluster
   if (of_w) tile -= p.dx_tiles;
@@ -538,8 +536,9 @@ int small_bwd_cluster(int64_t tiles, int64_t red) {
 
 // The launch's time is 3.2 us, 1.85 us a block of 32 terms that follow one
 // another in a CTA and 4 ns a block in all (14 measured sizes, M1..4096, N19..2048,
-// K27..3712).  The tensor cores' way takes 10..16 us on the device for small
-// products, but four to six launches, 21..29 us of a caller's time.
+// K27..3712).  The tensor cores' way takes 10..13 us for small products from a
+// graph, but is four to six launches, 16..20 us of a caller's time (M512 N512
+// K128: 13 us a call for 16.5; M200 N300 K400: 16.6 for 15.9).
 bool small_bwd_fits(int64_t M, int64_t N, int64_t K) {
   const int64_t m = (M + kBm - 1) / kBm, n = (N + kBm - 1) / kBm, k = (K + kBn - 1) / kBn;
   if (m > 4096 || n > 4096 || k > 4096) return false;

@@ -703,7 +703,6 @@ template <typename In, bool kSig, int VEC>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs p, int64_t n) {
   using Gate = typename std::conditional<kSig, In, float>::type;
   const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
-  chain_next();
   chain_wait();
   if (i0 >= n) return;
   const int64_t b = i0 / p.D, c = i0 - b * p.D;
