@@ -460,7 +460,10 @@ typedef enum {
  *
  * over B rows of T steps and D channels, a_t and u_t from the form above.  In
  * the linear form a step with a_t = 0 drops the state whatever it holds (Inf
- * and NaN included); in the sigmoid form a logit of -Inf gives a_t = 0.
+ * and NaN included), and nothing else does; in the sigmoid form a logit of -Inf
+ * gives a_t = 0.  Products of gates may leave float32's range where no state does
+ * (gates above 1, gates near 0 on states above 2^16): such channels are gone
+ * through again step by step, which is right and takes long.
  *
  *   x       [B, T, D]  dtype    element strides x_sb, x_st, 1
  *   gate    [B, T, D]  float32 (linear) or dtype (sigmoid), strides g_sb, g_st, 1

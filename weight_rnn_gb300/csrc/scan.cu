@@ -29,6 +29,24 @@
 // is wait for, every output store: it took a third of the cycles).  The fold
 // order is the time order, so results do not depend on scheduling.  All maps and states are
 // float32; two channels of a lane go through packed float32 pairs.
+//
+// A map stands for its steps only while its decay A and offsets B are float32
+// numbers, and a product of decays can leave float32's range where no state does.
+// In the linear form a warp's product is therefore taken with subnormals flushed:
+// one that has left the normal range at any point ends as 0, Inf or NaN, and is
+// then looked at again (look, settle):
+//   a reset among the steps: A is 0, and 0 in a warp's map means that;
+//   decays of at most 1: A is kept as a subnormal, never 0, which carries Inf and
+//     NaN on and is off by less than 2^-145, nothing next to states up to 2^16;
+//   else, where |A| passes 2^24 (B's rounding then hides a state that B all but
+//     cancels), and where B is not finite: A is NaN, the map is not used.
+// A warp whose map is one of these looks at its own state, which is what the map
+// was applied to.  A cluster's maps are joined and sent unchecked; their CTA checks
+// them while they are on their way (misjoined, misused).  Sigmoid decays are at
+// most 1 and drop nothing, so there only a state that became NaN is suspect (Inf
+// times a product that is 0).  Where a map did not hold, every CTA of the row goes
+// through those channels again at its end, step by step (redo): 130 to 290 ns a step,
+// which data in range never takes.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -125,6 +143,17 @@ __device__ __forceinline__ void vmul(const float (&a)[VEC], const float (&b)[VEC
     d[0] = __fmul_rn(a[0], b[0]);  // (not to be fused: the same bits on every path, as for pairs)
   }
 }
+// the same with subnormal factors and results as 0
+template <int VEC>
+__device__ __forceinline__ void vmul_ftz(const float (&a)[VEC], const float (&b)[VEC], float (&d)[VEC]) {
+  if constexpr (VEC == 2) {
+    uint64_t r;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    unpk(r, d);
+  } else {
+    asm("mul.rn.ftz.f32 %0, %1, %2;" : "=f"(d[0]) : "f"(a[0]), "f"(b[0]));
+  }
+}
 template <int VEC>
 __device__ __forceinline__ void vadd(const float (&a)[VEC], const float (&b)[VEC], float (&d)[VEC]) {
   if constexpr (VEC == 2) {
@@ -138,7 +167,7 @@ __device__ __forceinline__ void vadd(const float (&a)[VEC], const float (&b)[VEC
 
 // d = a h + b, the step map; with kDrop a = 0 drops h whatever it holds.  The
 // selects that this takes are half of the linear form's instructions, so a warp
-// uses them only where a map has a decay that is 0 (or not a number) in it.
+// uses them for its steps only where a reset is among them.
 template <bool kDrop, int VEC>
 __device__ __forceinline__ void affine(const float (&a)[VEC], const float (&h)[VEC], const float (&b)[VEC],
                                        float (&d)[VEC]) {
@@ -158,15 +187,6 @@ __device__ __forceinline__ void decay(const float (&a)[VEC], const float (&h)[VE
   vmul(a, h, r);
 #pragma unroll
   for (int i = 0; i < VEC; ++i) d[i] = kDrop && a[i] == 0.f ? 0.f : r[i];
-}
-
-// whether the map of any lane that has channels drops a state
-template <int VEC>
-__device__ __forceinline__ bool drops(const float (&a)[VEC], bool live) {
-  bool z = false;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) z |= !(fabsf(a[i]) > 0.f);
-  return __any_sync(0xffffffffu, z && live);
 }
 
 // a and u from the gate.  Sigmoid: e = 2^min(-f log2 e, 126) stays finite, so
@@ -261,6 +281,209 @@ struct Map {
   float a[VEC], b[kOffsets][VEC];
 };
 
+constexpr float kNormal = 1.1754943508222875e-38f;  // 2^-126
+constexpr float kLeast = 1.401298464324817e-45f;    // 2^-149, the smallest subnormal
+constexpr float kLooseState = 65536.f;              // the largest state that a subnormal decay is used on
+constexpr float kMostGrowth = 16777216.f;           // 2^24
+// A warp's decay that needs no look.  Eight such make a CTA's at most 2^8, and one
+// that falls to 0 on the way has lost no more than 2^-126 of a state of 2^16.
+constexpr float kPlain = 2.f;
+__device__ __forceinline__ float infinity() { return __int_as_float(0x7f800000); }
+__device__ __forceinline__ float unusable() { return __int_as_float(0x7fffffff); }
+__device__ __forceinline__ bool subnormal(float v) { return v != 0.f && fabsf(v) < kNormal; }
+
+// whether a map of the linear form needs no second look: its decays are normal
+// numbers of at most 2, or 0 by a reset
+template <int VEC, int kOffsets>
+__device__ __forceinline__ bool plain(const Map<VEC, kOffsets> &m, const bool (&reset)[VEC]) {
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) ok &= (m.a[i] != 0.f || reset[i]) && fabsf(m.a[i]) <= kPlain;
+  return ok;
+}
+
+// The map of a warp's n steps in the linear form again, step(s, a, x, d) giving
+// them (in the reverse d too).  For what a reset alone does not explain: a rolled
+// loop, so that it takes little of the instruction cache.
+struct Settled {
+  bool drop;     // a reset is among the steps of any lane
+  bool strange;  // some map has to be checked against the state that it is applied to
+  bool loose;    // some decay is neither 0 nor a normal number of at most 2
+};
+template <int S, int VEC, int kOffsets, typename F>
+__device__ __forceinline__ Settled settle(Map<VEC, kOffsets> &m, int64_t n, bool live, F &&step) {
+  float p[VEC], top[VEC], a[VEC], x[VEC], d[VEC];
+  bool reset[VEC], any = false, strange = false, loose = false;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    p[i] = 1.f, top[i] = 0.f, reset[i] = false;
+#pragma unroll
+    for (int o = 0; o < kOffsets; ++o) m.b[o][i] = 0.f;
+  }
+#pragma unroll 1
+  for (int s = 0; s < S && s < n; ++s) {
+    step(s, a, x, d);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const bool z = a[i] == 0.f;
+      reset[i] |= z;
+      p[i] = __fmul_rn(p[i], a[i]);
+      top[i] = fmaxf(top[i], fabsf(a[i]));
+      m.b[0][i] = z || s == 0 ? x[i] : fmaf(a[i], m.b[0][i], x[i]);
+    }
+  }
+  if constexpr (kOffsets == 2) {
+#pragma unroll 1
+    for (int s = n < S ? (int)n - 1 : S - 1; s >= 0; --s) {
+      step(s, a, x, d);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) m.b[1][i] = a[i] == 0.f ? 0.f : __fmul_rn(a[i], __fadd_rn(d[i], m.b[1][i]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    bool whole = true;
+#pragma unroll
+    for (int o = 0; o < kOffsets; ++o) whole &= fabsf(m.b[o][i]) < infinity();
+    if (reset[i])
+      m.a[i] = 0.f;
+    else if (m.a[i] == 0.f && top[i] <= 1.f && whole)
+      m.a[i] = p[i] != 0.f ? p[i] : copysignf(kLeast, p[i]);
+    else if (!(m.a[i] != 0.f && fabsf(m.a[i]) <= kMostGrowth && whole))
+      m.a[i] = unusable();
+    any |= reset[i];
+    strange |= m.a[i] != m.a[i] || subnormal(m.a[i]);
+    loose |= !whole || !(fabsf(m.a[i]) <= kPlain) || subnormal(m.a[i]);
+  }
+  return {__any_sync(0xffffffffu, any && live) != 0, __any_sync(0xffffffffu, strange && live) != 0,
+          __any_sync(0xffffffffu, loose && live) != 0};
+}
+
+// The CTA's warps have stored their maps.  Returns whether those of any warp are
+// loose, where that is asked for.
+template <bool kAsk>
+__device__ __forceinline__ bool meet(bool loose) {
+  if constexpr (kAsk) return __syncthreads_or(loose);
+  __syncthreads();
+  return false;
+}
+
+// A map as its product of decays came out, looked at again if need be: restart()
+// takes the offsets again with resets, step() is for settle.
+template <int S, int VEC, int kOffsets, typename R, typename F>
+__device__ __forceinline__ Settled look(const float (&a)[S][VEC], Map<VEC, kOffsets> &m, int64_t n, bool live,
+                                        R &&restart, F &&step) {
+  bool reset[VEC] = {};
+  if (!__any_sync(0xffffffffu, live && !plain(m, reset))) return {false, false, false};
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) reset[i] |= a[s][i] == 0.f;
+    m.a[i] = reset[i] ? 0.f : m.a[i];
+  }
+  restart();
+  if (!__any_sync(0xffffffffu, live && !plain(m, reset))) return {true, false, false};
+  return settle<S>(m, n, live, step);
+}
+
+template <int VEC>
+struct Steps {
+  const float (&a)[VEC], (&b)[VEC];
+};
+// m after k: the same care for two maps, with m's offset as k's state
+__device__ __forceinline__ void join(float &a, float &b, float ka, float kb) {
+  if (ka == 0.f) {
+    a = 0.f, b = kb;
+    return;
+  }
+  float p = __fmul_rn(ka, a);
+  const float sum = fmaf(ka, b, kb);
+  if (a != 0.f) {
+    if (p == 0.f) p = copysignf(kLeast, p);
+    if ((subnormal(a) && fabsf(ka) > 1.f) || (subnormal(ka) && fabsf(a) > 1.f)) p = unusable();
+    if (!(fabsf(p) <= kMostGrowth && fabsf(sum) < infinity())) p = unusable();
+  }
+  if (subnormal(ka) && fabsf(b) > kLooseState) p = unusable();
+  a = p, b = sum;
+}
+
+// A CTA's map from those of its warps: decays and offsets by at(w), in the order
+// of w.  It is sent as it comes out: checks before the send took 5 % of a launch
+// in clusters, since every other CTA waits for them.
+template <bool kSig, int VEC, typename At>
+__device__ __forceinline__ void join_warps(Map<VEC, 1> &m, At &&at) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) m.a[i] = at(0).a[i], m.b[0][i] = at(0).b[i];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    const Steps<VEC> k = at(w);
+    affine<!kSig>(k.a, m.b[0], k.b, m.b[0]);
+    vmul(m.a, k.a, m.a);
+  }
+}
+// whether that map does not hold, if the decays of some warp are loose
+template <int VEC>
+__device__ __noinline__ bool misjoined(const float *a, const float *b, int pitch) {
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < VEC; ++i) {
+    float ma = a[i], mb = b[i];
+#pragma unroll 1
+    for (int w = 1; w < kWarps; ++w) join(ma, mb, a[w * pitch + i], b[w * pitch + i]);
+    bad |= ma != ma;
+  }
+  return bad;
+}
+// Whether it does not hold for the state h that it is applied to: its decay is
+// subnormal, or 0 by the product alone, and h large or no number.
+template <int VEC>
+__device__ __noinline__ bool misused(const float *a, int pitch, float h0, float h1) {
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < VEC; ++i) {
+    const float h = i == 0 ? h0 : h1;
+    bool reset = false;
+    float p = 1.f;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      reset |= a[w * pitch + i] == 0.f;
+      p = __fmul_rn(p, a[w * pitch + i]);
+    }
+    // (a subnormal carries Inf and NaN on by itself)
+    if (!reset && fabsf(p) < kNormal && !(fabsf(h) <= kLooseState) && (p == 0.f || fabsf(h) < infinity())) bad = true;
+  }
+  return bad;
+}
+template <int VEC>
+__device__ __forceinline__ bool below_normal(const float (&a)[VEC]) {
+  bool u = false;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) u |= fabsf(a[i]) < kNormal;
+  return u;
+}
+template <int VEC>
+__device__ __forceinline__ bool beyond(const float (&h)[VEC]) {
+  bool u = false;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) u |= !(fabsf(h[i]) <= kLooseState);
+  return u;
+}
+// whether a map does not hold for a state
+template <int VEC>
+__device__ __forceinline__ bool unsafe(const float (&a)[VEC], const float (&h)[VEC]) {
+  bool u = false;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i)
+    u |= a[i] != a[i] || (subnormal(a[i]) && fabsf(h[i]) > kLooseState && fabsf(h[i]) < infinity());
+  return u;
+}
+template <int VEC>
+__device__ __forceinline__ bool not_numbers(const float (&h)[VEC]) {
+  bool n = false;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) n |= h[i] != h[i];
+  return n;
+}
 // The exchange of one map per CTA in a cluster.  Two buffers: a CTA sends
 // round r + 2 only after it has every map of round r + 1, which its peers send
 // after they have read round r.  Waits are bounded; one that runs out sets the
@@ -299,6 +522,79 @@ struct Exchange {
   }
 };
 
+// One channel's steps t .. t + kWalk - 1 as they lie in memory; those at or past
+// n become steps that change nothing.
+constexpr int kWalk = 16;
+template <typename In, typename Gate, bool kSig>
+__device__ __forceinline__ void walk(const In *x, int64_t xs, const Gate *g, int64_t gs, int64_t t, int64_t n,
+                                     float (&a)[kWalk], float (&u)[kWalk], float (&ux)[kWalk]) {
+  float xv[kWalk][1], gv[kWalk][1];
+#pragma unroll
+  for (int j = 0; j < kWalk; ++j) {
+    xv[j][0] = gv[j][0] = 0.f;
+    if (t + j < n) {
+      widen(load<In, 1>(x + (t + j) * xs), xv[j]);
+      widen(load<Gate, 1>(g + (t + j) * gs), gv[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kWalk; ++j) {
+    float a1[1], u1[1], ux1[1];
+    gates<kSig>(gv[j], a1, u1);
+    vmul(u1, xv[j], ux1);
+    a[j] = t + j < n ? a1[0] : 1.f;
+    u[j] = t + j < n ? u1[0] : 0.f;
+    ux[j] = t + j < n ? ux1[0] : 0.f;
+  }
+}
+template <bool kSig>
+__device__ __forceinline__ float one_step(float a, float h, float ux) {
+  return !kSig && a == 0.f ? ux : fmaf(a, h, ux);
+}
+
+// Tells every CTA of the cluster which lanes want to go through their channels
+// again.  All stores of the row come before those that replace them, and no CTA
+// leaves while another may reach into it.  (Plain stores of one value: with an
+// atomic in the kernel its loop takes a tenth longer.)
+template <bool kCluster>
+__device__ __forceinline__ void agree(int *flag, bool again, int cs) {
+  if constexpr (kCluster) {
+    if (again) {
+      for (int q = 0; q < cs; ++q)
+        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(sm100::map_cluster(flag, q)), "r"(1) : "memory");
+    }
+    __syncwarp();
+    sm100::cluster_sync();
+  } else {
+    if (again) *flag = 1;
+    __syncthreads();
+  }
+}
+
+// A channel's whole row, step by step: x, g, out and states at its first step,
+// states null where they are not wanted.  What lies in this CTA's tiles is
+// stored.  Returns the last state.
+template <typename In, typename Gate, bool kSig>
+__device__ __noinline__ float redo_fwd(const In *x, int64_t xs, const Gate *g, int64_t gs, In *out, float *states,
+                                       int64_t D, int64_t T, int64_t len, int rank, int cs, float h) {
+  constexpr int kTile = kWarps * kFwdSteps;
+  for (int64_t t = 0; t < T; t += kWalk) {
+    const bool mine = t / kTile % cs == rank;
+    if (mine && states && t % kScanBlock == 0) states[t / kScanBlock * D] = h;
+    if (t >= len) continue;
+    float a[kWalk], u[kWalk], ux[kWalk];
+    walk<In, Gate, kSig>(x, xs, g, gs, t, len, a, u, ux);
+#pragma unroll
+    for (int j = 0; j < kWalk; ++j) {
+      if (t + j >= len) break;
+      h = one_step<kSig>(a[j], h, ux[j]);
+      const float v[1] = {h};
+      if (mine) store<In, 1>(out + (t + j) * D, v);
+    }
+  }
+  return h;
+}
+
 // ------------------------------------------------------------------ forward
 template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, int cs, int64_t strips) {
@@ -308,6 +604,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
   constexpr int S = kFwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 1> s_map[2][kWarps][32];
+  __shared__ int s_again[32];  // a lane's channels are gone through again
+  __shared__ float s_first[32 * VEC];  // h0, which hT may overwrite
   __shared__ Exchange ex;
   // behind the ring: the maps of the cluster's CTAs, [2][cs][32]
   auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * (X::kPitch + G::kPitch));
@@ -339,6 +637,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
   float carry[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) carry[i] = live && p.h0 ? p.h0[b * p.D + c0 + i] : 0.f;
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s_first[lane * VEC + i] = carry[i];
+  }
+  if (threadIdx.x < 32) s_again[threadIdx.x] = 0;
+  bool again = false;  // the maps do not hold for this lane's channels
 
   const int64_t rounds = (tiles + cs - 1) / cs;
   // every CTA of the cluster runs before any writes into its shared memory
@@ -366,6 +670,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
       gates<kSig>(gv, a[s], u[s]);
       vmul(u[s], xv, u[s]);
     }
+    const int now = slot;
     slot = slot == kStages - 1 ? 0 : slot + 1;
     if (n < S) {
 #pragma unroll
@@ -376,7 +681,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
           u[s][i] = s < n ? u[s][i] : 0.f;
         }
     }
-    bool drop = false;
+    Settled map{};
     {
       Map<VEC, 1> m;
 #pragma unroll
@@ -384,30 +689,41 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 #pragma unroll
       for (int s = 1; s < S; ++s) {
         affine<false>(a[s], m.b[0], u[s], m.b[0]);
-        vmul(m.a, a[s], m.a);
+        kSig ? vmul(m.a, a[s], m.a) : vmul_ftz(m.a, a[s], m.a);
       }
-      if (!kSig && (drop = drops(m.a, live))) {
+      if constexpr (!kSig)
+        map = look(
+            a, m, n, live,
+            [&] {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) m.b[0][i] = u[0][i];
+              for (int i = 0; i < VEC; ++i) m.b[0][i] = u[0][i];
 #pragma unroll
-        for (int s = 1; s < S; ++s) affine<true>(a[s], m.b[0], u[s], m.b[0]);
-      }
+              for (int s = 1; s < S; ++s) affine<true>(a[s], m.b[0], u[s], m.b[0]);
+            },
+            [&](int s, float (&av)[VEC], float (&xv)[VEC], float (&)[VEC]) {
+              X::read(rx + now * S * X::kPitch, x + t0 * p.x_st, p.x_st, s, lane, xv);
+              G::read(rg + now * S * G::kPitch, g + t0 * p.g_st, p.g_st, s, lane, av);
+            });
       s_map[buf][warp][lane] = m;
     }
-    __syncthreads();
+    const bool loose = meet<kCluster && !kSig>(map.loose);
     float h[VEC], start[VEC];
     if (kCluster) {
       // one map per CTA to every CTA of the cluster: warp w serves CTAs w and w + 8
       if (threadIdx.x == 0) ex.expect(buf, cs * 32 * sizeof(Map<VEC, 1>));
+      bool small = false;  // a decay that may not hold for every state
       if (warp < cs) {
-        Map<VEC, 1> m = s_map[buf][0][lane];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          const Map<VEC, 1> k = s_map[buf][w][lane];
-          affine<!kSig>(k.a, m.b[0], k.b[0], m.b[0]);
-          vmul(m.a, k.a, m.a);
-        }
+        Map<VEC, 1> m;
+        join_warps<kSig>(m, [&](int w) {
+          const Map<VEC, 1> &k = s_map[buf][w][lane];
+          return Steps<VEC>{k.a, k.b[0]};
+        });
         for (int to = warp; to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
+        if (!kSig) small = below_normal(m.a);
+        if (!kSig && loose) {
+          const Map<VEC, 1> &k = s_map[buf][0][lane];
+          again |= not_numbers(m.a) || misjoined<VEC>(k.a, k.b[0], 32 * sizeof(k) / sizeof(float));
+        }
       }
       ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
@@ -419,6 +735,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
           for (int i = 0; i < VEC; ++i) h[i] = carry[i];
         }
         affine<!kSig>(k.a, carry, k.b[0], carry);
+      }
+      if (small && beyond(h)) {
+        const Map<VEC, 1> &k = s_map[buf][0][lane];
+        again |= misused<VEC>(k.a, 32 * sizeof(k) / sizeof(float), h[0], h[VEC - 1]);
       }
     } else {
 #pragma unroll
@@ -435,6 +755,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
         for (int i = 0; i < VEC; ++i) start[i] = h[i];
       }
     }
+    if (map.strange) again |= unsafe(s_map[buf][warp][lane].a, start);
+    if (kSig) again |= not_numbers(start);
     if (!kCluster) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) carry[i] = h[i];
@@ -443,7 +765,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
       store<float, VEC>(p.states + (b * saved + t0 / kScanBlock) * p.D + c0, start);
     if (live) {
       In *o = out + t0 * p.D;
-      if (n >= S && !drop) {
+      if (n >= S && !map.drop) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           affine<false>(a[s], start, u[s], start);
@@ -464,6 +786,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
     }
   }
   ring_wait<0>();
+  if (kSig) again |= not_numbers(carry);
+  agree<kCluster>(s_again + lane, again && live, cs);
+  if (warp == 0 && s_again[lane]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      carry[i] = redo_fwd<In, Gate, kSig>(x + lane * VEC + i, p.x_st, g + lane * VEC + i, p.g_st, out + i,
+                                          p.states ? p.states + b * saved * p.D + c0 + i : nullptr, p.D, p.T, len,
+                                          rank, cs, s_first[lane * VEC + i]);
+  }
   if (p.hT && rank == 0 && warp == 0 && live) store<float, VEC>(p.hT + b * p.D + c0, carry);
 }
 
@@ -472,6 +803,58 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
 // again from the state saved at the tile's start (the forward's states, kept
 // in float32, so no rounded output enters the gradients); the gradients are
 // the reversed recurrence, whose maps compose from the last step to the first.
+
+// A channel's whole row in reverse, step by step, likewise; dout and the
+// gradients are D apart.  A tile's states are run again from its saved one and
+// held in `before`, `pitch` apart.  Returns the gradient of the first state.
+template <typename In, typename Gate, bool kSig>
+__device__ __noinline__ float redo_bwd(const In *x, int64_t xs, const Gate *g, int64_t gs, const In *dout, In *dx,
+                                       Gate *dg, const float *states, int64_t D, int64_t T, int64_t len, int rank,
+                                       int cs, float grad, float *before, int pitch) {
+  const int64_t tiles = (T + kScanBlock - 1) / kScanBlock;
+  for (int64_t tile = (len + kScanBlock - 1) / kScanBlock - 1; tile >= 0; --tile) {
+    const int64_t t0 = tile * kScanBlock;
+    const bool mine = (tiles - 1 - tile) % cs == rank;
+    float a[kWalk], u[kWalk], ux[kWalk], d[kWalk];
+    if (mine) {
+      float h = states[tile * D];
+      for (int s = 0; s < kScanBlock; s += kWalk) {
+        walk<In, Gate, kSig>(x, xs, g, gs, t0 + s, len, a, u, ux);
+#pragma unroll
+        for (int j = 0; j < kWalk; ++j) {
+          before[(s + j) * pitch] = h;
+          h = one_step<kSig>(a[j], h, ux[j]);
+        }
+      }
+    }
+    for (int s = kScanBlock - kWalk; s >= 0; s -= kWalk) {
+      if (t0 + s >= len) continue;
+      walk<In, Gate, kSig>(x, xs, g, gs, t0 + s, len, a, u, ux);
+#pragma unroll
+      for (int j = 0; j < kWalk; ++j) {
+        float v[1] = {0.f};
+        if (t0 + s + j < len) widen(load<In, 1>(dout + (t0 + s + j) * D), v);
+        d[j] = v[0];
+      }
+#pragma unroll
+      for (int j = kWalk - 1; j >= 0; --j) {
+        const int64_t t = t0 + s + j;
+        if (t >= len) continue;
+        const float dh = __fadd_rn(d[j], grad);
+        if (mine) {
+          const float h = before[(s + j) * pitch];
+          const float vx[1] = {__fmul_rn(u[j], dh)};
+          const float vg[1] = {__fmul_rn(kSig ? __fmul_rn(a[j], fmaf(u[j], h, -ux[j])) : h, dh)};
+          store<In, 1>(dx + t * D, vx);
+          store<Gate, 1>(dg + t * D, vg);
+        }
+        grad = !kSig && a[j] == 0.f ? 0.f : __fmul_rn(a[j], dh);
+      }
+    }
+  }
+  return grad;
+}
+
 template <typename In, bool kSig, int VEC, bool kWide, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p, int cs, int64_t strips) {
   using Gate = typename std::conditional<kSig, In, float>::type;
@@ -480,6 +863,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   constexpr int S = kBwdSteps, kTile = kWarps * S, kRow = 32 * VEC;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) Map<VEC, 2> s_map[2][kWarps][32];  // offsets: forward, reverse
+  __shared__ int s_again[32];  // a lane's channels are gone through again
+  __shared__ float s_last[32 * VEC];  // dhT, which dh0 may overwrite
   __shared__ Exchange ex;
   // behind the ring: the maps of the cluster's CTAs, [2][cs][32]
   auto *s_cta = reinterpret_cast<Map<VEC, 1> *>(ring + kStages * kTile * (2 * X::kPitch + G::kPitch));
@@ -520,6 +905,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   float carry[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) carry[i] = live && p.dhT ? p.dhT[b * p.D + c0 + i] : 0.f;
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s_last[lane * VEC + i] = carry[i];
+  }
+  if (threadIdx.x < 32) s_again[threadIdx.x] = 0;
+  bool again = false;
 
   const int64_t rounds = (tiles + cs - 1) / cs;
   if (kCluster) {
@@ -548,6 +939,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
       gates<kSig>(gv, a[s], u[s]);
       vmul(u[s], xv, ux[s]);
     }
+    const int now = slot;
     slot = slot == kStages - 1 ? 0 : slot + 1;
     if (n < S) {
 #pragma unroll
@@ -563,13 +955,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
 #pragma unroll
     for (int i = 0; i < VEC; ++i) h[i] = ahead[i];
     if (it + 1 < rounds) fetch_state(tile - cs);
-    bool drop = false;
+    Settled map{};
     {
       Map<VEC, 2> m;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) m.a[i] = a[0][i];
 #pragma unroll
-      for (int s = 1; s < S; ++s) vmul(m.a, a[s], m.a);
+      for (int s = 1; s < S; ++s) kSig ? vmul(m.a, a[s], m.a) : vmul_ftz(m.a, a[s], m.a);
       const auto offsets = [&](auto with) {
         constexpr bool kDrop = decltype(with)::value;
 #pragma unroll
@@ -583,28 +975,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
           decay<kDrop>(a[s], m.b[1], m.b[1]);
         }
       };
-      if (!kSig && (drop = drops(m.a, live)))
-        offsets(std::true_type{});
-      else
-        offsets(std::false_type{});
+      offsets(std::false_type{});
+      if constexpr (!kSig)
+        map = look(
+            a, m, n, live, [&] { offsets(std::true_type{}); },
+            [&](int s, float (&av)[VEC], float (&xv)[VEC], float (&dv)[VEC]) {
+              X::read(rx + now * S * X::kPitch, x + t0 * p.x_st, p.x_st, s, lane, xv);
+              G::read(rg + now * S * G::kPitch, g + t0 * p.g_st, p.g_st, s, lane, av);
+              X::read(rd + now * S * X::kPitch, dout + t0 * p.D, p.D, s, lane, dv);
+            });
       s_map[buf][warp][lane] = m;
     }
-    __syncthreads();
+    const bool loose = meet<kCluster && !kSig>(map.loose);
     float r[VEC], c[VEC];
     if (kCluster) {
       if (threadIdx.x == 0) ex.expect(buf, cs * 32 * sizeof(Map<VEC, 1>));
+      bool small = false;  // a decay that may not hold for every state
       if (warp < cs) {
-        const Map<VEC, 2> last = s_map[buf][kWarps - 1][lane];
         Map<VEC, 1> m;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) m.a[i] = last.a[i], m.b[0][i] = last.b[1][i];
-#pragma unroll
-        for (int w = kWarps - 2; w >= 0; --w) {
-          const Map<VEC, 2> k = s_map[buf][w][lane];
-          affine<!kSig>(k.a, m.b[0], k.b[1], m.b[0]);
-          vmul(m.a, k.a, m.a);
-        }
+        join_warps<kSig>(m, [&](int w) {
+          const Map<VEC, 2> &k = s_map[buf][kWarps - 1 - w][lane];
+          return Steps<VEC>{k.a, k.b[1]};
+        });
         for (int to = warp; to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
+        if (!kSig) small = below_normal(m.a);
+        if (!kSig && loose) {
+          const Map<VEC, 2> &k = s_map[buf][kWarps - 1][lane];
+          again |= not_numbers(m.a) || misjoined<VEC>(k.a, k.b[1], -32 * (int)(sizeof(k) / sizeof(float)));
+        }
       }
       ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
@@ -616,6 +1014,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
           for (int i = 0; i < VEC; ++i) r[i] = carry[i];
         }
         affine<!kSig>(q.a, carry, q.b[0], carry);
+      }
+      if (small && beyond(r)) {
+        const Map<VEC, 2> &k = s_map[buf][kWarps - 1][lane];
+        again |= misused<VEC>(k.a, -32 * (int)(sizeof(k) / sizeof(float)), r[0], r[VEC - 1]);
       }
     } else {
 #pragma unroll
@@ -638,6 +1040,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
         for (int i = 0; i < VEC; ++i) c[i] = r[i];
       }
     }
+    if (map.strange) again |= unsafe(s_map[buf][warp][lane].a, h) || unsafe(s_map[buf][warp][lane].a, c);
+    if (kSig) again |= not_numbers(h) || not_numbers(c);
     if (!kCluster) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) carry[i] = r[i];
@@ -688,12 +1092,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
         }
       }
     };
-    if (!kSig && drop)
+    if (!kSig && map.drop)
       finish(std::true_type{});
     else
       finish(std::false_type{});
   }
   ring_wait<0>();
+  if (kSig) again |= not_numbers(carry);
+  agree<kCluster>(s_again + lane, again && live, cs);
+  if (warp == 0 && s_again[lane]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      carry[i] = redo_bwd<In, Gate, kSig>(x + lane * VEC + i, p.x_st, g + lane * VEC + i, p.g_st,
+                                          dout + lane * VEC + i, dx + i, dg + i, p.states + b * tiles * p.D + c0 + i,
+                                          p.D, p.T, len, rank, cs, s_last[lane * VEC + i],
+                                          reinterpret_cast<float *>(ring) + lane * VEC + i, kRow);
+  }
   if (p.dh0 && rank == 0 && warp == 0 && live) store<float, VEC>(p.dh0 + b * p.D + c0, carry);
 }
 
