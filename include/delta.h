@@ -437,6 +437,14 @@ int delta_inject_failure(int count);
 int delta_selftest_wait(int polls, struct CUstream_st *stream);
 
 /*
+ * delta_selftest_exchange -- the same for the exchange between the CTAs of a
+ * scan's cluster: two CTAs of which one never sends; the other gives up after
+ * `polls` (1 .. 2^22) tries, both meet at their end, and the next
+ * delta_check_device() returns DELTA_ERR_CUDA and clears the record.
+ */
+int delta_selftest_exchange(int polls, struct CUstream_st *stream);
+
+/*
  * ---- Operators around the token mixers in a block ------------------------
  *
  * The calls below follow the conventions above (asynchronous, checked before

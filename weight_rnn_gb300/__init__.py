@@ -26,7 +26,7 @@ __all__ = ["delta_fwd", "delta_bwd", "delta_fwd_kda", "delta_step_kda", "delta_p
            "delta_fwd_static_scratch", "delta_state_erank",
            "delta_attention_map", "delta_ut_transform", "delta_fwd_with_ut", "delta_step",
            "fwd_launches", "delta_status_string", "delta_last_error",
-           "delta_check_device", "delta_inject_failure", "delta_selftest_wait",
+           "delta_check_device", "delta_inject_failure", "delta_selftest_wait", "delta_selftest_exchange",
            "delta_version", "DeltaError", "library_path", "load_library",
            "DELTA_OK", "DELTA_ERR_INVALID", "DELTA_ERR_UNSUPPORTED",
            "DELTA_ERR_ALIGN", "DELTA_ERR_CUDA", "DELTA_F32", "DELTA_BF16",
@@ -50,7 +50,8 @@ EXPORTED_SYMBOLS = ("delta_fwd", "delta_bwd", "delta_fwd_kda", "delta_step_kda",
                     "delta_fwd_kernel_count", "delta_step", "delta_step_prologue",
                     "delta_status_string",
                     "delta_last_error", "delta_check_device", "delta_version",
-                    "delta_inject_failure", "delta_selftest_wait", "delta_state_erank",
+                    "delta_inject_failure", "delta_selftest_wait", "delta_selftest_exchange",
+                    "delta_state_erank",
                     "delta_attention_map") + block.SYMBOLS
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -123,6 +124,8 @@ def load_library():
         lib.delta_inject_failure.argtypes = [i]
         lib.delta_selftest_wait.restype = i
         lib.delta_selftest_wait.argtypes = [i, ctypes.c_void_p]
+        lib.delta_selftest_exchange.restype = i
+        lib.delta_selftest_exchange.argtypes = [i, ctypes.c_void_p]
         block.declare(lib)
         _lib = lib
         return lib
@@ -162,6 +165,15 @@ def delta_selftest_wait(polls: int = 1000, stream=None, device=None) -> None:
     next delta_check_device() reports."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     st = load_library().delta_selftest_wait(int(polls), _stream(dev, stream))
+    if st != DELTA_OK:
+        raise DeltaError(st, delta_last_error())
+
+
+def delta_selftest_exchange(polls: int = 1000, stream=None, device=None) -> None:
+    """The same for the exchange of a scan's cluster: one of two CTAs never sends,
+    the other gives up after ``polls`` tries."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    st = load_library().delta_selftest_exchange(int(polls), _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
 

@@ -352,6 +352,12 @@ int delta_selftest_wait(int polls, struct CUstream_st *stream) {
   return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "wait self-test launch");
 }
 
+int delta_selftest_exchange(int polls, struct CUstream_st *stream) {
+  if (polls < 1 || polls > (1 << 22)) return fail(DELTA_ERR_INVALID, "polls=%d not in [1, 2^22]", polls);
+  const cudaError_t err = delta::launch_exchange_selftest((unsigned)polls, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "exchange self-test launch");
+}
+
 int delta_check_device(void) {
   unsigned int word = 0, ut_word = 0, linear_word = 0, scan_word = 0;
   cudaError_t err = delta::read_and_clear_tc_error(&word);

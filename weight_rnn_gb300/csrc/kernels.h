@@ -141,6 +141,7 @@ cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanBwdArgs &a, cudaStream_t s);
 // one token: h0 is the state before and hT the state after (the same memory)
 cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s);
+cudaError_t launch_exchange_selftest(unsigned int polls, cudaStream_t s);
 cudaError_t read_and_clear_scan_error(unsigned int *word);
 // hT <- h0 (or 0): a sequence without steps
 cudaError_t launch_scan_passthrough(const float *h0, float *hT, int64_t n, cudaStream_t s);

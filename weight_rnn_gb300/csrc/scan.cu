@@ -486,8 +486,10 @@ __device__ __forceinline__ bool not_numbers(const float (&h)[VEC]) {
 }
 // The exchange of one map per CTA in a cluster.  Two buffers: a CTA sends
 // round r + 2 only after it has every map of round r + 1, which its peers send
-// after they have read round r.  Waits are bounded; one that runs out sets the
-// error word and lets the kernel end.
+// after they have read round r.  Waits are bounded.  One that runs out sets the
+// error word; its warp sends no more, its CTA's other waits end too, and the
+// kernel runs to its end, where every CTA meets the others (agree) and one that
+// has given up leaves late, when what was on its way to it has landed.
 struct Exchange {
   uint64_t bar[2];
   volatile int dead;
@@ -512,13 +514,20 @@ struct Exchange {
                    : "memory");
   }
   __device__ __forceinline__ void expect(int buf, uint32_t bytes) { sm100::mbar_arrive_expect_tx(&bar[buf], bytes); }
-  __device__ __forceinline__ void wait(int buf, uint32_t parity) {
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
-      if (sm100::mbar_try_wait(&bar[buf], parity)) return;
-      if (dead) return;
+  __device__ __forceinline__ bool wait(int buf, uint32_t parity, uint32_t limit = 1u << 22) {
+    for (uint32_t i = 0; i < limit; ++i) {
+      if (sm100::mbar_try_wait(&bar[buf], parity)) return true;
+      if (dead) return false;
     }
     dead = 1;
     atomicExch(&g_scan_error, 1u);
+    return false;
+  }
+  // after the closing barrier
+  __device__ __forceinline__ void leave() {
+    if (dead) {
+      for (int i = 0; i < 200; ++i) __nanosleep(1000);
+    }
   }
 };
 
@@ -642,6 +651,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
     for (int i = 0; i < VEC; ++i) s_first[lane * VEC + i] = carry[i];
   }
   if (threadIdx.x < 32) s_again[threadIdx.x] = 0;
+  bool alive = true;   // the exchange goes on
   bool again = false;  // the maps do not hold for this lane's channels
 
   const int64_t rounds = (tiles + cs - 1) / cs;
@@ -718,14 +728,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
           const Map<VEC, 1> &k = s_map[buf][w][lane];
           return Steps<VEC>{k.a, k.b[0]};
         });
-        for (int to = warp; to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
+        for (int to = warp; alive && to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
         if (!kSig) small = below_normal(m.a);
         if (!kSig && loose) {
           const Map<VEC, 1> &k = s_map[buf][0][lane];
           again |= not_numbers(m.a) || misjoined<VEC>(k.a, k.b[0], 32 * sizeof(k) / sizeof(float));
         }
       }
-      ex.wait(buf, (uint32_t)(it >> 1) & 1);
+      alive &= ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) h[i] = carry[i];
       for (int r = 0; r < cs; ++r) {
@@ -788,6 +798,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(ScanArgs p, in
   ring_wait<0>();
   if (kSig) again |= not_numbers(carry);
   agree<kCluster>(s_again + lane, again && live, cs);
+  if (kCluster) ex.leave();
   if (warp == 0 && s_again[lane]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
@@ -910,6 +921,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
     for (int i = 0; i < VEC; ++i) s_last[lane * VEC + i] = carry[i];
   }
   if (threadIdx.x < 32) s_again[threadIdx.x] = 0;
+  bool alive = true;   // the exchange goes on
   bool again = false;
 
   const int64_t rounds = (tiles + cs - 1) / cs;
@@ -997,14 +1009,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
           const Map<VEC, 2> &k = s_map[buf][kWarps - 1 - w][lane];
           return Steps<VEC>{k.a, k.b[1]};
         });
-        for (int to = warp; to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
+        for (int to = warp; alive && to < cs; to += kWarps) ex.send(buf, cta(buf, rank) + lane, to, m);
         if (!kSig) small = below_normal(m.a);
         if (!kSig && loose) {
           const Map<VEC, 2> &k = s_map[buf][kWarps - 1][lane];
           again |= not_numbers(m.a) || misjoined<VEC>(k.a, k.b[1], -32 * (int)(sizeof(k) / sizeof(float)));
         }
       }
-      ex.wait(buf, (uint32_t)(it >> 1) & 1);
+      alive &= ex.wait(buf, (uint32_t)(it >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) r[i] = carry[i];
       for (int k = 0; k < cs; ++k) {
@@ -1100,6 +1112,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(ScanBwdArgs p,
   ring_wait<0>();
   if (kSig) again |= not_numbers(carry);
   agree<kCluster>(s_again + lane, again && live, cs);
+  if (kCluster) ex.leave();
   if (warp == 0 && s_again[lane]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
@@ -1129,6 +1142,24 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs p, int64_t n) {
   affine<!kSig>(a, hv, u, hv);
   store<float, VEC>(p.hT + i0, hv);
   store<In, VEC>(static_cast<In *>(p.out) + i0, hv);
+}
+
+// The exchange of two CTAs of which one never sends: the other gives up.
+__global__ void __launch_bounds__(32) exchange_selftest_kernel(uint32_t polls) {
+  __shared__ __align__(16) Map<1, 1> s_cta[2][32];
+  __shared__ int s_flag[32];
+  __shared__ Exchange ex;
+  const int lane = threadIdx.x, rank = (int)cg::this_cluster().block_rank();
+  if (lane == 0) ex.init();
+  s_flag[lane] = 0;
+  cg::this_cluster().sync();
+  if (rank == 0) {
+    if (lane == 0) ex.expect(0, sizeof(s_cta));
+    for (int to = 0; to < 2; ++to) ex.send(0, &s_cta[0][lane], to, Map<1, 1>{{1.f}, {{0.f}}});
+    ex.wait(0, 0, polls);
+  }
+  agree<true>(s_flag + lane, false, 2);
+  ex.leave();
 }
 
 // ------------------------------------------------------------------ launches
@@ -1244,6 +1275,10 @@ cudaError_t launch_scan_step(const ScanArgs &a, cudaStream_t s) {
   }
   if (a.sigmoid) return v2 ? launch_one<float, true, 2>(a, s) : launch_one<float, true, 1>(a, s);
   return v2 ? launch_one<float, false, 2>(a, s) : launch_one<float, false, 1>(a, s);
+}
+
+cudaError_t launch_exchange_selftest(unsigned int polls, cudaStream_t s) {
+  return chain_launch(exchange_selftest_kernel, dim3(2), dim3(32), 0, 2, false, s, polls);
 }
 
 cudaError_t read_and_clear_scan_error(unsigned int *word) {
