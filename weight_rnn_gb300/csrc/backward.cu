@@ -338,7 +338,10 @@ cudaError_t launch_bwd(const BwdArgs &a, cudaStream_t s) {
   const int ng = col_groups(a.dv), dvs = a.dv / ng;
   const size_t smem =
       (size_t)(3 * a.dk * dvs + 3 * a.dk + 2 * dvs + kThreads / 32 + kThreads) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the largest shape's, which every thread of the program sets alike
+  constexpr size_t most = (3 * 128 * kCols + 3 * 128 + 2 * kCols + kThreads / 32 + kThreads) * sizeof(float);
+  if (smem > most) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   bwd_kernel<<<(unsigned)(a.B * a.H * ng), kThreads, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || ng == 1) return e;

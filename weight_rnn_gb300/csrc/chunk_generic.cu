@@ -283,7 +283,10 @@ cudaError_t launch_chunk_generic(const FwdArgs &a, cudaStream_t s) {
   const bool kda = a.alpha != nullptr;
   const size_t bytes = Smem::floats(a.chunk, a.dk, BV, kda) * sizeof(float);
   auto kern = kda ? chunk_generic_kernel<true> : chunk_generic_kernel<false>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  // the largest supported shape's, which every thread of the program sets alike
+  const size_t most = Smem::floats(64, 128, 32, kda) * sizeof(float);
+  if (bytes > most) return cudaErrorInvalidConfiguration;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (err != cudaSuccess) return err;
   dim3 grid((unsigned)(a.B * a.H), (unsigned)(a.dv / BV));
   kern<<<grid, kThreads, bytes, s>>>(a, BV);

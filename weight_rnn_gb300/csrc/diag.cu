@@ -201,7 +201,9 @@ int64_t erank_smem_bytes(int dk, int dv) { return (int64_t)dk * dv * 4; }
 cudaError_t launch_erank(const float *state, float *erank, int64_t BH, int dk, int dv,
                          cudaStream_t s) {
   const int smem = (int)erank_smem_bytes(dk, dv);
-  cudaError_t e = cudaFuncSetAttribute(erank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int most = 128 * 128 * 4;  // which every thread of the program sets alike
+  if (smem > most) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(erank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   erank_kernel<<<(unsigned)BH, kErankThreads, smem, s>>>(state, erank, dk, dv);
   return cudaGetLastError();
@@ -211,16 +213,18 @@ cudaError_t launch_attention_map(const void *q, const void *k, const float *beta
                                  float *attn, int64_t B, int64_t H, int N, int dk, bool bf16,
                                  cudaStream_t s) {
   const int smem = (2 * N * dk + 3 * N * N + 2 * N) * 4;
+  constexpr int most = (2 * 64 * 128 + 3 * 64 * 64 + 2 * 64) * 4;  // N and dk at their largest
+  if (smem > most) return cudaErrorInvalidConfiguration;
   if (bf16) {
     auto kern = attention_map_kernel<__nv_bfloat16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(B * H), kDiagThreads, smem, s>>>(static_cast<const __nv_bfloat16 *>(q),
                                                        static_cast<const __nv_bfloat16 *>(k), beta,
                                                        g, attn, (int)H, N, dk);
   } else {
     auto kern = attention_map_kernel<float>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(B * H), kDiagThreads, smem, s>>>(static_cast<const float *>(q),
                                                        static_cast<const float *>(k), beta, g,

@@ -33,6 +33,7 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr int kMostThreads = 512;  // of a CTA
+constexpr int kMostRing = 200 * 1024;  // bytes of a CTA's ring; the largest, float32 at D = 8189, takes 196704
 // Threads an SM is compiled to hold.  More of them and fewer registers were
 // slower but for the 8-bit output (32768 x 4096: 182 us for 192; 162 for 173).
 constexpr int kSmThreads = 768, kQuantThreads = 1024;
@@ -463,7 +464,7 @@ Plan plan(int64_t rows, int64_t D, int vec, int wide, int tensors, int resident,
   // 161 us, 6.7 TB/s, for 182 with the resident ones alone; the backward, which
   // ends in a row of sums per CTA, 195 for 173)
   int fit = resident / q.threads;
-  if (fit > 200 * 1024 / q.smem) fit = 200 * 1024 / q.smem;
+  if (fit > kMostRing / q.smem) fit = kMostRing / q.smem;
   int64_t cap = (int64_t)sms * (fit > 1 ? fit : 1);
   if (many && ctas / 12 >= 8 * sms) cap = ctas / 12 < 16 * sms ? ctas / 12 : 16 * sms;
   q.grid = ctas < cap ? ctas : cap;
@@ -499,8 +500,11 @@ cudaError_t dispatch(const Plan &q, X &&...x) {
 
 template <typename K, typename A>
 cudaError_t go(K kern, const A &a, const Plan &q, cudaStream_t s) {
+  if (q.smem > kMostRing) return cudaErrorInvalidConfiguration;
   if (q.smem > 48 * 1024 - 4096) {  // more than the default only after asking
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, q.smem);
+    // (the limit belongs to the kernel, not to the call: every thread of the
+    // program sets the same one)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing);
     if (e != cudaSuccess) return e;
   }
   return chain_launch(kern, dim3((unsigned)q.grid), dim3(q.nt, q.rpc), q.smem, 1, true, s, a);

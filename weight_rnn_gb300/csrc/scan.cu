@@ -1197,10 +1197,11 @@ int cluster_size(int64_t rows, int64_t tiles) {
   return cs;
 }
 
+// most: what the largest cluster takes.  The limit belongs to the kernel, not to
+// the call, so every thread of the program sets the same one.
 template <typename K, typename A>
-cudaError_t launch(K kern, const A &p, int64_t rows, int64_t strips, int cs, int smem, cudaStream_t s) {
-  // above 48 KB only after asking; asking again changes nothing
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch(K kern, const A &p, int64_t rows, int64_t strips, int cs, int smem, int most, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   if (cs > 8 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
     return e;
@@ -1213,9 +1214,11 @@ cudaError_t launch_fwd(const ScanArgs &a, cudaStream_t s) {
   const int cs = cluster_size(rows, (a.T + kWarps * kFwdSteps - 1) / (kWarps * kFwdSteps));
   using Gate = typename std::conditional<kSig, In, float>::type;
   constexpr int tile = kWarps * kFwdSteps * (Strip<In, VEC, kWide>::kPitch + Strip<Gate, VEC, kWide>::kPitch);
-  const int smem = kStages * tile + (cs > 1 ? 2 * cs * 32 * (int)sizeof(Map<VEC, 1>) : 0);
-  return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
-                : launch(scan_fwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
+  constexpr int maps = 2 * 32 * (int)sizeof(Map<VEC, 1>);  // for each CTA of a cluster
+  const int smem = kStages * tile + (cs > 1 ? cs * maps : 0);
+  return cs > 1 ? launch(scan_fwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem,
+                         kStages * tile + kMaxCluster * maps, s)
+                : launch(scan_fwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, kStages * tile, s);
 }
 template <typename In, bool kSig, int VEC, bool kWide>
 cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
@@ -1223,9 +1226,11 @@ cudaError_t launch_bwd(const ScanBwdArgs &a, cudaStream_t s) {
   const int cs = cluster_size(rows, (a.T + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps));
   using Gate = typename std::conditional<kSig, In, float>::type;
   constexpr int tile = kWarps * kBwdSteps * (2 * Strip<In, VEC, kWide>::kPitch + Strip<Gate, VEC, kWide>::kPitch);
-  const int smem = kStages * tile + (cs > 1 ? 2 * cs * 32 * (int)sizeof(Map<VEC, 1>) : 0);
-  return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem, s)
-                : launch(scan_bwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, s);
+  constexpr int maps = 2 * 32 * (int)sizeof(Map<VEC, 1>);  // for each CTA of a cluster
+  const int smem = kStages * tile + (cs > 1 ? cs * maps : 0);
+  return cs > 1 ? launch(scan_bwd_kernel<In, kSig, VEC, kWide, true>, a, rows, strips, cs, smem,
+                         kStages * tile + kMaxCluster * maps, s)
+                : launch(scan_bwd_kernel<In, kSig, VEC, kWide, false>, a, rows, strips, cs, smem, kStages * tile, s);
 }
 template <typename In, bool kSig, int VEC>
 cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
