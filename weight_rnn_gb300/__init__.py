@@ -205,6 +205,13 @@ def _check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _dims(t):
+    """The shape of a tensor whose axes are sizes of the ABI, which are C ints:
+    ctypes would cut larger ones without a word."""
+    block._within_int("a tensor", *t.shape)
+    return t.shape
+
+
 def _stream(device, stream):
     if stream is None:
         stream = torch.cuda.current_stream(device)
@@ -223,7 +230,7 @@ def delta_fwd(q, k, v, beta, g=None, h0=None, out=None, hT=None, *, n_h=1,
     passed as ``h0`` to update the state in place.
     """
     lib = load_library()
-    B, T, H, dk = q.shape
+    B, T, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_fwd needs CUDA tensors")
@@ -233,7 +240,7 @@ def delta_fwd(q, k, v, beta, g=None, h0=None, out=None, hT=None, *, n_h=1,
         kshape, vshape, bshape = (B, T, H, dk), (B, T, H, v.shape[-1]), (B, T, H)
     else:
         kshape, vshape, bshape = (B, T, n_h, H, dk), (B, T, n_h, H, v.shape[-1]), (B, T, n_h, H)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     _check(q, "q", (B, T, H, dk), dt, dev)
     _check(k, "k", kshape, dt, dev)
     _check(v, "v", vshape, dt, dev)
@@ -260,7 +267,7 @@ def delta_bwd(q, k, v, beta, g, h0, dout, dhT=None, *, n_h=1, want_dh0=True, str
     ``(dq, dk, dv, dbeta, dg, dh0)`` in float32 with the shapes of q, k, v,
     beta, g (None without g) and h0 (None unless ``want_dh0``)."""
     lib = load_library()
-    B, T, H, dk = q.shape
+    B, T, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_bwd needs CUDA tensors")
@@ -270,7 +277,7 @@ def delta_bwd(q, k, v, beta, g, h0, dout, dhT=None, *, n_h=1, want_dh0=True, str
         kshape, vshape, bshape = (B, T, H, dk), (B, T, H, v.shape[-1]), (B, T, H)
     else:
         kshape, vshape, bshape = (B, T, n_h, H, dk), (B, T, n_h, H, v.shape[-1]), (B, T, n_h, H)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     _check(q, "q", (B, T, H, dk), dt, dev)
     _check(k, "k", kshape, dt, dev)
     _check(v, "v", vshape, dt, dev)
@@ -298,7 +305,7 @@ def delta_fwd_kda(q, k, v, beta, alpha, h0=None, out=None, hT=None, *, n_h=1, ch
     [B,T,H,dk] float32 decays each key row of the state, in place of g.
     Other shapes and results as in ``delta_fwd``."""
     lib = load_library()
-    B, T, H, dk = q.shape
+    B, T, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_fwd_kda needs CUDA tensors")
@@ -308,7 +315,7 @@ def delta_fwd_kda(q, k, v, beta, alpha, h0=None, out=None, hT=None, *, n_h=1, ch
         kshape, vshape, bshape = (B, T, H, dk), (B, T, H, v.shape[-1]), (B, T, H)
     else:
         kshape, vshape, bshape = (B, T, n_h, H, dk), (B, T, n_h, H, v.shape[-1]), (B, T, n_h, H)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     _check(q, "q", (B, T, H, dk), dt, dev)
     _check(k, "k", kshape, dt, dev)
     _check(v, "v", vshape, dt, dev)
@@ -333,13 +340,13 @@ def delta_step_kda(q, k, v, beta, alpha, state, out=None, *, n_h=1, stream=None)
     """One decode token with a channel-wise gate (``delta_step_kda``): alpha
     [B,H,dk] float32 in place of g; ``state`` is updated in place."""
     lib = load_library()
-    B, H, dk = q.shape
+    B, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_step_kda needs CUDA tensors")
     dt = q.dtype
     code = _dtype_code(dt)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     _check(q, "q", (B, H, dk), dt, dev)
     _check(k, "k", (B, n_h, H, dk), dt, dev)
     _check(v, "v", (B, n_h, H, dv), dt, dev)
@@ -370,7 +377,7 @@ def delta_prologue(q_raw, k_raw, beta_raw, *, n_h=1, beta_map="sigmoid", stream=
     beta_raw [B,T,n_h,H] (or [B,T,H]) float32."""
     lib = load_library()
     code_map = _beta_map(beta_map)
-    B, T, H, dk = q_raw.shape
+    B, T, H, dk = _dims(q_raw)
     dev = q_raw.device
     if dev.type != "cuda":
         raise ValueError("delta_prologue needs CUDA tensors")
@@ -401,7 +408,7 @@ def delta_fwd_prologue(q_raw, k_raw, v, beta_raw, g=None, h0=None, out=None, hT=
     results as in ``delta_fwd``."""
     lib = load_library()
     code_map = _beta_map(beta_map)
-    B, T, H, dk = q_raw.shape
+    B, T, H, dk = _dims(q_raw)
     dev = q_raw.device
     if dev.type != "cuda":
         raise ValueError("delta_fwd_prologue needs CUDA tensors")
@@ -411,7 +418,7 @@ def delta_fwd_prologue(q_raw, k_raw, v, beta_raw, g=None, h0=None, out=None, hT=
         kshape, vshape, bshape = (B, T, H, dk), (B, T, H, v.shape[-1]), (B, T, H)
     else:
         kshape, vshape, bshape = (B, T, n_h, H, dk), (B, T, n_h, H, v.shape[-1]), (B, T, n_h, H)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     _check(q_raw, "q_raw", (B, T, H, dk), dt, dev)
     _check(k_raw, "k_raw", kshape, dt, dev)
     _check(v, "v", vshape, dt, dev)
@@ -439,13 +446,13 @@ def delta_fwd_static_scratch(q, k, v, beta, g=None, h0=None, out=None, hT=None, 
     dk = dv = 128 and chunk = 64 only).  Calls that overlap in time on one
     device race on that array.  Arguments and results as in ``delta_fwd``."""
     lib = load_library()
-    B, T, H, dk = q.shape
+    B, T, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_fwd_static_scratch needs CUDA tensors")
     dt = q.dtype
     code = _dtype_code(dt)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     kshape, vshape, bshape = _kvb_shapes(k, v, beta, B, T, H, dk, n_h)
     _check(q, "q", (B, T, H, dk), dt, dev)
     _check(k, "k", kshape, dt, dev)
@@ -472,7 +479,7 @@ def delta_state_erank(state, erank=None, *, stream=None):
     [B,H,dk,dv] float32 on the GPU -> erank [B,H] float32 (0 for a zero
     matrix)."""
     lib = load_library()
-    B, H, dk, dv = state.shape
+    B, H, dk, dv = _dims(state)
     dev = state.device
     if dev.type != "cuda":
         raise ValueError("delta_state_erank needs CUDA tensors")
@@ -492,7 +499,7 @@ def delta_attention_map(q, k, beta, g=None, attn=None, *, stream=None):
     attn [B,H,N,N] float32 with o_i = sum_j attn[i, j] v_j for a zero initial
     state."""
     lib = load_library()
-    B, N, H, dk = q.shape
+    B, N, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_attention_map needs CUDA tensors")
@@ -527,8 +534,7 @@ def delta_ut_transform(k, beta, g=None, t_mat=None, *, n_h=1, chunk=64, stream=N
     [B,H,NT,64,64] bfloat16, NT = ceil(n_h * T / 64).
     """
     lib = load_library()
-    B, T = k.shape[0], k.shape[1]
-    H, dk = k.shape[-2], k.shape[-1]
+    B, T, *_, H, dk = _dims(k)
     dev = k.device
     if dev.type != "cuda":
         raise ValueError("delta_ut_transform needs CUDA tensors")
@@ -554,13 +560,13 @@ def delta_fwd_with_ut(q, k, v, beta, g, h0, t_mat, out=None, hT=None, *, n_h=1, 
     ``delta_ut_transform`` returned for the same k, beta and g.  Arguments and
     results as in ``delta_fwd``."""
     lib = load_library()
-    B, T, H, dk = q.shape
+    B, T, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_fwd_with_ut needs CUDA tensors")
     dt = q.dtype
     code = _dtype_code(dt)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     kshape, vshape, bshape = _kvb_shapes(k, v, beta, B, T, H, dk, n_h)
     _check(q, "q", (B, T, H, dk), dt, dev)
     _check(k, "k", kshape, dt, dev)
@@ -600,13 +606,13 @@ def delta_step(q, k, v, beta, g, state, out=None, *, n_h=1, stream=None):
     g [B,H] float32 or None.  Returns ``out`` [B,H,dv] in q's dtype.
     """
     lib = load_library()
-    B, H, dk = q.shape
+    B, H, dk = _dims(q)
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("delta_step needs CUDA tensors")
     dt = q.dtype
     code = _dtype_code(dt)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     _check(q, "q", (B, H, dk), dt, dev)
     _check(k, "k", (B, n_h, H, dk), dt, dev)
     _check(v, "v", (B, n_h, H, dv), dt, dev)
@@ -630,13 +636,13 @@ def delta_step_prologue(q_raw, k_raw, v, beta_raw, g, state, out=None, *, n_h=1,
     and results as in ``delta_step``."""
     lib = load_library()
     code_map = _beta_map(beta_map)
-    B, H, dk = q_raw.shape
+    B, H, dk = _dims(q_raw)
     dev = q_raw.device
     if dev.type != "cuda":
         raise ValueError("delta_step_prologue needs CUDA tensors")
     dt = q_raw.dtype
     code = _dtype_code(dt)
-    dv = v.shape[-1]
+    dv = _dims(v)[-1]
     _check(q_raw, "q_raw", (B, H, dk), dt, dev)
     _check(k_raw, "k_raw", (B, n_h, H, dk), dt, dev)
     _check(v, "v", (B, n_h, H, dv), dt, dev)

@@ -121,8 +121,19 @@ def _optional(t, name, shape, dtype, device):
     return None if t is None else _tensor(t, name, shape, dtype, device)
 
 
+_MOST = (1 << 31) - 1
+
+
+def _within_int(what, *sizes):
+    """The ABI's sizes are C ints, which ctypes would cut without a word."""
+    for n in sizes:
+        if n > _MOST:
+            raise ValueError(f"{what} has a size of {n}, the most is 2^31 - 1")
+
+
 def _begin(x, name, dims, what="x"):
-    """dtype code and device of the operator's leading tensor"""
+    """dtype code and device of the operator's leading tensor, whose `dims` axes
+    (or, with 0, whose last one) are sizes of the call"""
     try:
         dev, dt = x.device, x.dtype
     except AttributeError:
@@ -134,6 +145,7 @@ def _begin(x, name, dims, what="x"):
     code = _CODES.get(dt)
     if code is None:
         raise TypeError(f"{what} must be bfloat16 or float32, got {dt}")
+    _within_int(what, *(x.shape if dims else x.shape[-1:]))
     return code, dev
 
 
@@ -393,6 +405,8 @@ def _linear_begin(x, w, bias, residual, act, dtype, odt, dev):
     M = 1
     for n in x.shape[:-1]:
         M *= n
+    _within_int("w", N, K)
+    _within_int("x's leading axes", M)
     return acode, M, N, K, px, ldx, pw, w.stride(0), pb, bcode, pr, ldr, shape
 
 
