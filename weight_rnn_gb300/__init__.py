@@ -164,7 +164,7 @@ def delta_selftest_wait(polls: int = 1000, stream=None, device=None) -> None:
     ``polls`` tries) and records that in the device error word, which the
     next delta_check_device() reports."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    st = load_library().delta_selftest_wait(int(polls), _stream(dev, stream))
+    st = block._on(dev, load_library().delta_selftest_wait)(int(polls), _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
 
@@ -173,7 +173,7 @@ def delta_selftest_exchange(polls: int = 1000, stream=None, device=None) -> None
     """The same for the exchange of a scan's cluster: one of two CTAs never sends,
     the other gives up after ``polls`` tries."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    st = load_library().delta_selftest_exchange(int(polls), _stream(dev, stream))
+    st = block._on(dev, load_library().delta_selftest_exchange)(int(polls), _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
 
@@ -208,8 +208,10 @@ def _check(t, name, shape, dtype, device):
 def _dims(t):
     """The shape of a tensor whose axes are sizes of the ABI, which are C ints:
     ctypes would cut larger ones without a word."""
-    block._within_int("a tensor", *t.shape)
-    return t.shape
+    shape = t.shape
+    if max(shape) > block._MOST:
+        raise ValueError(f"a tensor has a size of {max(shape)}, the most is 2^31 - 1")
+    return shape
 
 
 def _stream(device, stream):
@@ -253,9 +255,8 @@ def delta_fwd(q, k, v, beta, g=None, h0=None, out=None, hT=None, *, n_h=1,
     if hT is None and want_state:
         hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
     _check(hT, "hT", (B, H, dk, dv), torch.float32, dev)
-    st = lib.delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(h0),
-                       _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk, code,
-                       _stream(dev, stream))
+    st = block._on(dev, lib.delta_fwd)(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(h0),
+        _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk, code, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out, hT
@@ -291,9 +292,9 @@ def delta_bwd(q, k, v, beta, g, h0, dout, dhT=None, *, n_h=1, want_dh0=True, str
     gb = torch.empty(bshape, **f32)
     gg = None if g is None else torch.empty((B, T, H), **f32)
     gh0 = torch.empty((B, H, dk, dv), **f32) if want_dh0 else None
-    st = lib.delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(h0), _ptr(dout), _ptr(dhT),
-                       _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gb), _ptr(gg), _ptr(gh0),
-                       B, H, T, dk, dv, n_h, code, _stream(dev, stream))
+    st = block._on(dev, lib.delta_bwd)(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(h0),
+        _ptr(dout), _ptr(dhT), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gb), _ptr(gg), _ptr(gh0), B, H, T,
+        dk, dv, n_h, code, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return gq, gk, gv, gb, gg, gh0
@@ -328,9 +329,8 @@ def delta_fwd_kda(q, k, v, beta, alpha, h0=None, out=None, hT=None, *, n_h=1, ch
     if hT is None and want_state:
         hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
     _check(hT, "hT", (B, H, dk, dv), torch.float32, dev)
-    st = lib.delta_fwd_kda(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(alpha), _ptr(h0),
-                           _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk, code,
-                           _stream(dev, stream))
+    st = block._on(dev, lib.delta_fwd_kda)(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(alpha),
+        _ptr(h0), _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk, code, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out, hT
@@ -356,8 +356,8 @@ def delta_step_kda(q, k, v, beta, alpha, state, out=None, *, n_h=1, stream=None)
     if out is None:
         out = torch.empty((B, H, dv), dtype=dt, device=dev)
     _check(out, "out", (B, H, dv), dt, dev)
-    st = lib.delta_step_kda(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(alpha), _ptr(state),
-                            _ptr(out), B, H, dk, dv, n_h, code, _stream(dev, stream))
+    st = block._on(dev, lib.delta_step_kda)(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(alpha),
+        _ptr(state), _ptr(out), B, H, dk, dv, n_h, code, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out
@@ -393,8 +393,8 @@ def delta_prologue(q_raw, k_raw, beta_raw, *, n_h=1, beta_map="sigmoid", stream=
     q = torch.empty_like(q_raw)
     k = torch.empty_like(k_raw)
     beta = torch.empty_like(beta_raw)
-    st = lib.delta_prologue(_ptr(q_raw), _ptr(k_raw), _ptr(beta_raw), _ptr(q), _ptr(k), _ptr(beta),
-                            B, H, T, dk, n_h, code, code_map, _stream(dev, stream))
+    st = block._on(dev, lib.delta_prologue)(_ptr(q_raw), _ptr(k_raw), _ptr(beta_raw), _ptr(q),
+        _ptr(k), _ptr(beta), B, H, T, dk, n_h, code, code_map, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return q, k, beta
@@ -431,9 +431,9 @@ def delta_fwd_prologue(q_raw, k_raw, v, beta_raw, g=None, h0=None, out=None, hT=
     if hT is None and want_state:
         hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
     _check(hT, "hT", (B, H, dk, dv), torch.float32, dev)
-    st = lib.delta_fwd_prologue(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(beta_raw), _ptr(g),
-                                _ptr(h0), _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk,
-                                code, code_map, _stream(dev, stream))
+    st = block._on(dev, lib.delta_fwd_prologue)(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(beta_raw),
+        _ptr(g), _ptr(h0), _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk, code, code_map,
+        _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out, hT
@@ -466,9 +466,9 @@ def delta_fwd_static_scratch(q, k, v, beta, g=None, h0=None, out=None, hT=None, 
     if hT is None and want_state:
         hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
     _check(hT, "hT", (B, H, dk, dv), torch.float32, dev)
-    st = lib.delta_fwd_static_scratch(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g),
-                                      _ptr(h0), _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h,
-                                      chunk, code, _stream(dev, stream))
+    st = block._on(dev, lib.delta_fwd_static_scratch)(_ptr(q), _ptr(k), _ptr(v), _ptr(beta),
+        _ptr(g), _ptr(h0), _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk, code,
+        _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out, hT
@@ -487,7 +487,8 @@ def delta_state_erank(state, erank=None, *, stream=None):
     if erank is None:
         erank = torch.empty((B, H), dtype=torch.float32, device=dev)
     _check(erank, "erank", (B, H), torch.float32, dev)
-    st = lib.delta_state_erank(_ptr(state), _ptr(erank), B, H, dk, dv, _stream(dev, stream))
+    st = block._on(dev, lib.delta_state_erank)(_ptr(state), _ptr(erank), B, H, dk, dv,
+        _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return erank
@@ -511,8 +512,8 @@ def delta_attention_map(q, k, beta, g=None, attn=None, *, stream=None):
     if attn is None:
         attn = torch.empty((B, H, N, N), dtype=torch.float32, device=dev)
     _check(attn, "attn", (B, H, N, N), torch.float32, dev)
-    st = lib.delta_attention_map(_ptr(q), _ptr(k), _ptr(beta), _ptr(g), _ptr(attn), B, H, N,
-                                 dk, _dtype_code(dt), _stream(dev, stream))
+    st = block._on(dev, lib.delta_attention_map)(_ptr(q), _ptr(k), _ptr(beta), _ptr(g), _ptr(attn),
+        B, H, N, dk, _dtype_code(dt), _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return attn
@@ -547,8 +548,8 @@ def delta_ut_transform(k, beta, g=None, t_mat=None, *, n_h=1, chunk=64, stream=N
     if t_mat is None:
         t_mat = torch.empty((B, H, nt, chunk, chunk), dtype=torch.bfloat16, device=dev)
     _check(t_mat, "t_mat", (B, H, nt, chunk, chunk), torch.bfloat16, dev)
-    st = lib.delta_ut_transform(_ptr(k), _ptr(beta), _ptr(g), _ptr(t_mat), B, H, T, dk, n_h,
-                                chunk, code, _stream(dev, stream))
+    st = block._on(dev, lib.delta_ut_transform)(_ptr(k), _ptr(beta), _ptr(g), _ptr(t_mat), B, H, T,
+        dk, n_h, chunk, code, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return t_mat
@@ -582,9 +583,9 @@ def delta_fwd_with_ut(q, k, v, beta, g, h0, t_mat, out=None, hT=None, *, n_h=1, 
     if hT is None and want_state:
         hT = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
     _check(hT, "hT", (B, H, dk, dv), torch.float32, dev)
-    st = lib.delta_fwd_with_ut(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(h0),
-                               _ptr(t_mat), _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk,
-                               code, _stream(dev, stream))
+    st = block._on(dev, lib.delta_fwd_with_ut)(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g),
+        _ptr(h0), _ptr(t_mat), _ptr(out), _ptr(hT), B, H, T, dk, dv, n_h, chunk, code,
+        _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out, hT
@@ -622,8 +623,8 @@ def delta_step(q, k, v, beta, g, state, out=None, *, n_h=1, stream=None):
     if out is None:
         out = torch.empty((B, H, dv), dtype=dt, device=dev)
     _check(out, "out", (B, H, dv), dt, dev)
-    st = lib.delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(state),
-                        _ptr(out), B, H, dk, dv, n_h, code, _stream(dev, stream))
+    st = block._on(dev, lib.delta_step)(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(state),
+        _ptr(out), B, H, dk, dv, n_h, code, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out
@@ -652,9 +653,8 @@ def delta_step_prologue(q_raw, k_raw, v, beta_raw, g, state, out=None, *, n_h=1,
     if out is None:
         out = torch.empty((B, H, dv), dtype=dt, device=dev)
     _check(out, "out", (B, H, dv), dt, dev)
-    st = lib.delta_step_prologue(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(beta_raw), _ptr(g),
-                                 _ptr(state), _ptr(out), B, H, dk, dv, n_h, code, code_map,
-                                 _stream(dev, stream))
+    st = block._on(dev, lib.delta_step_prologue)(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(beta_raw),
+        _ptr(g), _ptr(state), _ptr(out), B, H, dk, dv, n_h, code, code_map, _stream(dev, stream))
     if st != DELTA_OK:
         raise DeltaError(st, delta_last_error())
     return out

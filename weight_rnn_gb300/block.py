@@ -121,14 +121,29 @@ def _optional(t, name, shape, dtype, device):
     return None if t is None else _tensor(t, name, shape, dtype, device)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on(dev, fn):
+    """A call of the library with the tensors' device current: it launches,
+    allocates scratch and asks for the number of SMs on the current one, and the
+    default stream's handle is the same on every device."""
+    if dev.index == _current_device():
+        return fn
+
+    def call(*args):
+        with torch.cuda.device(dev):
+            return fn(*args)
+    return call
+
+
 _MOST = (1 << 31) - 1
 
 
-def _within_int(what, *sizes):
+def _within_int(what, sizes):
     """The ABI's sizes are C ints, which ctypes would cut without a word."""
-    for n in sizes:
-        if n > _MOST:
-            raise ValueError(f"{what} has a size of {n}, the most is 2^31 - 1")
+    if sizes and max(sizes) > _MOST:
+        raise ValueError(f"{what} has a size of {max(sizes)}, the most is 2^31 - 1")
 
 
 def _begin(x, name, dims, what="x"):
@@ -145,7 +160,7 @@ def _begin(x, name, dims, what="x"):
     code = _CODES.get(dt)
     if code is None:
         raise TypeError(f"{what} must be bfloat16 or float32, got {dt}")
-    _within_int(what, *(x.shape if dims else x.shape[-1:]))
+    _within_int(what, x.shape if dims else x.shape[-1:])
     return code, dev
 
 
@@ -213,10 +228,9 @@ def delta_scan_fwd(x, gate, h0=None, *, form="sigmoid", lengths=None, save_state
     out = _output(out, "out", (B, T, D), x.dtype, dev, stream)
     hT = _output(hT, "hT", (B, D), torch.float32, dev, stream)
     states = _empty((B, -(-T // SCAN_BLOCK), D), torch.float32, dev, stream) if save_states else None
-    st = _lib().delta_scan_fwd(px, pg, ph, pl, out.data_ptr(), hT.data_ptr(),
-                               None if states is None else states.data_ptr(), B, T, D,
-                               x.stride(0), x.stride(1), gate.stride(0), gate.stride(1), code,
-                               fcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_scan_fwd)(px, pg, ph, pl, out.data_ptr(), hT.data_ptr(),
+        None if states is None else states.data_ptr(), B, T, D, x.stride(0), x.stride(1),
+        gate.stride(0), gate.stride(1), code, fcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return (out, hT, states) if save_states else (out, hT)
@@ -236,8 +250,8 @@ def delta_scan_step(x, gate, state, *, form="sigmoid", out=None, stream=None):
     pg = _tensor(gate, "gate", x.shape, gdt, dev, True)
     ps = _tensor(state, "state", x.shape, torch.float32, dev)
     out = _output(out, "out", x.shape, x.dtype, dev, stream)
-    st = _lib().delta_scan_step(px, pg, ps, out.data_ptr(), B, D, x.stride(0), gate.stride(0),
-                                code, fcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_scan_step)(px, pg, ps, out.data_ptr(), B, D, x.stride(0),
+        gate.stride(0), code, fcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return out
@@ -264,9 +278,9 @@ def delta_scan_bwd(x, gate, states, dout, dhT=None, *, form="sigmoid", lengths=N
     pl = _optional(lengths, "lengths", (B,), torch.int32, dev)
     dx, dgate = _empty(x.shape, x.dtype, dev, stream), _empty(x.shape, gdt, dev, stream)
     dh0 = _empty((B, D), torch.float32, dev, stream)
-    st = _lib().delta_scan_bwd(px, pg, ps, pl, po, pt, dx.data_ptr(), dgate.data_ptr(),
-                               dh0.data_ptr(), B, T, D, x.stride(0), x.stride(1),
-                               gate.stride(0), gate.stride(1), code, fcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_scan_bwd)(px, pg, ps, pl, po, pt, dx.data_ptr(), dgate.data_ptr(),
+        dh0.data_ptr(), B, T, D, x.stride(0), x.stride(1), gate.stride(0), gate.stride(1), code,
+        fcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return dx, dgate, dh0
@@ -331,9 +345,9 @@ def delta_add_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, sum_out=None, s
         sum_out = _output(sum_out, "sum_out", x.shape, x.dtype, dev, stream)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual: without one the sum is x")
-    st = _lib().delta_add_rmsnorm_fwd(px, pr, pw, y.data_ptr(),
-                                      None if sum_out is None else sum_out.data_ptr(),
-                                      rstd.data_ptr(), rows, D, ldx, ldr, eps, code, wcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_add_rmsnorm_fwd)(px, pr, pw, y.data_ptr(),
+        None if sum_out is None else sum_out.data_ptr(), rstd.data_ptr(), rows, D, ldx, ldr, eps,
+        code, wcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return y, (x if sum_out is None else sum_out), rstd
@@ -354,9 +368,9 @@ def delta_add_rmsnorm_quant(x, weight, residual=None, *, eps=1e-6, sum_out=None,
         sum_out = _output(sum_out, "sum_out", x.shape, x.dtype, dev, stream)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual: without one the sum is x")
-    st = _lib().delta_add_rmsnorm_quant(px, pr, pw, y.data_ptr(), scale.data_ptr(),
-                                        None if sum_out is None else sum_out.data_ptr(), rows, D,
-                                        ldx, ldr, eps, code, wcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_add_rmsnorm_quant)(px, pr, pw, y.data_ptr(), scale.data_ptr(),
+        None if sum_out is None else sum_out.data_ptr(), rows, D, ldx, ldr, eps, code, wcode,
+        _raw_stream(dev, stream))
     if st:
         _raise(st)
     return y, scale, (x if sum_out is None else sum_out)
@@ -382,8 +396,8 @@ def delta_add_rmsnorm_bwd(dy, sum, weight, rstd, dsum=None, *, dx=None, stream=N
     pw, wcode = _weight(weight, D, dy.dtype, dev)
     dx = _output(dx, "dx", dy.shape, dy.dtype, dev, stream)
     dweight = _empty((D,), torch.float32, dev, stream)
-    st = _lib().delta_add_rmsnorm_bwd(py, ps, pw, pr, pd, dx.data_ptr(), dweight.data_ptr(),
-                                      dy.numel() // D if D else 0, D, code, wcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_add_rmsnorm_bwd)(py, ps, pw, pr, pd, dx.data_ptr(),
+        dweight.data_ptr(), dy.numel() // D if D else 0, D, code, wcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return dx, dweight
@@ -405,8 +419,7 @@ def _linear_begin(x, w, bias, residual, act, dtype, odt, dev):
     M = 1
     for n in x.shape[:-1]:
         M *= n
-    _within_int("w", N, K)
-    _within_int("x's leading axes", M)
+    _within_int("the layer", (M, N, K))
     return acode, M, N, K, px, ldx, pw, w.stride(0), pb, bcode, pr, ldr, shape
 
 
@@ -429,9 +442,9 @@ def delta_linear_fwd(x, w, bias=None, residual=None, *, act="none", save_pre=Fal
         x, w, bias, residual, act, dt, dt, dev)
     out = _output(out, "out", shape, dt, dev, stream)
     pre = _empty(shape, dt, dev, stream) if save_pre else None
-    st = _lib().delta_linear_fwd(px, pw, pb, pr, out.data_ptr(),
-                                 None if pre is None else pre.data_ptr(), M, N, K, ldx, ldw, ldr,
-                                 acode, code, bcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_linear_fwd)(px, pw, pb, pr, out.data_ptr(),
+        None if pre is None else pre.data_ptr(), M, N, K, ldx, ldw, ldr, acode, code, bcode,
+        _raw_stream(dev, stream))
     if st:
         _raise(st)
     return (out, pre) if save_pre else out
@@ -457,8 +470,8 @@ def delta_linear_quant(x, x_scale, w, w_scale, bias=None, residual=None, *, act=
     psx = _tensor(x_scale, "x_scale", x.shape[:-1], torch.float32, dev)
     psw = _tensor(w_scale, "w_scale", (N,), torch.float32, dev)
     out = _output(out, "out", shape, torch.bfloat16, dev, stream)
-    st = _lib().delta_linear_quant(px, psx, pw, psw, pb, pr, out.data_ptr(), M, N, K, ldx, ldw,
-                                   ldr, acode, bcode, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_linear_quant)(px, psx, pw, psw, pb, pr, out.data_ptr(), M, N, K, ldx,
+        ldw, ldr, acode, bcode, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return out
@@ -482,8 +495,8 @@ def delta_linear_bwd(x, w, dout, pre=None, *, act="none", want=(True, True, True
     dw = _empty((N, K), dt, dev, stream) if want[1] else None
     db = _empty((N,), torch.float32, dev, stream) if want[2] else None
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    st = _lib().delta_linear_bwd(px, pw, po, pp, ptr(dx), ptr(dw), ptr(db), M, N, K, ldx, ldw,
-                                 acode, code, _raw_stream(dev, stream))
+    st = _on(dev, _lib().delta_linear_bwd)(px, pw, po, pp, ptr(dx), ptr(dw), ptr(db), M, N, K, ldx,
+        ldw, acode, code, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return dx, dw, db

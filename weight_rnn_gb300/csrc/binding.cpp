@@ -2,13 +2,15 @@
 // plain CUDA tensors of the right types and shapes, outputs to be allocated,
 // the current stream.  Checking, allocating and calling here takes about a
 // third of what the same does in Python, which is what a small call costs.
-// Whatever else comes (another stream, given outputs, a wrong argument) gets
+// Whatever else comes (another stream, given outputs, a wrong argument, tensors on
+// a device that is not the current one) gets
 // NotImplemented, and block.py takes it from there: its checks say what is
 // wrong.  A status other than DELTA_OK comes back as an int.
 #include <Python.h>
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -24,6 +26,9 @@ const Tensor *tensor(PyObject *o) {
   const Tensor &t = THPVariable_Unpack(o);
   return t.defined() && t.is_cuda() && t.layout() == at::kStrided ? &t : nullptr;
 }
+
+// the library launches on the current device
+bool here(int dev) { return c10::cuda::current_device() == dev; }
 
 int code(at::ScalarType t) { return t == at::kBFloat16 ? DELTA_BF16 : t == at::kFloat ? DELTA_F32 : -1; }
 
@@ -84,7 +89,7 @@ PyObject *scan_fwd(PyObject *const *a, Py_ssize_t n) {
   const int dev = x->get_device();
   const auto dt = x->scalar_type(), gt = form == DELTA_SCAN_LINEAR ? at::kFloat : dt;
   const int64_t B = x->size(0), T = x->size(1), D = x->size(2);
-  if (!fits(B) || !fits(T) || !fits(D) || !rows(x, dt, x->sizes(), dev) || !rows(g, gt, x->sizes(), dev) ||
+  if (!here(dev) || !fits(B) || !fits(T) || !fits(D) || !rows(x, dt, x->sizes(), dev) || !rows(g, gt, x->sizes(), dev) ||
       !optional_whole(a[2], h0, at::kFloat, {B, D}, dev) || !optional_whole(a[3], len, at::kInt, {B}, dev))
     return other();
   const bool save = truth(a[4]);
@@ -107,7 +112,7 @@ PyObject *scan_step(PyObject *const *a, Py_ssize_t n) {
   if (!x || x->dim() != 2 || code(x->scalar_type()) < 0 || (form != 0 && form != 1)) return other();
   const int dev = x->get_device();
   const auto dt = x->scalar_type();
-  if (!fits(x->size(0)) || !fits(x->size(1)) || !rows(x, dt, x->sizes(), dev) ||
+  if (!here(dev) || !fits(x->size(0)) || !fits(x->size(1)) || !rows(x, dt, x->sizes(), dev) ||
       !rows(g, form == DELTA_SCAN_LINEAR ? at::kFloat : dt, x->sizes(), dev) ||
       !whole(s, at::kFloat, x->sizes(), dev))
     return other();
@@ -128,7 +133,7 @@ PyObject *scan_bwd(PyObject *const *a, Py_ssize_t n) {
   const int dev = x->get_device();
   const auto dt = x->scalar_type(), gt = form == DELTA_SCAN_LINEAR ? at::kFloat : dt;
   const int64_t B = x->size(0), T = x->size(1), D = x->size(2);
-  if (!fits(B) || !fits(T) || !fits(D) || !rows(x, dt, x->sizes(), dev) || !rows(g, gt, x->sizes(), dev) ||
+  if (!here(dev) || !fits(B) || !fits(T) || !fits(D) || !rows(x, dt, x->sizes(), dev) || !rows(g, gt, x->sizes(), dev) ||
       !whole(s, at::kFloat, {B, (T + kScanBlock - 1) / kScanBlock, D}, dev) || !whole(d, dt, x->sizes(), dev) ||
       !optional_whole(a[4], dh, at::kFloat, {B, D}, dev) || !optional_whole(a[5], len, at::kInt, {B}, dev))
     return other();
@@ -162,7 +167,7 @@ PyObject *norm_fwd(PyObject *const *a, Py_ssize_t n) {
   const auto shape = x->sizes();
   const int64_t D = shape.back();
   int64_t ldx = 0, ldr = D;
-  if (!fits(D) || !as_rows(x, dt, shape, dev, ldx) || !whole(w, w->scalar_type(), {D}, dev) ||
+  if (!here(dev) || !fits(D) || !as_rows(x, dt, shape, dev, ldx) || !whole(w, w->scalar_type(), {D}, dev) ||
       (a[2] != Py_None && !as_rows(r, dt, shape, dev, ldr)))
     return other();
   const int64_t count = D > 0 ? x->numel() / D : 0;
@@ -191,7 +196,7 @@ PyObject *norm_bwd(PyObject *const *a, Py_ssize_t n) {
   const auto dt = dy->scalar_type();
   const auto shape = dy->sizes();
   const int64_t D = shape.back();
-  if (!fits(D) || !whole(dy, dt, shape, dev) || !whole(sum, dt, shape, dev) || !whole(w, w->scalar_type(), {D}, dev) ||
+  if (!here(dev) || !fits(D) || !whole(dy, dt, shape, dev) || !whole(sum, dt, shape, dev) || !whole(w, w->scalar_type(), {D}, dev) ||
       !whole(r, at::kFloat, shape.slice(0, shape.size() - 1), dev) || !optional_whole(a[4], ds, dt, shape, dev))
     return other();
   Tensor dx = empty(shape, dt, dev), dw = empty({D}, at::kFloat, dev);
@@ -216,7 +221,7 @@ struct Linear {
     dev = x->get_device();
     N = w->size(0);
     K = w->size(1);
-    if (!fits(N) || !fits(K) || x->size(-1) != K || !rows(w, dt, w->sizes(), dev) ||
+    if (!here(dev) || !fits(N) || !fits(K) || x->size(-1) != K || !rows(w, dt, w->sizes(), dev) ||
         !as_rows(x, dt, x->sizes(), dev, ldx))
       return false;
     ldw = w->stride(0);
