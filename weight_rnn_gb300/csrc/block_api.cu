@@ -127,9 +127,14 @@ int run_norm_fwd(const void *x, const void *residual, const void *weight, void *
   if ((st = check_overlap({ys, ds, cs}, {xs, rs, ws})) != DELTA_OK) return st;
   if ((st = check_overlap({ss}, {ws, ys, ds, cs})) != DELTA_OK) return st;
   // the residual stream may be updated in place: the same rows, or none
-  for (const Span &in : {xs, rs}) {
-    const bool same = in.r.lo == ss.r.lo && (rows == 1 || (in.r.lo == rs.r.lo ? ldr : ldx) == D);
-    if (overlap(ss.r, in.r) && !same) return fail(DELTA_ERR_INVALID, "sum_out partly overlaps %s", in.name);
+  const struct {
+    Span span;
+    int64_t ld;
+  } inputs[] = {{xs, ldx}, {rs, ldr}};
+  for (const auto &in : inputs) {
+    const bool same = in.span.r.lo == ss.r.lo && (rows == 1 || in.ld == D);
+    if (overlap(ss.r, in.span.r) && !same)
+      return fail(DELTA_ERR_INVALID, "sum_out partly overlaps %s", in.span.name);
   }
   if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
   delta::NormArgs a{};
