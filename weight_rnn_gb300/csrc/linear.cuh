@@ -42,7 +42,9 @@ __device__ __forceinline__ float slope(int act, float p) {
   }
   if (act == kActGelu) {
     const float s = sigmoid(kGelu2c * (p + kGelu3 * p * p * p));
-    return s + p * s * (1.f - s) * kGelu2c * (1.f + 3.f * kGelu3 * p * p);
+    // past 16, s (1 - s) is 0 in float32, but the square of a large p is not finite
+    const float q = fminf(fmaxf(p, -16.f), 16.f);
+    return s + q * s * (1.f - s) * kGelu2c * (1.f + 3.f * kGelu3 * q * q);
   }
   return 1.f;
 }
