@@ -80,6 +80,37 @@ def binding_command(obj):
             "-c", BINDING_SRC, "-o", obj]
 
 
+def binding_made_with():
+    """What a built module belongs to besides its sources."""
+    import importlib.metadata
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "none"
+    return f"torch {torch}, python {sys.version}, {os.environ.get('CXX') or shutil.which('g++')}"
+
+
+def _binding_note():
+    return os.path.join(BUILD, os.path.basename(BINDING) + ".from")
+
+
+def _binding_is_stale():
+    if _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "delta.h")]):
+        return True
+    try:
+        with open(_binding_note()) as f:
+            return f.read() != binding_made_with()
+    except OSError:
+        return True
+
+
+def _discard_binding():
+    """A module of other sources or another torch is not to be loaded."""
+    for path in (BINDING, _binding_note()):
+        if os.path.exists(path):
+            os.remove(path)
+
+
 def link_binding(obj):
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -92,6 +123,8 @@ def link_binding(obj):
     if r.returncode != 0:
         raise RuntimeError(r.stdout + r.stderr)
     os.replace(tmp, BINDING)
+    with open(_binding_note(), "w") as f:
+        f.write(binding_made_with())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -112,8 +145,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     bobj = os.path.join(BUILD, "binding.o")
     bcmd = None
-    if force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "delta.h")]):
+    if force or _binding_is_stale():
         bcmd = binding_command(bobj)
+        if bcmd is None:
+            _discard_binding()
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -143,6 +178,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 raise RuntimeError(r.stdout + r.stderr)
             link_binding(bobj)
         except RuntimeError as e:
+            _discard_binding()
             sys.stderr.write(f"binding.cpp was not built; calls go through ctypes alone:\n{e}\n")
     return LIB
 
