@@ -530,7 +530,8 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
  *                         may be x or residual itself (then contiguous)
  *   rstd        [rows]    float32 or NULL
  *
- * The norm is of the unrounded t.  D <= 8192, eps > 0.
+ * The norm is of the unrounded t.  D <= 8192, eps > 0.  With D = 0 nothing is
+ * written.
  */
 int delta_add_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *y, void *sum_out,
                           float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,

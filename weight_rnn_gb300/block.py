@@ -312,6 +312,15 @@ def _weight(weight, D, dt, dev, name="weight"):
     return _tensor(weight, name, (D,), wdt, dev), _CODES[wdt]
 
 
+def _per_row(shape, empty_value, D, dev, stream):
+    """A float32 a row; rows without elements are never reached by the kernels."""
+    t = _empty(shape, torch.float32, dev, stream)
+    if D == 0:
+        with torch.cuda.stream(stream):  # (None: the current one)
+            t.fill_(empty_value)
+    return t
+
+
 def _norm_begin(x, weight, residual, name):
     code, dev = _begin(x, name, 0)
     if x.dim() < 1:
@@ -340,7 +349,7 @@ def delta_add_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, sum_out=None, s
     code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
                                                                  "delta_add_rmsnorm_fwd")
     y = _empty(x.shape, x.dtype, dev, stream)
-    rstd = _empty(x.shape[:-1], torch.float32, dev, stream)
+    rstd = _per_row(x.shape[:-1], eps ** -0.5 if eps > 0 else 0.0, D, dev, stream)
     if residual is not None:
         sum_out = _output(sum_out, "sum_out", x.shape, x.dtype, dev, stream)
     elif sum_out is not None:
@@ -363,7 +372,7 @@ def delta_add_rmsnorm_quant(x, weight, residual=None, *, eps=1e-6, sum_out=None,
     code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
                                                                  "delta_add_rmsnorm_quant")
     y = _empty(x.shape, E4M3, dev, stream)
-    scale = _empty(x.shape[:-1], torch.float32, dev, stream)
+    scale = _per_row(x.shape[:-1], 1.0, D, dev, stream)
     if residual is not None:
         sum_out = _output(sum_out, "sum_out", x.shape, x.dtype, dev, stream)
     elif sum_out is not None:

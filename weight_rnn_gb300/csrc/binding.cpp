@@ -167,10 +167,10 @@ PyObject *norm_fwd(PyObject *const *a, Py_ssize_t n) {
   const auto shape = x->sizes();
   const int64_t D = shape.back();
   int64_t ldx = 0, ldr = D;
-  if (!here(dev) || !fits(D) || !as_rows(x, dt, shape, dev, ldx) || !whole(w, w->scalar_type(), {D}, dev) ||
+  if (!here(dev) || !fits(D) || D == 0 || !as_rows(x, dt, shape, dev, ldx) || !whole(w, w->scalar_type(), {D}, dev) ||
       (a[2] != Py_None && !as_rows(r, dt, shape, dev, ldr)))
     return other();
-  const int64_t count = D > 0 ? x->numel() / D : 0;
+  const int64_t count = x->numel() / D;
   const bool quant = truth(a[4]);
   Tensor y = empty(shape, quant ? at::kFloat8_e4m3fn : dt, dev), per = empty(shape.slice(0, shape.size() - 1), at::kFloat, dev);
   Tensor sum;
