@@ -416,7 +416,8 @@ int delta_version(void);
  * delta_inject_failure -- test hook: the next `count` calls of delta_fwd,
  * delta_bwd, delta_fwd_kda, delta_step_kda, delta_prologue,
  * delta_fwd_prologue, delta_ut_transform, delta_fwd_with_ut, delta_step,
- * delta_step_prologue, delta_state_erank and delta_attention_map (together)
+ * delta_step_prologue, delta_state_erank, delta_attention_map and the operators
+ * around the mixers (delta_scan_*, delta_add_rmsnorm_*, delta_linear_*; together)
  * return DELTA_ERR_CUDA, with "injected failure" in delta_last_error(),
  * right after their arguments pass validation and before
  * anything is enqueued.  count = 0 clears a pending injection; count < 0 is
@@ -531,7 +532,8 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
  *   rstd        [rows]    float32 or NULL
  *
  * The norm is of the unrounded t.  D <= 8192, eps > 0.  With D = 0 nothing is
- * written.
+ * written.  The mean of squares is float32: a row whose squares sum past its range
+ * (elements above 1.8e19) counts as infinite, rstd 0.
  */
 int delta_add_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *y, void *sum_out,
                           float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
@@ -601,6 +603,9 @@ int delta_linear_fwd(const void *x, const void *w, const void *bias, const void 
  * [N] float32 (a scale a row, as delta_add_rmsnorm_quant writes them):
  *
  *   pre = (x w^T) x_scale[m] w_scale[n] + bias.   out and residual are bfloat16.
+ *
+ * The product of the two scales is taken first, in float32, and has to be in its
+ * range.
  */
 int delta_linear_quant(const void *x, const float *x_scale, const void *w, const float *w_scale,
                        const void *bias, const void *residual, void *out, int M, int N, int K, int64_t ldx,
@@ -618,9 +623,10 @@ int delta_linear_quant(const void *x, const float *x_scale, const void *w, const
  *   dx     [M, K] dtype,  dw [N, K] dtype,  dbias [N] float32; NULL: not wanted
  *
  * In bfloat16, dpre is rounded to bfloat16 as an operand of the two products
- * (dbias sums it unrounded); layers small enough for one launch keep it in
- * float32.  It and packed operands go to scratch from the library's pool,
- * stream-ordered.
+ * (dbias sums it unrounded), which takes the error of dx and dw from 1.7e-3 to
+ * 2.4e-3 of their norm; layers small enough for one launch, which their sizes
+ * alone decide, keep it in float32.  It and packed operands go to scratch from
+ * the library's pool, stream-ordered.
  */
 int delta_linear_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                      float *dbias, int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act,

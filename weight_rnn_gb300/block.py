@@ -10,6 +10,9 @@ current stream) is taken by the compiled module ``_fast``; what that does not
 take is checked and called here, with the same results.
 With ``stream=`` the outputs are allocated for that stream; inputs made on
 another stream are the caller's to order and to keep, as with any kernel.
+None of the calls takes part in autograd, like the mixers': outputs carry no
+gradient function whatever their inputs ask for, and the gradients are calls of
+their own.  Tensors may be on any device; their own is made current for a call.
 """
 from __future__ import annotations
 

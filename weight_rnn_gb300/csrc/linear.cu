@@ -550,7 +550,6 @@ cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, con
                              float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
                              cudaStream_t s) {
   using T = __nv_bfloat16;
-  if (K == 0) dx = dw = nullptr;
   SmallBwd p{};
   p.dout = static_cast<const T *>(dout), p.pre = static_cast<const T *>(pre);
   p.x = static_cast<const T *>(x), p.w = static_cast<const T *>(w);
