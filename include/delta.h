@@ -417,7 +417,8 @@ int delta_version(void);
  * delta_bwd, delta_fwd_kda, delta_step_kda, delta_prologue,
  * delta_fwd_prologue, delta_ut_transform, delta_fwd_with_ut, delta_step,
  * delta_step_prologue, delta_state_erank, delta_attention_map and the operators
- * around the mixers (delta_scan_*, delta_add_rmsnorm_*, delta_linear_*; together)
+ * around the mixers (delta_scan_*, delta_decay_*, delta_add_rmsnorm_*,
+ * delta_add_layernorm_*, delta_linear_*, delta_glu_*; together)
  * return DELTA_ERR_CUDA, with "injected failure" in delta_last_error(),
  * right after their arguments pass validation and before
  * anything is enqueued.  count = 0 clears a pending injection; count < 0 is
@@ -518,6 +519,69 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
                    const void *dout, const float *dhT, void *dx, void *dgate, float *dh0, int B, int T,
                    int D, int64_t x_sb, int64_t x_st, int64_t g_sb, int64_t g_st, delta_dtype dtype,
                    delta_scan_form form, struct CUstream_st *stream);
+
+/*
+ * delta_decay_fwd -- linear attention with a decay for each head: a state per
+ * (b, h), no delta rule,
+ *
+ *   S_t = decay_h S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t.
+ *
+ *   q, k    [B, T, H, dk] dtype,  v [B, T, H, dv] dtype, channels contiguous;
+ *           strides: nine element strides in host memory, of the batch row, the
+ *           token and the head, of q, then k, then v
+ *   decay   [H]           float32 in [0, 1]; powers of it below float32's normal
+ *                         range count as 0
+ *   h0      [B, H, dk, dv] float32 or NULL (=> 0)
+ *   lengths [B]           int32 tokens of each row, taken into [0, T], or NULL
+ *                         (=> T); what later tokens hold does not matter, they
+ *                         leave the state alone and have out = 0
+ *   out     [B, T, H, dv] dtype
+ *   hT      [B, H, dk, dv] float32 state after the last token, or NULL; hT == h0
+ *                         allowed
+ *
+ * 1 <= dk, dv <= 256.  bfloat16 with dk <= 128, dk and dv multiples of 8 and q, k
+ * and v in whole 16-byte pieces (addresses and strides, none of them 0) runs on the
+ * tensor cores in chunks of 128 tokens; all else runs on the CUDA cores in float32,
+ * a correctness path.  The state is float32 throughout; on the tensor cores a
+ * token's way into it is rounded to 2^-16 of itself, and what out reads of it to
+ * bfloat16.  Where B * H does not fill the GPU the time axis is cut into segments,
+ * whose states (at most 1 GiB) go to scratch from the library's pool,
+ * stream-ordered.  Sizes alone decide the way, and the result does not depend on
+ * scheduling.
+ */
+int delta_decay_fwd(const void *q, const void *k, const void *v, const float *decay, const float *h0,
+                    const int *lengths, void *out, float *hT, int B, int T, int H, int dk, int dv,
+                    const int64_t *strides, float scale, delta_dtype dtype, struct CUstream_st *stream);
+
+/*
+ * delta_decay_step -- one token of the same: state [B, H, dk, dv] float32 is
+ * updated in place; q, k [B, H, dk], v [B, H, dv] with six strides (batch row and
+ * head of q, k, v); out [B, H, dv] dtype.  All in float32.
+ */
+int delta_decay_step(const void *q, const void *k, const void *v, const float *decay, float *state, void *out, int B,
+                     int H, int dk, int dv, const int64_t *strides, float scale, delta_dtype dtype,
+                     struct CUstream_st *stream);
+
+/*
+ * delta_decay_bwd -- gradients of delta_decay_fwd's out and hT (the decays are
+ * constants of the layer and have none):
+ *
+ *   R_t = scale q_t dout_t^T + decay_h R_{t+1}  (after the last token: + dhT),
+ *   dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dh0 = decay_h R_1.
+ *
+ *   q .. lengths, strides  as in the forward (h0 too: no states are kept)
+ *   dout    [B, T, H, dv] dtype, contiguous
+ *   dhT     [B, H, dk, dv] float32 or NULL (=> 0)
+ *   dq, dk_out [B, T, H, dk], dv_out [B, T, H, dv]  dtype; 0 past a row's length
+ *   dh0     [B, H, dk, dv] float32 or NULL
+ *
+ * Runs as the forward does, with the same bounds and scratch.  With T = 0, dh0 ==
+ * dhT is allowed.
+ */
+int delta_decay_bwd(const void *q, const void *k, const void *v, const float *decay, const float *h0,
+                    const int *lengths, const void *dout, const float *dhT, void *dq, void *dk_out, void *dv_out,
+                    float *dh0, int B, int T, int H, int dk, int dv, const int64_t *strides, float scale,
+                    delta_dtype dtype, struct CUstream_st *stream);
 
 /*
  * delta_add_rmsnorm_fwd -- the residual addition and the root-mean-square norm,

@@ -18,8 +18,9 @@ import torch
 
 from . import block
 from .block import (delta_add_rmsnorm_bwd, delta_add_rmsnorm_fwd, delta_add_rmsnorm_quant,
-                    delta_linear_bwd, delta_linear_fwd, delta_linear_quant, delta_scan_bwd,
-                    delta_scan_fwd, delta_scan_step)
+                    delta_decay_bwd, delta_decay_fwd, delta_decay_step, delta_linear_bwd,
+                    delta_linear_fwd, delta_linear_quant, delta_scan_bwd, delta_scan_fwd,
+                    delta_scan_step)
 
 __all__ = ["delta_fwd", "delta_bwd", "delta_fwd_kda", "delta_step_kda", "delta_prologue",
            "delta_fwd_prologue", "delta_step_prologue",

@@ -1,5 +1,6 @@
 """Operators around the token mixers in a block: the gated linear recurrence
-(``delta_scan_*``), the residual addition with RMS norm
+(``delta_scan_*``), linear attention with a decay for each head
+(``delta_decay_*``), the residual addition with RMS norm
 (``delta_add_rmsnorm_*``) and the linear layer with its epilogue
 (``delta_linear_*``).
 
@@ -31,7 +32,8 @@ _ACTS = {"none": DELTA_ACT_NONE, "silu": DELTA_ACT_SILU, "gelu": DELTA_ACT_GELU}
 _CODES = {torch.float32: 0, torch.bfloat16: 1}
 E4M3 = torch.float8_e4m3fn
 
-SYMBOLS = ("delta_scan_fwd", "delta_scan_step", "delta_scan_bwd", "delta_add_rmsnorm_fwd",
+SYMBOLS = ("delta_scan_fwd", "delta_scan_step", "delta_scan_bwd", "delta_decay_fwd",
+           "delta_decay_step", "delta_decay_bwd", "delta_add_rmsnorm_fwd",
            "delta_add_rmsnorm_quant", "delta_add_rmsnorm_bwd", "delta_linear_fwd",
            "delta_linear_quant", "delta_linear_bwd")
 
@@ -43,6 +45,9 @@ def declare(lib) -> None:
             ("delta_scan_fwd", [p] * 7 + [i] * 3 + [n] * 4 + [i] * 2 + [p]),
             ("delta_scan_step", [p] * 4 + [i] * 2 + [n] * 2 + [i] * 2 + [p]),
             ("delta_scan_bwd", [p] * 9 + [i] * 3 + [n] * 4 + [i] * 2 + [p]),
+            ("delta_decay_fwd", [p] * 8 + [i] * 5 + [p, f, i, p]),
+            ("delta_decay_step", [p] * 6 + [i] * 4 + [p, f, i, p]),
+            ("delta_decay_bwd", [p] * 12 + [i] * 5 + [p, f, i, p]),
             ("delta_add_rmsnorm_fwd", [p] * 6 + [n, i, n, n, f, i, i, p]),
             ("delta_add_rmsnorm_quant", [p] * 6 + [n, i, n, n, f, i, i, p]),
             ("delta_add_rmsnorm_bwd", [p] * 7 + [n, i, i, i, p]),
@@ -287,6 +292,90 @@ def delta_scan_bwd(x, gate, states, dout, dhT=None, *, form="sigmoid", lengths=N
     if st:
         _raise(st)
     return dx, dgate, dh0
+
+
+def _decay_begin(q, k, v, decay, dims, name):
+    """shared checks: types, sizes, pointers, and the strides of all axes but the last"""
+    code, dev = _begin(q, name, dims, "q")
+    if not isinstance(v, torch.Tensor) or v.dim() != dims:
+        raise ValueError(f"v must have {dims} axes")
+    _within_int("v", v.shape)
+    H, dk, dv = q.shape[-2], q.shape[-1], v.shape[-1]
+    pq = _tensor(q, "q", q.shape, q.dtype, dev, True)
+    pk = _tensor(k, "k", q.shape, q.dtype, dev, True)
+    pv = _tensor(v, "v", q.shape[:-1] + (dv,), q.dtype, dev, True)
+    pd = _tensor(decay, "decay", (H,), torch.float32, dev)
+    strides = [n for t in (q, k, v) for n in t.stride()[:-1]]
+    return code, dev, H, dk, dv, pq, pk, pv, pd, (ctypes.c_int64 * len(strides))(*strides)
+
+
+def delta_decay_fwd(q, k, v, decay, h0=None, *, scale=1.0, lengths=None, out=None, hT=None, stream=None):
+    """Linear attention with a decay for each head: ``S_t = decay_h S_{t-1} + k_t v_t^T``,
+    ``out_t = scale S_t^T q_t``.
+
+    q, k [B,T,H,dk] and v [B,T,H,dv] bfloat16 or float32 (contiguous last axis, dk and
+    dv up to 256), decay [H] float32 in [0, 1], h0 [B,H,dk,dv] float32 or None;
+    lengths [B] int32: later tokens do not count, leave the state alone and have
+    out = 0.  Returns ``(out [B,T,H,dv], hT [B,H,dk,dv] float32)``.  ``hT`` may be
+    ``h0`` to update the state in place.
+    """
+    if stream is None and out is None and hT is None:
+        r = (_fast or _open_fast()).decay_fwd(q, k, v, decay, h0, lengths, scale)
+        if r is not NotImplemented:
+            return _checked(r)
+    code, dev, H, dk, dv, pq, pk, pv, pd, strides = _decay_begin(q, k, v, decay, 4, "delta_decay_fwd")
+    B, T = q.shape[:2]
+    ph = _optional(h0, "h0", (B, H, dk, dv), torch.float32, dev)
+    pl = _optional(lengths, "lengths", (B,), torch.int32, dev)
+    out = _output(out, "out", (B, T, H, dv), q.dtype, dev, stream)
+    hT = _output(hT, "hT", (B, H, dk, dv), torch.float32, dev, stream)
+    st = _on(dev, _lib().delta_decay_fwd)(pq, pk, pv, pd, ph, pl, out.data_ptr(), hT.data_ptr(), B, T, H,
+        dk, dv, strides, scale, code, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return out, hT
+
+
+def delta_decay_step(q, k, v, decay, state, *, scale=1.0, out=None, stream=None):
+    """One token of the same: q, k [B,H,dk], v [B,H,dv] (strides above the last axis as
+    they are), state [B,H,dk,dv] float32 updated in place.  Returns out [B,H,dv]."""
+    if stream is None and out is None:
+        r = (_fast or _open_fast()).decay_step(q, k, v, decay, state, scale)
+        if r is not NotImplemented:
+            return _checked(r)
+    code, dev, H, dk, dv, pq, pk, pv, pd, strides = _decay_begin(q, k, v, decay, 3, "delta_decay_step")
+    B = q.shape[0]
+    ps = _tensor(state, "state", (B, H, dk, dv), torch.float32, dev)
+    out = _output(out, "out", (B, H, dv), q.dtype, dev, stream)
+    st = _on(dev, _lib().delta_decay_step)(pq, pk, pv, pd, ps, out.data_ptr(), B, H, dk, dv, strides, scale,
+        code, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return out
+
+
+def delta_decay_bwd(q, k, v, decay, dout, h0=None, dhT=None, *, scale=1.0, lengths=None, stream=None):
+    """Gradients of ``delta_decay_fwd``: its arguments, dout [B,T,H,dv] contiguous and
+    dhT [B,H,dk,dv] float32 or None.  Returns ``(dq, dk, dv, dh0)``, the first three in
+    q's type and contiguous, dh0 float32.  The decays are constants and have none."""
+    if stream is None:
+        r = (_fast or _open_fast()).decay_bwd(q, k, v, decay, dout, h0, dhT, lengths, scale)
+        if r is not NotImplemented:
+            return _checked(r)
+    code, dev, H, dk, dv, pq, pk, pv, pd, strides = _decay_begin(q, k, v, decay, 4, "delta_decay_bwd")
+    B, T = q.shape[:2]
+    po = _tensor(dout, "dout", (B, T, H, dv), q.dtype, dev)
+    ph = _optional(h0, "h0", (B, H, dk, dv), torch.float32, dev)
+    pt = _optional(dhT, "dhT", (B, H, dk, dv), torch.float32, dev)
+    pl = _optional(lengths, "lengths", (B,), torch.int32, dev)
+    gq, gk = (_empty((B, T, H, dk), q.dtype, dev, stream) for _ in range(2))
+    gv = _empty((B, T, H, dv), q.dtype, dev, stream)
+    dh0 = _empty((B, H, dk, dv), torch.float32, dev, stream)
+    st = _on(dev, _lib().delta_decay_bwd)(pq, pk, pv, pd, ph, pl, po, pt, gq.data_ptr(), gk.data_ptr(),
+        gv.data_ptr(), dh0.data_ptr(), B, T, H, dk, dv, strides, scale, code, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return gq, gk, gv, dh0
 
 
 def _rows(t, name, shape, dtype, dev):

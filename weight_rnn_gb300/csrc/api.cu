@@ -359,11 +359,12 @@ int delta_selftest_exchange(int polls, struct CUstream_st *stream) {
 }
 
 int delta_check_device(void) {
-  unsigned int word = 0, ut_word = 0, linear_word = 0, scan_word = 0;
+  unsigned int word = 0, ut_word = 0, linear_word = 0, scan_word = 0, decay_word = 0;
   cudaError_t err = delta::read_and_clear_tc_error(&word);
   if (err == cudaSuccess) err = delta::read_and_clear_ut_error(&ut_word);
   if (err == cudaSuccess) err = delta::read_and_clear_linear_error(&linear_word);
   if (err == cudaSuccess) err = delta::read_and_clear_scan_error(&scan_word);
+  if (err == cudaSuccess) err = delta::read_and_clear_decay_error(&decay_word);
   if (err != cudaSuccess) return cuda_fail(err, "device check");
   if (word != 0)
     return fail(DELTA_ERR_CUDA,
@@ -378,6 +379,9 @@ int delta_check_device(void) {
                 linear_word - 1);
   if (scan_word != 0)
     return fail(DELTA_ERR_CUDA, "a wait of a scan's cluster gave up: results of that call are invalid");
+  if (decay_word != 0)
+    return fail(DELTA_ERR_CUDA, "a wait of decay attention gave up (role %u): results of that call are invalid",
+                decay_word - 1);
   return DELTA_OK;
 }
 

@@ -146,6 +146,91 @@ PyObject *scan_bwd(PyObject *const *a, Py_ssize_t n) {
   return st == DELTA_OK ? tuple(wrap(dx), wrap(dg), wrap(dh0)) : PyLong_FromLong(st);
 }
 
+// q, k, v and decay of the decay calls; `axes` of them before the channels
+struct Decay {
+  const Tensor *q = nullptr, *k = nullptr, *v = nullptr, *decay = nullptr;
+  int dev = 0;
+  int64_t B = 0, T = 1, H = 0, dk = 0, dv = 0, strides[9];
+  at::ScalarType dt = at::kFloat;
+
+  bool take(PyObject *const *a, int axes) {
+    q = tensor(a[0]), k = tensor(a[1]), v = tensor(a[2]), decay = tensor(a[3]);
+    if (!q || !k || !v || !decay || q->dim() != axes + 1 || v->dim() != axes + 1 || code(q->scalar_type()) < 0)
+      return false;
+    dev = q->get_device();
+    dt = q->scalar_type();
+    B = q->size(0), H = q->size(axes - 1), dk = q->size(axes), dv = v->size(axes);
+    if (axes == 3) T = q->size(1);
+    c10::SmallVector<int64_t, 4> shape(q->sizes().begin(), q->sizes().end());
+    shape.back() = dv;
+    if (!here(dev) || !fits(B) || !fits(T) || !fits(H) || !fits(dk) || !fits(dv) || !rows(q, dt, q->sizes(), dev) ||
+        !rows(k, dt, q->sizes(), dev) || !rows(v, dt, shape, dev) || !whole(decay, at::kFloat, {H}, dev))
+      return false;
+    for (int i = 0; i < axes; ++i)
+      strides[i] = q->stride(i), strides[axes + i] = k->stride(i), strides[2 * axes + i] = v->stride(i);
+    return true;
+  }
+  const float *rates() const { return static_cast<const float *>(decay->data_ptr()); }
+};
+bool number(PyObject *o, float &x) {
+  if (!PyFloat_Check(o)) return false;
+  x = (float)PyFloat_AS_DOUBLE(o);
+  return true;
+}
+
+// q, k, v, decay, h0, lengths, scale
+PyObject *decay_fwd(PyObject *const *a, Py_ssize_t n) {
+  if (n != 7) return other();
+  Decay d;
+  const Tensor *h0 = nullptr, *len = nullptr;
+  float scale;
+  if (!d.take(a, 3) || !optional_whole(a[4], h0, at::kFloat, {d.B, d.H, d.dk, d.dv}, d.dev) ||
+      !optional_whole(a[5], len, at::kInt, {d.B}, d.dev) || !number(a[6], scale))
+    return other();
+  Tensor out = empty({d.B, d.T, d.H, d.dv}, d.dt, d.dev), hT = empty({d.B, d.H, d.dk, d.dv}, at::kFloat, d.dev);
+  const int st = delta_decay_fwd(ptr(d.q), ptr(d.k), ptr(d.v), d.rates(), static_cast<float *>(ptr(h0)),
+                                 static_cast<int *>(ptr(len)), out.data_ptr(), static_cast<float *>(hT.data_ptr()),
+                                 (int)d.B, (int)d.T, (int)d.H, (int)d.dk, (int)d.dv, d.strides, scale,
+                                 (delta_dtype)code(d.dt), stream(d.dev));
+  return st == DELTA_OK ? tuple(wrap(out), wrap(hT)) : PyLong_FromLong(st);
+}
+
+// q, k, v, decay, state, scale
+PyObject *decay_step(PyObject *const *a, Py_ssize_t n) {
+  if (n != 6) return other();
+  Decay d;
+  float scale;
+  if (!d.take(a, 2)) return other();
+  const Tensor *s = tensor(a[4]);
+  if (!whole(s, at::kFloat, {d.B, d.H, d.dk, d.dv}, d.dev) || !number(a[5], scale)) return other();
+  Tensor out = empty({d.B, d.H, d.dv}, d.dt, d.dev);
+  const int st = delta_decay_step(ptr(d.q), ptr(d.k), ptr(d.v), d.rates(), static_cast<float *>(ptr(s)), out.data_ptr(),
+                                  (int)d.B, (int)d.H, (int)d.dk, (int)d.dv, d.strides, scale, (delta_dtype)code(d.dt),
+                                  stream(d.dev));
+  return st == DELTA_OK ? wrap(out) : PyLong_FromLong(st);
+}
+
+// q, k, v, decay, dout, h0, dhT, lengths, scale
+PyObject *decay_bwd(PyObject *const *a, Py_ssize_t n) {
+  if (n != 9) return other();
+  Decay d;
+  const Tensor *g = tensor(a[4]), *h0 = nullptr, *dhT = nullptr, *len = nullptr;
+  float scale;
+  if (!d.take(a, 3) || !whole(g, d.dt, {d.B, d.T, d.H, d.dv}, d.dev) ||
+      !optional_whole(a[5], h0, at::kFloat, {d.B, d.H, d.dk, d.dv}, d.dev) ||
+      !optional_whole(a[6], dhT, at::kFloat, {d.B, d.H, d.dk, d.dv}, d.dev) ||
+      !optional_whole(a[7], len, at::kInt, {d.B}, d.dev) || !number(a[8], scale))
+    return other();
+  Tensor dq = empty(d.q->sizes(), d.dt, d.dev), dk = empty(d.q->sizes(), d.dt, d.dev),
+         dv = empty({d.B, d.T, d.H, d.dv}, d.dt, d.dev), dh0 = empty({d.B, d.H, d.dk, d.dv}, at::kFloat, d.dev);
+  const int st = delta_decay_bwd(ptr(d.q), ptr(d.k), ptr(d.v), d.rates(), static_cast<float *>(ptr(h0)),
+                                 static_cast<int *>(ptr(len)), ptr(g), static_cast<float *>(ptr(dhT)), dq.data_ptr(),
+                                 dk.data_ptr(), dv.data_ptr(), static_cast<float *>(dh0.data_ptr()), (int)d.B,
+                                 (int)d.T, (int)d.H, (int)d.dk, (int)d.dv, d.strides, scale, (delta_dtype)code(d.dt),
+                                 stream(d.dev));
+  return st == DELTA_OK ? tuple(wrap(dq), wrap(dk), wrap(dv), wrap(dh0)) : PyLong_FromLong(st);
+}
+
 // [..., D] as rows: contiguous, or two axes with contiguous rows
 bool as_rows(const Tensor *t, at::ScalarType dt, at::IntArrayRef shape, int dev, int64_t &ld) {
   if (!t || shape.empty() || t->scalar_type() != dt || t->get_device() != dev || t->sizes() != shape) return false;
@@ -304,7 +389,8 @@ PyObject *linear_bwd(PyObject *const *a, Py_ssize_t n) {
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))guarded<name>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(scan_fwd),   FAST(scan_step),    FAST(scan_bwd),   FAST(norm_fwd), FAST(norm_bwd),
-                         FAST(linear_fwd), FAST(linear_quant), FAST(linear_bwd), {nullptr, nullptr, 0, nullptr}};
+                         FAST(linear_fwd), FAST(linear_quant), FAST(linear_bwd), FAST(decay_fwd), FAST(decay_step), FAST(decay_bwd),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", "block operators, the common case", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

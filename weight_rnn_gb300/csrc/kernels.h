@@ -146,6 +146,65 @@ cudaError_t read_and_clear_scan_error(unsigned int *word);
 // hT <- h0 (or 0): a sequence without steps
 cudaError_t launch_scan_passthrough(const float *h0, float *hT, int64_t n, cudaStream_t s);
 
+// Linear attention with a decay for each head (decay.cu, decay_tc.cu).  One pass
+// over the time axis takes roles q, k, v:
+//
+//   forward: S_t = g S_{t-1} + kvs k_t v_t^T,  out_t = os S_t^T q_t,  final = S_T
+//   reverse: R_t = g R_{t+1} + kvs k_t v_t^T  (g left out before the first step, on
+//            init itself),  out_t = os R_t^T q_t,  final = g R_0
+//
+// Every gradient is such a pass with the roles exchanged.  Strides are in
+// elements, of the batch row, the token and the head.
+struct DecayPass {
+  const void *q, *k, *v;
+  int64_t qs[3], ks[3], vs[3];
+  void *out;           // [B][T][H][dv] contiguous
+  const float *init;   // [B][H][dk][dv], or [dv][dk] with init_t; nullptr: 0
+  float *final;        // [B][H][dk][dv] or nullptr
+  float os, kvs;
+  int dk, dv;
+  bool reverse, init_t;
+};
+// The time axis may be cut into `nseg` segments of `seg` tokens, each a CTA's
+// work; init then holds a state for every segment, [B][H][nseg].
+struct DecayArgs {
+  DecayPass pass[3];
+  int passes;
+  const float *decay;   // [H]
+  const int *lengths;   // [B], clamped to [0, T]; nullptr: T
+  int64_t B, T, H, seg;
+  int nseg;
+  bool bf16;
+};
+constexpr int kDecayMaxD = 256;
+constexpr int kDecayChunk = 128;  // segments are multiples of it
+// Segments' own last states (as from init = 0) into final [B][H][nseg][dk][dv];
+// q, out and init are not looked at.
+cudaError_t launch_decay_states(const DecayArgs &a, cudaStream_t s);
+cudaError_t launch_decay(const DecayArgs &a, cudaStream_t s);
+// The same two on the tensor cores: bfloat16, what decay_tc_fits() allows.
+bool decay_tc_fits(const DecayArgs &a);
+cudaError_t launch_decay_tc(const DecayArgs &a, bool states, cudaStream_t s);
+cudaError_t read_and_clear_decay_error(unsigned int *word);
+// states [B][H][nseg][n]: every segment's own last state becomes the state that
+// it begins with, given the row's (init, or 0).  pass: where the time begins.
+cudaError_t launch_decay_join(float *states, const float *init, const DecayArgs &a, bool reverse, int64_t n,
+                              cudaStream_t s);
+// One token: state [B][H][dk][dv] in place, out [B][H][dv]; strides of the batch
+// row and the head.
+struct DecayStepArgs {
+  const void *q, *k, *v;
+  int64_t qs[2], ks[2], vs[2];
+  const float *decay;
+  float *state;
+  void *out;
+  int64_t B, H;
+  int dk, dv;
+  float scale;
+  bool bf16;
+};
+cudaError_t launch_decay_step(const DecayStepArgs &a, cudaStream_t s);
+
 // Residual addition and RMS norm (norm.cu), rows of D elements.  Row strides
 // ld* in elements; weight is float32 or, with w_bf16, bfloat16.
 struct NormArgs {
