@@ -632,6 +632,40 @@ int delta_add_rmsnorm_bwd(const void *dy, const void *sum, const void *weight, c
                           const void *dsum, void *dx, float *dweight, int64_t rows, int D,
                           delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream);
 
+/*
+ * delta_add_layernorm_fwd -- the residual addition and layer norm,
+ *
+ *   t = x + residual,  mean = mean_d t_d,  rstd = (mean_d (t_d - mean)^2 + eps)^(-1/2),
+ *   y = (t - mean) * rstd * weight + bias.
+ *
+ *   x, residual, weight, y, sum_out, rstd   as in delta_add_rmsnorm_fwd
+ *   bias        [D]       bdtype, or NULL (=> 0)
+ *   mean        [rows]    float32 or NULL
+ *
+ * The norm is of the unrounded t, the variance that of the differences.  D <= 8192,
+ * eps > 0.  With D = 0 nothing is written.
+ */
+int delta_add_layernorm_fwd(const void *x, const void *residual, const void *weight, const void *bias, void *y,
+                            void *sum_out, float *mean, float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr,
+                            float eps, delta_dtype dtype, delta_dtype wdtype, delta_dtype bdtype,
+                            struct CUstream_st *stream);
+
+/*
+ * delta_add_layernorm_bwd -- its gradients: with t^ = (sum - mean) * rstd,
+ *
+ *   dx = rstd (w dy - mean_d(w dy) - t^ mean_d(w dy t^)) + dsum,
+ *   dweight = sum over rows of dy t^,   dbias = sum over rows of dy.
+ *
+ *   dy, sum, dsum, rstd, dx, dweight   as in delta_add_rmsnorm_bwd
+ *   mean        [rows]    float32, from the forward
+ *   dbias       [D]       float32
+ *
+ * Takes two float32 rows of D per resident CTA from the library's pool.
+ */
+int delta_add_layernorm_bwd(const void *dy, const void *sum, const void *weight, const float *mean, const float *rstd,
+                            const void *dsum, void *dx, float *dweight, float *dbias, int64_t rows, int D,
+                            delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream);
+
 typedef enum {
     DELTA_ACT_NONE = 0,
     DELTA_ACT_SILU = 1, /* p s(p), s the logistic function */

@@ -17,8 +17,8 @@ import threading
 import torch
 
 from . import block
-from .block import (delta_add_rmsnorm_bwd, delta_add_rmsnorm_fwd, delta_add_rmsnorm_quant,
-                    delta_decay_bwd, delta_decay_fwd, delta_decay_step, delta_linear_bwd,
+from .block import (delta_add_layernorm_bwd, delta_add_layernorm_fwd, delta_add_rmsnorm_bwd,
+                    delta_add_rmsnorm_fwd, delta_add_rmsnorm_quant, delta_decay_bwd, delta_decay_fwd, delta_decay_step, delta_linear_bwd,
                     delta_linear_fwd, delta_linear_quant, delta_scan_bwd, delta_scan_fwd,
                     delta_scan_step)
 

@@ -1,7 +1,7 @@
 """Operators around the token mixers in a block: the gated linear recurrence
 (``delta_scan_*``), linear attention with a decay for each head
 (``delta_decay_*``), the residual addition with RMS norm
-(``delta_add_rmsnorm_*``) and the linear layer with its epilogue
+(``delta_add_rmsnorm_*``) or layer norm (``delta_add_layernorm_*``) and the linear layer with its epilogue
 (``delta_linear_*``).
 
 Bindings over the C ABI of ``libdelta.so`` with the ABI's names: argument
@@ -34,7 +34,8 @@ E4M3 = torch.float8_e4m3fn
 
 SYMBOLS = ("delta_scan_fwd", "delta_scan_step", "delta_scan_bwd", "delta_decay_fwd",
            "delta_decay_step", "delta_decay_bwd", "delta_add_rmsnorm_fwd",
-           "delta_add_rmsnorm_quant", "delta_add_rmsnorm_bwd", "delta_linear_fwd",
+           "delta_add_rmsnorm_quant", "delta_add_rmsnorm_bwd", "delta_add_layernorm_fwd",
+           "delta_add_layernorm_bwd", "delta_linear_fwd",
            "delta_linear_quant", "delta_linear_bwd")
 
 
@@ -51,6 +52,8 @@ def declare(lib) -> None:
             ("delta_add_rmsnorm_fwd", [p] * 6 + [n, i, n, n, f, i, i, p]),
             ("delta_add_rmsnorm_quant", [p] * 6 + [n, i, n, n, f, i, i, p]),
             ("delta_add_rmsnorm_bwd", [p] * 7 + [n, i, i, i, p]),
+            ("delta_add_layernorm_fwd", [p] * 8 + [n, i, n, n, f, i, i, i, p]),
+            ("delta_add_layernorm_bwd", [p] * 9 + [n, i, i, i, p]),
             ("delta_linear_fwd", [p] * 6 + [i] * 3 + [n] * 3 + [i] * 3 + [p]),
             ("delta_linear_quant", [p] * 7 + [i] * 3 + [n] * 3 + [i] * 2 + [p]),
             ("delta_linear_bwd", [p] * 7 + [i] * 3 + [n] * 2 + [i] * 2 + [p])):
@@ -502,6 +505,65 @@ def delta_add_rmsnorm_bwd(dy, sum, weight, rstd, dsum=None, *, dx=None, stream=N
     if st:
         _raise(st)
     return dx, dweight
+
+
+def delta_add_layernorm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, sum_out=None, stream=None):
+    """``t = x + residual``, ``y = (t - mean) * rsqrt(var + eps) * weight + bias`` over the
+    last axis (at most 8192 wide), mean and var those of the row.
+
+    x, residual [..., D] bfloat16 or float32 (rows may be strided), weight and bias
+    [D] float32 or bfloat16.  Returns ``(y, sum, mean, rstd)``: y in x's type, sum = t
+    rounded to it (x itself without a residual), mean and rstd [...] float32.
+    ``sum_out`` may be ``x`` or ``residual`` to update the stream in place.
+    """
+    if stream is None and sum_out is None:
+        r = (_fast or _open_fast()).layernorm_fwd(x, weight, bias, residual, eps)
+        if r is not NotImplemented:
+            return _checked(r)
+    code, dev, D, rows, px, ldx, pr, ldr, pw, wcode = _norm_begin(x, weight, residual,
+                                                                 "delta_add_layernorm_fwd")
+    pb, bcode = (None, 0) if bias is None else _weight(bias, D, x.dtype, dev, "bias")
+    y = _empty(x.shape, x.dtype, dev, stream)
+    mean = _per_row(x.shape[:-1], 0.0, D, dev, stream)
+    rstd = _per_row(x.shape[:-1], eps ** -0.5 if eps > 0 else 0.0, D, dev, stream)
+    if residual is not None:
+        sum_out = _output(sum_out, "sum_out", x.shape, x.dtype, dev, stream)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual: without one the sum is x")
+    st = _on(dev, _lib().delta_add_layernorm_fwd)(px, pr, pw, pb, y.data_ptr(),
+        None if sum_out is None else sum_out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows, D, ldx,
+        ldr, eps, code, wcode, bcode, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return y, (x if sum_out is None else sum_out), mean, rstd
+
+
+def delta_add_layernorm_bwd(dy, sum, weight, mean, rstd, dsum=None, *, dx=None, stream=None):
+    """Gradients of ``delta_add_layernorm_fwd``: dy and the forward's sum [..., D]
+    (contiguous, one type), mean and rstd, and dsum, the gradient that arrives at sum,
+    or None.  Returns ``(dx, dweight, dbias)``: dx (of x and of residual alike) in
+    dy's type, dweight and dbias [D] float32.  ``dx`` may be ``dy`` or ``dsum``."""
+    if stream is None and dx is None:
+        r = (_fast or _open_fast()).layernorm_bwd(dy, sum, weight, mean, rstd, dsum)
+        if r is not NotImplemented:
+            return _checked(r)
+    code, dev = _begin(dy, "delta_add_layernorm_bwd", 0, "dy")
+    if dy.dim() < 1:
+        raise ValueError("dy must have at least one axis")
+    D = dy.shape[-1]
+    py = _tensor(dy, "dy", dy.shape, dy.dtype, dev)
+    ps = _tensor(sum, "sum", dy.shape, dy.dtype, dev)
+    pd = _optional(dsum, "dsum", dy.shape, dy.dtype, dev)
+    pm = _tensor(mean, "mean", dy.shape[:-1], torch.float32, dev)
+    pr = _tensor(rstd, "rstd", dy.shape[:-1], torch.float32, dev)
+    pw, wcode = _weight(weight, D, dy.dtype, dev)
+    dx = _output(dx, "dx", dy.shape, dy.dtype, dev, stream)
+    dweight, dbias = (_empty((D,), torch.float32, dev, stream) for _ in range(2))
+    st = _on(dev, _lib().delta_add_layernorm_bwd)(py, ps, pw, pm, pr, pd, dx.data_ptr(), dweight.data_ptr(),
+        dbias.data_ptr(), dy.numel() // D if D else 0, D, code, wcode, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return dx, dweight, dbias
 
 
 def _linear_begin(x, w, bias, residual, act, dtype, odt, dev):

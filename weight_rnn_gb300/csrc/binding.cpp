@@ -291,6 +291,59 @@ PyObject *norm_bwd(PyObject *const *a, Py_ssize_t n) {
   return st == DELTA_OK ? tuple(wrap(dx), wrap(dw)) : PyLong_FromLong(st);
 }
 
+// x, weight, bias, residual, eps: (y, sum, mean, rstd)
+PyObject *layernorm_fwd(PyObject *const *a, Py_ssize_t n) {
+  if (n != 5) return other();
+  const Tensor *x = tensor(a[0]), *w = tensor(a[1]), *b = a[2] == Py_None ? nullptr : tensor(a[2]),
+               *r = a[3] == Py_None ? nullptr : tensor(a[3]);
+  float eps;
+  if (!x || x->dim() < 1 || code(x->scalar_type()) < 0 || !w || code(w->scalar_type()) < 0 ||
+      (a[2] != Py_None && (!b || code(b->scalar_type()) < 0)) || !number(a[4], eps))
+    return other();
+  const int dev = x->get_device();
+  const auto dt = x->scalar_type();
+  const auto shape = x->sizes();
+  const int64_t D = shape.back();
+  int64_t ldx = 0, ldr = D;
+  if (!here(dev) || !fits(D) || D == 0 || !as_rows(x, dt, shape, dev, ldx) || !whole(w, w->scalar_type(), {D}, dev) ||
+      (b && !whole(b, b->scalar_type(), {D}, dev)) || (a[3] != Py_None && !as_rows(r, dt, shape, dev, ldr)))
+    return other();
+  const auto lead = shape.slice(0, shape.size() - 1);
+  Tensor y = empty(shape, dt, dev), mean = empty(lead, at::kFloat, dev), rstd = empty(lead, at::kFloat, dev), sum;
+  if (r) sum = empty(shape, dt, dev);
+  const int st = delta_add_layernorm_fwd(ptr(x), ptr(r), ptr(w), ptr(b), y.data_ptr(), r ? sum.data_ptr() : nullptr,
+                                         static_cast<float *>(mean.data_ptr()), static_cast<float *>(rstd.data_ptr()),
+                                         x->numel() / D, (int)D, ldx, ldr, eps, (delta_dtype)code(dt),
+                                         (delta_dtype)code(w->scalar_type()),
+                                         b ? (delta_dtype)code(b->scalar_type()) : DELTA_F32, stream(dev));
+  if (st != DELTA_OK) return PyLong_FromLong(st);
+  return tuple(wrap(y), r ? wrap(sum) : Py_NewRef(a[0]), wrap(mean), wrap(rstd));
+}
+
+// dy, sum, weight, mean, rstd, dsum
+PyObject *layernorm_bwd(PyObject *const *a, Py_ssize_t n) {
+  if (n != 6) return other();
+  const Tensor *dy = tensor(a[0]), *sum = tensor(a[1]), *w = tensor(a[2]), *m = tensor(a[3]), *r = tensor(a[4]),
+               *ds = nullptr;
+  if (!dy || dy->dim() < 1 || code(dy->scalar_type()) < 0 || !w || code(w->scalar_type()) < 0) return other();
+  const int dev = dy->get_device();
+  const auto dt = dy->scalar_type();
+  const auto shape = dy->sizes();
+  const int64_t D = shape.back();
+  const auto lead = shape.slice(0, shape.size() - 1);
+  if (!here(dev) || !fits(D) || !whole(dy, dt, shape, dev) || !whole(sum, dt, shape, dev) ||
+      !whole(w, w->scalar_type(), {D}, dev) || !whole(m, at::kFloat, lead, dev) || !whole(r, at::kFloat, lead, dev) ||
+      !optional_whole(a[5], ds, dt, shape, dev))
+    return other();
+  Tensor dx = empty(shape, dt, dev), dw = empty({D}, at::kFloat, dev), db = empty({D}, at::kFloat, dev);
+  const int st = delta_add_layernorm_bwd(ptr(dy), ptr(sum), ptr(w), static_cast<float *>(ptr(m)),
+                                         static_cast<float *>(ptr(r)), ptr(ds), dx.data_ptr(),
+                                         static_cast<float *>(dw.data_ptr()), static_cast<float *>(db.data_ptr()),
+                                         D > 0 ? dy->numel() / D : 0, (int)D, (delta_dtype)code(dt),
+                                         (delta_dtype)code(w->scalar_type()), stream(dev));
+  return st == DELTA_OK ? tuple(wrap(dx), wrap(dw), wrap(db)) : PyLong_FromLong(st);
+}
+
 // The operands that the linear calls share.
 struct Linear {
   const Tensor *x = nullptr, *w = nullptr, *bias = nullptr, *res = nullptr;
@@ -390,7 +443,7 @@ PyObject *linear_bwd(PyObject *const *a, Py_ssize_t n) {
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))guarded<name>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(scan_fwd),   FAST(scan_step),    FAST(scan_bwd),   FAST(norm_fwd), FAST(norm_bwd),
                          FAST(linear_fwd), FAST(linear_quant), FAST(linear_bwd), FAST(decay_fwd), FAST(decay_step), FAST(decay_bwd),
-                         {nullptr, nullptr, 0, nullptr}};
+                         FAST(layernorm_fwd), FAST(layernorm_bwd), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", "block operators, the common case", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

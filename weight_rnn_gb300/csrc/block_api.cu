@@ -76,19 +76,23 @@ int norm_sizes(int64_t rows, int D, int64_t ldx, int64_t ldr, float eps, delta_d
   return DELTA_OK;
 }
 
-int run_norm_fwd(const void *x, const void *residual, const void *weight, void *y, float *scale,
-                 void *sum_out, float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
-                 delta_dtype dtype, delta_dtype wdtype, bool quant, struct CUstream_st *stream) {
+enum class Norm { kRms, kRmsQuant, kLayer };
+
+int run_norm_fwd(Norm kind, const void *x, const void *residual, const void *weight, const void *bias, void *y,
+                 float *scale, void *sum_out, float *mean, float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr,
+                 float eps, delta_dtype dtype, delta_dtype wdtype, delta_dtype bdtype, struct CUstream_st *stream) {
+  const bool quant = kind == Norm::kRmsQuant;
   int st;
   if ((st = norm_sizes(rows, D, ldx, residual ? ldr : D, eps, dtype, wdtype)) != DELTA_OK) return st;
+  if ((st = check_dtype(bdtype)) != DELTA_OK) return st;
   if (rows == 0 || D == 0) return DELTA_OK;
   if (!x || !weight || !y || (quant && !scale))
     return fail(DELTA_ERR_INVALID, "x, weight, the output and its scales must be non-NULL");
   if (sum_out && !residual) return fail(DELTA_ERR_INVALID, "sum_out without a residual: the sum is x");
   const int64_t e = esize(dtype), we = esize(wdtype);
-  if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned_to(weight, we))
-    return fail(DELTA_ERR_ALIGN, "x, residual and weight must be aligned to their elements");
-  if (!aligned16(y) || !aligned16(sum_out) || !aligned16(rstd) || !aligned16(scale))
+  if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned_to(weight, we) || !aligned_to(bias, esize(bdtype)))
+    return fail(DELTA_ERR_ALIGN, "x, residual and the weights must be aligned to their elements");
+  if (!aligned16(y) || !aligned16(sum_out) || !aligned16(mean) || !aligned16(rstd) || !aligned16(scale))
     return fail(DELTA_ERR_ALIGN, "every output must be 16-byte aligned");
   const Span xs = {"x", range(x, ((rows - 1) * ldx + D) * e)};
   const Span rs = {"residual", range(residual, ((rows - 1) * ldr + D) * e)};
@@ -96,8 +100,9 @@ int run_norm_fwd(const void *x, const void *residual, const void *weight, void *
   const Span ys = {"y", range(y, rows * D * (quant ? 1 : e))};
   const Span ss = {"sum_out", range(sum_out, rows * D * e)};
   const Span ds = {"rstd", range(rstd, rows * 4)}, cs = {"y_scale", range(scale, rows * 4)};
-  if ((st = check_overlap({ys, ds, cs}, {xs, rs, ws})) != DELTA_OK) return st;
-  if ((st = check_overlap({ss}, {ws, ys, ds, cs})) != DELTA_OK) return st;
+  const Span bs = {"bias", range(bias, D * esize(bdtype))}, ms = {"mean", range(mean, rows * 4)};
+  if ((st = check_overlap({ys, ds, cs, ms}, {xs, rs, ws, bs})) != DELTA_OK) return st;
+  if ((st = check_overlap({ss}, {ws, bs, ys, ds, cs, ms})) != DELTA_OK) return st;
   // the residual stream may be updated in place: the same rows, or none
   const struct {
     Span span;
@@ -112,10 +117,55 @@ int run_norm_fwd(const void *x, const void *residual, const void *weight, void *
   delta::NormArgs a{};
   a.x = x; a.residual = residual; a.weight = weight; a.y = y; a.sum = sum_out; a.rstd = rstd;
   a.scale = quant ? scale : nullptr;
+  a.bias = bias; a.b_bf16 = bdtype == DELTA_BF16; a.mean = mean;
   a.rows = rows; a.D = D; a.ldx = rows > 1 ? ldx : 0; a.ldr = rows > 1 ? ldr : 0;
   a.eps = eps; a.bf16 = dtype == DELTA_BF16; a.w_bf16 = wdtype == DELTA_BF16;
-  const cudaError_t err = delta::launch_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = kind == Norm::kLayer ? delta::launch_layernorm_fwd(a, s) : delta::launch_norm_fwd(a, s);
   return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "norm kernel launch");
+}
+
+int run_norm_bwd(Norm kind, const void *dy, const void *sum, const void *weight, const float *mean, const float *rstd,
+                 const void *dsum, void *dx, float *dweight, float *dbias, int64_t rows, int D, delta_dtype dtype,
+                 delta_dtype wdtype, struct CUstream_st *stream) {
+  const bool layer = kind == Norm::kLayer;
+  int st;
+  if ((st = norm_sizes(rows, D, D, D, 1.f, dtype, wdtype)) != DELTA_OK) return st;
+  if (D == 0) return DELTA_OK;
+  if (!dweight || !weight || (layer && !dbias))
+    return fail(DELTA_ERR_INVALID, "weight and the gradients must be non-NULL");
+  if (rows > 0 && (!dy || !sum || !rstd || !dx || (layer && !mean)))
+    return fail(DELTA_ERR_INVALID, "dy, sum, the rows' statistics and dx must be non-NULL");
+  const int64_t e = esize(dtype), we = esize(wdtype);
+  if (!aligned16(dy) || !aligned16(sum) || !aligned16(dsum) || !aligned16(dx) || !aligned16(mean) || !aligned16(rstd) ||
+      !aligned16(dweight) || !aligned16(dbias) || !aligned_to(weight, we))
+    return fail(DELTA_ERR_ALIGN, "every pointer must be 16-byte aligned (weight: to its elements)");
+  const Span ys = {"dy", range(dy, rows * D * e)}, ss = {"sum", range(sum, rows * D * e)};
+  const Span gs = {"dsum", range(dsum, rows * D * e)}, ws = {"weight", range(weight, D * we)};
+  const Span rs = {"rstd", range(rstd, rows * 4)}, ms = {"mean", range(mean, rows * 4)};
+  const Span xs = {"dx", range(dx, rows * D * e)}, dws = {"dweight", range(dweight, (int64_t)D * 4)};
+  const Span dbs = {"dbias", range(dbias, (int64_t)D * 4)};
+  if ((st = check_overlap({xs, dws, dbs}, {ss, ws, rs, ms})) != DELTA_OK) return st;
+  if ((st = check_overlap({dws, dbs}, {ys, gs})) != DELTA_OK) return st;
+  for (const Span &in : {ys, gs})  // dx may take dy's or dsum's place
+    if (overlap(xs.r, in.r) && xs.r.lo != in.r.lo)
+      return fail(DELTA_ERR_INVALID, "dx partly overlaps %s", in.name);
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  delta::NormBwdArgs a{};
+  a.dy = dy; a.sum = sum; a.weight = weight; a.mean = mean; a.rstd = rstd; a.dsum = dsum; a.dx = dx;
+  a.dweight = dweight; a.dbias = dbias;
+  a.rows = rows; a.D = D; a.bf16 = dtype == DELTA_BF16; a.w_bf16 = wdtype == DELTA_BF16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t n = layer ? delta::layernorm_bwd_ctas(a) * 2 * D : delta::norm_bwd_ctas(a) * D;
+  Scratch scr(s);
+  scr.want(n * 4);
+  cudaError_t err = scr.take();
+  if (err != cudaSuccess) return cuda_fail(err, "scratch allocation");
+  a.partial = static_cast<float *>(scr.cut(n * 4));
+  err = layer ? delta::launch_layernorm_bwd(a, s) : delta::launch_norm_bwd(a, s);
+  const cudaError_t ef = scr.release();
+  if (err != cudaSuccess) return cuda_fail(err, "norm backward launch");
+  return ef == cudaSuccess ? DELTA_OK : cuda_fail(ef, "scratch release");
 }
 
 int linear_sizes(int M, int N, int K, int64_t ldx, int64_t ldw, int64_t ldr, delta_act act) {
@@ -380,58 +430,37 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
 int delta_add_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *y, void *sum_out,
                           float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
                           delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream) {
-  return run_norm_fwd(x, residual, weight, y, nullptr, sum_out, rstd, rows, D, ldx, ldr, eps, dtype,
-                      wdtype, false, stream);
+  return run_norm_fwd(Norm::kRms, x, residual, weight, nullptr, y, nullptr, sum_out, nullptr, rstd, rows, D, ldx, ldr,
+                      eps, dtype, wdtype, wdtype, stream);
 }
 
 int delta_add_rmsnorm_quant(const void *x, const void *residual, const void *weight, void *y, float *y_scale,
                             void *sum_out, int64_t rows, int D, int64_t ldx, int64_t ldr, float eps,
                             delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream) {
-  return run_norm_fwd(x, residual, weight, y, y_scale, sum_out, nullptr, rows, D, ldx, ldr, eps, dtype,
-                      wdtype, true, stream);
+  return run_norm_fwd(Norm::kRmsQuant, x, residual, weight, nullptr, y, y_scale, sum_out, nullptr, nullptr, rows, D, ldx,
+                      ldr, eps, dtype, wdtype, wdtype, stream);
+}
+
+int delta_add_layernorm_fwd(const void *x, const void *residual, const void *weight, const void *bias, void *y,
+                            void *sum_out, float *mean, float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr,
+                            float eps, delta_dtype dtype, delta_dtype wdtype, delta_dtype bdtype,
+                            struct CUstream_st *stream) {
+  return run_norm_fwd(Norm::kLayer, x, residual, weight, bias, y, nullptr, sum_out, mean, rstd, rows, D, ldx, ldr, eps,
+                      dtype, wdtype, bdtype, stream);
 }
 
 int delta_add_rmsnorm_bwd(const void *dy, const void *sum, const void *weight, const float *rstd,
                           const void *dsum, void *dx, float *dweight, int64_t rows, int D,
                           delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream) {
-  int st;
-  if ((st = norm_sizes(rows, D, D, D, 1.f, dtype, wdtype)) != DELTA_OK) return st;
-  if (D == 0) return DELTA_OK;
-  if (!dweight || !weight) return fail(DELTA_ERR_INVALID, "weight and dweight must be non-NULL");
-  if (rows > 0 && (!dy || !sum || !rstd || !dx))
-    return fail(DELTA_ERR_INVALID, "dy, sum, rstd and dx must be non-NULL");
-  const int64_t e = esize(dtype), we = esize(wdtype);
-  if (!aligned16(dy) || !aligned16(sum) || !aligned16(dsum) || !aligned16(dx) || !aligned16(rstd) ||
-      !aligned16(dweight) || !aligned_to(weight, we))
-    return fail(DELTA_ERR_ALIGN, "every pointer must be 16-byte aligned (weight: to its elements)");
-  const Span ys = {"dy", range(dy, rows * D * e)}, ss = {"sum", range(sum, rows * D * e)};
-  const Span gs = {"dsum", range(dsum, rows * D * e)}, ws = {"weight", range(weight, D * we)};
-  const Span rs = {"rstd", range(rstd, rows * 4)};
-  const Span xs = {"dx", range(dx, rows * D * e)}, dws = {"dweight", range(dweight, (int64_t)D * 4)};
-  if ((st = check_overlap({xs, dws}, {ss, ws, rs})) != DELTA_OK) return st;
-  if ((st = check_overlap({dws}, {ys, gs})) != DELTA_OK) return st;
-  for (const Span &in : {ys, gs})  // dx may take dy's or dsum's place
-    if (overlap(xs.r, in.r) && xs.r.lo != in.r.lo)
-      return fail(DELTA_ERR_INVALID, "dx partly overlaps %s", in.name);
-  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
-  delta::NormBwdArgs a{};
-  a.dy = dy; a.sum = sum; a.weight = weight; a.rstd = rstd; a.dsum = dsum; a.dx = dx; a.dweight = dweight;
-  a.rows = rows; a.D = D; a.bf16 = dtype == DELTA_BF16; a.w_bf16 = wdtype == DELTA_BF16;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t err;
-  const int64_t n = delta::norm_bwd_ctas(a) * D;
-  void *scr = nullptr;
-  if (n > 0) {
-    cudaMemPool_t pool;
-    if ((err = scratch_pool(&pool)) != cudaSuccess) return cuda_fail(err, "scratch pool");
-    if ((err = cudaMallocFromPoolAsync(&scr, (size_t)n * 4, pool, s)) != cudaSuccess)
-      return cuda_fail(err, "scratch allocation");
-  }
-  a.partial = static_cast<float *>(scr);
-  err = delta::launch_norm_bwd(a, s);
-  const cudaError_t ef = scr ? cudaFreeAsync(scr, s) : cudaSuccess;
-  if (err != cudaSuccess) return cuda_fail(err, "norm backward launch");
-  return ef == cudaSuccess ? DELTA_OK : cuda_fail(ef, "scratch release");
+  return run_norm_bwd(Norm::kRms, dy, sum, weight, nullptr, rstd, dsum, dx, dweight, nullptr, rows, D, dtype, wdtype,
+                      stream);
+}
+
+int delta_add_layernorm_bwd(const void *dy, const void *sum, const void *weight, const float *mean, const float *rstd,
+                            const void *dsum, void *dx, float *dweight, float *dbias, int64_t rows, int D,
+                            delta_dtype dtype, delta_dtype wdtype, struct CUstream_st *stream) {
+  return run_norm_bwd(Norm::kLayer, dy, sum, weight, mean, rstd, dsum, dx, dweight, dbias, rows, D, dtype, wdtype,
+                      stream);
 }
 
 int delta_linear_fwd(const void *x, const void *w, const void *bias, const void *residual, void *out, void *pre,

@@ -209,19 +209,19 @@ cudaError_t launch_decay_step(const DecayStepArgs &a, cudaStream_t s);
 // ld* in elements; weight is float32 or, with w_bf16, bfloat16.
 struct NormArgs {
   const void *x, *residual;  // residual nullptr: the sum is x and is not written
-  const void *weight;
+  const void *weight, *bias; // bias: layer norm alone; nullptr for none
   void *y;                   // input type, or e4m3 with scale set
   void *sum;                 // [rows][D] contiguous
-  float *rstd, *scale;       // [rows]; nullptr: not written
+  float *rstd, *scale, *mean;  // [rows]; nullptr: not written; mean: layer norm alone
   int64_t rows, D, ldx, ldr;
   float eps;
-  bool bf16, w_bf16;
+  bool bf16, w_bf16, b_bf16;
 };
 struct NormBwdArgs {
   const void *dy, *sum, *weight, *dsum;  // dsum nullptr: 0
-  const float *rstd;
+  const float *rstd, *mean;  // mean, dbias: layer norm alone
   void *dx;
-  float *dweight, *partial;  // partial [norm_bwd_ctas()][D]
+  float *dweight, *dbias, *partial;  // partial [norm_bwd_ctas()][D], [layernorm_bwd_ctas()][2][D]
   int64_t rows, D;
   bool bf16, w_bf16;
 };
@@ -229,6 +229,10 @@ constexpr int kNormMaxD = 8192;
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s);
 int64_t norm_bwd_ctas(const NormBwdArgs &a);
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t s);
+// The same with layer norm (layernorm.cu).
+cudaError_t launch_layernorm_fwd(const NormArgs &a, cudaStream_t s);
+int64_t layernorm_bwd_ctas(const NormBwdArgs &a);
+cudaError_t launch_layernorm_bwd(const NormBwdArgs &a, cudaStream_t s);
 
 // The linear layer (linear.cu, linear_tc.cu): out = act(x w^T + bias) +
 // residual, x [M][K], w [N][K], out and pre [M][N] contiguous.  kind: the type
@@ -291,5 +295,8 @@ int64_t dpre_parts(const DpreArgs &a);
 cudaError_t launch_dpre(const DpreArgs &a, cudaStream_t s);
 // out[c] = sum over n partial rows (norm.cu)
 cudaError_t launch_column_sum(const float *partial, float *out, int64_t n, int64_t D, cudaStream_t s);
+// the columns from `first` on go to rest[c - first]
+cudaError_t launch_column_sum(const float *partial, float *out, float *rest, int64_t first, int64_t n, int64_t D,
+                              cudaStream_t s);
 
 }  // namespace delta
