@@ -730,6 +730,42 @@ int delta_linear_bwd(const void *x, const void *w, const void *dout, const void 
                      float *dbias, int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act,
                      delta_dtype dtype, struct CUstream_st *stream);
 
+/*
+ * delta_glu_fwd -- the first half of a gated feed-forward layer: both projections,
+ * the activation and the product in one kernel,
+ *
+ *   pre = x w^T + bias = (g, u),   out = act(g) * u,
+ *
+ * summed and finished in float32 and rounded once.
+ *
+ *   x     [M, K]   dtype, row stride ldx
+ *   w     [2 N, K] dtype, row stride ldw: N rows for g, then N for u
+ *   bias  [2 N]    bdtype, or NULL
+ *   out   [M, N]   dtype
+ *   pre   [M, 2 N] dtype, for delta_glu_bwd, or NULL
+ *
+ * K > 0, N <= 2^30.  Runs where delta_linear_fwd runs; in float32, a correctness
+ * path, as a product and an elementwise kernel, with pre in scratch where it is not
+ * wanted.
+ */
+int delta_glu_fwd(const void *x, const void *w, const void *bias, void *out, void *pre, int M, int N, int K,
+                  int64_t ldx, int64_t ldw, delta_act act, delta_dtype dtype, delta_dtype bdtype,
+                  struct CUstream_st *stream);
+
+/*
+ * delta_glu_bwd -- its gradients: with dpre = (dout u act'(g), dout act(g)),
+ *
+ *   dx = dpre w,   dw = dpre^T x,   dbias = sum over rows of dpre.
+ *
+ *   x, w   as in the forward;  dout [M, N], pre [M, 2 N] dtype, contiguous
+ *   dx     [M, K] dtype,  dw [2 N, K] dtype,  dbias [2 N] float32; NULL: not wanted
+ *
+ * dpre is rounded, and scratch taken, as in delta_linear_bwd.
+ */
+int delta_glu_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw, float *dbias,
+                  int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act, delta_dtype dtype,
+                  struct CUstream_st *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,7 @@ arguments: shape/dtype checks, output allocation through PyTorch, the
 current CUDA stream, and status-to-exception mapping.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback, and a
 missing library raises immediately.  The operators around the mixers in a
-block (scan, norm, linear) are in ``block.py`` and exported here.
+block (scan, decay attention, norms, linear, gated layer) are in ``block.py`` and exported here.
 """
 from __future__ import annotations
 
@@ -18,7 +18,8 @@ import torch
 
 from . import block
 from .block import (delta_add_layernorm_bwd, delta_add_layernorm_fwd, delta_add_rmsnorm_bwd,
-                    delta_add_rmsnorm_fwd, delta_add_rmsnorm_quant, delta_decay_bwd, delta_decay_fwd, delta_decay_step, delta_linear_bwd,
+                    delta_add_rmsnorm_fwd, delta_add_rmsnorm_quant, delta_decay_bwd,
+                    delta_decay_fwd, delta_decay_step, delta_glu_bwd, delta_glu_fwd, delta_linear_bwd,
                     delta_linear_fwd, delta_linear_quant, delta_scan_bwd, delta_scan_fwd,
                     delta_scan_step)
 

@@ -1,8 +1,8 @@
 """Operators around the token mixers in a block: the gated linear recurrence
 (``delta_scan_*``), linear attention with a decay for each head
 (``delta_decay_*``), the residual addition with RMS norm
-(``delta_add_rmsnorm_*``) or layer norm (``delta_add_layernorm_*``) and the linear layer with its epilogue
-(``delta_linear_*``).
+(``delta_add_rmsnorm_*``) or layer norm (``delta_add_layernorm_*``), the linear layer with its epilogue
+(``delta_linear_*``) and the gated feed-forward layer (``delta_glu_*``).
 
 Bindings over the C ABI of ``libdelta.so`` with the ABI's names: argument
 checks, output allocation, the current CUDA stream, statuses as exceptions.
@@ -36,7 +36,7 @@ SYMBOLS = ("delta_scan_fwd", "delta_scan_step", "delta_scan_bwd", "delta_decay_f
            "delta_decay_step", "delta_decay_bwd", "delta_add_rmsnorm_fwd",
            "delta_add_rmsnorm_quant", "delta_add_rmsnorm_bwd", "delta_add_layernorm_fwd",
            "delta_add_layernorm_bwd", "delta_linear_fwd",
-           "delta_linear_quant", "delta_linear_bwd")
+           "delta_linear_quant", "delta_linear_bwd", "delta_glu_fwd", "delta_glu_bwd")
 
 
 def declare(lib) -> None:
@@ -56,7 +56,9 @@ def declare(lib) -> None:
             ("delta_add_layernorm_bwd", [p] * 9 + [n, i, i, i, p]),
             ("delta_linear_fwd", [p] * 6 + [i] * 3 + [n] * 3 + [i] * 3 + [p]),
             ("delta_linear_quant", [p] * 7 + [i] * 3 + [n] * 3 + [i] * 2 + [p]),
-            ("delta_linear_bwd", [p] * 7 + [i] * 3 + [n] * 2 + [i] * 2 + [p])):
+            ("delta_linear_bwd", [p] * 7 + [i] * 3 + [n] * 2 + [i] * 2 + [p]),
+            ("delta_glu_fwd", [p] * 5 + [i] * 3 + [n] * 2 + [i] * 3 + [p]),
+            ("delta_glu_bwd", [p] * 7 + [i] * 3 + [n] * 2 + [i] * 2 + [p])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = i, args
 
@@ -660,6 +662,62 @@ def delta_linear_bwd(x, w, dout, pre=None, *, act="none", want=(True, True, True
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     st = _on(dev, _lib().delta_linear_bwd)(px, pw, po, pp, ptr(dx), ptr(dw), ptr(db), M, N, K, ldx,
         ldw, acode, code, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return dx, dw, db
+
+
+def _glu_begin(x, w, act, name):
+    """shared checks: sizes, pointers and row strides of a gated layer"""
+    code, dev = _begin(x, name, 0)
+    if isinstance(w, torch.Tensor) and w.dim() == 2 and w.shape[0] % 2:
+        raise ValueError(f"w must have two halves of rows, got {w.shape[0]}")
+    acode, M, N, K, px, ldx, pw, ldw, _, _, _, _, shape = _linear_begin(x, w, None, None, act, x.dtype, x.dtype, dev)
+    return code, dev, acode, M, N // 2, K, px, ldx, pw, ldw, shape
+
+
+def delta_glu_fwd(x, w, bias=None, *, act="silu", save_pre=False, out=None, stream=None):
+    """The first half of a gated feed-forward layer: ``out = act(g) * u`` with
+    ``(g, u) = x w^T + bias``, finished in float32.
+
+    x [..., K] and w [2 N, K] bfloat16 or float32 (rows may be strided): N rows for the
+    gate, then N for the other projection; bias [2 N] float32 or bfloat16; ``act`` as in
+    ``delta_linear_fwd``.  Returns out [..., N], with ``save_pre`` ``(out, pre [..., 2 N])``
+    for ``delta_glu_bwd``.
+    """
+    if stream is None and out is None:
+        r = (_fast or _open_fast()).glu_fwd(x, w, bias, _ACTS.get(act, -1), save_pre)
+        if r is not NotImplemented:
+            return _checked(r)
+    code, dev, acode, M, N, K, px, ldx, pw, ldw, shape = _glu_begin(x, w, act, "delta_glu_fwd")
+    pb, bcode = (None, 0) if bias is None else _weight(bias, 2 * N, x.dtype, dev, "bias")
+    out = _output(out, "out", shape[:-1] + (N,), x.dtype, dev, stream)
+    pre = _empty(shape, x.dtype, dev, stream) if save_pre else None
+    st = _on(dev, _lib().delta_glu_fwd)(px, pw, pb, out.data_ptr(), None if pre is None else pre.data_ptr(),
+        M, N, K, ldx, ldw, acode, code, bcode, _raw_stream(dev, stream))
+    if st:
+        _raise(st)
+    return (out, pre) if save_pre else out
+
+
+def delta_glu_bwd(x, w, dout, pre, *, act="silu", want=(True, True, True), stream=None):
+    """Gradients of ``delta_glu_fwd``: x and w as there, dout [..., N] and pre [..., 2 N]
+    contiguous.  Returns ``(dx, dw, dbias)``, dx and dw in x's type, dbias float32; those
+    not wanted are None."""
+    if stream is None:
+        r = (_fast or _open_fast()).glu_bwd(x, w, dout, pre, _ACTS.get(act, -1), *want)
+        if r is not NotImplemented:
+            return _checked(r)
+    code, dev, acode, M, N, K, px, ldx, pw, ldw, shape = _glu_begin(x, w, act, "delta_glu_bwd")
+    dt = x.dtype
+    po = _tensor(dout, "dout", shape[:-1] + (N,), dt, dev)
+    pp = _tensor(pre, "pre", shape, dt, dev)
+    dx = _empty(x.shape, dt, dev, stream) if want[0] else None
+    dw = _empty((2 * N, K), dt, dev, stream) if want[1] else None
+    db = _empty((2 * N,), torch.float32, dev, stream) if want[2] else None
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = _on(dev, _lib().delta_glu_bwd)(px, pw, po, pp, ptr(dx), ptr(dw), ptr(db), M, N, K, ldx, ldw, acode,
+        code, _raw_stream(dev, stream))
     if st:
         _raise(st)
     return dx, dw, db

@@ -440,10 +440,55 @@ PyObject *linear_bwd(PyObject *const *a, Py_ssize_t n) {
   return tuple(give(dx), give(dw), give(db));
 }
 
+// x, w, bias, act, save_pre
+PyObject *glu_fwd(PyObject *const *a, Py_ssize_t n) {
+  if (n != 5) return other();
+  const Tensor *x = tensor(a[0]);
+  const int act = (int)PyLong_AsLong(a[3]);
+  Linear l;
+  if (!x || code(x->scalar_type()) < 0 || act < 0 || !l.take(a[0], a[1], x->scalar_type()) || l.N % 2 != 0 ||
+      !l.extras(a[2], Py_None, x->scalar_type()))
+    return other();
+  const auto dt = x->scalar_type();
+  Tensor out, pre;
+  if (truth(a[4])) pre = empty(l.shape, dt, l.dev);
+  l.shape.back() = l.N / 2;
+  out = empty(l.shape, dt, l.dev);
+  const int st = delta_glu_fwd(ptr(x), ptr(l.w), ptr(l.bias), out.data_ptr(), pre.defined() ? pre.data_ptr() : nullptr,
+                               (int)l.M, (int)(l.N / 2), (int)l.K, l.ldx, l.ldw, (delta_act)act, (delta_dtype)code(dt),
+                               l.bcode, stream(l.dev));
+  if (st != DELTA_OK) return PyLong_FromLong(st);
+  return pre.defined() ? tuple(wrap(out), wrap(pre)) : wrap(out);
+}
+
+// x, w, dout, pre, act, want_dx, want_dw, want_dbias
+PyObject *glu_bwd(PyObject *const *a, Py_ssize_t n) {
+  if (n != 8) return other();
+  const Tensor *x = tensor(a[0]), *d = tensor(a[2]), *pre = tensor(a[3]);
+  const int act = (int)PyLong_AsLong(a[4]);
+  Linear l;
+  if (!x || code(x->scalar_type()) < 0 || act < 0 || !l.take(a[0], a[1], x->scalar_type()) || l.N % 2 != 0) return other();
+  const auto dt = x->scalar_type();
+  if (!whole(pre, dt, l.shape, l.dev)) return other();
+  l.shape.back() = l.N / 2;
+  if (!whole(d, dt, l.shape, l.dev)) return other();
+  Tensor dx, dw, db;
+  if (truth(a[5])) dx = empty(x->sizes(), dt, l.dev);
+  if (truth(a[6])) dw = empty({l.N, l.K}, dt, l.dev);
+  if (truth(a[7])) db = empty({l.N}, at::kFloat, l.dev);
+  const auto at_ = [](Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+  const int st = delta_glu_bwd(ptr(x), ptr(l.w), ptr(d), ptr(pre), at_(dx), at_(dw), static_cast<float *>(at_(db)),
+                               (int)l.M, (int)(l.N / 2), (int)l.K, l.ldx, l.ldw, (delta_act)act, (delta_dtype)code(dt),
+                               stream(l.dev));
+  if (st != DELTA_OK) return PyLong_FromLong(st);
+  const auto give = [](Tensor &t) { return t.defined() ? wrap(t) : none(); };
+  return tuple(give(dx), give(dw), give(db));
+}
+
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))guarded<name>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(scan_fwd),   FAST(scan_step),    FAST(scan_bwd),   FAST(norm_fwd), FAST(norm_bwd),
                          FAST(linear_fwd), FAST(linear_quant), FAST(linear_bwd), FAST(decay_fwd), FAST(decay_step), FAST(decay_bwd),
-                         FAST(layernorm_fwd), FAST(layernorm_bwd), {nullptr, nullptr, 0, nullptr}};
+                         FAST(layernorm_fwd), FAST(layernorm_bwd), FAST(glu_fwd), FAST(glu_bwd), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", "block operators, the common case", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -282,10 +282,11 @@ int run_linear(const void *x, const void *w, const float *x_scale, const float *
 // products, 87 of the 110 us at M4096 N4096 K2048.  Layers that take one launch
 // (small_bwd_fits) form dpre in registers on the CUDA cores, where rounding it
 // would only cost, so they have the smaller error; a layer's sizes alone decide.
-// dbias sums the unrounded terms.
+// dbias sums the unrounded terms.  glu: the gated layer, whose w has N rows in two
+// halves; dpre has N columns and dout half as many.
 cudaError_t linear_backward(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                             float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
-                            bool bf16, cudaStream_t s) {
+                            bool bf16, bool glu, cudaStream_t s) {
   const int64_t e = bf16 ? 2 : 4;
   cudaError_t err = cudaSuccess;
   if (M == 0 || N == 0) {  // empty sums
@@ -295,10 +296,10 @@ cudaError_t linear_backward(const void *x, const void *w, const void *dout, cons
     return err;
   }
   if (bf16 && delta::small_bwd_fits(M, N, K))
-    return delta::launch_small_bwd(x, w, dout, pre, dx, dw, dbias, M, N, K, ldx, ldw, act, s);
-  const bool form = (dx || dw) && (act != delta::kActNone || (bf16 && N % 8 != 0));
+    return delta::launch_small_bwd(x, w, dout, pre, dx, dw, dbias, M, N, K, ldx, ldw, act, glu, s);
+  const bool form = (dx || dw) && (glu || act != delta::kActNone || (bf16 && N % 8 != 0));
   delta::DpreArgs d{};
-  d.dout = dout; d.pre = pre; d.dbias = dbias; d.M = M; d.N = N; d.act = act; d.bf16 = bf16;
+  d.dout = dout; d.pre = pre; d.dbias = dbias; d.M = M; d.N = glu ? N / 2 : N; d.act = act; d.bf16 = bf16; d.glu = glu;
   d.ldp = form && bf16 ? up(N, 64) : N;
   Operand ox = operand(x, M, K, ldx, (int)e), ow = operand(w, N, K, ldw, (int)e);
   const bool packx = bf16 && dw && !ox.whole(), packw = bf16 && dx && !ow.whole();
@@ -333,6 +334,48 @@ cudaError_t linear_backward(const void *x, const void *w, const void *dout, cons
   }
   const cudaError_t ef = scr.release();
   return err != cudaSuccess ? err : ef;
+}
+
+// The gated layer; a.N columns of the output, w [2 N][K], pre [M][2 N].
+cudaError_t glu_forward(const delta::LinearArgs &a, cudaStream_t s) {
+  Scratch scr(s);
+  cudaError_t err;
+  if (a.kind == delta::kLinF32) {
+    delta::LinearArgs g = a;
+    g.N = 2 * a.N, g.act = delta::kActNone, g.out = a.pre, g.pre = nullptr;
+    if (!a.pre) {
+      scr.want(a.M * g.N * 4);
+      if ((err = scr.take()) != cudaSuccess) return err;
+      g.out = scr.cut(a.M * g.N * 4);
+    }
+    err = delta::launch_gemm_f32(g, static_cast<const float *>(a.x), a.ldx, 1, static_cast<const float *>(a.w), a.ldw, 1,
+                                 a.K, s);
+    if (err == cudaSuccess)
+      err = delta::launch_glu_act(static_cast<const float *>(g.out), static_cast<float *>(a.out), a.M, a.N, a.act, s);
+  } else {
+    Operand x = operand(a.x, a.M, a.K, a.ldx, 2), w = operand(a.w, 2 * a.N, a.K, a.ldw, 2);
+    const bool pack = !x.whole() || !w.whole();
+    // few rows and small products stream w, as in linear_forward
+    if (a.M <= delta::kLinSmallM || delta::linear_small_us(a.M, 2 * a.N, a.K, false, !pack) <
+                                        delta::gemm_tc_us(a.M, 2 * a.N, a.K, false) + (pack ? kPackUs : 0.0))
+      return delta::launch_glu_small(a, s);
+    if (!x.whole()) scr.want(x.bytes());
+    if (!w.whole()) scr.want(w.bytes());
+    if ((err = scr.take()) != cudaSuccess) return err;
+    bool after = false;
+    err = x.pack(scr, after, s);
+    if (err == cudaSuccess) err = w.pack(scr, after, s);
+    if (err == cudaSuccess) err = delta::launch_glu_tc({x.p, w.p, x.ld, w.ld, a.K, false, false, a, after}, s);
+  }
+  const cudaError_t ef = scr.release();
+  return err != cudaSuccess ? err : ef;
+}
+
+int glu_sizes(int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act, delta_dtype dtype) {
+  const int st = check_dtype(dtype);
+  if (st != DELTA_OK) return st;
+  if (N > (1 << 30)) return fail(DELTA_ERR_UNSUPPORTED, "N=%d: two halves of it must be below 2^31", N);
+  return linear_sizes(M, 2 * N, K, ldx, ldw, 2 * (int64_t)N, act);
 }
 
 }  // namespace
@@ -504,9 +547,59 @@ int delta_linear_bwd(const void *x, const void *w, const void *dout, const void 
     return st;
   if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
   const cudaError_t err = linear_backward(x, w, dout, act == DELTA_ACT_NONE ? nullptr : pre, dx, dw, dbias, m, n, k,
-                                          ldx, ldw, (int)act, dtype == DELTA_BF16,
+                                          ldx, ldw, (int)act, dtype == DELTA_BF16, false,
                                           reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "linear layer's gradients");
+}
+
+int delta_glu_fwd(const void *x, const void *w, const void *bias, void *out, void *pre, int M, int N, int K,
+                  int64_t ldx, int64_t ldw, delta_act act, delta_dtype dtype, delta_dtype bdtype,
+                  struct CUstream_st *stream) {
+  int st;
+  if ((st = glu_sizes(M, N, K, ldx, ldw, act, dtype)) != DELTA_OK) return st;
+  if ((st = check_dtype(bdtype)) != DELTA_OK) return st;
+  if (M == 0 || N == 0) return DELTA_OK;
+  if (!x || !w || !out) return fail(DELTA_ERR_INVALID, "x, w and out must be non-NULL");
+  const int64_t e = esize(dtype), m = M, n = N, k = K;
+  if (!aligned_to(x, e) || !aligned_to(w, e) || !aligned_to(bias, esize(bdtype)))
+    return fail(DELTA_ERR_ALIGN, "every input must be aligned to its elements");
+  if (!aligned16(out) || !aligned16(pre)) return fail(DELTA_ERR_ALIGN, "out and pre must be 16-byte aligned");
+  if (M == 1) ldx = K;
+  if ((st = check_overlap({Span{"out", range(out, m * n * e)}, Span{"pre", range(pre, 2 * m * n * e)}},
+                          {Span{"x", range(x, ((m - 1) * ldx + k) * e)}, Span{"w", range(w, ((2 * n - 1) * ldw + k) * e)},
+                           Span{"bias", range(bias, 2 * n * esize(bdtype))}})) != DELTA_OK)
+    return st;
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  delta::LinearArgs a{};
+  a.x = x; a.w = w; a.bias = bias; a.out = out; a.pre = pre; a.M = m; a.N = n; a.K = k; a.ldx = ldx; a.ldw = ldw;
+  a.act = (int)act; a.kind = dtype == DELTA_BF16 ? delta::kLinBf16 : delta::kLinF32; a.bias_bf16 = bdtype == DELTA_BF16;
+  const cudaError_t err = glu_forward(a, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "gated layer");
+}
+
+int delta_glu_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw, float *dbias,
+                  int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act, delta_dtype dtype,
+                  struct CUstream_st *stream) {
+  int st;
+  if ((st = glu_sizes(M, N, K, ldx, ldw, act, dtype)) != DELTA_OK) return st;
+  if (!dx && !dw && !dbias) return DELTA_OK;
+  const int64_t e = esize(dtype), m = M, n = N, k = K;
+  if (M <= 1) ldx = K;
+  if (!aligned16(dout) || !aligned16(pre) || !aligned16(dx) || !aligned16(dw) || !aligned16(dbias))
+    return fail(DELTA_ERR_ALIGN, "dout, pre and the gradients must be 16-byte aligned");
+  if (!aligned_to(x, e) || !aligned_to(w, e)) return fail(DELTA_ERR_ALIGN, "x and w must be aligned to their elements");
+  if (M > 0 && N > 0 && (!dout || !pre || (dw && !x) || (dx && !w)))
+    return fail(DELTA_ERR_INVALID, "x, w, dout and pre must be non-NULL");
+  if ((st = check_overlap({Span{"dx", range(dx, m * k * e)}, Span{"dw", range(dw, 2 * n * k * e)},
+                           Span{"dbias", range(dbias, 2 * n * 4)}},
+                          {Span{"x", range(x, m > 0 ? ((m - 1) * ldx + k) * e : 0)},
+                           Span{"w", range(w, n > 0 ? ((2 * n - 1) * ldw + k) * e : 0)},
+                           Span{"dout", range(dout, m * n * e)}, Span{"pre", range(pre, 2 * m * n * e)}})) != DELTA_OK)
+    return st;
+  if (take_injection()) return fail(DELTA_ERR_CUDA, "injected failure (delta_inject_failure)");
+  const cudaError_t err = linear_backward(x, w, dout, pre, dx, dw, dbias, m, 2 * n, k, ldx, ldw, (int)act,
+                                          dtype == DELTA_BF16, true, reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? DELTA_OK : cuda_fail(err, "gated layer's gradients");
 }
 
 }  // extern "C"

@@ -263,33 +263,39 @@ struct GemmArgs {
 cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s);
 // about how long it takes
 double gemm_tc_us(int64_t M, int64_t N, int64_t K, bool f8);
+// The gated layer: epi.N columns of the output, b [2 N][K], epi.pre [M][2 N].
+cudaError_t launch_glu_tc(const GemmArgs &g, cudaStream_t s);
 cudaError_t read_and_clear_linear_error(unsigned int *word);
 // streams the weight once for every 16 rows of x: for M <= kLinSmallM once
 constexpr int kLinSmallM = 16;
 cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s);
+cudaError_t launch_glu_small(const LinearArgs &a, cudaStream_t s);  // w [2 N][K], pre [M][2 N]
+// out = act(g) u, pre [M][2 N] = (g, u), float32
+cudaError_t launch_glu_act(const float *pre, float *out, int64_t M, int64_t N, int act, cudaStream_t s);
 // about how long it takes
 double linear_small_us(int64_t M, int64_t N, int64_t K, bool f8, bool whole);
 // all gradients of a small bfloat16 layer (those whose pointers are set), in one
-// launch without scratch
+// launch without scratch; glu: w's N rows are the gated layer's two halves
 constexpr double kSmallBwdUs = 14;
 bool small_bwd_fits(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                              float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
-                             cudaStream_t s);
+                             bool glu, cudaStream_t s);
 // float32 on the CUDA cores, operands with any strides (elements)
 cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, int64_t ak, const float *b,
                             int64_t bn, int64_t bk, int64_t K, cudaStream_t s);
 // rows x cols elements of `size` bytes into rows of ldp elements
 cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, int64_t ldp,
                         int size, bool dependent, cudaStream_t s);
-// dpre = dout * act'(pre) in rows of ldp elements where dpre is set, and dbias = its column sums in float32 where dbias is set
+// dpre = dout * act'(pre) in rows of ldp elements where dpre is set, and dbias = its column sums in float32 where dbias is set;
+// glu: pre, dpre, dbias and a row of partial have 2 N columns
 struct DpreArgs {
   const void *dout, *pre;
   void *dpre;
   float *dbias, *partial;  // partial [dpre_parts()][N]
   int64_t M, N, ldp;
   int act;
-  bool bf16;
+  bool bf16, glu;
 };
 int64_t dpre_parts(const DpreArgs &a);
 cudaError_t launch_dpre(const DpreArgs &a, cudaStream_t s);

@@ -89,7 +89,8 @@ __device__ __forceinline__ uint4 piece(const uint8_t *row, int64_t k, int64_t by
   }
 }
 
-template <bool kF8, int NT, bool kVec>
+// The gated form (kGlu) takes 8 rows of either half of w for the 16.
+template <bool kF8, int NT, bool kVec, bool kGlu>
 __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, int cs) {
   constexpr int kSize = kF8 ? 1 : 2, kTok = 8 * NT;
   __shared__ float part[kSmallWarps][16][kTok + 1];
@@ -98,12 +99,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
   const int g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)(blockIdx.x % cs) : 0;
   chain_wait();
-  const int64_t n0 = (int64_t)(blockIdx.x / cs) * 16, m0 = (int64_t)blockIdx.y * kTok;
+  constexpr int kRows = kGlu ? 8 : 16;  // output columns of a CTA
+  const int64_t n0 = (int64_t)(blockIdx.x / cs) * kRows, m0 = (int64_t)blockIdx.y * kTok;
   if (cs > 1) cg::this_cluster().barrier_arrive();
   const int64_t bytes = a.K * kSize;
   // rows past the end repeat the last one; their results are not stored
   const uint8_t *w0 = static_cast<const uint8_t *>(a.w) + (n0 + g < a.N ? n0 + g : a.N - 1) * a.ldw * kSize;
-  const uint8_t *w1 = static_cast<const uint8_t *>(a.w) + (n0 + g + 8 < a.N ? n0 + g + 8 : a.N - 1) * a.ldw * kSize;
+  const uint8_t *w1 = kGlu ? w0 + a.N * a.ldw * kSize
+                           : static_cast<const uint8_t *>(a.w) + (n0 + g + 8 < a.N ? n0 + g + 8 : a.N - 1) * a.ldw * kSize;
   const uint8_t *x[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -152,37 +155,50 @@ __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, i
   }
   __syncthreads();
   if (cs > 1) cg::this_cluster().barrier_wait();  // every CTA of the cluster has begun
-  for (int i = threadIdx.x; i < 16 * kTok; i += kSmallWarps * 32) {
-    const int r = i & 15, tok = i >> 4;
-    float s = 0.f;
+  const auto sum = [&](int r, int tok) {
+    float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSmallWarps; ++w) s += part[w][r][tok];
-    if (cs > 1)
-      cg::this_cluster().map_shared_rank(&ranks[rank][0], 0)[i] = s;
-    else if (m0 + tok < a.M && n0 + r < a.N)
-      finish<__nv_bfloat16>(a, m0 + tok, n0 + r, s);
+    for (int w = 0; w < kSmallWarps; ++w) v += part[w][r][tok];
+    return v;
+  };
+  const auto store = [&](int r, int tok, float v, float u) {  // (u: the other half's, gated alone)
+    if (m0 + tok >= a.M || n0 + r >= a.N) return;
+    if constexpr (kGlu)
+      finish_glu<__nv_bfloat16>(a, m0 + tok, n0 + r, v, u);
+    else
+      finish<__nv_bfloat16>(a, m0 + tok, n0 + r, v);
+  };
+  if (cs == 1) {
+    for (int i = threadIdx.x; i < kRows * kTok; i += kSmallWarps * 32) {
+      const int r = i % kRows, tok = i / kRows;
+      store(r, tok, sum(r, tok), kGlu ? sum(r + 8 & 15, tok) : 0.f);
+    }
+    return;
   }
-  if (cs > 1) {
-    cg::this_cluster().sync();
-    if (rank == 0)
-      for (int i = threadIdx.x; i < 16 * kTok; i += kSmallWarps * 32) {
-        const int r = i & 15, tok = i >> 4;
-        float s = 0.f;
-        for (int q = 0; q < cs; ++q) s += ranks[q][i];
-        if (m0 + tok < a.M && n0 + r < a.N) finish<__nv_bfloat16>(a, m0 + tok, n0 + r, s);
+  for (int i = threadIdx.x; i < 16 * kTok; i += kSmallWarps * 32)
+    cg::this_cluster().map_shared_rank(&ranks[rank][0], 0)[i] = sum(i & 15, i >> 4);
+  cg::this_cluster().sync();
+  if (rank == 0)
+    for (int i = threadIdx.x; i < kRows * kTok; i += kSmallWarps * 32) {
+      const int r = i % kRows, tok = i / kRows;
+      float v = 0.f, u = 0.f;
+      for (int q = 0; q < cs; ++q) {
+        v += ranks[q][tok * 16 + r];
+        if constexpr (kGlu) u += ranks[q][tok * 16 + r + 8];
       }
-  }
+      store(r, tok, v, u);
+    }
 }
 
-template <bool kF8, int NT>
+template <bool kF8, int NT, bool kGlu = false>
 cudaError_t run_small(const LinearArgs &a, cudaStream_t s) {
   const int64_t size = kF8 ? 1 : 2, e = 16 / size;
   const bool vec = a.K % e == 0 && a.ldx % e == 0 && a.ldw % e == 0 && aligned_to(a.x, 16) && aligned_to(a.w, 16);
   // CTAs along k until every SM has two, as far as k has a turn for each warp
-  const int64_t groups = (a.N + 15) / 16, passes = (a.M + 8 * NT - 1) / (8 * NT), turns = (a.K * size + kBlocks * 64 - 1) / (kBlocks * 64);
+  const int64_t groups = (a.N + (kGlu ? 7 : 15)) / (kGlu ? 8 : 16), passes = (a.M + 8 * NT - 1) / (8 * NT), turns = (a.K * size + kBlocks * 64 - 1) / (kBlocks * 64);
   int cs = 1;
   while (cs < kMaxCluster && groups * passes * cs < 2 * sm_count() && turns > (int64_t)kSmallWarps * cs) cs *= 2;
-  return chain_launch(vec ? small_kernel<kF8, NT, true> : small_kernel<kF8, NT, false>,
+  return chain_launch(vec ? small_kernel<kF8, NT, true, kGlu> : small_kernel<kF8, NT, false, kGlu>,
                       dim3((unsigned)(groups * cs), (unsigned)passes), dim3(kSmallWarps * 32), 0, cs, true, s, a, cs);
 }
 
@@ -270,6 +286,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const unsigned char *src, uns
 // dpre = dout act'(pre) and its column sums: a CTA has 32 V columns and every
 // parts-th group of 8 rows; one element (V = 1) or 16 bytes a lane.  The sums
 // take the unrounded products; part sums meet in launch_column_sum.
+// (The gated layer's is glu_dpre_kernel.)
 template <typename T, int V>
 __global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
   struct __align__(sizeof(T) * V) Vec { T v[V]; };
@@ -319,6 +336,72 @@ __global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
   }
 }
 
+// The gated layer's: dpre [M][2 N] = (dout u act'(g), dout act(g)) from pre = (g, u),
+// and the sums of its 2 N columns.  As above, a column of either half a lane.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) glu_dpre_kernel(DpreArgs p) {
+  struct __align__(sizeof(T) * V) Vec { T v[V]; };
+  __shared__ float sum[2][8][32 * V];
+  const int64_t c = ((int64_t)blockIdx.x * 32 + threadIdx.x) * V;
+  chain_next();
+  float s[2][V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[0][i] = s[1][i] = 0.f;
+  constexpr int kAhead = V == 1 ? 4 : 2;  // rows a thread asks for at a time
+  const int64_t step = (int64_t)gridDim.y * 8;
+  if (c < p.N)
+    for (int64_t m0 = (int64_t)blockIdx.y * 8 + threadIdx.y; m0 < p.M; m0 += step * kAhead) {
+      Vec d[kAhead], g[kAhead], u[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t m = m0 + k * step;
+        if (m >= p.M) continue;
+        d[k] = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.dout) + m * p.N + c);
+        g[k] = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.pre) + m * 2 * p.N + c);
+        u[k] = *reinterpret_cast<const Vec *>(static_cast<const T *>(p.pre) + m * 2 * p.N + p.N + c);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t m = m0 + k * step;
+        if (m >= p.M) continue;
+        Vec o[2];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float dv = to_f(d[k].v[i]), gv = to_f(g[k].v[i]);
+          const float a = dv * to_f(u[k].v[i]) * slope(p.act, gv), b = dv * activate(p.act, gv);
+          s[0][i] = __fadd_rn(s[0][i], a), s[1][i] = __fadd_rn(s[1][i], b);  // (as in dpre_kernel)
+          from_f(a, o[0].v[i]), from_f(b, o[1].v[i]);
+        }
+        if (p.dpre) {
+          *reinterpret_cast<Vec *>(static_cast<T *>(p.dpre) + m * p.ldp + c) = o[0];
+          *reinterpret_cast<Vec *>(static_cast<T *>(p.dpre) + m * p.ldp + p.N + c) = o[1];
+        }
+      }
+    }
+  if (!p.dbias) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    sum[0][threadIdx.y][threadIdx.x * V + i] = s[0][i], sum[1][threadIdx.y][threadIdx.x * V + i] = s[1][i];
+  __syncthreads();
+  for (int i = threadIdx.y * 32 + threadIdx.x; i < 64 * V; i += 256) {
+    const int h = i / (32 * V), j = i % (32 * V);
+    const int64_t n = (int64_t)blockIdx.x * 32 * V + j;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += sum[h][w][j];
+    if (n < p.N) p.partial[((int64_t)blockIdx.y * 2 + h) * p.N + n] = v;
+  }
+}
+
+// out = act(g) u from pre = (g, u), float32
+__global__ void __launch_bounds__(256) glu_act_kernel(const float *pre, float *out, int64_t M, int64_t N, int act) {
+  chain_wait();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * 256) {
+    const float *at = pre + i / N * 2 * N + i % N;
+    out[i] = activate(act, at[0]) * at[N];
+  }
+}
+
 // Small gradients, all in one kernel: C[m][n] = sum_r A(r, m) B(r, n) with A
 // formed on the way in as dpre = dout act'(pre), so that nothing is packed and
 // dpre is not rounded.  For dx, m is the row and r the output channel, B is w;
@@ -339,6 +422,8 @@ struct SmallBwd {
   int act, cs;
 };
 
+// kGlu: the gated layer, whose N rows of w are two halves; dout is [M][N / 2]
+template <bool kGlu>
 __global__ void __launch_bounds__(256) small_bwd_kernel(SmallBwd p) {
   __shared__ float sa[kBr][kBm + 1];
   __shared__ __align__(16) float sb[kBr][kBn + 4];
@@ -359,7 +444,8 @@ __global__ void __launch_bounds__(256) small_bwd_kernel(SmallBwd p) {
   const bool sums = of_w && p.dbias && n0 == 0;
   const int tm = tid / 16 * 2, tn = tid % 16 * 4;
   float c[2][4] = {}, s = 0.f;
-  __nv_bfloat16 ra[kBr * kBm / 256], rp[kBr * kBm / 256], rb[kBr * kBn / 256];
+  __nv_bfloat16 ra[kBr * kBm / 256], rp[kBr * kBm / 256], rb[kBr * kBn / 256], ru[kGlu ? kBr * kBm / 256 : 1];
+  bool up[kGlu ? kBr * kBm / 256 : 1];
   const __nv_bfloat16 zero = __float2bfloat16_rn(0.f);
   const auto fetch = [&](int64_t r0) {
 #pragma unroll
@@ -368,8 +454,17 @@ __global__ void __launch_bounds__(256) small_bwd_kernel(SmallBwd p) {
       const int a = tid % 32, b = tid / 32 + 8 * k;
       const int64_t row = of_w ? r0 + b : m0 + b, col = of_w ? m0 + a : r0 + a;
       const bool in = row < p.M && col < p.N;
-      ra[k] = in ? p.dout[row * p.N + col] : zero;
-      rp[k] = in && p.act != kActNone ? p.pre[row * p.N + col] : zero;
+      if constexpr (kGlu) {
+        const int64_t half = p.N / 2;
+        up[k] = col >= half;
+        const int64_t at = up[k] ? col - half : col;
+        ra[k] = in ? p.dout[row * half + at] : zero;
+        rp[k] = in ? p.pre[row * p.N + at] : zero;
+        ru[k] = in && !up[k] ? p.pre[row * p.N + half + at] : zero;
+      } else {
+        ra[k] = in ? p.dout[row * p.N + col] : zero;
+        rp[k] = in && p.act != kActNone ? p.pre[row * p.N + col] : zero;
+      }
     }
     if (out) {
 #pragma unroll
@@ -387,7 +482,12 @@ __global__ void __launch_bounds__(256) small_bwd_kernel(SmallBwd p) {
       const int a = tid % 32, b = tid / 32 + 8 * k;
       const float g = __bfloat162float(ra[k]);
       // outside, dout stands as 0 and takes no factor
-      const float v = p.act == kActNone ? g : g * slope(p.act, __bfloat162float(rp[k]));
+      float v;
+      if constexpr (kGlu)
+        v = up[k] ? g * activate(p.act, __bfloat162float(rp[k]))
+                  : g * __bfloat162float(ru[k]) * slope(p.act, __bfloat162float(rp[k]));
+      else
+        v = p.act == kActNone ? g : g * slope(p.act, __bfloat162float(rp[k]));
       if (of_w)
         sa[b][a] = v;
       else
@@ -477,6 +577,16 @@ cudaError_t launch_linear_small(const LinearArgs &a, cudaStream_t s) {
   return a.M <= 8 ? run_small<false, 1>(a, s) : run_small<false, 2>(a, s);
 }
 
+cudaError_t launch_glu_small(const LinearArgs &a, cudaStream_t s) {
+  return a.M <= 8 ? run_small<false, 1, true>(a, s) : run_small<false, 2, true>(a, s);
+}
+
+cudaError_t launch_glu_act(const float *pre, float *out, int64_t M, int64_t N, int act, cudaStream_t s) {
+  const int64_t want = (M * N + 255) / 256, cap = (int64_t)sm_count() * 8;
+  return chain_launch(glu_act_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, 1, true, s, pre, out, M,
+                      N, act);
+}
+
 cudaError_t launch_gemm_f32(const LinearArgs &epi, const float *a, int64_t am, int64_t ak, const float *b,
                             int64_t bn, int64_t bk, int64_t K, cudaStream_t s) {
   const int64_t grid = ((epi.M + 63) / 64) * ((epi.N + 63) / 64);
@@ -507,7 +617,12 @@ cudaError_t launch_dpre(const DpreArgs &p, cudaStream_t s) {
   const int v = dpre_vec(p);
   const int64_t parts = dpre_parts(p);
   const dim3 grid((unsigned)((p.N + 32 * v - 1) / (32 * v)), (unsigned)parts), block(32, 8);
-  if (p.bf16) {
+  if (p.glu) {
+    if (p.bf16)
+      (v == 1 ? glu_dpre_kernel<__nv_bfloat16, 1> : glu_dpre_kernel<__nv_bfloat16, 8>)<<<grid, block, 0, s>>>(p);
+    else
+      (v == 1 ? glu_dpre_kernel<float, 1> : glu_dpre_kernel<float, 4>)<<<grid, block, 0, s>>>(p);
+  } else if (p.bf16) {
     if (v == 1)
       dpre_kernel<__nv_bfloat16, 1><<<grid, block, 0, s>>>(p);
     else
@@ -520,7 +635,7 @@ cudaError_t launch_dpre(const DpreArgs &p, cudaStream_t s) {
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.dbias) return e;
-  return launch_column_sum(p.partial, p.dbias, parts, p.N, s);
+  return launch_column_sum(p.partial, p.dbias, parts, (p.glu ? 2 : 1) * p.N, s);
 }
 
 namespace {
@@ -548,7 +663,7 @@ bool small_bwd_fits(int64_t M, int64_t N, int64_t K) {
 
 cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, const void *pre, void *dx, void *dw,
                              float *dbias, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
-                             cudaStream_t s) {
+                             bool glu, cudaStream_t s) {
   using T = __nv_bfloat16;
   SmallBwd p{};
   p.dout = static_cast<const T *>(dout), p.pre = static_cast<const T *>(pre);
@@ -561,7 +676,8 @@ cudaError_t launch_small_bwd(const void *x, const void *w, const void *dout, con
   if (tiles == 0) return cudaSuccess;
   // of all gradients' tiles, whichever are wanted, so that each has the same value
   p.cs = small_bwd_cluster(tiles_of(M, K) + tiles_of(N, K), max(M, N));
-  return chain_launch(small_bwd_kernel, dim3((unsigned)(tiles * p.cs)), dim3(256), 0, p.cs, true, s, p);
+  return chain_launch(glu ? small_bwd_kernel<true> : small_bwd_kernel<false>, dim3((unsigned)(tiles * p.cs)), dim3(256),
+                      0, p.cs, true, s, p);
 }
 
 }  // namespace delta

@@ -3,6 +3,10 @@
 //   pre = acc * x_scale[m] * w_scale[n] + bias[n]      (scales: 8-bit operands)
 //   out = act(pre) + residual
 //
+// and of the gated layer, whose w has a half of N rows for the gate g and one for u:
+//
+//   pre = (acc_g + bias[n], acc_u + bias[N + n]),   out = act(pre_g) pre_u
+//
 // in float32 throughout; pre and out are rounded once, when they are stored.
 #pragma once
 
@@ -69,6 +73,17 @@ __device__ __forceinline__ void finish(const LinearArgs &a, int64_t m, int64_t n
   float o = activate(a.act, pre);
   if (a.residual) o += to_f(static_cast<const Out *>(a.residual)[m * a.ldr + n]);
   from_f(o, static_cast<Out *>(a.out)[m * a.N + n]);
+}
+
+// the same of the gated layer: the sums of both halves
+template <typename Out>
+__device__ __forceinline__ void finish_glu(const LinearArgs &a, int64_t m, int64_t n, float gate, float up) {
+  gate += bias_at(a, n), up += bias_at(a, a.N + n);
+  if (a.pre) {
+    from_f(gate, static_cast<Out *>(a.pre)[m * 2 * a.N + n]);
+    from_f(up, static_cast<Out *>(a.pre)[m * 2 * a.N + a.N + n]);
+  }
+  from_f(activate(a.act, gate) * up, static_cast<Out *>(a.out)[m * a.N + n]);
 }
 
 }  // namespace linear

@@ -1,6 +1,6 @@
 // linear_tc.cu -- the linear layer's matrix products on the 5th-generation
 // tensor cores, D[M][N] = sum_k A(m, k) B(n, k), with the epilogue of
-// linear.cuh.  The forward takes x and w with k contiguous; the gradients take
+// linear.cuh, or that of the gated layer, D's columns in two halves (kGlu).  The forward takes x and w with k contiguous; the gradients take
 // them as they lie, with k as the row (w for dx, both operands for dw), which
 // the shared-memory descriptors express as MN-major operands, so nothing is
 // transposed in memory.
@@ -255,6 +255,88 @@ __device__ __forceinline__ void finish_column(const LinearArgs &e, const float *
   }
 }
 
+// The gated form (kGlu): a tile's left half of columns are rows of w's gate half, its
+// right half the same rows of the other half, so that one thread finds both in its row
+// of TMEM: out = act(g + bg) (u + bu), pre [M][2 N] = g + bg beside u + bu.
+// One chunk of one row; cols: the chunk's biases, the gate's [32] and the other's [32].
+__device__ __forceinline__ void finish_row_glu(const LinearArgs &e, int64_t m, int64_t n0, const uint32_t (&g)[32],
+                                               const uint32_t (&u)[32], const float *cols, bool wide) {
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + m * e.N + n0;
+  __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(e.pre) + m * 2 * e.N + n0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint4 po[2], pg[2], pu[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8], w[8], q[8];
+      const int at = 16 * k + 8 * h;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(g[at + i]), w[i] = __uint_as_float(u[at + i]);
+      if (e.bias) {
+        load8(cols + at, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += q[i];
+        load8(cols + 32 + at, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] += q[i];
+      }
+      pg[h] = narrow8(v), pu[h] = narrow8(w);
+      activate8(e, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= w[i];
+      po[h] = narrow8(v);
+    }
+    if (n0 + 16 * k + 16 <= e.N) {
+      if (e.pre) {
+        store16(pre + 16 * k, pg[0], pg[1], wide);
+        store16(pre + e.N + 16 * k, pu[0], pu[1], wide);
+      }
+      store16(out + 16 * k, po[0], po[1], wide);
+    } else if (n0 + 16 * k + 8 <= e.N) {
+      if (e.pre) {
+        *reinterpret_cast<uint4 *>(pre + 16 * k) = pg[0];
+        *reinterpret_cast<uint4 *>(pre + e.N + 16 * k) = pu[0];
+      }
+      *reinterpret_cast<uint4 *>(out + 16 * k) = po[0];
+    }
+  }
+}
+// The same where rows are not whole 16-byte pieces: what each lane has of its row is
+// turned through shared memory, and a lane stores one column of all 32 rows.
+__device__ __forceinline__ void finish_columns_glu(const LinearArgs &e, float *stage, int lane, int64_t m0, int64_t n0,
+                                                   uint32_t (&g)[32], uint32_t (&u)[32]) {
+  const int64_t n = n0 + lane;
+  const float bg = n < e.N ? linear::bias_at(e, n) : 0.f, bu = n < e.N ? linear::bias_at(e, e.N + n) : 0.f;
+  const int rows = e.M - m0 < 32 ? (int)(e.M - m0) : 32;
+  const auto turn = [&](const uint32_t(&r)[32]) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<uint4 *>(stage + lane * kPitch + 4 * k) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+    __syncwarp();
+  };
+  // after this g and u are this lane's column
+  turn(g);
+#pragma unroll
+  for (int r = 0; r < 32; ++r) g[r] = __float_as_uint(stage[r * kPitch + lane] + bg);
+  turn(u);
+#pragma unroll
+  for (int r = 0; r < 32; ++r) u[r] = __float_as_uint(stage[r * kPitch + lane] + bu);
+  if (n >= e.N) return;
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + m0 * e.N + n;
+  __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(e.pre) + m0 * 2 * e.N + n;
+#pragma unroll
+  for (int r = 0; r < 32; ++r) {
+    if (r >= rows) break;
+    const float a = __uint_as_float(g[r]), b = __uint_as_float(u[r]);
+    if (e.pre) {
+      pre[(int64_t)r * 2 * e.N] = __float2bfloat16_rn(a);
+      pre[(int64_t)r * 2 * e.N + e.N] = __float2bfloat16_rn(b);
+    }
+    out[(int64_t)r * e.N] = __float2bfloat16_rn(linear::activate(e.act, a) * b);
+  }
+}
+
 // A tile whose k was shared by `split` CTAs of the cluster, `apart` ranks from
 // one another: each has its float32 sums in its own shared memory ([kBM] rows
 // of BN + 4), and finishes 1 / split of the rows, adding in rank order.
@@ -299,12 +381,65 @@ __device__ __forceinline__ void finish_split(const LinearArgs &e, const float *s
   }
 }
 
-template <int BN, bool kPair, bool kSplit, bool kAMn, bool kBMn, bool kF8>
+// The same for the gated form: 8 columns of either half a thread.
+template <int BN>
+__device__ __forceinline__ void finish_split_glu(const LinearArgs &e, const float *sums, int split, int apart, int rank,
+                                                 int64_t m0, int64_t n0, bool aligned) {
+  const int rows = kBM / split, mine = rank / apart, first = rank % apart;
+  for (int i = threadIdx.x; i < rows * (BN / 16); i += kThreads) {
+    const int r = mine * rows + i / (BN / 16), c = i % (BN / 16) * 8;
+    const int64_t row = m0 + r, n = n0 + c;
+    if (row >= e.M || n >= e.N) continue;
+    float v[2][8] = {};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float4 a[kMaxSplit], b[kMaxSplit];
+#pragma unroll
+      for (int q = 0; q < kMaxSplit; ++q)
+        if (q < split) {
+          const uint32_t at = map_cluster(sums + r * (BN + 4) + half * (BN / 2) + c, first + q * apart);
+          a[q] = ld_cluster_f4(at);
+          b[q] = ld_cluster_f4(at + 16);
+        }
+#pragma unroll
+      for (int q = 0; q < kMaxSplit; ++q)
+        if (q < split) {
+          v[half][0] += a[q].x, v[half][1] += a[q].y, v[half][2] += a[q].z, v[half][3] += a[q].w;
+          v[half][4] += b[q].x, v[half][5] += b[q].y, v[half][6] += b[q].z, v[half][7] += b[q].w;
+        }
+    }
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (n + j < e.N) v[0][j] += linear::bias_at(e, n + j), v[1][j] += linear::bias_at(e, e.N + n + j);
+      o[j] = linear::activate(e.act, v[0][j]) * v[1][j];
+    }
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + row * e.N + n;
+    __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(e.pre) + row * 2 * e.N + n;
+    if (aligned) {
+      if (e.pre) {
+        *reinterpret_cast<uint4 *>(pre) = narrow8(v[0]);
+        *reinterpret_cast<uint4 *>(pre + e.N) = narrow8(v[1]);
+      }
+      *reinterpret_cast<uint4 *>(out) = narrow8(o);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (n + j >= e.N) continue;
+        if (e.pre) pre[j] = __float2bfloat16_rn(v[0][j]), pre[e.N + j] = __float2bfloat16_rn(v[1][j]);
+        out[j] = __float2bfloat16_rn(o[j]);
+      }
+    }
+  }
+}
+
+template <int BN, bool kPair, bool kSplit, bool kAMn, bool kBMn, bool kF8, bool kGlu>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                 Tiles tiles, LinearArgs epi, bool aligned, bool wide) {
   constexpr int kStages = stages(BN, kPair), kStage = stage_bytes(BN, kPair), kBRows = b_rows(BN, kPair);
   constexpr int kTM = kPair ? 2 * kBM : kBM;             // rows of a tile
+  constexpr int kOut = kGlu ? BN / 2 : BN;               // columns of the output that a tile gives
   constexpr int kElems = kF8 ? 128 : 64;                 // of k in a stage
   constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;  // TMEM columns: two accumulators
   extern __shared__ unsigned char raw[];
@@ -359,7 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = worker; ok && i < tiles.total; i += workers) {
       int64_t tm, tn;
       tile_at(tiles, i, tm, tn);
-      const int m0 = (int)(tm * kTM) + rank * kBM, n0 = (int)(tn * BN) + rank * kBRows;
+      // (gated: w's halves are tiles' halves, so a pair's second CTA has the second)
+      const int m0 = (int)(tm * kTM) + rank * kBM;
+      const int n0 = (int)(tn * kOut) + rank * (kGlu ? (int)epi.N : kBRows);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = __all_sync(0xffffffffu, wait(&sh, &sh.empty[slot], phase ^ 1, 0)))) break;
         if (elect_one()) {
@@ -382,6 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kBMn) {
 #pragma unroll
             for (int j = 0; j < kBRows / 64; ++j) copy(stb + j * 8192, &mb, n0 + 64 * j, kb * 64);
+          } else if constexpr (kGlu && !kPair) {
+            copy(stb, &mb, kb * kElems, n0);
+            copy(stb + kOut * kRowBytes, &mb, kb * kElems, (int)epi.N + n0);
           } else {
             copy(stb, &mb, kb * kElems, n0);
           }
@@ -459,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = worker; i < tiles.total; i += workers) {
       int64_t tm, tn;
       tile_at(tiles, i, tm, tn);
-      const int64_t m0 = tm * kTM + rank * kBM + quarter * 32, m = m0 + lane, n0 = tn * BN;
-      const int chunks = (int)(epi.N - n0 < BN ? (epi.N - n0 + 31) / 32 : BN / 32);
+      const int64_t m0 = tm * kTM + rank * kBM + quarter * 32, m = m0 + lane, n0 = tn * kOut;
+      const int chunks = (int)(epi.N - n0 < kOut ? (epi.N - n0 + 31) / 32 : kOut / 32);
       // what a chunk needs from memory is asked for a chunk ahead; a lane has
       // the bias and scale of one column, which shared memory hands to all
       const bool rows = aligned && !kSplit;
@@ -468,11 +608,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       Residual now, next;
       const auto ask = [&](int c) {
         if (!rows || c >= chunks) return;
-        ask_residual(epi, m, n0 + c * 32, wide, next);
+        if constexpr (!kGlu) ask_residual(epi, m, n0 + c * 32, wide, next);
         const int64_t n = n0 + c * 32 + lane;
         if (n < epi.N) {
           bias = linear::bias_at(epi, n);
-          if (epi.x_scale) sw = epi.w_scale[n];
+          if constexpr (kGlu)
+            sw = linear::bias_at(epi, epi.N + n);  // (the other half's)
+          else if (epi.x_scale)
+            sw = epi.w_scale[n];
         }
       };
       if (rows && epi.x_scale && m < epi.M) sx = epi.x_scale[m];
@@ -491,24 +634,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sh.tempty[acc]);
         }
       };
-      uint32_t r[32];
+      uint32_t r[32], r2[kGlu ? 32 : 1];
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + c * 32), r);
+        if constexpr (kGlu) tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + kOut + c * 32), r2);
         if (rows) {
           if (epi.bias) stage[lane] = bias;
-          if (epi.x_scale) stage[32 + lane] = sw;
+          if (kGlu ? epi.bias != nullptr : epi.x_scale != nullptr) stage[32 + lane] = sw;
           __syncwarp();
           now = next;
           ask(c + 2);
         }
         tmem_wait_ld_regs(r);
+        if constexpr (kGlu) tmem_wait_ld_regs(r2);
         if (c + 2 >= chunks) release();
         if constexpr (kSplit) {  // the one tile: its sums to shared memory, where the ring was
           float *row = reinterpret_cast<float *>(base) + (quarter * 32 + lane) * (BN + 4) + c * 32;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             *reinterpret_cast<uint4 *>(row + 4 * k) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          if constexpr (kGlu) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4 *>(row + kOut + 4 * k) =
+                  make_uint4(r2[4 * k], r2[4 * k + 1], r2[4 * k + 2], r2[4 * k + 3]);
+          }
+        } else if constexpr (kGlu) {
+          if (!aligned)
+            finish_columns_glu(epi, stage, lane, m0, n0 + c * 32, r, r2);
+          else if (m < epi.M)
+            finish_row_glu(epi, m, n0 + c * 32, r, r2, stage, wide);
         } else if (aligned) {
           if (m < epi.M) finish_row(epi, m, n0 + c * 32, r, sx, stage, now, wide);
         } else {
@@ -533,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     int64_t tm, tn;
     tile_at(tiles, worker, tm, tn);
-    finish_split<BN>(epi, reinterpret_cast<const float *>(base), tiles.split, kWide, crank, tm * kTM + rank * kBM,
-                     tn * BN, aligned);
+    (kGlu ? finish_split_glu<BN> : finish_split<BN>)(epi, reinterpret_cast<const float *>(base), tiles.split, kWide,
+                                                     crank, tm * kTM + rank * kBM, tn * kOut, aligned);
   }
   if constexpr (kPair || kSplit) cluster_sync_relaxed();  // no CTA leaves while another may reach into it
   tc_fence_after();
@@ -552,8 +708,9 @@ int sm_count() {
   return n;
 }
 
-template <int BN, bool kPair, bool kSplit, bool kAMn, bool kBMn, bool kF8>
+template <int BN, bool kPair, bool kSplit, bool kAMn, bool kBMn, bool kF8, bool kGlu>
 cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
+  constexpr int kOut = kGlu ? BN / 2 : BN;
   const int size = kF8 ? 1 : 2;
   const LinearArgs &e = g.epi;
   CUtensorMap ma, mb;
@@ -562,12 +719,13 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
              : make_map_2d_sw128(&ma, g.a, (uint64_t)g.K, (uint64_t)e.M, (uint64_t)g.lda, size, kBM);
   if (err != cudaSuccess) return err;
   err = kBMn ? make_map_2d_sw128(&mb, g.b, (uint64_t)e.N, (uint64_t)g.K, (uint64_t)g.ldb, size, 64)
-             : make_map_2d_sw128(&mb, g.b, (uint64_t)g.K, (uint64_t)e.N, (uint64_t)g.ldb, size, b_rows(BN, kPair));
+             : make_map_2d_sw128(&mb, g.b, (uint64_t)g.K, (uint64_t)(kGlu ? 2 : 1) * e.N, (uint64_t)g.ldb, size,
+                                 kGlu ? kOut : b_rows(BN, kPair));
   if (err != cudaSuccess) return err;
   Tiles t;
   constexpr int kTM = kPair ? 2 * kBM : kBM;
   t.m_tiles = (e.M + kTM - 1) / kTM;
-  t.n_tiles = (e.N + BN - 1) / BN;
+  t.n_tiles = (e.N + kOut - 1) / kOut;
   t.total = t.m_tiles * t.n_tiles;
   if (t.total >= (int64_t(1) << 31) / kMaxSplit) return cudaErrorInvalidConfiguration;
   const int elems = kF8 ? 128 : 64;
@@ -580,7 +738,7 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
   const auto ok32 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };
   const bool wide = aligned && e.N % 16 == 0 && ok32(e.out) && ok32(e.pre) && ok32(e.residual) &&
                     (!e.residual || e.ldr % 16 == 0);
-  auto kern = gemm_kernel<BN, kPair, kSplit, kAMn, kBMn, kF8>;
+  auto kern = gemm_kernel<BN, kPair, kSplit, kAMn, kBMn, kF8, kGlu>;
   constexpr int smem = smem_bytes(BN, kPair);
   if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
   const int64_t ctas = (kPair ? 2 : 1) * split, fit = sm_count() / ctas;
@@ -589,10 +747,10 @@ cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
                       (int)ctas, g.dependent, s, ma, mb, t, e, aligned, wide);
 }
 
-template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8>
+template <int BN, bool kPair, bool kAMn, bool kBMn, bool kF8, bool kGlu>
 cudaError_t run(const GemmArgs &g, int split, cudaStream_t s) {
-  return split > 1 ? run<BN, kPair, true, kAMn, kBMn, kF8>(g, split, s)
-                   : run<BN, kPair, false, kAMn, kBMn, kF8>(g, 1, s);
+  return split > 1 ? run<BN, kPair, true, kAMn, kBMn, kF8, kGlu>(g, split, s)
+                   : run<BN, kPair, false, kAMn, kBMn, kF8, kGlu>(g, 1, s);
 }
 
 // The tile and the split of k, by an estimate of the time.  A block of k takes
@@ -628,15 +786,15 @@ Choice choose(int64_t M, int64_t N, int64_t K, bool f8) {
   return c;
 }
 
-template <bool kAMn, bool kBMn, bool kF8>
+template <bool kAMn, bool kBMn, bool kF8, bool kGlu = false>
 cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
-  const Choice c = choose(g.epi.M, g.epi.N, g.K, kF8);
+  const Choice c = choose(g.epi.M, (kGlu ? 2 : 1) * g.epi.N, g.K, kF8);
   const int best = c.shape, split = c.split;
   switch (best) {
-    case 0: return run<256, true, kAMn, kBMn, kF8>(g, split, s);
-    case 1: return run<128, true, kAMn, kBMn, kF8>(g, split, s);
-    case 2: return run<128, false, kAMn, kBMn, kF8>(g, split, s);
-    default: return run<64, false, kAMn, kBMn, kF8>(g, split, s);
+    case 0: return run<256, true, kAMn, kBMn, kF8, kGlu>(g, split, s);
+    case 1: return run<128, true, kAMn, kBMn, kF8, kGlu>(g, split, s);
+    case 2: return run<128, false, kAMn, kBMn, kF8, kGlu>(g, split, s);
+    default: return run<64, false, kAMn, kBMn, kF8, kGlu>(g, split, s);
   }
 }
 
@@ -649,6 +807,8 @@ cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s) {
   if (!g.a_mn) return g.b_mn ? pick<false, true, false>(g, s) : pick<false, false, false>(g, s);
   return g.b_mn ? pick<true, true, false>(g, s) : cudaErrorNotSupported;
 }
+
+cudaError_t launch_glu_tc(const GemmArgs &g, cudaStream_t s) { return pick<false, false, false, true>(g, s); }
 
 cudaError_t read_and_clear_linear_error(unsigned int *word) {
   cudaError_t e = cudaMemcpyFromSymbol(word, g_linear_error, sizeof(unsigned int));
