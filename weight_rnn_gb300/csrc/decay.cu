@@ -278,30 +278,37 @@ cudaError_t generic(const DecayArgs &a, cudaStream_t s) {
 }
 
 // -------------------------------------------------------------------- joining
+// V neighbouring elements a thread; the segments' states are asked for kAhead at a time.
+template <int V>
 __global__ void __launch_bounds__(256) decay_join_kernel(float *states, const float *init, const float *decay,
-                                                         const int *lengths, int64_t T, int64_t H, int64_t seg,
-                                                         int nseg, bool reverse, int64_t n, int64_t blocks) {
-  const int64_t bh = blockIdx.x / blocks, e = (blockIdx.x % blocks) * 256 + threadIdx.x;
+                                                         const int *lengths, int64_t T, int H, int64_t seg, int nseg,
+                                                         bool reverse, int64_t n, int blocks) {
+  struct __align__(4 * V) Vec { float v[V]; };
+  constexpr int kAhead = 8;
+  const int bh = (int)(blockIdx.x / (unsigned)blocks);
+  const int64_t e = ((int64_t)(blockIdx.x % (unsigned)blocks) * 256 + threadIdx.x) * V;
   chain_wait();
   if (e >= n) return;
   int64_t len = lengths ? lengths[bh / H] : T;
   len = len < 0 ? 0 : len > T ? T : len;
-  const float lg = log2f(decay[bh % H]);
-  float carry = init ? init[bh * n + e] : 0.f;
-  float *at = states + bh * nseg * n + e;
-  constexpr int kAhead = 8;  // segments asked for at a time
+  const float lg = log2f(decay[bh % H]), whole = power(lg, seg);
+  Vec carry = {};
+  if (init) carry = *reinterpret_cast<const Vec *>(init + bh * n + e);
+  float *at = states + (int64_t)bh * nseg * n + e;
   for (int i0 = 0; i0 < nseg; i0 += kAhead) {
-    float own[kAhead];
+    Vec own[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (i0 + i < nseg) own[i] = at[(reverse ? nseg - 1 - i0 - i : i0 + i) * n];
+      if (i0 + i < nseg) own[i] = *reinterpret_cast<const Vec *>(at + (reverse ? nseg - 1 - i0 - i : i0 + i) * n);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= nseg) break;
-      const int64_t sg = reverse ? nseg - 1 - i0 - i : i0 + i;
-      const int64_t lo = sg * seg, hi = min(lo + seg, len);
-      at[sg * n] = carry;
-      carry = fmaf(power(lg, hi > lo ? hi - lo : 0), carry, own[i]);
+      const int sg = reverse ? nseg - 1 - i0 - i : i0 + i;
+      const int64_t have = len - sg * seg;  // tokens of the row from the segment's first on
+      const float keep = have >= seg ? whole : power(lg, have);
+      *reinterpret_cast<Vec *>(at + sg * n) = carry;
+#pragma unroll
+      for (int j = 0; j < V; ++j) carry.v[j] = fmaf(keep, carry.v[j], own[i].v[j]);
     }
   }
 }
@@ -322,10 +329,11 @@ cudaError_t launch_decay(const DecayArgs &a, cudaStream_t s) {
 
 cudaError_t launch_decay_join(float *states, const float *init, const DecayArgs &a, bool reverse, int64_t n,
                               cudaStream_t s) {
-  const int64_t blocks = (n + 255) / 256, grid = blocks * a.B * a.H;
+  const int V = n % 4 == 0 ? 4 : 1;  // (init and states are whole 16-byte pieces)
+  const int64_t blocks = (n / V + 255) / 256, grid = blocks * a.B * a.H;
   if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-  return chain_launch(decay_join_kernel, dim3((unsigned)grid), dim3(256), 0, 1, true, s, states, init, a.decay,
-                      a.lengths, a.T, a.H, a.seg, a.nseg, reverse, n, blocks);
+  return chain_launch(V == 4 ? decay_join_kernel<4> : decay_join_kernel<1>, dim3((unsigned)grid), dim3(256), 0, 1, true, s,
+                      states, init, a.decay, a.lengths, a.T, (int)a.H, a.seg, a.nseg, reverse, n, (int)blocks);
 }
 
 }  // namespace delta

@@ -25,16 +25,19 @@
 // (G, P, K', loads, stores) is work ahead of or behind it.
 //
 // Shared memory, 224 KB: two tiles each of Q, K and V (32 KB, 128-byte swizzle, as
-// two blocks of 64 channels), S.  A finished O is staged where its Q was and leaves
-// by TMA.  TMEM, all 512 columns: G (then P, packed over it), O, dS, K' hi and lo.
+// two blocks of 64 channels), S.  TMEM, all 512 columns: G (then P, packed over it), O,
+// dS, K' hi and lo.  O leaves from registers, a token a lane in 32-byte pieces: staged
+// for TMA where its Q was, it kept that tile for 2500 cycles more, and the ring's wait
+// for Q set the pace (6800 cycles a chunk).
 //
 // Warps (640 threads):
 //   0      TMA producer
-//   1      issues the products
-//   2      TMEM; stores finished tiles
-//   4-7    P from G
-//   8-11   K' from K, transposed on the way to TMEM; O to the staging tile
-//   12-19  the state: 64 value columns each half
+//   1      issues G and P V
+//   2      TMEM
+//   3      issues Q S and K'^T V
+//   4-11   P from G, and K' from K, transposed on the way to TMEM: half of the columns,
+//          of the tokens, each warpgroup
+//   12-19  the state, and O: 64 value columns each warpgroup
 //
 // Bound by HBM: 4 tensors of 32 KB a chunk.  Every mbarrier wait is bounded: a
 // timeout sets a device error word and the kernel winds down.
@@ -63,13 +66,13 @@ constexpr float kFloor = -100.f;   // log2 of the least c_p
 constexpr float kLogZero = -200.f; // log2 g of g = 0: any power of it vanishes, also over c_p
 
 struct TcPass {
-  CUtensorMap q, k, v, out;
+  CUtensorMap q, k, v;
   const float *init;
   float *final;
   __nv_bfloat16 *to;  // out
   float os, kvs;
   int dk, dv;
-  bool reverse, init_t;
+  bool reverse, init_t, wide;  // wide: out's rows are whole 32-byte pieces
 };
 struct TcArgs {
   TcPass pass[3];
@@ -80,24 +83,24 @@ struct TcArgs {
 };
 
 struct Shared {
-  uint64_t qfull[2], qempty[2], kfull[2], kempty[2], vfull[2], vempty[2], staged[2];
-  uint64_t gfull, pfull, ofull, oempty, dsfull, dsempty, kpfull, sfull, sempty, drain;
+  uint64_t qfull[2], qempty[2], kfull[2], kempty[2], vfull[2], vempty[2];
+  uint64_t gfull, pfull, ofull, oempty, dsfull, dsempty, kpfull, sfull, sempty, drain[2];
   uint32_t tmem;
   volatile int dead;
 };
 
-__device__ __noinline__ bool wait_slow(Shared *sh, uint64_t *bar, uint32_t parity, int role) {
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 63 && sh->dead) return false;
-  }
-  sh->dead = 1;
-  atomicCAS(&g_decay_error, 0u, (unsigned)(1 + role));
-  return false;
-}
-// by whole warps, so that they leave their loops together
+// By whole warps, so that they leave their loops together.  (Inline: a call here would
+// save what is live around it, 64 registers of state among them, at every place.)
 __device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity, int role) {
-  const bool ok = mbar_try_wait(bar, parity) || wait_slow(sh, bar, parity, role);
+  bool ok = true;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if ((i & 63) == 0 && (sh->dead || i == (1u << 22))) {
+      if (!sh->dead) atomicCAS(&g_decay_error, 0u, (unsigned)(1 + role));
+      sh->dead = 1;
+      ok = false;
+      break;
+    }
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -107,6 +110,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x128b.x8.b32"
@@ -114,6 +123,71 @@ __device__ __forceinline__ void tmem_st16x128b_x8(uint32_t taddr, const uint32_t
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// float32 pairs: one instruction for two elements
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pk(uint32_t a, uint32_t b) { return pk(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(pk(-1.f, -1.f)), "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t narrow2(uint64_t v) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+  return pack_bf16(a, b);
+}
+__device__ __forceinline__ uint64_t widen2(uint32_t u) { return pk(u << 16, u & 0xFFFF0000u); }
+
+// A lane's row of the state, up to 64 columns (a multiple of 8), between registers and
+// memory: 32 bytes at a time, or 16.  (Lanes' rows are apart, so an access takes as long
+// as it has lines, whatever its width: by single columns 64 of them took 8 us.)
+__device__ __forceinline__ void load_row(uint64_t (&S)[32], const float *from, int live) {
+  const bool wide = (reinterpret_cast<uintptr_t>(from) & 31u) == 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (8 * i < live) {
+      if (wide) {
+        asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
+                     : "=l"(S[4 * i]), "=l"(S[4 * i + 1]), "=l"(S[4 * i + 2]), "=l"(S[4 * i + 3])
+                     : "l"(from + 8 * i)
+                     : "memory");
+      } else {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(from + 8 * i);
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(from + 8 * i + 4);
+        S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = y.x, S[4 * i + 3] = y.y;
+      }
+    }
+}
+__device__ __forceinline__ void store_row(const uint64_t (&S)[32], float *to, int live) {
+  const bool wide = (reinterpret_cast<uintptr_t>(to) & 31u) == 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (8 * i < live) {
+      if (wide) {
+        asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(to + 8 * i), "l"(S[4 * i]), "l"(S[4 * i + 1]),
+                     "l"(S[4 * i + 2]), "l"(S[4 * i + 3])
+                     : "memory");
+      } else {
+        *reinterpret_cast<ulonglong2 *>(to + 8 * i) = make_ulonglong2(S[4 * i], S[4 * i + 1]);
+        *reinterpret_cast<ulonglong2 *>(to + 8 * i + 4) = make_ulonglong2(S[4 * i + 2], S[4 * i + 3]);
+      }
+    }
 }
 
 // byte offset of 16-byte piece `piece` (0..7) of a row of a 64-channel block
@@ -127,26 +201,26 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
   __shared__ Shared sh;
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  int64_t item = blockIdx.x;
-  const TcPass &p = a.pass[item % a.passes];
-  item /= a.passes;
-  const int sg = (int)(item % a.nseg);
-  item /= a.nseg;
-  const int c0 = (int)(item % a.groups) * kD;
-  const int64_t bh = item / a.groups;
-  const int b = (int)(bh / a.H), h = (int)(bh % a.H);
+  uint32_t item = blockIdx.x;
+  const TcPass &p = a.pass[item % (uint32_t)a.passes];
+  item /= (uint32_t)a.passes;
+  const int sg = (int)(item % (uint32_t)a.nseg);
+  item /= (uint32_t)a.nseg;
+  const int c0 = (int)(item % (uint32_t)a.groups) * kD;
+  const uint32_t bh = item / (uint32_t)a.groups;
+  const int b = (int)(bh / (uint32_t)a.H), h = (int)(bh % (uint32_t)a.H);
   if (c0 >= p.dv) return;
   const int dk = p.dk, cols = min(kD, p.dv - c0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 1);
-      mbar_init(&sh.kfull[i], 1), mbar_init(&sh.kempty[i], kStates ? 4 : 5);
-      mbar_init(&sh.vfull[i], 1), mbar_init(&sh.vempty[i], 1);
-      mbar_init(&sh.staged[i], 4);
+      mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 2);
+      mbar_init(&sh.kfull[i], 1), mbar_init(&sh.kempty[i], kStates ? 8 : 9);
+      mbar_init(&sh.vfull[i], 1), mbar_init(&sh.vempty[i], kStates ? 1 : 2);
     }
-    mbar_init(&sh.gfull, 1), mbar_init(&sh.pfull, 4), mbar_init(&sh.ofull, 1), mbar_init(&sh.oempty, 4);
-    mbar_init(&sh.dsfull, 1), mbar_init(&sh.dsempty, 8), mbar_init(&sh.kpfull, 4);
-    mbar_init(&sh.sfull, 8), mbar_init(&sh.sempty, 1), mbar_init(&sh.drain, 1);
+    mbar_init(&sh.gfull, 1), mbar_init(&sh.pfull, 8), mbar_init(&sh.ofull, 1), mbar_init(&sh.oempty, 8);
+    mbar_init(&sh.dsfull, 1), mbar_init(&sh.dsempty, 8), mbar_init(&sh.kpfull, 8);
+    mbar_init(&sh.sfull, 8), mbar_init(&sh.sempty, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.drain[i], 1);
     sh.dead = 0;
     fence_mbar_init();
   }
@@ -179,172 +253,120 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     for (int c = 0; c < chunks; ++c, ++issued) {
       const int slot = c & 1, t0 = start_of(c);
       const uint32_t phase = (uint32_t)(c >> 1) & 1u ^ 1u;
-      const auto load = [&](const CUtensorMap *map, uint32_t off, uint64_t *full, uint64_t *empty, int d0) {
-        if (!(ok = wait(&sh, empty, phase, 0))) return;
+      // (a tile of each, in the order in which they are wanted)
+#pragma unroll 1
+      for (int i = 0; ok && i < 3; ++i) {
+        if (kStates && i == 1) continue;
+        const CUtensorMap *map = i == 0 ? &p.k : i == 1 ? &p.q : &p.v;
+        uint64_t *full = i == 0 ? &sh.kfull[slot] : i == 1 ? &sh.qfull[slot] : &sh.vfull[slot];
+        uint64_t *empty = i == 0 ? &sh.kempty[slot] : i == 1 ? &sh.qempty[slot] : &sh.vempty[slot];
+        unsigned char *to = base + (i == 0 ? kOffK : i == 1 ? kOffQ : kOffV) + slot * kTile;
+        if (!(ok = wait(&sh, empty, phase, 0))) break;
         if (elect_one()) {
+          const int d0 = i == 2 ? c0 : 0;
           mbar_arrive_expect_tx(full, kTile);
-          tma_load_4d(base + off + slot * kTile, map, full, d0, h, t0, b);
-          tma_load_4d(base + off + slot * kTile + kBlk, map, full, d0 + 64, h, t0, b);
+          tma_load_4d(to, map, full, d0, h, t0, b);
+          tma_load_4d(to + kBlk, map, full, d0 + 64, h, t0, b);
         }
         __syncwarp();
-      };
-      load(&p.k, kOffK, &sh.kfull[slot], &sh.kempty[slot], 0);
-      if (!kStates && ok) load(&p.q, kOffQ, &sh.qfull[slot], &sh.qempty[slot], 0);
-      if (ok) load(&p.v, kOffV, &sh.vfull[slot], &sh.vempty[slot], c0);
+      }
       if (!ok) break;
     }
     // winding down: what is in flight lands first (a tile that was never asked
     // for lets its wait run out)
-    if (!ok)
+    if (!ok) {
+#pragma unroll 1
       for (int i = 0; i < 1000; ++i) __nanosleep(1000);
-  } else if (warp == 1) {
+    }
+  } else if (warp == 1 || warp == 3) {
     const uint32_t nv = (uint32_t)(cols + 15) & ~15u;
     const int ksteps = (dk + 15) / 16;
     const uint32_t id_g = idesc_bf16(kC, kC, false, false), id_v = idesc_bf16(128, (int)nv, false, true);
     bool ok = true;
     // K-major: 16 channels are 32 bytes of a 128-byte row
     const auto step_k = [](int k) { return (uint64_t)((k >> 2) * kBlk + (k & 3) * 32) >> 4; };
-    const auto product_g = [&](int c) {
-      const int slot = c & 1;
-      const uint32_t ph = (uint32_t)(c >> 1) & 1u;
-      if (!(ok = wait(&sh, &sh.qfull[slot], ph, 1) && wait(&sh, &sh.kfull[slot], ph, 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t dq = sdesc_sw128(smem_u32(base + kOffQ + slot * kTile), 0, 1024);
-        const uint64_t dkk = sdesc_sw128(smem_u32(base + kOffK + slot * kTile), 0, 1024);
-        for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kG, dq + step_k(k), dkk + step_k(k), id_g, k > 0);
-        mma_commit(&sh.gfull);
-        mma_commit(&sh.kempty[slot]);
-      }
-      __syncwarp();
-    };
-    if (!kStates && chunks > 0) product_g(0);
     for (int c = 0; ok && c < chunks; ++c) {
       const int slot = c & 1;
       const uint32_t ph = (uint32_t)(c >> 1) & 1u, one = (uint32_t)c & 1u;
-      if (!(ok = wait(&sh, &sh.vfull[slot], ph, 1) && wait(&sh, &sh.kpfull, one, 1) &&
-                 (c == 0 || wait(&sh, &sh.dsempty, one ^ 1u, 1))))
-        break;
-      tc_fence_after();
+      const uint64_t dq = sdesc_sw128(smem_u32(base + kOffQ + slot * kTile), 0, 1024);
       // MN-major: 16 tokens are 16 rows of 128 bytes
       const uint64_t dvv = sdesc_sw128(smem_u32(base + kOffV + slot * kTile), kBlk, 1024);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ts(tmem + kDs, tmem + kHi + 8 * k, dvv + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
-        if (two) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mma_ts(tmem + kDs, tmem + kLo + 8 * k, dvv + (uint64_t)(k * 2048 >> 4), id_v, true);
+      if (warp == 1) {
+        if constexpr (!kStates) {  // (G is written over P, which this warp's products before have read)
+          if (!(ok = wait(&sh, &sh.qfull[slot], ph, 1) && wait(&sh, &sh.kfull[slot], ph, 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t dkk = sdesc_sw128(smem_u32(base + kOffK + slot * kTile), 0, 1024);
+#pragma unroll 1
+            for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kG, dq + step_k(k), dkk + step_k(k), id_g, k > 0);
+            mma_commit(&sh.gfull);
+            mma_commit(&sh.kempty[slot]);
+            mma_commit(&sh.qempty[slot]);
+          }
+          __syncwarp();
+          // (sempty: Q S is in O; V has been waited for by the other issuer before)
+          if (!(ok = wait(&sh, &sh.pfull, one, 1) && wait(&sh, &sh.sempty, one, 1) && wait(&sh, &sh.vfull[slot], ph, 1)))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k)
+              mma_ts(tmem + kO, tmem + kG + 32 * (k >> 1) + 8 * (k & 1), dvv + (uint64_t)(k * 2048 >> 4), id_v, true);
+            mma_commit(&sh.ofull);
+            mma_commit(&sh.vempty[slot]);
+          }
+          __syncwarp();
         }
-        mma_commit(&sh.dsfull);
-        if (kStates) mma_commit(&sh.vempty[slot]);
-      }
-      __syncwarp();
-      if constexpr (!kStates) {
-        if (!(ok = wait(&sh, &sh.sfull, one, 1) && (c == 0 || wait(&sh, &sh.oempty, one ^ 1u, 1)))) break;
+      } else {
+        if (!(ok = wait(&sh, &sh.kpfull, one, 2) && wait(&sh, &sh.vfull[slot], ph, 2) &&
+                   (c == 0 || wait(&sh, &sh.dsempty, one ^ 1u, 2))))
+          break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t dq = sdesc_sw128(smem_u32(base + kOffQ + slot * kTile), 0, 1024);
-          const uint64_t ds = sdesc_sw128(smem_u32(base + kOffS), kBlk, 1024);
-          for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kO, dq + step_k(k), ds + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
-          mma_commit(&sh.sempty);
-        }
-        __syncwarp();
-        if (!(ok = wait(&sh, &sh.pfull, one, 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mma_ts(tmem + kO, tmem + kG + 8 * k, dvv + (uint64_t)(k * 2048 >> 4), id_v, true);
-          mma_commit(&sh.ofull);
+          const int parts = two ? 16 : 8;
+#pragma unroll 1
+          for (int k = 0; k < parts; ++k)  // hi's 8 steps of 16 tokens, lo's 8
+            mma_ts(tmem + kDs, tmem + kHi + 8 * k, dvv + (uint64_t)((k & 7) * 2048 >> 4), id_v, k > 0);
+          mma_commit(&sh.dsfull);
           mma_commit(&sh.vempty[slot]);
         }
         __syncwarp();
-        if (c + 1 < chunks) product_g(c + 1);
+        if constexpr (!kStates) {
+          if (!(ok = wait(&sh, &sh.sfull, one, 2) && (c == 0 || wait(&sh, &sh.oempty, one ^ 1u, 2)) &&
+                     wait(&sh, &sh.qfull[slot], ph, 2)))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ds = sdesc_sw128(smem_u32(base + kOffS), kBlk, 1024);
+#pragma unroll 1
+            for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kO, dq + step_k(k), ds + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
+            mma_commit(&sh.sempty);
+            mma_commit(&sh.qempty[slot]);
+          }
+          __syncwarp();
+        }
       }
     }
     if (!ok) {  // products in flight end before TMEM is given back
-      if (elect_one()) mma_commit(&sh.drain);
-      for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.drain, 0); ++j) {
+      uint64_t *drain = &sh.drain[warp >> 1];
+      if (elect_one()) mma_commit(drain);
+      for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(drain, 0); ++j) {
       }
     }
-  } else if (warp == 2) {
-    if constexpr (!kStates) {
-      for (int c = 0; c < chunks; ++c) {
-        const int slot = c & 1;
-        if (!wait(&sh, &sh.staged[slot], (uint32_t)(c >> 1) & 1u, 2)) break;
-        if (elect_one()) {
-          const unsigned char *from = base + kOffQ + slot * kTile;
-          const int t0 = start_of(c);
-          // 4-D tiled store of a block of 64 channels; past the tensor's end nothing is written
-          for (int k = 0; 64 * k < cols; ++k)
-            asm volatile(
-                "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
-                    reinterpret_cast<uint64_t>(&p.out)),
-                "r"(smem_u32(from + k * kBlk)), "r"(c0 + 64 * k), "r"(h), "r"(t0), "r"(b)
-                : "memory");
-          bulk_commit();
-          bulk_wait_read0();
-          mbar_arrive(&sh.qempty[slot]);
-        }
-        __syncwarp();
-      }
-      bulk_wait0();  // (of the lane that issued them; the others have none)
-    }
-  } else if (warp >= 4 && warp < 8) {
-    if constexpr (!kStates) {
-      const int quarter = warp & 3, row = quarter * 32 + lane;
-      for (int c = 0; c < chunks; ++c) {
-        const int n = min(kC, t_end - start_of(c));
-        if (!wait(&sh, &sh.gfull, (uint32_t)c & 1u, 3)) break;
-        tc_fence_after();
-        // P = G 2^(lg |row - j| - log2 c_row); the difference of places is taken first,
-        // so that a steep lg does not cancel
-        const float cp = fmaxf(lg * (float)(p.reverse ? n - 1 - row : row + 1), kFloor);
-        const float slope = p.reverse ? -lg : lg;
-#pragma unroll 1
-        for (int j0 = 0; j0 < kC; j0 += 32) {
-          uint32_t out[16];
-          // (whole warps: these columns are past every row of the warp, or before)
-          const bool none = p.reverse ? j0 + 31 < quarter * 32 || j0 >= n : j0 > quarter * 32 + 31;
-          if (none) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) out[i] = 0u;
-          } else {
-            uint32_t g[32];
-            tmem_ld32(tmem_addr(tmem, quarter * 32, kG + j0), g);
-            tmem_wait_ld_regs(g);
-            const int lo = p.reverse ? row : 0, hi = p.reverse ? n - 1 : row;  // columns lo..hi count
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float v[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int j = j0 + 2 * i + e;
-                const float w = ex2(fmaf(slope, (float)row - (float)j, -cp)) * p.kvs;
-                v[e] = j >= lo && j <= hi ? __uint_as_float(g[2 * i + e]) * w : 0.f;
-              }
-              out[i] = pack_bf16(v[0], v[1]);
-            }
-          }
-          // over columns of G that this warp has read
-          tmem_st16(tmem_addr(tmem, quarter * 32, kG + j0 / 2), out);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pfull);
-      }
-    }
-  } else if (warp >= 8 && warp < 12) {
-    const int quarter = warp & 3, row = quarter * 32 + lane;
-    bool ok = true;
-    const auto keys = [&](int c) {  // K' of chunk c
+  } else if (warp >= 4 && warp < 12) {
+    const int quarter = warp & 3, half = (warp - 4) / 4;
+    const int row = quarter * 32 + lane;
+    uint64_t w[8];  // weights of this lane's tokens in a chunk of `weighed` tokens
+    int weighed = -1;
+    // K' of chunk c: this warp's 32 channels, half of the tokens
+    const auto keys = [&](int c) {
       const int slot = c & 1, n = min(kC, t_end - start_of(c));
       const uint32_t ph = (uint32_t)(c >> 1) & 1u;
-      if (!(ok = wait(&sh, &sh.kfull[slot], ph, 4))) return;
+      if (!wait(&sh, &sh.kfull[slot], ph, 4)) return false;
       if (n < kC) {
         // tokens past the row's end: their values take no part, whatever they are
-        if (!(ok = wait(&sh, &sh.vfull[slot], ph, 4))) return;
-        for (int r = n + quarter; r < kC; r += 4)
+        if (!wait(&sh, &sh.vfull[slot], ph, 4)) return false;
+        for (int r = n + warp - 4; r < kC; r += 8)
           if (lane < 16)
             *reinterpret_cast<uint4 *>(base + kOffV + slot * kTile + (lane >> 3) * kBlk + r * 128 + (lane & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -354,101 +376,144 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       // lane / 4 of tokens 2 (lane % 4) and the next one.  That is what a 16-lane
       // store to TMEM takes, tokens 8 i.. in register pair i.
       const uint32_t tile = smem_u32(base + kOffK + slot * kTile);
+      if (n != weighed) {  // (at most two lengths: whole chunks, and the last)
+        weighed = n;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = half * 64 + i * 8 + 2 * (lane & 3);
+          w[i] = p.reverse ? pk(ex2(lg * (float)(j + 1)) * p.kvs, ex2(lg * (float)(j + 2)) * p.kvs)
+                           : pk(ex2(lg * (float)max(n - 1 - j, 0)) * p.kvs, ex2(lg * (float)max(n - 2 - j, 0)) * p.kvs);
+        }
+      }
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {       // of the tokens
-#pragma unroll 1
-        for (int d16 = 0; d16 < 2; ++d16) {        // of the warp's 32 channels
-          const uint32_t ch = (uint32_t)(quarter * 32 + d16 * 16 + ((lane >> 3) & 1) * 8);
-          uint32_t hi[16], lo[16];
+      for (int d16 = 0; d16 < 2; ++d16) {  // of the warp's 32 channels
+        const uint32_t ch = (uint32_t)(quarter * 32 + d16 * 16 + ((lane >> 3) & 1) * 8);
+        const uint32_t from = tile + (ch >> 6) * kBlk;
+        uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {            // 16 tokens
-            const uint32_t tok = (uint32_t)(half * 64 + i * 16 + (lane >> 4) * 8 + (lane & 7));
-            uint32_t x[4];
-            ldsm_x4_trans(tile + (ch >> 6) * kBlk + piece_at(tok, (ch & 63) >> 3), x);
+        for (int i = 0; i < 4; ++i) {      // 16 tokens
+          const uint32_t tok = (uint32_t)(half * 64 + i * 16 + (lane >> 4) * 8 + (lane & 7));
+          uint32_t x[4];
+          ldsm_x4_trans(from + piece_at(tok, (ch & 63) >> 3), x);
+          if (n < kC) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const int j = half * 64 + i * 16 + g * 8 + 2 * (lane & 3);
-              float w[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                w[e] = ex2(lg * (float)(p.reverse ? j + e + 1 : n - 1 - j - e)) * p.kvs;
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t u = x[2 * g + y];
-                const float k0 = j < n ? __uint_as_float(u << 16) * w[0] : 0.f;
-                const float k1 = j + 1 < n ? __uint_as_float(u & 0xFFFF0000u) * w[1] : 0.f;
-                const uint32_t top = pack_bf16(k0, k1);
-                hi[4 * i + 2 * g + y] = top;
-                lo[4 * i + 2 * g + y] =
-                    pack_bf16(k0 - __uint_as_float(top << 16), k1 - __uint_as_float(top & 0xFFFF0000u));
-              }
+            for (int g = 0; g < 4; ++g) {
+              const int j = half * 64 + i * 16 + (g >> 1) * 8 + 2 * (lane & 3);
+              x[g] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
             }
           }
-          tmem_st16x128b_x8(tmem_addr(tmem, quarter * 32 + d16 * 16, kHi + half * 32), hi);
-          if (two) tmem_st16x128b_x8(tmem_addr(tmem, quarter * 32 + d16 * 16, kLo + half * 32), lo);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint64_t v = mul2(widen2(x[g]), w[2 * i + (g >> 1)]);
+            hi[4 * i + g] = narrow2(v);
+            lo[4 * i + g] = narrow2(sub2(v, widen2(hi[4 * i + g])));
+          }
         }
+        if (d16 == 0 && c > 0) {  // the K' before has been read
+          if (!wait(&sh, &sh.dsfull, (uint32_t)(c - 1) & 1u, 4)) return false;
+          tc_fence_after();
+        }
+        tmem_st16x128b_x8(tmem_addr(tmem, quarter * 32 + d16 * 16, kHi + half * 32), hi);
+        if (two) tmem_st16x128b_x8(tmem_addr(tmem, quarter * 32 + d16 * 16, kLo + half * 32), lo);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.kpfull), mbar_arrive(&sh.kempty[slot]);
+      return true;
     };
-    if (chunks > 0) keys(0);
-    for (int c = 0; ok && c < chunks; ++c) {
-      if (c + 1 < chunks) {
-        if (!wait(&sh, &sh.dsfull, (uint32_t)c & 1u, 4)) break;  // K' has been read
-        tc_fence_after();
-        keys(c + 1);
-        if (!ok) break;
-      }
-      if constexpr (!kStates) {
-        const int slot = c & 1, n = min(kC, t_end - start_of(c));
-        if (!wait(&sh, &sh.ofull, (uint32_t)c & 1u, 4)) break;
-        tc_fence_after();
-        const float cp = row < n ? p.os * ex2(fmaxf(lg * (float)(p.reverse ? n - 1 - row : row + 1), kFloor)) : 0.f;
-        unsigned char *to = base + kOffQ + slot * kTile;
+    const bool steep = lg < -16.f;  // 2^(-7 lg) would leave float32's range
+    uint64_t c2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c2[i] = p.reverse ? pk(ex2(-lg * (float)(7 - 2 * i)), ex2(-lg * (float)(6 - 2 * i)))
+                        : pk(ex2(-lg * (float)(2 * i)), ex2(-lg * (float)(2 * i + 1)));
+    // P of chunk c: this lane's row, every second block of 32 columns
+    const auto scores = [&](int c) {
+      const int n = min(kC, t_end - start_of(c));
+      if (!wait(&sh, &sh.gfull, (uint32_t)c & 1u, 3)) return false;
+      tc_fence_after();
+      // P = G 2^(lg |row - j| - log2 c_row).  The power is taken for one column of
+      // eight, the one furthest from the row's own, and times eight constants 2^(-lg i):
+      // below 2^-126 it is nothing beside the row's own 2^-log2 c_row.
+      const float cp = fmaxf(lg * (float)(p.reverse ? n - 1 - row : row + 1), kFloor);
+      const int lo = p.reverse ? row : 0, hi = p.reverse ? n - 1 : row;  // the columns that count
 #pragma unroll 1
-        for (int j0 = 0; j0 < cols; j0 += 32) {
-          uint32_t o[32];
-          tmem_ld32(tmem_addr(tmem, quarter * 32, kO + j0), o);
-          tmem_wait_ld_regs(o);
+      for (int i16 = 0; i16 < 4; ++i16) {  // 16 columns of the blocks half and half + 2
+        const int blk = half * 32 + (i16 >> 1) * 64, j0 = blk + (i16 & 1) * 16;
+        uint32_t out[8];
+        // (whole warps: these columns are past every row of the warp, or before)
+        const bool none = p.reverse ? j0 + 15 < quarter * 32 || j0 >= n : j0 > quarter * 32 + 31;
+        if (none) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 8; ++i) out[i] = 0u;
+        } else {
+          uint32_t g[16];
+          tmem_ld16(tmem_addr(tmem, quarter * 32, kG + j0), g);
+          tmem_wait_ld_regs(g);
+          if (steep) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = __uint_as_float(o[8 * i + 2 * e]) * cp, y = __uint_as_float(o[8 * i + 2 * e + 1]) * cp;
-              w[e] = row < n ? pack_bf16(x, y) : 0u;
+            for (int i = 0; i < 16; ++i) {
+              const float apart = p.reverse ? (float)(j0 + i - row) : (float)(row - j0 - i);
+              g[i] = __float_as_uint(__uint_as_float(g[i]) * (ex2(fmaf(lg, apart, -cp)) * p.kvs));
             }
-            *reinterpret_cast<uint4 *>(to + (j0 >> 6) * kBlk + piece_at(row, ((j0 & 63) >> 3) + i)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int b8 = 0; b8 < 2; ++b8) {
+              const int j = j0 + 8 * b8 + (p.reverse ? 7 : 0);
+              const float first = ex2(fmaf(lg, (float)(p.reverse ? j - row : row - j), -cp)) * p.kvs;
+              const uint64_t f2 = pk(first, first);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint64_t v = mul2(pk(g[8 * b8 + 2 * i], g[8 * b8 + 2 * i + 1]), mul2(f2, c2[i]));
+                asm("mov.b64 {%0, %1}, %2;" : "=r"(g[8 * b8 + 2 * i]), "=r"(g[8 * b8 + 2 * i + 1]) : "l"(v));
+              }
+            }
           }
+          // (most pieces have no columns that do not count)
+          if (p.reverse ? j0 < quarter * 32 + 31 || j0 + 15 >= n : j0 + 15 > quarter * 32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (j0 + i < lo || j0 + i > hi) g[i] = 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
         }
-        tc_fence_before();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.oempty), mbar_arrive(&sh.staged[slot]);
+        // over columns of the block that this warp has read
+        tmem_st8(tmem_addr(tmem, quarter * 32, kG + blk + (i16 & 1) * 8), out);
       }
-    }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pfull);
+      return true;
+    };
+    for (int c = 0; c < chunks; ++c)
+      if (!keys(c) || (!kStates && !scores(c))) break;
   } else if (warp >= 12) {
     const int quarter = warp & 3, d = quarter * 32 + lane, half = (warp - 12) / 4;
     const int v0 = c0 + half * 64, live = d < dk ? min(64, p.dv - v0) : 0;  // this lane's columns of the state
     const int64_t n_state = (int64_t)dk * p.dv;
-    float S[64];
+    uint64_t S[32];  // pairs of columns
 #pragma unroll
-    for (int i = 0; i < 64; ++i) S[i] = 0.f;
+    for (int i = 0; i < 32; ++i) S[i] = 0;
     if (!kStates && p.init) {
-      const float *from = p.init + (a.nseg > 1 ? bh * a.nseg + sg : bh) * n_state;
+      const float *from = p.init + (a.nseg > 1 ? (int64_t)bh * a.nseg + sg : bh) * n_state;
+      if (p.init_t) {
+        from += (int64_t)v0 * dk + d;
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (i < live) S[i] = p.init_t ? from[(int64_t)(v0 + i) * dk + d] : from[(int64_t)d * p.dv + v0 + i];
+        for (int i = 0; i < 32; ++i, from += 2 * dk)  // (an even number of columns)
+          if (2 * i < live) S[i] = pk(from[0], from[dk]);
+      } else {
+        from += (int64_t)d * p.dv + v0;
+        load_row(S, from, live);
+      }
     }
     const auto publish = [&] {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         *reinterpret_cast<uint4 *>(base + kOffS + half * kBlk + piece_at(d, i)) =
-            make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
-                       pack_bf16(S[8 * i + 4], S[8 * i + 5]), pack_bf16(S[8 * i + 6], S[8 * i + 7]));
+            make_uint4(narrow2(S[4 * i]), narrow2(S[4 * i + 1]), narrow2(S[4 * i + 2]), narrow2(S[4 * i + 3]));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sfull);
@@ -458,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     for (int c = 0; c < chunks; ++c) {
       const int n = min(kC, t_end - start_of(c));
       const float keep = exp2f(lg * (float)n);
+      const uint64_t keep2 = pk(keep, keep);
       if (!(ok = wait(&sh, &sh.dsfull, (uint32_t)c & 1u, 5))) break;
       tc_fence_after();
 #pragma unroll
@@ -466,28 +532,56 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         tmem_ld16(tmem_addr(tmem, quarter * 32, kDs + half * 64 + 16 * j), r);
         tmem_wait_ld_regs(r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[16 * j + i] = fmaf(keep, S[16 * j + i], __uint_as_float(r[i]));
+        for (int i = 0; i < 8; ++i) S[8 * j + i] = fma2(keep2, S[8 * j + i], pk(r[2 * i], r[2 * i + 1]));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.dsempty);
-      if (!kStates && c + 1 < chunks) {
-        if (!(ok = wait(&sh, &sh.sempty, (uint32_t)c & 1u, 5))) break;
-        publish();
+      if constexpr (!kStates) {
+        if (c + 1 < chunks) {
+          if (!(ok = wait(&sh, &sh.sempty, (uint32_t)c & 1u, 5))) break;
+          publish();
+        }
+        // O, this half of its columns: a token a lane
+        if (!(ok = wait(&sh, &sh.ofull, (uint32_t)c & 1u, 5))) break;
+        tc_fence_after();
+        const int t0 = start_of(c), row = quarter * 32 + lane;
+        const float cp = p.os * ex2(fmaxf(lg * (float)(p.reverse ? n - 1 - row : row + 1), kFloor));
+        const uint64_t cp2 = pk(cp, cp);
+        __nv_bfloat16 *to = p.to + (((int64_t)b * a.T + t0 + row) * a.H + h) * p.dv + v0;
+        const int have = t0 + row < t_hi ? p.dv - v0 : 0;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[16], w[8];
+          tmem_ld16(tmem_addr(tmem, quarter * 32, kO + half * 64 + 16 * j), o);
+          tmem_wait_ld_regs(o);
+          if (j == 3) {  // O may be written again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.oempty);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = row < n ? narrow2(mul2(pk(o[2 * i], o[2 * i + 1]), cp2)) : 0u;
+          if (p.wide && 16 * j + 16 <= have) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * j), "r"(w[0]),
+                         "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+          } else {
+            if (16 * j + 8 <= have) *reinterpret_cast<uint4 *>(to + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (16 * j + 16 <= have) *reinterpret_cast<uint4 *>(to + 16 * j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
       }
     }
     if (ok && (kStates || (p.final && sg == (p.reverse ? 0 : a.nseg - 1)))) {
-      float *to = p.final + (kStates ? bh * a.nseg + sg : bh) * n_state + (int64_t)d * p.dv + v0;
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (i < live) to[i] = S[i];
+      float *to = p.final + (kStates ? (int64_t)bh * a.nseg + sg : bh) * n_state + (int64_t)d * p.dv + v0;
+      store_row(S, to, live);
     }
   }
   if constexpr (!kStates) {  // tokens past the row's end, in chunks that no tile reached
-    const int t0 = t_lo + chunks * kC, pieces = cols / 8;
-    for (int64_t e = threadIdx.x; e < (int64_t)(t_hi - t0) * pieces; e += kThreads)
-      *reinterpret_cast<uint4 *>(p.to + (((int64_t)b * a.T + t0 + e / pieces) * a.H + h) * p.dv + c0 + e % pieces * 8) =
-          make_uint4(0, 0, 0, 0);
+    for (int t = t_lo + chunks * kC + warp; t < t_hi; t += kThreads / 32)
+      if (lane < cols / 8)
+        *reinterpret_cast<uint4 *>(p.to + (((int64_t)b * a.T + t) * a.H + h) * p.dv + c0 + lane * 8) = make_uint4(0, 0, 0, 0);
   }
   __syncwarp();
   tc_fence_before();
@@ -521,14 +615,13 @@ cudaError_t run(const DecayArgs &a, cudaStream_t s) {
   for (int i = 0; i < a.passes; ++i) {
     const DecayPass &p = a.pass[i];
     TcPass &o = t.pass[i];
-    const int64_t whole[3] = {a.T * a.H * p.dv, a.H * p.dv, p.dv};
     cudaError_t e = make_map(&o.k, p.k, p.dk, a.H, a.T, a.B, p.ks);
     if (e == cudaSuccess) e = make_map(&o.v, p.v, p.dv, a.H, a.T, a.B, p.vs);
     if (e == cudaSuccess && !kStates) e = make_map(&o.q, p.q, p.dk, a.H, a.T, a.B, p.qs);
-    if (e == cudaSuccess && !kStates) e = make_map(&o.out, p.out, p.dv, a.H, a.T, a.B, whole);
     if (e != cudaSuccess) return e;
     o.init = p.init; o.final = p.final; o.to = static_cast<__nv_bfloat16 *>(p.out);
     o.os = p.os; o.kvs = p.kvs; o.dk = p.dk; o.dv = p.dv; o.reverse = p.reverse; o.init_t = p.init_t;
+    o.wide = p.dv % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     const int g = (p.dv + kD - 1) / kD;
     if (g > t.groups) t.groups = g;
   }
