@@ -27,6 +27,177 @@
 namespace delta {
 namespace {
 
+// ------------------------------------------------------------------ forward
+// blockDim (nt, rows a CTA); a thread's vectors are nt apart
+template <typename In, int V, int kPer, int kT, bool kQuant>
+__global__ void __launch_bounds__(kT, V *kPer <= 16 ? (kQuant ? kQuantThreads : kSmThreads) / kT : 1) norm_fwd_kernel(NormArgs p) {
+  __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
+  extern __shared__ __align__(16) unsigned char ring[];
+  const int nwarp = blockDim.x >> 5;
+  float w[kPer][V];
+  chain_wait();
+  load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  Rows<In, V, kPer, 2, kT> in;
+  in.base[0] = static_cast<const In *>(p.x); in.base[1] = static_cast<const In *>(p.residual);
+  in.ld[0] = p.ldx; in.ld[1] = p.ldr; in.rows = p.rows; in.D = p.D;
+  in.ring = ring;
+  in.start(first, step);
+  int buf = 0;
+  // every row of the CTA takes part in the barriers until the last is done
+  for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
+    in.turn(row, step);
+    float t[kPer][V], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool on = row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
+      const APack<In, V> xv = in.get(0, j), rv = in.get(1, j);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        t[j][i] = on ? to_f(xv.v[i]) + (p.residual ? to_f(rv.v[i]) : 0.f) : 0.f;
+        ss = fmaf(t[j][i], t[j][i], ss);
+      }
+    }
+    in.done();
+    ss = row_reduce<false>(ss, part[kQuant ? 0 : buf], nwarp);
+    const float rstd = rsqrtf(ss / (float)p.D + p.eps);
+    float inv = 1.f;
+    if constexpr (kQuant) {
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(t[j][i] * rstd * w[j][i]));
+      top = row_reduce<true>(top, part[1], nwarp);
+      // a row of zeros, or of values too small for a float32 scale: scale 1
+      float scale = top / kE4m3Max;
+      if (scale < 1.1754944e-38f) scale = 1.f;
+      inv = 1.f / scale;
+      if (row < p.rows && threadIdx.x == 0) p.scale[row] = scale;
+    }
+    if (row < p.rows) {
+      if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+        if (d >= p.D) continue;
+        if (p.sum) store_v<In, V>(static_cast<In *>(p.sum) + row * p.D + d, t[j]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[j][i] = t[j][i] * rstd * w[j][i] * inv;
+        if constexpr (kQuant)
+          store_e4m3<V>(static_cast<uint8_t *>(p.y) + row * p.D + d, t[j]);
+        else
+          store_v<In, V>(static_cast<In *>(p.y) + row * p.D + d, t[j]);
+      }
+    }
+  }
+  in.finish();
+}
+
+// ----------------------------------------------------------------- backward
+// The row is read from its ring twice, before and after the reduction, rather
+// than held: that is what lets two CTAs of 512 threads share an SM.
+template <typename In, int V, int kPer, int kT>
+__global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) norm_bwd_kernel(NormBwdArgs p) {
+  __shared__ float part[2][8 * 32];
+  extern __shared__ __align__(16) unsigned char ring[];
+  const int nwarp = blockDim.x >> 5;
+  chain_next();
+  chain_wait();
+  float w[kPer][V], dw[kPer][V];
+  load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  Rows<In, V, kPer, 3, kT> in;
+  in.base[0] = static_cast<const In *>(p.dy); in.base[1] = static_cast<const In *>(p.sum);
+  in.base[2] = static_cast<const In *>(p.dsum);
+  in.ld[0] = in.ld[1] = in.ld[2] = in.D = p.D; in.rows = p.rows;
+  in.ring = ring;
+  in.start(first, step);
+  float ahead = first < p.rows ? p.rstd[first] : 0.f;
+  int buf = 0;
+  for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
+    in.turn(row, step);
+    const float rstd = ahead;
+    if (row + step < p.rows) ahead = p.rstd[row + step];
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const APack<In, V> gv = in.get(0, j), tv = in.get(1, j);
+      if (row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D) {
+        if constexpr (V > 1) {
+          uint64_t sum = pk(0.f, 0.f);
+          const uint64_t rr = pk(rstd, rstd);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            const uint64_t t = mul2(pair_of(tv, i), rr), y = pair_of(gv, i);
+            unpk(fma2(y, t, pk(dw[j][2 * i], dw[j][2 * i + 1])), dw[j][2 * i], dw[j][2 * i + 1]);
+            sum = fma2(mul2(y, pk(w[j][2 * i], w[j][2 * i + 1])), t, sum);
+          }
+          float a, b;
+          unpk(sum, a, b);
+          dot += a + b;
+        } else {
+          const float t = to_f(tv.v[0]) * rstd, y = to_f(gv.v[0]);
+          dw[j][0] = fmaf(y, t, dw[j][0]);
+          dot = fmaf(y * w[j][0], t, dot);
+        }
+      }
+    }
+    dot = row_reduce<false>(dot, part[buf], nwarp) / (float)p.D;
+    if (row < p.rows) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
+        if (d >= p.D) continue;
+        const APack<In, V> gv = in.get(0, j), tv = in.get(1, j), sv = in.get(2, j);
+        float g[V];
+        // rstd (w dy - t^ dot) + dsum, with t^ = sum * rstd
+        const float c = -rstd * rstd * dot;
+        if constexpr (V > 1) {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            const uint64_t wy = mul2(pair_of(gv, i), pk(w[j][2 * i], w[j][2 * i + 1]));
+            const uint64_t low = p.dsum ? pair_of(sv, i) : pk(0.f, 0.f);
+            unpk(fma2(wy, pk(rstd, rstd), fma2(pair_of(tv, i), pk(c, c), low)), g[2 * i], g[2 * i + 1]);
+          }
+        } else {
+          g[0] = fmaf(rstd, to_f(gv.v[0]) * w[j][0], fmaf(to_f(tv.v[0]), c, p.dsum ? to_f(sv.v[0]) : 0.f));
+        }
+        store_v<In, V>(static_cast<In *>(p.dx) + row * p.D + d, g);
+      }
+    }
+    in.done();
+  }
+  in.finish();
+  // the CTA's rows of threads meet in order, where the ring was
+  float *sums = reinterpret_cast<float *>(ring);
+  const int width = blockDim.x * kPer * V;
+  if (blockDim.y > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sums[threadIdx.y * width + (j * blockDim.x + threadIdx.x) * V + i] = dw[j][i];
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int d = (j * blockDim.x + threadIdx.x) * V + i;
+      float s = dw[j][i];
+      for (int y = 1; y < blockDim.y; ++y) s += sums[y * width + d];
+      if (d < p.D) p.partial[(int64_t)blockIdx.x * p.D + d] = s;
+    }
+}
+
 // dw[d] = sum of n partial rows (db from the first `first` columns on): C columns a CTA, every R-th row to a thread,
 // then a warp a column over the R sums.  Few columns take 8 at a time (a sector
 // of each row), so that there are CTAs; many take 32 (4096 x 8192: 53 us with
@@ -60,10 +231,10 @@ template <typename In, int V, int kPer>
 struct FwdOne {
   static cudaError_t run(const NormArgs &a, const Plan &q, cudaStream_t s) {
     if (q.threads == 256)
-      return a.scale ? go(norm_fwd_kernel<In, V, kPer, 256, true, false>, a, q, s)
-                     : go(norm_fwd_kernel<In, V, kPer, 256, false, false>, a, q, s);
-    return a.scale ? go(norm_fwd_kernel<In, V, kPer, kMostThreads, true, false>, a, q, s)
-                   : go(norm_fwd_kernel<In, V, kPer, kMostThreads, false, false>, a, q, s);
+      return a.scale ? go(norm_fwd_kernel<In, V, kPer, 256, true>, a, q, s)
+                     : go(norm_fwd_kernel<In, V, kPer, 256, false>, a, q, s);
+    return a.scale ? go(norm_fwd_kernel<In, V, kPer, kMostThreads, true>, a, q, s)
+                   : go(norm_fwd_kernel<In, V, kPer, kMostThreads, false>, a, q, s);
   }
 };
 template <typename In, int V, int kPer>
@@ -82,7 +253,7 @@ cudaError_t fwd_all(const NormArgs &a, cudaStream_t s) {
 
 template <typename In>
 cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
-  const Plan q = bwd_plan<In>(a);
+  const Plan q = bwd_plan<In>(a, kSmThreads);
   cudaError_t e = q.grid > 0 ? dispatch<In, BwdOne>(q, a, q, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
   return launch_column_sum(a.partial, a.dweight, q.grid, a.D, s);
@@ -106,7 +277,7 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s) {
 }
 
 int64_t norm_bwd_ctas(const NormBwdArgs &a) {
-  const Plan q = a.bf16 ? bwd_plan<__nv_bfloat16>(a) : bwd_plan<float>(a);
+  const Plan q = a.bf16 ? bwd_plan<__nv_bfloat16>(a, kSmThreads) : bwd_plan<float>(a, kSmThreads);
   return q.grid;
 }
 

@@ -1,6 +1,6 @@
-// norm.cuh -- the kernels of the residual addition with a norm, root-mean-square
-// (norm.cu, where the formulas and the reasons stand) or, with kMean, layer norm
-// (layernorm.cu), and how they are launched.
+// norm.cuh -- what the residual addition with a norm, root-mean-square (norm.cu, where
+// the reasons stand) or layer norm (layernorm.cu), is built of: how rows are shared
+// out, copied ahead, reduced and stored, and how the kernels are launched.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -101,25 +101,6 @@ __device__ __forceinline__ float row_reduce(float v, float *part, int nwarp) {
   __syncthreads();
   v = part[threadIdx.y * 32];
   for (int i = 1; i < nwarp; ++i) v = join<kMax>(v, part[threadIdx.y * 32 + i]);
-  return v;
-}
-
-// The same for two sums at once; part: [2][8 * 32].
-__device__ __forceinline__ float2 row_reduce2(float a, float b, float2 *part, int nwarp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  if (nwarp == 1) return make_float2(a, b);
-  const int w = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) part[threadIdx.y * 32 + w] = make_float2(a, b);
-  __syncthreads();
-  float2 v = part[threadIdx.y * 32];
-  for (int i = 1; i < nwarp; ++i) {
-    const float2 u = part[threadIdx.y * 32 + i];
-    v.x += u.x, v.y += u.y;
-  }
   return v;
 }
 
@@ -224,318 +205,6 @@ struct Rows {
   }
 };
 
-// ------------------------------------------------------------------ forward
-// blockDim (nt, rows a CTA); a thread's vectors are nt apart
-template <typename In, int V, int kPer, int kT, bool kQuant, bool kMean>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 ? (kQuant ? kQuantThreads : kSmThreads) / kT : 1) norm_fwd_kernel(NormArgs p) {
-  __shared__ float part[2][8 * 32];  // at most 8 rows a CTA, 16 warps a row
-  extern __shared__ __align__(16) unsigned char ring[];
-  const int nwarp = blockDim.x >> 5;
-  float w[kPer][V];
-  chain_wait();
-  load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
-  float bias[kMean ? kPer : 1][V];
-  if constexpr (kMean) load_weight<V, kPer>(p.bias, p.b_bf16, p.D, bias);
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Rows<In, V, kPer, 2, kT> in;
-  in.base[0] = static_cast<const In *>(p.x); in.base[1] = static_cast<const In *>(p.residual);
-  in.ld[0] = p.ldx; in.ld[1] = p.ldr; in.rows = p.rows; in.D = p.D;
-  in.ring = ring;
-  in.start(first, step);
-  int buf = 0;
-  // every row of the CTA takes part in the barriers until the last is done
-  for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
-    in.turn(row, step);
-    float t[kPer][V], ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const bool on = row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
-      const APack<In, V> xv = in.get(0, j), rv = in.get(1, j);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        t[j][i] = on ? to_f(xv.v[i]) + (p.residual ? to_f(rv.v[i]) : 0.f) : 0.f;
-        ss = kMean ? ss + t[j][i] : fmaf(t[j][i], t[j][i], ss);
-      }
-    }
-    in.done();
-    ss = row_reduce<false>(ss, part[kQuant || kMean ? 0 : buf], nwarp);
-    [[maybe_unused]] float mean = 0.f;
-    if constexpr (kMean) {  // the squares of what is left without the mean, not mean t^2 - mean^2
-      mean = ss / (float)p.D;
-      ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const bool on = ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float c = on ? t[j][i] - mean : 0.f;
-          ss = fmaf(c, c, ss);
-        }
-      }
-      ss = row_reduce<false>(ss, part[1], nwarp);
-    }
-    const float rstd = rsqrtf(ss / (float)p.D + p.eps);
-    float inv = 1.f;
-    if constexpr (kQuant) {
-      float top = 0.f;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(t[j][i] * rstd * w[j][i]));
-      top = row_reduce<true>(top, part[1], nwarp);
-      // a row of zeros, or of values too small for a float32 scale: scale 1
-      float scale = top / kE4m3Max;
-      if (scale < 1.1754944e-38f) scale = 1.f;
-      inv = 1.f / scale;
-      if (row < p.rows && threadIdx.x == 0) p.scale[row] = scale;
-    }
-    if (row < p.rows) {
-      if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-      if constexpr (kMean)
-        if (p.mean && threadIdx.x == 0) p.mean[row] = mean;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
-        if (d >= p.D) continue;
-        if (p.sum) store_v<In, V>(static_cast<In *>(p.sum) + row * p.D + d, t[j]);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if constexpr (kMean)
-            t[j][i] = fmaf((t[j][i] - mean) * rstd, w[j][i], bias[j][i]);
-          else
-            t[j][i] = t[j][i] * rstd * w[j][i] * inv;
-        if constexpr (kQuant)
-          store_e4m3<V>(static_cast<uint8_t *>(p.y) + row * p.D + d, t[j]);
-        else
-          store_v<In, V>(static_cast<In *>(p.y) + row * p.D + d, t[j]);
-      }
-    }
-  }
-  in.finish();
-}
-
-// ----------------------------------------------------------------- backward
-// The row is read from its ring twice, before and after the reduction, rather
-// than held: that is what lets two CTAs of 512 threads share an SM.
-template <typename In, int V, int kPer, int kT>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) norm_bwd_kernel(NormBwdArgs p) {
-  __shared__ float part[2][8 * 32];
-  extern __shared__ __align__(16) unsigned char ring[];
-  const int nwarp = blockDim.x >> 5;
-  chain_next();
-  chain_wait();
-  float w[kPer][V], dw[kPer][V];
-  load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Rows<In, V, kPer, 3, kT> in;
-  in.base[0] = static_cast<const In *>(p.dy); in.base[1] = static_cast<const In *>(p.sum);
-  in.base[2] = static_cast<const In *>(p.dsum);
-  in.ld[0] = in.ld[1] = in.ld[2] = in.D = p.D; in.rows = p.rows;
-  in.ring = ring;
-  in.start(first, step);
-  float ahead = first < p.rows ? p.rstd[first] : 0.f;
-  int buf = 0;
-  for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
-    in.turn(row, step);
-    const float rstd = ahead;
-    if (row + step < p.rows) ahead = p.rstd[row + step];
-    float dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const APack<In, V> gv = in.get(0, j), tv = in.get(1, j);
-      if (row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D) {
-        if constexpr (V > 1) {
-          uint64_t sum = pk(0.f, 0.f);
-          const uint64_t rr = pk(rstd, rstd);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            const uint64_t t = mul2(pair_of(tv, i), rr), y = pair_of(gv, i);
-            unpk(fma2(y, t, pk(dw[j][2 * i], dw[j][2 * i + 1])), dw[j][2 * i], dw[j][2 * i + 1]);
-            sum = fma2(mul2(y, pk(w[j][2 * i], w[j][2 * i + 1])), t, sum);
-          }
-          float a, b;
-          unpk(sum, a, b);
-          dot += a + b;
-        } else {
-          const float t = to_f(tv.v[0]) * rstd, y = to_f(gv.v[0]);
-          dw[j][0] = fmaf(y, t, dw[j][0]);
-          dot = fmaf(y * w[j][0], t, dot);
-        }
-      }
-    }
-    dot = row_reduce<false>(dot, part[buf], nwarp) / (float)p.D;
-    if (row < p.rows) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
-        if (d >= p.D) continue;
-        const APack<In, V> gv = in.get(0, j), tv = in.get(1, j), sv = in.get(2, j);
-        float g[V];
-        // rstd (w dy - t^ dot) + dsum, with t^ = sum * rstd
-        const float c = -rstd * rstd * dot;
-        if constexpr (V > 1) {
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            const uint64_t wy = mul2(pair_of(gv, i), pk(w[j][2 * i], w[j][2 * i + 1]));
-            const uint64_t low = p.dsum ? pair_of(sv, i) : pk(0.f, 0.f);
-            unpk(fma2(wy, pk(rstd, rstd), fma2(pair_of(tv, i), pk(c, c), low)), g[2 * i], g[2 * i + 1]);
-          }
-        } else {
-          g[0] = fmaf(rstd, to_f(gv.v[0]) * w[j][0], fmaf(to_f(tv.v[0]), c, p.dsum ? to_f(sv.v[0]) : 0.f));
-        }
-        store_v<In, V>(static_cast<In *>(p.dx) + row * p.D + d, g);
-      }
-    }
-    in.done();
-  }
-  in.finish();
-  // the CTA's rows of threads meet in order, where the ring was
-  float *sums = reinterpret_cast<float *>(ring);
-  const int width = blockDim.x * kPer * V;
-  if (blockDim.y > 1) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) sums[threadIdx.y * width + (j * blockDim.x + threadIdx.x) * V + i] = dw[j][i];
-    __syncthreads();
-    if (threadIdx.y > 0) return;
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int d = (j * blockDim.x + threadIdx.x) * V + i;
-      float s = dw[j][i];
-      for (int y = 1; y < blockDim.y; ++y) s += sums[y * width + d];
-      if (d < p.D) p.partial[(int64_t)blockIdx.x * p.D + d] = s;
-    }
-}
-
-// The backward of layer norm: two dot products a row, and two column sums, which go
-// out side by side, [CTA][2 D].
-template <typename In, int V, int kPer, int kT>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layernorm_bwd_kernel(NormBwdArgs p) {
-  __shared__ float2 part[2][8 * 32];
-  extern __shared__ __align__(16) unsigned char ring[];
-  const int nwarp = blockDim.x >> 5;
-  chain_next();
-  chain_wait();
-  float w[kPer][V], dw[kPer][V], db[kPer][V];
-  load_weight<V, kPer>(p.weight, p.w_bf16, p.D, w);
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i) dw[j][i] = db[j][i] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Rows<In, V, kPer, 3, kT> in;
-  in.base[0] = static_cast<const In *>(p.dy); in.base[1] = static_cast<const In *>(p.sum);
-  in.base[2] = static_cast<const In *>(p.dsum);
-  in.ld[0] = in.ld[1] = in.ld[2] = in.D = p.D; in.rows = p.rows;
-  in.ring = ring;
-  in.start(first, step);
-  float ahead = first < p.rows ? p.rstd[first] : 0.f, ahead_m = first < p.rows ? p.mean[first] : 0.f;
-  int buf = 0;
-  for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
-    in.turn(row, step);
-    const float rstd = ahead, mean = ahead_m;
-    if (row + step < p.rows) ahead = p.rstd[row + step], ahead_m = p.mean[row + step];
-    float sum = 0.f, dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const APack<In, V> gv = in.get(0, j), tv = in.get(1, j);
-      if (row < p.rows && ((int64_t)j * blockDim.x + threadIdx.x) * V < p.D) {
-        if constexpr (V > 1) {
-          uint64_t s2 = pk(0.f, 0.f), d2 = pk(0.f, 0.f);
-          const uint64_t rr = pk(rstd, rstd), mm = pk(-mean, -mean), one = pk(1.f, 1.f);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            // (the difference first: a product of the mean would cancel)
-            const uint64_t t = mul2(fma2(pair_of(tv, i), one, mm), rr), y = pair_of(gv, i);
-            unpk(fma2(y, t, pk(dw[j][2 * i], dw[j][2 * i + 1])), dw[j][2 * i], dw[j][2 * i + 1]);
-            unpk(fma2(y, one, pk(db[j][2 * i], db[j][2 * i + 1])), db[j][2 * i], db[j][2 * i + 1]);
-            const uint64_t wy = mul2(y, pk(w[j][2 * i], w[j][2 * i + 1]));
-            s2 = fma2(wy, one, s2);
-            d2 = fma2(wy, t, d2);
-          }
-          float a, b;
-          unpk(s2, a, b);
-          sum += a + b;
-          unpk(d2, a, b);
-          dot += a + b;
-        } else {
-          const float t = (to_f(tv.v[0]) - mean) * rstd, y = to_f(gv.v[0]);
-          dw[j][0] = fmaf(y, t, dw[j][0]);
-          db[j][0] += y;
-          sum += y * w[j][0];
-          dot = fmaf(y * w[j][0], t, dot);
-        }
-      }
-    }
-    const float2 both = row_reduce2(sum, dot, part[buf], nwarp);
-    sum = both.x / (float)p.D, dot = both.y / (float)p.D;
-    if (row < p.rows) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t d = ((int64_t)j * blockDim.x + threadIdx.x) * V;
-        if (d >= p.D) continue;
-        const APack<In, V> gv = in.get(0, j), tv = in.get(1, j), sv = in.get(2, j);
-        float g[V];
-        // rstd (w dy - sum - t^ dot) + dsum, with t^ = (t - mean) rstd
-        const float c = -rstd * dot;
-        if constexpr (V > 1) {
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            const uint64_t t = fma2(pair_of(tv, i), pk(1.f, 1.f), pk(-mean, -mean));
-            const uint64_t in_ = fma2(pair_of(gv, i), pk(w[j][2 * i], w[j][2 * i + 1]), fma2(t, pk(c, c), pk(-sum, -sum)));
-            const uint64_t low = p.dsum ? pair_of(sv, i) : pk(0.f, 0.f);
-            unpk(fma2(in_, pk(rstd, rstd), low), g[2 * i], g[2 * i + 1]);
-          }
-        } else {
-          const float t = to_f(tv.v[0]) - mean;
-          g[0] = fmaf(rstd, fmaf(to_f(gv.v[0]), w[j][0], fmaf(t, c, -sum)), p.dsum ? to_f(sv.v[0]) : 0.f);
-        }
-        store_v<In, V>(static_cast<In *>(p.dx) + row * p.D + d, g);
-      }
-    }
-    in.done();
-  }
-  in.finish();
-  // the CTA's rows of threads meet in order, where the ring was, one sum after the other
-  float *sums = reinterpret_cast<float *>(ring);
-  const int width = blockDim.x * kPer * V;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if (blockDim.y > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          sums[threadIdx.y * width + (j * blockDim.x + threadIdx.x) * V + i] = which ? db[j][i] : dw[j][i];
-      __syncthreads();
-    }
-    if (threadIdx.y == 0) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int d = (j * blockDim.x + threadIdx.x) * V + i;
-          float s = which ? db[j][i] : dw[j][i];
-          for (int y = 1; y < blockDim.y; ++y) s += sums[y * width + d];
-          if (d < p.D) p.partial[((int64_t)blockIdx.x * 2 + which) * p.D + d] = s;
-        }
-    }
-  }
-}
-
 // ------------------------------------------------------------------ launches
 struct Plan {
   int V, per, nt, rpc;  // elements a vector, vectors a thread, threads a row, rows a CTA
@@ -634,9 +303,9 @@ int fwd_width(const NormArgs &a) {
   return ok(V) ? V : V == 8 && ok(2) ? 2 : 1;
 }
 template <typename In>
-Plan bwd_plan(const NormBwdArgs &a) {
+Plan bwd_plan(const NormBwdArgs &a, int resident) {
   constexpr int V = 16 / sizeof(In);
-  return plan(a.rows, a.D, V, a.D % V == 0 ? V : V == 8 && a.D % 2 == 0 ? 2 : 1, 3, kSmThreads, false);
+  return plan(a.rows, a.D, V, a.D % V == 0 ? V : V == 8 && a.D % 2 == 0 ? 2 : 1, 3, resident, false);
 }
 
 }  // namespace
