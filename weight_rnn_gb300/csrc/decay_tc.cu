@@ -44,6 +44,7 @@
 #include <cuda_bf16.h>
 
 #include "chain.cuh"
+#include "decay.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tma_host.h"
@@ -52,6 +53,7 @@ namespace delta {
 namespace {
 
 using namespace sm100;
+using decay::ex2;
 
 __device__ unsigned int g_decay_error = 0;
 
@@ -102,12 +104,6 @@ __device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity,
       break;
     }
   return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -519,11 +515,16 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(&sh.sfull);
     };
     if (!kStates) publish();
+    uint64_t keep_a = 0, keep_b = 0;  // of a chunk of `kept` tokens
+    int kept = -1;
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       const int n = min(kC, t_end - start_of(c));
-      const float keep = exp2f(lg * (float)n);
-      const uint64_t keep2 = pk(keep, keep);
+      if (n != kept) {  // (whole chunks, and the last)
+        const decay::Keep keep = decay::keep_of(lg, n);
+        keep_a = pk(keep.a, keep.a), keep_b = pk(keep.b, keep.b);
+        kept = n;
+      }
       if (!(ok = wait(&sh, &sh.dsfull, (uint32_t)c & 1u, 5))) break;
       tc_fence_after();
 #pragma unroll
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         tmem_ld16(tmem_addr(tmem, quarter * 32, kDs + half * 64 + 16 * j), r);
         tmem_wait_ld_regs(r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) S[8 * j + i] = fma2(keep2, S[8 * j + i], pk(r[2 * i], r[2 * i + 1]));
+        for (int i = 0; i < 8; ++i) S[8 * j + i] = fma2(keep_a, S[8 * j + i], fma2(keep_b, S[8 * j + i], pk(r[2 * i], r[2 * i + 1])));
       }
       tc_fence_before();
       __syncwarp();
