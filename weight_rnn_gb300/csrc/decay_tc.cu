@@ -91,19 +91,33 @@ struct Shared {
   volatile int dead;
 };
 
-// By whole warps, so that they leave their loops together.  (Inline: a call here would
-// save what is live around it, 64 registers of state among them, at every place.)
+// What waits gave up on is not waited for by the others, once they look.
+__device__ __forceinline__ void give_up(Shared *sh, int role) {
+  if (!sh->dead) atomicCAS(&g_decay_error, 0u, (unsigned)(1 + role));
+  sh->dead = 1;
+}
+// By whole warps, so that they leave their loops together.  Few instructions, since they
+// stand at every hand-over: the warps' loops have to share small instruction caches.
 __device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity, int role) {
-  bool ok = true;
-#pragma unroll 1
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
-    if ((i & 63) == 0 && (sh->dead || i == (1u << 22))) {
-      if (!sh->dead) atomicCAS(&g_decay_error, 0u, (unsigned)(1 + role));
-      sh->dead = 1;
-      ok = false;
-      break;
-    }
-  return __all_sync(0xffffffffu, ok);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra.uni DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.gt.u32 p, n, %3;\n\t"
+      "@!p bra.uni TRY;\n"
+      "DONE:\n\t"
+      "setp.le.u32 p, n, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(1 << 21)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
+  give_up(sh, role);
+  return false;
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -112,13 +126,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32"
-      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st16x128b_x2(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
 }
 
 // float32 pairs: one instruction for two elements
@@ -136,6 +147,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(pk(-1.f, -1.f)), "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -191,15 +207,12 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t row, uint32_t piece) {
   return row * 128u + ((piece ^ (row & 7u)) * 16u);
 }
 
-template <bool kStates>
-__global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs a) {
-  extern __shared__ unsigned char raw[];
-  __shared__ Shared sh;
+// One item, in either direction of the time: two bodies rather than one that asks, which
+// would be the longer for every warp.
+template <bool kStates, bool kReverse>
+__device__ __forceinline__ void decay_tc_body(const TcArgs &a, unsigned char *raw, Shared &sh, uint32_t item, const TcPass &p) {
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  uint32_t item = blockIdx.x;
-  const TcPass &p = a.pass[item % (uint32_t)a.passes];
-  item /= (uint32_t)a.passes;
   const int sg = (int)(item % (uint32_t)a.nseg);
   item /= (uint32_t)a.nseg;
   const int c0 = (int)(item % (uint32_t)a.groups) * kD;
@@ -234,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
   len = len < 0 ? 0 : len > a.T ? a.T : len;
   const int t_lo = sg * a.seg, t_hi = min(t_lo + a.seg, a.T), t_end = min(t_hi, len);
   const int chunks = t_end > t_lo ? (t_end - t_lo + kC - 1) / kC : 0;
-  const auto start_of = [&](int c) { return t_lo + (p.reverse ? chunks - 1 - c : c) * kC; };
+  const auto start_of = [&](int c) { return t_lo + (kReverse ? chunks - 1 - c : c) * kC; };
   const float lg = fmaxf(log2f(a.decay[h]), kLogZero);
   const bool two = lg != 0.f || p.kvs != 1.f;  // else K' is K itself
 
@@ -352,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
   } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) / 4;
     const int row = quarter * 32 + lane;
-    uint64_t w[8];  // weights of this lane's tokens in a chunk of `weighed` tokens
-    int weighed = -1;
+    const float s16 = ex2(16.f * lg);
+    const uint64_t step16 = pk(s16, s16);
     // K' of chunk c: this warp's 32 channels, half of the tokens
     const auto keys = [&](int c) {
       const int slot = c & 1, n = min(kC, t_end - start_of(c));
@@ -372,45 +385,50 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       // lane / 4 of tokens 2 (lane % 4) and the next one.  That is what a 16-lane
       // store to TMEM takes, tokens 8 i.. in register pair i.
       const uint32_t tile = smem_u32(base + kOffK + slot * kTile);
-      if (n != weighed) {  // (at most two lengths: whole chunks, and the last)
-        weighed = n;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = half * 64 + i * 8 + 2 * (lane & 3);
-          w[i] = p.reverse ? pk(ex2(lg * (float)(j + 1)) * p.kvs, ex2(lg * (float)(j + 2)) * p.kvs)
-                           : pk(ex2(lg * (float)max(n - 1 - j, 0)) * p.kvs, ex2(lg * (float)max(n - 2 - j, 0)) * p.kvs);
-        }
-      }
+      // 16 tokens x 16 channels a turn, from the heaviest tokens on: the next ones' weights
+      // are these times g^16, which can only vanish
+      const int j0 = half * 64 + 2 * (lane & 3);  // of the lane's first pair, and 8 on its second
+      uint64_t w[2];
 #pragma unroll 1
-      for (int d16 = 0; d16 < 2; ++d16) {  // of the warp's 32 channels
-        const uint32_t ch = (uint32_t)(quarter * 32 + d16 * 16 + ((lane >> 3) & 1) * 8);
-        const uint32_t from = tile + (ch >> 6) * kBlk;
-        uint32_t hi[16], lo[16];
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const int i = kReverse ? i4 : 3 - i4;
+        const uint32_t tok = (uint32_t)(half * 64 + i * 16 + (lane >> 4) * 8 + (lane & 7));
+        if (i4 == 0 || n < kC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {      // 16 tokens
-          const uint32_t tok = (uint32_t)(half * 64 + i * 16 + (lane >> 4) * 8 + (lane & 7));
-          uint32_t x[4];
-          ldsm_x4_trans(from + piece_at(tok, (ch & 63) >> 3), x);
-          if (n < kC) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int j = half * 64 + i * 16 + (g >> 1) * 8 + 2 * (lane & 3);
-              x[g] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
-            }
+          for (int y = 0; y < 2; ++y) {
+            const int j = j0 + i * 16 + 8 * y;
+            const int e = kReverse ? j + 1 : max(n - 1 - j, 0), f = kReverse ? j + 2 : max(n - 2 - j, 0);
+            w[y] = pk(ex2(lg * (float)e) * p.kvs, ex2(lg * (float)f) * p.kvs);
           }
+        }
+        uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (n < kC) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int j = j0 + i * 16 + 8 * y;
+            mask[y] = (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int d16 = 0; d16 < 2; ++d16) {  // of the warp's 32 channels
+          const uint32_t ch = (uint32_t)(quarter * 32 + d16 * 16 + ((lane >> 3) & 1) * 8);
+          uint32_t x[4], hi[4], lo[4];
+          ldsm_x4_trans(tile + (ch >> 6) * kBlk + piece_at(tok, (ch & 63) >> 3), x);
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const uint64_t v = mul2(widen2(x[g]), w[2 * i + (g >> 1)]);
-            hi[4 * i + g] = narrow2(v);
-            lo[4 * i + g] = narrow2(sub2(v, widen2(hi[4 * i + g])));
+            const uint64_t v = mul2(widen2(x[g] & mask[g >> 1]), w[g >> 1]);
+            hi[g] = narrow2(v);
+            lo[g] = narrow2(sub2(v, widen2(hi[g])));
           }
+          if (i4 == 0 && d16 == 0 && c > 0) {  // the K' before has been read
+            if (!wait(&sh, &sh.dsfull, (uint32_t)(c - 1) & 1u, 4)) return false;
+            tc_fence_after();
+          }
+          const uint32_t to = tmem_addr(tmem, quarter * 32 + d16 * 16, kHi + half * 32 + i * 8);
+          tmem_st16x128b_x2(to, hi);
+          if (two) tmem_st16x128b_x2(to + (kLo - kHi), lo);
         }
-        if (d16 == 0 && c > 0) {  // the K' before has been read
-          if (!wait(&sh, &sh.dsfull, (uint32_t)(c - 1) & 1u, 4)) return false;
-          tc_fence_after();
-        }
-        tmem_st16x128b_x8(tmem_addr(tmem, quarter * 32 + d16 * 16, kHi + half * 32), hi);
-        if (two) tmem_st16x128b_x8(tmem_addr(tmem, quarter * 32 + d16 * 16, kLo + half * 32), lo);
+        w[0] = mul2(w[0], step16), w[1] = mul2(w[1], step16);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -422,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     uint64_t c2[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      c2[i] = p.reverse ? pk(ex2(-lg * (float)(7 - 2 * i)), ex2(-lg * (float)(6 - 2 * i)))
+      c2[i] = kReverse ? pk(ex2(-lg * (float)(7 - 2 * i)), ex2(-lg * (float)(6 - 2 * i)))
                         : pk(ex2(-lg * (float)(2 * i)), ex2(-lg * (float)(2 * i + 1)));
     // P of chunk c: this lane's row, every second block of 32 columns
     const auto scores = [&](int c) {
@@ -432,14 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       // P = G 2^(lg |row - j| - log2 c_row).  The power is taken for one column of
       // eight, the one furthest from the row's own, and times eight constants 2^(-lg i):
       // below 2^-126 it is nothing beside the row's own 2^-log2 c_row.
-      const float cp = fmaxf(lg * (float)(p.reverse ? n - 1 - row : row + 1), kFloor);
-      const int lo = p.reverse ? row : 0, hi = p.reverse ? n - 1 : row;  // the columns that count
+      const float cp = fmaxf(lg * (float)(kReverse ? n - 1 - row : row + 1), kFloor);
+      const int lo = kReverse ? row : 0, hi = kReverse ? n - 1 : row;  // the columns that count
 #pragma unroll 1
       for (int i16 = 0; i16 < 4; ++i16) {  // 16 columns of the blocks half and half + 2
         const int blk = half * 32 + (i16 >> 1) * 64, j0 = blk + (i16 & 1) * 16;
         uint32_t out[8];
         // (whole warps: these columns are past every row of the warp, or before)
-        const bool none = p.reverse ? j0 + 15 < quarter * 32 || j0 >= n : j0 > quarter * 32 + 31;
+        const bool none = kReverse ? j0 + 15 < quarter * 32 || j0 >= n : j0 > quarter * 32 + 31;
         if (none) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) out[i] = 0u;
@@ -450,14 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           if (steep) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float apart = p.reverse ? (float)(j0 + i - row) : (float)(row - j0 - i);
+              const float apart = kReverse ? (float)(j0 + i - row) : (float)(row - j0 - i);
               g[i] = __float_as_uint(__uint_as_float(g[i]) * (ex2(fmaf(lg, apart, -cp)) * p.kvs));
             }
           } else {
 #pragma unroll
             for (int b8 = 0; b8 < 2; ++b8) {
-              const int j = j0 + 8 * b8 + (p.reverse ? 7 : 0);
-              const float first = ex2(fmaf(lg, (float)(p.reverse ? j - row : row - j), -cp)) * p.kvs;
+              const int j = j0 + 8 * b8 + (kReverse ? 7 : 0);
+              const float first = ex2(fmaf(lg, (float)(kReverse ? j - row : row - j), -cp)) * p.kvs;
               const uint64_t f2 = pk(first, first);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -467,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             }
           }
           // (most pieces have no columns that do not count)
-          if (p.reverse ? j0 < quarter * 32 + 31 || j0 + 15 >= n : j0 + 15 > quarter * 32) {
+          if (kReverse ? j0 < quarter * 32 + 31 || j0 + 15 >= n : j0 + 15 > quarter * 32) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (j0 + i < lo || j0 + i > hi) g[i] = 0u;
@@ -515,14 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(&sh.sfull);
     };
     if (!kStates) publish();
-    uint64_t keep_a = 0, keep_b = 0;  // of a chunk of `kept` tokens
+    uint64_t keep_a = 0;  // of a chunk of `kept` tokens
+    bool near = false;
     int kept = -1;
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       const int n = min(kC, t_end - start_of(c));
       if (n != kept) {  // (whole chunks, and the last)
         const decay::Keep keep = decay::keep_of(lg, n);
-        keep_a = pk(keep.a, keep.a), keep_b = pk(keep.b, keep.b);
+        keep_a = pk(keep.a, keep.a), near = keep.b != 0.f;
         kept = n;
       }
       if (!(ok = wait(&sh, &sh.dsfull, (uint32_t)c & 1u, 5))) break;
@@ -533,7 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         tmem_ld16(tmem_addr(tmem, quarter * 32, kDs + half * 64 + 16 * j), r);
         tmem_wait_ld_regs(r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) S[8 * j + i] = fma2(keep_a, S[8 * j + i], fma2(keep_b, S[8 * j + i], pk(r[2 * i], r[2 * i + 1])));
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t x = pk(r[2 * i], r[2 * i + 1]);
+          S[8 * j + i] = fma2(keep_a, S[8 * j + i], near ? add2(S[8 * j + i], x) : x);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -547,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         if (!(ok = wait(&sh, &sh.ofull, (uint32_t)c & 1u, 5))) break;
         tc_fence_after();
         const int t0 = start_of(c), row = quarter * 32 + lane;
-        const float cp = p.os * ex2(fmaxf(lg * (float)(p.reverse ? n - 1 - row : row + 1), kFloor));
+        const float cp = p.os * ex2(fmaxf(lg * (float)(kReverse ? n - 1 - row : row + 1), kFloor));
         const uint64_t cp2 = pk(cp, cp);
         __nv_bfloat16 *to = p.to + (((int64_t)b * a.T + t0 + row) * a.H + h) * p.dv + v0;
         const int have = t0 + row < t_hi ? p.dv - v0 : 0;
@@ -574,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         }
       }
     }
-    if (ok && (kStates || (p.final && sg == (p.reverse ? 0 : a.nseg - 1)))) {
+    if (ok && (kStates || (p.final && sg == (kReverse ? 0 : a.nseg - 1)))) {
       float *to = p.final + (kStates ? (int64_t)bh * a.nseg + sg : bh) * n_state + (int64_t)d * p.dv + v0;
       store_row(S, to, live);
     }
@@ -589,6 +611,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+template <bool kStates>
+__global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs a) {
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
+  const uint32_t item = blockIdx.x / (uint32_t)a.passes;
+  const TcPass &p = a.pass[blockIdx.x % (uint32_t)a.passes];
+  if (p.reverse)
+    decay_tc_body<kStates, true>(a, raw, sh, item, p);
+  else
+    decay_tc_body<kStates, false>(a, raw, sh, item, p);
 }
 
 // [B][T][H][d] with strides as a 4-D tensor {d, H, T, B} in tiles of 64 channels x
