@@ -54,28 +54,32 @@ int sm_count() {
   return n;
 }
 
-// Into how many segments the time axis is cut.  One CTA an SM on the tensor
-// cores, 128 tokens in about 1.9 us with all products and 1.1 with those of the
-// states alone (two CTAs, 40 and 20 us, on the CUDA cores); a cut adds the pass
-// for the states, its states' way through memory, and two launches.
+// Into how many segments the time axis is cut.  On the tensor cores 128 tokens take a CTA
+// about 2.5 us with all products and 1.7 with those of the states alone, and CTAs share
+// the work evenly where there is more than a round of it; on the CUDA cores 36 and 12 us
+// at two CTAs an SM, in whole rounds.  A cut adds the pass for the states, its states'
+// way through memory, and two launches.
 int segments(const DecayArgs &a, int64_t state_passes, bool tc) {
   const int64_t chunks = (a.T + delta::kDecayChunk - 1) / delta::kDecayChunk;
   const int width = tc ? 128 : 64;
-  const double whole = tc ? 1.9 : 40.0, part = tc ? 1.1 : 20.0;
+  const double whole = tc ? 2.5 : 36.0, part = tc ? 1.7 : 12.0;
   const int64_t slots = (int64_t)sm_count() * (tc ? 1 : 2);
   int64_t items = 0, bytes = 0;
   for (int i = 0; i < a.passes; ++i) items += a.B * a.H * ((a.pass[i].dv + width - 1) / width);
   bytes = state_passes * a.B * a.H * a.pass[0].dk * a.pass[0].dv * 4;
   const int64_t state_items = state_passes * a.B * a.H * ((a.pass[0].dv + width - 1) / width);
   const auto up_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const auto rounds = [&](int64_t n) {
+    return tc ? (n <= slots ? 1.0 : (double)n / (double)slots) : (double)up_div(n, slots);
+  };
   int best = 1;
   double least = 1e30;
   for (int64_t n = 1; n <= chunks && n <= 256; ++n) {
     const int64_t each = up_div(chunks, n);
     if (up_div(chunks, each) != n) continue;  // every segment has tokens
     if (n > 1 && bytes * n > (int64_t(1) << 30)) break;
-    double us = (double)(up_div(items * n, slots) * each) * whole;
-    if (n > 1) us += (double)(up_div(state_items * n, slots) * each) * part + 8.0 + (double)(bytes * n) * 4 / 5e6;
+    double us = rounds(items * n) * (double)each * whole;
+    if (n > 1) us += rounds(state_items * n) * (double)each * part + 9.0 + (double)(bytes * n) * 4 / 5e6;
     if (us < 0.95 * least) least = us, best = (int)n;
   }
   return best;
@@ -92,22 +96,29 @@ cudaError_t run(DecayArgs &a, const Start *starts, int count, cudaStream_t s) {
   a.nseg = segments(a, count, tc);
   const int64_t chunks = (a.T + delta::kDecayChunk - 1) / delta::kDecayChunk;
   a.seg = (chunks + a.nseg - 1) / a.nseg * delta::kDecayChunk;
-  if (a.nseg == 1) return tc ? delta::launch_decay_tc(a, false, s) : delta::launch_decay(a, s);
-  const int64_t n = (int64_t)starts[0].pass.dk * starts[0].pass.dv, bytes = a.B * a.H * a.nseg * n * 4;
-  Scratch scr(s);
-  for (int i = 0; i < count; ++i) scr.want(bytes);
-  cudaError_t err = scr.take();
-  if (err != cudaSuccess) return err;
+  const bool cut = a.nseg > 1;
+  const int64_t n = (int64_t)starts[0].pass.dk * starts[0].pass.dv, bytes = cut ? a.B * a.H * a.nseg * n * 4 : 0;
   DecayArgs st = a;
   st.passes = count;
-  for (int i = 0; i < count; ++i) {
-    st.pass[i] = starts[i].pass;
-    st.pass[i].final = static_cast<float *>(scr.cut(bytes));
-    for (int j = 0; j < starts[i].count; ++j) a.pass[starts[i].into[j]].init = st.pass[i].final;
+  for (int i = 0; i < count; ++i) st.pass[i] = starts[i].pass;
+  const int64_t handed = tc ? delta::decay_tc_scratch(a) : 0, handed_st = tc && cut ? delta::decay_tc_scratch(st) : 0;
+  Scratch scr(s);
+  for (int i = 0; cut && i < count; ++i) scr.want(bytes);
+  scr.want(handed);
+  scr.want(handed_st);
+  cudaError_t err = scr.take();
+  if (err != cudaSuccess) return err;
+  if (cut) {
+    for (int i = 0; i < count; ++i) {
+      st.pass[i].final = static_cast<float *>(scr.cut(bytes));
+      for (int j = 0; j < starts[i].count; ++j) a.pass[starts[i].into[j]].init = st.pass[i].final;
+    }
+    st.handed = handed_st ? scr.cut(handed_st) : nullptr;
+    err = tc ? delta::launch_decay_tc(st, true, s) : delta::launch_decay_states(st, s);
+    for (int i = 0; err == cudaSuccess && i < count; ++i)
+      err = delta::launch_decay_join(st.pass[i].final, starts[i].pass.init, a, starts[i].pass.reverse, n, s);
   }
-  err = tc ? delta::launch_decay_tc(st, true, s) : delta::launch_decay_states(st, s);
-  for (int i = 0; err == cudaSuccess && i < count; ++i)
-    err = delta::launch_decay_join(st.pass[i].final, starts[i].pass.init, a, starts[i].pass.reverse, n, s);
+  a.handed = handed ? scr.cut(handed) : nullptr;
   if (err == cudaSuccess) err = tc ? delta::launch_decay_tc(a, false, s) : delta::launch_decay(a, s);
   const cudaError_t ef = scr.release();
   return err != cudaSuccess ? err : ef;

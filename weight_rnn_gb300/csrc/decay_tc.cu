@@ -63,7 +63,7 @@ constexpr uint32_t kTile = 32768, kBlk = 16384;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffS = 6 * kTile;
 constexpr int kSmem = 7 * kTile + 1024;
 // TMEM columns
-constexpr uint32_t kG = 0, kO = 128, kDs = 256, kHi = 384, kLo = 448;
+constexpr uint32_t kG = 0, kO = 128, kDs = 256, kHi = 384;  // (lo: 64 after hi)
 constexpr float kFloor = -100.f;   // log2 of the least c_p
 constexpr float kLogZero = -200.f; // log2 g of g = 0: any power of it vanishes, also over c_p
 
@@ -78,17 +78,80 @@ struct TcPass {
 };
 struct TcArgs {
   TcPass pass[3];
-  int passes, groups, nseg;
+  int passes, groups, nseg, chunks;  // chunks: of a whole segment
+  uint32_t items;
   const float *decay;
   const int *lengths;
   int T, H, seg;
+  bool shared;      // CTAs share items, and hand over states:
+  uint32_t *flags;  // [CTA][8], zeroes
+  float4 *handed;   // [CTA][8][16][32]
 };
 
+// A CTA's work.  It has one of the passes; an item is a segment of a head and a group of
+// value channels.  Where there are more items than CTAs can be resident, the CTAs of a
+// pass get equal runs of its items' chunks, one after another, so that the last round is
+// as full as the others (384 items in 2.6 rounds of 152 for 3).  An item that two CTAs
+// share is begun by the first, before all else, and ended by the second, after all else,
+// which takes the state over through memory; it is there by then, as no CTA has less than
+// an item's chunks.  CTAs of different passes that are neighbours work on one head at one
+// time, so that what both read comes from memory once (the two in reverse share two of
+// three tensors).
+constexpr int kParts = 24;
+struct Part {
+  int pass, c0, b, h;
+  int t_lo, t_hi, t_end, chunks;  // of the item: tokens, those that count, their chunks
+  int from, to;                   // the chunks of this part, in the order of the pass
+  float lg;
+  bool head, tail, two, last;     // begins, ends the item; K' needs two parts; ends the row
+  int64_t state;                  // place among the states
+};
+
+template <bool kStates>
+__device__ bool part_at(const TcArgs &a, int k, Part &r) {
+  uint32_t item = blockIdx.x / (uint32_t)a.passes;
+  r.pass = (int)(blockIdx.x % (uint32_t)a.passes);
+  r.from = 0, r.to = a.chunks;
+  if (a.shared) {
+    const uint64_t units = (uint64_t)(a.items / (uint32_t)a.passes) * (uint32_t)a.chunks;
+    const uint32_t ctas = gridDim.x / (uint32_t)a.passes;
+    const uint64_t u0 = units * item / ctas, u1 = units * (item + 1) / ctas;
+    const uint32_t first = (uint32_t)(u0 / (uint32_t)a.chunks), last = (uint32_t)((u1 - 1) / (uint32_t)a.chunks);
+    const int count = (int)(last - first) + 1;
+    if (k >= count) return false;
+    item = k == 0 ? last : k == count - 1 ? first : first + (uint32_t)k;
+    if (item == first) r.from = (int)(u0 - (uint64_t)first * (uint32_t)a.chunks);
+    if (item == last) r.to = (int)(u1 - (uint64_t)last * (uint32_t)a.chunks);
+  } else if (k > 0) {
+    return false;
+  }
+  r.head = r.from == 0, r.tail = r.to == a.chunks;
+  const TcPass &p = a.pass[r.pass];
+  const int sg = (int)(item % (uint32_t)a.nseg);
+  item /= (uint32_t)a.nseg;
+  r.c0 = (int)(item % (uint32_t)a.groups) * kD;
+  const uint32_t bh = item / (uint32_t)a.groups;
+  r.b = (int)(bh / (uint32_t)a.H), r.h = (int)(bh % (uint32_t)a.H);
+  int len = a.lengths ? a.lengths[r.b] : a.T;
+  len = len < 0 ? 0 : len > a.T ? a.T : len;
+  r.t_lo = sg * a.seg, r.t_hi = min(r.t_lo + a.seg, a.T), r.t_end = min(r.t_hi, len);
+  r.chunks = r.t_end > r.t_lo ? (r.t_end - r.t_lo + kC - 1) / kC : 0;
+  if (r.c0 >= p.dv) r.chunks = 0, r.t_hi = r.t_lo;  // a pass with fewer groups
+  r.to = min(r.to, r.chunks);
+  r.lg = fmaxf(log2f(a.decay[r.h]), kLogZero);
+  r.two = r.lg != 0.f || p.kvs != 1.f;  // else K' is K itself
+  r.last = kStates || sg == (p.reverse ? 0 : a.nseg - 1);
+  r.state = kStates || a.nseg > 1 ? (int64_t)bh * a.nseg + sg : bh;
+  return true;
+}
+
 struct Shared {
-  uint64_t qfull[2], qempty[2], kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t gfull, pfull, ofull, oempty, dsfull, dsempty, kpfull, sfull, sempty, drain[2];
+  uint64_t qfull[2], qempty[2], kfull[3], kempty[3], vfull[3], vempty[3];
+  uint64_t gfull, pfull, ofull, oempty, dsfull[2], dsempty[2], kpfull[2], sfull, sempty, drain[2];
   uint32_t tmem;
+  int parts;
   volatile int dead;
+  Part part[kParts];
 };
 
 // What waits gave up on is not waited for by the others, once they look.
@@ -119,6 +182,28 @@ __device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity,
   give_up(sh, role);
   return false;
 }
+
+// The same for a flag that another CTA sets, after what it has for this warp.
+__device__ __forceinline__ bool wait_flag(Shared *sh, const uint32_t *flag) {
+  uint32_t there = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 22) && !sh->dead; ++i) {
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(flag) : "memory");
+    if (there) break;
+    __nanosleep(200);
+  }
+  if (__all_sync(0xffffffffu, there != 0)) return true;
+  give_up(sh, 6);
+  return false;
+}
+// products in flight end before TMEM is given back
+__device__ __noinline__ void drain(uint64_t *bar) {
+  if (elect_one()) mma_commit(bar);
+  for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(bar, 0); ++j) {
+  }
+}
+// K-major: 16 channels are 32 bytes of a 128-byte row
+__device__ __forceinline__ uint64_t step_k(int k) { return (uint64_t)((k >> 2) * kBlk + (k & 3) * 32) >> 4; }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -207,29 +292,53 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t row, uint32_t piece) {
   return row * 128u + ((piece ^ (row & 7u)) * 16u);
 }
 
-// One item, in either direction of the time: two bodies rather than one that asks, which
-// would be the longer for every warp.
-template <bool kStates, bool kReverse>
-__device__ __forceinline__ void decay_tc_body(const TcArgs &a, unsigned char *raw, Shared &sh, uint32_t item, const TcPass &p) {
+// where a ring stands at a chunk of the CTA's share
+template <int kRing>
+struct Turn {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kRing) slot = 0, phase ^= 1u;
+  }
+};
+
+// tokens past a row's end, in chunks that no tile reached: a share of the rows a warp
+__device__ __noinline__ void zero_rest(const TcArgs &a, const Part &t, int share, int lane) {
+  const TcPass &p = a.pass[t.pass];
+  const int pieces = min(kD, p.dv - t.c0) / 8;
+  if (t.head)
+    for (int i = t.t_lo + t.chunks * kC + share; i < t.t_hi; i += 17)
+      if (lane < pieces)
+        *reinterpret_cast<uint4 *>(p.to + (((int64_t)t.b * a.T + i) * a.H + t.h) * p.dv + t.c0 + lane * 8) =
+            make_uint4(0, 0, 0, 0);
+}
+
+template <bool kIs>
+struct Bool {
+  static constexpr bool value = kIs;
+};
+
+template <bool kStates>
+__global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs a) {
+  // The states alone have no Q, S, G and O: their tiles and tensor memory make the
+  // rings of K and V one deeper, and K' and dS two.
+  constexpr int kRing = kStates ? 3 : 2, kBufs = kStates ? 2 : 1;
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int sg = (int)(item % (uint32_t)a.nseg);
-  item /= (uint32_t)a.nseg;
-  const int c0 = (int)(item % (uint32_t)a.groups) * kD;
-  const uint32_t bh = item / (uint32_t)a.groups;
-  const int b = (int)(bh / (uint32_t)a.H), h = (int)(bh % (uint32_t)a.H);
-  if (c0 >= p.dv) return;
-  const int dk = p.dk, cols = min(kD, p.dv - c0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 2);
+      mbar_init(&sh.dsfull[i], 1), mbar_init(&sh.dsempty[i], 8), mbar_init(&sh.kpfull[i], 8);
+      mbar_init(&sh.drain[i], 1);
+    }
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&sh.kfull[i], 1), mbar_init(&sh.kempty[i], kStates ? 8 : 9);
       mbar_init(&sh.vfull[i], 1), mbar_init(&sh.vempty[i], kStates ? 1 : 2);
     }
     mbar_init(&sh.gfull, 1), mbar_init(&sh.pfull, 8), mbar_init(&sh.ofull, 1), mbar_init(&sh.oempty, 8);
-    mbar_init(&sh.dsfull, 1), mbar_init(&sh.dsempty, 8), mbar_init(&sh.kpfull, 8);
     mbar_init(&sh.sfull, 8), mbar_init(&sh.sempty, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.drain[i], 1);
     sh.dead = 0;
     fence_mbar_init();
   }
@@ -237,49 +346,51 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs &a, unsigned char *ra
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
+  chain_wait();
+  if (warp == 4) {
+    bool there = false;
+    if (lane < kParts) there = part_at<kStates>(a, lane, sh.part[lane]);
+    const unsigned all = __ballot_sync(0xffffffffu, there);
+    if (lane == 0) sh.parts = __popc(all);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  chain_wait();
-
-  int len = a.lengths ? a.lengths[b] : a.T;
-  len = len < 0 ? 0 : len > a.T ? a.T : len;
-  const int t_lo = sg * a.seg, t_hi = min(t_lo + a.seg, a.T), t_end = min(t_hi, len);
-  const int chunks = t_end > t_lo ? (t_end - t_lo + kC - 1) / kC : 0;
-  const auto start_of = [&](int c) { return t_lo + (kReverse ? chunks - 1 - c : c) * kC; };
-  const float lg = fmaxf(log2f(a.decay[h]), kLogZero);
-  const bool two = lg != 0.f || p.kvs != 1.f;  // else K' is K itself
+  const int parts = sh.parts;
+  const auto tile_q = [&](int slot) { return base + kOffQ + slot * kTile; };
+  const auto tile_k = [&](int slot) { return base + (kStates ? 2 * slot * kTile : kOffK + slot * kTile); };
+  const auto tile_v = [&](int slot) { return base + (kStates ? (2 * slot + 1) * kTile : kOffV + slot * kTile); };
+  const auto cols_kp = [&](int buf) { return buf ? kG : kHi; };  // K' hi, lo 64 columns on
+  const auto cols_ds = [&](int buf) { return buf ? kO : kDs; };
+  bool ok = true;
 
   if (warp == 0) {
-    bool ok = true;
-    int issued = 0;
-    if (elect_one()) {
-      if (!kStates) tma_prefetch_desc(&p.q);
-      tma_prefetch_desc(&p.k);
-      tma_prefetch_desc(&p.v);
-    }
-    for (int c = 0; c < chunks; ++c, ++issued) {
-      const int slot = c & 1, t0 = start_of(c);
-      const uint32_t phase = (uint32_t)(c >> 1) & 1u ^ 1u;
-      // (a tile of each, in the order in which they are wanted)
+    Turn<kRing> g;
+    for (int n = 0; ok && n < parts; ++n) {
+      const Part &t = sh.part[n];
+      const TcPass &p = a.pass[t.pass];
+      const int b = t.b, h = t.h, c0 = t.c0, to = t.to, step = p.reverse ? -kC : kC;
+      int t0 = t.t_lo + (p.reverse ? t.chunks - 1 - t.from : t.from) * kC;
+      for (int c = t.from; ok && c < to; ++c, g.next(), t0 += step) {
+        // (a tile of each, in the order in which they are wanted)
 #pragma unroll 1
-      for (int i = 0; ok && i < 3; ++i) {
-        if (kStates && i == 1) continue;
-        const CUtensorMap *map = i == 0 ? &p.k : i == 1 ? &p.q : &p.v;
-        uint64_t *full = i == 0 ? &sh.kfull[slot] : i == 1 ? &sh.qfull[slot] : &sh.vfull[slot];
-        uint64_t *empty = i == 0 ? &sh.kempty[slot] : i == 1 ? &sh.qempty[slot] : &sh.vempty[slot];
-        unsigned char *to = base + (i == 0 ? kOffK : i == 1 ? kOffQ : kOffV) + slot * kTile;
-        if (!(ok = wait(&sh, empty, phase, 0))) break;
-        if (elect_one()) {
-          const int d0 = i == 2 ? c0 : 0;
-          mbar_arrive_expect_tx(full, kTile);
-          tma_load_4d(to, map, full, d0, h, t0, b);
-          tma_load_4d(to + kBlk, map, full, d0 + 64, h, t0, b);
+        for (int i = 0; i < 3; ++i) {
+          if (kStates && i == 1) continue;
+          const CUtensorMap *map = i == 0 ? &p.k : i == 1 ? &p.q : &p.v;
+          uint64_t *full = i == 0 ? &sh.kfull[g.slot] : i == 1 ? &sh.qfull[g.slot] : &sh.vfull[g.slot];
+          uint64_t *empty = i == 0 ? &sh.kempty[g.slot] : i == 1 ? &sh.qempty[g.slot] : &sh.vempty[g.slot];
+          unsigned char *tile = i == 0 ? tile_k(g.slot) : i == 1 ? tile_q(g.slot) : tile_v(g.slot);
+          if (!(ok = wait(&sh, empty, g.phase ^ 1u, 0))) break;
+          if (elect_one()) {
+            const int d0 = i == 2 ? c0 : 0;
+            mbar_arrive_expect_tx(full, kTile);
+            tma_load_4d(tile, map, full, d0, h, t0, b);
+            tma_load_4d(tile + kBlk, map, full, d0 + 64, h, t0, b);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
-      if (!ok) break;
     }
     // winding down: what is in flight lands first (a tile that was never asked
     // for lets its wait run out)
@@ -287,243 +398,263 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs &a, unsigned char *ra
 #pragma unroll 1
       for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
-  } else if (warp == 1 || warp == 3) {
-    const uint32_t nv = (uint32_t)(cols + 15) & ~15u;
-    const int ksteps = (dk + 15) / 16;
-    const uint32_t id_g = idesc_bf16(kC, kC, false, false), id_v = idesc_bf16(128, (int)nv, false, true);
-    bool ok = true;
-    // K-major: 16 channels are 32 bytes of a 128-byte row
-    const auto step_k = [](int k) { return (uint64_t)((k >> 2) * kBlk + (k & 3) * 32) >> 4; };
-    for (int c = 0; ok && c < chunks; ++c) {
-      const int slot = c & 1;
-      const uint32_t ph = (uint32_t)(c >> 1) & 1u, one = (uint32_t)c & 1u;
-      const uint64_t dq = sdesc_sw128(smem_u32(base + kOffQ + slot * kTile), 0, 1024);
-      // MN-major: 16 tokens are 16 rows of 128 bytes
-      const uint64_t dvv = sdesc_sw128(smem_u32(base + kOffV + slot * kTile), kBlk, 1024);
-      if (warp == 1) {
-        if constexpr (!kStates) {  // (G is written over P, which this warp's products before have read)
-          if (!(ok = wait(&sh, &sh.qfull[slot], ph, 1) && wait(&sh, &sh.kfull[slot], ph, 1))) break;
+  } else if (warp == 1) {
+    if constexpr (!kStates) {
+      Turn<kRing> g;
+      Turn<1> o;
+      for (int n = 0; ok && n < parts; ++n) {
+        const Part &t = sh.part[n];
+        const TcPass &p = a.pass[t.pass];
+        const uint32_t nv = (uint32_t)(min(kD, p.dv - t.c0) + 15) & ~15u;
+        const int ksteps = (p.dk + 15) / 16, to = t.to;
+        constexpr uint32_t id_g = idesc_bf16(kC, kC, false, false);
+        const uint32_t id_v = idesc_bf16(128, (int)nv, false, true);
+        for (int c = t.from; c < to; ++c, g.next(), o.next()) {
+          // G (over P, which this warp's products before have read)
+          if (!(ok = wait(&sh, &sh.qfull[g.slot], g.phase, 1) && wait(&sh, &sh.kfull[g.slot], g.phase, 1))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t dkk = sdesc_sw128(smem_u32(base + kOffK + slot * kTile), 0, 1024);
+            const uint64_t dq = sdesc_sw128(smem_u32(tile_q(g.slot)), 0, 1024);
+            const uint64_t dkk = sdesc_sw128(smem_u32(tile_k(g.slot)), 0, 1024);
 #pragma unroll 1
             for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kG, dq + step_k(k), dkk + step_k(k), id_g, k > 0);
             mma_commit(&sh.gfull);
-            mma_commit(&sh.kempty[slot]);
-            mma_commit(&sh.qempty[slot]);
+            mma_commit(&sh.kempty[g.slot]);
+            mma_commit(&sh.qempty[g.slot]);
           }
           __syncwarp();
-          // (sempty: Q S is in O; V has been waited for by the other issuer before)
-          if (!(ok = wait(&sh, &sh.pfull, one, 1) && wait(&sh, &sh.sempty, one, 1) && wait(&sh, &sh.vfull[slot], ph, 1)))
+          // P V, after Q S (sempty)
+          if (!(ok = wait(&sh, &sh.pfull, o.phase, 1) && wait(&sh, &sh.sempty, o.phase, 1) &&
+                     wait(&sh, &sh.vfull[g.slot], g.phase, 1)))
             break;
           tc_fence_after();
           if (elect_one()) {
+            // MN-major: 16 tokens are 16 rows of 128 bytes
+            const uint64_t dvv = sdesc_sw128(smem_u32(tile_v(g.slot)), kBlk, 1024);
 #pragma unroll 1
             for (int k = 0; k < 8; ++k)
               mma_ts(tmem + kO, tmem + kG + 32 * (k >> 1) + 8 * (k & 1), dvv + (uint64_t)(k * 2048 >> 4), id_v, true);
             mma_commit(&sh.ofull);
-            mma_commit(&sh.vempty[slot]);
+            mma_commit(&sh.vempty[g.slot]);
           }
           __syncwarp();
         }
-      } else {
-        if (!(ok = wait(&sh, &sh.kpfull, one, 2) && wait(&sh, &sh.vfull[slot], ph, 2) &&
-                   (c == 0 || wait(&sh, &sh.dsempty, one ^ 1u, 2))))
+      }
+      if (!ok) drain(&sh.drain[0]);
+    }
+  } else if (warp == 3) {
+    Turn<kRing> g;
+    Turn<kBufs> u;
+    Turn<1> o;
+    int gone = 0;  // chunks before, up to kBufs
+    for (int n = 0; ok && n < parts; ++n) {
+      const Part &t = sh.part[n];
+      const TcPass &p = a.pass[t.pass];
+      const uint32_t nv = (uint32_t)(min(kD, p.dv - t.c0) + 15) & ~15u;
+      const int ksteps = (p.dk + 15) / 16, steps = t.two ? 16 : 8, to = t.to;
+      const uint32_t id_v = idesc_bf16(128, (int)nv, false, true);
+      for (int c = t.from; c < to; ++c, g.next(), u.next(), o.next()) {
+        if (!(ok = wait(&sh, &sh.kpfull[u.slot], u.phase, 2) && wait(&sh, &sh.vfull[g.slot], g.phase, 2) &&
+                   (gone < kBufs || wait(&sh, &sh.dsempty[u.slot], u.phase ^ 1u, 2))))
           break;
         tc_fence_after();
         if (elect_one()) {
-          const int parts = two ? 16 : 8;
+          const uint64_t dvv = sdesc_sw128(smem_u32(tile_v(g.slot)), kBlk, 1024);
+          const uint32_t kp = tmem + cols_kp(u.slot), ds = tmem + cols_ds(u.slot);
 #pragma unroll 1
-          for (int k = 0; k < parts; ++k)  // hi's 8 steps of 16 tokens, lo's 8
-            mma_ts(tmem + kDs, tmem + kHi + 8 * k, dvv + (uint64_t)((k & 7) * 2048 >> 4), id_v, k > 0);
-          mma_commit(&sh.dsfull);
-          mma_commit(&sh.vempty[slot]);
+          for (int k = 0; k < steps; ++k)  // hi's 8 steps of 16 tokens, lo's 8
+            mma_ts(ds, kp + 8 * k, dvv + (uint64_t)((k & 7) * 2048 >> 4), id_v, k > 0);
+          mma_commit(&sh.dsfull[u.slot]);
+          mma_commit(&sh.vempty[g.slot]);
         }
         __syncwarp();
         if constexpr (!kStates) {
-          if (!(ok = wait(&sh, &sh.sfull, one, 2) && (c == 0 || wait(&sh, &sh.oempty, one ^ 1u, 2)) &&
-                     wait(&sh, &sh.qfull[slot], ph, 2)))
+          if (!(ok = wait(&sh, &sh.sfull, o.phase, 2) && (gone == 0 || wait(&sh, &sh.oempty, o.phase ^ 1u, 2)) &&
+                     wait(&sh, &sh.qfull[g.slot], g.phase, 2)))
             break;
           tc_fence_after();
           if (elect_one()) {
+            const uint64_t dq = sdesc_sw128(smem_u32(tile_q(g.slot)), 0, 1024);
             const uint64_t ds = sdesc_sw128(smem_u32(base + kOffS), kBlk, 1024);
 #pragma unroll 1
             for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kO, dq + step_k(k), ds + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
             mma_commit(&sh.sempty);
-            mma_commit(&sh.qempty[slot]);
+            mma_commit(&sh.qempty[g.slot]);
           }
           __syncwarp();
         }
+        if (gone < kBufs) ++gone;
       }
     }
-    if (!ok) {  // products in flight end before TMEM is given back
-      uint64_t *drain = &sh.drain[warp >> 1];
-      if (elect_one()) mma_commit(drain);
-      for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(drain, 0); ++j) {
-      }
-    }
-  } else if (warp >= 4 && warp < 12) {
+    if (!ok) drain(&sh.drain[1]);
+  } else if (warp == 2) {
+    if constexpr (!kStates)
+      for (int n = 0; n < parts; ++n) zero_rest(a, sh.part[n], 0, lane);
+  } else if (warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) / 4;
     const int row = quarter * 32 + lane;
-    const float s16 = ex2(16.f * lg);
-    const uint64_t step16 = pk(s16, s16);
-    // K' of chunk c: this warp's 32 channels, half of the tokens
-    const auto keys = [&](int c) {
-      const int slot = c & 1, n = min(kC, t_end - start_of(c));
-      const uint32_t ph = (uint32_t)(c >> 1) & 1u;
-      if (!wait(&sh, &sh.kfull[slot], ph, 4)) return false;
-      if (n < kC) {
-        // tokens past the row's end: their values take no part, whatever they are
-        if (!wait(&sh, &sh.vfull[slot], ph, 4)) return false;
-        for (int r = n + warp - 4; r < kC; r += 8)
-          if (lane < 16)
-            *reinterpret_cast<uint4 *>(base + kOffV + slot * kTile + (lane >> 3) * kBlk + r * 128 + (lane & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-      }
-      // Tiles of 8 tokens x 8 channels, transposed by the load: a lane gets channel
-      // lane / 4 of tokens 2 (lane % 4) and the next one.  That is what a 16-lane
-      // store to TMEM takes, tokens 8 i.. in register pair i.
-      const uint32_t tile = smem_u32(base + kOffK + slot * kTile);
-      // 16 tokens x 16 channels a turn, from the heaviest tokens on: the next ones' weights
-      // are these times g^16, which can only vanish
-      const int j0 = half * 64 + 2 * (lane & 3);  // of the lane's first pair, and 8 on its second
-      uint64_t w[2];
-#pragma unroll 1
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const int i = kReverse ? i4 : 3 - i4;
-        const uint32_t tok = (uint32_t)(half * 64 + i * 16 + (lane >> 4) * 8 + (lane & 7));
-        if (i4 == 0 || n < kC) {
+    Turn<kRing> g;
+    Turn<kBufs> u;
+    Turn<1> o;
+    int gone = 0;
+    const auto share = [&](const Part &t, auto direction) {
+      constexpr bool kReverse = decltype(direction)::value;
+      const float lg = t.lg, kvs = a.pass[t.pass].kvs;
+      const bool two = t.two;
+      const float s16 = ex2(16.f * lg);
+      const uint64_t step16 = pk(s16, s16);
+      uint64_t c2[4];  // (see scores)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int j = j0 + i * 16 + 8 * y;
-            const int e = kReverse ? j + 1 : max(n - 1 - j, 0), f = kReverse ? j + 2 : max(n - 2 - j, 0);
-            w[y] = pk(ex2(lg * (float)e) * p.kvs, ex2(lg * (float)f) * p.kvs);
-          }
-        }
-        uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      for (int i = 0; i < 4; ++i)
+        c2[i] = kReverse ? pk(ex2(-lg * (float)(7 - 2 * i)), ex2(-lg * (float)(6 - 2 * i)))
+                         : pk(ex2(-lg * (float)(2 * i)), ex2(-lg * (float)(2 * i + 1)));
+      const int to = t.to;
+      int left = t.t_end - t.t_lo - (kReverse ? t.chunks - 1 - t.from : t.from) * kC;  // tokens from the chunk's first on
+      for (int c = t.from; c < to; ++c, left += kReverse ? kC : -kC) {
+        const int n = min(kC, left);
+        // ---- K': this warp's 32 channels, half of the tokens
+        if (!wait(&sh, &sh.kfull[g.slot], g.phase, 4)) return false;
         if (n < kC) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int j = j0 + i * 16 + 8 * y;
-            mask[y] = (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
-          }
+          // tokens past the row's end: their values take no part, whatever they are
+          if (!wait(&sh, &sh.vfull[g.slot], g.phase, 4)) return false;
+          for (int r = n + warp - 4; r < kC; r += 8)
+            if (lane < 16)
+              *reinterpret_cast<uint4 *>(tile_v(g.slot) + (lane >> 3) * kBlk + r * 128 + (lane & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
         }
-#pragma unroll
-        for (int d16 = 0; d16 < 2; ++d16) {  // of the warp's 32 channels
-          const uint32_t ch = (uint32_t)(quarter * 32 + d16 * 16 + ((lane >> 3) & 1) * 8);
-          uint32_t x[4], hi[4], lo[4];
-          ldsm_x4_trans(tile + (ch >> 6) * kBlk + piece_at(tok, (ch & 63) >> 3), x);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint64_t v = mul2(widen2(x[g] & mask[g >> 1]), w[g >> 1]);
-            hi[g] = narrow2(v);
-            lo[g] = narrow2(sub2(v, widen2(hi[g])));
-          }
-          if (i4 == 0 && d16 == 0 && c > 0) {  // the K' before has been read
-            if (!wait(&sh, &sh.dsfull, (uint32_t)(c - 1) & 1u, 4)) return false;
-            tc_fence_after();
-          }
-          const uint32_t to = tmem_addr(tmem, quarter * 32 + d16 * 16, kHi + half * 32 + i * 8);
-          tmem_st16x128b_x2(to, hi);
-          if (two) tmem_st16x128b_x2(to + (kLo - kHi), lo);
-        }
-        w[0] = mul2(w[0], step16), w[1] = mul2(w[1], step16);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.kpfull), mbar_arrive(&sh.kempty[slot]);
-      return true;
-    };
-    const bool steep = lg < -16.f;  // 2^(-7 lg) would leave float32's range
-    uint64_t c2[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c2[i] = kReverse ? pk(ex2(-lg * (float)(7 - 2 * i)), ex2(-lg * (float)(6 - 2 * i)))
-                        : pk(ex2(-lg * (float)(2 * i)), ex2(-lg * (float)(2 * i + 1)));
-    // P of chunk c: this lane's row, every second block of 32 columns
-    const auto scores = [&](int c) {
-      const int n = min(kC, t_end - start_of(c));
-      if (!wait(&sh, &sh.gfull, (uint32_t)c & 1u, 3)) return false;
-      tc_fence_after();
-      // P = G 2^(lg |row - j| - log2 c_row).  The power is taken for one column of
-      // eight, the one furthest from the row's own, and times eight constants 2^(-lg i):
-      // below 2^-126 it is nothing beside the row's own 2^-log2 c_row.
-      const float cp = fmaxf(lg * (float)(kReverse ? n - 1 - row : row + 1), kFloor);
-      const int lo = kReverse ? row : 0, hi = kReverse ? n - 1 : row;  // the columns that count
+        // Tiles of 8 tokens x 8 channels, transposed by the load: a lane gets channel
+        // lane / 4 of tokens 2 (lane % 4) and the next one.  That is what a 16-lane
+        // store to TMEM takes, tokens 8 i.. in register pair i.  16 tokens x 16 channels
+        // at a time, from the heaviest tokens on: the next ones' weights are these times
+        // g^16, which can only vanish.
+        const uint32_t tile = smem_u32(tile_k(g.slot));
+        const int j0 = half * 64 + 2 * (lane & 3);  // of the lane's first pair, and 8 on its second
+        uint64_t w[2];
 #pragma unroll 1
-      for (int i16 = 0; i16 < 4; ++i16) {  // 16 columns of the blocks half and half + 2
-        const int blk = half * 32 + (i16 >> 1) * 64, j0 = blk + (i16 & 1) * 16;
-        uint32_t out[8];
-        // (whole warps: these columns are past every row of the warp, or before)
-        const bool none = kReverse ? j0 + 15 < quarter * 32 || j0 >= n : j0 > quarter * 32 + 31;
-        if (none) {
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const int i = kReverse ? i4 : 3 - i4;
+          const uint32_t tok = (uint32_t)(half * 64 + i * 16 + (lane >> 4) * 8 + (lane & 7));
+          if (i4 == 0 || n < kC) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) out[i] = 0u;
-        } else {
-          uint32_t g[16];
-          tmem_ld16(tmem_addr(tmem, quarter * 32, kG + j0), g);
-          tmem_wait_ld_regs(g);
-          if (steep) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float apart = kReverse ? (float)(j0 + i - row) : (float)(row - j0 - i);
-              g[i] = __float_as_uint(__uint_as_float(g[i]) * (ex2(fmaf(lg, apart, -cp)) * p.kvs));
+            for (int y = 0; y < 2; ++y) {
+              const int j = j0 + i * 16 + 8 * y;
+              const int e = kReverse ? j + 1 : max(n - 1 - j, 0), f = kReverse ? j + 2 : max(n - 2 - j, 0);
+              w[y] = pk(ex2(lg * (float)e) * kvs, ex2(lg * (float)f) * kvs);
             }
-          } else {
+          }
+          uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+          if (n < kC) {
 #pragma unroll
-            for (int b8 = 0; b8 < 2; ++b8) {
-              const int j = j0 + 8 * b8 + (kReverse ? 7 : 0);
-              const float first = ex2(fmaf(lg, (float)(kReverse ? j - row : row - j), -cp)) * p.kvs;
-              const uint64_t f2 = pk(first, first);
+            for (int y = 0; y < 2; ++y) {
+              const int j = j0 + i * 16 + 8 * y;
+              mask[y] = (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+            }
+          }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint64_t v = mul2(pk(g[8 * b8 + 2 * i], g[8 * b8 + 2 * i + 1]), mul2(f2, c2[i]));
-                asm("mov.b64 {%0, %1}, %2;" : "=r"(g[8 * b8 + 2 * i]), "=r"(g[8 * b8 + 2 * i + 1]) : "l"(v));
+          for (int d16 = 0; d16 < 2; ++d16) {  // of the warp's 32 channels
+            const uint32_t ch = (uint32_t)(quarter * 32 + d16 * 16 + ((lane >> 3) & 1) * 8);
+            uint32_t x[4], hi[4], lo[4];
+            ldsm_x4_trans(tile + (ch >> 6) * kBlk + piece_at(tok, (ch & 63) >> 3), x);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint64_t v = mul2(widen2(x[y] & mask[y >> 1]), w[y >> 1]);
+              hi[y] = narrow2(v);
+              lo[y] = narrow2(sub2(v, widen2(hi[y])));
+            }
+            if (i4 == 0 && d16 == 0) {  // what lay here has been read
+              if (gone == kBufs) {
+                if (!wait(&sh, &sh.dsfull[u.slot], u.phase ^ 1u, 4)) return false;
+                tc_fence_after();
+              } else {
+                ++gone;
               }
             }
+            const uint32_t at = tmem_addr(tmem, quarter * 32 + d16 * 16, cols_kp(u.slot) + half * 32 + i * 8);
+            tmem_st16x128b_x2(at, hi);
+            if (two) tmem_st16x128b_x2(at + 64, lo);
           }
-          // (most pieces have no columns that do not count)
-          if (kReverse ? j0 < quarter * 32 + 31 || j0 + 15 >= n : j0 + 15 > quarter * 32) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (j0 + i < lo || j0 + i > hi) g[i] = 0u;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) out[i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+          w[0] = mul2(w[0], step16), w[1] = mul2(w[1], step16);
         }
-        // over columns of the block that this warp has read
-        tmem_st8(tmem_addr(tmem, quarter * 32, kG + blk + (i16 & 1) * 8), out);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kpfull[u.slot]), mbar_arrive(&sh.kempty[g.slot]);
+        // ---- P: this lane's row, every second block of 32 columns
+        if constexpr (!kStates) {
+          if (!wait(&sh, &sh.gfull, o.phase, 3)) return false;
+          tc_fence_after();
+          // P = G 2^(lg |row - j| - log2 c_row).  The power is taken for one column of
+          // eight, the one furthest from the row's own, and times eight constants
+          // 2^(-lg i): below 2^-126 it is nothing beside the row's own 2^-log2 c_row.
+          const float cp = fmaxf(lg * (float)(kReverse ? n - 1 - row : row + 1), kFloor);
+          const int lo = kReverse ? row : 0, hi = kReverse ? n - 1 : row;  // the columns that count
+#pragma unroll 1
+          for (int i16 = 0; i16 < 4; ++i16) {  // 16 columns of the blocks half and half + 2
+            const int blk = half * 32 + (i16 >> 1) * 64, j1 = blk + (i16 & 1) * 16;
+            uint32_t out[8];
+            // (whole warps: these columns are past every row of the warp, or before)
+            const bool none = kReverse ? j1 + 15 < quarter * 32 || j1 >= n : j1 > quarter * 32 + 31;
+            if (none) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) out[i] = 0u;
+            } else {
+              uint32_t s[16];
+              tmem_ld16(tmem_addr(tmem, quarter * 32, kG + j1), s);
+              tmem_wait_ld_regs(s);
+              if (lg < -16.f) {  // 2^(-7 lg) would leave float32's range
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float apart = kReverse ? (float)(j1 + i - row) : (float)(row - j1 - i);
+                  s[i] = __float_as_uint(__uint_as_float(s[i]) * (ex2(fmaf(lg, apart, -cp)) * kvs));
+                }
+              } else {
+#pragma unroll
+                for (int b8 = 0; b8 < 2; ++b8) {
+                  const int j = j1 + 8 * b8 + (kReverse ? 7 : 0);
+                  const float first = ex2(fmaf(lg, (float)(kReverse ? j - row : row - j), -cp)) * kvs;
+                  const uint64_t f2 = pk(first, first);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint64_t v = mul2(pk(s[8 * b8 + 2 * i], s[8 * b8 + 2 * i + 1]), mul2(f2, c2[i]));
+                    asm("mov.b64 {%0, %1}, %2;" : "=r"(s[8 * b8 + 2 * i]), "=r"(s[8 * b8 + 2 * i + 1]) : "l"(v));
+                  }
+                }
+              }
+              // (most pieces have no columns that do not count)
+              if (kReverse ? j1 < quarter * 32 + 31 || j1 + 15 >= n : j1 + 15 > quarter * 32) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (j1 + i < lo || j1 + i > hi) s[i] = 0u;
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) out[i] = pack_bf16(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+            }
+            // over columns of the block that this warp has read
+            tmem_st8(tmem_addr(tmem, quarter * 32, kG + blk + (i16 & 1) * 8), out);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.pfull);
+        }
+        g.next(), u.next(), o.next();
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.pfull);
       return true;
     };
-    for (int c = 0; c < chunks; ++c)
-      if (!keys(c) || (!kStates && !scores(c))) break;
-  } else if (warp >= 12) {
-    const int quarter = warp & 3, d = quarter * 32 + lane, half = (warp - 12) / 4;
-    const int v0 = c0 + half * 64, live = d < dk ? min(64, p.dv - v0) : 0;  // this lane's columns of the state
-    const int64_t n_state = (int64_t)dk * p.dv;
-    uint64_t S[32];  // pairs of columns
-#pragma unroll
-    for (int i = 0; i < 32; ++i) S[i] = 0;
-    if (!kStates && p.init) {
-      const float *from = p.init + (a.nseg > 1 ? (int64_t)bh * a.nseg + sg : bh) * n_state;
-      if (p.init_t) {
-        from += (int64_t)v0 * dk + d;
-#pragma unroll
-        for (int i = 0; i < 32; ++i, from += 2 * dk)  // (an even number of columns)
-          if (2 * i < live) S[i] = pk(from[0], from[dk]);
-      } else {
-        from += (int64_t)d * p.dv + v0;
-        load_row(S, from, live);
-      }
+    for (int n = 0; ok && n < parts; ++n) {
+      const Part &t = sh.part[n];
+      ok = a.pass[t.pass].reverse ? share(t, Bool<true>{}) : share(t, Bool<false>{});
+      if constexpr (!kStates) zero_rest(a, t, warp - 3, lane);
     }
-    const auto publish = [&] {
+  } else {
+    const int quarter = warp & 3, half = (warp - 12) / 4, d = quarter * 32 + lane;
+    Turn<kBufs> u;
+    Turn<1> o;
+    bool begun = false;
+    uint64_t S[32];  // pairs of columns
+    const auto publish = [&] {  // the bfloat16 copy that Q S reads, once the one before has been read
+      if (begun && !wait(&sh, &sh.sempty, o.phase ^ 1u, 5)) return false;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         *reinterpret_cast<uint4 *>(base + kOffS + half * kBlk + piece_at(d, i)) =
@@ -531,80 +662,127 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs &a, unsigned char *ra
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sfull);
+      return true;
     };
-    if (!kStates) publish();
-    uint64_t keep_a = 0;  // of a chunk of `kept` tokens
-    bool near = false;
-    int kept = -1;
-    bool ok = true;
-    for (int c = 0; c < chunks; ++c) {
-      const int n = min(kC, t_end - start_of(c));
-      if (n != kept) {  // (whole chunks, and the last)
-        const decay::Keep keep = decay::keep_of(lg, n);
-        keep_a = pk(keep.a, keep.a), near = keep.b != 0.f;
-        kept = n;
-      }
-      if (!(ok = wait(&sh, &sh.dsfull, (uint32_t)c & 1u, 5))) break;
-      tc_fence_after();
+    for (int m = 0; ok && m < parts; ++m) {
+      const Part &t = sh.part[m];
+      const TcPass &p = a.pass[t.pass];
+      const int v0 = t.c0 + half * 64, live = d < p.dk ? min(64, p.dv - v0) : 0;  // this lane's columns
+      if (t.head) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t r[16];
-        tmem_ld16(tmem_addr(tmem, quarter * 32, kDs + half * 64 + 16 * j), r);
-        tmem_wait_ld_regs(r);
+        for (int i = 0; i < 32; ++i) S[i] = 0;
+        if (!kStates && p.init) {
+          const float *from = p.init + t.state * p.dk * p.dv;
+          if (p.init_t) {
+            from += (int64_t)v0 * p.dk + d;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t x = pk(r[2 * i], r[2 * i + 1]);
-          S[8 * j + i] = fma2(keep_a, S[8 * j + i], near ? add2(S[8 * j + i], x) : x);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.dsempty);
-      if constexpr (!kStates) {
-        if (c + 1 < chunks) {
-          if (!(ok = wait(&sh, &sh.sempty, (uint32_t)c & 1u, 5))) break;
-          publish();
-        }
-        // O, this half of its columns: a token a lane
-        if (!(ok = wait(&sh, &sh.ofull, (uint32_t)c & 1u, 5))) break;
-        tc_fence_after();
-        const int t0 = start_of(c), row = quarter * 32 + lane;
-        const float cp = p.os * ex2(fmaxf(lg * (float)(kReverse ? n - 1 - row : row + 1), kFloor));
-        const uint64_t cp2 = pk(cp, cp);
-        __nv_bfloat16 *to = p.to + (((int64_t)b * a.T + t0 + row) * a.H + h) * p.dv + v0;
-        const int have = t0 + row < t_hi ? p.dv - v0 : 0;
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint32_t o[16], w[8];
-          tmem_ld16(tmem_addr(tmem, quarter * 32, kO + half * 64 + 16 * j), o);
-          tmem_wait_ld_regs(o);
-          if (j == 3) {  // O may be written again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.oempty);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = row < n ? narrow2(mul2(pk(o[2 * i], o[2 * i + 1]), cp2)) : 0u;
-          if (p.wide && 16 * j + 16 <= have) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * j), "r"(w[0]),
-                         "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                         : "memory");
+            for (int i = 0; i < 32; ++i, from += 2 * p.dk)  // (an even number of columns)
+              if (2 * i < live) S[i] = pk(from[0], from[p.dk]);
           } else {
-            if (16 * j + 8 <= have) *reinterpret_cast<uint4 *>(to + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (16 * j + 16 <= have) *reinterpret_cast<uint4 *>(to + 16 * j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            load_row(S, from + (int64_t)d * p.dv + v0, live);
+          }
+        }
+      } else {  // from the CTA before
+        if (!(ok = wait_flag(&sh, a.flags + (blockIdx.x - a.passes) * 8 + (warp - 12)))) break;
+        const float4 *from = a.handed + ((int64_t)(blockIdx.x - a.passes) * 8 + (warp - 12)) * 512 + lane;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 v = __ldcg(from + i * 32);
+          S[2 * i] = pk(v.x, v.y), S[2 * i + 1] = pk(v.z, v.w);
+        }
+      }
+      const int to = t.to;
+      if (!kStates && t.from < to && !(ok = publish())) break;
+      const float lg = t.lg;
+      uint64_t keep_a = 0;  // of a chunk of `kept` tokens
+      bool near = false;
+      int kept = -1;
+      const int first = p.reverse ? t.chunks - 1 - t.from : t.from, step = p.reverse ? -kC : kC;
+      int left = t.t_end - t.t_lo - first * kC, rest = t.t_hi - t.t_lo - first * kC - (quarter * 32 + lane);
+      __nv_bfloat16 *out = kStates ? nullptr
+                                   : p.to + (((int64_t)t.b * a.T + t.t_lo + (int64_t)first * kC + quarter * 32 + lane) * a.H + t.h) * p.dv + v0;
+      const int64_t hop = (int64_t)step * a.H * p.dv;
+      for (int c = t.from; c < to; ++c, left -= step, rest -= step, out += hop) {
+        const int n = min(kC, left);
+        if (n != kept) {  // (whole chunks, and the last)
+          const decay::Keep keep = decay::keep_of(lg, n);
+          keep_a = pk(keep.a, keep.a), near = keep.b != 0.f;
+          kept = n;
+        }
+        if (!(ok = wait(&sh, &sh.dsfull[u.slot], u.phase, 5))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t r[16];
+          tmem_ld16(tmem_addr(tmem, quarter * 32, cols_ds(u.slot) + half * 64 + 16 * j), r);
+          tmem_wait_ld_regs(r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t x = pk(r[2 * i], r[2 * i + 1]);
+            S[8 * j + i] = fma2(keep_a, S[8 * j + i], near ? add2(S[8 * j + i], x) : x);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.dsempty[u.slot]);
+        u.next();
+        if constexpr (!kStates) {
+          const uint32_t phase = o.phase;
+          o.next();
+          begun = true;
+          if (c + 1 < to && !(ok = publish())) break;
+          // O, this half of its columns: a token a lane
+          if (!(ok = wait(&sh, &sh.ofull, phase, 5))) break;
+          tc_fence_after();
+          const int row = quarter * 32 + lane;
+          const float cp = p.os * ex2(fmaxf(lg * (float)(p.reverse ? n - 1 - row : row + 1), kFloor));
+          const uint64_t cp2 = pk(cp, cp);
+          const int have = rest > 0 ? p.dv - v0 : 0;
+          const bool wide = p.wide;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[16], w[8];
+            tmem_ld16(tmem_addr(tmem, quarter * 32, kO + half * 64 + 16 * j), x);
+            tmem_wait_ld_regs(x);
+            if (j == 3) {  // O may be written again
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.oempty);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = row < n ? narrow2(mul2(pk(x[2 * i], x[2 * i + 1]), cp2)) : 0u;
+            if (wide && 16 * j + 16 <= have) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 16 * j), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                           : "memory");
+            } else {
+              if (16 * j + 8 <= have) *reinterpret_cast<uint4 *>(out + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+              if (16 * j + 16 <= have) *reinterpret_cast<uint4 *>(out + 16 * j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
       }
+      if (!ok) break;
+      if (!t.tail) {  // for the CTA after
+        float4 *to4 = a.handed + ((int64_t)blockIdx.x * 8 + (warp - 12)) * 512 + lane;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float4 v;
+          asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(S[2 * i]));
+          asm("mov.b64 {%0, %1}, %2;" : "=f"(v.z), "=f"(v.w) : "l"(S[2 * i + 1]));
+          __stcg(to4 + i * 32, v);
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flags + blockIdx.x * 8 + (warp - 12)), "r"(1u) : "memory");
+      } else if (p.final && t.last) {
+        // (with segments, the states' own pass has a place for each, the row one)
+        const int64_t at = kStates ? t.state : (int64_t)t.b * a.H + t.h;
+        store_row(S, p.final + at * p.dk * p.dv + (int64_t)d * p.dv + v0, live);
+      }
+      if constexpr (!kStates) zero_rest(a, t, warp - 3, lane);
     }
-    if (ok && (kStates || (p.final && sg == (kReverse ? 0 : a.nseg - 1)))) {
-      float *to = p.final + (kStates ? (int64_t)bh * a.nseg + sg : bh) * n_state + (int64_t)d * p.dv + v0;
-      store_row(S, to, live);
-    }
-  }
-  if constexpr (!kStates) {  // tokens past the row's end, in chunks that no tile reached
-    for (int t = t_lo + chunks * kC + warp; t < t_hi; t += kThreads / 32)
-      if (lane < cols / 8)
-        *reinterpret_cast<uint4 *>(p.to + (((int64_t)b * a.T + t) * a.H + h) * p.dv + c0 + lane * 8) = make_uint4(0, 0, 0, 0);
   }
   __syncwarp();
   tc_fence_before();
@@ -613,16 +791,10 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs &a, unsigned char *ra
   if (warp == 2) tmem_dealloc(tmem, 512);
 }
 
-template <bool kStates>
-__global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs a) {
-  extern __shared__ unsigned char raw[];
-  __shared__ Shared sh;
-  const uint32_t item = blockIdx.x / (uint32_t)a.passes;
-  const TcPass &p = a.pass[blockIdx.x % (uint32_t)a.passes];
-  if (p.reverse)
-    decay_tc_body<kStates, true>(a, raw, sh, item, p);
-  else
-    decay_tc_body<kStates, false>(a, raw, sh, item, p);
+int sm_count() {
+  int dev = 0, n = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
 }
 
 // [B][T][H][d] with strides as a 4-D tensor {d, H, T, B} in tiles of 64 channels x
@@ -641,6 +813,20 @@ cudaError_t make_map(CUtensorMap *map, const void *p, int64_t d, int64_t H, int6
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+int64_t tc_items(const DecayArgs &a) {
+  int dv = 1;
+  for (int i = 0; i < a.passes; ++i) dv = max(dv, a.pass[i].dv);
+  return a.B * a.H * ((dv + kD - 1) / kD) * a.nseg * a.passes;
+}
+// CTAs share items where that fills the last round.  Many rounds need it not, and rows of
+// differing lengths are better dealt out one by one.
+bool tc_shared(const DecayArgs &a) {
+  const int64_t items = tc_items(a), sms = sm_count();
+  return !a.lengths && items > sms && items <= (kParts - 4) * sms && (items + sms - 1) / sms * sms * 20 > items * 21;
+}
+int64_t flag_bytes(int sms) { return ((int64_t)sms * 32 + 255) / 256 * 256; }
+
+// (not launched as a dependent: it takes tensor memory before it waits)
 template <bool kStates>
 cudaError_t run(const DecayArgs &a, cudaStream_t s) {
   TcArgs t{};
@@ -660,13 +846,32 @@ cudaError_t run(const DecayArgs &a, cudaStream_t s) {
     const int g = (p.dv + kD - 1) / kD;
     if (g > t.groups) t.groups = g;
   }
-  const int64_t grid = a.B * a.H * t.groups * a.nseg * a.passes;
-  if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  const int64_t items = tc_items(a);
+  if (items >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  t.items = (uint32_t)items;
+  t.chunks = (int)(a.seg / kC);
   auto kern = decay_tc_kernel<kStates>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  // (not as a dependent: it takes tensor memory before it waits)
-  return chain_launch(kern, dim3((unsigned)grid), dim3(kThreads), kSmem, 1, false, s, t);
+  // CTAs that hand states to one another are resident together
+  const int sms = sm_count();
+  t.shared = tc_shared(a);
+  if (t.shared) {
+    t.flags = static_cast<uint32_t *>(a.handed);
+    t.handed = reinterpret_cast<float4 *>(static_cast<unsigned char *>(a.handed) + flag_bytes(sms));
+    if ((e = cudaMemsetAsync(t.flags, 0, (size_t)sms * 32, s)) != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(t.shared ? sms / a.passes * a.passes : items));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeCooperative;
+  at.val.cooperative = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = t.shared ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, t);
 }
 
 }  // namespace
@@ -687,6 +892,12 @@ bool decay_tc_fits(const DecayArgs &a) {
     if (p.dk > kD || p.dk % 8 || p.dv % 8 || !ok(p.q, p.qs) || !ok(p.k, p.ks) || !ok(p.v, p.vs)) return false;
   }
   return true;
+}
+
+// what CTAs hand over
+int64_t decay_tc_scratch(const DecayArgs &a) {
+  const int sms = sm_count();
+  return tc_shared(a) ? flag_bytes(sms) + (int64_t)sms * 65536 : 0;
 }
 
 cudaError_t launch_decay_tc(const DecayArgs &a, bool states, cudaStream_t s) {

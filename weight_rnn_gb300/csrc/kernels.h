@@ -175,6 +175,7 @@ struct DecayArgs {
   int64_t B, T, H, seg;
   int nseg;
   bool bf16;
+  void *handed;         // decay_tc_scratch() bytes for launch_decay_tc
 };
 constexpr int kDecayMaxD = 256;
 constexpr int kDecayChunk = 128;  // segments are multiples of it
@@ -184,6 +185,7 @@ cudaError_t launch_decay_states(const DecayArgs &a, cudaStream_t s);
 cudaError_t launch_decay(const DecayArgs &a, cudaStream_t s);
 // The same two on the tensor cores: bfloat16, what decay_tc_fits() allows.
 bool decay_tc_fits(const DecayArgs &a);
+int64_t decay_tc_scratch(const DecayArgs &a);
 cudaError_t launch_decay_tc(const DecayArgs &a, bool states, cudaStream_t s);
 cudaError_t read_and_clear_decay_error(unsigned int *word);
 // states [B][H][nseg][n]: every segment's own last state becomes the state that
