@@ -228,11 +228,15 @@ __global__ void __launch_bounds__(kThreads, kMost == 2 ? 2 : 1) decay_generic_ke
 #pragma unroll
     for (int i = 0; i < 2; ++i) nv[i] = on ? load4<In, kVec>(vrow + t * p.vs[1], (l8 + 8 * i) * 4, cols) : zero;
   };
+  Keep keep = {0.f, 0.f};  // of a chunk of `kept` tokens
+  float owed = 0.f;
+  int kept = -1;
   if (chunks > 0) ask(0);
   for (int64_t ci = 0; ci < chunks; ++ci) {
     const int64_t t0 = start_of(ci);
     const int n = (int)min((int64_t)kC, t_end - t0);
-    const Keep keep = keep_of(lg, n);
+    if (n != kept) keep = keep_of(lg, n), kept = n;
+    const float now = keep_now(keep, owed);
     __syncthreads();  // what the last chunk read may be written
     {
       const float w = p.kvs * power(lg, p.reverse ? row + 1 : n - 1 - row);  // to the chunk's end, or past its start
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, kMost == 2 ? 2 : 1) decay_generic_ke
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) st[i][x][y] = fmaf(keep.a, st[i][x][y], keep.b * st[i][x][y]);
+        for (int y = 0; y < 4; ++y) st[i][x][y] *= now;
       // (channels past the last vector of k lie in the next row: of no state that counts)
       const int d = min(64 * i + 4 * r16, ld - 4);
 #pragma unroll 4
@@ -412,6 +416,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(float *states, const fl
   len = len < 0 ? 0 : len > T ? T : len;
   const float lg = log2f(decay[bh % H]);
   const Keep whole = keep_of(lg, seg);
+  float owed = 0.f;
   Vec carry = {};
   if (init) carry = *reinterpret_cast<const Vec *>(init + bh * n + e);
   float *at = states + (int64_t)bh * nseg * n + e;
@@ -425,10 +430,10 @@ __global__ void __launch_bounds__(256) decay_join_kernel(float *states, const fl
       if (i0 + i >= nseg) break;
       const int sg = reverse ? nseg - 1 - i0 - i : i0 + i;
       const int64_t have = len - sg * seg;  // tokens of the row from the segment's first on
-      const Keep keep = have >= seg ? whole : keep_of(lg, have);
+      const float keep = keep_now(have >= seg ? whole : keep_of(lg, have), owed);
       *reinterpret_cast<Vec *>(at + sg * n) = carry;
 #pragma unroll
-      for (int j = 0; j < V; ++j) carry.v[j] = fmaf(keep.a, carry.v[j], fmaf(keep.b, carry.v[j], own[i].v[j]));
+      for (int j = 0; j < V; ++j) carry.v[j] = fmaf(keep, carry.v[j], own[i].v[j]);
     }
   }
 }

@@ -16,16 +16,25 @@ __device__ __forceinline__ float ex2(float x) {
 // error about 2^-22 and that of the exponent's product
 __device__ __forceinline__ float power(float lg, int e) { return e <= 0 ? 1.f : ex2(lg * (float)e); }
 
-// g^n as a factor of the state, chunk after chunk: S -> a S + b S.  Where it is near 1
-// its rounding would add up over all chunks that a state remembers, so it is split into
-// 1 and g^n - 1, whose rounding is as small as it is.
+// g^n as a factor of the state, chunk after chunk, a + b.  Rounded to one float32 its
+// error would add up over all chunks that a state remembers (3e-8 each, many where g is
+// near 1); so what a chunk's factor leaves out is owed to the next.
 struct Keep {
   float a, b;
 };
 __device__ __forceinline__ Keep keep_of(float lg, int64_t n) {
-  if (n <= 0) return {0.f, 1.f};
+  if (n <= 0) return {1.f, 0.f};
   const float x = lg * (float)n, k = exp2f(x);
-  return k > 0.5f ? Keep{expm1f(0.6931471805599453f * x), 1.f} : Keep{k, 0.f};
+  if (k <= 0.5f) return {k, 0.f};
+  const float m = expm1f(0.6931471805599453f * x), a = 1.f + m;  // (1 - a is exact)
+  return {a, (1.f - a) + m};
+}
+// the factor of the next chunk
+__device__ __forceinline__ float keep_now(const Keep &k, float &owed) {
+  owed += k.b;
+  const float now = k.a + owed;
+  owed -= now - k.a;
+  return now;
 }
 
 }  // namespace decay

@@ -55,10 +55,11 @@ int sm_count() {
 }
 
 // Into how many segments the time axis is cut.  On the tensor cores 128 tokens take a CTA
-// about 2.5 us with all products and 1.7 with those of the states alone, and CTAs share
-// the work evenly where there is more than a round of it; on the CUDA cores 36 and 12 us
-// at two CTAs an SM, in whole rounds.  A cut adds the pass for the states, its states'
-// way through memory, and two launches.
+// about 2.5 us with all products and 1.7 with those of the states alone, an item's start
+// and end 4 us, and CTAs share the work evenly where there is more than a round of it,
+// but for rows with lengths; on the CUDA cores 36 and 12 us at two CTAs an SM, in whole
+// rounds.  A cut adds the pass for the states, its states' way through memory, and two
+// launches.
 int segments(const DecayArgs &a, int64_t state_passes, bool tc) {
   const int64_t chunks = (a.T + delta::kDecayChunk - 1) / delta::kDecayChunk;
   const int width = tc ? 128 : 64;
@@ -70,16 +71,18 @@ int segments(const DecayArgs &a, int64_t state_passes, bool tc) {
   const int64_t state_items = state_passes * a.B * a.H * ((a.pass[0].dv + width - 1) / width);
   const auto up_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   const auto rounds = [&](int64_t n) {
-    return tc ? (n <= slots ? 1.0 : (double)n / (double)slots) : (double)up_div(n, slots);
+    return tc && !a.lengths && n > slots ? (double)n / (double)slots : (double)up_div(n, slots);
   };
+  const auto ends = [&](int64_t n) { return 4.0 * (double)up_div(n, slots); };
   int best = 1;
   double least = 1e30;
   for (int64_t n = 1; n <= chunks && n <= 256; ++n) {
     const int64_t each = up_div(chunks, n);
     if (up_div(chunks, each) != n) continue;  // every segment has tokens
     if (n > 1 && bytes * n > (int64_t(1) << 30)) break;
-    double us = rounds(items * n) * (double)each * whole;
-    if (n > 1) us += rounds(state_items * n) * (double)each * part + 9.0 + (double)(bytes * n) * 4 / 5e6;
+    double us = rounds(items * n) * (double)each * whole + ends(items * n);
+    if (n > 1)
+      us += rounds(state_items * n) * (double)each * part + ends(state_items * n) + 9.0 + (double)(bytes * n) * 4 / 5e6;
     if (us < 0.95 * least) least = us, best = (int)n;
   }
   return best;

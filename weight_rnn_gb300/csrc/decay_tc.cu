@@ -234,11 +234,6 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(pk(-1.f, -1.f)), "l"(a));
   return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -302,15 +297,14 @@ struct Turn {
   }
 };
 
-// tokens past a row's end, in chunks that no tile reached: a share of the rows a warp
+// tokens past a row's end, in chunks that no tile reached: every 17th row a warp
 __device__ __noinline__ void zero_rest(const TcArgs &a, const Part &t, int share, int lane) {
   const TcPass &p = a.pass[t.pass];
-  const int pieces = min(kD, p.dv - t.c0) / 8;
-  if (t.head)
-    for (int i = t.t_lo + t.chunks * kC + share; i < t.t_hi; i += 17)
-      if (lane < pieces)
-        *reinterpret_cast<uint4 *>(p.to + (((int64_t)t.b * a.T + i) * a.H + t.h) * p.dv + t.c0 + lane * 8) =
-            make_uint4(0, 0, 0, 0);
+  const int pieces = min(kD, p.dv - t.c0) / 8, first = t.t_lo + t.chunks * kC + share, t_hi = t.t_hi;
+  if (!t.head || lane >= pieces) return;
+  const int64_t row = (int64_t)a.H * p.dv;
+  __nv_bfloat16 *to = p.to + ((int64_t)t.b * a.T + first) * row + (int64_t)t.h * p.dv + t.c0 + lane * 8;
+  for (int i = first; i < t_hi; i += 17, to += 17 * row) *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
 }
 
 template <bool kIs>
@@ -543,22 +537,21 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
               w[y] = pk(ex2(lg * (float)e) * kvs, ex2(lg * (float)f) * kvs);
             }
           }
-          uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-          if (n < kC) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int j = j0 + i * 16 + 8 * y;
-              mask[y] = (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
-            }
-          }
 #pragma unroll
           for (int d16 = 0; d16 < 2; ++d16) {  // of the warp's 32 channels
             const uint32_t ch = (uint32_t)(quarter * 32 + d16 * 16 + ((lane >> 3) & 1) * 8);
             uint32_t x[4], hi[4], lo[4];
             ldsm_x4_trans(tile + (ch >> 6) * kBlk + piece_at(tok, (ch & 63) >> 3), x);
+            if (n < kC) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int j = j0 + i * 16 + 8 * (y >> 1);
+                x[y] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+              }
+            }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const uint64_t v = mul2(widen2(x[y] & mask[y >> 1]), w[y >> 1]);
+              const uint64_t v = mul2(widen2(x[y]), w[y >> 1]);
               hi[y] = narrow2(v);
               lo[y] = narrow2(sub2(v, widen2(hi[y])));
             }
@@ -588,7 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           // eight, the one furthest from the row's own, and times eight constants
           // 2^(-lg i): below 2^-126 it is nothing beside the row's own 2^-log2 c_row.
           const float cp = fmaxf(lg * (float)(kReverse ? n - 1 - row : row + 1), kFloor);
-          const int lo = kReverse ? row : 0, hi = kReverse ? n - 1 : row;  // the columns that count
 #pragma unroll 1
           for (int i16 = 0; i16 < 4; ++i16) {  // 16 columns of the blocks half and half + 2
             const int blk = half * 32 + (i16 >> 1) * 64, j1 = blk + (i16 & 1) * 16;
@@ -623,9 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
               }
               // (most pieces have no columns that do not count)
               if (kReverse ? j1 < quarter * 32 + 31 || j1 + 15 >= n : j1 + 15 > quarter * 32) {
+                // bit i: column j1 + i counts, up to the row's own, or from it to the last
+                const uint32_t upto = kReverse ? (n - j1 >= 16 ? 0xFFFFu : (1u << (n - j1)) - 1u)
+                                               : (row - j1 >= 15 ? 0xFFFFu : row < j1 ? 0u : (2u << (row - j1)) - 1u);
+                const uint32_t below = !kReverse || row <= j1 ? 0u : row - j1 >= 16 ? 0xFFFFu : (1u << (row - j1)) - 1u;
+                const uint32_t keep = upto & ~below;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  if (j1 + i < lo || j1 + i > hi) s[i] = 0u;
+                  if (!(keep >> i & 1u)) s[i] = 0u;
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i) out[i] = pack_bf16(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
@@ -694,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       const int to = t.to;
       if (!kStates && t.from < to && !(ok = publish())) break;
       const float lg = t.lg;
-      uint64_t keep_a = 0;  // of a chunk of `kept` tokens
-      bool near = false;
+      decay::Keep keep = {0.f, 0.f};  // of a chunk of `kept` tokens
+      float owed = 0.f;
       int kept = -1;
       const int first = p.reverse ? t.chunks - 1 - t.from : t.from, step = p.reverse ? -kC : kC;
       int left = t.t_end - t.t_lo - first * kC, rest = t.t_hi - t.t_lo - first * kC - (quarter * 32 + lane);
@@ -704,11 +701,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       const int64_t hop = (int64_t)step * a.H * p.dv;
       for (int c = t.from; c < to; ++c, left -= step, rest -= step, out += hop) {
         const int n = min(kC, left);
-        if (n != kept) {  // (whole chunks, and the last)
-          const decay::Keep keep = decay::keep_of(lg, n);
-          keep_a = pk(keep.a, keep.a), near = keep.b != 0.f;
-          kept = n;
-        }
+        if (n != kept) keep = decay::keep_of(lg, n), kept = n;  // (whole chunks, and the last)
+        const float k1 = decay::keep_now(keep, owed);
+        const uint64_t k2 = pk(k1, k1);
         if (!(ok = wait(&sh, &sh.dsfull[u.slot], u.phase, 5))) break;
         tc_fence_after();
 #pragma unroll
@@ -717,10 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           tmem_ld16(tmem_addr(tmem, quarter * 32, cols_ds(u.slot) + half * 64 + 16 * j), r);
           tmem_wait_ld_regs(r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t x = pk(r[2 * i], r[2 * i + 1]);
-            S[8 * j + i] = fma2(keep_a, S[8 * j + i], near ? add2(S[8 * j + i], x) : x);
-          }
+          for (int i = 0; i < 8; ++i) S[8 * j + i] = fma2(k2, S[8 * j + i], pk(r[2 * i], r[2 * i + 1]));
         }
         tc_fence_before();
         __syncwarp();
@@ -750,7 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
               if (lane == 0) mbar_arrive(&sh.oempty);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = row < n ? narrow2(mul2(pk(x[2 * i], x[2 * i + 1]), cp2)) : 0u;
+            for (int i = 0; i < 8; ++i) w[i] = narrow2(mul2(pk(x[2 * i], x[2 * i + 1]), cp2));
+            if (n < kC) {  // (whatever their products are)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = row < n ? w[i] : 0u;
+            }
             if (wide && 16 * j + 16 <= have) {
               asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 16 * j), "r"(w[0]),
                            "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
