@@ -139,6 +139,15 @@ def test_segments(B, T, H, dk, dv, dtype):
     check(q, k, v, decay, h0, lengths=lengths)
 
 
+# more heads than the GPU has SMs: CTAs share heads and hand states over; in the gradients
+# also beside one another.  160 and 51 heads, 480 and 153 with all three passes.
+@pytest.mark.parametrize("B,T,H,dk,dv", [(5, 640, 32, 32, 32), (3, 389, 17, 64, 24), (2, 300, 80, 16, 136)])
+def test_more_heads_than_sms(B, T, H, dk, dv):
+    q, k, v, decay, h0 = inputs(B, T, H, dk, dv, BF)
+    decay[0], decay[1], decay[5] = 1.0, 0.0, 1.0
+    check(q, k, v, decay, h0)
+
+
 def test_precision_of_states_and_outputs():
     """Over many elements the roundings are at random: the states within a tenth of the
     bound above, out within bfloat16's half step over sqrt(3) for each of its own rounding
@@ -195,8 +204,9 @@ def test_state_in_place_and_given_outputs():
     assert torch.equal(out, want[0]) and torch.equal(state, want[1])
 
 
-def test_the_same_on_a_side_stream_again_and_from_a_graph():
-    q, k, v, decay, h0 = (t.to(DEV) for t in inputs(1, 1500, 2, 64, 64, BF))
+@pytest.mark.parametrize("B,T,H", [(1, 1500, 2), (5, 400, 40)])
+def test_the_same_on_a_side_stream_again_and_from_a_graph(B, T, H):
+    q, k, v, decay, h0 = (t.to(DEV) for t in inputs(B, T, H, 64, 64, BF))
     do, dh = torch.randn_like(v).contiguous(), torch.randn_like(h0)
     state = h0.clone()
     step_in = [t[:, 5] for t in (q, k, v)]
@@ -249,8 +259,9 @@ def test_gradients_are_the_forwards_slopes():
         assert abs(slope - want) <= 1e-4 * size, (i, slope.item(), want.item())
 
 
-def test_calls_on_two_streams_at_once():
-    sets = [[t.to(DEV) for t in inputs(2, 900, 3, 128, 128, BF, seed=s)] for s in range(2)]
+@pytest.mark.parametrize("B,T,H", [(2, 900, 3), (5, 400, 40)])
+def test_calls_on_two_streams_at_once(B, T, H):
+    sets = [[t.to(DEV) for t in inputs(B, T, H, 128, 128, BF, seed=s)] for s in range(2)]
     want = [wr.delta_decay_fwd(*s) for s in sets]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in sets]

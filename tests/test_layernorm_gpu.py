@@ -18,7 +18,9 @@ EPS = 1e-5
 within = ref.within
 
 SHAPES = [(1, 1), (3, 7), (1, 4096), (2, 8192), (5, 8191), (700, 64), (700, 72), (513, 1001),
-          (4, 2050), (1300, 2048), (400, 4100), (1, 256), (37, 520)]
+          (4, 2050), (1300, 2048), (400, 4100), (1, 256), (37, 520),
+          # several rows to a warp
+          (1000, 128), (1001, 16), (65, 32), (7, 8), (5000, 40), (333, 120), (1, 64)]
 
 
 def inputs(rows, D, dtype, seed, wdtype=F32):

@@ -110,6 +110,25 @@ __device__ __forceinline__ void store_lane(T *p, const Lane<V> &v) {
   store_v<T, V>(p, f);
 }
 
+// over the lanes of a row in this warp: all of them, or 4, 8 or 16 where rows are narrow
+__device__ __forceinline__ float row_sum(float v) {
+  if (blockDim.x < 32) {
+    for (int o = blockDim.x / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ void row_sum(float &a, float &b) {  // (both at a time)
+  if (blockDim.x < 32) {
+    for (int o = blockDim.x / 2; o > 0; o >>= 1)
+      a += __shfl_xor_sync(0xffffffffu, a, o), b += __shfl_xor_sync(0xffffffffu, b, o);
+    return;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o), b += __shfl_xor_sync(0xffffffffu, b, o);
+}
 template <int kFrom>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -156,7 +175,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
       }
     }
     in.done();
-    float s = lanes_sum<16>(acc.sum());
+    float s = row_sum(acc.sum());
     float m_w = s * inv_w;
     acc = Lane<V>::all(0.f);
 #pragma unroll
@@ -165,7 +184,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
         const Lane<V> c = t[j] + Lane<V>::all(-m_w);
         acc = c.fma(c, acc);
       }
-    float q = lanes_sum<16>(acc.sum()), mean = m_w;
+    float q = row_sum(acc.sum()), mean = m_w;
     if (nwarp > 1) {
       if (lane == 0) part[buf][threadIdx.y * 16 + warp] = make_float4(s, q, m_w, n_w);
       __syncthreads();
@@ -240,7 +259,8 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kBwdThreads / kT : 1) laye
         d2 = wy[j].fma(t[j], d2);
       }
     }
-    float sum = lanes_sum<16>(s2.sum()), dot = lanes_sum<16>(d2.sum());
+    float sum = s2.sum(), dot = d2.sum();
+    row_sum(sum, dot);
     if (nwarp > 1) {
       if (lane == 0) part[buf][threadIdx.y * 16 + warp] = make_float2(sum, dot);
       __syncthreads();
@@ -308,12 +328,12 @@ struct BwdOne {
 
 template <typename In>
 cudaError_t fwd_all(const NormArgs &a, cudaStream_t s) {
-  const Plan q = plan(a.rows, a.D, 16 / sizeof(In), fwd_width<In>(a), 2, kSmThreads, true);
+  const Plan q = plan(a.rows, a.D, 16 / sizeof(In), fwd_width<In>(a), 2, kSmThreads, true, true);
   return dispatch<In, FwdOne>(q, a, q, s);
 }
 template <typename In>
 cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
-  const Plan q = bwd_plan<In>(a, kBwdThreads);
+  const Plan q = bwd_plan<In>(a, kBwdThreads, true);
   const cudaError_t e = q.grid > 0 ? dispatch<In, BwdOne>(q, a, q, s) : cudaSuccess;
   return e != cudaSuccess ? e : launch_column_sum(a.partial, a.dweight, a.dbias, a.D, q.grid, 2 * a.D, s);
 }
@@ -324,7 +344,7 @@ cudaError_t launch_layernorm_fwd(const NormArgs &a, cudaStream_t s) {
   return a.bf16 ? fwd_all<__nv_bfloat16>(a, s) : fwd_all<float>(a, s);
 }
 int64_t layernorm_bwd_ctas(const NormBwdArgs &a) {
-  return (a.bf16 ? bwd_plan<__nv_bfloat16>(a, kBwdThreads) : bwd_plan<float>(a, kBwdThreads)).grid;
+  return (a.bf16 ? bwd_plan<__nv_bfloat16>(a, kBwdThreads, true) : bwd_plan<float>(a, kBwdThreads, true)).grid;
 }
 cudaError_t launch_layernorm_bwd(const NormBwdArgs &a, cudaStream_t s) {
   return a.bf16 ? bwd_all<__nv_bfloat16>(a, s) : bwd_all<float>(a, s);

@@ -218,7 +218,7 @@ struct Plan {
 // CTAs); more only where a row would not fit kMostThreads threads.  Of single
 // elements as many as keep a row to few warps, one if it can be: then rows need
 // no barrier.
-Plan plan(int64_t rows, int64_t D, int vec, int wide, int tensors, int resident, bool many) {
+Plan plan(int64_t rows, int64_t D, int vec, int wide, int tensors, int resident, bool many, bool narrow = false) {
   Plan q;
   const int size = 16 / vec;
   const bool aligned = wide == vec;
@@ -233,6 +233,8 @@ Plan plan(int64_t rows, int64_t D, int vec, int wide, int tensors, int resident,
   if (q.V == 2 && q.per > 8) q.per = 8;
   while (n > (int64_t)q.per * kMostThreads) q.per *= 2;
   q.nt = (int)((n + q.per - 1) / q.per + 31) / 32 * 32;
+  // rows of a few vectors: several to a warp, where the kernel can (layer norm)
+  if (narrow && aligned && n <= 16) q.per = 1, q.nt = n <= 4 ? 4 : n <= 8 ? 8 : 16;
   q.rpc = q.nt >= 256 ? 1 : 256 / q.nt;
   const int64_t ctas = (rows + q.rpc - 1) / q.rpc;
   q.threads = q.nt * q.rpc <= 256 ? 256 : kMostThreads;
@@ -303,9 +305,9 @@ int fwd_width(const NormArgs &a) {
   return ok(V) ? V : V == 8 && ok(2) ? 2 : 1;
 }
 template <typename In>
-Plan bwd_plan(const NormBwdArgs &a, int resident) {
+Plan bwd_plan(const NormBwdArgs &a, int resident, bool narrow = false) {
   constexpr int V = 16 / sizeof(In);
-  return plan(a.rows, a.D, V, a.D % V == 0 ? V : V == 8 && a.D % 2 == 0 ? 2 : 1, 3, resident, false);
+  return plan(a.rows, a.D, V, a.D % V == 0 ? V : V == 8 && a.D % 2 == 0 ? 2 : 1, 3, resident, false, narrow);
 }
 
 }  // namespace
