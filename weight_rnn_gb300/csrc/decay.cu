@@ -407,10 +407,11 @@ __global__ void __launch_bounds__(256) decay_join_kernel(float *states, const fl
                                                          const int *lengths, int64_t T, int H, int64_t seg, int nseg,
                                                          bool reverse, int64_t n, int blocks) {
   struct __align__(4 * V) Vec { float v[V]; };
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   const int bh = (int)(blockIdx.x / (unsigned)blocks);
   const int64_t e = ((int64_t)(blockIdx.x % (unsigned)blocks) * 256 + threadIdx.x) * V;
   chain_wait();
+  chain_next();  // (the pass that follows sets itself up meanwhile)
   if (e >= n) return;
   int64_t len = lengths ? lengths[bh / H] : T;
   len = len < 0 ? 0 : len > T ? T : len;

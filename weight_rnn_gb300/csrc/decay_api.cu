@@ -55,15 +55,15 @@ int sm_count() {
 }
 
 // Into how many segments the time axis is cut.  On the tensor cores 128 tokens take a CTA
-// about 2.5 us with all products and 1.7 with those of the states alone, an item's start
-// and end 4 us, and CTAs share the work evenly where there is more than a round of it,
+// about 2.4 us with all products and 1.7 with those of the states alone, an item's start
+// and end 6 us, and CTAs share the work evenly where there is more than a round of it,
 // but for rows with lengths; on the CUDA cores 36 and 12 us at two CTAs an SM, in whole
 // rounds.  A cut adds the pass for the states, its states' way through memory, and two
 // launches.
 int segments(const DecayArgs &a, int64_t state_passes, bool tc) {
   const int64_t chunks = (a.T + delta::kDecayChunk - 1) / delta::kDecayChunk;
   const int width = tc ? 128 : 64;
-  const double whole = tc ? 2.5 : 36.0, part = tc ? 1.7 : 12.0;
+  const double whole = tc ? 2.4 : 36.0, part = tc ? 1.7 : 12.0;
   const int64_t slots = (int64_t)sm_count() * (tc ? 1 : 2);
   int64_t items = 0, bytes = 0;
   for (int i = 0; i < a.passes; ++i) items += a.B * a.H * ((a.pass[i].dv + width - 1) / width);
@@ -73,7 +73,7 @@ int segments(const DecayArgs &a, int64_t state_passes, bool tc) {
   const auto rounds = [&](int64_t n) {
     return tc && !a.lengths && n > slots ? (double)n / (double)slots : (double)up_div(n, slots);
   };
-  const auto ends = [&](int64_t n) { return 4.0 * (double)up_div(n, slots); };
+  const auto ends = [&](int64_t n) { return 6.0 * (double)up_div(n, slots); };
   int best = 1;
   double least = 1e30;
   for (int64_t n = 1; n <= chunks && n <= 256; ++n) {
@@ -82,8 +82,8 @@ int segments(const DecayArgs &a, int64_t state_passes, bool tc) {
     if (n > 1 && bytes * n > (int64_t(1) << 30)) break;
     double us = rounds(items * n) * (double)each * whole + ends(items * n);
     if (n > 1)
-      us += rounds(state_items * n) * (double)each * part + ends(state_items * n) + 9.0 + (double)(bytes * n) * 4 / 5e6;
-    if (us < 0.95 * least) least = us, best = (int)n;
+      us += rounds(state_items * n) * (double)each * part + ends(state_items * n) + 5.0 + (double)(bytes * n) * 4 / 5e6;
+    if (us < 0.97 * least) least = us, best = (int)n;
   }
   return best;
 }
@@ -120,6 +120,7 @@ cudaError_t run(DecayArgs &a, const Start *starts, int count, cudaStream_t s) {
     err = tc ? delta::launch_decay_tc(st, true, s) : delta::launch_decay_states(st, s);
     for (int i = 0; err == cudaSuccess && i < count; ++i)
       err = delta::launch_decay_join(st.pass[i].final, starts[i].pass.init, a, starts[i].pass.reverse, n, s);
+    a.joined = true;
   }
   a.handed = handed ? scr.cut(handed) : nullptr;
   if (err == cudaSuccess) err = tc ? delta::launch_decay_tc(a, false, s) : delta::launch_decay(a, s);

@@ -315,7 +315,9 @@ struct Bool {
 template <bool kStates>
 __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcArgs a) {
   // The states alone have no Q, S, G and O: their tiles and tensor memory make the
-  // rings of K and V one deeper, and K' and dS two.
+  // rings of K and V one deeper, and K' and dS two.  They are sums, each chunk's own part
+  // times a power of g, and the chunks are taken in the opposite order: what is read last
+  // is what the pass with all products, which follows, reads first, from L2.
   constexpr int kRing = kStates ? 3 : 2, kBufs = kStates ? 2 : 1;
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
@@ -364,8 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     for (int n = 0; ok && n < parts; ++n) {
       const Part &t = sh.part[n];
       const TcPass &p = a.pass[t.pass];
-      const int b = t.b, h = t.h, c0 = t.c0, to = t.to, step = p.reverse ? -kC : kC;
-      int t0 = t.t_lo + (p.reverse ? t.chunks - 1 - t.from : t.from) * kC;
+      const bool down = p.reverse != kStates;
+      const int b = t.b, h = t.h, c0 = t.c0, to = t.to, step = down ? -kC : kC;
+      int t0 = t.t_lo + (down ? t.chunks - 1 - t.from : t.from) * kC;
       for (int c = t.from; ok && c < to; ++c, g.next(), t0 += step) {
         // (a tile of each, in the order in which they are wanted)
 #pragma unroll 1
@@ -503,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         c2[i] = kReverse ? pk(ex2(-lg * (float)(7 - 2 * i)), ex2(-lg * (float)(6 - 2 * i)))
                          : pk(ex2(-lg * (float)(2 * i)), ex2(-lg * (float)(2 * i + 1)));
       const int to = t.to;
-      int left = t.t_end - t.t_lo - (kReverse ? t.chunks - 1 - t.from : t.from) * kC;  // tokens from the chunk's first on
-      for (int c = t.from; c < to; ++c, left += kReverse ? kC : -kC) {
+      constexpr bool kDown = kReverse != kStates;
+      int left = t.t_end - t.t_lo - (kDown ? t.chunks - 1 - t.from : t.from) * kC;  // tokens from the chunk's first on
+      for (int c = t.from; c < to; ++c, left += kDown ? kC : -kC) {
         const int n = min(kC, left);
         // ---- K': this warp's 32 channels, half of the tokens
         if (!wait(&sh, &sh.kfull[g.slot], g.phase, 4)) return false;
@@ -694,16 +698,22 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       decay::Keep keep = {0.f, 0.f};  // of a chunk of `kept` tokens
       float owed = 0.f;
       int kept = -1;
-      const int first = p.reverse ? t.chunks - 1 - t.from : t.from, step = p.reverse ? -kC : kC;
+      const bool down = p.reverse != kStates;
+      const int first = down ? t.chunks - 1 - t.from : t.from, step = down ? -kC : kC;
       int left = t.t_end - t.t_lo - first * kC, rest = t.t_hi - t.t_lo - first * kC - (quarter * 32 + lane);
       __nv_bfloat16 *out = kStates ? nullptr
                                    : p.to + (((int64_t)t.b * a.T + t.t_lo + (int64_t)first * kC + quarter * 32 + lane) * a.H + t.h) * p.dv + v0;
       const int64_t hop = (int64_t)step * a.H * p.dv;
       for (int c = t.from; c < to; ++c, left -= step, rest -= step, out += hop) {
         const int n = min(kC, left);
-        if (n != kept) keep = decay::keep_of(lg, n), kept = n;  // (whole chunks, and the last)
-        const float k1 = decay::keep_now(keep, owed);
-        const uint64_t k2 = pk(k1, k1);
+        float f;
+        if constexpr (kStates) {  // the tokens between the chunk and the pass's end
+          f = exp2f(lg * (float)(p.reverse ? t.t_end - t.t_lo - left : left - n));
+        } else {
+          if (n != kept) keep = decay::keep_of(lg, n), kept = n;  // (whole chunks, and the last)
+          f = decay::keep_now(keep, owed);
+        }
+        const uint64_t f2 = pk(f, f);
         if (!(ok = wait(&sh, &sh.dsfull[u.slot], u.phase, 5))) break;
         tc_fence_after();
 #pragma unroll
@@ -712,7 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           tmem_ld16(tmem_addr(tmem, quarter * 32, cols_ds(u.slot) + half * 64 + 16 * j), r);
           tmem_wait_ld_regs(r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) S[8 * j + i] = fma2(k2, S[8 * j + i], pk(r[2 * i], r[2 * i + 1]));
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t x = pk(r[2 * i], r[2 * i + 1]);
+            S[8 * j + i] = kStates ? fma2(f2, x, S[8 * j + i]) : fma2(f2, S[8 * j + i], x);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -822,7 +835,8 @@ bool tc_shared(const DecayArgs &a) {
 }
 int64_t flag_bytes(int sms) { return ((int64_t)sms * 32 + 255) / 256 * 256; }
 
-// (not launched as a dependent: it takes tensor memory before it waits)
+// (Not launched as a dependent, but where this call's own joining of states goes before:
+// it takes tensor memory before it waits, which a caller's kernel may have yet to take.)
 template <bool kStates>
 cudaError_t run(const DecayArgs &a, cudaStream_t s) {
   TcArgs t{};
@@ -863,10 +877,15 @@ cudaError_t run(const DecayArgs &a, cudaStream_t s) {
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeCooperative;
-  at.val.cooperative = 1;
+  if (t.shared) {
+    at.id = cudaLaunchAttributeCooperative;
+    at.val.cooperative = 1;
+  } else {
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = &at;
-  cfg.numAttrs = t.shared ? 1 : 0;
+  cfg.numAttrs = t.shared || a.joined ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, t);
 }
 

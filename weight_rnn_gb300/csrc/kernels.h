@@ -176,6 +176,7 @@ struct DecayArgs {
   int nseg;
   bool bf16;
   void *handed;         // decay_tc_scratch() bytes for launch_decay_tc
+  bool joined;          // launch_decay_join has gone before in this call
 };
 constexpr int kDecayMaxD = 256;
 constexpr int kDecayChunk = 128;  // segments are multiples of it

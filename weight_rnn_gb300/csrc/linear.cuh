@@ -53,6 +53,19 @@ __device__ __forceinline__ float slope(int act, float p) {
   return 1.f;
 }
 
+// both, for one exponential
+__device__ __forceinline__ void curve(int act, float p, float &value, float &der) {
+  value = p, der = 1.f;
+  if (act == kActSilu) {
+    const float s = sigmoid(p);
+    value = p * s, der = s * (1.f + p * (1.f - s));
+  } else if (act == kActGelu) {
+    const float s = sigmoid(kGelu2c * (p + kGelu3 * p * p * p));
+    const float q = fminf(fmaxf(p, -16.f), 16.f);  // (as in slope)
+    value = p * s, der = s + q * s * (1.f - s) * kGelu2c * (1.f + 3.f * kGelu3 * q * q);
+  }
+}
+
 __device__ __forceinline__ float bias_at(const LinearArgs &a, int64_t n) {
   if (!a.bias) return 0.f;
   return a.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.bias)[n])
