@@ -543,11 +543,15 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
  * and v in whole 16-byte pieces (addresses and strides, none of them 0) runs on the
  * tensor cores in chunks of 128 tokens; all else runs on the CUDA cores in float32,
  * a correctness path.  The state is float32 throughout; on the tensor cores a
- * token's way into it is rounded to 2^-16 of itself, and what out reads of it to
- * bfloat16.  Where B * H does not fill the GPU the time axis is cut into segments,
- * whose states (at most 1 GiB) go to scratch from the library's pool,
- * stream-ordered.  Sizes alone decide the way, and the result does not depend on
- * scheduling.
+ * token's way into it is rounded to 2^-16 of itself, what out reads of it to bfloat16,
+ * and of the state before a chunk out reads no less than 2^-64.  A token whose values
+ * are not finite may reach all of its chunk's outputs, and those after it.
+ *
+ * Where B * H does not fill the GPU the time axis is cut into segments, whose states
+ * (at most 1 GiB) go to scratch from the library's pool, stream-ordered.  Where there are more heads than SMs, a
+ * cooperative launch shares them out evenly, and 64 KB for each SM are scratch too.
+ * Sizes, alignment and whether there are lengths decide the way, and the result does not
+ * depend on scheduling.
  */
 int delta_decay_fwd(const void *q, const void *k, const void *v, const float *decay, const float *h0,
                     const int *lengths, void *out, float *hT, int B, int T, int H, int dk, int dv,
@@ -575,8 +579,8 @@ int delta_decay_step(const void *q, const void *k, const void *v, const float *d
  *   dq, dk_out [B, T, H, dk], dv_out [B, T, H, dv]  dtype; 0 past a row's length
  *   dh0     [B, H, dk, dv] float32 or NULL
  *
- * Runs as the forward does, with the same bounds and scratch.  With T = 0, dh0 ==
- * dhT is allowed.
+ * Runs as the forward does, with the same bounds and scratch; on the tensor cores
+ * where dv <= 128 too.  With T = 0, dh0 == dhT is allowed.
  */
 int delta_decay_bwd(const void *q, const void *k, const void *v, const float *decay, const float *h0,
                     const int *lengths, const void *dout, const float *dhT, void *dq, void *dk_out, void *dv_out,

@@ -117,6 +117,14 @@ def test_ends_of_the_decays_range(dtype):
     check(q, k, v, decay, h0)
 
 
+def test_large_values_under_strong_decays():
+    """A row's products pass over its least power of the decay on their way, and stay in
+    float32's range."""
+    q, k, v, _, h0 = inputs(1, 300, 6, 64, 32, BF)
+    decay = torch.tensor([0.0, 1e-30, 1e-3, 0.3, 0.5, 0.6])
+    check(1e4 * q, 1e4 * k, 1e4 * v, decay, h0)
+
+
 @pytest.mark.parametrize("scale", [0.0, -1.5, 1.0, 64.0])
 def test_scales(scale):
     check(*inputs(1, 140, 2, 64, 64, BF), scale=scale)

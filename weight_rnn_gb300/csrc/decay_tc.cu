@@ -17,8 +17,9 @@
 //
 // Both parts of O share one accumulator: with c_p the factor of S's part (g^(p+1),
 // in reverse g^(n-1-p)), P is formed as G_pj g^|p-j| / c_p and the whole row is
-// multiplied by c_p when it goes out.  c_p is taken no lower than 2^-100, so the
-// quotient stays in range for any g; where that matters S's part is below 2^-100 of S.
+// multiplied by c_p when it goes out.  c_p is taken no lower than 2^-64, so that the
+// quotient stays in range for any g while q k v stays below 2^63; where that matters S's
+// part is 2^-64 of S in place of something less.
 //
 // The state is float32 in registers, a row of dk a lane; what the chain from chunk
 // to chunk costs is dS -> registers -> bfloat16 S in shared memory -> O.  All else
@@ -64,7 +65,7 @@ constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffS = 6 * 
 constexpr int kSmem = 7 * kTile + 1024;
 // TMEM columns
 constexpr uint32_t kG = 0, kO = 128, kDs = 256, kHi = 384;  // (lo: 64 after hi)
-constexpr float kFloor = -100.f;   // log2 of the least c_p
+constexpr float kFloor = -64.f;    // log2 of the least c_p
 constexpr float kLogZero = -200.f; // log2 g of g = 0: any power of it vanishes, also over c_p
 
 struct TcPass {
