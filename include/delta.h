@@ -541,11 +541,12 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
  *
  * 1 <= dk, dv <= 256.  bfloat16 with dk <= 128, dk and dv multiples of 8 and q, k
  * and v in whole 16-byte pieces (addresses and strides, none of them 0) runs on the
- * tensor cores in chunks of 128 tokens; all else runs on the CUDA cores in float32,
- * a correctness path.  The state is float32 throughout; on the tensor cores a
- * token's way into it is rounded to 2^-16 of itself, what out reads of it to bfloat16,
- * and of the state before a chunk out reads no less than 2^-64.  A token whose values
- * are not finite may reach all of its chunk's outputs, and those after it.
+ * tensor cores in chunks of 128 tokens, all else in float32 in chunks of 32, each
+ * product as three of tf32 that leave out 2^-22 of a term.  The state is float32
+ * throughout; in bfloat16's chunks a token's way into it is rounded to 2^-16 of itself,
+ * what out reads of it to bfloat16, and of the state before a chunk out reads no less
+ * than 2^-64.  A token whose values are not finite may reach all of its chunk's outputs,
+ * and those after it, and an infinity may come out as a NaN.
  *
  * Where B * H does not fill the GPU the time axis is cut into segments, whose states
  * (at most 1 GiB) go to scratch from the library's pool, stream-ordered.  Where there are more heads than SMs, a
@@ -579,7 +580,7 @@ int delta_decay_step(const void *q, const void *k, const void *v, const float *d
  *   dq, dk_out [B, T, H, dk], dv_out [B, T, H, dv]  dtype; 0 past a row's length
  *   dh0     [B, H, dk, dv] float32 or NULL
  *
- * Runs as the forward does, with the same bounds and scratch; on the tensor cores
+ * Runs as the forward does, with the same bounds and scratch; in bfloat16's chunks
  * where dv <= 128 too.  With T = 0, dh0 == dhT is allowed.
  */
 int delta_decay_bwd(const void *q, const void *k, const void *v, const float *decay, const float *h0,

@@ -1,6 +1,6 @@
-// decay.cu -- linear attention with a decay g for each head, outside the tensor
-// cores: the step of one token, the pass over the time axis for float32 and for
-// layouts that the tensor-core kernel does not take, and the joining of segments.
+// decay.cu -- linear attention with a decay g for each head: the step of one token,
+// the pass over the time axis in float32, also for bfloat16 layouts that decay_tc.cu's
+// kernel does not take, and the joining of segments.
 //
 //   S_t = g S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t
 //
@@ -130,51 +130,118 @@ cudaError_t step_all(const DecayStepArgs &a, cudaStream_t s) {
                       dim3(kStepThreads), 0, 1, true, s, a, slab);
 }
 
-// ----------------------------------------------------- the pass on CUDA cores
-// In float32: a CTA has a segment of a head and 64 value columns, in chunks of 32
-// tokens.  Its state is in registers, 4 x 4 elements a thread for every 64 key channels,
-// with a copy in shared memory that the outputs read; two CTAs share an SM up to 128
-// channels.  Operands are read from shared memory four at a time: 32 products for 6
-// reads in the outputs, 16 for 2 in the state.  The next chunk's elements are asked for
-// before this one's products.
+// -------------------------------------------------------- the pass in float32
+// A CTA has a segment of a head and 64 value columns, in chunks of 32 tokens.  The
+// products run on the warp-level matrix instructions, which take tf32: each factor is
+// x = hi + lo, hi rounded to 11 bits and lo what that leaves, and a product is hi hi +
+// hi lo + lo hi, which leaves out 2^-22 of a term at most.  The instructions' own sums
+// are cut off, not rounded, so the small products have sums of their own, and no sum
+// stays there for more than a chunk: the state is kept in float32 beside them,
+// transposed, in the layout of their results, with a copy in shared memory that the
+// outputs read.  (B7 T1021 H5 dk64 dv96 with errors of 3.7e-7: 61 us; on the float32
+// units 96, of plain float32's 2e-7.)  The order of channels and tokens within a product
+// is free, and such that a lane's factors are neighbours in shared memory.  The next
+// chunk's elements are asked for before this one's products.
+//
+// Bound by the matrix instructions, a little: 576 a warp and 128 tokens at dk 64, 8
+// cycles each on a quarter of an SM, take half of the time, and the rest are the three
+// barriers of a chunk, which two CTAs an SM hide in part.
 constexpr int kC = 32, kCols = 64, kThreads = 256;
-constexpr int kPre = 4;  // vectors of a row asked for ahead, of 8 lanes: 128 channels
+constexpr int kLdV = kCols + 8, kLdP = kC + 4;  // of a row of v, of P
 
 struct Floats {  // shared memory
-  int ld;        // of a row of q and k: whole vectors, one more against bank conflicts
-  __host__ __device__ explicit Floats(int dk) : ld((dk + 3) / 4 * 4 + 4) {}
-  __host__ __device__ int rows() const { return (ld - 4 + 63) / 64 * 64; }  // of the state
+  int ld, lds;   // of a row of q and k, of a row (a value column) of the state
+  __host__ __device__ explicit Floats(int dk) : ld((dk + 15) / 16 * 16 + 8), lds((dk + 7) / 8 * 8 + 4) {}
   __host__ __device__ int total(bool states) const {
-    return rows() * kCols + 2 * kC * kCols + (states ? kC * ld : 2 * kC * ld + kC * (kC + 4));
+    return kC * kLdV + kC * ld + (states ? 32 : kC * ld + kC * kLdV + kCols * lds + kC * kLdP);
   }
 };
 
-__device__ __forceinline__ float4 scaled(const float4 &a, float f) { return make_float4(a.x * f, a.y * f, a.z * f, a.w * f); }
-__device__ __forceinline__ void axpy(float (&o)[4], float f, const float4 &x) {
-  o[0] = fmaf(f, x.x, o[0]), o[1] = fmaf(f, x.y, o[1]), o[2] = fmaf(f, x.z, o[2]), o[3] = fmaf(f, x.w, o[3]);
+// x = hi + lo, of which the instructions read the upper 19 bits each
+template <int kN>
+struct Parts {
+  uint32_t hi[kN], lo[kN];
+  __device__ __forceinline__ void set(int i, float x) {
+    hi[i] = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    lo[i] = __float_as_uint(x - __uint_as_float(hi[i]));
+  }
+};
+// Lane 4 g + t has, of A (16 x 8), (g, t), (g + 8, t), (g, t + 4), (g + 8, t + 4), of B
+// (8 x 8) (t, g), (t + 4, g), of D (16 x 8) (g, 2 t), (g, 2 t + 1), (g + 8, 2 t), (g + 8, 2 t + 1).
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
+struct Sum {
+  float big[4] = {}, small[4] = {};
+  __device__ __forceinline__ float operator[](int i) const { return big[i] + small[i]; }
+};
+// the three products of several sums in turn, so that none waits for its own last one
+template <int kN>
+__device__ __forceinline__ void add(Sum (&s)[kN], const Parts<4> &a, const Parts<2> (&b)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    mma_tf32(s[i].small, a.lo, b[i].hi);
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    mma_tf32(s[i].big, a.hi, b[i].hi);
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    mma_tf32(s[i].small, a.hi, b[i].lo);
+}
+__device__ __forceinline__ Parts<2> pair_of(float x, float y) {
+  Parts<2> b;
+  b.set(0, x), b.set(1, y);
+  return b;
+}
+__device__ __forceinline__ Parts<4> quad_of(float x, float y, float z, float w) {
+  Parts<4> a;
+  a.set(0, x), a.set(1, y), a.set(2, z), a.set(3, w);
+  return a;
+}
+__device__ __forceinline__ float2 two_at(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
-// four elements of a row from column c on, zeros past its end; kVec: whole vectors
+__device__ __forceinline__ float4 scaled(const float4 &a, float f) { return make_float4(a.x * f, a.y * f, a.z * f, a.w * f); }
+
+// four neighbouring elements, zeros past the row's `live` ones; kVec: whole vectors
 template <typename In, bool kVec>
-__device__ __forceinline__ float4 load4(const In *row, int c, int width) {
-  if (c >= width) return make_float4(0.f, 0.f, 0.f, 0.f);
+__device__ __forceinline__ float4 load4(const In *row, int live) {
+  if (live <= 0) return make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (kVec) {
     if constexpr (sizeof(In) == 4) {
-      return *reinterpret_cast<const float4 *>(row + c);
+      return *reinterpret_cast<const float4 *>(row);
     } else {
-      const uint2 u = *reinterpret_cast<const uint2 *>(row + c);
+      const uint2 u = *reinterpret_cast<const uint2 *>(row);
       return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
                          __uint_as_float(u.y & 0xFFFF0000u));
     }
   } else {
-    return make_float4(to_f(row[c]), c + 1 < width ? to_f(row[c + 1]) : 0.f, c + 2 < width ? to_f(row[c + 2]) : 0.f,
-                       c + 3 < width ? to_f(row[c + 3]) : 0.f);
+    return make_float4(to_f(row[0]), live > 1 ? to_f(row[1]) : 0.f, live > 2 ? to_f(row[2]) : 0.f,
+                       live > 3 ? to_f(row[3]) : 0.f);
   }
 }
 
-// kMost: blocks of 64 key channels, 2 or 4
+// and back; live: columns to the row's end
+template <typename In, bool kVec>
+__device__ __forceinline__ void store4(In *to, const float4 &x, int live) {
+  const float v[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (kVec) {
+    struct __align__(4 * sizeof(In)) Vec { In v[4]; } w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) from_f(v[i], w.v[i]);
+    if (live > 0) *reinterpret_cast<Vec *>(to) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < live) from_f(v[i], to[i]);
+  }
+}
+
+// kMost: blocks of 64 key channels, 1, 2 or 4
 template <typename In, int kMost, bool kStates, bool kVec>
-__global__ void __launch_bounds__(kThreads, kMost == 2 ? 2 : 1) decay_generic_kernel(const __grid_constant__ DecayArgs a, int groups) {
+__global__ void __launch_bounds__(kThreads, kMost <= 2 ? 2 : 1) decay_generic_kernel(const __grid_constant__ DecayArgs a, int groups) {
+  constexpr int kPre = kMost == 1 ? 2 : 4;  // vectors of a row asked for ahead, of 8 lanes: up to 128 channels
   extern __shared__ __align__(16) float smem[];
   uint32_t item = blockIdx.x;
   const DecayPass &p = a.pass[item % (uint32_t)a.passes];
@@ -186,10 +253,12 @@ __global__ void __launch_bounds__(kThreads, kMost == 2 ? 2 : 1) decay_generic_ke
   if (c0 >= p.dv) return;
   const int dk = p.dk, cols = min(kCols, p.dv - c0);
   const Floats f(dk);
-  const int ld = f.ld, srows = f.rows();
-  float *S = smem, *sv = S + srows * kCols, *sw = sv + kC * kCols, *sk = sw + kC * kCols, *sq = sk + kC * ld, *sp = sq + kC * ld;
-  const int tid = threadIdx.x, r16 = tid / 16, c16 = tid % 16;  // a thread's places in products
-  const int row = tid / 8, l8 = tid % 8;                         // and in copies
+  const int ld = f.ld, lds = f.lds;
+  float *sw = smem, *sk = sw + kC * kLdV, *sq = sk + kC * ld, *sv = sq + kC * ld, *S = sv + kC * kLdV, *sp = S + kCols * lds;
+  const int tid = threadIdx.x, row = tid / 8, l8 = tid % 8;  // a thread's place in copies
+  const int warp = tid / 32, g = tid % 32 / 4, t = tid % 4;  // and in products:
+  const int m0 = warp % 2 * 16, n0 = warp / 2;               // 16 tokens, 8 of P's columns, 16 of O's
+  const int s0 = warp % 4 * 16, d0 = warp / 4 * 32;          // 16 value columns and 32 channels, every 64, of the state
   chain_wait();
   const float lg = log2f(a.decay[h]);
   int64_t len = a.lengths ? a.lengths[b] : a.T;
@@ -197,162 +266,156 @@ __global__ void __launch_bounds__(kThreads, kMost == 2 ? 2 : 1) decay_generic_ke
   const int64_t t_lo = sg * a.seg, t_hi = min(t_lo + a.seg, a.T);
   const int64_t t_end = min(t_hi, len);  // tokens [t_lo, t_end) count
   const int64_t state_at = kStates || a.nseg > 1 ? bh * a.nseg + sg : bh;
-  float st[kMost][4][4];  // state rows 64 i + 4 r16 .. + 3, columns 4 c16 .. + 3
+  // st[i][x][y]: channel 64 i + d0 + 8 t + 4 (y % 2) + x, value column s0 + 2 g + y / 2
+  float st[kMost][4][4];
 #pragma unroll
   for (int i = 0; i < kMost; ++i)
 #pragma unroll
     for (int x = 0; x < 4; ++x)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const int d = 64 * i + 4 * r16 + x, c = 4 * c16 + y;
+        const int d = 64 * i + d0 + 8 * t + 4 * (y % 2) + x, c = s0 + 2 * g + y / 2;
         st[i][x][y] = 0.f;
         if (!kStates && p.init && d < dk && c < cols)
           st[i][x][y] = p.init[state_at * dk * p.dv + (p.init_t ? (int64_t)(c0 + c) * dk + d : (int64_t)d * p.dv + c0 + c)];
       }
   const int64_t chunks = t_end > t_lo ? (t_end - t_lo + kC - 1) / kC : 0;
-  const auto start_of = [&](int64_t ci) { return t_lo + (p.reverse ? chunks - 1 - ci : ci) * kC; };
-  const In *krow = static_cast<const In *>(p.k) + b * p.ks[0] + h * p.ks[2];
-  const In *qrow = kStates ? nullptr : static_cast<const In *>(p.q) + b * p.qs[0] + h * p.qs[2];
-  const In *vrow = static_cast<const In *>(p.v) + b * p.vs[0] + h * p.vs[2] + c0;
+  const int64_t from = t_lo + (p.reverse && chunks > 0 ? chunks - 1 : 0) * kC, hop = p.reverse ? -kC : kC;
+  // this thread's rows, of the chunk that is asked for
+  const In *krow = static_cast<const In *>(p.k) + b * p.ks[0] + h * p.ks[2] + (from + row) * p.ks[1] + l8 * 4;
+  const In *qrow = kStates ? nullptr : static_cast<const In *>(p.q) + b * p.qs[0] + h * p.qs[2] + (from + row) * p.qs[1] + l8 * 4;
+  const In *vrow = static_cast<const In *>(p.v) + b * p.vs[0] + h * p.vs[2] + (from + row) * p.vs[1] + c0 + l8 * 4;
+  const int64_t khop = hop * p.ks[1], qhop = hop * p.qs[1], vhop = hop * p.vs[1];
+  const bool reverse = p.reverse;
+  const float kvs = p.kvs, os = p.os;
+  int left = (int)(t_end - from);  // tokens from the chunk's first on
+  In *out = kStates ? nullptr : static_cast<In *>(p.out) + ((b * a.T + from + m0 + g) * a.H + h) * p.dv + c0 + 16 * n0 + 4 * t;
+  const int64_t out8 = (int64_t)8 * a.H * p.dv;  // eight tokens on
   float4 nk[kPre], nq[kStates ? 1 : kPre], nv[2];
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  const auto ask = [&](int64_t ci) {
-    const int64_t t = start_of(ci) + row;
-    const bool on = t < t_end;
+  const auto ask = [&](bool on) {
 #pragma unroll
     for (int i = 0; i < kPre; ++i) {
-      const int c = (l8 + 8 * i) * 4;
-      nk[i] = on ? load4<In, kVec>(krow + t * p.ks[1], c, dk) : zero;
-      if constexpr (!kStates) nq[i] = on ? load4<In, kVec>(qrow + t * p.qs[1], c, dk) : zero;
+      const int live = on ? dk - l8 * 4 - 32 * i : 0;
+      nk[i] = load4<In, kVec>(krow + 32 * i, live);
+      if constexpr (!kStates) nq[i] = load4<In, kVec>(qrow + 32 * i, live);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) nv[i] = on ? load4<In, kVec>(vrow + t * p.vs[1], (l8 + 8 * i) * 4, cols) : zero;
+    for (int i = 0; i < 2; ++i) nv[i] = load4<In, kVec>(vrow + 32 * i, on ? cols - l8 * 4 - 32 * i : 0);
   };
   Keep keep = {0.f, 0.f};  // of a chunk of `kept` tokens
   float owed = 0.f;
   int kept = -1;
-  if (chunks > 0) ask(0);
+  ask(row < left);
   for (int64_t ci = 0; ci < chunks; ++ci) {
-    const int64_t t0 = start_of(ci);
-    const int n = (int)min((int64_t)kC, t_end - t0);
+    const int n = min(kC, left);
     if (n != kept) keep = keep_of(lg, n), kept = n;
     const float now = keep_now(keep, owed);
     __syncthreads();  // what the last chunk read may be written
     {
-      const float w = p.kvs * power(lg, p.reverse ? row + 1 : n - 1 - row);  // to the chunk's end, or past its start
+      const float w = row < n ? kvs * power(lg, reverse ? row + 1 : n - 1 - row) : 0.f;  // to the chunk's end, or past its start
 #pragma unroll
       for (int i = 0; i < kPre; ++i) {
         const int c = (l8 + 8 * i) * 4;
-        if (c < ld - 4) {
+        if (c < ld - 8) {
           *reinterpret_cast<float4 *>(sk + row * ld + c) = nk[i];
           if constexpr (!kStates) *reinterpret_cast<float4 *>(sq + row * ld + c) = nq[i];
         }
       }
-      for (int c = (l8 + 8 * kPre) * 4; kMost > 2 && c < ld - 4; c += 32) {
-        const bool on = row < n;
-        *reinterpret_cast<float4 *>(sk + row * ld + c) = on ? load4<In, kVec>(krow + (t0 + row) * p.ks[1], c, dk) : zero;
-        if constexpr (!kStates)
-          *reinterpret_cast<float4 *>(sq + row * ld + c) = on ? load4<In, kVec>(qrow + (t0 + row) * p.qs[1], c, dk) : zero;
+      for (int c = (l8 + 8 * kPre) * 4; kMost > 2 && c < ld - 8; c += 32) {
+        const int live = row < n ? dk - c : 0;
+        *reinterpret_cast<float4 *>(sk + row * ld + c) = load4<In, kVec>(krow + c - l8 * 4, live);
+        if constexpr (!kStates) *reinterpret_cast<float4 *>(sq + row * ld + c) = load4<In, kVec>(qrow + c - l8 * 4, live);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int c = (l8 + 8 * i) * 4;
-        if constexpr (!kStates) *reinterpret_cast<float4 *>(sv + row * kCols + c) = scaled(nv[i], p.kvs);
-        *reinterpret_cast<float4 *>(sw + row * kCols + c) = row < n ? scaled(nv[i], w) : zero;
+        if constexpr (!kStates) *reinterpret_cast<float4 *>(sv + row * kLdV + c) = scaled(nv[i], kvs);
+        *reinterpret_cast<float4 *>(sw + row * kLdV + c) = scaled(nv[i], w);
       }
     }
     if constexpr (!kStates) {
 #pragma unroll
       for (int i = 0; i < kMost; ++i)
-        if (64 * i < srows)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<float4 *>(S + (64 * i + 4 * r16 + x) * kCols + 4 * c16) =
-                make_float4(st[i][x][0], st[i][x][1], st[i][x][2], st[i][x][3]);
+        for (int y = 0; y < 4; ++y) {
+          const int d = 64 * i + d0 + 8 * t + 4 * (y % 2);
+          if (d < lds - 4)
+            *reinterpret_cast<float4 *>(S + (s0 + 2 * g + y / 2) * lds + d) =
+                make_float4(st[i][0][y], st[i][1][y], st[i][2][y], st[i][3][y]);
+        }
     }
     __syncthreads();
-    if (ci + 1 < chunks) ask(ci + 1);
+    left -= (int)hop;
+    krow += khop, vrow += vhop;
+    if constexpr (!kStates) qrow += qhop;
+    if (ci + 1 < chunks) ask(row < left);
     if constexpr (!kStates) {
-      // P: rows r16 and r16 + 16, columns c16 and c16 + 16
-      float s[2][2] = {};
-#pragma unroll 1
-      for (int d = 0; d < ld - 4; d += 4) {
-        float4 q[2], k[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          q[x] = *reinterpret_cast<const float4 *>(sq + (r16 + 16 * x) * ld + d);
-          k[x] = *reinterpret_cast<const float4 *>(sk + (c16 + 16 * x) * ld + d);
+      // G, and the state's part of O: column 2 x + e of 16 is e of the product's x
+      const bool none = reverse ? 8 * n0 + 7 < m0 : 8 * n0 > m0 + 15;  // all of it is masked
+      Sum o[3], out2[2];  // O's two, and G
+      {
+        const float *qa = sq + (m0 + g) * ld + 2 * t, *ka = sk + (8 * n0 + g) * ld + 2 * t;
+        const float *sa = S + (16 * n0 + 2 * g) * lds + 2 * t;
+#pragma unroll kMost == 1 ? 1 : 2
+        for (int d = 0; d < lds - 4; d += 8) {
+          const float2 x = two_at(qa + d), y = two_at(qa + 8 * ld + d), k = two_at(ka + d);
+          const float2 u = two_at(sa + d), w = two_at(sa + lds + d);
+          const Parts<4> q = quad_of(x.x, y.x, x.y, y.y);
+          add(o, q, {pair_of(u.x, u.y), pair_of(w.x, w.y), pair_of(k.x, k.y)});
         }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = m0 + g + 8 * y, j = 8 * n0 + 2 * t, apart = reverse ? j - i : i - j;
+        if (!none)
+          *reinterpret_cast<float2 *>(sp + i * kLdP + j) =
+              make_float2(apart < 0 ? 0.f : o[2][2 * y] * power(lg, apart),
+                          apart < (reverse ? -1 : 1) ? 0.f : o[2][2 * y + 1] * power(lg, apart + (reverse ? 1 : -1)));
+        const float c = power(lg, reverse ? n - 1 - i : i + 1);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-            s[x][y] = fmaf(q[x].w, k[y].w, fmaf(q[x].z, k[y].z, fmaf(q[x].y, k[y].y, fmaf(q[x].x, k[y].x, s[x][y]))));
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int i = r16 + 16 * x, j = c16 + 16 * y, apart = p.reverse ? j - i : i - j;
-          sp[i * (kC + 4) + j] = apart < 0 ? 0.f : s[x][y] * power(lg, apart);
-        }
-      // O: rows r16 and r16 + 16, columns 4 c16 ..; the state's part first, then its factor
-      float o[2][4] = {};
-#pragma unroll 1
-      for (int d = 0; d < ld - 4; d += 4) {
-        float4 q[2], x[4];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) q[y] = *reinterpret_cast<const float4 *>(sq + (r16 + 16 * y) * ld + d);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4 *>(S + (d + y) * kCols + 4 * c16);
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          axpy(o[y], q[y].x, x[0]), axpy(o[y], q[y].y, x[1]), axpy(o[y], q[y].z, x[2]), axpy(o[y], q[y].w, x[3]);
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int i = r16 + 16 * y;
-        const float c = power(lg, p.reverse ? n - 1 - i : i + 1);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[y][x] *= c;
+          for (int e = 2 * y; e < 2 * y + 2; ++e) out2[x].big[e] = o[x][e] * c;
       }
       __syncthreads();  // P is there
+      {
+        const float *pa = sp + (m0 + g) * kLdP + t, *va = sv + t * kLdV + 16 * n0 + 2 * g;
+        const int first = reverse ? m0 : 0, end = reverse ? kC : m0 + 16;
 #pragma unroll 2
-      for (int r = 0; r < kC; r += 4) {
-        float4 w[2], x[4];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) w[y] = *reinterpret_cast<const float4 *>(sp + (r16 + 16 * y) * (kC + 4) + r);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4 *>(sv + (r + y) * kCols + 4 * c16);
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          axpy(o[y], w[y].x, x[0]), axpy(o[y], w[y].y, x[1]), axpy(o[y], w[y].z, x[2]), axpy(o[y], w[y].w, x[3]);
+        for (int r = first; r < end; r += 8) {
+          const Parts<4> w = quad_of(pa[r], pa[8 * kLdP + r], pa[r + 4], pa[8 * kLdP + r + 4]);
+          const float2 x = two_at(va + r * kLdV), y = two_at(va + (r + 4) * kLdV);
+          add(out2, w, {pair_of(x.x, y.x), pair_of(x.y, y.y)});
+        }
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int i = r16 + 16 * y;
+        const int i = m0 + g + 8 * y, c = 16 * n0 + 4 * t;
         if (i >= n) continue;
-        In *out = static_cast<In *>(p.out) + ((b * a.T + t0 + i) * a.H + h) * p.dv + c0 + 4 * c16;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (4 * c16 + x < cols) from_f(p.os * o[y][x], out[x]);
+        const float4 r = scaled(make_float4(out2[0][2 * y], out2[1][2 * y], out2[0][2 * y + 1], out2[1][2 * y + 1]), os);
+        store4<In, kVec>(out + y * out8, r, cols - c);
       }
+      out += reverse ? -4 * out8 : 4 * out8;
     }
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
-      if (64 * i >= srows) break;
+      const int d = 64 * i + d0;
+      if (d >= dk) break;
+      Sum sum[4];
+      // (channels past the last vector of k lie in the next row: of no state that counts)
+      const float *va = sw + t * kLdV + s0 + 2 * g, *ka = sk + t * ld + d + 4 * g;
+#pragma unroll 1
+      for (int r = 0; r < kC; r += 8) {
+        const float2 x = two_at(va + r * kLdV), y = two_at(va + (r + 4) * kLdV);
+        const float4 k = *reinterpret_cast<const float4 *>(ka + r * ld);
+        const float4 l = *reinterpret_cast<const float4 *>(ka + (r + 4) * ld);
+        const Parts<4> v = quad_of(x.x, x.y, y.x, y.y);
+        add(sum, v, {pair_of(k.x, l.x), pair_of(k.y, l.y), pair_of(k.z, l.z), pair_of(k.w, l.w)});
+      }
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) st[i][x][y] *= now;
-      // (channels past the last vector of k lie in the next row: of no state that counts)
-      const int d = min(64 * i + 4 * r16, ld - 4);
-#pragma unroll 4
-      for (int r = 0; r < kC; ++r) {
-        const float4 k = *reinterpret_cast<const float4 *>(sk + r * ld + d);
-        const float4 v = *reinterpret_cast<const float4 *>(sw + r * kCols + 4 * c16);
-        axpy(st[i][0], k.x, v), axpy(st[i][1], k.y, v), axpy(st[i][2], k.z, v), axpy(st[i][3], k.w, v);
-      }
+        for (int y = 0; y < 4; ++y) st[i][x][y] = fmaf(now, st[i][x][y], sum[x][y]);
     }
   }
   if (kStates || (p.final && sg == (p.reverse ? 0 : a.nseg - 1))) {
@@ -363,14 +426,14 @@ __global__ void __launch_bounds__(kThreads, kMost == 2 ? 2 : 1) decay_generic_ke
       for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const int d = 64 * i + 4 * r16 + x, c = 4 * c16 + y;
+          const int d = 64 * i + d0 + 8 * t + 4 * (y % 2) + x, c = s0 + 2 * g + y / 2;
           if (d < dk && c < cols) to[(int64_t)d * p.dv + c0 + c] = st[i][x][y];
         }
   }
   if constexpr (!kStates) {  // tokens past the row's end
-    for (int64_t t = max(t_lo, t_end) + row; t < t_hi; t += kThreads / 8)
+    for (int64_t at = max(t_lo, t_end) + row; at < t_hi; at += kThreads / 8)
       for (int c = l8; c < cols; c += 8)
-        from_f(0.f, static_cast<In *>(p.out)[((b * a.T + t) * a.H + h) * p.dv + c0 + c]);
+        from_f(0.f, static_cast<In *>(p.out)[((b * a.T + at) * a.H + h) * p.dv + c0 + c]);
   }
 }
 
@@ -392,8 +455,9 @@ cudaError_t generic(const DecayArgs &a, cudaStream_t s) {
   const int groups = (dv + kCols - 1) / kCols;
   const int64_t grid = a.B * a.H * groups * a.nseg * a.passes;
   if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-  auto kern = dk <= 128 ? (vec ? decay_generic_kernel<In, 2, kStates, true> : decay_generic_kernel<In, 2, kStates, false>)
-                        : (vec ? decay_generic_kernel<In, 4, kStates, true> : decay_generic_kernel<In, 4, kStates, false>);
+  auto kern = dk <= 64    ? (vec ? decay_generic_kernel<In, 1, kStates, true> : decay_generic_kernel<In, 1, kStates, false>)
+              : dk <= 128 ? (vec ? decay_generic_kernel<In, 2, kStates, true> : decay_generic_kernel<In, 2, kStates, false>)
+                          : (vec ? decay_generic_kernel<In, 4, kStates, true> : decay_generic_kernel<In, 4, kStates, false>);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Floats(kDecayMaxD).total(kStates) * 4);
   if (e != cudaSuccess) return e;

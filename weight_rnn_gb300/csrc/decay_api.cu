@@ -57,14 +57,17 @@ int sm_count() {
 // Into how many segments the time axis is cut.  On the tensor cores 128 tokens take a CTA
 // about 2.4 us with all products and 1.7 with those of the states alone, an item's start
 // and end 6 us, and CTAs share the work evenly where there is more than a round of it,
-// but for rows with lengths; on the CUDA cores 36 and 12 us at two CTAs an SM, in whole
-// rounds.  A cut adds the pass for the states, its states' way through memory, and two
-// launches.
+// but for rows with lengths.  In float32 they take 20 and 5 us at 64 channels, 36 and 11
+// at 128, two CTAs an SM (one above that), in whole rounds.  A cut adds the pass for the
+// states, their way through memory, and two launches.
 int segments(const DecayArgs &a, int64_t state_passes, bool tc) {
   const int64_t chunks = (a.T + delta::kDecayChunk - 1) / delta::kDecayChunk;
   const int width = tc ? 128 : 64;
-  const double whole = tc ? 2.4 : 36.0, part = tc ? 1.7 : 12.0;
-  const int64_t slots = (int64_t)sm_count() * (tc ? 1 : 2);
+  int dk = 1;
+  for (int i = 0; i < a.passes; ++i) dk = dk > a.pass[i].dk ? dk : a.pass[i].dk;
+  const double two = dk > 128 ? 0.5 : 1.0;
+  const double whole = tc ? 2.4 : (4.0 + 0.25 * dk) * two, part = tc ? 1.7 : (0.3 + 0.08 * dk) * two;
+  const int64_t slots = (int64_t)sm_count() * (tc || dk > 128 ? 1 : 2);
   int64_t items = 0, bytes = 0;
   for (int i = 0; i < a.passes; ++i) items += a.B * a.H * ((a.pass[i].dv + width - 1) / width);
   bytes = state_passes * a.B * a.H * a.pass[0].dk * a.pass[0].dv * 4;
