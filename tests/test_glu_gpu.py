@@ -10,6 +10,7 @@ import torch
 
 import block_ref as ref
 import weight_rnn_gb300 as wr
+from test_slopes_gpu import MAGNITUDES, bound
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -203,3 +204,37 @@ def test_graph_and_side_stream(M, N):
     for p, q in zip((*out, *grads, tiny), (*want, *wgrad, small)):
         assert torch.equal(p, q)
     wr.delta_check_device()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype,M,N,K", [(BF, 3, 72, 64), (BF, 300, 72, 64), (BF, 1500, 2088, 512), (F32, 5, 72, 40)])
+def test_ends_of_the_activations_range(act, dtype, M, N, K):
+    """Gates of every size, through weights that each copy one element of a row; the other
+    half is 1.5.  The value's error is |g| times the logistic function's (test_slopes_gpu),
+    which is 0 where it is below float32's range."""
+    g = torch.tensor([v for m in MAGNITUDES for v in (m, -m)]).repeat(-(-N // 36))[:N].to(dtype)
+    x, w = torch.zeros(M, K, dtype=dtype), torch.zeros(2 * N, K, dtype=dtype)
+    x[:, 0], w[:N, 0], w[N:, 0] = 1.0, g, 1.5
+    out, pre = wr.delta_glu_fwd(x.cuda(), w.cuda(), act=act, save_pre=True)
+    dout = torch.zeros(M, N, dtype=dtype)
+    dout[M // 2] = 1.0
+    dx, dw, db = wr.delta_glu_bwd(x.cuda(), w.cuda(), dout.cuda(), pre, act=act)
+    p = g.double().requires_grad_(True)
+    value = ref.act(act, p)
+    (slope,) = torch.autograd.grad(value.sum(), p)
+    p, value = p.detach(), value.detach()
+    c, k = (8.0 / torch.pi) ** 0.5, 0.044715
+    s = torch.special.expit(p if act == "silu" else c * (p + k * p ** 3))
+    arg = p.abs() if act == "silu" else c * (p.abs() + k * p.abs() ** 3)
+    ev = p.abs() * (s * 2.0 ** -21 + s * (1 - s) * arg * 2.0 ** -22 + 2.0 ** -125) + U * value.abs()
+    es, half = bound(act, p), ref.HALF[dtype]
+    within(pre, torch.cat([p, torch.full_like(p, 1.5)]).expand(M, 2 * N), 0.0, "pre")
+    eo = 1.5 * ev + U * (1.5 * value).abs()
+    o = torch.where(1.5 * value > torch.finfo(dtype).max, torch.inf, 1.5 * value)  # 1.5 times 3e38 has no value
+    within(out, o.expand(M, N), eo + half * (1.5 * value.abs() + eo), "out")
+    d = torch.cat([1.5 * slope, value])
+    e = torch.cat([1.5 * es, ev]) + 2 * U * d.abs()
+    within(db, d, e, "dbias")
+    want = d[:, None] * x[M // 2].double()
+    e = (e + half * (d.abs() + e))[:, None] * x[M // 2].double()  # dpre is rounded, and dw
+    within(dw, want, e + half * (want.abs() + e), "dw")

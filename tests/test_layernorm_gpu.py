@@ -197,3 +197,15 @@ def test_graph_and_side_stream():
     torch.cuda.synchronize()
     for p, q in zip((*out, *grads), (*want, *wgrad)):
         assert torch.equal(p, q)
+
+
+def test_sizes_of_elements():
+    """Squares within float32's range up to its end; past it a row counts as infinitely
+    wide: rstd is 0 and y the bias."""
+    x, _, w, b, _, _ = inputs(6, 512, F32, 11)
+    for i, size in enumerate((1e-30, 1e-10, 1e10, 1e17, 1e22, 1e30)):
+        x[i] *= size
+    got = [t.cpu() for t in wr.delta_add_layernorm_fwd(x.cuda(), w.cuda(), b.cuda(), eps=EPS)]
+    check([t[:4] for t in got], x[:4], None, w, b)
+    assert not got[3][4:].any()
+    assert torch.equal(got[0][4:], b.float().expand(2, -1))
