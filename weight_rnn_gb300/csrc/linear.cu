@@ -337,9 +337,11 @@ __global__ void __launch_bounds__(256) dpre_kernel(DpreArgs p) {
 }
 
 // The gated layer's: dpre [M][2 N] = (dout u act'(g), dout act(g)) from pre = (g, u),
-// and the sums of its 2 N columns.  As above, a column of either half a lane.
+// and the sums of its 2 N columns.  As above, a column of either half a lane.  One row at
+// a time leaves room for four CTAs an SM, all of them resident at once (two rows, and two
+// CTAs: 35 us for 26 at M4096 N4096, where reading and writing 168 MB takes 25).
 template <typename T, int V>
-__global__ void __launch_bounds__(256) glu_dpre_kernel(DpreArgs p) {
+__global__ void __launch_bounds__(256, 4) glu_dpre_kernel(DpreArgs p) {
   struct __align__(sizeof(T) * V) Vec { T v[V]; };
   __shared__ float sum[2][8][32 * V];
   const int64_t c = ((int64_t)blockIdx.x * 32 + threadIdx.x) * V;
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(256) glu_dpre_kernel(DpreArgs p) {
   float s[2][V];
 #pragma unroll
   for (int i = 0; i < V; ++i) s[0][i] = s[1][i] = 0.f;
-  constexpr int kAhead = V == 1 ? 4 : 2;  // rows a thread asks for at a time
+  constexpr int kAhead = V == 1 ? 4 : 1;  // rows a thread asks for at a time
   const int64_t step = (int64_t)gridDim.y * 8;
   if (c < p.N)
     for (int64_t m0 = (int64_t)blockIdx.y * 8 + threadIdx.y; m0 < p.M; m0 += step * kAhead) {
@@ -605,7 +607,7 @@ cudaError_t launch_pack(const void *src, void *dst, int64_t rows, int64_t cols, 
                       ld * size, ldp * size);
 }
 
-// (the gated layer's: fewer CTAs of more rows, M4096 N4096 35 us for 42)
+// (the gated layer's: as many as are resident; twice as many take 2 us more at M4096 N4096)
 constexpr int64_t kGluCtas = 4;
 int64_t dpre_parts(const DpreArgs &p) {
   // CTAs for every SM many times over, but no fewer than 4 rows a thread (M512
