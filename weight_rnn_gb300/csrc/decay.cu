@@ -41,7 +41,8 @@ int sm_count() {
 }
 
 // ------------------------------------------------------------------ one token
-// HBM-bound: the state is read and written once.  A CTA has a head's state, or 32
+// HBM-bound: the state is read and written once (256 sequences of 32 heads, d 128:
+// 156 us, 6.9 TB/s; one sequence 2.5, a launch).  A CTA has a head's state, or 32
 // of its columns where there are few heads; a thread keeps V neighbouring columns
 // of every RG-th row, kAhead rows asked for at a time, and the rows' partial
 // outputs meet in shared memory in a fixed order.

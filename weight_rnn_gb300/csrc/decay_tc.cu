@@ -40,8 +40,15 @@
 //          of the tokens, each warpgroup
 //   12-19  the state, and O: 64 value columns each warpgroup
 //
-// Bound by HBM: 4 tensors of 32 KB a chunk.  Every mbarrier wait is bounded: a
-// timeout sets a device error word and the kernel winds down.
+// Bound by HBM where every SM has its share of a long call, 4 tensors of 32 KB a chunk
+// (2.9 us at 152 CTAs; the warps' own work is 2.3): B4 T8192 H32 d128 170 us, 6.3 TB/s.
+// The gradients, three such passes at a time, read 9.5 tensors from memory for the 7 of
+// the call: B4 T4096 H32 240 us, 5.3 TB/s of them.  Where the time axis is cut, k and v
+// are read twice: B1 T65536 H8 143 us.  What the pace hangs on is instructions, in caches
+// shared by five groups of warps (from 111 KB of code to 70 KB: 204 -> 171 us), and lines
+// of the epilogue's stores.  (A warpgroup of its own for O's way out, 768 threads with
+// registers moved by setmaxnreg: 205 us, 278 for the gradients.)  Every mbarrier wait is
+// bounded: a timeout sets a device error word and the kernel winds down.
 #include <cuda_bf16.h>
 
 #include "chain.cuh"

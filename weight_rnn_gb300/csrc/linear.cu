@@ -89,7 +89,8 @@ __device__ __forceinline__ uint4 piece(const uint8_t *row, int64_t k, int64_t by
   }
 }
 
-// The gated form (kGlu) takes 8 rows of either half of w for the 16.
+// The gated form (kGlu) takes 8 rows of either half of w for the 16 (one row through 2 x
+// 8192 x 4096: 19.8 us, 6.8 TB/s of w).
 template <bool kF8, int NT, bool kVec, bool kGlu>
 __global__ void __launch_bounds__(kSmallWarps * 32) small_kernel(LinearArgs a, int cs) {
   constexpr int kSize = kF8 ? 1 : 2, kTok = 8 * NT;

