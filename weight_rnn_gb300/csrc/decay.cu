@@ -260,26 +260,13 @@ __global__ void __launch_bounds__(kThreads, kMost <= 2 ? 2 : 1) decay_generic_ke
   const int warp = tid / 32, g = tid % 32 / 4, t = tid % 4;  // and in products:
   const int m0 = warp % 2 * 16, n0 = warp / 2;               // 16 tokens, 8 of P's columns, 16 of O's
   const int s0 = warp % 4 * 16, d0 = warp / 4 * 32;          // 16 value columns and 32 channels, every 64, of the state
-  chain_wait();
+  if (kStates || !a.joined) chain_wait();
   const float lg = log2f(a.decay[h]);
   int64_t len = a.lengths ? a.lengths[b] : a.T;
   len = len < 0 ? 0 : len > a.T ? a.T : len;
   const int64_t t_lo = sg * a.seg, t_hi = min(t_lo + a.seg, a.T);
   const int64_t t_end = min(t_hi, len);  // tokens [t_lo, t_end) count
   const int64_t state_at = kStates || a.nseg > 1 ? bh * a.nseg + sg : bh;
-  // st[i][x][y]: channel 64 i + d0 + 8 t + 4 (y % 2) + x, value column s0 + 2 g + y / 2
-  float st[kMost][4][4];
-#pragma unroll
-  for (int i = 0; i < kMost; ++i)
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int d = 64 * i + d0 + 8 * t + 4 * (y % 2) + x, c = s0 + 2 * g + y / 2;
-        st[i][x][y] = 0.f;
-        if (!kStates && p.init && d < dk && c < cols)
-          st[i][x][y] = p.init[state_at * dk * p.dv + (p.init_t ? (int64_t)(c0 + c) * dk + d : (int64_t)d * p.dv + c0 + c)];
-      }
   const int64_t chunks = t_end > t_lo ? (t_end - t_lo + kC - 1) / kC : 0;
   const int64_t from = t_lo + (p.reverse && chunks > 0 ? chunks - 1 : 0) * kC, hop = p.reverse ? -kC : kC;
   // this thread's rows, of the chunk that is asked for
@@ -307,6 +294,20 @@ __global__ void __launch_bounds__(kThreads, kMost <= 2 ? 2 : 1) decay_generic_ke
   float owed = 0.f;
   int kept = -1;
   ask(row < left);
+  if (!kStates && a.joined) chain_wait();  // (all but the joined states was there before)
+  // st[i][x][y]: channel 64 i + d0 + 8 t + 4 (y % 2) + x, value column s0 + 2 g + y / 2
+  float st[kMost][4][4];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int d = 64 * i + d0 + 8 * t + 4 * (y % 2) + x, c = s0 + 2 * g + y / 2;
+        st[i][x][y] = 0.f;
+        if (!kStates && p.init && d < dk && c < cols)
+          st[i][x][y] = p.init[state_at * dk * p.dv + (p.init_t ? (int64_t)(c0 + c) * dk + d : (int64_t)d * p.dv + c0 + c)];
+      }
   for (int64_t ci = 0; ci < chunks; ++ci) {
     const int n = min(kC, left);
     if (n != kept) keep = keep_of(lg, n), kept = n;

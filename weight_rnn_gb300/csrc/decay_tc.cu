@@ -350,7 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
-  chain_wait();
   if (warp == 4) {
     bool there = false;
     if (lane < kParts) there = part_at<kStates>(a, lane, sh.part[lane]);
@@ -662,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     Turn<1> o;
     bool begun = false;
     uint64_t S[32];  // pairs of columns
+    chain_wait();  // for the joined states: all else was there before that kernel began
     const auto publish = [&] {  // the bfloat16 copy that Q S reads, once the one before has been read
       if (begun && !wait(&sh, &sh.sempty, o.phase ^ 1u, 5)) return false;
 #pragma unroll
