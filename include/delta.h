@@ -540,7 +540,7 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
  *                         allowed
  *
  * 1 <= dk, dv <= 256.  bfloat16 with dk <= 128, dk and dv multiples of 8 and q, k
- * and v in whole 16-byte pieces (addresses and strides, none of them 0) runs on the
+ * and v in whole 16-byte pieces (addresses and strides; the tokens' not 0) runs on the
  * tensor cores in chunks of 128 tokens, all else in float32 in chunks of 32, each
  * product as three of tf32 that leave out 2^-22 of a term.  The state is float32
  * throughout; in bfloat16's chunks a token's way into it is rounded to 2^-16 of itself,

@@ -35,8 +35,8 @@ def same_strides(t):
 
 def on_tc(q, k, v):
     dk, dv = q.shape[-1], v.shape[-1]
-    whole = all(t.storage_offset() % 8 == 0 and all(s % 8 == 0 and s > 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1)
-                for t in (q, k, v))
+    whole = all(t.storage_offset() % 8 == 0 and (t.stride(1) > 0 or t.shape[1] == 1) and
+                all(s % 8 == 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1) for t in (q, k, v))
     return q.dtype == BF and dk <= 128 and dk % 8 == 0 and dv % 8 == 0 and whole
 
 
@@ -98,6 +98,24 @@ def test_dims_without_the_tensor_cores(shape, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_layouts(layout, dtype):
     check(*inputs(2, 150, 3, 64, 32, dtype, layout=layout))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("what", ["heads of k and v", "rows of q", "rows of k, heads of v", "tokens"])
+def test_shared_heads_rows_and_tokens(what, dtype):
+    """Axes with a stride of 0; a gradient is that of each place by itself."""
+    B, T, H = 3, 150, 4
+    q, k, v, decay, h0 = inputs(B, T, H, 64, 48, dtype, layout="heads")
+    wide = lambda t: t.expand(B, T, H, t.shape[-1])  # noqa: E731
+    if what == "heads of k and v":
+        k, v = wide(k[:, :, 1:2]), wide(v[:, :, 2:3])
+    elif what == "rows of q":
+        q = wide(q[1:2])
+    elif what == "rows of k, heads of v":
+        k, v = wide(k[2:]), wide(v[:, :, :1])
+    else:
+        v = wide(v[:, 7:8])
+    check(q, k, v, decay, h0, lengths=torch.tensor([150, 0, 129], dtype=torch.int32))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])

@@ -82,6 +82,7 @@ struct TcPass {
   __nv_bfloat16 *to;  // out
   float os, kvs;
   int dk, dv;
+  int8_t rows[3], heads[3];    // of q, k, v: 1, or 0 where all share one batch row, one head
   bool reverse, init_t, wide;  // wide: out's rows are whole 32-byte pieces
 };
 struct TcArgs {
@@ -387,10 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           unsigned char *tile = i == 0 ? tile_k(g.slot) : i == 1 ? tile_q(g.slot) : tile_v(g.slot);
           if (!(ok = wait(&sh, empty, g.phase ^ 1u, 0))) break;
           if (elect_one()) {
-            const int d0 = i == 2 ? c0 : 0;
+            const int x = i == 0 ? 1 : i == 1 ? 0 : 2, d0 = i == 2 ? c0 : 0;
+            const int hx = h * p.heads[x], bx = b * p.rows[x];
             mbar_arrive_expect_tx(full, kTile);
-            tma_load_4d(tile, map, full, d0, h, t0, b);
-            tma_load_4d(tile + kBlk, map, full, d0 + 64, h, t0, b);
+            tma_load_4d(tile, map, full, d0, hx, t0, bx);
+            tma_load_4d(tile + kBlk, map, full, d0 + 64, hx, t0, bx);
           }
           __syncwarp();
         }
@@ -819,6 +821,8 @@ int sm_count() {
 cudaError_t make_map(CUtensorMap *map, const void *p, int64_t d, int64_t H, int64_t T, int64_t B, const int64_t (&st)[3]) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
+  if (st[2] == 0) H = 1;  // (shared)
+  if (st[0] == 0) B = 1;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
   // (the stride of an axis with one entry is never used)
   const auto bytes = [](int64_t n, int64_t s) { return (cuuint64_t)(n > 1 ? s * 2 : 16); };
@@ -860,6 +864,8 @@ cudaError_t run(const DecayArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     o.init = p.init; o.final = p.final; o.to = static_cast<__nv_bfloat16 *>(p.out);
     o.os = p.os; o.kvs = p.kvs; o.dk = p.dk; o.dv = p.dv; o.reverse = p.reverse; o.init_t = p.init_t;
+    const int64_t *strides[3] = {p.qs, p.ks, p.vs};
+    for (int x = 0; x < 3; ++x) o.rows[x] = strides[x][0] != 0, o.heads[x] = strides[x][2] != 0;
     o.wide = p.dv % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     const int g = (p.dv + kD - 1) / kD;
     if (g > t.groups) t.groups = g;
@@ -900,14 +906,14 @@ cudaError_t run(const DecayArgs &a, cudaStream_t s) {
 }  // namespace
 
 // What the tensor maps can describe: addresses and strides in whole 16-byte
-// pieces, no axis walked without a step, sizes in 32 bits.
+// pieces, sizes in 32 bits; heads or batch rows that share their values as one.
 bool decay_tc_fits(const DecayArgs &a) {
   if (!a.bf16 || a.T >= (int64_t(1) << 30)) return false;
   const int64_t n[3] = {a.B, a.T, a.H};
   const auto ok = [&](const void *p, const int64_t (&st)[3]) {
     if (reinterpret_cast<uintptr_t>(p) % 16) return false;
     for (int i = 0; i < 3; ++i)
-      if (n[i] > 1 && (st[i] % 8 || st[i] <= 0 || st[i] >= (int64_t(1) << 38))) return false;
+      if (n[i] > 1 && (st[i] % 8 || (i == 1 && st[i] == 0) || st[i] >= (int64_t(1) << 38))) return false;
     return true;
   };
   for (int i = 0; i < a.passes; ++i) {
