@@ -41,14 +41,17 @@
 //   12-19  the state, and O: 64 value columns each warpgroup
 //
 // Bound by HBM where every SM has its share of a long call, 4 tensors of 32 KB a chunk
-// (2.9 us at 152 CTAs; the warps' own work is 2.3): B4 T8192 H32 d128 170 us, 6.3 TB/s.
-// The gradients, three such passes at a time, read 9.5 tensors from memory for the 7 of
-// the call: B4 T4096 H32 240 us, 5.3 TB/s of them.  Where the time axis is cut, k and v
-// are read twice: B1 T65536 H8 143 us.  What the pace hangs on is instructions, in caches
-// shared by five groups of warps (from 111 KB of code to 70 KB: 204 -> 171 us), and lines
-// of the epilogue's stores.  (A warpgroup of its own for O's way out, 768 threads with
-// registers moved by setmaxnreg: 205 us, 278 for the gradients.)  Every mbarrier wait is
-// bounded: a timeout sets a device error word and the kernel winds down.
+// (2.9 us at 152 CTAs): B4 T8192 H32 d128 170 us, 6.3 TB/s.  The warps' own work takes 2.3
+// us a chunk, 4400 cycles, of which shared memory is busy for 3000: tiles in, 96 KB, what
+// the products read, 224 (SS ones both operands, 64 cycles for 16 channels, where the
+// tensor cores would take 32), K' and S, 64.  Bound by that are heads of 64 channels (B4
+// T8192 H32 125 us; what a narrow head has not is left out: 146 with it) and in part the
+// gradients, three such passes at a time, which read 9.5 tensors from memory for the 7 of
+// the call: B4 T4096 H32 236 us.  Where the time axis is cut, k and v are read twice: B1
+// T65536 H8 142 us.  Next is instruction fetch, with caches shared by five groups of warps
+// (from 111 KB of code to 70 KB: 204 -> 171 us).  (A warpgroup of its own for O's way out,
+// 768 threads with registers moved by setmaxnreg: 205 us, 278 for the gradients.)  Every
+// mbarrier wait is bounded: a timeout sets a device error word and the kernel winds down.
 #include <cuda_bf16.h>
 
 #include "chain.cuh"
@@ -390,9 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           if (elect_one()) {
             const int x = i == 0 ? 1 : i == 1 ? 0 : 2, d0 = i == 2 ? c0 : 0;
             const int hx = h * p.heads[x], bx = b * p.rows[x];
-            mbar_arrive_expect_tx(full, kTile);
+            const bool both = (i == 2 ? p.dv - c0 : p.dk) > 64;  // (else nothing reads the second block)
+            mbar_arrive_expect_tx(full, both ? kTile : kBlk);
             tma_load_4d(tile, map, full, d0, hx, t0, bx);
-            tma_load_4d(tile + kBlk, map, full, d0 + 64, hx, t0, bx);
+            if (both) tma_load_4d(tile + kBlk, map, full, d0 + 64, hx, t0, bx);
           }
           __syncwarp();
         }
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           if (elect_one()) {
             // MN-major: 16 tokens are 16 rows of 128 bytes
             const uint64_t dvv = sdesc_sw128(smem_u32(tile_v(g.slot)), kBlk, 1024);
-#pragma unroll 1
+#pragma unroll
             for (int k = 0; k < 8; ++k)
               mma_ts(tmem + kO, tmem + kG + 32 * (k >> 1) + 8 * (k & 1), dvv + (uint64_t)(k * 2048 >> 4), id_v, true);
             mma_commit(&sh.ofull);
@@ -482,8 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           if (elect_one()) {
             const uint64_t dq = sdesc_sw128(smem_u32(tile_q(g.slot)), 0, 1024);
             const uint64_t ds = sdesc_sw128(smem_u32(base + kOffS), kBlk, 1024);
-#pragma unroll 1
-            for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kO, dq + step_k(k), ds + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < ksteps) mma_ss(tmem + kO, dq + step_k(k), ds + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
             mma_commit(&sh.sempty);
             mma_commit(&sh.qempty[g.slot]);
           }
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     const auto share = [&](const Part &t, auto direction) {
       constexpr bool kReverse = decltype(direction)::value;
       const float lg = t.lg, kvs = a.pass[t.pass].kvs;
-      const bool two = t.two;
+      const bool two = t.two, mine = quarter * 32 < a.pass[t.pass].dk;  // else no such channels
       const float s16 = ex2(16.f * lg);
       const uint64_t step16 = pk(s16, s16);
       uint64_t c2[4];  // (see scores)
@@ -538,8 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         const uint32_t tile = smem_u32(tile_k(g.slot));
         const int j0 = half * 64 + 2 * (lane & 3);  // of the lane's first pair, and 8 on its second
         uint64_t w[2];
+        if (!mine && gone == kBufs && !wait(&sh, &sh.dsfull[u.slot], u.phase ^ 1u, 4)) return false;
+        if (!mine && gone < kBufs) ++gone;
 #pragma unroll 1
-        for (int i4 = 0; i4 < 4; ++i4) {
+        for (int i4 = mine ? 0 : 4; i4 < 4; ++i4) {
           const int i = kReverse ? i4 : 3 - i4;
           const uint32_t tok = (uint32_t)(half * 64 + i * 16 + (lane >> 4) * 8 + (lane & 7));
           if (i4 == 0 || n < kC) {
@@ -661,16 +668,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     const int quarter = warp & 3, half = (warp - 12) / 4, d = quarter * 32 + lane;
     Turn<kBufs> u;
     Turn<1> o;
-    bool begun = false;
+    bool begun = false, mine = true;  // mine: some of the warp's rows and columns are there
     uint64_t S[32];  // pairs of columns
     chain_wait();  // for the joined states: all else was there before that kernel began
     const auto publish = [&] {  // the bfloat16 copy that Q S reads, once the one before has been read
       if (begun && !wait(&sh, &sh.sempty, o.phase ^ 1u, 5)) return false;
+      if (mine) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4 *>(base + kOffS + half * kBlk + piece_at(d, i)) =
-            make_uint4(narrow2(S[4 * i]), narrow2(S[4 * i + 1]), narrow2(S[4 * i + 2]), narrow2(S[4 * i + 3]));
-      fence_proxy_async_smem();
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4 *>(base + kOffS + half * kBlk + piece_at(d, i)) =
+              make_uint4(narrow2(S[4 * i]), narrow2(S[4 * i + 1]), narrow2(S[4 * i + 2]), narrow2(S[4 * i + 3]));
+        fence_proxy_async_smem();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sfull);
       return true;
@@ -679,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
       const Part &t = sh.part[m];
       const TcPass &p = a.pass[t.pass];
       const int v0 = t.c0 + half * 64, live = d < p.dk ? min(64, p.dv - v0) : 0;  // this lane's columns
+      mine = quarter * 32 < p.dk && v0 < p.dv;
       if (t.head) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) S[i] = 0;
@@ -728,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          if (!mine) break;
           uint32_t r[16];
           tmem_ld16(tmem_addr(tmem, quarter * 32, cols_ds(u.slot) + half * 64 + 16 * j), r);
           tmem_wait_ld_regs(r);
@@ -754,8 +765,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           const uint64_t cp2 = pk(cp, cp);
           const int have = rest > 0 ? p.dv - v0 : 0;
           const bool wide = p.wide;
+          if (v0 >= p.dv && lane == 0) mbar_arrive(&sh.oempty);
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
+          for (int j = v0 < p.dv ? 0 : 4; j < 4; ++j) {
             uint32_t x[16], w[8];
             tmem_ld16(tmem_addr(tmem, quarter * 32, kO + half * 64 + 16 * j), x);
             tmem_wait_ld_regs(x);
