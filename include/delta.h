@@ -750,7 +750,7 @@ int delta_linear_bwd(const void *x, const void *w, const void *dout, const void 
  *   out   [M, N]   dtype
  *   pre   [M, 2 N] dtype, for delta_glu_bwd, or NULL
  *
- * K > 0, N <= 2^30.  Runs where delta_linear_fwd runs; in float32, a correctness
+ * K > 0, N < 2^30.  Runs where delta_linear_fwd runs; in float32, a correctness
  * path, as a product and an elementwise kernel, with pre in scratch where it is not
  * wanted.
  */

@@ -28,7 +28,7 @@ BWD = dict(x=P(1), w=P(2), dout=P(3), pre=P(4), dx=P(5), dw=P(6), dbias=P(7), M=
            dtype=1, stream=None)
 
 COMMON = [(dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(K=-1), INVALID), (dict(K=0), INVALID),
-          (dict(N=(1 << 30) + 1), UNSUP), (dict(act=3), INVALID), (dict(dtype=2), INVALID), (dict(ldx=15), INVALID),
+          (dict(N=(1 << 30) + 1), UNSUP), (dict(N=1 << 30), UNSUP), (dict(act=3), INVALID), (dict(dtype=2), INVALID), (dict(ldx=15), INVALID),
           (dict(ldw=15), INVALID), (dict(N=1, ldw=8), INVALID), (dict(ldw=1 << 31), UNSUP),
           (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(x=P(1, 1)), ALIGN), (dict(w=P(2, 1)), ALIGN)]
 

@@ -374,7 +374,7 @@ cudaError_t glu_forward(const delta::LinearArgs &a, cudaStream_t s) {
 int glu_sizes(int M, int N, int K, int64_t ldx, int64_t ldw, delta_act act, delta_dtype dtype) {
   const int st = check_dtype(dtype);
   if (st != DELTA_OK) return st;
-  if (N > (1 << 30)) return fail(DELTA_ERR_UNSUPPORTED, "N=%d: two halves of it must be below 2^31", N);
+  if (N >= (1 << 30)) return fail(DELTA_ERR_UNSUPPORTED, "N=%d: two halves of it must be below 2^31", N);
   return linear_sizes(M, 2 * N, K, ldx, ldw, 2 * (int64_t)N, act);
 }
 
