@@ -218,11 +218,15 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
 // w dy and t^ stay in registers between the dots and dx: 512 threads an SM, at up to
 // 128 registers.  32768 x 2048 bfloat16 takes 95 us, 5.6 TB/s, 5 of them in the kernel
 // that adds the CTAs' column sums up.  (w dy and t^ read from the ring a second time, at
-// 80 registers: 152 us.)
-constexpr int kBwdThreads = 512;
+// 80 registers: 152 us.)  With one vector of a row a thread, 768 (rows of up to 32
+// vectors; a million of 128 elements 205 -> 180 us, 1024 threads 202; wider rows take two
+// a thread, 32768 x 2048 with one 111 us).
+template <typename In, int V, int kPer>
+constexpr int bwd_threads() { return kPer == 1 && V * sizeof(In) == 16 ? 768 : 512; }
 
 template <typename In, int V, int kPer, int kT>
-__global__ void __launch_bounds__(kT, V *kPer <= 16 ? kBwdThreads / kT : 1) layernorm_bwd_kernel(NormBwdArgs p) {
+__global__ void __launch_bounds__(kT, V *kPer <= 16 ? bwd_threads<In, V, kPer>() / kT : 1)
+    layernorm_bwd_kernel(NormBwdArgs p) {
   __shared__ float2 part[2][8 * 16];
   extern __shared__ __align__(16) unsigned char ring[];
   const int nwarp = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -334,8 +338,14 @@ cudaError_t fwd_all(const NormArgs &a, cudaStream_t s) {
   return dispatch<In, FwdOne>(q, a, q, s);
 }
 template <typename In>
+Plan plan_of(const NormBwdArgs &a) {
+  constexpr int V = 16 / sizeof(In);
+  const bool one = a.D % V == 0 && a.D <= 32 * V;  // (as plan() has it)
+  return bwd_plan<In>(a, one ? bwd_threads<In, V, 1>() : bwd_threads<In, V, 2>(), true);
+}
+template <typename In>
 cudaError_t bwd_all(const NormBwdArgs &a, cudaStream_t s) {
-  const Plan q = bwd_plan<In>(a, kBwdThreads, true);
+  const Plan q = plan_of<In>(a);
   const cudaError_t e = q.grid > 0 ? dispatch<In, BwdOne>(q, a, q, s) : cudaSuccess;
   return e != cudaSuccess ? e : launch_column_sum(a.partial, a.dweight, a.dbias, a.D, q.grid, 2 * a.D, s);
 }
@@ -346,7 +356,7 @@ cudaError_t launch_layernorm_fwd(const NormArgs &a, cudaStream_t s) {
   return a.bf16 ? fwd_all<__nv_bfloat16>(a, s) : fwd_all<float>(a, s);
 }
 int64_t layernorm_bwd_ctas(const NormBwdArgs &a) {
-  return (a.bf16 ? bwd_plan<__nv_bfloat16>(a, kBwdThreads, true) : bwd_plan<float>(a, kBwdThreads, true)).grid;
+  return (a.bf16 ? plan_of<__nv_bfloat16>(a) : plan_of<float>(a)).grid;
 }
 cudaError_t launch_layernorm_bwd(const NormBwdArgs &a, cudaStream_t s) {
   return a.bf16 ? bwd_all<__nv_bfloat16>(a, s) : bwd_all<float>(a, s);
