@@ -12,7 +12,10 @@
 //
 // K' is k_j g^(n-1-j) (in reverse g^(j+1)) in two bfloat16 parts, hi + lo, which
 // hold it to 2^-16: the states are float32 and returned as such, and with hi alone
-// they would be off by 1e-3.  P and the copy of S that O reads are single bfloat16:
+// they would be off by 1e-3.  With both they are off by 2.4e-6 (plain float32 sums:
+// 2.8e-7).  A third part finds no room in tensor memory: with K' in turns of 32 tokens
+// the states were off by less than 1e-6, and B4 T8192 H32 took 197 us for 170, its
+// gradients' three passes 272 for 236.  P and the copy of S that O reads are single bfloat16:
 // each is off by 2^-8 at most, at random, as the rounding of out itself.
 //
 // Both parts of O share one accumulator: with c_p the factor of S's part (g^(p+1),
@@ -33,9 +36,9 @@
 //
 // Warps (640 threads):
 //   0      TMA producer
-//   1      issues G and P V
+//   1      issues G, Q S and P V
 //   2      TMEM
-//   3      issues Q S and K'^T V
+//   3      issues K'^T V
 //   4-11   P from G, and K' from K, transposed on the way to TMEM: half of the columns,
 //          of the tokens, each warpgroup
 //   12-19  the state, and O: 64 value columns each warpgroup
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 2);
+      mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 1);
       mbar_init(&sh.dsfull[i], 1), mbar_init(&sh.dsempty[i], 8), mbar_init(&sh.kpfull[i], 8);
       mbar_init(&sh.drain[i], 1);
     }
@@ -412,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     if constexpr (!kStates) {
       Turn<kRing> g;
       Turn<1> o;
+      bool begun = false;
       for (int n = 0; ok && n < parts; ++n) {
         const Part &t = sh.part[n];
         const TcPass &p = a.pass[t.pass];
@@ -430,13 +434,23 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             for (int k = 0; k < ksteps; ++k) mma_ss(tmem + kG, dq + step_k(k), dkk + step_k(k), id_g, k > 0);
             mma_commit(&sh.gfull);
             mma_commit(&sh.kempty[g.slot]);
+          }
+          __syncwarp();
+          // Q S, then P V
+          if (!(ok = wait(&sh, &sh.sfull, o.phase, 2) && (!begun || wait(&sh, &sh.oempty, o.phase ^ 1u, 2)))) break;
+          begun = true;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t dq = sdesc_sw128(smem_u32(tile_q(g.slot)), 0, 1024);
+            const uint64_t ds = sdesc_sw128(smem_u32(base + kOffS), kBlk, 1024);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < ksteps) mma_ss(tmem + kO, dq + step_k(k), ds + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
+            mma_commit(&sh.sempty);
             mma_commit(&sh.qempty[g.slot]);
           }
           __syncwarp();
-          // P V, after Q S (sempty)
-          if (!(ok = wait(&sh, &sh.pfull, o.phase, 1) && wait(&sh, &sh.sempty, o.phase, 1) &&
-                     wait(&sh, &sh.vfull[g.slot], g.phase, 1)))
-            break;
+          if (!(ok = wait(&sh, &sh.pfull, o.phase, 1) && wait(&sh, &sh.vfull[g.slot], g.phase, 1))) break;
           tc_fence_after();
           if (elect_one()) {
             // MN-major: 16 tokens are 16 rows of 128 bytes
@@ -455,15 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
   } else if (warp == 3) {
     Turn<kRing> g;
     Turn<kBufs> u;
-    Turn<1> o;
     int gone = 0;  // chunks before, up to kBufs
     for (int n = 0; ok && n < parts; ++n) {
       const Part &t = sh.part[n];
       const TcPass &p = a.pass[t.pass];
       const uint32_t nv = (uint32_t)(min(kD, p.dv - t.c0) + 15) & ~15u;
-      const int ksteps = (p.dk + 15) / 16, steps = t.two ? 16 : 8, to = t.to;
+      const int steps = t.two ? 16 : 8, to = t.to;
       const uint32_t id_v = idesc_bf16(128, (int)nv, false, true);
-      for (int c = t.from; c < to; ++c, g.next(), u.next(), o.next()) {
+      for (int c = t.from; c < to; ++c, g.next(), u.next()) {
         if (!(ok = wait(&sh, &sh.kpfull[u.slot], u.phase, 2) && wait(&sh, &sh.vfull[g.slot], g.phase, 2) &&
                    (gone < kBufs || wait(&sh, &sh.dsempty[u.slot], u.phase ^ 1u, 2))))
           break;
@@ -478,22 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
           mma_commit(&sh.vempty[g.slot]);
         }
         __syncwarp();
-        if constexpr (!kStates) {
-          if (!(ok = wait(&sh, &sh.sfull, o.phase, 2) && (gone == 0 || wait(&sh, &sh.oempty, o.phase ^ 1u, 2)) &&
-                     wait(&sh, &sh.qfull[g.slot], g.phase, 2)))
-            break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t dq = sdesc_sw128(smem_u32(tile_q(g.slot)), 0, 1024);
-            const uint64_t ds = sdesc_sw128(smem_u32(base + kOffS), kBlk, 1024);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < ksteps) mma_ss(tmem + kO, dq + step_k(k), ds + (uint64_t)(k * 2048 >> 4), id_v, k > 0);
-            mma_commit(&sh.sempty);
-            mma_commit(&sh.qempty[g.slot]);
-          }
-          __syncwarp();
-        }
         if (gone < kBufs) ++gone;
       }
     }
