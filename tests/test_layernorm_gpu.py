@@ -4,7 +4,10 @@ sum in chains of at most 16 elements a thread, 5 shuffles and 16 warps, 40 of th
 magnitude m1; the differences, one more, and the mean's error in each; the variance, 40
 for its sum, and twice the mean's error over the deviation, whose square is all that
 stays of it where the deviations add up to 0, so that rstd is off by 64 U and by
-(40 U m1 / s)^2, s the deviation.  An output's own rounding is half a step."""
+(40 U m1 / s)^2, s the deviation.  The sum's rounding, U |t| an element, moves the
+variance by 2 mean(c e) for differences c and roundings e, which is at most 2 U rms(c)
+rms(t), and rstd by half of that times rstd^2.  An output's own rounding is half a
+step."""
 import pytest
 import torch
 
@@ -20,7 +23,7 @@ within = ref.within
 SHAPES = [(1, 1), (3, 7), (1, 4096), (2, 8192), (5, 8191), (700, 64), (700, 72), (513, 1001),
           (4, 2050), (1300, 2048), (400, 4100), (1, 256), (37, 520),
           # several rows to a warp
-          (1000, 128), (1001, 16), (65, 32), (7, 8), (5000, 40), (333, 120), (1, 64)]
+          (1000, 128), (1001, 16), (65, 32), (7, 8), (5000, 40), (333, 120), (1, 64), (1363, 2)]
 
 
 def inputs(rows, D, dtype, seed, wdtype=F32):
@@ -36,7 +39,8 @@ def stats(t):
     mean = t.mean(-1)
     var = (t - mean[..., None]).square().mean(-1)
     rstd = (var + EPS).rsqrt()
-    return mean, rstd, 41 * U * m1, 64 * U + 4 * (41 * U * m1 * rstd) ** 2
+    moved = U * (var * t.square().mean(-1)).sqrt() * rstd ** 2
+    return mean, rstd, 41 * U * m1, 64 * U + 4 * (41 * U * m1 * rstd) ** 2 + moved
 
 
 def check(got, x, res, w, b):
