@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, kMost <= 2 ? 2 : 1) decay_generic_ke
   const int64_t t_lo = sg * a.seg, t_hi = min(t_lo + a.seg, a.T);
   const int64_t t_end = min(t_hi, len);  // tokens [t_lo, t_end) count
   const int64_t state_at = kStates || a.nseg > 1 ? bh * a.nseg + sg : bh;
-  const int64_t chunks = t_end > t_lo ? (t_end - t_lo + kC - 1) / kC : 0;
+  const bool unread = kStates && sg == (p.reverse ? 0 : a.nseg - 1);  // no segment begins with its state
+  const int64_t chunks = t_end > t_lo && !unread ? (t_end - t_lo + kC - 1) / kC : 0;
   const int64_t from = t_lo + (p.reverse && chunks > 0 ? chunks - 1 : 0) * kC, hop = p.reverse ? -kC : kC;
   // this thread's rows, of the chunk that is asked for
   const In *krow = static_cast<const In *>(p.k) + b * p.ks[0] + h * p.ks[2] + (from + row) * p.ks[1] + l8 * 4;
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kMost <= 2 ? 2 : 1) decay_generic_ke
   Keep keep = {0.f, 0.f};  // of a chunk of `kept` tokens
   float owed = 0.f;
   int kept = -1;
-  ask(row < left);
+  ask(chunks > 0 && row < left);
   if (!kStates && a.joined) chain_wait();  // (all but the joined states was there before)
   // st[i][x][y]: channel 64 i + d0 + 8 t + 4 (y % 2) + x, value column s0 + 2 g + y / 2
   float st[kMost][4][4];
@@ -379,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, kMost <= 2 ? 2 : 1) decay_generic_ke
 #pragma unroll
           for (int e = 2 * y; e < 2 * y + 2; ++e) out2[x].big[e] = o[x][e] * c;
       }
-      __syncthreads();  // P is there
+      // the four warps of these 16 tokens have their part of P
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + warp % 2) : "memory");
       {
         const float *pa = sp + (m0 + g) * kLdP + t, *va = sv + t * kLdV + 16 * n0 + 2 * g;
         const int first = reverse ? m0 : 0, end = reverse ? kC : m0 + 16;

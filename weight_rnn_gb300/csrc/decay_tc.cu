@@ -152,6 +152,7 @@ __device__ bool part_at(const TcArgs &a, int k, Part &r) {
   r.t_lo = sg * a.seg, r.t_hi = min(r.t_lo + a.seg, a.T), r.t_end = min(r.t_hi, len);
   r.chunks = r.t_end > r.t_lo ? (r.t_end - r.t_lo + kC - 1) / kC : 0;
   if (r.c0 >= p.dv) r.chunks = 0, r.t_hi = r.t_lo;  // a pass with fewer groups
+  if (kStates && sg == (p.reverse ? 0 : a.nseg - 1)) r.chunks = 0;  // no segment begins with its state
   r.to = min(r.to, r.chunks);
   r.lg = fmaxf(log2f(a.decay[r.h]), kLogZero);
   r.two = r.lg != 0.f || p.kvs != 1.f;  // else K' is K itself
