@@ -51,7 +51,7 @@
 // T8192 H32 125 us; what a narrow head has not is left out: 146 with it) and in part the
 // gradients, three such passes at a time, which read 9.5 tensors from memory for the 7 of
 // the call: B4 T4096 H32 236 us.  Where the time axis is cut, k and v are read twice: B1
-// T65536 H8 142 us.  Next is instruction fetch, with caches shared by five groups of warps
+// T65536 H8 140 us.  Next is instruction fetch, with caches shared by five groups of warps
 // (from 111 KB of code to 70 KB: 204 -> 171 us).  (A warpgroup of its own for O's way out,
 // 768 threads with registers moved by setmaxnreg: 205 us, 278 for the gradients.)  Every
 // mbarrier wait is bounded: a timeout sets a device error word and the kernel winds down.
