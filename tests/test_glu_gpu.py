@@ -238,3 +238,27 @@ def test_ends_of_the_activations_range(act, dtype, M, N, K):
     want = d[:, None] * x[M // 2].double()
     e = (e + half * (d.abs() + e))[:, None] * x[M // 2].double()  # dpre is rounded, and dw
     within(dw, want, e + half * (want.abs() + e), "dw")
+
+
+@pytest.mark.parametrize("glu", [True, False])
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 2048), (2600, 3000, 5000), (5000, 1300, 4104), (3001, 4100, 2570), (9000, 2048, 1500)])
+def test_gradients_together_are_those_alone(M, N, K, glu):
+    """Large layers have both products in one launch where that is shorter: the same sums,
+    also of some rows and columns in 64 bits."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF)  # noqa: E731
+    x, do = r(M, K), r(M, N)
+    w, pre = (r(2 * N, K), r(M, 2 * N)) if glu else (r(N, K), r(M, N))
+    fn = wr.delta_glu_bwd if glu else wr.delta_linear_bwd
+    got = fn(x, w, do, pre, act="silu")
+    dx = fn(x, w, do, pre, act="silu", want=(True, False, False))[0]
+    dw = fn(x, w, do, pre, act="silu", want=(False, True, False))[1]
+    wr.delta_check_device()
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+    p = pre.double().requires_grad_(True)
+    out = ref.act("silu", p[:, :N]) * p[:, N:] if glu else ref.act("silu", p)
+    (dpre,) = torch.autograd.grad(out, p, do.double())
+    rows, cols = [0, 127, 128, 255, M // 2, M - 1], [0, 129, w.shape[0] // 2, w.shape[0] - 1]
+    # two roundings, each within half a step, of the whole of what is looked at
+    for name, g, want in (("dx", dx[rows], dpre[rows] @ w.double()), ("dw", dw[cols], dpre[:, cols].T @ x.double())):
+        assert (g.double() - want).norm() <= (2 * ref.HALF[BF] + 1e-5) * want.norm(), name

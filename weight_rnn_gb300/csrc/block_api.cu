@@ -319,19 +319,24 @@ cudaError_t linear_backward(const void *x, const void *w, const void *dout, cons
   const void *g = form ? d.dpre : dout;
   delta::LinearArgs p{};
   p.kind = bf16 ? delta::kLinBf16 : delta::kLinF32;
-  if (err == cudaSuccess && dx) {
-    p.out = dx; p.M = M; p.N = K;
-    err = bf16 ? delta::launch_gemm_tc({g, ow.p, d.ldp, ow.ld, N, false, true, p, after}, s)
-               : delta::launch_gemm_f32(p, static_cast<const float *>(g), d.ldp, 1, static_cast<const float *>(w), 1,
+  delta::LinearArgs px = p, pw = p;  // of dx, of dw
+  px.out = dx, px.M = M, px.N = K, pw.out = dw, pw.M = N, pw.N = K;
+  const delta::GemmArgs to_x = {g, ow.p, d.ldp, ow.ld, N, false, true, px, after};
+  delta::GemmArgs to_w = {g, ox.p, d.ldp, ox.ld, M, true, true, pw, after};
+  if (err == cudaSuccess && bf16 && dx && dw && delta::gradients_fit(to_x, to_w)) {
+    err = delta::launch_gradients_tc(to_x, to_w, s);
+    const cudaError_t ef = scr.release();
+    return err != cudaSuccess ? err : ef;
+  }
+  if (err == cudaSuccess && dx)
+    err = bf16 ? delta::launch_gemm_tc(to_x, s)
+               : delta::launch_gemm_f32(px, static_cast<const float *>(g), d.ldp, 1, static_cast<const float *>(w), 1,
                                         ldw, N, s);
-    after = true;
-  }
-  if (err == cudaSuccess && dw) {
-    p.out = dw; p.M = N; p.N = K;
-    err = bf16 ? delta::launch_gemm_tc({g, ox.p, d.ldp, ox.ld, M, true, true, p, after}, s)
-               : delta::launch_gemm_f32(p, static_cast<const float *>(g), 1, d.ldp, static_cast<const float *>(x), 1,
+  to_w.dependent = after || dx;
+  if (err == cudaSuccess && dw)
+    err = bf16 ? delta::launch_gemm_tc(to_w, s)
+               : delta::launch_gemm_f32(pw, static_cast<const float *>(g), 1, d.ldp, static_cast<const float *>(x), 1,
                                         ldx, M, s);
-  }
   const cudaError_t ef = scr.release();
   return err != cudaSuccess ? err : ef;
 }

@@ -266,6 +266,10 @@ struct GemmArgs {
 cudaError_t launch_gemm_tc(const GemmArgs &g, cudaStream_t s);
 // about how long it takes
 double gemm_tc_us(int64_t M, int64_t N, int64_t K, bool f8);
+// Both gradients of a layer, x.b and w.b MN-major, in one launch, where that is the shorter
+// way: the same sums as two.
+bool gradients_fit(const GemmArgs &x, const GemmArgs &w);
+cudaError_t launch_gradients_tc(const GemmArgs &x, const GemmArgs &w, cudaStream_t s);
 // The gated layer: epi.N columns of the output, b [2 N][K], epi.pre [M][2 N].
 cudaError_t launch_glu_tc(const GemmArgs &g, cudaStream_t s);
 cudaError_t read_and_clear_linear_error(unsigned int *word);

@@ -803,7 +803,264 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
   }
 }
 
+// ------------------------------------------------------- both gradients at once
+// dx and dw are two products whose tiles fill the last of their rounds badly (M4096
+// K2048, 8192 rows of w: 1.7 and 3.4 rounds of 76 pairs), and one's tiles take longer than
+// the other's, N and M long.  In one launch the pairs take the long tiles in turn, and
+// then as many of the short ones as evens out what they have: those with one long tile
+// fewer `extra` more, before the rest goes round.  A tile's sums are in the order that it
+// has in a launch of its own.  The gated layer's gradients at M4096 N4096 K2048: 186 ->
+// 170 us, the linear layer's 104 -> 98, at M2048 N8192 105 -> 91; M5000 N1300 K4104 takes
+// 2 % longer.
+struct Product {
+  Tiles tiles;
+  LinearArgs epi;
+  bool aligned, wide, a_mn;
+};
+struct Deal {
+  uint32_t workers, fewer, extra, total[2];  // the first `workers - fewer` have a long tile more
+};
+// the n-th task of a worker: which product, which tile
+__device__ __forceinline__ bool task(const Deal &d, uint32_t w, uint32_t n, int &which, uint32_t &tile) {
+  which = 0, tile = w + n * d.workers;
+  if (tile < d.total[0]) return true;
+  n -= w < d.total[0] ? (d.total[0] - w + d.workers - 1) / d.workers : 0u;
+  which = 1;
+  const uint32_t more = d.workers - d.fewer;
+  if (w >= more) {
+    if (n < d.extra) return (tile = n * d.fewer + (w - more)) < d.total[1];
+    n -= d.extra;
+  }
+  return (tile = d.extra * d.fewer + n * d.workers + w) < d.total[1];
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    gradients_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap mb0,
+                     const __grid_constant__ CUtensorMap ma1, const __grid_constant__ CUtensorMap mb1,
+                     const __grid_constant__ Product p0, const __grid_constant__ Product p1, Deal deal) {
+  constexpr int BN = 256, kStages = stages(BN, true), kStage = stage_bytes(BN, true);
+  constexpr uint32_t kCols = 2 * BN;
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
+  unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const uint32_t worker = blockIdx.x / 2;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], 2 * kEpi);
+    mbar_init(&sh.drain, 1);
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&sh.tmem, kCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  chain_wait();
+  int which;
+  uint32_t tile;
+
+  // (roles and waits as in gemm_kernel)
+  if (warp == 0) {
+    int slot = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok && task(deal, worker, n, which, tile); ++n) {
+      const Product &p = which ? p1 : p0;
+      const CUtensorMap *ma = which ? &ma1 : &ma0, *mb = which ? &mb1 : &mb0;
+      int64_t tm, tn;
+      tile_at(p.tiles, tile, tm, tn);
+      const int m0 = (int)(tm * 256) + rank * kBM, n0 = (int)(tn * BN) + rank * (BN / 2), kblocks = p.tiles.kblocks;
+      const bool a_mn = p.a_mn;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!(ok = __all_sync(0xffffffffu, wait(&sh, &sh.empty[slot], phase ^ 1, 0)))) break;
+        if (elect_one()) {
+          unsigned char *st = base + slot * kStage, *stb = st + kBM * kRowBytes;
+          const uint32_t bar = map_cluster(&sh.full[slot], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * kStage);
+          if (a_mn) {
+            tma_load_2d_pair(st, ma, bar, m0, kb * 64);
+            tma_load_2d_pair(st + 8192, ma, bar, m0 + 64, kb * 64);
+          } else {
+            tma_load_2d_pair(st, ma, bar, kb * 64, m0);
+          }
+          tma_load_2d_pair(stb, mb, bar, n0, kb * 64);
+          tma_load_2d_pair(stb + 8192, mb, bar, n0 + 64, kb * 64);
+        }
+        __syncwarp();
+        ++issued;
+        if (++slot == kStages) slot = 0, phase ^= 1;
+      }
+    }
+    if (!ok && rank != 0) {
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    } else if (!ok) {
+      for (int64_t i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
+        for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.full[i % kStages], (i / kStages) & 1); ++j) {
+        }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int slot = 0, acc = 0;
+      uint32_t phase = 0, accphase = 0;
+      bool ok = true;
+      for (uint32_t n = 0; ok && task(deal, worker, n, which, tile); ++n) {
+        const Product &p = which ? p1 : p0;
+        const int kblocks = p.tiles.kblocks;
+        const bool a_mn = p.a_mn;
+        const uint32_t id = a_mn ? idesc_bf16(256, BN, true, true) : idesc_bf16(256, BN, false, true);
+        const uint64_t step = (a_mn ? 2048 : 32) >> 4;
+        if (!(ok = __all_sync(0xffffffffu, wait(&sh, &sh.tempty[acc], accphase ^ 1, 1)))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!(ok = __all_sync(0xffffffffu, wait(&sh, &sh.full[slot], phase, 1)))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t st = smem_u32(base + slot * kStage);
+            const uint64_t da = sdesc_sw128(st, a_mn ? 8192 : 0, 1024), db = sdesc_sw128(st + kBM * kRowBytes, 8192, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss_pair<false>(d, da + k * step, db + (uint64_t)(k * 2048 >> 4), id, kb > 0 || k > 0);
+            mma_commit_pair(&sh.empty[slot], 3);
+            if (kb + 1 == kblocks) mma_commit_pair(&sh.tfull[acc], 3);
+          }
+          __syncwarp();
+          if (++slot == kStages) slot = 0, phase ^= 1;
+        }
+        acc ^= 1;
+        if (acc == 0) accphase ^= 1;
+      }
+      if (!ok) {
+        if (elect_one()) mma_commit_pair(&sh.drain, 3);
+        for (uint32_t j = 0; j < (1u << 20) && !mbar_try_wait(&sh.drain, 0); ++j) {
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) / 4;
+    float *stage = reinterpret_cast<float *>(base + kStages * kStage + (warp - 2) * kEpiBytes);
+    int acc = 0;
+    uint32_t accphase = 0;
+    for (uint32_t n = 0; task(deal, worker, n, which, tile); ++n) {
+      const Product &p = which ? p1 : p0;
+      const LinearArgs &epi = p.epi;
+      int64_t tm, tn;
+      tile_at(p.tiles, tile, tm, tn);
+      const int64_t m0 = tm * 256 + rank * kBM + quarter * 32, m = m0 + lane, n0 = tn * BN;
+      const int chunks = (int)(epi.N - n0 < BN ? (epi.N - n0 + 31) / 32 : BN / 32);
+      if (!__all_sync(0xffffffffu, wait(&sh, &sh.tfull[acc], accphase, 2))) break;
+      tc_fence_after();
+      const auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_cluster(&sh.tempty[acc], 0));
+      };
+      uint32_t r[32];
+#pragma unroll 1
+      for (int c = half; c < chunks; c += 2) {
+        tmem_ld32(tmem_addr(tmem, quarter * 32, acc * BN + c * 32), r);
+        tmem_wait_ld_regs(r);
+        if (c + 2 >= chunks) release();
+        if (p.aligned) {
+          if (m < epi.M) finish_row(epi, m, n0 + c * 32, r, 1.f, stage, Residual{}, p.wide);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(stage + lane * kPitch + 4 * k) =
+                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          __syncwarp();
+          finish_column(epi, stage, lane, m0, n0 + c * 32 + lane);
+        }
+        __syncwarp();
+      }
+      if (half >= chunks) release();
+      acc ^= 1;
+      if (acc == 0) accphase ^= 1;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_relaxed();  // no CTA leaves while another may reach into it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kCols);
+}
+
+// Tiles of 256 x 256, their blocks of k and what one takes (as in choose())
+struct Whole {
+  int64_t tiles;
+  double us;
+};
+Whole whole_of(int64_t M, int64_t N, int64_t K) {
+  return {((M + 255) / 256) * ((N + 255) / 256), (double)((K + 63) / 64) * 0.26 + 256 * 0.005};
+}
+// The least time in which `workers` finish a's tiles, in turn, and then b's (each no
+// longer), and how many more of b's those with a tile of a's fewer take.
+double deal_out(const Whole &a, const Whole &b, int64_t workers, Deal &d) {
+  const int64_t more = a.tiles % workers, fewer = workers - more, each = a.tiles / workers;
+  d.workers = (uint32_t)workers, d.fewer = (uint32_t)fewer;
+  d.total[0] = (uint32_t)a.tiles, d.total[1] = (uint32_t)b.tiles;
+  int64_t extra = more ? (int64_t)(a.us / b.us) : 0;
+  if (extra * fewer > b.tiles) extra = b.tiles / fewer;
+  double best = 1e30;
+  for (int64_t x = extra; x <= extra + (more ? 2 : 0); ++x) {
+    const int64_t rest = b.tiles - x * fewer > 0 ? b.tiles - x * fewer : 0, rounds = rest / workers, left = rest % workers;
+    // (what is left of the rounds goes to the first: those with a tile more, if there are any)
+    const double first = (each + (more ? 1 : 0)) * a.us + (rounds + (left > 0)) * b.us;
+    const double others = each * a.us + (x + rounds + (left > more)) * b.us;
+    const double us = first > others ? first : others;
+    if (us < best) best = us, d.extra = (uint32_t)x;
+  }
+  return best;
+}
+
 }  // namespace
+
+bool gradients_fit(const GemmArgs &x, const GemmArgs &w) {
+  const Choice a = choose(x.epi.M, x.epi.N, x.K, false), b = choose(w.epi.M, w.epi.N, w.K, false);
+  // (parts of k, or other tiles, would be other sums than a product by itself has)
+  if (a.shape != 0 || b.shape != 0 || a.split != 1 || b.split != 1) return false;
+  Whole p = whole_of(x.epi.M, x.epi.N, x.K), q = whole_of(w.epi.M, w.epi.N, w.K);
+  if (p.tiles + q.tiles >= (int64_t(1) << 30)) return false;
+  Deal d;
+  return deal_out(p.us >= q.us ? p : q, p.us >= q.us ? q : p, sm_count() / 2, d) + 3.0 < 0.97 * (a.us + b.us + 0.7);
+}
+
+cudaError_t launch_gradients_tc(const GemmArgs &x, const GemmArgs &w, cudaStream_t s) {
+  const Whole px = whole_of(x.epi.M, x.epi.N, x.K), pw = whole_of(w.epi.M, w.epi.N, w.K);
+  const bool first = px.us >= pw.us;  // dx has the longer tiles
+  const GemmArgs *g[2] = {first ? &x : &w, first ? &w : &x};
+  Deal d{};
+  deal_out(first ? px : pw, first ? pw : px, sm_count() / 2, d);
+  CUtensorMap ma[2], mb[2];
+  Product p[2];
+  for (int i = 0; i < 2; ++i) {
+    const LinearArgs &e = g[i]->epi;
+    cudaError_t err = g[i]->a_mn ? make_map_2d_sw128(&ma[i], g[i]->a, (uint64_t)e.M, (uint64_t)g[i]->K, (uint64_t)g[i]->lda, 2, 64)
+                                 : make_map_2d_sw128(&ma[i], g[i]->a, (uint64_t)g[i]->K, (uint64_t)e.M, (uint64_t)g[i]->lda, 2, kBM);
+    if (err == cudaSuccess) err = make_map_2d_sw128(&mb[i], g[i]->b, (uint64_t)e.N, (uint64_t)g[i]->K, (uint64_t)g[i]->ldb, 2, 64);
+    if (err != cudaSuccess) return err;
+    Tiles &t = p[i].tiles;
+    t.m_tiles = (e.M + 255) / 256, t.n_tiles = (e.N + 255) / 256, t.total = t.m_tiles * t.n_tiles;
+    t.kblocks = (int)((g[i]->K + 63) / 64), t.split = 1, t.per = t.kblocks;
+    p[i].epi = e, p[i].a_mn = g[i]->a_mn;
+    p[i].aligned = e.N % 8 == 0 && reinterpret_cast<uintptr_t>(e.out) % 16 == 0;
+    p[i].wide = p[i].aligned && e.N % 16 == 0 && reinterpret_cast<uintptr_t>(e.out) % 32 == 0;
+  }
+  constexpr int smem = smem_bytes(256, true);
+  const cudaError_t err = cudaFuncSetAttribute(gradients_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  return chain_launch(gradients_kernel, dim3(d.workers * 2), dim3(kThreads), smem, 2, x.dependent, s, ma[0], mb[0], ma[1],
+                      mb[1], p[0], p[1], d);
+}
 
 double gemm_tc_us(int64_t M, int64_t N, int64_t K, bool f8) { return choose(M, N, K, f8).us + 0.7; }
 
