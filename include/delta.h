@@ -530,7 +530,9 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
  *           strides: nine element strides in host memory, of the batch row, the
  *           token and the head, of q, then k, then v
  *   decay   [H]           float32 in [0, 1]; powers of it below float32's normal
- *                         range count as 0
+ *                         range count as 0; one that is NaN or negative makes
+ *                         its head's outputs and states NaN, but for rows
+ *                         without tokens
  *   h0      [B, H, dk, dv] float32 or NULL (=> 0)
  *   lengths [B]           int32 tokens of each row, taken into [0, T], or NULL
  *                         (=> T); what later tokens hold does not matter, they
@@ -561,7 +563,8 @@ int delta_decay_fwd(const void *q, const void *k, const void *v, const float *de
 /*
  * delta_decay_step -- one token of the same: state [B, H, dk, dv] float32 is
  * updated in place; q, k [B, H, dk], v [B, H, dv] with six strides (batch row and
- * head of q, k, v); out [B, H, dv] dtype.  All in float32.
+ * head of q, k, v); out [B, H, dv] dtype.  All in float32; the state is multiplied by
+ * the decay as it is.
  */
 int delta_decay_step(const void *q, const void *k, const void *v, const float *decay, float *state, void *out, int B,
                      int H, int dk, int dv, const int64_t *strides, float scale, delta_dtype dtype,

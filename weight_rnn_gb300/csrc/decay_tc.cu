@@ -154,7 +154,8 @@ __device__ bool part_at(const TcArgs &a, int k, Part &r) {
   if (r.c0 >= p.dv) r.chunks = 0, r.t_hi = r.t_lo;  // a pass with fewer groups
   if (kStates && sg == (p.reverse ? 0 : a.nseg - 1)) r.chunks = 0;  // no segment begins with its state
   r.to = min(r.to, r.chunks);
-  r.lg = fmaxf(log2f(a.decay[r.h]), kLogZero);
+  r.lg = log2f(a.decay[r.h]);
+  if (r.lg < kLogZero) r.lg = kLogZero;  // (not fmaxf, which would drop the NaN of a decay that has no logarithm)
   r.two = r.lg != 0.f || p.kvs != 1.f;  // else K' is K itself
   r.last = kStates || sg == (p.reverse ? 0 : a.nseg - 1);
   r.state = kStates || a.nseg > 1 ? (int64_t)bh * a.nseg + sg : bh;
