@@ -652,7 +652,8 @@ int delta_add_rmsnorm_bwd(const void *dy, const void *sum, const void *weight, c
  *
  * The norm is of the unrounded t, the variance that of the differences.  D <= 8192,
  * eps > 0.  With D = 0 nothing is written.  As in delta_add_rmsnorm_fwd a row whose
- * squares sum past float32's range counts as infinitely wide, rstd 0 and y = bias.
+ * squares sum past float32's range counts as infinitely wide, rstd 0 and y = bias, as
+ * long as its elements t are in that range.
  */
 int delta_add_layernorm_fwd(const void *x, const void *residual, const void *weight, const void *bias, void *y,
                             void *sum_out, float *mean, float *rstd, int64_t rows, int D, int64_t ldx, int64_t ldr,

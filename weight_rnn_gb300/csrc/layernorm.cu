@@ -16,7 +16,9 @@
 //
 //   sum (t - mean)^2 = sum_w M_w + n_w (m_w - mean)^2,
 //
-// nothing of which cancels, at one barrier a row.  (A second barrier for the squares
+// nothing of which cancels, at one barrier a row.  Sums behind means are of elements times
+// 2^-13, the power of two of the widest row: the same roundings, and a row of finite
+// elements has a finite mean.  (A second barrier for the squares
 // about the row's mean, and single elements in place of pairs: 32768 x 4096 bfloat16
 // 198 us.)  32768 x 4096 bfloat16 takes 163 us, 6.6 TB/s; one row of 4096 3.3, a launch.
 #include "norm.cuh"
@@ -110,6 +112,13 @@ __device__ __forceinline__ void store_lane(T *p, const Lane<V> &v) {
   store_v<T, V>(p, f);
 }
 
+constexpr float kDown = 1.f / kNormMaxD;  // what a sum's elements are scaled by
+static_assert((kNormMaxD & (kNormMaxD - 1)) == 0, "a power of two, so that scaling rounds nothing");
+
+// A row whose squares pass float32's range has rstd 0; its differences may be infinite,
+// and are left out.
+__device__ __forceinline__ float mean_used(float mean, float rstd) { return rstd == 0.f ? 0.f : mean; }
+
 // over the lanes of a row in this warp: all of them, or 4, 8 or 16 where rows are narrow
 __device__ __forceinline__ float row_sum(float v) {
   if (blockDim.x < 32) {
@@ -152,7 +161,8 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
     const int left = (int)p.D - (j * (int)blockDim.x + warp * 32) * V;
     own += left < 0 ? 0 : left < 32 * V ? left : 32 * V;
   }
-  const float n_w = (float)own, inv_w = own ? 1.f / n_w : 0.f;
+  const float n_w = (float)own, inv_w = own ? (1.f / n_w) * kNormMaxD : 0.f;
+  const float sum_of_ones = (float)p.D * kDown;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   Rows<In, V, kPer, 2, kT> in;
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
       if (row < p.rows && (int64_t)(j * blockDim.x + threadIdx.x) * V < p.D) {
         t[j] = Lane<V>::of(in.get(0, j));
         if (p.residual) t[j] = t[j] + Lane<V>::of(in.get(1, j));
-        acc = acc + t[j];
+        acc = t[j].fma(Lane<V>::all(kDown), acc);
       }
     }
     in.done();
@@ -191,7 +201,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
       // 16 lanes take a warp's part each
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       if ((lane & 15) < nwarp) a = part[buf][threadIdx.y * 16 + (lane & 15)];
-      mean = lanes_sum<8>(a.x) / (float)p.D;
+      mean = lanes_sum<8>(a.x) / sum_of_ones;
       q = lanes_sum<8>(fmaf(a.w * (a.z - mean), a.z - mean, a.y));
     }
     const float rstd = rsqrtf(q / (float)p.D + p.eps);
@@ -200,12 +210,13 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
         if (p.rstd) p.rstd[row] = rstd;
         if (p.mean) p.mean[row] = mean;
       }
+      const Lane<V> away = Lane<V>::all(-mean_used(mean, rstd));
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int64_t d = (int64_t)(j * blockDim.x + threadIdx.x) * V;
         if (d >= p.D) continue;
         if (p.sum) store_lane<In, V>(static_cast<In *>(p.sum) + row * p.D + d, t[j]);
-        const Lane<V> c = (t[j] + Lane<V>::all(-mean)) * Lane<V>::all(rstd);
+        const Lane<V> c = (t[j] + away) * Lane<V>::all(rstd);
         store_lane<In, V>(static_cast<In *>(p.y) + row * p.D + d, c.fma(w[j], b[j]));
       }
     }
@@ -248,7 +259,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? bwd_threads<In, V, kPer>()
   int buf = 0;
   for (int64_t row = first; row - threadIdx.y < p.rows; row += step, buf ^= 1) {
     in.turn(row, step);
-    const float rstd = ahead, mean = ahead_m;
+    const float rstd = ahead, mean = mean_used(ahead_m, rstd);
     if (row + step < p.rows) ahead = p.rstd[row + step], ahead_m = p.mean[row + step];
     Lane<V> wy[kPer], t[kPer], s2 = Lane<V>::all(0.f), d2 = Lane<V>::all(0.f);
 #pragma unroll
