@@ -171,31 +171,20 @@ struct Shared {
   Part part[kParts];
 };
 
-// What waits gave up on is not waited for by the others, once they look.
+// The first wait of a CTA that gives up is the one reported.  (Barriers' other waits run
+// out by themselves, all at about one time; those for another CTA's flag look at `dead`.)
 __device__ __forceinline__ void give_up(Shared *sh, int role) {
   if (!sh->dead) atomicCAS(&g_decay_error, 0u, (unsigned)(1 + role));
   sh->dead = 1;
 }
-// By whole warps, so that they leave their loops together.  Few instructions, since they
-// stand at every hand-over: the warps' loops have to share small instruction caches.
+// By whole warps, so that they leave their loops together: a lane's try may time out where
+// another's sees the phase, so the warp goes on only when all of its lanes have seen it.
+// Few instructions, since they stand at every hand-over: the warps' loops have to share
+// small instruction caches.
 __device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity, int role) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n"
-      "TRY:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra.uni DONE;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.gt.u32 p, n, %3;\n\t"
-      "@!p bra.uni TRY;\n"
-      "DONE:\n\t"
-      "setp.le.u32 p, n, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "n"(1 << 21)
-      : "memory");
-  if (__all_sync(0xffffffffu, ok)) return true;
+#pragma unroll 1
+  for (uint32_t n = 0; n < (1u << 21); ++n)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   give_up(sh, role);
   return false;
 }
