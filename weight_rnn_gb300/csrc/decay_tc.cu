@@ -59,6 +59,7 @@
 
 #include "chain.cuh"
 #include "decay.cuh"
+#include "decay_share.h"
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tma_host.h"
@@ -103,16 +104,11 @@ struct TcArgs {
   float4 *handed;   // [CTA][8][16][32]
 };
 
-// A CTA's work.  It has one of the passes; an item is a segment of a head and a group of
-// value channels.  Where there are more items than CTAs can be resident, the CTAs of a
-// pass get equal runs of its items' chunks, one after another, so that the last round is
-// as full as the others (384 items in 2.6 rounds of 152 for 3).  An item that two CTAs
-// share is begun by the first, before all else, and ended by the second, after all else,
-// which takes the state over through memory; it is there by then, as no CTA has less than
-// an item's chunks.  CTAs of different passes that are neighbours work on one head at one
-// time, so that what both read comes from memory once (the two in reverse share two of
+// A CTA's work: one of the passes, and of its items one, or a run of several that CTAs
+// share (decay_share.h).  CTAs of different passes that are neighbours work on one head at
+// one time, so that what both read comes from memory once (the two in reverse share two of
 // three tensors).
-constexpr int kParts = 24;
+using decay::kParts;
 struct Part {
   int pass, c0, b, h;
   int t_lo, t_hi, t_end, chunks;  // of the item: tokens, those that count, their chunks
@@ -128,15 +124,10 @@ __device__ bool part_at(const TcArgs &a, int k, Part &r) {
   r.pass = (int)(blockIdx.x % (uint32_t)a.passes);
   r.from = 0, r.to = a.chunks;
   if (a.shared) {
-    const uint64_t units = (uint64_t)(a.items / (uint32_t)a.passes) * (uint32_t)a.chunks;
-    const uint32_t ctas = gridDim.x / (uint32_t)a.passes;
-    const uint64_t u0 = units * item / ctas, u1 = units * (item + 1) / ctas;
-    const uint32_t first = (uint32_t)(u0 / (uint32_t)a.chunks), last = (uint32_t)((u1 - 1) / (uint32_t)a.chunks);
-    const int count = (int)(last - first) + 1;
-    if (k >= count) return false;
-    item = k == 0 ? last : k == count - 1 ? first : first + (uint32_t)k;
-    if (item == first) r.from = (int)(u0 - (uint64_t)first * (uint32_t)a.chunks);
-    if (item == last) r.to = (int)(u1 - (uint64_t)last * (uint32_t)a.chunks);
+    decay::Run run;
+    if (!decay::shared_part(a.items / (uint32_t)a.passes, (uint32_t)a.chunks, item, gridDim.x / (uint32_t)a.passes, k, run))
+      return false;
+    item = run.item, r.from = run.from, r.to = run.to;
   } else if (k > 0) {
     return false;
   }
@@ -839,12 +830,8 @@ int64_t tc_items(const DecayArgs &a) {
   for (int i = 0; i < a.passes; ++i) dv = max(dv, a.pass[i].dv);
   return a.B * a.H * ((dv + kD - 1) / kD) * a.nseg * a.passes;
 }
-// CTAs share items where that fills the last round.  Many rounds need it not, and rows of
-// differing lengths are better dealt out one by one.
-bool tc_shared(const DecayArgs &a) {
-  const int64_t items = tc_items(a), sms = sm_count();
-  return !a.lengths && items > sms && items <= (kParts - 4) * sms && (items + sms - 1) / sms * sms * 20 > items * 21;
-}
+// (rows of differing lengths are better dealt out one by one)
+bool tc_shared(const DecayArgs &a) { return !a.lengths && decay::share_items(tc_items(a), a.passes, sm_count()); }
 int64_t flag_bytes(int sms) { return ((int64_t)sms * 32 + 255) / 256 * 256; }
 
 // (Not launched as a dependent, but where this call's own joining of states goes before:
@@ -886,7 +873,7 @@ cudaError_t run(const DecayArgs &a, cudaStream_t s) {
     if ((e = cudaMemsetAsync(t.flags, 0, (size_t)sms * 32, s)) != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(t.shared ? sms / a.passes * a.passes : items));
+  cfg.gridDim = dim3((unsigned)(t.shared ? decay::shared_ctas(a.passes, sms) * a.passes : items));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
