@@ -809,9 +809,10 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t s) {
 // the other's, N and M long.  In one launch the pairs take the long tiles in turn, and
 // then as many of the short ones as evens out what they have: those with one long tile
 // fewer `extra` more, before the rest goes round.  A tile's sums are in the order that it
-// has in a launch of its own.  The gated layer's gradients at M4096 N4096 K2048: 186 ->
-// 170 us, the linear layer's 104 -> 98, at M2048 N8192 105 -> 91; M5000 N1300 K4104 takes
-// 2 % longer.
+// has in a launch of its own.  After a second's rest, from graphs, the gated layer's
+// gradients at M4096 N4096 K2048 take 170 us for 186, the linear layer's 98 for 104, at
+// M2048 N8192 91 for 105; the gated ones as calls back to back, the clock down with power,
+// 193 for 201.
 struct Product {
   Tiles tiles;
   LinearArgs epi;
