@@ -546,8 +546,10 @@ int delta_scan_bwd(const void *x, const void *gate, const float *states, const i
  * tensor cores in chunks of 128 tokens, all else in float32 in chunks of 32, each
  * product as three of tf32 that leave out 2^-22 of a term.  The state is float32
  * throughout; in bfloat16's chunks a token's way into it is rounded to 2^-16 of itself,
- * what out reads of it to bfloat16, and of the state before a chunk out reads no less
- * than 2^-64.  A token whose values are not finite may reach all of its chunk's outputs,
+ * what out reads of it, and of the products of q and k, to bfloat16.  Two limits hold
+ * there under strong decays: of the state before a chunk out reads no less than 2^-64,
+ * and sums of q k v (in the gradients, of what stands in their places, times scale) have
+ * to stay below 2^63.  A token whose values are not finite may reach all of its chunk's outputs,
  * and those after it, and an infinity may come out as a NaN.
  *
  * Where B * H does not fill the GPU the time axis is cut into segments, whose states

@@ -59,3 +59,21 @@ def test_step_takes_the_decay_as_it_is():
     assert torch.isnan(out[:, 0]).all() and torch.isnan(state[:, 0]).all()
     torch.testing.assert_close(state[:, 1:], want[:, 1:], rtol=1e-6, atol=1e-6)
     torch.testing.assert_close(out[:, 1:], (q[..., None] * want).sum(-2)[:, 1:], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,d", [(300, 32), (1500, 64)])
+def test_what_dout_holds_past_a_row_does_not_matter(T, d, dtype, bad):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    normal = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    n = torch.tensor([0, 1, 129, T - 1], dtype=torch.int32, device="cuda")
+    q, k, v, do = (normal(4, T, 2, d).to(dtype) for _ in range(4))
+    decay, h0, dh = torch.tensor([0.9, 1.0], device="cuda"), normal(4, 2, d, d), normal(4, 2, d, d)
+    want = wr.delta_decay_bwd(q, k, v, decay, do, h0, dh, lengths=n)
+    past = torch.arange(T, device="cuda") >= n[:, None]
+    spoiled = [t.masked_fill(past[:, :, None, None], bad) for t in (q, k, v, do)]
+    got = wr.delta_decay_bwd(*spoiled[:3], decay, spoiled[3], h0, dh, lengths=n)
+    wr.delta_check_device()
+    assert all(torch.isfinite(t).all() for t in want)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

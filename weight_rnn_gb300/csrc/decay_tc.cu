@@ -44,17 +44,19 @@
 //   12-19  the state, and O: 64 value columns each warpgroup
 //
 // Bound by HBM where every SM has its share of a long call, 4 tensors of 32 KB a chunk
-// (2.9 us at 152 CTAs): B4 T8192 H32 d128 170 us, 6.3 TB/s.  The warps' own work takes 2.3
-// us a chunk, 4400 cycles, of which shared memory is busy for 3000: tiles in, 96 KB, what
-// the products read, 224 (SS ones both operands, 64 cycles for 16 channels, where the
-// tensor cores would take 32), K' and S, 64.  Bound by that are heads of 64 channels (B4
-// T8192 H32 125 us; what a narrow head has not is left out: 146 with it) and in part the
-// gradients, three such passes at a time, which read 9.5 tensors from memory for the 7 of
-// the call: B4 T4096 H32 236 us.  Where the time axis is cut, k and v are read twice: B1
-// T65536 H8 140 us.  Next is instruction fetch, with caches shared by five groups of warps
-// (from 111 KB of code to 70 KB: 204 -> 171 us).  (A warpgroup of its own for O's way out,
-// 768 threads with registers moved by setmaxnreg: 205 us, 278 for the gradients.)  Every
-// mbarrier wait is bounded: a timeout sets a device error word and the kernel winds down.
+// (2.9 us at 152 CTAs): B4 T8192 H32 d128 170 us, 6.3 TB/s.  (Figures are of graphs after
+// a second's rest; in calls back to back, the clock down with power, this one takes 180 to
+// 187 us and the gradients below 253 to 263.)  The warps' own work takes 2.3 us a chunk,
+// 4400 cycles, of which shared memory is busy for 3000: tiles in, 96 KB, what the products
+// read, 224 (SS ones both operands, 64 cycles for 16 channels, where the tensor cores would
+// take 32), K' and S, 64.  Bound by that are heads of 64 channels (B4 T8192 H32 125 us; what
+// a narrow head has not is left out: 146 with it) and in part the gradients, three such
+// passes at a time, which read 9.5 tensors from memory for the 7 of the call: B4 T4096 H32
+// 236 us.  Where the time axis is cut, k and v are read twice: B1 T65536 H8 140 us.  Next is
+// instruction fetch, with caches shared by five groups of warps (from 111 KB of code to 70
+// KB: 204 -> 171 us).  (A warpgroup of its own for O's way out, 768 threads with registers
+// moved by setmaxnreg: 205 us, 278 for the gradients.)  Every mbarrier wait is bounded: a
+// timeout sets a device error word and the kernel winds down.
 #include <cuda_bf16.h>
 
 #include "chain.cuh"

@@ -18,9 +18,9 @@
 //
 // nothing of which cancels, at one barrier a row.  Sums behind means are of elements times
 // 2^-13, the power of two of the widest row: the same roundings, and a row of finite
-// elements has a finite mean.  (A second barrier for the squares
-// about the row's mean, and single elements in place of pairs: 32768 x 4096 bfloat16
-// 198 us.)  32768 x 4096 bfloat16 takes 163 us, 6.6 TB/s; one row of 4096 3.3, a launch.
+// elements has a finite mean.  (A second barrier for the squares about the row's mean, and
+// single elements in place of pairs: 32768 x 4096 bfloat16 198 us.)  32768 x 4096 bfloat16
+// takes 164 us, 6.5 TB/s (163 without the scaling); one row of 4096 3.2, a launch.
 #include "norm.cuh"
 
 namespace delta {
