@@ -62,3 +62,16 @@ def test_infinite_rows_stay_not_numbers(dtype):
     y, _, _, rstd = wr.delta_add_layernorm_fwd(x.cuda(), torch.ones(512, device="cuda"))
     assert torch.isnan(y[1:3]).all() and torch.isnan(rstd[1:3]).all()
     assert not y[0].any() and not y[3].any()
+
+
+@pytest.mark.parametrize("D", [1, 2, 3, 8, 64, 65, 1000, 1024, 1025, 8192])
+def test_tiny_rows_keep_their_mean(D):
+    """Elements near the end of float32's normal range, and below it: sums are of elements
+    over D's power of two, and lose at most 2^-150 in each of 40 roundings, which is less
+    than 2^-143 of the mean."""
+    x = torch.randn(6, D, generator=torch.Generator().manual_seed(D)).abs() + 1.0
+    x *= torch.tensor([1e-30, 1e-34, 1e-36, 1e-37, 1.2e-38, 1e-40])[:, None]
+    y, _, mean, _ = wr.delta_add_layernorm_fwd(x.cuda(), torch.ones(D, device="cuda"), eps=EPS)
+    t = x.double()
+    within(mean, t.mean(-1), 41 * U * t.abs().mean(-1) + 2.0 ** -143, "mean")
+    assert (y.abs().cpu() <= 1e-25).all()

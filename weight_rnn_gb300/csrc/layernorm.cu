@@ -16,11 +16,11 @@
 //
 //   sum (t - mean)^2 = sum_w M_w + n_w (m_w - mean)^2,
 //
-// nothing of which cancels, at one barrier a row.  Sums behind means are of elements times
-// 2^-13, the power of two of the widest row: the same roundings, and a row of finite
-// elements has a finite mean.  (A second barrier for the squares about the row's mean, and
-// single elements in place of pairs: 32768 x 4096 bfloat16 198 us.)  32768 x 4096 bfloat16
-// takes 164 us, 6.5 TB/s (163 without the scaling); one row of 4096 3.2, a launch.
+// nothing of which cancels, at one barrier a row.  Sums behind means are of elements over
+// D's power of two: the same roundings, and a row of finite elements has a finite mean.
+// (A second barrier for the squares about the row's mean, and single elements in place of
+// pairs: 32768 x 4096 bfloat16 198 us.)  32768 x 4096 bfloat16 takes 164 us, 6.5 TB/s (163
+// without the scaling); one row of 4096 3.2, a launch.
 #include "norm.cuh"
 
 namespace delta {
@@ -112,8 +112,9 @@ __device__ __forceinline__ void store_lane(T *p, const Lane<V> &v) {
   store_v<T, V>(p, f);
 }
 
-constexpr float kDown = 1.f / kNormMaxD;  // what a sum's elements are scaled by
-static_assert((kNormMaxD & (kNormMaxD - 1)) == 0, "a power of two, so that scaling rounds nothing");
+// the least power of two that is no less than D: its logarithm
+__device__ __forceinline__ int log2_up(int D) { return 32 - __clz(D - 1); }
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
 
 // A row whose squares pass float32's range has rstd 0; its differences may be infinite,
 // and are left out.
@@ -161,8 +162,9 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
     const int left = (int)p.D - (j * (int)blockDim.x + warp * 32) * V;
     own += left < 0 ? 0 : left < 32 * V ? left : 32 * V;
   }
-  const float n_w = (float)own, inv_w = own ? (1.f / n_w) * kNormMaxD : 0.f;
-  const float sum_of_ones = (float)p.D * kDown;
+  const int up = log2_up((int)p.D);
+  const float down = power_of_two(-up), sum_of_ones = (float)p.D * down;
+  const float n_w = (float)own, inv_w = own ? 1.f / n_w * power_of_two(up) : 0.f;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   Rows<In, V, kPer, 2, kT> in;
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kT, V *kPer <= 16 ? kSmThreads / kT : 1) layer
       if (row < p.rows && (int64_t)(j * blockDim.x + threadIdx.x) * V < p.D) {
         t[j] = Lane<V>::of(in.get(0, j));
         if (p.residual) t[j] = t[j] + Lane<V>::of(in.get(1, j));
-        acc = t[j].fma(Lane<V>::all(kDown), acc);
+        acc = t[j].fma(Lane<V>::all(down), acc);
       }
     }
     in.done();
